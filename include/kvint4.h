@@ -63,6 +63,7 @@ extern "C" {
 #define KV_INT4_ERR_WORKSPACE 6     /* workspace NULL or smaller than kv_int4_attention_workspace_size() */
 #define KV_INT4_ERR_SIZE 7          /* a negative count, or a size that overflows the index types */
 #define KV_INT4_ERR_CUDA 8          /* a CUDA call or kernel launch failed */
+#define KV_INT4_ERR_ROT 10          /* kv_qk_norm_rope: rot_dim negative, above head_size or no multiple of 16 */
 #define KV_INT4_ERR_SCRATCH_LIMIT 9 /* kv_int4_attention_noalloc: the call needs more workspace than
                                        KV_INT4_NOALLOC_SCRATCH_BYTES */
 
@@ -75,6 +76,9 @@ extern "C" {
 #define KV_INT4_DEV_BAD_SIGNS 8     /* a sign entry other than +1 / -1 */
 #define KV_INT4_DEV_TIMEOUT 16      /* a wait for staged input exceeded its iteration limit: the kernel
                                        stopped early and its outputs are incomplete (not expected to occur) */
+#define KV_INT4_DEV_NONFINITE 32    /* kv_fp8_write: an infinity or NaN among the values (stored as the largest
+                                       finite magnitude, or 0) */
+#define KV_INT4_DEV_BAD_POS 64      /* kv_qk_norm_rope: a position outside [0, max_position) */
 
 /*
  * kv_int4_write -- reshape_and_cache_int4: quantise new K/V head vectors into
@@ -343,6 +347,125 @@ KVINT4_API int kv_int8_attention_inslot(const void* q, int64_t q_token_stride, c
                                         int32_t* dev_status, void* stream);
 
 /*
+ * FP8 cache with block scales: E4M3 codes, one scale per (block, kv head).
+ *
+ *   k_cache, v_cache:             uint8 [num_blocks][block_size][num_kv_heads][head_size]  E4M3 codes
+ *   k_scale_cache, v_scale_cache: float [num_blocks][num_kv_heads]                         2^k, k in [-60, 60]
+ * A code c of a block with scale s stands for c * s.  head_size is one of 64,
+ * 96, 128, 192, 256; block_size is 16; code caches are 16-byte aligned, scale
+ * caches 4-byte aligned.  Against kv_int8_write's scale per (token, head) the
+ * scales take 1 / 16 of the bytes and a block's codes share one exponent;
+ * E4M3 itself keeps four significant bits over 2^-9 .. 448.
+ *
+ * kv_fp8_write quantises the new tokens of a batch into the cache.  The tokens
+ * are named as kv_int4_attention names them: sequence i's new tokens are
+ * [start_loc[i], start_loc[i+1]) of k and v, n_i of them, and are its last n_i
+ * positions [seq_lens[i] - n_i, seq_lens[i]); position p lives in block
+ * block_table[i*max_blocks_per_seq + p/16], row p % 16.  Tokens of k and v
+ * behind start_loc[num_seqs] are padding and are not read.  For each touched
+ * block, kv head, and K and V on their own, with a the largest magnitude among
+ * the call's rows of the block:
+ *   k = the smallest exponent in [-60, 60] with a <= 448 * 2^k
+ *   when the call does not write the block's row 0: k = max(k, stored exponent),
+ *     and if that is larger than the stored one, the codes c of the rows the
+ *     block held before become e4m3(c * 2^(stored - k))
+ *   codes of the new rows: e4m3(x * 2^-k), nearest even; scale: 2^k
+ * so writing a block's row 0 begins the block, whatever was in it.  Codes move
+ * to a larger scale exactly unless they become subnormal, so a sequence
+ * written token by token and one written at once hold the same codes but for
+ * those.  Magnitudes above 448 * 2^60 saturate (infinities with them); NaN is
+ * stored as 0; either non-finite value sets KV_INT4_DEV_NONFINITE.  Rows no
+ * call wrote keep their bytes.  A stored scale that no write stores (no power of
+ * two, or out of range) means that the block was not begun: it is replaced, and
+ * the rows before the call's are left as they are.  Two sequences of one call must not name the same block for their new
+ * tokens (the block's contents are then unspecified); calls that write the
+ * same blocks must be ordered by the caller.
+ *
+ * kv_fp8_read writes the last n_i positions of each sequence back as bf16
+ * (code * scale, nearest even): the same arguments, with k and v as outputs.
+ * Rows of k and v behind start_loc[num_seqs] are left as they were; rows of a
+ * block outside [0, num_blocks) are written as zeros and set
+ * KV_INT4_DEV_BAD_BLOCK.
+ *
+ * k, v: bf16, element (t, h, i) at k[t*k_token_stride + h*head_size + i];
+ *   16-byte aligned, strides multiples of 8 elements.
+ * block_table: int32 [num_seqs][max_blocks_per_seq]; seq_lens: int32 [num_seqs];
+ *   start_loc: int32 [num_seqs+1], non-decreasing, within [0, num_tokens].
+ * max_len: an upper bound of the n_i (used to size the launch; with max_len 1
+ *   sequences map to work without a search).  A sequence with n_i > max_len,
+ *   n_i > seq_lens[i], or seq_lens[i] > max_blocks_per_seq * 16 is skipped and
+ *   sets KV_INT4_DEV_BAD_SEQ; a write to a block outside [0, num_blocks) is
+ *   skipped and sets KV_INT4_DEV_BAD_BLOCK.
+ * num_seqs == 0 or num_tokens == 0 is a no-op.
+ */
+KVINT4_API int kv_fp8_write(const void* k, int64_t k_token_stride, const void* v, int64_t v_token_stride,
+                            const int32_t* block_table, int max_blocks_per_seq, const int32_t* seq_lens,
+                            const int32_t* start_loc, int num_seqs, int num_tokens, int max_len, uint8_t* k_cache,
+                            uint8_t* v_cache, float* k_scale_cache, float* v_scale_cache, int num_blocks,
+                            int block_size, int num_kv_heads, int head_size, int32_t* dev_status, void* stream);
+KVINT4_API int kv_fp8_read(const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale_cache,
+                           const float* v_scale_cache, const int32_t* block_table, int max_blocks_per_seq,
+                           const int32_t* seq_lens, const int32_t* start_loc, int num_seqs, int num_tokens,
+                           int max_len, void* k, int64_t k_token_stride, void* v, int64_t v_token_stride,
+                           int num_blocks, int block_size, int num_kv_heads, int head_size, int32_t* dev_status,
+                           void* stream);
+
+/*
+ * kv_fp8_attention -- attention over the FP8 cache with block scales:
+ *   out[t][hq][:] = sum_p softmax_p(softmax_scale * q[t][hq] . k_hat_p) v_hat_p,
+ *   k_hat_p = c_p * s_block(p), v_hat_p likewise.
+ * Arguments, masks (causal, sliding_window), workspace
+ * (kv_int4_attention_workspace_size), device status bits and errors are those
+ * of kv_int8_attention, except for the caches (above) and:
+ * - with causal == 0 the keys need not hold the queries: q_len may exceed
+ *   seq_lens[i] (decoder queries over an encoder's states, say), and seq_lens[i]
+ *   may be 0.  A sliding window then counts from query position
+ *   seq_lens[i] - q_len + j, as ever;
+ * - a query that sees no key (an empty sequence, or only blocks outside
+ *   [0, num_blocks)) gets zeros;
+ * - rows of a block at or behind seq_lens[i] may hold any bytes; visible codes
+ *   must be finite (0x7F and 0xFF, which no write stores, are NaN) and V scales
+ *   powers of two in the range above.
+ */
+KVINT4_API int kv_fp8_attention(const void* q, int64_t q_token_stride, const uint8_t* k_cache,
+                                const uint8_t* v_cache, const float* k_scale_cache, const float* v_scale_cache,
+                                const int32_t* block_table, int max_blocks_per_seq, const int32_t* seq_lens,
+                                const int32_t* query_start_loc, int num_seqs, int num_q_tokens, int max_query_len,
+                                int max_seq_len, int num_q_heads, int num_kv_heads, int head_size, int block_size,
+                                int num_blocks, float softmax_scale, int causal, int sliding_window, void* out,
+                                int64_t out_token_stride, void* workspace, size_t workspace_bytes,
+                                int32_t* dev_status, void* stream);
+
+/*
+ * kv_qk_norm_rope -- RMS norm of every query and key head vector and the rotary
+ * position rotation in one pass, the step before a cache write:
+ *   y = x / sqrt(mean_i(x_i^2) + eps) * w
+ *   (y_i, y_j) <- (y_i cos - y_j sin, y_j cos + y_i sin)
+ * over the rot_dim / 2 pairs of the first rot_dim elements: (i, i + rot_dim / 2),
+ * or (2 i, 2 i + 1) with interleaved != 0; later elements are only normed.
+ * fp32 arithmetic, one rounding to bf16 (nearest even).
+ *
+ * q, k: bf16, element (t, h, i) at q[t*q_token_stride + h*head_size + i], h <
+ *   num_q_heads (k: num_kv_heads); q_out, k_out likewise.  16-byte aligned,
+ *   strides multiples of 8 elements.  An output may be its input (same
+ *   pointer and stride); other overlaps are not allowed.
+ * q_weight, k_weight: bf16 [head_size], 16-byte aligned, or both NULL: no norm.
+ * positions: int64 [num_tokens], 8-byte aligned.  cos_sin: float
+ *   [max_position][rot_dim], 16-byte aligned: the rot_dim / 2 cosines of a
+ *   position, then the sines.  Neither is read when rot_dim == 0.  A token
+ *   whose position is outside [0, max_position) is skipped (its output rows are
+ *   not written) and sets KV_INT4_DEV_BAD_POS.
+ * rot_dim: a multiple of 16 in [0, head_size] (KV_INT4_ERR_ROT otherwise).
+ * eps >= 0 (KV_INT4_ERR_SIZE otherwise, or for NaN).  num_tokens == 0 is a no-op.
+ */
+KVINT4_API int kv_qk_norm_rope(const void* q, int64_t q_token_stride, const void* k, int64_t k_token_stride,
+                               int num_tokens, int num_q_heads, int num_kv_heads, int head_size,
+                               const void* q_weight, const void* k_weight, float eps, const int64_t* positions,
+                               const float* cos_sin, int64_t max_position, int rot_dim, int interleaved,
+                               void* q_out, int64_t q_out_token_stride, void* k_out, int64_t k_out_token_stride,
+                               int32_t* dev_status, void* stream);
+
+/*
  * kv_int4_rht -- the block-diagonal randomized Hadamard rotation on its own:
  * the rotation the write path applies to K and V before quantising them (the
  * pages' single_rht step), and its inverse.
@@ -415,7 +538,8 @@ KVINT4_API int kv_int4_selftest_wait(int iterations, int32_t* dev_status, uint64
 /* kv_int4_version -- the library's ABI version: 4 (2: kv_int4_rht and the int8_per_token_head
  * entry points kv_int8_write / kv_int8_attention, sliding_window in the attention entry points;
  * 3: the in-slot entry points, kv_int4_attention_noalloc's window argument, kv_int4_selftest_wait;
- * 4: kv_int4_selftest_wait takes its stream as void*, like every other entry point). */
+ * 4: kv_int4_selftest_wait takes its stream as void*, like every other entry point; the kv_fp8_*
+ * entry points and kv_qk_norm_rope came under version 4 too, which changed nothing that was there). */
 KVINT4_API int kv_int4_version(void);
 
 #ifdef __cplusplus

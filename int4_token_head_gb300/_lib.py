@@ -63,10 +63,27 @@ _SIGNATURES = {
     "kv_int4_version": (c_int, []),
 }
 
+# the FP8 block-scaled cache and the step before it
+_SIGNATURES_FP8 = {
+    "kv_fp8_write": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int, c_void_p, c_void_p, c_int, c_int,
+                             c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_void_p,
+                             c_void_p]),
+    "kv_fp8_read": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_int, c_int,
+                            c_int, c_void_p, c_int64, c_void_p, c_int64, c_int, c_int, c_int, c_int, c_void_p,
+                            c_void_p]),
+    "kv_fp8_attention": (c_int, [c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_void_p,
+                                 c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_float,
+                                 c_int, c_int, c_void_p, c_int64, c_void_p, c_size_t, c_void_p, c_void_p]),
+    "kv_qk_norm_rope": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_int, c_int, c_int, c_int, c_void_p, c_void_p,
+                                c_float, c_void_p, c_void_p, c_int64, c_int, c_int, c_void_p, c_int64, c_void_p,
+                                c_int64, c_void_p, c_void_p]),
+}
+
 OK = 0
 ERR_SCRATCH_LIMIT = 9
 NOALLOC_SCRATCH_BYTES = 64 << 20
 DEV_BAD_SLOT, DEV_BAD_BLOCK, DEV_BAD_SEQ, DEV_BAD_SIGNS, DEV_TIMEOUT = 1, 2, 4, 8, 16
+DEV_NONFINITE, DEV_BAD_POS = 32, 64
 
 
 class KvInt4Error(RuntimeError):
@@ -85,7 +102,7 @@ def load(path: Optional[str] = None):
         # locally modified one); otherwise the in-tree library is built if stale.
         p = path or os.environ.get("KVINT4_LIBRARY") or _build.build()
         lib = ctypes.CDLL(p)
-        for name, (res, args) in _SIGNATURES.items():
+        for name, (res, args) in {**_SIGNATURES, **_SIGNATURES_FP8}.items():
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
@@ -397,3 +414,155 @@ def attention_inslot(q, kv_cache, block_table, seq_lens, query_start_loc, max_qu
         _check(signs is not None and signs.dtype == torch.int8 and signs.numel() == d, "signs must be int8 [d]")
         code = lib.kv_int4_attention_inslot(*common, _ptr(signs), *tail)
     _raise(code, "kv_int8_attention_inslot" if int8 else "kv_int4_attention_inslot")
+
+
+# ---------------------------------------------------------------------------
+# FP8 (E4M3) cache with one power-of-two scale per (block, kv head)
+# ---------------------------------------------------------------------------
+def _on_device(tensors, stream, call) -> int:
+    """call(raw stream) with the tensors' device current; they must share one CUDA device."""
+    dev = tensors[0].device
+    for t in tensors:
+        _check(t is None or t.device == dev, "tensors must be on one device")
+    _check(dev.type == "cuda", "tensors must be on a CUDA device")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    raw = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if dev.index == torch.cuda.current_device():
+        return call(raw)
+    with torch.cuda.device(dev):
+        return call(raw)
+
+
+def _status_ptr(dev_status: Optional[torch.Tensor]):
+    if dev_status is None:
+        return None
+    _check(dev_status.dtype == torch.int32 and dev_status.numel() >= 1, "dev_status must be int32 [1]")
+    return dev_status.data_ptr()
+
+
+def _cache_dims_fp8(k_cache, v_cache, k_scale, v_scale):
+    _check(k_cache.dtype in (torch.float8_e4m3fn, torch.uint8) and v_cache.dtype == k_cache.dtype,
+           "fp8 caches must be float8_e4m3fn (or its bytes as uint8)")
+    shape = k_cache.shape
+    _check(len(shape) == 4 and shape == v_cache.shape, "caches must be [blocks, block_size, heads, d]")
+    _check(k_cache.is_contiguous() and v_cache.is_contiguous(), "caches must be contiguous")
+    nb, bs, hkv, d = shape
+    for s in (k_scale, v_scale):
+        _check(s.dtype == torch.float32 and s.shape == (nb, hkv) and s.is_contiguous(),
+               "scale caches must be contiguous float32 [blocks, heads]")
+    return nb, bs, hkv, d
+
+
+def _sequences(block_table, seq_lens, start_loc):
+    _check(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.is_contiguous(),
+           "block_table must be contiguous int32 [seqs, max_blocks]")
+    _check(seq_lens.dtype == torch.int32 and start_loc.dtype == torch.int32 and seq_lens.dim() == 1 and
+           start_loc.dim() == 1 and seq_lens.is_contiguous() and start_loc.is_contiguous(),
+           "sequence lengths and start locations must be contiguous int32 vectors")
+    num_seqs, width = block_table.shape
+    _check(seq_lens.shape[0] == num_seqs and start_loc.shape[0] == num_seqs + 1, "metadata shapes")
+    return num_seqs, width
+
+
+def write_fp8(k, v, block_table, seq_lens, start_loc, max_len, k_cache, v_cache, k_scale, v_scale,
+              dev_status: Optional[torch.Tensor] = None, stream=None):
+    """Quantise each sequence's last start_loc[i+1] - start_loc[i] positions into
+    the FP8 cache through kv_fp8_write (max_len bounds those counts)."""
+    nb, bs, hkv, d = _cache_dims_fp8(k_cache, v_cache, k_scale, v_scale)
+    num_seqs, width = _sequences(block_table, seq_lens, start_loc)
+    ks = _token_major(k, "k", hkv, d)
+    vs = _token_major(v, "v", hkv, d)
+    _check(k.shape[0] == v.shape[0], "k and v disagree on tokens")
+    code = _on_device(
+        (k, v, block_table, seq_lens, start_loc, k_cache, v_cache, k_scale, v_scale, dev_status), stream,
+        lambda st: load().kv_fp8_write(k.data_ptr(), ks, v.data_ptr(), vs, block_table.data_ptr(), width,
+                                       seq_lens.data_ptr(), start_loc.data_ptr(), num_seqs, k.shape[0], int(max_len),
+                                       k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                       v_scale.data_ptr(), nb, bs, hkv, d, _status_ptr(dev_status), st))
+    _raise(code, "kv_fp8_write")
+
+
+def read_fp8(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, start_loc, max_len, k, v,
+             dev_status: Optional[torch.Tensor] = None, stream=None):
+    """Write each sequence's last start_loc[i+1] - start_loc[i] positions of the
+    FP8 cache to k and v (bf16 [tokens, heads, d]) through kv_fp8_read."""
+    nb, bs, hkv, d = _cache_dims_fp8(k_cache, v_cache, k_scale, v_scale)
+    num_seqs, width = _sequences(block_table, seq_lens, start_loc)
+    ks = _token_major(k, "k", hkv, d)
+    vs = _token_major(v, "v", hkv, d)
+    _check(k.shape[0] == v.shape[0], "k and v disagree on tokens")
+    code = _on_device(
+        (k, v, block_table, seq_lens, start_loc, k_cache, v_cache, k_scale, v_scale, dev_status), stream,
+        lambda st: load().kv_fp8_read(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                      block_table.data_ptr(), width, seq_lens.data_ptr(), start_loc.data_ptr(),
+                                      num_seqs, k.shape[0], int(max_len), k.data_ptr(), ks, v.data_ptr(), vs, nb, bs,
+                                      hkv, d, _status_ptr(dev_status), st))
+    _raise(code, "kv_fp8_read")
+
+
+def attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, query_start_loc,
+                  max_query_len, max_seq_len, softmax_scale, causal, out, workspace,
+                  dev_status: Optional[torch.Tensor] = None, stream=None, sliding_window: int = 0):
+    """Attention over the FP8 cache through kv_fp8_attention; writes ``out`` in
+    place.  With ``causal`` false, queries may attend keys of any length."""
+    nb, bs, hkv, d = _cache_dims_fp8(k_cache, v_cache, k_scale, v_scale)
+    num_seqs, width = _sequences(block_table, seq_lens, query_start_loc)
+    _check(q.dim() == 3, "q must be [tokens, q_heads, d]")
+    tokens, hq = q.shape[:2]
+    qs = _token_major(q, "q", hq, d)
+    os_ = _token_major(out, "out", hq, d)
+    _check(out.shape[0] == tokens, "out must match q")
+    _check(workspace.dtype == torch.uint8 and workspace.is_contiguous(), "workspace must be contiguous uint8")
+    code = _on_device(
+        (q, out, block_table, seq_lens, query_start_loc, k_cache, v_cache, k_scale, v_scale, workspace, dev_status),
+        stream,
+        lambda st: load().kv_fp8_attention(q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(),
+                                           k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), width,
+                                           seq_lens.data_ptr(), query_start_loc.data_ptr(), num_seqs, tokens,
+                                           int(max_query_len), int(max_seq_len), hq, hkv, d, bs, nb,
+                                           float(softmax_scale), int(bool(causal)), int(sliding_window),
+                                           out.data_ptr(), os_, workspace.data_ptr(), workspace.numel(),
+                                           _status_ptr(dev_status), st))
+    _raise(code, "kv_fp8_attention")
+
+
+def qk_norm_rope(q, k, positions, cos_sin, q_weight, k_weight, eps, q_out, k_out, interleaved: bool = False,
+                 dev_status: Optional[torch.Tensor] = None, stream=None):
+    """RMS norm of every query and key head vector, then the rotary rotation,
+    through kv_qk_norm_rope.
+
+    q, k and their outputs: bf16 [tokens, heads, d] (an output may be its
+    input).  positions: int64 [tokens]; cos_sin: float32 [max_position, rot]
+    (cosines, then sines), or both None for no rotation.  q_weight, k_weight:
+    bf16 [d], or both None for no norm."""
+    _check(q.dim() == 3 and k.dim() == 3, "q and k must be [tokens, heads, d]")
+    tokens, hq, d = q.shape
+    hkv = k.shape[1]
+    qs = _token_major(q, "q", hq, d)
+    ks = _token_major(k, "k", hkv, d)
+    qo = _token_major(q_out, "q_out", hq, d)
+    ko = _token_major(k_out, "k_out", hkv, d)
+    _check(k.shape[0] == q_out.shape[0] == k_out.shape[0] == tokens, "q, k and the outputs disagree on tokens")
+    _check((q_weight is None) == (k_weight is None), "q_weight and k_weight: both or neither")
+    if q_weight is not None:
+        for w in (q_weight, k_weight):
+            _check(w.dtype == torch.bfloat16 and w.shape == (d,) and w.is_contiguous(), "weights must be bfloat16 [d]")
+    _check((cos_sin is None) == (positions is None), "positions and cos_sin: both or neither")
+    max_pos = rot = 0
+    if cos_sin is not None:
+        _check(cos_sin.dtype == torch.float32 and cos_sin.dim() == 2 and cos_sin.is_contiguous(),
+               "cos_sin must be contiguous float32 [max_position, rot]")
+        _check(positions.dtype == torch.int64 and positions.shape == (tokens,) and positions.is_contiguous(),
+               "positions must be contiguous int64 [tokens]")
+        max_pos, rot = cos_sin.shape
+    code = _on_device(
+        (q, k, q_out, k_out, positions, cos_sin, q_weight, k_weight, dev_status), stream,
+        lambda st: load().kv_qk_norm_rope(q.data_ptr(), qs, k.data_ptr(), ks, tokens, hq, hkv, d,
+                                          None if q_weight is None else q_weight.data_ptr(),
+                                          None if k_weight is None else k_weight.data_ptr(), float(eps),
+                                          None if positions is None else positions.data_ptr(),
+                                          None if cos_sin is None else cos_sin.data_ptr(), max_pos, rot,
+                                          int(bool(interleaved)), q_out.data_ptr(), qo, k_out.data_ptr(), ko,
+                                          _status_ptr(dev_status), st))
+    _raise(code, "kv_qk_norm_rope")

@@ -92,10 +92,6 @@ bool workspace_layout(int num_seqs, int num_q_tokens, int num_q_heads, int num_k
   return true;
 }
 
-static bool head_size_ok(int d) { return d == 64 || d == 96 || d == 128 || d == 192 || d == 256; }
-static bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-static bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
-
 }  // namespace kvint4
 
 using namespace kvint4;
@@ -117,6 +113,7 @@ const char* kv_int4_status_string(int status) {
     case KV_INT4_ERR_WORKSPACE: return "workspace is NULL or smaller than kv_int4_attention_workspace_size()";
     case KV_INT4_ERR_SIZE: return "a count is negative or a size overflows the index types";
     case KV_INT4_ERR_CUDA: return "a CUDA call or kernel launch failed";
+    case KV_INT4_ERR_ROT: return "rot_dim must be a multiple of 16 between 0 and head_size";
     case KV_INT4_ERR_SCRATCH_LIMIT:
       return "the call needs more workspace than the static no-allocation scratch holds "
              "(KV_INT4_NOALLOC_SCRATCH_BYTES); use kv_int4_attention with a caller workspace";

@@ -1,0 +1,198 @@
+// kv_fp8_attention for sm_103a: varlen prefill + decode with GQA over the
+// paged E4M3 cache with one power-of-two scale per (block, kv head).
+//
+// With key p in block b, ks_b = 2^kk, vs_b = 2^kv, codes ck_p and cv_p:
+//   s_p = softmax_scale * ks_b * q . ck_p
+//   out = sum_p 2^(s_p log2 e) vs_b cv_p / sum_p 2^(s_p log2 e)
+// The V scale joins the exponent: with t_p = s_p log2 e + kv_b and the running
+// maximum M of t, the weights w_p = 2^(t_p - M) never exceed 1, whatever the
+// V scales are, so they fit f16 MMA operands without a range limit on V; the
+// denominator in the same units is sum_b 2^-kv_b sum_{p in b} w_p (a block's
+// sum times a power of two, fp32).  A score costs one FMA (scale and kv
+// together) and one exp2.
+// Queries are used at full precision too: a row is divided by the power of two
+// of its largest magnitude (bf16 to f16, exact but for elements 2^-14 of the
+// largest, whose f16 spacing is 2^-24 of it) and that power multiplies the
+// fp32 score.  Codes convert to f16 exactly (cvt.rn.f16x2.e4m3x2).
+//
+// Launches, all on the caller's stream: the schedule (one CTA), prefill (if a
+// sequence may need it), decode, merge.
+
+#include <type_traits>
+
+#include "common.cuh"
+#include "fp8.cuh"
+#include "internal.h"
+#include "schedule.cuh"
+
+namespace kvint4 {
+namespace {
+
+__global__ void __launch_bounds__(kPrepThreads) plan_fp8_kernel(Common c, PlanView pv) { build_schedule<true>(c, pv); }
+
+// A query row's power of two from its largest bf16 magnitude bits: rows are
+// multiplied by 2^-e (so that |q'| < 2) and scores by 2^e.  Rows of zeros and
+// subnormals use the smallest exponent; rows with an infinity or NaN end as NaN.
+__device__ __forceinline__ int q_exponent(uint32_t amax_bits) {
+  return min(max((int)(amax_bits >> 7) - 127, -126), 126);
+}
+
+#include "decode_fp8.cuh"
+#include "prefill_fp8.cuh"
+
+// ---------------------------------------------------------------------------
+// host launcher
+// ---------------------------------------------------------------------------
+template <int D>
+int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
+  WorkspaceLayout L;
+  workspace_layout(a.num_seqs, a.num_q_tokens, a.num_q_heads, a.num_kv_heads, a.head_size, &L);
+  const PlanView pv = plan_view(a.workspace, L);
+  const int dev = current_device();
+  const int sms = sm_count(dev);
+  Common c{};
+  c.q = static_cast<const uint16_t*>(a.q);
+  c.q_stride = a.q_stride;
+  c.k_cache = a.k_cache;
+  c.v_cache = a.v_cache;
+  c.k_scale = a.k_scale;
+  c.v_scale = a.v_scale;
+  c.geo = a.geo;
+  c.block_table = a.block_table;
+  c.max_blocks = a.max_blocks_per_seq;
+  c.seq_lens = a.seq_lens;
+  c.qsl = a.query_start_loc;
+  c.num_seqs = a.num_seqs;
+  c.num_q_tokens = a.num_q_tokens;
+  c.max_qlen = a.max_query_len;
+  c.hq = a.num_q_heads;
+  c.hkv = a.num_kv_heads;
+  c.group = a.num_q_heads / a.num_kv_heads;
+  c.gdiv = FastDiv((uint32_t)c.group);
+  c.num_blocks = a.num_blocks;
+  c.causal = a.causal;
+  c.window = a.sliding_window;
+  c.qscale = a.softmax_scale * kLog2e;
+  c.out = static_cast<uint16_t*>(a.out);
+  c.out_stride = a.out_stride;
+  c.status = a.dev_status;
+  c.max_items = L.max_prefill_items;
+  c.tile_tokens = kPrefillRows / c.group;
+
+  // decode: blocks per position, kv heads per CTA, CTAs
+  c.hg = c.ng = c.nl = c.np = 1;
+  const bool any_decode = c.group <= kDecodeCols;
+  int dec_grid = 0;
+  if (any_decode) {
+    static PerContext<int> occ_cache[3][5];
+    int occ = 0;
+    auto take = [&](auto np_tag) {
+      constexpr int NP = decltype(np_tag)::value;
+      using G = Fp8Dec<D, NP>;
+      c.np = NP;
+      // the largest divisor of Hkv up to 4 whose ring leaves room for two CTAs per SM
+      for (int h = 4; h >= 1; h--)
+        if (a.num_kv_heads % h == 0 && (h == 1 || 2 * (G::smem_bytes(h) + 1024) <= 228 * 1024)) {
+          c.hg = h;
+          break;
+        }
+      return occ_cache[NP / 2][c.hg].get(dev, [&](int* v) {
+        int unused;  // the attribute is raised once, to the largest ring in use
+        return configure(decode_fp8_kernel<D, NP>, (228 * 1024) / 2 - 1024, 128, &unused) &&
+               cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, decode_fp8_kernel<D, NP>, c.hg * 32,
+                                                             G::smem_bytes(c.hg)) == cudaSuccess && *v >= 1;
+      }, &occ);
+    };
+    // query columns of the batch's decode sequences: paired blocks need at
+    // most four, four blocks at most two; when the batch also holds prefills
+    // decode is sized for single-token queries and longer ones go to prefill
+    const long long mq = (long long)(a.max_query_len > 0 ? a.max_query_len : 1) * c.group;
+    const long long cols = mq <= kDecodeCols ? mq : c.group;
+    bool ok;
+    if (cols > 4)
+      ok = take(std::integral_constant<int, 1>{});
+    else if (cols > 2 || !kFp8Quad<D>)
+      ok = take(std::integral_constant<int, 2>{});
+    else
+      ok = take(std::integral_constant<int, kFp8Quad<D> ? 4 : 2>{});
+    if (!ok) return KV_INT4_ERR_CUDA;
+    c.ng = a.num_kv_heads / c.hg;
+    long long grid = (long long)sms * occ;
+    if (grid * c.hg > kMaxDecodeWarps) grid = kMaxDecodeWarps / c.hg;
+    // lanes: as many as divide the head groups, so that the groups' slices of
+    // a block's rows are read side by side
+    for (int l = (int)(grid < c.ng ? grid : c.ng); l >= 1; l--)
+      if (c.ng % l == 0) {
+        c.nl = l;
+        break;
+      }
+    dec_grid = (int)(grid / c.nl * c.nl);
+  }
+  c.dcols = kDecodeCols / c.np;
+
+  plan_fp8_kernel<<<1, kPrepThreads, 0, stream>>>(c, pv);
+  if (cudaGetLastError() != cudaSuccess) return KV_INT4_ERR_CUDA;
+
+  const bool may_prefill = c.group > c.dcols || (long long)a.max_query_len * c.group > c.dcols;
+  if (may_prefill) {
+    static PerContext<int> occ_c;
+    int occ = 0;
+    using G = Fp8Pre<D>;
+    if (!occ_c.get(dev, [](int* o) { return configure(prefill_fp8_kernel<D>, G::SMEM, G::THREADS, o); }, &occ))
+      return KV_INT4_ERR_CUDA;
+    long long grid = (long long)sms * occ;
+    if (grid > L.max_prefill_items) grid = L.max_prefill_items;
+    if (grid < 1) grid = 1;
+    timing_begin(kTimedPrefill, stream);
+    prefill_fp8_kernel<D><<<(unsigned)grid, G::THREADS, G::SMEM, stream>>>(c, pv);
+    timing_end(kTimedPrefill, stream);
+    if (cudaGetLastError() != cudaSuccess) return KV_INT4_ERR_CUDA;
+  }
+  if (any_decode) {
+    const Fp8DecParams prm{c, pv, dec_grid};
+    const int threads = c.hg * 32;
+    timing_begin(kTimedDecode, stream);
+    auto go = [&](auto np_tag) {
+      constexpr int NP = decltype(np_tag)::value;
+      decode_fp8_kernel<D, NP><<<dec_grid, threads, Fp8Dec<D, NP>::smem_bytes(c.hg), stream>>>(prm);
+    };
+    if (c.np == 1)
+      go(std::integral_constant<int, 1>{});
+    else if (c.np == 2)
+      go(std::integral_constant<int, 2>{});
+    else
+      go(std::integral_constant<int, kFp8Quad<D> ? 4 : 2>{});
+    timing_end(kTimedDecode, stream);
+    if (cudaGetLastError() != cudaSuccess) return KV_INT4_ERR_CUDA;
+    // merge: a CTA per (sequence, kv head) segment, a warp per query column
+    // and piece lane; lanes enough that each merges about four pieces
+    const long long mcols = (long long)(a.max_query_len > 0 ? a.max_query_len : 1) * c.group;
+    const int cols = (int)(mcols < c.dcols ? mcols : c.dcols);
+    const long long segs = (long long)a.num_seqs * a.num_kv_heads;
+    const long long pieces = 1 + (long long)dec_grid * c.hg / (segs > 0 ? segs : 1);
+    int lanes = 1;
+    while (lanes < 8 && lanes * 4 < pieces && 2 * lanes * cols <= 32) lanes *= 2;
+    if (segs > 0x7fffffff) return KV_INT4_ERR_SIZE;
+    timing_begin(kTimedReduce, stream);
+    merge_fp8_kernel<D><<<(unsigned)segs, cols * lanes * 32, merge_smem<D>(cols, lanes), stream>>>(
+        Fp8MergeParams{c, pv, dec_grid, cols, lanes});
+    timing_end(kTimedReduce, stream);
+    if (cudaGetLastError() != cudaSuccess) return KV_INT4_ERR_CUDA;
+  }
+  return KV_INT4_OK;
+}
+
+}  // namespace
+
+int launch_attention_fp8(const AttnArgs& a, cudaStream_t stream) {
+  switch (a.head_size) {
+    case 64: return launch_attention_t<64>(a, stream);
+    case 96: return launch_attention_t<96>(a, stream);
+    case 128: return launch_attention_t<128>(a, stream);
+    case 192: return launch_attention_t<192>(a, stream);
+    case 256: return launch_attention_t<256>(a, stream);
+    default: return KV_INT4_ERR_HEAD_SIZE;
+  }
+}
+
+}  // namespace kvint4

@@ -1,0 +1,616 @@
+// Split-KV decode over the FP8 cache and the merge of its pieces, included by
+// attention_fp8.cu.
+//
+// Work: lanes of CTAs over the flattened (decode sequence, head group,
+// position) units, each CTA an equal contiguous range of its lane (the
+// schedule of decode.cuh; a position is NP consecutive 16-key blocks that
+// share the MMA's eight query columns, COLS = 8 / NP each).  A CTA has one
+// warp per kv head of its group; all its threads copy the blocks' codes of the
+// group's heads (contiguous runs of the cache) with 16-byte cp.async into a
+// ring of block slots.  Rows behind the sequence's end, absent and unusable
+// blocks are filled with zeros by the copies, so that no stale byte (E4M3 has
+// NaN codes) reaches a product with a zero weight.
+//
+// Per block and head: S^T = K Q'^T with the 16 keys as the MMA's M, K codes
+// straight from shared memory to f16 A fragments (a lane's four consecutive
+// codes are one k-step's four elements: head dimensions are permuted the same
+// way in q'), then the weights' transpose as B operand of O'^T += V^T W^T, V
+// by ldmatrix.trans of byte pairs (one byte permute and two conversions per
+// four codes).
+template <int D, int NP>
+struct Fp8Dec {
+  static constexpr int COLS = kDecodeCols / NP;
+  static constexpr int CHR = D / 16;  // 16-byte chunks per code row
+  // rows of a power-of-two number of chunks: chunk c of row r at chunk
+  // c ^ swz(r), which spreads both an ldmatrix piece (8 rows, one chunk) and a
+  // quarter-warp's K loads (2 rows, 4 chunks) over all banks; other row sizes
+  // (96 and 192 bytes) do so for K as they are and for V with 16 bytes more
+  static constexpr bool SWZ = (CHR & (CHR - 1)) == 0;
+  static constexpr int VROW = SWZ ? D : D + 16;
+  static constexpr int KTILE = 16 * D;
+  static constexpr int VTILE = 16 * VROW;
+  // neighbouring heads' rows in different bank halves
+  static constexpr int HTILE = (KTILE + VTILE + 63) / 128 * 128 + 64;
+  static constexpr int NS = NP == 1 ? 4 : NP == 2 ? 5 : 8;  // block slots
+  static constexpr int WAIT = NS - 2 * NP;                  // copy groups that may stay pending
+  static constexpr int KSTEPS = D / 16;
+  // head tiles, then the scales [K/V][hg]
+  __host__ __device__ static constexpr int slot_bytes(int hg) { return hg * HTILE + 32; }
+  __host__ __device__ static constexpr int smem_bytes(int hg) { return NS * slot_bytes(hg) + 32; }
+  __host__ __device__ static constexpr int swz(int r) {
+    return CHR >= 8 ? ((r & 1) << 2) | ((r >> 1) & 3) : (r >> 1) & 3;
+  }
+  static_assert(WAIT >= 0 && HTILE % 16 == 0, "ring");
+};
+
+// head sizes with four blocks per position (queries of at most two columns):
+// where the eight-slot ring of four heads leaves room for two CTAs per SM
+template <int D>
+constexpr bool kFp8Quad = 2 * (Fp8Dec<D, 4>::smem_bytes(4) + 1024) <= 228 * 1024;
+
+struct Fp8Walk {
+  int i;     // decode sequence
+  int grp;   // head group (grp mod nl = lane)
+  int lane;
+  int kp;    // position within the sequence
+  int npos;  // positions of the sequence
+  int fb;    // first block read (the sliding window's)
+  int seq;   // sequence id
+  int len;   // keys
+};
+
+struct Fp8DecParams {
+  Common c;
+  PlanView pv;
+  int num_ctas;
+};
+
+template <int NP>
+__device__ __forceinline__ void fp8_walk_load(Fp8Walk& w, const Common& c, const PlanView& pv) {
+  const int4 di = pv.dseq[w.i];  // (sequence, seq_len, first query token, q_len)
+  w.seq = di.x;
+  w.len = di.y;
+  w.fb = first_block(c, di.y, di.w);
+  w.npos = ((di.y + 15) / 16 - w.fb + NP - 1) / NP;
+}
+// the next unit of the lane (there is one: the caller counts)
+template <int NP>
+__device__ __forceinline__ void fp8_walk_next(Fp8Walk& w, const Common& c, const PlanView& pv) {
+  if (++w.kp == w.npos) {
+    w.kp = 0;
+    if ((w.grp += c.nl) >= c.ng) {
+      w.grp = w.lane;
+      do {
+        ++w.i;
+        fp8_walk_load<NP>(w, c, pv);
+      } while (w.npos == 0);  // sequences without keys have no units
+    }
+  }
+}
+
+// head dimension of element 0 of lane quarter cq's k-step s: the lane reads
+// whole 16-byte chunks cq, cq + 4, ... of a swizzled row, else its contiguous quarter
+template <int D>
+__device__ __forceinline__ int fp8_kdim(int cq, int s) {
+  if constexpr (Fp8Dec<D, 1>::SWZ) return 16 * (cq + 4 * (s >> 2)) + 4 * (s & 3);
+  else return cq * (D / 4) + 4 * s;
+}
+
+template <int D, int NP>
+__global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
+  using G = Fp8Dec<D, NP>;
+  const Common& c = prm.c;
+  const PlanView& pv = prm.pv;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int HG = c.hg;
+  const int tid = threadIdx.x, nthr = HG * 32;
+  const int hl = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, cq = lane & 3;
+  const int SB = G::slot_bytes(HG);
+  int* sflag = reinterpret_cast<int*>(smem + G::NS * SB);
+
+  const int n_dseq = pv.plan[0];
+  if (n_dseq == 0) return;
+  const int gpl = c.ng / c.nl;  // head groups per lane
+  const int my_lane = blockIdx.x % c.nl, rr = blockIdx.x / c.nl;
+  const long long Tu = pv.dprefix[n_dseq] * gpl;
+  const int R = prm.num_ctas / c.nl;
+  const long long P0 = Tu * rr / R, P1 = Tu * (rr + 1) / R;
+  if (P0 >= P1) return;
+  const int nunits = (int)(P1 - P0);
+
+  // largest i with dprefix[i] * gpl <= P0 (32-ary search, per warp)
+  int lo = 0, hi = n_dseq;
+  while (hi - lo > 1) {
+    const long long span = hi - lo;
+    const int probe = lo + (int)((span * lane) / 32);
+    const bool le = lane == 0 || pv.dprefix[probe] * gpl <= P0;
+    const unsigned m = __ballot_sync(0xffffffffu, le);
+    const int last = 31 - __clz(m);
+    const int nlo = lo + (int)((span * last) / 32);
+    const int nhi = last == 31 ? hi : lo + (int)((span * (last + 1)) / 32);
+    lo = nlo;
+    hi = nhi > nlo ? nhi : nlo + 1;
+  }
+  Fp8Walk cw;
+  cw.i = lo;
+  cw.lane = my_lane;
+  fp8_walk_load<NP>(cw, c, pv);
+  {
+    const long long off = P0 - pv.dprefix[cw.i] * gpl;
+    const int gs = (int)(off / cw.npos);
+    cw.grp = gs * c.nl + my_lane;
+    cw.kp = (int)(off - (long long)gs * cw.npos);
+  }
+  Fp8Walk pw = cw;
+
+  // staging: chunk index ((kv * 16 + r) * HG + h) * CHR + col, CHR chunks
+  // a thread; consecutive threads read consecutive bytes
+  uint32_t c_saddr[G::CHR];      // shared address within slot 0
+  const uint8_t* c_src[G::CHR];  // cache address within block 0, head group 0
+#pragma unroll
+  for (int j = 0; j < G::CHR; j++) {
+    const int idx = tid + nthr * j;
+    const int col = idx % G::CHR, rest = idx / G::CHR;
+    const int h = rest % HG, kvr = rest / HG;
+    const int kv = kvr / 16, r = kvr % 16;
+    const int pos = G::SWZ ? col ^ G::swz(r) : col;
+    c_saddr[j] = smem_addr(smem) + h * G::HTILE + (kv ? G::KTILE + r * G::VROW : r * D) + pos * 16;
+    c_src[j] = (kv ? c.v_cache : c.k_cache) + r * c.geo.crow + (long long)h * D + col * 16;
+  }
+  const uint32_t s_saddr = smem_addr(smem) + HG * G::HTILE + tid * 4;  // scale [K/V][h], threads 0 .. 2 hg - 1
+  const float* s_src = tid < HG ? c.k_scale + tid : c.v_scale + (tid - HG);
+
+  // block j of a position
+  auto block_at = [&](const Fp8Walk& w, int j) {
+    const int kb = w.fb + w.kp * NP + j;
+    return kb * 16 < w.len ? c.block_table[(long long)w.seq * c.max_blocks + kb] : -1;
+  };
+  auto issue = [&](int blk, int kb, int len, int grp, int slot) {
+    const bool ok = blk >= 0 && blk < c.num_blocks;
+    const int rows = ok ? len - kb * 16 : 0;  // rows that hold keys (<= 0: an absent block)
+    const uint32_t soff = (uint32_t)(slot * SB);
+    const uint64_t base = ok ? (uint64_t)(uint32_t)blk * (uint64_t)c.geo.cblk + (uint64_t)(grp * HG) * D : 0;
+    if (rows >= 16) {
+#pragma unroll
+      for (int j = 0; j < G::CHR; j++)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(c_saddr[j] + soff), "l"(c_src[j] + base));
+    } else {
+#pragma unroll
+      for (int j = 0; j < G::CHR; j++) {
+        const int r = (tid + nthr * j) / G::CHR / HG % 16;
+        const bool in = r < rows;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(c_saddr[j] + soff),
+                     "l"(in ? c_src[j] + base : c.k_cache), "r"(in ? 16 : 0));
+      }
+    }
+    if (tid < 2 * HG) {
+      const float* src = ok ? s_src + (uint64_t)(uint32_t)blk * (uint64_t)c.hkv + grp * HG : c.k_scale;
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(s_saddr + soff), "l"(src), "r"(ok ? 4 : 0));
+    }
+    if (tid == 0) {
+      sflag[slot] = ok;
+      if (!ok && kb * 16 < len) flag(c.status, KV_INT4_DEV_BAD_BLOCK);
+    }
+  };
+  // producer: one block per call into the next ring slot, the next block id
+  // loaded one call ahead; one commit group per call (empty past the range)
+  int ppos = 0, pj = 0, ps = 0;
+  int pblk = block_at(pw, 0);
+  auto produce = [&]() {
+    if (ppos < nunits) {
+      issue(pblk, pw.fb + pw.kp * NP + pj, pw.len, pw.grp, ps);
+      ps = ps + 1 == G::NS ? 0 : ps + 1;
+      if (++pj == NP) {
+        pj = 0;
+        if (++ppos < nunits) fp8_walk_next<NP>(pw, c, pv);
+      }
+      if (ppos < nunits) pblk = block_at(pw, pj);
+    }
+    cp_async_commit();
+  };
+#pragma unroll 1
+  for (int s = 0; s < G::NS - NP; s++) produce();
+
+  // per-segment state of this warp's head
+  uint32_t qb[G::KSTEPS][2];
+  float oacc[G::KSTEPS][4];
+  float m0, m1, l0, l1;
+  float cf0, cf1;  // score factor of columns 2cq, 2cq+1: 2^e of the query row * softmax_scale * log2 e
+  int lim0, lim1, lo0, lo1;  // keys visible to the columns: positions [lo, lim)
+  int lim_warp, lo_warp;     // smallest limit, largest first position of all columns
+  bool first_piece = cw.kp == 0;
+
+  auto begin_segment = [&]() {
+    const int head = cw.grp * HG + hl;
+    const int4 di = pv.dseq[cw.i];
+    const int q0 = di.z, ql = di.w, L = di.y;
+    const int ctx = L - ql;
+    // B fragments of this lane's column g, which holds query column g % COLS
+    const int n = g & (G::COLS - 1);
+    const bool colok = n < ql * c.group;
+    const int j = n / c.group, jj = n - j * c.group;
+    const uint16_t* qrow = c.q + (long long)(q0 + (colok ? j : 0)) * c.q_stride +
+                           (long long)(head * c.group + (colok ? jj : 0)) * D;
+    uint2 qv[G::KSTEPS];
+    uint32_t am = 0;
+#pragma unroll
+    for (int s = 0; s < G::KSTEPS; s++) {
+      qv[s] = make_uint2(0, 0);
+      if (colok) qv[s] = *reinterpret_cast<const uint2*>(qrow + fp8_kdim<D>(cq, s));
+      am = __vmaxu2(am, __vmaxu2(qv[s].x & 0x7fff7fffu, qv[s].y & 0x7fff7fffu));
+    }
+    am = max(am & 0xffffu, am >> 16);
+    am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+    am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+    const int e = q_exponent(am);
+    const float mul = exp2_int(-e);
+#pragma unroll
+    for (int s = 0; s < G::KSTEPS; s++) {
+      qb[s][0] = pack_f16x2(bf16lo_to_f32(qv[s].x) * mul, bf16hi_to_f32(qv[s].x) * mul);
+      qb[s][1] = pack_f16x2(bf16lo_to_f32(qv[s].y) * mul, bf16hi_to_f32(qv[s].y) * mul);
+    }
+    const float cf = c.qscale * exp2_int(e);
+    cf0 = __shfl_sync(0xffffffffu, cf, 8 * cq);      // column 2 cq is held by lanes 4 (2 cq) ..
+    cf1 = __shfl_sync(0xffffffffu, cf, 8 * cq + 4);
+    const int col0 = (2 * cq) & (G::COLS - 1), col1 = (2 * cq + 1) & (G::COLS - 1);
+    const int j0 = min(col0 / c.group, max(ql - 1, 0)), j1 = min(col1 / c.group, max(ql - 1, 0));
+    lim0 = c.causal ? min(L, ctx + j0 + 1) : L;
+    lim1 = c.causal ? min(L, ctx + j1 + 1) : L;
+    lo0 = window_lo(c, ctx + j0);
+    lo1 = window_lo(c, ctx + j1);
+    lim_warp = __reduce_min_sync(0xffffffffu, min(lim0, lim1));
+    lo_warp = __reduce_max_sync(0xffffffffu, max(lo0, lo1));
+#pragma unroll
+    for (int i = 0; i < G::KSTEPS; i++) oacc[i][0] = oacc[i][1] = oacc[i][2] = oacc[i][3] = 0.f;
+    m0 = m1 = -INFINITY;
+    l0 = l1 = 0.f;
+  };
+
+  auto flush = [&]() {
+    float a0 = l0, a1 = l1;
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      a0 += __shfl_xor_sync(0xffffffffu, a0, o);
+      a1 += __shfl_xor_sync(0xffffffffu, a1, o);
+    }
+    float mm0 = m0, mm1 = m1;
+    if constexpr (NP == 4) {
+      // the four blocks' columns c, c + 2, c + 4, c + 6 hold the same queries:
+      // merged here, so that a piece leaves columns 0 and 1 only
+#pragma unroll
+      for (int x = 1; x < 4; x <<= 1) {
+        const float p0 = __shfl_xor_sync(0xffffffffu, mm0, x), p1 = __shfl_xor_sync(0xffffffffu, mm1, x);
+        const float n0 = fmaxf(mm0, p0), n1 = fmaxf(mm1, p1);
+        const float u0 = n0 == -INFINITY ? 0.f : n0, u1 = n1 == -INFINITY ? 0.f : n1;
+        const float sa0 = fast_exp2(mm0 - u0), sb0 = fast_exp2(p0 - u0);
+        const float sa1 = fast_exp2(mm1 - u1), sb1 = fast_exp2(p1 - u1);
+        a0 = a0 * sa0 + __shfl_xor_sync(0xffffffffu, a0, x) * sb0;
+        a1 = a1 * sa1 + __shfl_xor_sync(0xffffffffu, a1, x) * sb1;
+#pragma unroll
+        for (int i = 0; i < G::KSTEPS; i++) {
+          oacc[i][0] = oacc[i][0] * sa0 + __shfl_xor_sync(0xffffffffu, oacc[i][0], x) * sb0;
+          oacc[i][2] = oacc[i][2] * sa0 + __shfl_xor_sync(0xffffffffu, oacc[i][2], x) * sb0;
+          oacc[i][1] = oacc[i][1] * sa1 + __shfl_xor_sync(0xffffffffu, oacc[i][1], x) * sb1;
+          oacc[i][3] = oacc[i][3] * sa1 + __shfl_xor_sync(0xffffffffu, oacc[i][3], x) * sb1;
+        }
+        mm0 = n0;
+        mm1 = n1;
+      }
+      if (cq > 0) return;
+    }
+    float* dst_o;
+    float* dst_ml;
+    if (first_piece) {
+      const long long slot = (long long)cw.i * c.hkv + cw.grp * HG + hl;
+      dst_o = pv.direct_o + slot * kDecodeCols * D;
+      dst_ml = pv.direct_ml + slot * kDecodeCols * 2;
+    } else {
+      const long long slot = (long long)blockIdx.x * HG + hl;
+      dst_o = pv.warp_o + slot * kDecodeCols * D;
+      dst_ml = pv.warp_ml + slot * kDecodeCols * 2;
+    }
+    // m-tile t holds d = 16 t + 2g (row g) and 16 t + 2g + 1 (row g + 8)
+    float* o0 = dst_o + (2 * cq) * D + 2 * g;
+    float* o1 = dst_o + (2 * cq + 1) * D + 2 * g;
+#pragma unroll
+    for (int i = 0; i < G::KSTEPS; i++) {
+      *reinterpret_cast<float2*>(o0 + 16 * i) = make_float2(oacc[i][0], oacc[i][2]);
+      *reinterpret_cast<float2*>(o1 + 16 * i) = make_float2(oacc[i][1], oacc[i][3]);
+    }
+    if (g == 0) {
+      dst_ml[(2 * cq) * 2 + 0] = mm0;
+      dst_ml[(2 * cq) * 2 + 1] = a0;
+      dst_ml[(2 * cq + 1) * 2 + 0] = mm1;
+      dst_ml[(2 * cq + 1) * 2 + 1] = a1;
+    }
+  };
+
+  begin_segment();
+  const int jb = (cq * NP) >> 2;  // block of this thread's score columns
+  const int jv = (g * NP) >> 3;   // block of this lane's W^T column g
+  // this lane's ldmatrix row of the V tile: key 8 ((l >> 3) & 1) + (l & 7) of chunk (l >> 4)
+  const int vrow = ((lane >> 3) & 1) * 8 + (lane & 7), vchunk = lane >> 4;
+  const uint32_t v_lane = smem_addr(smem) + hl * G::HTILE + G::KTILE + vrow * G::VROW;
+  const int vx = G::SWZ ? G::swz(vrow) : 0;
+  const int kx0 = G::SWZ ? G::swz(g) : 0, kx1 = G::SWZ ? G::swz(g + 8) : 0;
+  int cs = 0;
+#pragma unroll 1
+  for (int it = 0; it < nunits; it++) {
+    cp_async_wait<G::WAIT>();
+    __syncthreads();  // this position's copies visible; every warp done with the previous slots
+#pragma unroll
+    for (int j = 0; j < NP; j++) produce();
+
+    int slot[NP];
+    slot[0] = cs;
+#pragma unroll
+    for (int j = 1; j < NP; j++) slot[j] = slot[j - 1] + 1 == G::NS ? 0 : slot[j - 1] + 1;
+    bool allok = true;
+    int my = slot[0];
+#pragma unroll
+    for (int j = 0; j < NP; j++) {
+      allok = allok && sflag[slot[j]] != 0;
+      if (j > 0 && jb == j) my = slot[j];
+    }
+    const bool bok = sflag[my] != 0;
+    const float* sc = reinterpret_cast<const float*>(smem + my * SB + HG * G::HTILE) + hl;
+    const float ks = sc[0], vs = sc[HG];
+
+    // ---- S^T = K Q'^T, one accumulator per block ----
+    float sacc[NP][4];
+#pragma unroll
+    for (int j = 0; j < NP; j++) {
+      sacc[j][0] = sacc[j][1] = sacc[j][2] = sacc[j][3] = 0.f;
+      const uint8_t* x = smem + slot[j] * SB + hl * G::HTILE + g * D;
+      const uint8_t* y = x + 8 * D;
+      uint32_t xk[G::KSTEPS], yk[G::KSTEPS];
+      if constexpr (G::SWZ) {
+#pragma unroll
+        for (int i = 0; i < G::CHR / 4; i++) {
+          const uint4 a = *reinterpret_cast<const uint4*>(x + ((cq + 4 * i) ^ kx0) * 16);
+          const uint4 b = *reinterpret_cast<const uint4*>(y + ((cq + 4 * i) ^ kx1) * 16);
+          xk[4 * i] = a.x; xk[4 * i + 1] = a.y; xk[4 * i + 2] = a.z; xk[4 * i + 3] = a.w;
+          yk[4 * i] = b.x; yk[4 * i + 1] = b.y; yk[4 * i + 2] = b.z; yk[4 * i + 3] = b.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < G::KSTEPS / 2; i++) {
+          const uint2 a = *reinterpret_cast<const uint2*>(x + cq * (D / 4) + 8 * i);
+          const uint2 b = *reinterpret_cast<const uint2*>(y + cq * (D / 4) + 8 * i);
+          xk[2 * i] = a.x; xk[2 * i + 1] = a.y;
+          yk[2 * i] = b.x; yk[2 * i + 1] = b.y;
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < G::KSTEPS; s++) {
+        uint32_t a[4];
+        e4m3x4_to_f16x2(xk[s], a[0], a[2]);
+        e4m3x4_to_f16x2(yk[s], a[1], a[3]);
+        mma_16816(sacc[j], a, qb[s][0], qb[s][1]);
+      }
+    }
+    float sa[4] = {sacc[0][0], sacc[0][1], sacc[0][2], sacc[0][3]};
+#pragma unroll
+    for (int j = 1; j < NP; j++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) sa[e] = jb == j ? sacc[j][e] : sa[e];
+
+    const int kb0 = cw.fb + cw.kp * NP;
+    const int pos0 = (kb0 + jb) * 16 + g, pos1 = pos0 + 8;
+    const float f0 = cf0 * ks, f1 = cf1 * ks;
+    const float kvf = (float)exp_of(vs);                                  // log2 of the V scale
+    const float ivs = __uint_as_float((254u << 23) - (__float_as_uint(vs) & 0x7f800000u));  // its reciprocal
+    float t00 = fmaf(sa[0], f0, kvf), t01 = fmaf(sa[1], f1, kvf);
+    float t10 = fmaf(sa[2], f0, kvf), t11 = fmaf(sa[3], f1, kvf);
+    // keys outside a column's visible range (or in an unusable or absent
+    // block) only occur in positions that reach past the smallest limit or
+    // start before the largest window start
+    const bool full = allok && (kb0 + NP) * 16 <= lim_warp && kb0 * 16 >= lo_warp;
+    if (!full) {
+      t00 = (bok && pos0 < lim0 && pos0 >= lo0) ? t00 : -INFINITY;
+      t01 = (bok && pos0 < lim1 && pos0 >= lo1) ? t01 : -INFINITY;
+      t10 = (bok && pos1 < lim0 && pos1 >= lo0) ? t10 : -INFINITY;
+      t11 = (bok && pos1 < lim1 && pos1 >= lo1) ? t11 : -INFINITY;
+    }
+    float mx0 = fmaxf(t00, t10), mx1 = fmaxf(t01, t11);
+    // exact running max: reduced across the key lanes only when some lane
+    // holds a value above its column's current max
+    if (__any_sync(0xffffffffu, mx0 > m0 || mx1 > m1)) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+      }
+      const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
+      const float al0 = mn0 == -INFINITY ? 1.f : fast_exp2(m0 - mn0);  // a column with no key yet keeps -inf
+      const float al1 = mn1 == -INFINITY ? 1.f : fast_exp2(m1 - mn1);
+      m0 = mn0;
+      m1 = mn1;
+      l0 *= al0;
+      l1 *= al1;
+#pragma unroll
+      for (int i = 0; i < G::KSTEPS; i++) {
+        oacc[i][0] *= al0;
+        oacc[i][1] *= al1;
+        oacc[i][2] *= al0;
+        oacc[i][3] *= al1;
+      }
+    }
+    const float mu0 = m0 == -INFINITY ? 0.f : m0, mu1 = m1 == -INFINITY ? 0.f : m1;
+    const float w00 = fast_exp2(t00 - mu0), w01 = fast_exp2(t01 - mu1);
+    const float w10 = fast_exp2(t10 - mu0), w11 = fast_exp2(t11 - mu1);
+    l0 = fmaf(w00 + w10, ivs, l0);
+    l1 = fmaf(w01 + w11, ivs, l1);
+    const uint32_t b0 = movmatrix_trans(pack_f16x2(w00, w01)), b1 = movmatrix_trans(pack_f16x2(w10, w11));
+
+    // ---- O'^T += V^T W^T ----
+#pragma unroll
+    for (int j = 0; j < NP; j++) {
+      // block j's weights only: the other blocks' columns are zero
+      const uint32_t bj0 = NP == 1 || jv == j ? b0 : 0u, bj1 = NP == 1 || jv == j ? b1 : 0u;
+      const uint32_t va = v_lane + slot[j] * SB;
+#pragma unroll
+      for (int p = 0; p < G::CHR / 2; p++) {
+        uint32_t r[4];
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(va + ((2 * p + vchunk) ^ vx) * 16));
+        // a word: bytes (2g, 2g + 1) of keys 2cq and 2cq + 1
+#pragma unroll
+        for (int q = 0; q < 2; q++) {
+          uint32_t a[4];
+          e4m3x4_to_f16x2(__byte_perm(r[2 * q], 0, 0x3120), a[0], a[1]);
+          e4m3x4_to_f16x2(__byte_perm(r[2 * q + 1], 0, 0x3120), a[2], a[3]);
+          mma_16816(oacc[2 * p + q], a, bj0, bj1);
+        }
+      }
+    }
+
+    const bool last_in_seg = cw.kp == cw.npos - 1;
+    const bool last_in_range = it + 1 == nunits;
+    if (last_in_seg || last_in_range) flush();
+    if (!last_in_range) {
+      fp8_walk_next<NP>(cw, c, pv);
+      if (last_in_seg) {
+        first_piece = true;
+        begin_segment();
+      }
+    }
+    cs += NP;
+    if (cs >= G::NS) cs -= G::NS;
+  }
+  cp_async_wait<0>();
+}
+
+// ---------------------------------------------------------------------------
+// merge: the pieces of every segment, normalised and written as bf16
+// ---------------------------------------------------------------------------
+struct Fp8MergeParams {
+  Common c;
+  PlanView pv;
+  int num_ctas;
+  int cols;   // query columns per segment (warps)
+  int lanes;  // piece lanes per column (warps)
+};
+
+template <int D>
+__host__ __device__ constexpr int merge_smem(int cols, int lanes) {
+  return lanes > 1 ? cols * lanes * (D + 2) * 4 : 0;
+}
+
+template <int D>
+__global__ void __launch_bounds__(1024) merge_fp8_kernel(Fp8MergeParams prm) {
+  const Common& c = prm.c;
+  const PlanView& pv = prm.pv;
+  extern __shared__ __align__(16) float spart[];  // [cols][lanes][D + 2]
+  constexpr int PER = D / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int col = warp % prm.cols, pl = warp / prm.cols;
+  const int n_dseq = pv.plan[0];
+  const int seg = blockIdx.x;
+  if (seg >= n_dseq * c.hkv) return;
+  const int i = seg / c.hkv, h = seg - i * c.hkv;
+  const int4 di = pv.dseq[i];  // (sequence, seq_len, first query token, q_len)
+  const int ql = di.w;
+  const int npos = ((di.y + 15) / 16 - first_block(c, di.y, ql) + c.np - 1) / c.np;
+  const int grp = h / c.hg, hl = h - grp * c.hg;
+  const int gpl = c.ng / c.nl, lane_g = grp % c.nl, gs = grp / c.nl;
+  const long long Tu = pv.dprefix[n_dseq] * gpl;
+  const long long sbeg = pv.dprefix[i] * gpl + (long long)gs * npos, send = sbeg + npos;
+  const int W = prm.num_ctas / c.nl;  // the lane's CTAs
+  auto wstart = [&](long long w) { return div_nn(Tu * w, W); };
+  // pieces: the direct slot (the piece that starts the segment), then every
+  // CTA whose range is not empty and starts strictly inside the segment;
+  // candidates are those CTAs or the positions, whichever are fewer
+  long long w_first = 0, cand = 0;
+  bool by_cta = true;
+  if (npos > 0) {
+    w_first = div_nn((sbeg + 1) * W + Tu - 1, Tu);
+    const long long w_end = div_nn(send * W + Tu - 1, Tu);
+    by_cta = w_end - w_first <= npos - 1;
+    cand = 1 + (by_cta ? w_end - w_first : (long long)npos - 1);
+  }
+  const int nsub = c.np == 2 ? 2 : 1;  // paired blocks: columns col and col + dcols hold the same query
+  const bool used = col < ql * c.group;
+  float acc[PER];
+#pragma unroll
+  for (int k = 0; k < PER; k++) acc[k] = 0.f;
+  float M = -INFINITY, Ls = 0.f;
+  auto merge = [&](float m, float l, const float (&o)[PER]) {
+    const float mn = fmaxf(M, m);
+    const float mu = mn == -INFINITY ? 0.f : mn;
+    const float a = fast_exp2(M - mu), b = fast_exp2(m - mu);
+#pragma unroll
+    for (int k = 0; k < PER; k++) acc[k] = acc[k] * a + o[k] * b;
+    Ls = Ls * a + l * b;
+    M = mn;
+  };
+  if (used) {
+    constexpr int CH = 4;  // candidates loaded together
+#pragma unroll 1
+    for (long long k0 = pl; k0 < cand; k0 += (long long)CH * prm.lanes) {
+      float mw[CH][2], lw[CH][2], ov[CH][2][PER];
+#pragma unroll
+      for (int j = 0; j < CH; j++) {
+        const long long k = k0 + (long long)j * prm.lanes;
+        bool ok = k < cand;
+        long long w = 0;
+        if (ok && k > 0) {
+          if (by_cta) {
+            w = w_first + k - 1;
+            ok = wstart(w + 1) > wstart(w);
+          } else {
+            const long long p = sbeg + k;
+            w = div_nn((p + 1) * W + Tu - 1, Tu) - 1;  // last CTA starting at or before p
+            ok = wstart(w) == p;
+          }
+        }
+        const long long sl = (w * c.nl + lane_g) * c.hg + hl;
+        const float* o = ok && k > 0 ? pv.warp_o + sl * kDecodeCols * D : pv.direct_o + (long long)seg * kDecodeCols * D;
+        const float* ml = ok && k > 0 ? pv.warp_ml + sl * kDecodeCols * 2 : pv.direct_ml + (long long)seg * kDecodeCols * 2;
+#pragma unroll
+        for (int sub = 0; sub < 2; sub++) {
+          const bool use = ok && sub < nsub;
+          const int cc = col + sub * c.dcols;
+          mw[j][sub] = use ? ml[cc * 2] : -INFINITY;
+          lw[j][sub] = use ? ml[cc * 2 + 1] : 0.f;
+#pragma unroll
+          for (int e = 0; e < PER; e++) ov[j][sub][e] = use ? o[cc * D + lane + 32 * e] : 0.f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < CH; j++)
+#pragma unroll
+        for (int sub = 0; sub < 2; sub++) merge(mw[j][sub], lw[j][sub], ov[j][sub]);
+    }
+  }
+  if (prm.lanes > 1) {
+    float* mine = spart + (col * prm.lanes + pl) * (D + 2);
+    if (pl > 0) {
+#pragma unroll
+      for (int k = 0; k < PER; k++) mine[lane + 32 * k] = acc[k];
+      if (lane == 0) {
+        mine[D] = M;
+        mine[D + 1] = Ls;
+      }
+    }
+    __syncthreads();
+    if (pl > 0) return;
+#pragma unroll 1
+    for (int p = 1; p < prm.lanes; p++) {
+      const float* o = mine + p * (D + 2);
+      float v[PER];
+#pragma unroll
+      for (int k = 0; k < PER; k++) v[k] = o[lane + 32 * k];
+      merge(o[D], o[D + 1], v);
+    }
+  }
+  if (!used) return;
+  const float inv = Ls == 0.f ? 0.f : 1.f / Ls;  // no visible key: zeros
+  const int j = col / c.group, jj = col - j * c.group;
+  uint16_t* dst = c.out + (long long)(di.z + j) * c.out_stride + (long long)(h * c.group + jj) * D;
+#pragma unroll
+  for (int k = 0; k < PER; k++)
+    dst[lane + 32 * k] = (uint16_t)(pack_bf16x2_rn(acc[k] * inv, 0.f) & 0xffffu);
+}

@@ -75,6 +75,10 @@ struct CacheGeo {
 inline CacheGeo separate_geo(int hkv, int code_bytes) {
   return CacheGeo{16ll * hkv * code_bytes, (int64_t)hkv * code_bytes, code_bytes, 16ll * hkv, hkv, 1};
 }
+// one scale per (block, head): [blocks][Hkv] f32
+inline CacheGeo block_scale_geo(int hkv, int code_bytes) {
+  return CacheGeo{16ll * hkv * code_bytes, (int64_t)hkv * code_bytes, code_bytes, hkv, 0, 1};
+}
 // bytes of one in-slot (token, head) slot: codes + f32 scale, rounded up to 16
 inline int inslot_bytes(int code_bytes) { return (code_bytes + 4 + 15) / 16 * 16; }
 inline CacheGeo inslot_geo(int hkv, int code_bytes) {
@@ -121,6 +125,57 @@ struct WriteArgs {
 int launch_write(const WriteArgs& a, bool prerotated, cudaStream_t stream);
 // int8_per_token_head write (write_int8.cu): caches of d bytes per head vector
 int launch_write_int8(const WriteArgs& a, cudaStream_t stream);
+
+// kv_fp8_write / kv_fp8_read (cache_fp8.cu): k and v are the input or the output
+struct CacheFp8Args {
+  void* k;
+  int64_t k_stride;
+  void* v;
+  int64_t v_stride;
+  const int32_t* block_table;
+  int max_blocks_per_seq;
+  const int32_t* seq_lens;
+  const int32_t* start_loc;
+  int num_seqs;
+  int num_tokens;
+  int max_len;
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  float* k_scale;
+  float* v_scale;
+  int num_blocks;
+  int num_kv_heads;
+  int head_size;
+  int32_t* dev_status;
+};
+int launch_write_fp8(const CacheFp8Args& a, cudaStream_t stream);
+int launch_read_fp8(const CacheFp8Args& a, cudaStream_t stream);
+
+// kv_qk_norm_rope (norm_rope.cu)
+struct NormRopeArgs {
+  const void* q;
+  int64_t q_stride;
+  const void* k;
+  int64_t k_stride;
+  int num_tokens;
+  int num_q_heads;
+  int num_kv_heads;
+  int head_size;
+  const void* q_weight;
+  const void* k_weight;
+  float eps;
+  const int64_t* positions;
+  const float* cos_sin;
+  int64_t max_position;
+  int rot_dim;
+  bool interleaved;
+  void* q_out;
+  int64_t q_out_stride;
+  void* k_out;
+  int64_t k_out_stride;
+  int32_t* dev_status;
+};
+int launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
 
 struct AttnArgs {
   const void* q;
@@ -179,6 +234,16 @@ bool workspace_layout(int num_seqs, int num_q_tokens, int num_q_heads, int num_k
                       int head_size, WorkspaceLayout* out);
 
 int launch_attention(const AttnArgs& a, cudaStream_t stream);
+// FP8 block-scaled cache (attention_fp8.cu): E4M3 codes of d bytes per head
+// vector, one scale per (block, head)
+int launch_attention_fp8(const AttnArgs& a, cudaStream_t stream);
+
+// host-side argument checks shared by the entry points
+inline bool head_size_ok(int d) { return d == 64 || d == 96 || d == 128 || d == 192 || d == 256; }
+inline bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+inline bool aligned16(const void* p) { return aligned(p, 16); }
+// token strides of bf16 rows (elements)
+inline bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0; }
 
 // opt-in kernel timing (timing.cu); kinds match the order documented in kvint4.h
 enum TimedKind { kTimedWrite = 0, kTimedPrep = 1, kTimedPrefill = 2, kTimedDecode = 3, kTimedReduce = 4 };

@@ -1,5 +1,5 @@
-"""Device-side state of a paged INT4 (or int8_per_token_head) KV cache for
-one synthetic workload.
+"""Device-side state of a paged INT4 (or int8_per_token_head, or FP8
+block-scaled) KV cache for one synthetic workload.
 
 Allocates the sentinel-filled caches and metadata on the GPU, populates each
 sequence's history through the library's write path, and runs the step
@@ -20,12 +20,12 @@ from .synthetic import Workload
 
 class PagedKV:
     def __init__(self, w: Workload, device: str = "cuda", fmt: str = "int4"):
-        if fmt not in ("int4", "int8"):
+        if fmt not in ("int4", "int8", "fp8"):
             raise ValueError(f"unknown cache format {fmt!r}")
         self.w = w
         self.device = device
         self.fmt = fmt
-        caches = w.empty_cache(device) if fmt == "int4" else w.empty_cache_int8(device)
+        caches = {"int4": w.empty_cache, "int8": w.empty_cache_int8, "fp8": w.empty_cache_fp8}[fmt](device)
         self.k_cache, self.v_cache, self.k_scale, self.v_scale = caches
         self.signs = w.signs.to(device)
         self.block_table = w.block_table.to(device)
@@ -38,6 +38,8 @@ class PagedKV:
 
     # -------------------------------------------------------------------
     def write(self, k, v, slots, stream=None, prerotated=False):
+        if self.fmt == "fp8":
+            raise ValueError("the fp8 cache is written by sequences: write_tokens()")
         if self.fmt == "int8":
             if prerotated:
                 raise ValueError("the int8 cache stores unrotated vectors")
@@ -46,6 +48,19 @@ class PagedKV:
             return
         _lib.write(k, v, slots, self.k_cache, self.v_cache, self.k_scale, self.v_scale, self.signs,
                    dev_status=self.status, stream=stream, prerotated=prerotated)
+
+    def write_tokens(self, k, v, seq_lens=None, start_loc=None, max_len=None, block_table=None, stream=None):
+        """FP8: write the last start_loc[i+1] - start_loc[i] positions of each
+        sequence (default: the step's new tokens)."""
+        if seq_lens is None:
+            seq_lens, start_loc, max_len = self.seq_lens, self.query_start_loc, self.w.max_query_len
+        _lib.write_fp8(k, v, self.block_table if block_table is None else block_table, seq_lens, start_loc, max_len,
+                       self.k_cache, self.v_cache, self.k_scale, self.v_scale, dev_status=self.status, stream=stream)
+
+    def read_tokens(self, k, v, stream=None):
+        """FP8: the step's tokens (each sequence's last q_len positions) back as bf16."""
+        _lib.read_fp8(self.k_cache, self.v_cache, self.k_scale, self.v_scale, self.block_table, self.seq_lens,
+                      self.query_start_loc, self.w.max_query_len, k, v, dev_status=self.status, stream=stream)
 
     def populate_history(self, gen_device: Optional[str] = None, chunk_tokens: int = 65536,
                          timer: Optional[List[float]] = None):
@@ -59,6 +74,16 @@ class PagedKV:
         w = self.w
         gen_device = gen_device or self.device
         pend_k, pend_v, pend_s, n = [], [], [], 0
+        pend_seq = []  # FP8: the sequences of the pending tokens
+
+        def write_pending(k, v, s):
+            if self.fmt != "fp8":
+                self.write(k, v, s)
+                return
+            lens = [w.seqs[i][1] - w.seqs[i][0] for i in pend_seq]
+            start = torch.tensor([0] + lens).cumsum(0).to(torch.int32).to(self.device)
+            self.write_tokens(k, v, torch.tensor(lens, dtype=torch.int32, device=self.device), start, max(lens),
+                              self.block_table[torch.tensor(pend_seq, device=self.device)])
 
         def flush():
             nonlocal pend_k, pend_v, pend_s, n
@@ -70,13 +95,14 @@ class PagedKV:
             if timer is not None:
                 e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
                 e0.record()
-                self.write(k, v, s)
+                write_pending(k, v, s)
                 e1.record()
                 e1.synchronize()
                 timer.append((e0.elapsed_time(e1), int(k.shape[0])))
             else:
-                self.write(k, v, s)
+                write_pending(k, v, s)
             pend_k, pend_v, pend_s, n = [], [], [], 0
+            pend_seq.clear()
 
         for s, (q, kv) in enumerate(w.seqs):
             if kv - q <= 0:
@@ -85,6 +111,7 @@ class PagedKV:
             pend_k.append(k)
             pend_v.append(v)
             pend_s.append(w.slots(s, 0, kv - q))
+            pend_seq.append(s)
             n += k.shape[0]
             if n >= chunk_tokens:
                 flush()
@@ -99,6 +126,12 @@ class PagedKV:
 
     def attend(self, q, out, stream=None):
         w = self.w
+        if self.fmt == "fp8":
+            _lib.attention_fp8(q, self.k_cache, self.v_cache, self.k_scale, self.v_scale, self.block_table,
+                               self.seq_lens, self.query_start_loc, w.max_query_len, w.max_seq_len,
+                               self.softmax_scale, w.causal, out, self.workspace, dev_status=self.status,
+                               stream=stream, sliding_window=w.sliding_window)
+            return
         if self.fmt == "int8":
             _lib.attention_int8(q, self.k_cache, self.v_cache, self.k_scale, self.v_scale, self.block_table,
                                 self.seq_lens, self.query_start_loc, w.max_query_len, w.max_seq_len,
@@ -111,7 +144,10 @@ class PagedKV:
                        dev_status=self.status, stream=stream, sliding_window=w.sliding_window)
 
     def step(self, q, k_new, v_new, slots, out, stream=None):
-        self.write(k_new, v_new, slots, stream=stream)
+        if self.fmt == "fp8":  # its step's tokens are named by the batch's lengths
+            self.write_tokens(k_new, v_new, stream=stream)
+        else:
+            self.write(k_new, v_new, slots, stream=stream)
         self.attend(q, out, stream=stream)
 
     # -------------------------------------------------------------------

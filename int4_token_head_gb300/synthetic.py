@@ -124,6 +124,13 @@ class Workload:
         ks = torch.full((nb, bs, h), SENTINEL_SCALE_BITS, dtype=torch.int32, device=device).view(torch.float32)
         return kc, vc, ks, ks.clone()
 
+    def empty_cache_fp8(self, device="cpu"):
+        """Sentinel-filled FP8 caches: codes 0xFF (an E4M3 NaN), scales a NaN payload."""
+        nb, bs, h, d = self.num_blocks, self.block_size, self.num_kv_heads, self.head_size
+        kc = torch.full((nb, bs, h, d), 0xFF, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+        ks = torch.full((nb, h), SENTINEL_SCALE_BITS, dtype=torch.int32, device=device).view(torch.float32)
+        return kc, kc.clone(), ks, ks.clone()
+
     # ---- token values -------------------------------------------------
     def seq_kv(self, seq: int, device="cpu", positions: Optional[Tuple[int, int]] = None):
         """bf16 K and V [kv_len, Hkv, d] of every position of sequence ``seq``.
