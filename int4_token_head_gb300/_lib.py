@@ -419,50 +419,74 @@ def attention_inslot(q, kv_cache, block_table, seq_lens, query_start_loc, max_qu
 # ---------------------------------------------------------------------------
 # FP8 (E4M3) cache with one power-of-two scale per (block, kv head)
 # ---------------------------------------------------------------------------
-def _on_device(tensors, stream, call) -> int:
-    """call(raw stream) with the tensors' device current; they must share one CUDA device."""
-    dev = tensors[0].device
+def _refuse(msg):
+    raise ValueError(msg)
+
+
+def _stream_of(tensors, stream) -> int:
+    """The raw stream of a call on these tensors, which must share the current
+    CUDA device (None entries are skipped)."""
+    dev = tensors[0].get_device()  # -1: a CPU tensor
     for t in tensors:
-        _check(t is None or t.device == dev, "tensors must be on one device")
-    _check(dev.type == "cuda", "tensors must be on a CUDA device")
+        if t is not None and t.get_device() != dev:
+            _refuse("tensors must be on one device")
+    if dev < 0:
+        _refuse("tensors must be on a CUDA device")
+    if dev != torch.cuda.current_device():
+        _refuse(f"tensors are on cuda:{dev}, which is not the current device (torch.cuda.device selects it)")
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    raw = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-    if dev.index == torch.cuda.current_device():
-        return call(raw)
-    with torch.cuda.device(dev):
-        return call(raw)
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def _status_ptr(dev_status: Optional[torch.Tensor]):
     if dev_status is None:
         return None
-    _check(dev_status.dtype == torch.int32 and dev_status.numel() >= 1, "dev_status must be int32 [1]")
+    if dev_status.dtype != torch.int32 or dev_status.numel() < 1:
+        _refuse("dev_status must be int32 [1]")
     return dev_status.data_ptr()
 
 
+def _rows(x: torch.Tensor, name: str, tokens: int, heads: int, d: int) -> int:
+    """Token stride of bf16 head vectors [tokens, heads, d] (as _token_major, with
+    nothing formatted unless it is refused)."""
+    shape, stride = x.shape, x.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != d:
+        _refuse(f"{name} must be [tokens, {heads}, {d}], got {tuple(shape)}")
+    if shape[0] != tokens:
+        _refuse(f"{name} must have {tokens} tokens: the tensors disagree on tokens, got {shape[0]}")
+    if x.dtype != torch.bfloat16:
+        _refuse(f"{name} must be bfloat16")
+    if stride[2] != 1 or (heads > 1 and stride[1] != d):
+        _refuse(f"{name} must have contiguous heads and head dims")
+    return stride[0] if tokens > 0 else heads * d
+
+
 def _cache_dims_fp8(k_cache, v_cache, k_scale, v_scale):
-    _check(k_cache.dtype in (torch.float8_e4m3fn, torch.uint8) and v_cache.dtype == k_cache.dtype,
-           "fp8 caches must be float8_e4m3fn (or its bytes as uint8)")
     shape = k_cache.shape
-    _check(len(shape) == 4 and shape == v_cache.shape, "caches must be [blocks, block_size, heads, d]")
-    _check(k_cache.is_contiguous() and v_cache.is_contiguous(), "caches must be contiguous")
+    if k_cache.dtype not in (torch.float8_e4m3fn, torch.uint8) or v_cache.dtype != k_cache.dtype:
+        _refuse("fp8 caches must be float8_e4m3fn (or its bytes as uint8)")
+    if len(shape) != 4 or shape != v_cache.shape:
+        _refuse("caches must be [blocks, block_size, heads, d]")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        _refuse("caches must be contiguous")
     nb, bs, hkv, d = shape
     for s in (k_scale, v_scale):
-        _check(s.dtype == torch.float32 and s.shape == (nb, hkv) and s.is_contiguous(),
-               "scale caches must be contiguous float32 [blocks, heads]")
+        if s.dtype != torch.float32 or s.shape != (nb, hkv) or not s.is_contiguous():
+            _refuse("scale caches must be contiguous float32 [blocks, heads]")
     return nb, bs, hkv, d
 
 
 def _sequences(block_table, seq_lens, start_loc):
-    _check(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.is_contiguous(),
-           "block_table must be contiguous int32 [seqs, max_blocks]")
-    _check(seq_lens.dtype == torch.int32 and start_loc.dtype == torch.int32 and seq_lens.dim() == 1 and
-           start_loc.dim() == 1 and seq_lens.is_contiguous() and start_loc.is_contiguous(),
-           "sequence lengths and start locations must be contiguous int32 vectors")
-    num_seqs, width = block_table.shape
-    _check(seq_lens.shape[0] == num_seqs and start_loc.shape[0] == num_seqs + 1, "metadata shapes")
-    return num_seqs, width
+    table = block_table.shape
+    if block_table.dtype != torch.int32 or len(table) != 2 or not block_table.is_contiguous():
+        _refuse("block_table must be contiguous int32 [seqs, max_blocks]")
+    for t, n in ((seq_lens, table[0]), (start_loc, table[0] + 1)):
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            _refuse("sequence lengths and start locations must be contiguous int32 vectors")
+        if t.shape != (n,):
+            _refuse("metadata shapes: seq_lens must be [seqs] and start locations [seqs + 1]")
+    return table
 
 
 def write_fp8(k, v, block_table, seq_lens, start_loc, max_len, k_cache, v_cache, k_scale, v_scale,
@@ -471,16 +495,15 @@ def write_fp8(k, v, block_table, seq_lens, start_loc, max_len, k_cache, v_cache,
     the FP8 cache through kv_fp8_write (max_len bounds those counts)."""
     nb, bs, hkv, d = _cache_dims_fp8(k_cache, v_cache, k_scale, v_scale)
     num_seqs, width = _sequences(block_table, seq_lens, start_loc)
-    ks = _token_major(k, "k", hkv, d)
-    vs = _token_major(v, "v", hkv, d)
-    _check(k.shape[0] == v.shape[0], "k and v disagree on tokens")
-    code = _on_device(
-        (k, v, block_table, seq_lens, start_loc, k_cache, v_cache, k_scale, v_scale, dev_status), stream,
-        lambda st: load().kv_fp8_write(k.data_ptr(), ks, v.data_ptr(), vs, block_table.data_ptr(), width,
-                                       seq_lens.data_ptr(), start_loc.data_ptr(), num_seqs, k.shape[0], int(max_len),
-                                       k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-                                       v_scale.data_ptr(), nb, bs, hkv, d, _status_ptr(dev_status), st))
-    _raise(code, "kv_fp8_write")
+    tokens = k.shape[0]
+    ks, vs = _rows(k, "k", tokens, hkv, d), _rows(v, "v", tokens, hkv, d)
+    st = _stream_of((k, v, block_table, seq_lens, start_loc, k_cache, v_cache, k_scale, v_scale, dev_status), stream)
+    code = (_lib or load()).kv_fp8_write(
+        k.data_ptr(), ks, v.data_ptr(), vs, block_table.data_ptr(), width, seq_lens.data_ptr(), start_loc.data_ptr(),
+        num_seqs, tokens, max_len, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), nb,
+        bs, hkv, d, _status_ptr(dev_status), st)
+    if code:
+        _raise(code, "kv_fp8_write")
 
 
 def read_fp8(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, start_loc, max_len, k, v,
@@ -489,16 +512,15 @@ def read_fp8(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, start_lo
     FP8 cache to k and v (bf16 [tokens, heads, d]) through kv_fp8_read."""
     nb, bs, hkv, d = _cache_dims_fp8(k_cache, v_cache, k_scale, v_scale)
     num_seqs, width = _sequences(block_table, seq_lens, start_loc)
-    ks = _token_major(k, "k", hkv, d)
-    vs = _token_major(v, "v", hkv, d)
-    _check(k.shape[0] == v.shape[0], "k and v disagree on tokens")
-    code = _on_device(
-        (k, v, block_table, seq_lens, start_loc, k_cache, v_cache, k_scale, v_scale, dev_status), stream,
-        lambda st: load().kv_fp8_read(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                                      block_table.data_ptr(), width, seq_lens.data_ptr(), start_loc.data_ptr(),
-                                      num_seqs, k.shape[0], int(max_len), k.data_ptr(), ks, v.data_ptr(), vs, nb, bs,
-                                      hkv, d, _status_ptr(dev_status), st))
-    _raise(code, "kv_fp8_read")
+    tokens = k.shape[0]
+    ks, vs = _rows(k, "k", tokens, hkv, d), _rows(v, "v", tokens, hkv, d)
+    st = _stream_of((k, v, block_table, seq_lens, start_loc, k_cache, v_cache, k_scale, v_scale, dev_status), stream)
+    code = (_lib or load()).kv_fp8_read(
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), width,
+        seq_lens.data_ptr(), start_loc.data_ptr(), num_seqs, tokens, max_len, k.data_ptr(), ks, v.data_ptr(), vs, nb,
+        bs, hkv, d, _status_ptr(dev_status), st)
+    if code:
+        _raise(code, "kv_fp8_read")
 
 
 def attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, query_start_loc,
@@ -508,23 +530,21 @@ def attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, 
     place.  With ``causal`` false, queries may attend keys of any length."""
     nb, bs, hkv, d = _cache_dims_fp8(k_cache, v_cache, k_scale, v_scale)
     num_seqs, width = _sequences(block_table, seq_lens, query_start_loc)
-    _check(q.dim() == 3, "q must be [tokens, q_heads, d]")
-    tokens, hq = q.shape[:2]
-    qs = _token_major(q, "q", hq, d)
-    os_ = _token_major(out, "out", hq, d)
-    _check(out.shape[0] == tokens, "out must match q")
-    _check(workspace.dtype == torch.uint8 and workspace.is_contiguous(), "workspace must be contiguous uint8")
-    code = _on_device(
-        (q, out, block_table, seq_lens, query_start_loc, k_cache, v_cache, k_scale, v_scale, workspace, dev_status),
-        stream,
-        lambda st: load().kv_fp8_attention(q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(),
-                                           k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), width,
-                                           seq_lens.data_ptr(), query_start_loc.data_ptr(), num_seqs, tokens,
-                                           int(max_query_len), int(max_seq_len), hq, hkv, d, bs, nb,
-                                           float(softmax_scale), int(bool(causal)), int(sliding_window),
-                                           out.data_ptr(), os_, workspace.data_ptr(), workspace.numel(),
-                                           _status_ptr(dev_status), st))
-    _raise(code, "kv_fp8_attention")
+    if q.dim() != 3:
+        _refuse("q must be [tokens, q_heads, d]")
+    tokens, hq, _ = q.shape
+    qs, os_ = _rows(q, "q", tokens, hq, d), _rows(out, "out", tokens, hq, d)
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        _refuse("workspace must be contiguous uint8")
+    st = _stream_of((q, out, block_table, seq_lens, query_start_loc, k_cache, v_cache, k_scale, v_scale, workspace,
+                     dev_status), stream)
+    code = (_lib or load()).kv_fp8_attention(
+        q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        block_table.data_ptr(), width, seq_lens.data_ptr(), query_start_loc.data_ptr(), num_seqs, tokens,
+        max_query_len, max_seq_len, hq, hkv, d, bs, nb, softmax_scale, 1 if causal else 0, sliding_window,
+        out.data_ptr(), os_, workspace.data_ptr(), workspace.numel(), _status_ptr(dev_status), st)
+    if code:
+        _raise(code, "kv_fp8_attention")
 
 
 def qk_norm_rope(q, k, positions, cos_sin, q_weight, k_weight, eps, q_out, k_out, interleaved: bool = False,
@@ -536,33 +556,33 @@ def qk_norm_rope(q, k, positions, cos_sin, q_weight, k_weight, eps, q_out, k_out
     input).  positions: int64 [tokens]; cos_sin: float32 [max_position, rot]
     (cosines, then sines), or both None for no rotation.  q_weight, k_weight:
     bf16 [d], or both None for no norm."""
-    _check(q.dim() == 3 and k.dim() == 3, "q and k must be [tokens, heads, d]")
+    if q.dim() != 3 or k.dim() != 3:
+        _refuse("q and k must be [tokens, heads, d]")
     tokens, hq, d = q.shape
     hkv = k.shape[1]
-    qs = _token_major(q, "q", hq, d)
-    ks = _token_major(k, "k", hkv, d)
-    qo = _token_major(q_out, "q_out", hq, d)
-    ko = _token_major(k_out, "k_out", hkv, d)
-    _check(k.shape[0] == q_out.shape[0] == k_out.shape[0] == tokens, "q, k and the outputs disagree on tokens")
-    _check((q_weight is None) == (k_weight is None), "q_weight and k_weight: both or neither")
-    if q_weight is not None:
-        for w in (q_weight, k_weight):
-            _check(w.dtype == torch.bfloat16 and w.shape == (d,) and w.is_contiguous(), "weights must be bfloat16 [d]")
-    _check((cos_sin is None) == (positions is None), "positions and cos_sin: both or neither")
+    qs, ks = _rows(q, "q", tokens, hq, d), _rows(k, "k", tokens, hkv, d)
+    qo, ko = _rows(q_out, "q_out", tokens, hq, d), _rows(k_out, "k_out", tokens, hkv, d)
+    qw = kw = pos = table = None
     max_pos = rot = 0
-    if cos_sin is not None:
-        _check(cos_sin.dtype == torch.float32 and cos_sin.dim() == 2 and cos_sin.is_contiguous(),
-               "cos_sin must be contiguous float32 [max_position, rot]")
-        _check(positions.dtype == torch.int64 and positions.shape == (tokens,) and positions.is_contiguous(),
-               "positions must be contiguous int64 [tokens]")
+    if q_weight is not None and k_weight is not None:
+        for w in (q_weight, k_weight):
+            if w.dtype != torch.bfloat16 or w.shape != (d,) or not w.is_contiguous():
+                _refuse("weights must be bfloat16 [d]")
+        qw, kw = q_weight.data_ptr(), k_weight.data_ptr()
+    elif q_weight is not k_weight:
+        _refuse("q_weight and k_weight: both or neither")
+    if cos_sin is not None and positions is not None:
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+            _refuse("cos_sin must be contiguous float32 [max_position, rot]")
+        if positions.dtype != torch.int64 or positions.shape != (tokens,) or not positions.is_contiguous():
+            _refuse("positions must be contiguous int64 [tokens]")
         max_pos, rot = cos_sin.shape
-    code = _on_device(
-        (q, k, q_out, k_out, positions, cos_sin, q_weight, k_weight, dev_status), stream,
-        lambda st: load().kv_qk_norm_rope(q.data_ptr(), qs, k.data_ptr(), ks, tokens, hq, hkv, d,
-                                          None if q_weight is None else q_weight.data_ptr(),
-                                          None if k_weight is None else k_weight.data_ptr(), float(eps),
-                                          None if positions is None else positions.data_ptr(),
-                                          None if cos_sin is None else cos_sin.data_ptr(), max_pos, rot,
-                                          int(bool(interleaved)), q_out.data_ptr(), qo, k_out.data_ptr(), ko,
-                                          _status_ptr(dev_status), st))
-    _raise(code, "kv_qk_norm_rope")
+        pos, table = positions.data_ptr(), cos_sin.data_ptr()
+    elif cos_sin is not positions:
+        _refuse("positions and cos_sin: both or neither")
+    st = _stream_of((q, k, q_out, k_out, positions, cos_sin, q_weight, k_weight, dev_status), stream)
+    code = (_lib or load()).kv_qk_norm_rope(
+        q.data_ptr(), qs, k.data_ptr(), ks, tokens, hq, hkv, d, qw, kw, eps, pos, table, max_pos, rot,
+        1 if interleaved else 0, q_out.data_ptr(), qo, k_out.data_ptr(), ko, _status_ptr(dev_status), st)
+    if code:
+        _raise(code, "kv_qk_norm_rope")

@@ -217,7 +217,7 @@ def test_binding_refuses_bad_tensors():
         kv.read_fp8(a["kc"], a["vc"], a["ks"], a["vs"], a["bt"], a["sl"], a["st"], 2, a["k"], a["v"])
     q = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
     ws = torch.zeros(16, dtype=torch.uint8)
-    for qq, out, w, what in [(q, q, ws, "CUDA device"), (q, q[:2], ws, "out must match"), (q[0], q, ws, "q must be"),
+    for qq, out, w, what in [(q, q, ws, "CUDA device"), (q, q[:2], ws, "out must have"), (q[0], q, ws, "q must be"),
                              (q, q, ws.int(), "workspace"), (q, q.float(), ws, "bfloat16")]:
         with pytest.raises(ValueError, match=what):
             kv.attention_fp8(qq, a["kc"], a["vc"], a["ks"], a["vs"], a["bt"], a["sl"], a["st"], 2, 16, 0.1, True, out, w)
