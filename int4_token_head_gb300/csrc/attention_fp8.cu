@@ -39,6 +39,7 @@ __device__ __forceinline__ int q_exponent(uint32_t amax_bits) {
 
 #include "decode_fp8.cuh"
 #include "prefill_fp8.cuh"
+#include "prefill_ws_fp8.cuh"
 
 // ---------------------------------------------------------------------------
 // host launcher
@@ -77,7 +78,11 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
   c.out_stride = a.out_stride;
   c.status = a.dev_status;
   c.max_items = L.max_prefill_items;
-  c.tile_tokens = kPrefillRows / c.group;
+  // prefill items: 256 rows on the tensor-core kernel (head sizes up to 192:
+  // two accumulators of 256 columns would leave no TMEM for scores), 64 on the
+  // warp-MMA one
+  constexpr bool kTcPrefill = D <= 192;
+  c.tile_tokens = (kTcPrefill ? 256 : kPrefillRows) / c.group;
 
   // decode: blocks per position, kv heads per CTA, CTAs
   c.hg = c.ng = c.nl = c.np = 1;
@@ -137,14 +142,26 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
   if (may_prefill) {
     static PerContext<int> occ_c;
     int occ = 0;
-    using G = Fp8Pre<D>;
-    if (!occ_c.get(dev, [](int* o) { return configure(prefill_fp8_kernel<D>, G::SMEM, G::THREADS, o); }, &occ))
-      return KV_INT4_ERR_CUDA;
-    long long grid = (long long)sms * occ;
-    if (grid > L.max_prefill_items) grid = L.max_prefill_items;
-    if (grid < 1) grid = 1;
-    timing_begin(kTimedPrefill, stream);
-    prefill_fp8_kernel<D><<<(unsigned)grid, G::THREADS, G::SMEM, stream>>>(c, pv);
+    auto go = [&](auto kern, int smem, int threads, auto conf) {
+      if (!occ_c.get(dev, conf, &occ)) return false;
+      long long grid = (long long)sms * occ;
+      if (grid > L.max_prefill_items) grid = L.max_prefill_items;
+      timing_begin(kTimedPrefill, stream);
+      kern<<<(unsigned)(grid < 1 ? 1 : grid), threads, smem, stream>>>(c, pv);
+      return true;
+    };
+    bool ok;
+    if constexpr (kTcPrefill) {
+      using G = Fp8Ws<D>;
+      ok = go(prefill_ws_fp8_kernel<D>, G::SMEM, G::THREADS, [](int* o) {
+        return configure_tmem(prefill_ws_fp8_kernel<D>, G::SMEM, G::THREADS, 512, o);
+      });
+    } else {
+      using G = Fp8Pre<D>;
+      ok = go(prefill_fp8_kernel<D>, G::SMEM, G::THREADS,
+              [](int* o) { return configure(prefill_fp8_kernel<D>, G::SMEM, G::THREADS, o); });
+    }
+    if (!ok) return KV_INT4_ERR_CUDA;
     timing_end(kTimedPrefill, stream);
     if (cudaGetLastError() != cudaSuccess) return KV_INT4_ERR_CUDA;
   }
