@@ -10,13 +10,16 @@
 // denominator in the same units is sum_b 2^-kv_b sum_{p in b} w_p (a block's
 // sum times a power of two, fp32).  A score costs one FMA (scale and kv
 // together) and one exp2.
-// Queries are used at full precision too: a row is divided by the power of two
-// of its largest magnitude (bf16 to f16, exact but for elements 2^-14 of the
-// largest, whose f16 spacing is 2^-24 of it) and that power multiplies the
-// fp32 score.  Codes convert to f16 exactly (cvt.rn.f16x2.e4m3x2).
+// Queries are used at full precision: the tensor-core prefill multiplies them
+// as they are (bf16, K codes converted to bf16); the warp-MMA kernels divide a
+// row by the power of two of its largest magnitude (bf16 to f16, exact but for
+// elements 2^-14 of the largest, whose f16 spacing is 2^-24 of it) and multiply
+// the fp32 score by that power.  Codes convert exactly to either type.
 //
 // Launches, all on the caller's stream: the schedule (one CTA), prefill (if a
 // sequence may need it), decode, merge.
+
+#include <cuda.h>
 
 #include <type_traits>
 
@@ -44,6 +47,61 @@ __device__ __forceinline__ int q_exponent(uint32_t amax_bits) {
 // ---------------------------------------------------------------------------
 // host launcher
 // ---------------------------------------------------------------------------
+// cuTensorMapEncodeTiled, reached through the runtime (the library links the
+// static runtime only); null if the driver does not have it
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  return fn;
+}
+
+int launch_plan(const Common& c, const PlanView& pv, cudaStream_t stream) {
+  plan_fp8_kernel<<<1, kPrepThreads, 0, stream>>>(c, pv);
+  return cudaGetLastError() == cudaSuccess ? KV_INT4_OK : KV_INT4_ERR_CUDA;
+}
+
+// the tensor maps of a call's prefill; false where its tensors have no such
+// map (query rows that overlap, say)
+template <int D>
+bool make_maps(const AttnArgs& a, int tile_tokens, Fp8Maps* m) {
+  using G = Fp8Ws<D>;
+  const EncodeTiled enc = encode_tiled();
+  const cuuint64_t hq = a.num_q_heads, hkv = a.num_kv_heads, rows = (cuuint64_t)a.num_blocks * 16;
+  const cuuint64_t group = hq / hkv;
+  if (!enc || rows == 0 || rows >= (1ull << 31) || (a.num_q_tokens > 1 && a.q_stride < (int64_t)(hq * D))) return false;
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  {
+    const cuuint64_t dims[3] = {D, hq, (cuuint64_t)a.num_q_tokens};
+    const cuuint64_t strides[2] = {D * 2, (a.num_q_tokens > 1 ? (cuuint64_t)a.q_stride : hq * D) * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)tile_tokens};
+    if (enc(&m->q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), dims, strides, box, ones,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  }
+  const cuuint64_t dims[4] = {G::W, D / G::W, hkv, rows};
+  const cuuint64_t strides[3] = {G::W, D, hkv * D};
+  const cuuint32_t box[4] = {G::W, D / G::W, 1, 16};
+  const CUtensorMapSwizzle sw = G::W == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                : G::W == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                             : CU_TENSOR_MAP_SWIZZLE_32B;
+  for (int i = 0; i < 2; i++)
+    if (enc(i ? &m->v : &m->k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(i ? a.v_cache : a.k_cache), dims,
+            strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return false;
+  return true;
+}
+
 template <int D>
 int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
   WorkspaceLayout L;
@@ -78,12 +136,6 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
   c.out_stride = a.out_stride;
   c.status = a.dev_status;
   c.max_items = L.max_prefill_items;
-  // prefill items: 256 rows on the tensor-core kernel (head sizes up to 192:
-  // two accumulators of 256 columns would leave no TMEM for scores), 64 on the
-  // warp-MMA one
-  constexpr bool kTcPrefill = D <= 192;
-  c.tile_tokens = (kTcPrefill ? 256 : kPrefillRows) / c.group;
-
   // decode: blocks per position, kv heads per CTA, CTAs
   c.hg = c.ng = c.nl = c.np = 1;
   const bool any_decode = c.group <= kDecodeCols;
@@ -135,33 +187,43 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
   }
   c.dcols = kDecodeCols / c.np;
 
-  plan_fp8_kernel<<<1, kPrepThreads, 0, stream>>>(c, pv);
-  if (cudaGetLastError() != cudaSuccess) return KV_INT4_ERR_CUDA;
-
+  // prefill items: 256 rows on the tensor-core kernel (head sizes up to 192:
+  // two accumulators of 256 columns would leave no TMEM for scores), 64 on the
+  // warp-MMA one
   const bool may_prefill = c.group > c.dcols || (long long)a.max_query_len * c.group > c.dcols;
-  if (may_prefill) {
+  bool tc = false;
+  if constexpr (D <= 192) {
+    Fp8Maps maps;
+    tc = may_prefill && make_maps<D>(a, Fp8Ws<D>::ROWS / c.group, &maps);
+    c.tile_tokens = (tc ? Fp8Ws<D>::ROWS : kPrefillRows) / c.group;
+    if (int e = launch_plan(c, pv, stream)) return e;
+    if (tc) {
+      using G = Fp8Ws<D>;
+      static PerContext<int> occ_c;
+      int occ = 0;
+      if (!occ_c.get(dev, [](int* o) { return configure_tmem(prefill_ws_fp8_kernel<D>, G::SMEM, G::THREADS, 512, o); },
+                     &occ))
+        return KV_INT4_ERR_CUDA;
+      const long long grid = sms < L.max_prefill_items ? sms : L.max_prefill_items;
+      timing_begin(kTimedPrefill, stream);
+      prefill_ws_fp8_kernel<D><<<(unsigned)grid, G::THREADS, G::SMEM, stream>>>(c, pv, maps);
+      timing_end(kTimedPrefill, stream);
+      if (cudaGetLastError() != cudaSuccess) return KV_INT4_ERR_CUDA;
+    }
+  } else {
+    c.tile_tokens = kPrefillRows / c.group;
+    if (int e = launch_plan(c, pv, stream)) return e;
+  }
+  if (may_prefill && !tc) {
     static PerContext<int> occ_c;
     int occ = 0;
-    auto go = [&](auto kern, int smem, int threads, auto conf) {
-      if (!occ_c.get(dev, conf, &occ)) return false;
-      long long grid = (long long)sms * occ;
-      if (grid > L.max_prefill_items) grid = L.max_prefill_items;
-      timing_begin(kTimedPrefill, stream);
-      kern<<<(unsigned)(grid < 1 ? 1 : grid), threads, smem, stream>>>(c, pv);
-      return true;
-    };
-    bool ok;
-    if constexpr (kTcPrefill) {
-      using G = Fp8Ws<D>;
-      ok = go(prefill_ws_fp8_kernel<D>, G::SMEM, G::THREADS, [](int* o) {
-        return configure_tmem(prefill_ws_fp8_kernel<D>, G::SMEM, G::THREADS, 512, o);
-      });
-    } else {
-      using G = Fp8Pre<D>;
-      ok = go(prefill_fp8_kernel<D>, G::SMEM, G::THREADS,
-              [](int* o) { return configure(prefill_fp8_kernel<D>, G::SMEM, G::THREADS, o); });
-    }
-    if (!ok) return KV_INT4_ERR_CUDA;
+    using G = Fp8Pre<D>;
+    if (!occ_c.get(dev, [](int* o) { return configure(prefill_fp8_kernel<D>, G::SMEM, G::THREADS, o); }, &occ))
+      return KV_INT4_ERR_CUDA;
+    long long grid = (long long)sms * occ;
+    if (grid > L.max_prefill_items) grid = L.max_prefill_items;
+    timing_begin(kTimedPrefill, stream);
+    prefill_fp8_kernel<D><<<(unsigned)grid, G::THREADS, G::SMEM, stream>>>(c, pv);
     timing_end(kTimedPrefill, stream);
     if (cudaGetLastError() != cudaSuccess) return KV_INT4_ERR_CUDA;
   }

@@ -265,7 +265,7 @@ def _attend(b, q, dev, hq, causal=True, window=0, scale=None, out=None, meta=Non
     if out is None:
         out = torch.full((q.shape[0], hq, b.d), float("nan"), dtype=torch.bfloat16, device="cuda")
     kv.attention_fp8(q, *dev, *(meta or b.meta()), b.max_len if max_q is None else max_q, int(b.lens.max()),
-                     scale if scale is not None else b.d ** -0.5, causal, out, ws, dev_status=b.status,
+                     b.d ** -0.5 if scale is None else scale, causal, out, ws, dev_status=b.status,
                      sliding_window=window, stream=stream)
     return out
 
@@ -653,3 +653,25 @@ def test_paged_cache_step(name):
         F.write(x[n - ql:], row, [n], [0, ql], *want)
     assert np.array_equal(host[1], want[0]) and np.array_equal(host[3], want[1], equal_nan=True)
     assert math.isfinite(float(vv.float().abs().max())) and (vv.float() - v.float()).abs().max() < 0.3
+
+
+@pytest.mark.parametrize("d", HEADS)
+@pytest.mark.parametrize("seqs", [[(1, 40), (1, 9)], [(40, 90), (7, 7)]])
+def test_one_query_row_for_every_token(d, seqs):
+    """q may repeat one row (token stride 0)."""
+    b = Batch(seqs, 2, d).fill()
+    q = _bf16((1, 4, d), 1).expand(b.tokens, 4, d)
+    out = _attend(b, q.cuda()[:1].expand(b.tokens, 4, d), b.device(), 4)
+    ref, bound = F.attention(q.double().numpy(), b.host(), b.table, b.lens, b.start, d ** -0.5, True)
+    _assert_attention(out, ref, bound)
+
+
+@pytest.mark.parametrize("d", HEADS)
+def test_negative_and_zero_softmax_scale(d):
+    for scale in (-0.3, 0.0):
+        for seqs in ([(1, 70), (1, 9)], [(40, 90), (7, 7)]):
+            b = Batch(seqs, 2, d).fill()
+            q = _bf16((b.tokens, 4, d), 1)
+            out = _attend(b, q.cuda(), b.device(), 4, scale=scale)
+            ref, bound = F.attention(q.double().numpy(), b.host(), b.table, b.lens, b.start, scale, True)
+            _assert_attention(out, ref, bound)
