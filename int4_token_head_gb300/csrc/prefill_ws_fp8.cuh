@@ -4,26 +4,27 @@
 // One CTA per SM (all 512 TMEM columns); an item is 256 query rows (query
 // token x q head of one kv group) in two halves of 128, the MMA's M.  A step
 // is NK keys: 128 for head sizes up to 128 (a 128 x 128 score tile per half,
-// full tensor rate), 64 at 192 (the accumulators leave no more TMEM).  Sixteen
-// warps in four roles that meet only at mbarriers:
-//   * producer warp (14): claims items (longest first) and hands them on
+// full tensor rate), 64 at 192 (the accumulators leave no more TMEM).  Eighteen
+// warps in five roles that meet only at mbarriers:
+//   * producer warp (16): claims items (longest first) and hands them on
 //     through a two-entry ring; TMA copies of the item's Q rows (bf16, straight
 //     into the MMA's swizzled tile) and of the step's K and V code blocks (one
 //     box per block; a block that the table does not name is a box outside the
 //     tensor, which arrives as zeros); the blocks' scales into a three-entry ring;
-//   * convert warps (8-13): K codes into one of two bf16 tiles, V codes into
-//     one of two f16 tiles, exactly.  K meets the unconverted bf16 queries, so
-//     an item starts without any work on Q; V meets the f16 weights;
-//   * MMA warp (15, lane 0 issues): S_h = Q_h K^T, then O_h += W_h V with the
+//   * convert warps (8-11 K, 12-15 V): K codes into one of two bf16 tiles, V
+//     codes into one of two f16 tiles, exactly.  K meets the unconverted bf16
+//     queries, so an item starts without any work on Q; V meets the f16 weights;
+//   * MMA warp (17, lane 0 issues): S_h = Q_h K^T, then O_h += W_h V with the
 //     weights W_h (f16 pairs over S_h's columns) read from TMEM.  Issue order
 //     S0 S1 | WV0 S0' | WV1 S1' | ...: a half's softmax runs during the other's MMAs;
 //   * softmax warps (0-3 half 0, 4-7 half 1): one query row per thread.  With
 //     f_b = |softmax_scale| log2 e ks_b (a negative scale's sign is in K) and
 //     kv_b per block, the row's maximum needs only the blocks' largest raw
-//     scores, and a weight is exp2(fma(s, f_b, kv_b - m_ref)): one max, one fma
-//     and one exp2 per score.  m_ref moves (and the row's O in TMEM is
-//     rescaled) only when the maximum passes it by more than 8: weights stay
-//     below 2^8, inside f16 whatever the V scales.
+//     scores, and a weight is exp2(fma(s, f_b, kv_b - m_ref)).  m_ref moves to
+//     the row's maximum (and its O in TMEM is rescaled) only when a step's
+//     weights add up to more than 2^14: they stay inside f16 whatever the V
+//     scales, and most steps need no maximum (one fma, one exp2, one add and
+//     half a conversion per score).
 // Shared operands are K-major (Q, K) or MN-major (V) tiles [D / 64][rows][128
 // bytes] with the 16-byte chunk index XORed by row % 8.
 //
@@ -67,8 +68,14 @@ struct Fp8Ws {
   static constexpr int NBARS = 23;
   static constexpr int S_COLS = NK, O_COL = 2 * NK;  // TMEM: S_h at h NK, O_h at 2 NK + h D
   static constexpr int SMEM = 1024 + QBYTES + 4 * KVBYTES + 2 * STG + NRING * RING + NBARS * 8 + 48;
-  static constexpr int THREADS = 16 * 32;
-  static constexpr int CV_WARPS = 6;  // convert warps
+  static constexpr int THREADS = 20 * 32;  // five warpgroups; the last two warps only give up registers
+  static constexpr int CV_WARPS = 4;       // convert warps for K, and for V
+  // byte offset of chunk g of key k in a stage
+  __device__ static constexpr int stage_off(int k, int g) {
+    return CHR == 8   ? k * 128 + ((g ^ (k & 7)) << 4)
+           : CHR == 4 ? k * 64 + ((g ^ ((k >> 1) & 3)) << 4)
+                      : chunk(k * CHR + g) * 16;
+  }
   static_assert(O_COL + 2 * D <= 512 && SMEM <= 227 * 1024, "TMEM and shared memory");
 };
 
@@ -88,6 +95,51 @@ __device__ __forceinline__ bool fp8_wait(uint32_t bar, uint32_t parity, volatile
 __device__ __forceinline__ void fp8_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
+// MMAs issued by the lane of a converged warp whose `lead` is set.  The code
+// around them stays the same for all lanes, so that descriptors live in uniform
+// registers: under a branch on the lane, each MMA costs half a dozen moves from
+// vector registers, and issuing one half's MMAs of a step takes longer than
+// the tensor cores do
+__device__ __forceinline__ void fp8_mma(uint32_t lead, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"((int)acc), "r"(lead));
+}
+__device__ __forceinline__ void fp8_mma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                           bool acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"((int)acc), "r"(lead));
+}
+__device__ __forceinline__ void fp8_commit(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+      "r"(lead)
+      : "memory");
+}
+// fp8_wait by a converged warp, for control flow that is the same for all lanes
+__device__ __forceinline__ void fp8_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
+  for (int n = 0; n < kMaxWaitIters; n++) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
+    if ((n & 255) == 255 && __any_sync(0xffffffffu, *abort)) return;
+  }
+  *abort = 1;
+  flag(status, KV_INT4_DEV_TIMEOUT);
+}
+// a warp's 32 lanes x 32 words to TMEM, not waited for
+__device__ __forceinline__ void tmem_st32_async(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
 // a tensor-map box at coordinates (0, 0, head, row) into shared memory
 __device__ __forceinline__ void tma_box4(uint32_t dst, const CUtensorMap* m, int head, int row, uint32_t bar) {
   asm volatile(
@@ -103,24 +155,35 @@ __device__ __forceinline__ void tma_box3(uint32_t dst, const CUtensorMap* m, int
       "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(head), "r"(row), "r"(bar)
       : "memory");
 }
-// four E4M3 codes as two bf16x2, exactly: sign and the seven other bits moved to
-// bf16's places stand for the value * 2^-120 (bf16 subnormals for E4M3's), which
-// one multiplication undoes; neg flips the signs
-__device__ __forceinline__ void e4m3x4_to_bf16x2(uint32_t w, uint32_t neg, uint32_t& lo, uint32_t& hi) {
+// Four E4M3 codes as two words of two 16-bit floats, exactly but for a power of
+// two: with a code byte p = 128 sign + m in the low byte of each half, the
+// sign goes to bit 15 (times 256) and m to the format's place (times 16 for
+// bf16, 128 for f16) by two multiply-adds, 16 p + 240 sign or 128 p + 128 sign:
+// half of the work on the FMA pipe (the converts' ALU work bounded the kernel).
+// m then stands for the value * 2^-120 in bf16, which one multiplication undoes
+// (f = +-2^120), and for the value * 2^-8 in f16, which the caller undoes.
+// E4M3's subnormals are the formats' subnormals.
+__device__ __forceinline__ uint32_t mad_u32(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("mad.lo.u32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+__device__ __forceinline__ void e4m3x4_to_bf16x2(uint32_t w, __nv_bfloat162 f, uint32_t& lo, uint32_t& hi) {
   uint32_t r[2];
 #pragma unroll
   for (int i = 0; i < 2; i++) {
-    const uint32_t p = __byte_perm(w, 0, i ? 0x3424 : 0x1404);
-    uint32_t sg;
-    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(sg) : "r"(p), "r"(0x80008000u), "r"(neg));          // (p & m) ^ neg
-    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r[i]) : "r"(p >> 4), "r"(0x07f007f0u), "r"(sg));  // (p >> 4 & m) | sign
-    const uint32_t two120 = 0x7b807b80u;
-    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&r[i]),
-                                     *reinterpret_cast<const __nv_bfloat162*>(&two120));
+    const uint32_t p = __byte_perm(w, 0, i ? 0x4342 : 0x4140);
+    r[i] = mad_u32(p & 0x00800080u, 240u, mad_u32(p, 16u, 0u));
+    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&r[i]), f);
     r[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
   lo = r[0];
   hi = r[1];
+}
+__device__ __forceinline__ void e4m3x4_to_f16x2_256th(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t p = __byte_perm(w, 0, 0x4140), q = __byte_perm(w, 0, 0x4342);
+  lo = mad_u32(p & 0x00800080u, 128u, mad_u32(p, 128u, 0u));
+  hi = mad_u32(q & 0x00800080u, 128u, mad_u32(q, 128u, 0u));
 }
 
 // tensor maps of a call: q {d, q heads, tokens} bf16, boxes of 64 elements x
@@ -131,7 +194,7 @@ struct Fp8Maps {
 };
 
 template <int D>
-__global__ void __launch_bounds__(16 * 32, 1)
+__global__ void __launch_bounds__(20 * 32, 1)
     prefill_ws_fp8_kernel(Common c, PlanView pv, const __grid_constant__ Fp8Maps maps) {
   using G = Fp8Ws<D>;
   constexpr int KSTEPS = D / 16;
@@ -165,7 +228,7 @@ __global__ void __launch_bounds__(16 * 32, 1)
       mbar_init(bar(SFULL + b), 1);
       mbar_init(bar(PFULL + b), 4);
       mbar_init(bar(IFULL + b), 1);
-      mbar_init(bar(IFREE + b), 8 + 1 + G::CV_WARPS);
+      mbar_init(bar(IFREE + b), 8 + 2 * G::CV_WARPS + 1);
       mbar_init(bar(RKFULL + b), 1);  // RKFULL, RVFULL
       mbar_init(bar(RKFREE + b), G::CV_WARPS);
     }
@@ -192,11 +255,11 @@ __global__ void __launch_bounds__(16 * 32, 1)
     if (lane == 0) fp8_arrive(bar(IFREE + e));
     return item.x >= 0;
   };
-  // registers: 128 a thread at launch (65,536); the softmax warpgroups take
-  // 160, the others 96 (2 x 128 x 160 + 2 x 128 x 96 = 65,536)
+  // registers: 96 a thread at launch (640 threads, 61,440); the softmax
+  // warpgroups take 144, the others 64 (256 x 144 + 384 x 64 = 61,440)
   if (warp < 8) {
     // ======================= softmax warpgroups =======================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 160;\n");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;\n");
     uint32_t ph_sfull = 0, ph_odone = 0, ph_ifull = 0;
     const float cf = fabsf(c.qscale);  // its sign is in K
     int n = 0;  // steps of earlier items
@@ -245,75 +308,88 @@ __global__ void __launch_bounds__(16 * 32, 1)
         const bool full = __all_sync(0xffffffffu, pos0 >= lo && pos0 + NK <= lim && ok[NB] != 0);
         auto step = [&](auto masked_tag) {
           constexpr bool MASKED = decltype(masked_tag)::value;
-          float mx = -INFINITY;
-#pragma unroll
-          for (int u = 0; u < NK / 32; u++) {
-            float s[32];
-            tmem_ld32(tS + 32 * u, s);
-            if constexpr (MASKED) {
-              const uint32_t vis = visible(u);
-#pragma unroll
-              for (int k = 0; k < 32; k++) s[k] = (vis >> k) & 1 ? s[k] : -INFINITY;
-            }
-#pragma unroll
-            for (int b = 0; b < 2; b++) {
-              const float* t = s + 16 * b;
-              const float a = fmax3(fmax3(t[0], t[1], t[2]), fmax3(t[3], t[4], t[5]), fmax3(t[6], t[7], t[8]));
-              const float d = fmax3(fmax3(t[9], t[10], t[11]), fmax3(t[12], t[13], t[14]), t[15]);
-              const float top = fmaxf(a, d);
-              const float v = fmaf(top, cf * re[2 * u + b], kvf[2 * u + b]);
-              mx = fmaxf(mx, MASKED && top == -INFINITY ? -INFINITY : v);
-            }
-          }
-          const bool grow = m_ref != -INFINITY && mx > m_ref + 8.f;
-          const float alpha = grow ? fast_exp2(m_ref - mx) : 1.f;
-          if (grow || m_ref == -INFINITY) m_ref = mx;
-          if (__any_sync(0xffffffffu, grow)) {
-            // O of this half is complete up to the previous step (S_h of this step was issued after it)
+          uint32_t w[NK / 2];
+          // The weights are computed against the reference as it stands; their
+          // sum bounds the largest, so the row's maximum is only looked for
+          // where some row of the warp has no reference yet or a sum above 2^14
+          // (S is whole until the weights are stored)
+          bool find = __any_sync(0xffffffffu, m_ref == -INFINITY);
+          float add, tot = INFINITY;
 #pragma unroll 1
-            for (int cc = 0; cc < D / 32; cc++) {
-              float o[32];
-              tmem_ld32(tO + cc * 32, o);
+          while (true) {
+            if (find) {
+              float mx = -INFINITY;
 #pragma unroll
-              for (int i = 0; i < 32; i++) o[i] *= alpha;
-              tmem_st32(tO + cc * 32, o);
-            }
-          }
-          l_run *= alpha;
-          const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-#pragma unroll
-          for (int u = 0; u < NK / 32; u++) {
-            float s[32];
-            tmem_ld32(tS + 32 * u, s);
-            uint32_t vis = 0;
-            if constexpr (MASKED) vis = visible(u);
-            uint32_t w[16];
-#pragma unroll
-            for (int b = 0; b < 2; b++) {
-              const float f = cf * re[2 * u + b], o = kvf[2 * u + b] - mu;
-              const float2 f2 = make_float2(f, f), o2 = make_float2(o, o);
-              float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-              for (int k = 0; k < 16; k += 2) {
-                const float2 t = f2fma(make_float2(s[16 * b + k], s[16 * b + k + 1]), f2, o2);
-                float2 p = make_float2(fast_exp2(t.x), fast_exp2(t.y));
+              for (int u = 0; u < NK / 32; u++) {
+                float s[32];
+                tmem_ld32(tS + 32 * u, s);
                 if constexpr (MASKED) {
-                  p.x = (vis >> (16 * b + k)) & 1 ? p.x : 0.f;
-                  p.y = (vis >> (16 * b + k + 1)) & 1 ? p.y : 0.f;
+                  const uint32_t vis = visible(u);
+#pragma unroll
+                  for (int k = 0; k < 32; k++) s[k] = (vis >> k) & 1 ? s[k] : -INFINITY;
                 }
-                sum = f2add(sum, p);
-                w[8 * b + k / 2] = pack_f16x2(p.x, p.y);
+#pragma unroll
+                for (int b = 0; b < 2; b++) {
+                  const float* t = s + 16 * b;
+                  const float a = fmax3(fmax3(t[0], t[1], t[2]), fmax3(t[3], t[4], t[5]), fmax3(t[6], t[7], t[8]));
+                  const float d = fmax3(fmax3(t[9], t[10], t[11]), fmax3(t[12], t[13], t[14]), t[15]);
+                  const float top = fmaxf(a, d);
+                  const float v = fmaf(top, cf * re[2 * u + b], kvf[2 * u + b]);
+                  mx = fmaxf(mx, MASKED && top == -INFINITY ? -INFINITY : v);
+                }
               }
-              l_run = fmaf(sum.x + sum.y, ivs[2 * u + b], l_run);
+              const bool grow = m_ref == -INFINITY || (tot > 16384.f && mx > m_ref);
+              const float alpha = grow && m_ref != -INFINITY ? fast_exp2(m_ref - mx) : 1.f;
+              if (grow) m_ref = mx;
+              if (__any_sync(0xffffffffu, alpha != 1.f)) {
+                // O of this half is complete up to the previous step (S_h of this step was issued after it)
+#pragma unroll 1
+                for (int cc = 0; cc < D / 32; cc++) {
+                  float o[32];
+                  tmem_ld32(tO + cc * 32, o);
+#pragma unroll
+                  for (int i = 0; i < 32; i++) o[i] *= alpha;
+                  tmem_st32(tO + cc * 32, o);
+                }
+              }
+              l_run *= alpha;
             }
-            // the weights over the row's first NK / 2 columns: columns [16 u, 16 u + 16) have been read
-            asm volatile(
-                "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-                "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(tS + 16 * u),
-                "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]),
-                "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
-                : "memory");
+            const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+            add = tot = 0.f;
+#pragma unroll
+            for (int u = 0; u < NK / 32; u++) {
+              float s[32];
+              tmem_ld32(tS + 32 * u, s);
+              uint32_t vis = 0;
+              if constexpr (MASKED) vis = visible(u);
+#pragma unroll
+              for (int b = 0; b < 2; b++) {
+                const float f = cf * re[2 * u + b], o = kvf[2 * u + b] - mu;
+                const float2 f2 = make_float2(f, f), o2 = make_float2(o, o);
+                float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) {
+                  const float2 t = f2fma(make_float2(s[16 * b + k], s[16 * b + k + 1]), f2, o2);
+                  float2 p = make_float2(fast_exp2(t.x), fast_exp2(t.y));
+                  if constexpr (MASKED) {
+                    p.x = (vis >> (16 * b + k)) & 1 ? p.x : 0.f;
+                    p.y = (vis >> (16 * b + k + 1)) & 1 ? p.y : 0.f;
+                  }
+                  sum = f2add(sum, p);
+                  w[16 * u + 8 * b + k / 2] = pack_f16x2(p.x, p.y);
+                }
+                const float both = sum.x + sum.y;
+                tot += both;
+                add = fmaf(both, ivs[2 * u + b], add);
+              }
+            }
+            if (find || !__any_sync(0xffffffffu, tot > 16384.f)) break;
+            find = true;
           }
+          l_run += add;
+#pragma unroll
+          for (int u = 0; u < NK / 2; u += 32)  // the weights over the row's first NK / 2 columns
+            tmem_st32_async(tS + u, w + u);
         };
         if (full)
           step(std::false_type{});
@@ -329,8 +405,24 @@ __global__ void __launch_bounds__(16 * 32, 1)
       fp8_wait(bar(ODONE), ph_odone, abort_flag, c.status);
       ph_odone ^= 1;
       tc_fence_after();
-      const bool none = l_run == 0.f;  // the row saw no usable key: zeros
-      const float inv = none ? 0.f : 1.f / l_run;
+      // a row that saw no usable key is zeros: O is 0 then, but for an item
+      // without steps, whose O is not read (V's factor 2^-8 is undone here)
+      const float inv = l_run == 0.f ? 0.f : 256.f / l_run;
+      const float2 inv2 = make_float2(inv, inv);
+      auto out_words = [&](int col, uint32_t* w) {  // 32 columns as bf16 pairs
+        if (nsteps == 0) {
+#pragma unroll
+          for (int i = 0; i < 16; i++) w[i] = 0;
+          return;
+        }
+        float o[32];
+        tmem_ld32(tO + col, o);
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+          const float2 y = __fmul2_rn(make_float2(o[2 * i], o[2 * i + 1]), inv2);
+          w[i] = pack_bf16x2_rn(y.x, y.y);
+        }
+      };
       uint16_t* const orow = c.out + (long long)(q0 + tok0 + (rok ? j : 0)) * c.out_stride +
                              (long long)(h * c.group + (rok ? r - j * c.group : 0)) * D;
       const bool al32 = ((reinterpret_cast<uintptr_t>(c.out) | (uintptr_t)(c.out_stride * 2) | (uintptr_t)(D * 2)) & 31) == 0;
@@ -356,15 +448,9 @@ __global__ void __launch_bounds__(16 * 32, 1)
       const int qi = lane & 3;
 #pragma unroll 1
       for (int base = 0; base < D / 64 * 64; base += 64) {
-        uint32_t u[4][8];  // unit t: columns base + 16 t .. of this thread's row
-#pragma unroll
-        for (int hh = 0; hh < 2; hh++) {
-          float o[32];
-          tmem_ld32(tO + base + 32 * hh, o);
-#pragma unroll
-          for (int i = 0; i < 16; i++)
-            u[2 * hh + (i >> 3)][i & 7] = none ? 0u : pack_bf16x2_rn(o[2 * i] * inv, o[2 * i + 1] * inv);
-        }
+        uint32_t u[32];  // unit t, words 8 t ..: columns base + 16 t .. of this thread's row
+        out_words(base, u);
+        out_words(base + 32, u + 16);
 #pragma unroll
         for (int x = 1; x <= 2; x <<= 1) {
           const bool upper = (qi & x) != 0;
@@ -373,22 +459,20 @@ __global__ void __launch_bounds__(16 * 32, 1)
             if (a & x) continue;  // pairs (a, a + x)
 #pragma unroll
             for (int k = 0; k < 8; k++) {
-              const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? u[a][k] : u[a + x][k], x);
-              if (upper) u[a][k] = got;
-              else u[a + x][k] = got;
+              const int mine = 8 * a + k, other = 8 * (a + x) + k;
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? u[mine] : u[other], x);
+              if (upper) u[mine] = got;
+              else u[other] = got;
             }
           }
         }
 #pragma unroll
         for (int t = 0; t < 4; t++)
-          if (qrow[t] != nullptr) st32(qrow[t] + base + 16 * qi, u[t]);
+          if (qrow[t] != nullptr) st32(qrow[t] + base + 16 * qi, u + 8 * t);
       }
       if constexpr (D % 64 != 0) {  // the last 32 columns, each thread its own row
-        float o[32];
-        tmem_ld32(tO + D - 32, o);
         uint32_t w[16];
-#pragma unroll
-        for (int i = 0; i < 16; i++) w[i] = none ? 0u : pack_bf16x2_rn(o[2 * i] * inv, o[2 * i + 1] * inv);
+        out_words(D - 32, w);
         if (rok) {
           st32(orow + D - 32, w);
           st32(orow + D - 16, w + 8);
@@ -397,75 +481,81 @@ __global__ void __launch_bounds__(16 * 32, 1)
     }
   } else {
     // ============== convert, producer and MMA warps ==============
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
     // waits for completions of a barrier pair indexed by step parity, counted
     auto wait_until = [&](int first, int& done, int count) {
       for (; done < count; done++) fp8_wait(bar(first + (done & 1)), (done >> 1) & 1, abort_flag, c.status);
     };
-    if (warp < 14) {
+    if (warp < 16) {
       // ================= convert warps =================
-      const int ct = tid - 256;
-      uint32_t ph_ifull = 0;
-      const uint32_t neg = c.qscale < 0.f ? 0x80008000u : 0u;
-      int n = 0, kfree = 0, vfree = 0;
+      // one team's loop: kv = 0 K codes, 1 V codes
+      auto team = [&](auto kv_tag) {
+        constexpr int KV = decltype(kv_tag)::value;
+        constexpr int FULL = KV ? VFULL : KFULL, FREE = KV ? VFREE : KFREE;
+        // a thread takes 16-code chunks of one key, consecutive threads
+        // consecutive keys (the eight keys of a load or store phase fall in
+        // eight bank groups)
+        constexpr int TPK = 128 / NK;  // threads per key
+        const int t = tid & 127, k = t & (NK - 1), g0 = t / NK;
+        const uint8_t* const src = stg + KV * G::STG;
+        uint8_t* const tile = KV ? sV : sK;
+        const __nv_bfloat162 kf = __float2bfloat162_rn(c.qscale < 0.f ? -exp2_int(120) : exp2_int(120));
+        uint32_t ph_ifull = 0;
+        int n = 0, freed = 0;
 #pragma unroll 1
-      for (int itc = 0;; itc++) {
-        int4 item;
-        if (!take_item(itc & 1, ph_ifull, item)) break;
-        const int seq = item.x, tile = item.z, nkb = item.w;
-        const int L = c.seq_lens[seq], ctx = L - (c.qsl[seq + 1] - c.qsl[seq]);
-        const int kb0 = window_lo(c, ctx + tile * c.tile_tokens) >> 4;
-        const int nsteps = (nkb - kb0 + NB - 1) / NB;
+        for (int itc = 0;; itc++) {
+          int4 item;
+          if (!take_item(itc & 1, ph_ifull, item)) break;
+          const int seq = item.x, nkb = item.w;
+          const int L = c.seq_lens[seq], ctx = L - (c.qsl[seq + 1] - c.qsl[seq]);
+          const int kb0 = window_lo(c, ctx + item.z * c.tile_tokens) >> 4;
+          const int nsteps = (nkb - kb0 + NB - 1) / NB;
+          int keys = L - kb0 * 16;  // rows of the step that hold keys
 #pragma unroll 1
-        for (int st = 0; st < nsteps; st++, n++) {
-          const int b = n & 1;
-          // the staged codes into a tile: a thread takes 16 codes of one key,
-          // consecutive threads consecutive keys (the eight keys of a load or
-          // store phase fall in eight bank groups); rows behind the sequence
-          // are zeros in V (a NaN code would survive its zero weight)
-          const int keys = L - (kb0 + st * NB) * 16;
-          auto convert = [&](uint8_t* tile_dst, int kv) {
-            const uint8_t* sb = stg + kv * G::STG;
-#pragma unroll 3
-            for (int q = ct; q < NK * G::CHR; q += 32 * G::CV_WARPS) {
-              const int k = q & (NK - 1), g = q / NK;
-              uint4 x = *reinterpret_cast<const uint4*>(sb + G::chunk(k * G::CHR + g) * 16);
-              uint4 lo, hi;
-              if (kv) {
-                if (k >= keys) x = make_uint4(0, 0, 0, 0);
-                e4m3x4_to_f16x2(x.x, lo.x, lo.y);
-                e4m3x4_to_f16x2(x.y, lo.z, lo.w);
-                e4m3x4_to_f16x2(x.z, hi.x, hi.y);
-                e4m3x4_to_f16x2(x.w, hi.z, hi.w);
-              } else {
-                e4m3x4_to_bf16x2(x.x, neg, lo.x, lo.y);
-                e4m3x4_to_bf16x2(x.y, neg, lo.z, lo.w);
-                e4m3x4_to_bf16x2(x.z, neg, hi.x, hi.y);
-                e4m3x4_to_bf16x2(x.w, neg, hi.z, hi.w);
-              }
-              *reinterpret_cast<uint4*>(tile_dst + fp8_sw128(NK, k, 2 * g)) = lo;
-              *reinterpret_cast<uint4*>(tile_dst + fp8_sw128(NK, k, 2 * g + 1)) = hi;
-            }
-            fence_proxy_async_smem();  // the tile is read by the tensor cores, the stage rewritten by TMA
+          for (int st = 0; st < nsteps; st++, n++, keys -= NK) {
+            uint8_t* const dst = tile + (n & 1) * G::KVBYTES;
+            fp8_wait(bar(RKFULL + KV), n & 1, abort_flag, c.status);
+            // the step's codes are taken into registers first, so that the
+            // next step's copies run during the conversion
+            constexpr int U = G::CHR / TPK;
+            uint4 x[U];
+#pragma unroll
+            for (int i = 0; i < U; i++)
+              x[i] = *reinterpret_cast<const uint4*>(src + G::stage_off(k, i * TPK + (TPK > 1 ? g0 : 0)));
             __syncwarp();
-          };
-          fp8_wait(bar(RKFULL), n & 1, abort_flag, c.status);
-          wait_until(KFREE, kfree, n - 1);  // S of step n - 2
-          convert(sK + b * G::KVBYTES, 0);
-          if (lane == 0) {
-            fp8_arrive(bar(KFULL + b));
-            fp8_arrive(bar(RKFREE));
-          }
-          fp8_wait(bar(RVFULL), n & 1, abort_flag, c.status);
-          wait_until(VFREE, vfree, n - 1);  // WVs of step n - 2
-          convert(sV + b * G::KVBYTES, 1);
-          if (lane == 0) {
-            fp8_arrive(bar(VFULL + b));
-            fp8_arrive(bar(RVFREE));
+            if (lane == 0) fp8_arrive(bar(RKFREE + KV));
+            wait_until(FREE, freed, n - 1);  // the MMAs of step n - 2 that read this tile
+#pragma unroll
+            for (int i = 0; i < U; i++) {
+              const int g = i * TPK + (TPK > 1 ? g0 : 0);
+              uint4 lo, hi;
+              if constexpr (KV) {
+                // rows behind the sequence are zeros (a NaN code would survive its zero weight)
+                if (k >= keys) x[i] = make_uint4(0, 0, 0, 0);
+                e4m3x4_to_f16x2_256th(x[i].x, lo.x, lo.y);
+                e4m3x4_to_f16x2_256th(x[i].y, lo.z, lo.w);
+                e4m3x4_to_f16x2_256th(x[i].z, hi.x, hi.y);
+                e4m3x4_to_f16x2_256th(x[i].w, hi.z, hi.w);
+              } else {
+                e4m3x4_to_bf16x2(x[i].x, kf, lo.x, lo.y);
+                e4m3x4_to_bf16x2(x[i].y, kf, lo.z, lo.w);
+                e4m3x4_to_bf16x2(x[i].z, kf, hi.x, hi.y);
+                e4m3x4_to_bf16x2(x[i].w, kf, hi.z, hi.w);
+              }
+              *reinterpret_cast<uint4*>(dst + fp8_sw128(NK, k, 2 * g)) = lo;
+              *reinterpret_cast<uint4*>(dst + fp8_sw128(NK, k, 2 * g + 1)) = hi;
+            }
+            fence_proxy_async_smem();  // the tile is read by the tensor cores
+            __syncwarp();
+            if (lane == 0) fp8_arrive(bar(FULL + (n & 1)));
           }
         }
-      }
-    } else if (warp == 14) {
+      };
+      if (warp < 12)
+        team(std::integral_constant<int, 0>{});
+      else
+        team(std::integral_constant<int, 1>{});
+    } else if (warp == 16) {
       // ================= producer warp =================
       uint32_t ph_ifree = 0;
       int n = 0, nq = 0, kfree = 0;
@@ -554,86 +644,90 @@ __global__ void __launch_bounds__(16 * 32, 1)
       if (n > 0 && !(mbar_wait_bounded(bar(RKFULL), (n - 1) & 1) && mbar_wait_bounded(bar(RVFULL), (n - 1) & 1) &&
                      mbar_wait_bounded(bar(QFULL), (nq - 1) & 1)))
         flag(c.status, KV_INT4_DEV_TIMEOUT);
-    } else {
+    } else if (warp == 17) {
       // ================= MMA warp =================
-      const bool leader = lane == 0;
-      uint32_t ph_ifull = 0, ph_q = 0, ph_pfull = 0;
-      int n = 0, kfull = 0, vfull = 0;
+      uint32_t lead;
+      asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(lead));
+      int n = 0, kfull = 0, vfull = 0, items = 0, pfull = 0;
       const uint64_t dq = umma_desc(smem_addr(sQ), 16, 1024);
       const uint64_t dk = umma_desc(smem_addr(sK), 16, 1024);
       const uint64_t dv = umma_desc(smem_addr(sV), NK * 128, 1024);
+      const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);  // in a uniform register
+      auto wait = [&](int i, uint32_t parity) { fp8_wait_warp(bar(i), parity, abort_flag, c.status); };
+      auto until = [&](int first, int& done, int count) {
+        for (; done < count; done++) wait(first + (done & 1), (done >> 1) & 1);
+      };
+      auto issue_s = [&](int hh, int b) {
+        const uint64_t kt = dk + (uint64_t)(b * (G::KVBYTES >> 4));
+#pragma unroll
+        for (int ks = 0; ks < KSTEPS; ks++)
+          fp8_mma(lead, tm + NK * hh, dq + (uint64_t)(((ks >> 2) * ROWS * 128 + hh * 128 * 128 + (ks & 3) * 32) >> 4),
+                  kt + (uint64_t)(((ks >> 2) * NK * 128 + (ks & 3) * 32) >> 4), IDESC_S, ks > 0);
+      };
+      auto issue_wv = [&](int hh, int b, bool first) {
+        const uint64_t vt = dv + (uint64_t)(b * (G::KVBYTES >> 4));
+#pragma unroll
+        for (int kk = 0; kk < NB; kk++)
+          fp8_mma_ts(lead, tm + G::O_COL + hh * D, tm + NK * hh + kk * 8, vt + (uint64_t)(kk * (2048 >> 4)), IDESC_O,
+                     !first || kk > 0);
+      };
 #pragma unroll 1
       for (int itc = 0;; itc++) {
-        int4 item;
-        if (!take_item(itc & 1, ph_ifull, item)) break;
-        const int seq = item.x, tile = item.z, nkb = item.w;
-        const int ql = c.qsl[seq + 1] - c.qsl[seq];
-        const int ctx = c.seq_lens[seq] - ql;
-        const int kb0 = window_lo(c, ctx + tile * c.tile_tokens) >> 4;
-        const int nsteps = (nkb - kb0 + NB - 1) / NB;
-        auto issue_s = [&](int hh, int b) {
-          if (leader) {
-            const uint64_t kt = dk + (uint64_t)(b * (G::KVBYTES >> 4));
-#pragma unroll
-            for (int ks = 0; ks < KSTEPS; ks++)
-              umma_f16(tmem + NK * hh, dq + (uint64_t)(((ks >> 2) * ROWS * 128 + hh * 128 * 128 + (ks & 3) * 32) >> 4),
-                       kt + (uint64_t)(((ks >> 2) * NK * 128 + (ks & 3) * 32) >> 4), IDESC_S, ks > 0);
-          }
-        };
-        auto issue_wv = [&](int hh, int b, bool first) {
-          if (leader) {
-            const uint64_t vt = dv + (uint64_t)(b * (G::KVBYTES >> 4));
-#pragma unroll
-            for (int kk = 0; kk < NB; kk++)
-              umma_f16_ts(tmem + G::O_COL + hh * D, tmem + NK * hh + kk * 8, vt + (uint64_t)(kk * (2048 >> 4)), IDESC_O,
-                          !first || kk > 0);
-          }
-        };
-        auto commit = [&](int i) {
-          if (leader) umma_commit(bar(i));
-          __syncwarp();
-        };
+        wait(IFULL + (itc & 1), (itc >> 1) & 1);
+        const int4 item = item_at(itc & 1);
+        __syncwarp();
+        if (lane == 0) fp8_arrive(bar(IFREE + (itc & 1)));
+        __syncwarp();
+        // the step count through a warp reduction, whose result is uniform;
+        // none once a wait has run out
+        int steps = -1;
+        if (item.x >= 0 && !*abort_flag) {
+          const int ql = c.qsl[item.x + 1] - c.qsl[item.x];
+          const int kb0 = window_lo(c, c.seq_lens[item.x] - ql + item.z * c.tile_tokens) >> 4;
+          steps = (item.w - kb0 + NB - 1) / NB;
+        }
+        const int nsteps = __reduce_min_sync(0xffffffffu, steps);
+        if (nsteps < 0) break;
         if (nsteps > 0) {
-          fp8_wait(bar(QFULL), ph_q, abort_flag, c.status);
-          ph_q ^= 1;
-          wait_until(KFULL, kfull, n + 1);
+          wait(QFULL, items & 1);
+          items++;
+          until(KFULL, kfull, n + 1);
           tc_fence_after();
           issue_s(0, n & 1);
-          commit(SFULL);
+          fp8_commit(lead, bar(SFULL));
           issue_s(1, n & 1);
-          commit(SFULL + 1);
-          commit(KFREE + (n & 1));
+          fp8_commit(lead, bar(SFULL + 1));
+          fp8_commit(lead, bar(KFREE + (n & 1)));
         }
 #pragma unroll 1
         for (int st = 0; st < nsteps; st++, n++) {
           const int b = n & 1, nb = b ^ 1;
           const bool more = st + 1 < nsteps;
-          wait_until(VFULL, vfull, n + 1);
-          if (more) wait_until(KFULL, kfull, n + 2);
-          fp8_wait(bar(PFULL), ph_pfull & 1, abort_flag, c.status);
-          ph_pfull ^= 1;
+          until(VFULL, vfull, n + 1);
+          if (more) until(KFULL, kfull, n + 2);
+          wait(PFULL, pfull & 1);
           tc_fence_after();
           issue_wv(0, b, st == 0);
           if (more) {
             issue_s(0, nb);
-            commit(SFULL);
+            fp8_commit(lead, bar(SFULL));
           }
-          fp8_wait(bar(PFULL + 1), (ph_pfull >> 1) & 1, abort_flag, c.status);
-          ph_pfull ^= 2;
+          wait(PFULL + 1, pfull & 1);
+          pfull++;
           tc_fence_after();
           issue_wv(1, b, st == 0);
-          commit(VFREE + b);
+          fp8_commit(lead, bar(VFREE + b));
           if (more) {
             issue_s(1, nb);
-            commit(SFULL + 1);
-            commit(KFREE + nb);
+            fp8_commit(lead, bar(SFULL + 1));
+            fp8_commit(lead, bar(KFREE + nb));
           }
         }
-        commit(ODONE);
+        fp8_commit(lead, bar(ODONE));
       }
     }
   }
-  if (warp == 15) {
+  if (warp == 17) {
     // after a time-out MMAs may still be in flight: they end by themselves
     // and must end before the columns are freed
     if (lane == 0) umma_commit(bar(DRAIN));
