@@ -20,6 +20,7 @@
 // sequence may need it), decode, merge.
 
 #include <cuda.h>
+#include <float.h>
 
 #include <type_traits>
 

@@ -129,8 +129,36 @@ __device__ __forceinline__ void fp8_wait_warp(uint32_t bar, uint32_t parity, vol
   *abort = 1;
   flag(status, KV_INT4_DEV_TIMEOUT);
 }
-// a warp's 32 lanes x 32 words to TMEM, not waited for
-__device__ __forceinline__ void tmem_st32_async(uint32_t taddr, const uint32_t* v) {
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+// a warp's 32 lanes x 64 consecutive columns, one wait for both halves
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+  uint32_t r[64];
+#pragma unroll
+  for (int h = 0; h < 64; h += 32)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        : "=r"(r[h + 0]), "=r"(r[h + 1]), "=r"(r[h + 2]), "=r"(r[h + 3]), "=r"(r[h + 4]), "=r"(r[h + 5]),
+          "=r"(r[h + 6]), "=r"(r[h + 7]), "=r"(r[h + 8]), "=r"(r[h + 9]), "=r"(r[h + 10]), "=r"(r[h + 11]),
+          "=r"(r[h + 12]), "=r"(r[h + 13]), "=r"(r[h + 14]), "=r"(r[h + 15]), "=r"(r[h + 16]), "=r"(r[h + 17]),
+          "=r"(r[h + 18]), "=r"(r[h + 19]), "=r"(r[h + 20]), "=r"(r[h + 21]), "=r"(r[h + 22]), "=r"(r[h + 23]),
+          "=r"(r[h + 24]), "=r"(r[h + 25]), "=r"(r[h + 26]), "=r"(r[h + 27]), "=r"(r[h + 28]), "=r"(r[h + 29]),
+          "=r"(r[h + 30]), "=r"(r[h + 31])
+        : "r"(taddr + h));
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 64; i++) v[i] = __uint_as_float(r[i]);
+}
+// not waited for
+__device__ __forceinline__ void tmem_st32w(uint32_t taddr, const uint32_t (&v)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
       "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
@@ -138,6 +166,14 @@ __device__ __forceinline__ void tmem_st32_async(uint32_t taddr, const uint32_t* 
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
       "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
       "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&w)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(
+          taddr),
+      "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]), "r"(w[9]),
+      "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
       : "memory");
 }
 // a tensor-map box at coordinates (0, 0, head, row) into shared memory
@@ -295,106 +331,106 @@ __global__ void __launch_bounds__(20 * 32, 1)
         ph_sfull ^= 1;
         tc_fence_after();
         const int pos0 = (kb0 + st * NB) * 16;
-        // keys of the step that the row sees: [lo - pos0, lim - pos0) of usable blocks
-        auto visible = [&](int u) -> uint32_t {  // columns 32 u .. 32 u + 31
-          const int a = lo - pos0 - 32 * u, z = lim - pos0 - 32 * u;
-          const uint32_t from = a <= 0 ? 0xffffffffu : a >= 32 ? 0u : 0xffffffffu << a;
-          const uint32_t to = z >= 32 ? 0xffffffffu : z <= 0 ? 0u : 0xffffffffu >> (32 - z);
-          return from & to & (ok[2 * u] ? 0x0000ffffu : 0u) | from & to & (ok[2 * u + 1] ? 0xffff0000u : 0u);
-        };
-        // the warp's rows all see the whole step: no mask (the usual case; the
-        // two cases are compiled apart, a mask on every score would cost more
-        // than the softmax)
+        // the warp's rows all see the whole step: no mask (the usual case)
         const bool full = __all_sync(0xffffffffu, pos0 >= lo && pos0 + NK <= lim && ok[NB] != 0);
-        auto step = [&](auto masked_tag) {
-          constexpr bool MASKED = decltype(masked_tag)::value;
-          uint32_t w[NK / 2];
-          // The weights are computed against the reference as it stands; their
-          // sum bounds the largest, so the row's maximum is only looked for
-          // where some row of the warp has no reference yet or a sum above 2^14
-          // (S is whole until the weights are stored)
-          bool find = __any_sync(0xffffffffu, m_ref == -INFINITY);
-          float add, tot = INFINITY;
+        // 64 columns (four blocks) at a time, as a loop: eighteen warps in five
+        // roles share the instruction caches, and steps written out in full
+        // stalled on instruction fetch more than on anything else
 #pragma unroll 1
-          while (true) {
-            if (find) {
-              float mx = -INFINITY;
+        for (int u = 0; u < NK / 64; u++) {
+          const float4 fk = *reinterpret_cast<const float4*>(re + 4 * u);
+          const float4 kvb = *reinterpret_cast<const float4*>(kvf + 4 * u);
+          // (never 0, so that a hidden key's -inf stays -inf)
+          const float f[4] = {fmaxf(cf * fk.x, FLT_MIN), fmaxf(cf * fk.y, FLT_MIN), fmaxf(cf * fk.z, FLT_MIN),
+                              fmaxf(cf * fk.w, FLT_MIN)};
+          const float kb[4] = {kvb.x, kvb.y, kvb.z, kvb.w};
+          float s[64];
+          tmem_ld64(tS + 64 * u, s);
+          if (!full) {
+            __syncwarp();  // a branch, not 64 selects in every step
 #pragma unroll
-              for (int u = 0; u < NK / 32; u++) {
-                float s[32];
-                tmem_ld32(tS + 32 * u, s);
-                if constexpr (MASKED) {
-                  const uint32_t vis = visible(u);
+            for (int b = 0; b < 4; b++) {
+              // keys of block b that the row sees: [lo, lim), if it is usable
+              const int first = lo - pos0 - 64 * u - 16 * b, last = lim - pos0 - 64 * u - 16 * b;
+              uint32_t vis = first <= 0 ? 0xffffu : first >= 16 ? 0u : 0xffffu << first;
+              vis &= last >= 16 ? 0xffffu : last <= 0 ? 0u : 0xffffu >> (16 - last);
+              if (!ok[4 * u + b]) vis = 0;
 #pragma unroll
-                  for (int k = 0; k < 32; k++) s[k] = (vis >> k) & 1 ? s[k] : -INFINITY;
-                }
-#pragma unroll
-                for (int b = 0; b < 2; b++) {
-                  const float* t = s + 16 * b;
-                  const float a = fmax3(fmax3(t[0], t[1], t[2]), fmax3(t[3], t[4], t[5]), fmax3(t[6], t[7], t[8]));
-                  const float d = fmax3(fmax3(t[9], t[10], t[11]), fmax3(t[12], t[13], t[14]), t[15]);
-                  const float top = fmaxf(a, d);
-                  const float v = fmaf(top, cf * re[2 * u + b], kvf[2 * u + b]);
-                  mx = fmaxf(mx, MASKED && top == -INFINITY ? -INFINITY : v);
-                }
-              }
-              const bool grow = m_ref == -INFINITY || (tot > 16384.f && mx > m_ref);
-              const float alpha = grow && m_ref != -INFINITY ? fast_exp2(m_ref - mx) : 1.f;
-              if (grow) m_ref = mx;
-              if (__any_sync(0xffffffffu, alpha != 1.f)) {
-                // O of this half is complete up to the previous step (S_h of this step was issued after it)
-#pragma unroll 1
-                for (int cc = 0; cc < D / 32; cc++) {
-                  float o[32];
-                  tmem_ld32(tO + cc * 32, o);
-#pragma unroll
-                  for (int i = 0; i < 32; i++) o[i] *= alpha;
-                  tmem_st32(tO + cc * 32, o);
-                }
-              }
-              l_run *= alpha;
+              for (int k = 0; k < 16; k++)
+                if (!(vis & (1u << k))) s[16 * b + k] = -INFINITY;
             }
-            const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-            add = tot = 0.f;
-#pragma unroll
-            for (int u = 0; u < NK / 32; u++) {
-              float s[32];
-              tmem_ld32(tS + 32 * u, s);
-              uint32_t vis = 0;
-              if constexpr (MASKED) vis = visible(u);
-#pragma unroll
-              for (int b = 0; b < 2; b++) {
-                const float f = cf * re[2 * u + b], o = kvf[2 * u + b] - mu;
-                const float2 f2 = make_float2(f, f), o2 = make_float2(o, o);
-                float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int k = 0; k < 16; k += 2) {
-                  const float2 t = f2fma(make_float2(s[16 * b + k], s[16 * b + k + 1]), f2, o2);
-                  float2 p = make_float2(fast_exp2(t.x), fast_exp2(t.y));
-                  if constexpr (MASKED) {
-                    p.x = (vis >> (16 * b + k)) & 1 ? p.x : 0.f;
-                    p.y = (vis >> (16 * b + k + 1)) & 1 ? p.y : 0.f;
-                  }
-                  sum = f2add(sum, p);
-                  w[16 * u + 8 * b + k / 2] = pack_f16x2(p.x, p.y);
-                }
-                const float both = sum.x + sum.y;
-                tot += both;
-                add = fmaf(both, ivs[2 * u + b], add);
-              }
-            }
-            if (find || !__any_sync(0xffffffffu, tot > 16384.f)) break;
-            find = true;
           }
-          l_run += add;
+          // moves the reference to the row's maximum where it has none or is more
+          // than 8 behind; whole numbers, so that O, l and the step's weights so
+          // far move by exact powers of two
+          auto find = [&]() {
+            float mx = -INFINITY;
 #pragma unroll
-          for (int u = 0; u < NK / 2; u += 32)  // the weights over the row's first NK / 2 columns
-            tmem_st32_async(tS + u, w + u);
-        };
-        if (full)
-          step(std::false_type{});
-        else
-          step(std::true_type{});
+            for (int b = 0; b < 4; b++) {
+              float t = s[16 * b];
+#pragma unroll
+              for (int k = 1; k < 16; k++) t = fmaxf(t, s[16 * b + k]);
+              mx = fmaxf(mx, fmaf(t, f[b], kb[b]));
+            }
+            mx = ceilf(mx);
+            const bool grow = mx > m_ref + (m_ref == -INFINITY ? 0.f : 8.f);
+            const float alpha = grow && m_ref != -INFINITY ? fast_exp2(m_ref - mx) : 1.f;
+            if (grow) m_ref = mx;
+            if (!__any_sync(0xffffffffu, alpha != 1.f)) return;
+            l_run *= alpha;
+            // O is complete up to the previous step (S_h of this step was issued after it)
+#pragma unroll 1
+            for (int cc = 0; cc < D / 32; cc++) {
+              float o[32];
+              tmem_ld32(tO + cc * 32, o);
+#pragma unroll
+              for (int i = 0; i < 32; i++) o[i] *= alpha;
+              tmem_st32(tO + cc * 32, o);
+            }
+            asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+#pragma unroll 1
+            for (int cc = 0; cc < 2 * u; cc++) {
+              uint32_t x[16];
+              tmem_ld16(tS + 16 * cc, x);
+#pragma unroll
+              for (int i = 0; i < 16; i++) {
+                const float2 y = __half22float2(*reinterpret_cast<__half2*>(&x[i]));
+                x[i] = pack_f16x2(y.x * alpha, y.y * alpha);
+              }
+              tmem_st16(tS + 16 * cc, x);
+            }
+          };
+          uint32_t w[32];
+          float tot[4];
+          auto weights = [&]() {
+            const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+#pragma unroll
+            for (int b = 0; b < 4; b++) {
+              const float2 g = make_float2(f[b], f[b]), o = make_float2(kb[b] - mu, kb[b] - mu);
+              float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int k = 0; k < 16; k += 2) {
+                const float2 a = f2fma(make_float2(s[16 * b + k], s[16 * b + k + 1]), g, o);
+                const float2 p = make_float2(fast_exp2(a.x), fast_exp2(a.y));
+                sum = f2add(sum, p);
+                w[8 * b + k / 2] = pack_f16x2(p.x, p.y);
+              }
+              tot[b] = sum.x + sum.y;
+            }
+          };
+          // The weights against the reference as it stands; their sum bounds the
+          // largest, so that maximum is only looked for where some row of the
+          // warp has no reference yet or a sum above 2^14
+          if (__any_sync(0xffffffffu, m_ref == -INFINITY)) find();
+          weights();
+          if (__any_sync(0xffffffffu, (tot[0] + tot[1]) + (tot[2] + tot[3]) > 16384.f)) {
+            find();
+            weights();
+          }
+          const float4 iv = *reinterpret_cast<const float4*>(ivs + 4 * u);
+          l_run = fmaf(tot[0], iv.x, fmaf(tot[1], iv.y, fmaf(tot[2], iv.z, fmaf(tot[3], iv.w, l_run))));
+          tmem_st32w(tS + 32 * u, w);  // over columns [32 u, 32 u + 32), which have been read
+        }
         asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
         tc_fence_before();
         __syncwarp();
@@ -515,35 +551,43 @@ __global__ void __launch_bounds__(20 * 32, 1)
           for (int st = 0; st < nsteps; st++, n++, keys -= NK) {
             uint8_t* const dst = tile + (n & 1) * G::KVBYTES;
             fp8_wait(bar(RKFULL + KV), n & 1, abort_flag, c.status);
-            // the step's codes are taken into registers first, so that the
-            // next step's copies run during the conversion
-            constexpr int U = G::CHR / TPK;
-            uint4 x[U];
+            // the step's codes are taken into registers first: the next step's
+            // copies (about 2000 cycles) run during the conversion
+            constexpr int CH = G::CHR / TPK, U = (CH + 1) / 2;  // chunks, and as a loop of two (instruction caches)
+            uint4 x[U], y[U];
 #pragma unroll
-            for (int i = 0; i < U; i++)
+            for (int i = 0; i < U; i++) {
               x[i] = *reinterpret_cast<const uint4*>(src + G::stage_off(k, i * TPK + (TPK > 1 ? g0 : 0)));
+              y[i] = *reinterpret_cast<const uint4*>(src + G::stage_off(k, (U + i) * TPK + (TPK > 1 ? g0 : 0)));
+            }
+            static_assert(2 * U == CH, "an even number of chunks");
             __syncwarp();
             if (lane == 0) fp8_arrive(bar(RKFREE + KV));
             wait_until(FREE, freed, n - 1);  // the MMAs of step n - 2 that read this tile
+#pragma unroll 1
+            for (int i0 = 0; i0 < CH; i0 += U) {
 #pragma unroll
-            for (int i = 0; i < U; i++) {
-              const int g = i * TPK + (TPK > 1 ? g0 : 0);
-              uint4 lo, hi;
-              if constexpr (KV) {
-                // rows behind the sequence are zeros (a NaN code would survive its zero weight)
-                if (k >= keys) x[i] = make_uint4(0, 0, 0, 0);
-                e4m3x4_to_f16x2_256th(x[i].x, lo.x, lo.y);
-                e4m3x4_to_f16x2_256th(x[i].y, lo.z, lo.w);
-                e4m3x4_to_f16x2_256th(x[i].z, hi.x, hi.y);
-                e4m3x4_to_f16x2_256th(x[i].w, hi.z, hi.w);
-              } else {
-                e4m3x4_to_bf16x2(x[i].x, kf, lo.x, lo.y);
-                e4m3x4_to_bf16x2(x[i].y, kf, lo.z, lo.w);
-                e4m3x4_to_bf16x2(x[i].z, kf, hi.x, hi.y);
-                e4m3x4_to_bf16x2(x[i].w, kf, hi.z, hi.w);
+              for (int i = 0; i < U; i++) {
+                const int g = (i0 + i) * TPK + (TPK > 1 ? g0 : 0);
+                uint4 lo, hi;
+                if constexpr (KV) {
+                  // rows behind the sequence are zeros (a NaN code would survive its zero weight)
+                  if (k >= keys) x[i] = make_uint4(0, 0, 0, 0);
+                  e4m3x4_to_f16x2_256th(x[i].x, lo.x, lo.y);
+                  e4m3x4_to_f16x2_256th(x[i].y, lo.z, lo.w);
+                  e4m3x4_to_f16x2_256th(x[i].z, hi.x, hi.y);
+                  e4m3x4_to_f16x2_256th(x[i].w, hi.z, hi.w);
+                } else {
+                  e4m3x4_to_bf16x2(x[i].x, kf, lo.x, lo.y);
+                  e4m3x4_to_bf16x2(x[i].y, kf, lo.z, lo.w);
+                  e4m3x4_to_bf16x2(x[i].z, kf, hi.x, hi.y);
+                  e4m3x4_to_bf16x2(x[i].w, kf, hi.z, hi.w);
+                }
+                *reinterpret_cast<uint4*>(dst + fp8_sw128(NK, k, 2 * g)) = lo;
+                *reinterpret_cast<uint4*>(dst + fp8_sw128(NK, k, 2 * g + 1)) = hi;
               }
-              *reinterpret_cast<uint4*>(dst + fp8_sw128(NK, k, 2 * g)) = lo;
-              *reinterpret_cast<uint4*>(dst + fp8_sw128(NK, k, 2 * g + 1)) = hi;
+#pragma unroll
+              for (int i = 0; i < U; i++) x[i] = y[i];
             }
             fence_proxy_async_smem();  // the tile is read by the tensor cores
             __syncwarp();
@@ -691,36 +735,28 @@ __global__ void __launch_bounds__(20 * 32, 1)
         if (nsteps > 0) {
           wait(QFULL, items & 1);
           items++;
-          until(KFULL, kfull, n + 1);
-          tc_fence_after();
-          issue_s(0, n & 1);
-          fp8_commit(lead, bar(SFULL));
-          issue_s(1, n & 1);
-          fp8_commit(lead, bar(SFULL + 1));
-          fp8_commit(lead, bar(KFREE + (n & 1)));
         }
+        // iteration st: for each half, the WV of step st - 1 and the S of step st
 #pragma unroll 1
-        for (int st = 0; st < nsteps; st++, n++) {
-          const int b = n & 1, nb = b ^ 1;
-          const bool more = st + 1 < nsteps;
-          until(VFULL, vfull, n + 1);
-          if (more) until(KFULL, kfull, n + 2);
-          wait(PFULL, pfull & 1);
-          tc_fence_after();
-          issue_wv(0, b, st == 0);
-          if (more) {
-            issue_s(0, nb);
-            fp8_commit(lead, bar(SFULL));
+        for (int st = 0; st <= nsteps; st++) {
+          const bool wv = st > 0, sc = st < nsteps;
+          if (wv) until(VFULL, vfull, n);
+          if (sc) until(KFULL, kfull, n + 1);
+#pragma unroll 1
+          for (int hh = 0; hh < 2; hh++) {
+            if (wv) wait(PFULL + hh, pfull & 1);
+            tc_fence_after();
+            if (wv) issue_wv(hh, (n - 1) & 1, st == 1);
+            if (wv && hh) fp8_commit(lead, bar(VFREE + ((n - 1) & 1)));
+            if (sc) {
+              issue_s(hh, n & 1);
+              fp8_commit(lead, bar(SFULL + hh));
+            }
           }
-          wait(PFULL + 1, pfull & 1);
-          pfull++;
-          tc_fence_after();
-          issue_wv(1, b, st == 0);
-          fp8_commit(lead, bar(VFREE + b));
-          if (more) {
-            issue_s(1, nb);
-            fp8_commit(lead, bar(SFULL + 1));
-            fp8_commit(lead, bar(KFREE + nb));
+          if (wv) pfull++;
+          if (sc) {
+            fp8_commit(lead, bar(KFREE + (n & 1)));
+            n++;
           }
         }
         fp8_commit(lead, bar(ODONE));
