@@ -120,10 +120,12 @@ __device__ __forceinline__ void fp8_commit(uint32_t lead, uint32_t bar) {
       "r"(lead)
       : "memory");
 }
-// fp8_wait by a converged warp, for control flow that is the same for all lanes
-__device__ __forceinline__ void fp8_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
+// fp8_wait by a converged warp, for control flow that is the same for all
+// lanes; each lane that is not idle may wait for a barrier of its own
+__device__ __forceinline__ void fp8_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status,
+                                              bool idle = false) {
   for (int n = 0; n < kMaxWaitIters; n++) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
+    if (__all_sync(0xffffffffu, idle || mbar_try_wait(bar, parity))) return;
     if ((n & 255) == 255 && __any_sync(0xffffffffu, *abort)) return;
   }
   *abort = 1;
@@ -692,15 +694,12 @@ __global__ void __launch_bounds__(20 * 32, 1)
       // ================= MMA warp =================
       uint32_t lead;
       asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(lead));
-      int n = 0, kfull = 0, vfull = 0, items = 0, pfull = 0;
+      int n = 0, items = 0, pfull = 0;
       const uint64_t dq = umma_desc(smem_addr(sQ), 16, 1024);
       const uint64_t dk = umma_desc(smem_addr(sK), 16, 1024);
       const uint64_t dv = umma_desc(smem_addr(sV), NK * 128, 1024);
       const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);  // in a uniform register
       auto wait = [&](int i, uint32_t parity) { fp8_wait_warp(bar(i), parity, abort_flag, c.status); };
-      auto until = [&](int first, int& done, int count) {
-        for (; done < count; done++) wait(first + (done & 1), (done >> 1) & 1);
-      };
       auto issue_s = [&](int hh, int b) {
         const uint64_t kt = dk + (uint64_t)(b * (G::KVBYTES >> 4));
 #pragma unroll
@@ -736,24 +735,32 @@ __global__ void __launch_bounds__(20 * 32, 1)
           wait(QFULL, items & 1);
           items++;
         }
-        // iteration st: for each half, the WV of step st - 1 and the S of step st
+        // iteration st: for each half, the WV of step st - 1 and the S of step
+        // st.  A wait costs the warp some 400 cycles even when it is satisfied,
+        // so the first half's three barriers are waited for at once, a lane each
 #pragma unroll 1
         for (int st = 0; st <= nsteps; st++) {
           const bool wv = st > 0, sc = st < nsteps;
-          if (wv) until(VFULL, vfull, n);
-          if (sc) until(KFULL, kfull, n + 1);
+          {
+            // V of step n - 1, the first half's W of it, K of step n
+            const int i = lane == 0 ? VFULL + ((n - 1) & 1) : lane == 1 ? PFULL : KFULL + (n & 1);
+            const uint32_t ph = lane == 0 ? ((n - 1) >> 1) & 1 : lane == 1 ? pfull & 1 : (n >> 1) & 1;
+            const bool idle = lane > 2 || !(lane == 2 ? sc : wv);
+            fp8_wait_warp(bar(i), ph, abort_flag, c.status, idle);
+          }
 #pragma unroll 1
           for (int hh = 0; hh < 2; hh++) {
-            if (wv) wait(PFULL + hh, pfull & 1);
+            if (wv && hh) wait(PFULL + 1, pfull++ & 1);
             tc_fence_after();
-            if (wv) issue_wv(hh, (n - 1) & 1, st == 1);
-            if (wv && hh) fp8_commit(lead, bar(VFREE + ((n - 1) & 1)));
+            if (wv) {
+              issue_wv(hh, (n - 1) & 1, st == 1);
+              if (hh) fp8_commit(lead, bar(VFREE + ((n - 1) & 1)));
+            }
             if (sc) {
               issue_s(hh, n & 1);
               fp8_commit(lead, bar(SFULL + hh));
             }
           }
-          if (wv) pfull++;
           if (sc) {
             fp8_commit(lead, bar(KFREE + (n & 1)));
             n++;
