@@ -32,7 +32,11 @@
 namespace kvint4 {
 namespace {
 
-__global__ void __launch_bounds__(kPrepThreads) plan_fp8_kernel(Common c, PlanView pv) { build_schedule<true>(c, pv); }
+__global__ void __launch_bounds__(kPrepThreads) plan_fp8_kernel(Common c, PlanView pv) {
+  pdl_trigger();
+  pdl_wait();
+  build_schedule<true>(c, pv);
+}
 
 // A query row's power of two from its largest bf16 magnitude bits: rows are
 // multiplied by 2^-e (so that |q'| < 2) and scores by 2^e.  Rows of zeros and
@@ -66,8 +70,7 @@ EncodeTiled encode_tiled() {
 }
 
 int launch_plan(const Common& c, const PlanView& pv, cudaStream_t stream) {
-  plan_fp8_kernel<<<1, kPrepThreads, 0, stream>>>(c, pv);
-  return cudaGetLastError() == cudaSuccess ? KV_INT4_OK : KV_INT4_ERR_CUDA;
+  return launch_pdl(plan_fp8_kernel, dim3(1), kPrepThreads, 0, stream, 1, c, pv);
 }
 
 // the tensor maps of a call's prefill; false where its tensors have no such
@@ -137,13 +140,19 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
   c.out_stride = a.out_stride;
   c.status = a.dev_status;
   c.max_items = L.max_prefill_items;
+  // f with the number of blocks per position as a constant
+  auto with_np = [](int np, auto&& f) {
+    if (np == 1) return f(std::integral_constant<int, 1>{});
+    if (np == 2) return f(std::integral_constant<int, 2>{});
+    return f(std::integral_constant<int, kFp8Quad<D> ? 4 : 2>{});
+  };
   // decode: blocks per position, kv heads per CTA, CTAs
   c.hg = c.ng = c.nl = c.np = 1;
   const bool any_decode = c.group <= kDecodeCols;
-  int dec_grid = 0;
+  int dec_grid = 0, dec_occ = 0;
   if (any_decode) {
     static PerContext<int> occ_cache[3][5];
-    int occ = 0;
+    int& occ = dec_occ;
     auto take = [&](auto np_tag) {
       constexpr int NP = decltype(np_tag)::value;
       using G = Fp8Dec<D, NP>;
@@ -156,8 +165,9 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
         }
       return occ_cache[NP / 2][c.hg].get(dev, [&](int* v) {
         int unused;  // the attribute is raised once, to the largest ring in use
-        return configure(decode_fp8_kernel<D, NP>, (228 * 1024) / 2 - 1024, 128, &unused) &&
-               cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, decode_fp8_kernel<D, NP>, c.hg * 32,
+        return configure(decode_fp8_kernel<D, NP, true>, (228 * 1024) / 2 - 1024, 128, &unused) &&
+               configure(decode_fp8_kernel<D, NP, false>, (228 * 1024) / 2 - 1024, 128, &unused) &&
+               cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, decode_fp8_kernel<D, NP, false>, c.hg * 32,
                                                              G::smem_bytes(c.hg)) == cudaSuccess && *v >= 1;
       }, &occ);
     };
@@ -166,14 +176,7 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
     // decode is sized for single-token queries and longer ones go to prefill
     const long long mq = (long long)(a.max_query_len > 0 ? a.max_query_len : 1) * c.group;
     const long long cols = mq <= kDecodeCols ? mq : c.group;
-    bool ok;
-    if (cols > 4)
-      ok = take(std::integral_constant<int, 1>{});
-    else if (cols > 2 || !kFp8Quad<D>)
-      ok = take(std::integral_constant<int, 2>{});
-    else
-      ok = take(std::integral_constant<int, kFp8Quad<D> ? 4 : 2>{});
-    if (!ok) return KV_INT4_ERR_CUDA;
+    if (!with_np(cols > 4 ? 1 : cols > 2 || !kFp8Quad<D> ? 2 : 4, take)) return KV_INT4_ERR_CUDA;
     c.ng = a.num_kv_heads / c.hg;
     long long grid = (long long)sms * occ;
     if (grid * c.hg > kMaxDecodeWarps) grid = kMaxDecodeWarps / c.hg;
@@ -188,10 +191,33 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
   }
   c.dcols = kDecodeCols / c.np;
 
+  const bool may_prefill = c.group > c.dcols || (long long)a.max_query_len * c.group > c.dcols;
+  if (!may_prefill) {
+    // one launch of clusters where the whole batch runs at once and the shares
+    // are short: the largest cluster that leaves every CTA resident, or shares
+    // of two positions (1 x 97 keys: 7.4 us against 11.5; 8 x 1024: 12 against
+    // 18; shares of more than 16 positions, or a second wave of CTAs, do better
+    // with the balanced split)
+    const long long tasks = (long long)a.num_seqs * c.ng, room = (long long)sms * dec_occ;
+    const long long table = (long long)a.max_blocks_per_seq * 16;
+    const long long most = ((a.max_seq_len < table ? a.max_seq_len : table) + 16 * c.np - 1) / (16 * c.np);
+    int cl = 1;
+    while (cl < 8 && 2 * tasks * cl <= room && most > 2 * cl) cl *= 2;
+    if (tasks * cl <= room && most <= 16 * cl) {
+      timing_begin(kTimedDecode, stream);
+      const int e = with_np(c.np, [&](auto np_tag) {
+        constexpr int NP = decltype(np_tag)::value;
+        return launch_pdl(decode_fp8_kernel<D, NP, true>, dim3((unsigned)(tasks * cl)), c.hg * 32,
+                          Fp8Dec<D, NP>::smem_bytes(c.hg), stream, cl, Fp8DecParams{c, pv, 0, cl});
+      });
+      timing_end(kTimedDecode, stream);
+      return e;
+    }
+  }
+
   // prefill items: 256 rows on the tensor-core kernel (head sizes up to 192:
   // two accumulators of 256 columns would leave no TMEM for scores), 64 on the
   // warp-MMA one
-  const bool may_prefill = c.group > c.dcols || (long long)a.max_query_len * c.group > c.dcols;
   bool tc = false;
   if constexpr (D <= 192) {
     Fp8Maps maps;
@@ -207,9 +233,9 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
         return KV_INT4_ERR_CUDA;
       const long long grid = sms < L.max_prefill_items ? sms : L.max_prefill_items;
       timing_begin(kTimedPrefill, stream);
-      prefill_ws_fp8_kernel<D><<<(unsigned)grid, G::THREADS, G::SMEM, stream>>>(c, pv, maps);
+      const int e = launch_pdl(prefill_ws_fp8_kernel<D>, dim3((unsigned)grid), G::THREADS, G::SMEM, stream, 1, c, pv, maps);
       timing_end(kTimedPrefill, stream);
-      if (cudaGetLastError() != cudaSuccess) return KV_INT4_ERR_CUDA;
+      if (e) return e;
     }
   } else {
     c.tile_tokens = kPrefillRows / c.group;
@@ -224,40 +250,35 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
     long long grid = (long long)sms * occ;
     if (grid > L.max_prefill_items) grid = L.max_prefill_items;
     timing_begin(kTimedPrefill, stream);
-    prefill_fp8_kernel<D><<<(unsigned)grid, G::THREADS, G::SMEM, stream>>>(c, pv);
+    const int e = launch_pdl(prefill_fp8_kernel<D>, dim3((unsigned)grid), G::THREADS, G::SMEM, stream, 1, c, pv);
     timing_end(kTimedPrefill, stream);
-    if (cudaGetLastError() != cudaSuccess) return KV_INT4_ERR_CUDA;
+    if (e) return e;
   }
   if (any_decode) {
-    const Fp8DecParams prm{c, pv, dec_grid};
+    const Fp8DecParams prm{c, pv, dec_grid, 1};
     const int threads = c.hg * 32;
     timing_begin(kTimedDecode, stream);
-    auto go = [&](auto np_tag) {
+    int e = with_np(c.np, [&](auto np_tag) {
       constexpr int NP = decltype(np_tag)::value;
-      decode_fp8_kernel<D, NP><<<dec_grid, threads, Fp8Dec<D, NP>::smem_bytes(c.hg), stream>>>(prm);
-    };
-    if (c.np == 1)
-      go(std::integral_constant<int, 1>{});
-    else if (c.np == 2)
-      go(std::integral_constant<int, 2>{});
-    else
-      go(std::integral_constant<int, kFp8Quad<D> ? 4 : 2>{});
+      return launch_pdl(decode_fp8_kernel<D, NP, false>, dim3(dec_grid), threads, Fp8Dec<D, NP>::smem_bytes(c.hg), stream,
+                        1, prm);
+    });
     timing_end(kTimedDecode, stream);
-    if (cudaGetLastError() != cudaSuccess) return KV_INT4_ERR_CUDA;
+    if (e) return e;
     // merge: a CTA per (sequence, kv head) segment, a warp per query column
-    // and piece lane; lanes enough that each merges about four pieces
+    // and piece lane; lanes enough that each merges one or two pieces
     const long long mcols = (long long)(a.max_query_len > 0 ? a.max_query_len : 1) * c.group;
     const int cols = (int)(mcols < c.dcols ? mcols : c.dcols);
     const long long segs = (long long)a.num_seqs * a.num_kv_heads;
     const long long pieces = 1 + (long long)dec_grid * c.hg / (segs > 0 ? segs : 1);
     int lanes = 1;
-    while (lanes < 8 && lanes * 4 < pieces && 2 * lanes * cols <= 32) lanes *= 2;
+    while (lanes < 16 && lanes < pieces && 2 * lanes * cols <= 32) lanes *= 2;
     if (segs > 0x7fffffff) return KV_INT4_ERR_SIZE;
     timing_begin(kTimedReduce, stream);
-    merge_fp8_kernel<D><<<(unsigned)segs, cols * lanes * 32, merge_smem<D>(cols, lanes), stream>>>(
-        Fp8MergeParams{c, pv, dec_grid, cols, lanes});
+    e = launch_pdl(merge_fp8_kernel<D>, dim3((unsigned)segs), cols * lanes * 32, merge_smem<D>(cols, lanes), stream, 1,
+                   Fp8MergeParams{c, pv, dec_grid, cols, lanes});
     timing_end(kTimedReduce, stream);
-    if (cudaGetLastError() != cudaSuccess) return KV_INT4_ERR_CUDA;
+    if (e) return e;
   }
   return KV_INT4_OK;
 }

@@ -49,6 +49,8 @@ template <int D>
 __global__ void __launch_bounds__(kFp8Warps * 32) write_fp8_kernel(CacheFp8 a) {
   constexpr int CH = D / 8;   // 16-byte chunks per input row
   constexpr int PER = D / 16; // chunks per lane (16 rows)
+  pdl_trigger();
+  pdl_wait();
   if (blockIdx.x == 0 && blockIdx.y == 0) fp8_check_seqs(a.s);
   const int lane = threadIdx.x & 31;
   const int task = blockIdx.y * kFp8Warps + (threadIdx.x >> 5);
@@ -150,6 +152,8 @@ template <int D>
 __global__ void __launch_bounds__(kFp8Warps * 32) read_fp8_kernel(CacheFp8 a) {
   constexpr int CH = D / 8;    // 8-code chunks per row
   constexpr int PER = D / 16;  // chunks per lane (16 rows)
+  pdl_trigger();
+  pdl_wait();
   if (blockIdx.x == 0 && blockIdx.y == 0) fp8_check_seqs(a.s);
   const int lane = threadIdx.x & 31;
   const int task = blockIdx.y * kFp8Warps + (threadIdx.x >> 5);
@@ -197,14 +201,10 @@ int launch_t(const CacheFp8& a, bool write, cudaStream_t stream) {
   const int tasks = 2 * a.hkv;
   const dim3 grid((unsigned)units, (unsigned)((tasks + kFp8Warps - 1) / kFp8Warps));
   if (units > 0x7fffffff || grid.y > 65535) return KV_INT4_ERR_SIZE;
-  if (write) {
-    timing_begin(kTimedWrite, stream);
-    write_fp8_kernel<D><<<grid, kFp8Warps * 32, 0, stream>>>(a);
-    timing_end(kTimedWrite, stream);
-  } else {
-    read_fp8_kernel<D><<<grid, kFp8Warps * 32, 0, stream>>>(a);
-  }
-  return cudaGetLastError() == cudaSuccess ? KV_INT4_OK : KV_INT4_ERR_CUDA;
+  if (write) timing_begin(kTimedWrite, stream);
+  const int e = launch_pdl(write ? write_fp8_kernel<D> : read_fp8_kernel<D>, grid, kFp8Warps * 32, 0, stream, 1, a);
+  if (write) timing_end(kTimedWrite, stream);
+  return e;
 }
 
 int launch(const CacheFp8& a, int head_size, bool write, cudaStream_t stream) {

@@ -31,7 +31,11 @@ struct Fp8Dec {
   static constexpr int VTILE = 16 * VROW;
   // neighbouring heads' rows in different bank halves
   static constexpr int HTILE = (KTILE + VTILE + 63) / 128 * 128 + 64;
-  static constexpr int NS = NP == 1 ? 4 : NP == 2 ? 5 : 8;  // block slots
+  // block slots: the copies in flight per SM set the pace.  Two CTAs of four
+  // heads fit an SM with six slots at 128 (two of two heads at 256), with eight
+  // at 96 and 192 (32 x 32768 keys, 32/8 heads of 128: five slots 350 us, six
+  // 325, seven, one CTA, 447)
+  static constexpr int NS = NP == 1 ? 4 : NP == 4 || !SWZ ? 8 : 6;
   static constexpr int WAIT = NS - 2 * NP;                  // copy groups that may stay pending
   static constexpr int KSTEPS = D / 16;
   // head tiles, then the scales [K/V][hg]
@@ -63,6 +67,7 @@ struct Fp8DecParams {
   Common c;
   PlanView pv;
   int num_ctas;
+  int cluster;  // DIRECT: CTAs per (sequence, head group)
 };
 
 template <int NP>
@@ -96,7 +101,29 @@ __device__ __forceinline__ int fp8_kdim(int cq, int s) {
   else return cq * (D / 4) + 4 * s;
 }
 
-template <int D, int NP>
+// this CTA's rank in its cluster, and the cluster's barrier
+__device__ __forceinline__ int cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return (int)r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+// a float of CTA `rank`'s shared memory, at this CTA's address p
+__device__ __forceinline__ float ld_cluster(const float* p, int rank) {
+  uint32_t a;
+  float v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// DIRECT: no schedule, no pieces in the workspace and no merge launch.  A
+// cluster of CTAs serves one (sequence, head group), its CTAs equal shares of
+// the positions, and merges them through distributed shared memory: one launch
+// for batches whose shares are short (latency counts there, not balance).
+template <int D, int NP, bool DIRECT>
 __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
   using G = Fp8Dec<D, NP>;
   const Common& c = prm.c;
@@ -107,40 +134,67 @@ __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
   const int hl = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, cq = lane & 3;
   const int SB = G::slot_bytes(HG);
+  pdl_trigger();
+  pdl_wait();
   int* sflag = reinterpret_cast<int*>(smem + G::NS * SB);
 
-  const int n_dseq = pv.plan[0];
-  if (n_dseq == 0) return;
-  const int gpl = c.ng / c.nl;  // head groups per lane
-  const int my_lane = blockIdx.x % c.nl, rr = blockIdx.x / c.nl;
-  const long long Tu = pv.dprefix[n_dseq] * gpl;
-  const int R = prm.num_ctas / c.nl;
-  const long long P0 = Tu * rr / R, P1 = Tu * (rr + 1) / R;
-  if (P0 >= P1) return;
-  const int nunits = (int)(P1 - P0);
-
-  // largest i with dprefix[i] * gpl <= P0 (32-ary search, per warp)
-  int lo = 0, hi = n_dseq;
-  while (hi - lo > 1) {
-    const long long span = hi - lo;
-    const int probe = lo + (int)((span * lane) / 32);
-    const bool le = lane == 0 || pv.dprefix[probe] * gpl <= P0;
-    const unsigned m = __ballot_sync(0xffffffffu, le);
-    const int last = 31 - __clz(m);
-    const int nlo = lo + (int)((span * last) / 32);
-    const int nhi = last == 31 ? hi : lo + (int)((span * (last + 1)) / 32);
-    lo = nlo;
-    hi = nhi > nlo ? nhi : nlo + 1;
-  }
   Fp8Walk cw;
-  cw.i = lo;
-  cw.lane = my_lane;
-  fp8_walk_load<NP>(cw, c, pv);
-  {
-    const long long off = P0 - pv.dprefix[cw.i] * gpl;
-    const int gs = (int)(off / cw.npos);
-    cw.grp = gs * c.nl + my_lane;
-    cw.kp = (int)(off - (long long)gs * cw.npos);
+  int4 dseq0 = make_int4(0, 0, 0, 0);  // DIRECT: the sequence's record (sequence, seq_len, first query token, q_len)
+  int nunits;
+  const int rank = DIRECT ? cluster_rank() : 0;
+  if constexpr (DIRECT) {
+    const int task = blockIdx.x / prm.cluster;  // (sequence, head group)
+    cw.seq = task / c.ng;
+    cw.grp = task - cw.seq * c.ng;
+    const int q0 = c.qsl[cw.seq], ql = c.qsl[cw.seq + 1] - q0;
+    cw.len = c.seq_lens[cw.seq];
+    // the same for the whole cluster
+    if (!schedule_seq_ok<true>(c, q0, ql, cw.len)) {
+      if (tid == 0 && rank == 0 && cw.grp == 0) flag(c.status, KV_INT4_DEV_BAD_SEQ);
+      return;
+    }
+    if (ql == 0) return;
+    dseq0 = make_int4(cw.seq, cw.len, q0, ql);
+    cw.i = cw.lane = 0;
+    cw.fb = first_block(c, cw.len, ql);
+    const int npos = ((cw.len + 15) / 16 - cw.fb + NP - 1) / NP;
+    const int first = (int)((long long)npos * rank / prm.cluster), end = (int)((long long)npos * (rank + 1) / prm.cluster);
+    nunits = end - first;
+    cw.kp = first;
+    cw.npos = end;  // the CTA's last position ends its segment
+  } else {
+    const int n_dseq = pv.plan[0];
+    if (n_dseq == 0) return;
+    const int gpl = c.ng / c.nl;  // head groups per lane
+    const int my_lane = blockIdx.x % c.nl, rr = blockIdx.x / c.nl;
+    const long long Tu = pv.dprefix[n_dseq] * gpl;
+    const int R = prm.num_ctas / c.nl;
+    const long long P0 = Tu * rr / R, P1 = Tu * (rr + 1) / R;
+    if (P0 >= P1) return;
+    nunits = (int)(P1 - P0);
+
+    // largest i with dprefix[i] * gpl <= P0 (32-ary search, per warp)
+    int lo = 0, hi = n_dseq;
+    while (hi - lo > 1) {
+      const long long span = hi - lo;
+      const int probe = lo + (int)((span * lane) / 32);
+      const bool le = lane == 0 || pv.dprefix[probe] * gpl <= P0;
+      const unsigned m = __ballot_sync(0xffffffffu, le);
+      const int last = 31 - __clz(m);
+      const int nlo = lo + (int)((span * last) / 32);
+      const int nhi = last == 31 ? hi : lo + (int)((span * (last + 1)) / 32);
+      lo = nlo;
+      hi = nhi > nlo ? nhi : nlo + 1;
+    }
+    cw.i = lo;
+    cw.lane = my_lane;
+    fp8_walk_load<NP>(cw, c, pv);
+    {
+      const long long off = P0 - pv.dprefix[cw.i] * gpl;
+      const int gs = (int)(off / cw.npos);
+      cw.grp = gs * c.nl + my_lane;
+      cw.kp = (int)(off - (long long)gs * cw.npos);
+    }
   }
   Fp8Walk pw = cw;
 
@@ -193,17 +247,21 @@ __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
       if (!ok && kb * 16 < len) flag(c.status, KV_INT4_DEV_BAD_BLOCK);
     }
   };
+  auto next = [&](Fp8Walk& w) {
+    if constexpr (DIRECT) ++w.kp;
+    else fp8_walk_next<NP>(w, c, pv);
+  };
   // producer: one block per call into the next ring slot, the next block id
   // loaded one call ahead; one commit group per call (empty past the range)
   int ppos = 0, pj = 0, ps = 0;
-  int pblk = block_at(pw, 0);
+  int pblk = nunits > 0 ? block_at(pw, 0) : -1;
   auto produce = [&]() {
     if (ppos < nunits) {
       issue(pblk, pw.fb + pw.kp * NP + pj, pw.len, pw.grp, ps);
       ps = ps + 1 == G::NS ? 0 : ps + 1;
       if (++pj == NP) {
         pj = 0;
-        if (++ppos < nunits) fp8_walk_next<NP>(pw, c, pv);
+        if (++ppos < nunits) next(pw);
       }
       if (ppos < nunits) pblk = block_at(pw, pj);
     }
@@ -223,7 +281,7 @@ __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
 
   auto begin_segment = [&]() {
     const int head = cw.grp * HG + hl;
-    const int4 di = pv.dseq[cw.i];
+    const int4 di = DIRECT ? dseq0 : pv.dseq[cw.i];
     const int q0 = di.z, ql = di.w, L = di.y;
     const int ctx = L - ql;
     // B fragments of this lane's column g, which holds query column g % COLS
@@ -301,7 +359,10 @@ __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
     }
     float* dst_o;
     float* dst_ml;
-    if (first_piece) {
+    if constexpr (DIRECT) {  // over the ring: every copy has landed, every warp is done
+      dst_o = reinterpret_cast<float*>(smem) + hl * kDecodeCols * (D + 2);
+      dst_ml = dst_o + kDecodeCols * D;
+    } else if (first_piece) {
       const long long slot = (long long)cw.i * c.hkv + cw.grp * HG + hl;
       dst_o = pv.direct_o + slot * kDecodeCols * D;
       dst_ml = pv.direct_ml + slot * kDecodeCols * 2;
@@ -467,11 +528,11 @@ __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
       }
     }
 
-    const bool last_in_seg = cw.kp == cw.npos - 1;
+    const bool last_in_seg = !DIRECT && cw.kp == cw.npos - 1;
     const bool last_in_range = it + 1 == nunits;
-    if (last_in_seg || last_in_range) flush();
+    if (!DIRECT && (last_in_seg || last_in_range)) flush();
     if (!last_in_range) {
-      fp8_walk_next<NP>(cw, c, pv);
+      next(cw);
       if (last_in_seg) {
         first_piece = true;
         begin_segment();
@@ -481,6 +542,54 @@ __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
     if (cs >= G::NS) cs -= G::NS;
   }
   cp_async_wait<0>();
+  if constexpr (DIRECT) {
+    __syncthreads();
+    flush();
+    cluster_sync();
+    // (head, query column) rows in turn over the cluster's CTAs and their
+    // warps; the shares (and with paired blocks a row's two columns) by the
+    // log-sum-exp rule, all of a row's values loaded before any is used
+    constexpr int PER = D / 32, SUB = NP == 2 ? 2 : 1;
+    const int cols = dseq0.w * c.group;
+#pragma unroll 1
+    for (int p = rank * HG + hl; p < HG * cols; p += prm.cluster * HG) {
+      const int h = p / cols, col = p - h * cols;
+      const float* base = reinterpret_cast<const float*>(smem) + h * kDecodeCols * (D + 2);
+      float M = -INFINITY, Ls = 0.f, acc[PER];
+#pragma unroll
+      for (int k = 0; k < PER; k++) acc[k] = 0.f;
+#pragma unroll 2
+      for (int r = 0; r < prm.cluster; r++) {
+        float mw[SUB], lw[SUB], o[SUB][PER];
+#pragma unroll
+        for (int sub = 0; sub < SUB; sub++) {
+          const int cc = col + sub * G::COLS;
+          mw[sub] = ld_cluster(base + kDecodeCols * D + 2 * cc, r);
+          lw[sub] = ld_cluster(base + kDecodeCols * D + 2 * cc + 1, r);
+#pragma unroll
+          for (int k = 0; k < PER; k++) o[sub][k] = ld_cluster(base + cc * D + lane + 32 * k, r);
+        }
+#pragma unroll
+        for (int sub = 0; sub < SUB; sub++) {
+          const float mn = fmaxf(M, mw[sub]);
+          const float mu = mn == -INFINITY ? 0.f : mn;
+          const float a = fast_exp2(M - mu), b = fast_exp2(mw[sub] - mu);
+#pragma unroll
+          for (int k = 0; k < PER; k++) acc[k] = acc[k] * a + o[sub][k] * b;
+          Ls = Ls * a + lw[sub] * b;
+          M = mn;
+        }
+      }
+      const float inv = Ls == 0.f ? 0.f : 1.f / Ls;  // no visible key: zeros
+      const int j = col / c.group, jj = col - j * c.group;
+      uint16_t* dst = c.out + (long long)(dseq0.z + j) * c.out_stride +
+                      (long long)((cw.grp * HG + h) * c.group + jj) * D;
+#pragma unroll
+      for (int k = 0; k < PER; k++)
+        dst[lane + 32 * k] = (uint16_t)(pack_bf16x2_rn(acc[k] * inv, 0.f) & 0xffffu);
+    }
+    cluster_sync();  // no CTA leaves while its shares are read
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -504,6 +613,8 @@ __global__ void __launch_bounds__(1024) merge_fp8_kernel(Fp8MergeParams prm) {
   const Common& c = prm.c;
   const PlanView& pv = prm.pv;
   extern __shared__ __align__(16) float spart[];  // [cols][lanes][D + 2]
+  pdl_trigger();
+  pdl_wait();
   constexpr int PER = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int col = warp % prm.cols, pl = warp / prm.cols;
@@ -547,42 +658,37 @@ __global__ void __launch_bounds__(1024) merge_fp8_kernel(Fp8MergeParams prm) {
     M = mn;
   };
   if (used) {
-    constexpr int CH = 4;  // candidates loaded together
-#pragma unroll 1
-    for (long long k0 = pl; k0 < cand; k0 += (long long)CH * prm.lanes) {
-      float mw[CH][2], lw[CH][2], ov[CH][2][PER];
-#pragma unroll
-      for (int j = 0; j < CH; j++) {
-        const long long k = k0 + (long long)j * prm.lanes;
-        bool ok = k < cand;
-        long long w = 0;
-        if (ok && k > 0) {
-          if (by_cta) {
-            w = w_first + k - 1;
-            ok = wstart(w + 1) > wstart(w);
-          } else {
-            const long long p = sbeg + k;
-            w = div_nn((p + 1) * W + Tu - 1, Tu) - 1;  // last CTA starting at or before p
-            ok = wstart(w) == p;
-          }
-        }
-        const long long sl = (w * c.nl + lane_g) * c.hg + hl;
-        const float* o = ok && k > 0 ? pv.warp_o + sl * kDecodeCols * D : pv.direct_o + (long long)seg * kDecodeCols * D;
-        const float* ml = ok && k > 0 ? pv.warp_ml + sl * kDecodeCols * 2 : pv.direct_ml + (long long)seg * kDecodeCols * 2;
-#pragma unroll
-        for (int sub = 0; sub < 2; sub++) {
-          const bool use = ok && sub < nsub;
-          const int cc = col + sub * c.dcols;
-          mw[j][sub] = use ? ml[cc * 2] : -INFINITY;
-          lw[j][sub] = use ? ml[cc * 2 + 1] : 0.f;
-#pragma unroll
-          for (int e = 0; e < PER; e++) ov[j][sub][e] = use ? o[cc * D + lane + 32 * e] : 0.f;
+    // a candidate's two column sets are loaded together; the lanes of a column
+    // keep their candidates' loads in flight side by side
+#pragma unroll 2
+    for (long long k = pl; k < cand; k += prm.lanes) {
+      bool ok = true;
+      long long w = 0;
+      if (k > 0) {
+        if (by_cta) {
+          w = w_first + k - 1;
+          ok = wstart(w + 1) > wstart(w);
+        } else {
+          const long long p = sbeg + k;
+          w = div_nn((p + 1) * W + Tu - 1, Tu) - 1;  // last CTA starting at or before p
+          ok = wstart(w) == p;
         }
       }
+      const long long sl = (w * c.nl + lane_g) * c.hg + hl;
+      const float* o = k > 0 ? pv.warp_o + sl * kDecodeCols * D : pv.direct_o + (long long)seg * kDecodeCols * D;
+      const float* ml = k > 0 ? pv.warp_ml + sl * kDecodeCols * 2 : pv.direct_ml + (long long)seg * kDecodeCols * 2;
+      float mw[2], lw[2], ov[2][PER];
 #pragma unroll
-      for (int j = 0; j < CH; j++)
+      for (int sub = 0; sub < 2; sub++) {
+        const bool use = ok && sub < nsub;
+        const int cc = col + sub * c.dcols;
+        mw[sub] = use ? ml[cc * 2] : -INFINITY;
+        lw[sub] = use ? ml[cc * 2 + 1] : 0.f;
 #pragma unroll
-        for (int sub = 0; sub < 2; sub++) merge(mw[j][sub], lw[j][sub], ov[j][sub]);
+        for (int e = 0; e < PER; e++) ov[sub][e] = use ? o[cc * D + lane + 32 * e] : 0.f;
+      }
+#pragma unroll
+      for (int sub = 0; sub < 2; sub++) merge(mw[sub], lw[sub], ov[sub]);
     }
   }
   if (prm.lanes > 1) {

@@ -8,6 +8,39 @@
 
 namespace kvint4 {
 
+// ---------------------------------------------------------------------------
+// Programmatic dependent launch: a kernel may be scheduled while the one before
+// it on the stream still runs, and waits there (pdl_wait, before it touches
+// any memory that another kernel writes or reads) until that one is complete
+// and its writes are visible.  A kernel lets the next one start (pdl_trigger)
+// once all its CTAs run.  Between short kernels this hides the launch latency.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+
+// launches on `stream` with that permission, as clusters of `cluster` CTAs;
+// KV_INT4_OK or KV_INT4_ERR_CUDA
+template <typename... P, typename... A>
+inline int launch_pdl(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, int cluster,
+                      A&&... args) {
+  cudaLaunchAttribute at[2] = {};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kern, static_cast<A&&>(args)...) == cudaSuccess) return KV_INT4_OK;
+  cudaGetLastError();
+  return KV_INT4_ERR_CUDA;
+}
+
 // Scales are 2^k with k in [kFp8MinExp, kFp8MaxExp].  E4M3 keeps four
 // significant bits at every magnitude, so a power of two loses nothing against
 // absmax / 448, and it moves codes between scales by their exponent alone

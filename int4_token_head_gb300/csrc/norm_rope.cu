@@ -16,6 +16,7 @@
 
 #include "../../include/kvint4.h"
 #include "common.cuh"
+#include "fp8.cuh"
 #include "internal.h"
 
 namespace kvint4 {
@@ -61,6 +62,8 @@ __global__ void __launch_bounds__(kNormWarps * 32) norm_rope_kernel(NormRope p) 
   constexpr int LPV = D / 16;    // lanes per vector
   constexpr int VPW = 32 / LPV;  // vectors per warp step
   const NormRopeArgs& a = p.a;
+  pdl_trigger();
+  pdl_wait();
   const int lane = threadIdx.x & 31;
   const int gw = blockIdx.x * kNormWarps + (threadIdx.x >> 5);
   const int t = (int)p.by_parts.div((uint32_t)gw);
@@ -168,8 +171,8 @@ int launch_t(const NormRopeArgs& a, cudaStream_t stream) {
   p.by_parts = FastDiv((uint32_t)p.parts);
   const int64_t warps = (int64_t)a.num_tokens * p.parts;
   if (warps >= (1ll << 31) - kNormWarps) return KV_INT4_ERR_SIZE;
-  norm_rope_kernel<D, U><<<(unsigned)((warps + kNormWarps - 1) / kNormWarps), kNormWarps * 32, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? KV_INT4_OK : KV_INT4_ERR_CUDA;
+  return launch_pdl(norm_rope_kernel<D, U>, dim3((unsigned)((warps + kNormWarps - 1) / kNormWarps)), kNormWarps * 32, 0,
+                    stream, 1, p);
 }
 
 }  // namespace

@@ -276,6 +276,10 @@ __global__ void __launch_bounds__(20 * 32, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
+  // shared memory and TMEM are this CTA's own; the schedule and the caches come
+  // from the kernels before
+  pdl_trigger();
+  pdl_wait();
   if (warp == 0) tmem_alloc(smem_addr(tslot), 512);
   tc_fence_before();
   __syncthreads();

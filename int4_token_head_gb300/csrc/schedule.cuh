@@ -145,9 +145,18 @@ __device__ T block_exclusive_scan(T v, T* total, T* sbuf /*[kPrepThreads/32]*/) 
   return before + x - v;
 }
 
-// The schedule, by one CTA of kPrepThreads threads.  A sequence's queries are
-// its last q_len positions, so its length is at least q_len; with ANY_LEN a
-// non-causal call may attend keys of another length (none included).
+// Whether a sequence's metadata is consistent.  Its queries are its last q_len
+// positions, so its length is at least q_len; with ANY_LEN a non-causal call
+// may attend keys of another length (none included).  A q_len above
+// max_query_len would fall outside the launches sized from it (decode columns,
+// the prefill launch, the reduce segments).
+template <bool ANY_LEN>
+__device__ __forceinline__ bool schedule_seq_ok(const Common& c, int q0, int ql, int L) {
+  return !(q0 < 0 || (long long)q0 + ql > c.num_q_tokens || ql < 0 || L < (ANY_LEN && !c.causal ? 0 : ql) ||
+           ql > c.max_qlen || (long long)L > (long long)c.max_blocks * 16);
+}
+
+// The schedule, by one CTA of kPrepThreads threads.
 template <bool ANY_LEN>
 __device__ void build_schedule(const Common& c, const PlanView& pv) {
   __shared__ int32_t s_i32[kPrepThreads / 32];
@@ -159,14 +168,9 @@ __device__ void build_schedule(const Common& c, const PlanView& pv) {
     int kind = 0, nblk = 0, ntiles = 0, ql = 0, L = 0, q0 = 0;
     if (s < c.num_seqs) {
       q0 = c.qsl[s];
-      const int q1 = c.qsl[s + 1];
       L = c.seq_lens[s];
-      ql = q1 - q0;
-      // a q_len above max_query_len would fall outside the launches sized
-      // from it (decode columns, the prefill launch, the reduce segments)
-      const bool bad = q0 < 0 || q1 > c.num_q_tokens || ql < 0 || L < (ANY_LEN && !c.causal ? 0 : ql) ||
-                       ql > c.max_qlen || (long long)L > (long long)c.max_blocks * 16;
-      if (bad) {
+      ql = c.qsl[s + 1] - q0;
+      if (!schedule_seq_ok<ANY_LEN>(c, q0, ql, L)) {
         flag(c.status, KV_INT4_DEV_BAD_SEQ);
       } else if (ql > 0) {
         kind = is_decode_kind(ql, c) ? 1 : 2;
