@@ -17,7 +17,11 @@
 // d / 16 chunks of 8 elements a lane, all loaded before any is used (2 or 4
 // KB in flight per warp at d = 128), so a block's absmax, its rows and its
 // scale never leave the warp: no second pass, no atomics, and results that
-// depend on neither the launch shape nor the order of warps.
+// depend on neither the launch shape nor the order of warps.  Four-warp CTAs at
+// most 72 registers a thread (28 warps per SM) and streaming loads of K and V:
+// 65,536 tokens, 8 heads of 128, 403 MB: 65.8 us = 0.90 of the measured copy
+// bandwidth (eight-warp CTAs 68.5; streaming stores of the codes 65.0, not kept:
+// attention reads them next).  Read: 396 MB in 60 us = 0.97.
 
 #include <cuda_runtime.h>
 
@@ -29,7 +33,7 @@
 namespace kvint4 {
 namespace {
 
-constexpr int kFp8Warps = 8;
+constexpr int kFp8Warps = 4;
 
 struct CacheFp8 {
   Fp8Seqs s;
@@ -46,7 +50,7 @@ struct CacheFp8 {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kFp8Warps * 32) write_fp8_kernel(CacheFp8 a) {
+__global__ void __launch_bounds__(kFp8Warps * 32, D <= 96 ? 8 : 7) write_fp8_kernel(CacheFp8 a) {
   constexpr int CH = D / 8;   // 16-byte chunks per input row
   constexpr int PER = D / 16; // chunks per lane (16 rows)
   pdl_trigger();
@@ -72,7 +76,7 @@ __global__ void __launch_bounds__(kFp8Warps * 32) write_fp8_kernel(CacheFp8 a) {
   for (int j = 0; j < PER; j++) {
     const int c = lane + 32 * j, r = c / CH, col = c - r * CH;
     x[j] = make_uint4(0, 0, 0, 0);
-    if (r >= u.r0 && r < u.r1) x[j] = *reinterpret_cast<const uint4*>(src + r * stride + col * 8);
+    if (r >= u.r0 && r < u.r1) x[j] = __ldcs(reinterpret_cast<const uint4*>(src + r * stride + col * 8));
   }
   auto absmax = [&]() {
     uint32_t m = 0;  // both halves; the sign bits carry nothing
