@@ -4,27 +4,29 @@
 // One CTA per SM (all 512 TMEM columns); an item is 256 query rows (query
 // token x q head of one kv group) in two halves of 128, the MMA's M.  A step
 // is NK keys: 128 for head sizes up to 128 (a 128 x 128 score tile per half,
-// full tensor rate), 64 at 192 (the accumulators leave no more TMEM).  Eighteen
+// full tensor rate), 64 at 192 (the accumulators leave no more TMEM).  Twenty-six
 // warps in five roles that meet only at mbarriers:
-//   * producer warp (16): claims items (longest first) and hands them on
+//   * producer warp (24): claims items (longest first) and hands them on
 //     through a two-entry ring; TMA copies of the item's Q rows (bf16, straight
 //     into the MMA's swizzled tile) and of the step's K and V code blocks (one
 //     box per block; a block that the table does not name is a box outside the
 //     tensor, which arrives as zeros); the blocks' scales into a three-entry ring;
-//   * convert warps (8-11 K, 12-15 V): K codes into one of two bf16 tiles, V
+//   * convert warps (16-19 K, 20-23 V): K codes into one of two bf16 tiles, V
 //     codes into one of two f16 tiles, exactly.  K meets the unconverted bf16
 //     queries, so an item starts without any work on Q; V meets the f16 weights;
-//   * MMA warp (17, lane 0 issues): S_h = Q_h K^T, then O_h += W_h V with the
+//   * MMA warp (25, one elected lane issues): S_h = Q_h K^T, then O_h += W_h V with the
 //     weights W_h (f16 pairs over S_h's columns) read from TMEM.  Issue order
 //     S0 S1 | WV0 S0' | WV1 S1' | ...: a half's softmax runs during the other's MMAs;
-//   * softmax warps (0-3 half 0, 4-7 half 1): one query row per thread.  With
+//   * softmax warps (0-7 half 0, 8-15 half 1): two threads per query row, one
+//     for each half of the step's keys (the half's chain S -> softmax -> WV is
+//     what bounds a step; 4700 cycles with one thread per row).  With
 //     f_b = |softmax_scale| log2 e ks_b (a negative scale's sign is in K) and
-//     kv_b per block, the row's maximum needs only the blocks' largest raw
-//     scores, and a weight is exp2(fma(s, f_b, kv_b - m_ref)).  m_ref moves to
+//     kv_b per block, a weight is exp2(fma(s, f_b, kv_b - m_ref)).  m_ref moves to
 //     the row's maximum (and its O in TMEM is rescaled) only when a step's
 //     weights add up to more than 2^14: they stay inside f16 whatever the V
 //     scales, and most steps need no maximum (one fma, one exp2, one add and
-//     half a conversion per score).
+//     half a conversion per score).  The two warps of a row agree on that by a
+//     barrier that votes; the weights stay in registers until then, S is whole.
 // Shared operands are K-major (Q, K) or MN-major (V) tiles [D / 64][rows][128
 // bytes] with the 16-byte chunk index XORed by row % 8.
 //
@@ -67,8 +69,9 @@ struct Fp8Ws {
   static constexpr int NRING = 3;
   static constexpr int NBARS = 23;
   static constexpr int S_COLS = NK, O_COL = 2 * NK;  // TMEM: S_h at h NK, O_h at 2 NK + h D
-  static constexpr int SMEM = 1024 + QBYTES + 4 * KVBYTES + 2 * STG + NRING * RING + NBARS * 8 + 48;
-  static constexpr int THREADS = 20 * 32;  // five warpgroups; the last two warps only give up registers
+  static constexpr int XCH = 2 * ROWS * 4;  // a float per row and key half: maxima, sums
+  static constexpr int SMEM = QBYTES + 4 * KVBYTES + 2 * STG + NRING * RING + NBARS * 8 + 48 + XCH;
+  static constexpr int THREADS = 28 * 32;  // seven warpgroups; the last two warps only give up registers
   static constexpr int CV_WARPS = 4;       // convert warps for K, and for V
   // byte offset of chunk g of key k in a stage
   __device__ static constexpr int stage_off(int k, int g) {
@@ -140,36 +143,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr)
       : "memory");
 }
-// a warp's 32 lanes x 64 consecutive columns, one wait for both halves
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
-  uint32_t r[64];
-#pragma unroll
-  for (int h = 0; h < 64; h += 32)
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-        : "=r"(r[h + 0]), "=r"(r[h + 1]), "=r"(r[h + 2]), "=r"(r[h + 3]), "=r"(r[h + 4]), "=r"(r[h + 5]),
-          "=r"(r[h + 6]), "=r"(r[h + 7]), "=r"(r[h + 8]), "=r"(r[h + 9]), "=r"(r[h + 10]), "=r"(r[h + 11]),
-          "=r"(r[h + 12]), "=r"(r[h + 13]), "=r"(r[h + 14]), "=r"(r[h + 15]), "=r"(r[h + 16]), "=r"(r[h + 17]),
-          "=r"(r[h + 18]), "=r"(r[h + 19]), "=r"(r[h + 20]), "=r"(r[h + 21]), "=r"(r[h + 22]), "=r"(r[h + 23]),
-          "=r"(r[h + 24]), "=r"(r[h + 25]), "=r"(r[h + 26]), "=r"(r[h + 27]), "=r"(r[h + 28]), "=r"(r[h + 29]),
-          "=r"(r[h + 30]), "=r"(r[h + 31])
-        : "r"(taddr + h));
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 64; i++) v[i] = __uint_as_float(r[i]);
-}
 // not waited for
-__device__ __forceinline__ void tmem_st32w(uint32_t taddr, const uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&w)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(
@@ -232,16 +206,15 @@ struct Fp8Maps {
 };
 
 template <int D>
-__global__ void __launch_bounds__(20 * 32, 1)
+__global__ void __launch_bounds__(28 * 32, 1)
     prefill_ws_fp8_kernel(Common c, PlanView pv, const __grid_constant__ Fp8Maps maps) {
   using G = Fp8Ws<D>;
   constexpr int KSTEPS = D / 16;
   constexpr int NK = G::NK, NB = G::NB, ROWS = G::ROWS;
   constexpr uint32_t IDESC_S = umma_idesc_f16(128, NK, false) | (1u << 7) | (1u << 10);  // bf16 operands
   constexpr uint32_t IDESC_O = umma_idesc_f16(128, D, true);
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* const sQ = sm;                     // [KB][256 rows][128 B], swizzled
+  extern __shared__ __align__(1024) uint8_t smem_ws[];  // the swizzled tiles want 1024-byte bases
+  uint8_t* const sQ = smem_ws;                // [KB][256 rows][128 B], swizzled
   uint8_t* const sK = sQ + G::QBYTES;         // two K tiles [KB][NK][128 B]
   uint8_t* const sV = sK + 2 * G::KVBYTES;    // two V tiles
   uint8_t* const stg = sV + 2 * G::KVBYTES;   // staged K codes, V codes
@@ -250,6 +223,7 @@ __global__ void __launch_bounds__(20 * 32, 1)
   int* const sitem = reinterpret_cast<int*>(bars + G::NBARS);  // item ring [2][4], abort flag
   uint32_t* const tslot = reinterpret_cast<uint32_t*>(sitem + 10);
   volatile int* const abort_flag = sitem + 8;
+  float* const sxch = reinterpret_cast<float*>(sitem + 12);  // [key half][256 rows]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   enum {
@@ -257,6 +231,10 @@ __global__ void __launch_bounds__(20 * 32, 1)
     QFULL = 18, RKFULL = 19, RVFULL = 20, RKFREE = 21, RVFREE = 22
   };
   auto bar = [&](int i) { return smem_addr(&bars[i]); };
+  if (smem_addr(smem_ws) & 1023) {  // dynamic shared memory starts the window: does not occur
+    flag(c.status, KV_INT4_DEV_TIMEOUT);
+    return;
+  }
   if (tid == 0) {
     for (int b = 0; b < 2; b++) {
       mbar_init(bar(KFULL + b), G::CV_WARPS + 1);  // and the producer's ring entry
@@ -264,9 +242,9 @@ __global__ void __launch_bounds__(20 * 32, 1)
       mbar_init(bar(KFREE + b), 1);
       mbar_init(bar(VFREE + b), 1);
       mbar_init(bar(SFULL + b), 1);
-      mbar_init(bar(PFULL + b), 4);
+      mbar_init(bar(PFULL + b), 8);
       mbar_init(bar(IFULL + b), 1);
-      mbar_init(bar(IFREE + b), 8 + 2 * G::CV_WARPS + 1);
+      mbar_init(bar(IFREE + b), 16 + 2 * G::CV_WARPS + 1);
       mbar_init(bar(RKFULL + b), 1);  // RKFULL, RVFULL
       mbar_init(bar(RKFREE + b), G::CV_WARPS);
     }
@@ -297,238 +275,212 @@ __global__ void __launch_bounds__(20 * 32, 1)
     if (lane == 0) fp8_arrive(bar(IFREE + e));
     return item.x >= 0;
   };
-  // registers: 96 a thread at launch (640 threads, 61,440); the softmax
-  // warpgroups take 144, the others 64 (256 x 144 + 384 x 64 = 61,440)
-  if (warp < 8) {
+  // registers: 72 a thread at launch (896 threads, 64,512); the softmax
+  // warpgroups take 80, the others 56 (512 x 80 + 384 x 56 = 62,464)
+  if (warp < 16) {
     // ======================= softmax warpgroups =======================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 144;\n");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 80;\n");
     uint32_t ph_sfull = 0, ph_odone = 0, ph_ifull = 0;
     const float cf = fabsf(c.qscale);  // its sign is in K
+    const int hf = warp >> 3, kh = (warp >> 2) & 1;  // query half, key half
+    const int r = hf * 128 + (warp & 3) * 32 + lane;  // row of the item
+    const int j = (int)c.gdiv.div((uint32_t)r);
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    constexpr int NC = NK / 2, NBH = NB / 2;  // keys and blocks of a key half
+    const uint32_t tS = tmem + NK * hf + NC * kh + lane_off, tO = tmem + G::O_COL + hf * D + lane_off;
+    const int pair = 1 + hf * 4 + (warp & 3);  // named barrier of a row's two warps
+    auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;\n" ::"r"(pair) : "memory"); };
+    auto pair_any = [&](bool v) -> bool {
+      uint32_t any;
+      asm volatile(
+          "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+          : "=r"(any)
+          : "r"((uint32_t)v), "r"(pair)
+          : "memory");
+      return any != 0;
+    };
     int n = 0;  // steps of earlier items
 #pragma unroll 1
     for (int itc = 0;; itc++) {
+      // both warps of a row go on or neither (after a time-out one may get an
+      // item that the other does not)
       int4 item;
-      const int e = itc & 1;
-      if (!take_item(e, ph_ifull, item)) break;
+      const bool taken = take_item(itc & 1, ph_ifull, item);
+      if (pair_any(!taken)) break;
       const int seq = item.x, h = item.y, tile = item.z, nkb = item.w;
       const int q0 = c.qsl[seq], ql = c.qsl[seq + 1] - q0;
       const int L = c.seq_lens[seq], ctx = L - ql;
       const int tok0 = tile * c.tile_tokens;
-      const int nrows = min(c.tile_tokens, ql - tok0) * c.group;
+      const bool rok = r < min(c.tile_tokens, ql - tok0) * c.group;
       const int kb0 = window_lo(c, ctx + tok0) >> 4;
       const int nsteps = (nkb - kb0 + NB - 1) / NB;
-      const int hf = warp >> 2;
-      const int r = tid;  // row of the item
-      const int j = (int)c.gdiv.div((uint32_t)r);
-      const bool rok = r < nrows;
       const int qp = ctx + tok0 + (rok ? j : 0);
-      const int lim = c.causal ? min(L, qp + 1) : L;
-      const int lo = window_lo(c, qp);
-      const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-      const uint32_t tS = tmem + NK * hf + lane_off, tO = tmem + G::O_COL + hf * D + lane_off;
+      // the row sees positions [lo, lim), counted from this thread's first key
+      int lim = (c.causal ? min(L, qp + 1) : L) - kb0 * 16 - NC * kh, lo = window_lo(c, qp) - kb0 * 16 - NC * kh;
       float m_ref = -INFINITY, l_run = 0.f;
 #pragma unroll 1
-      for (int st = 0; st < nsteps; st++, n++) {
-        const float* re = reinterpret_cast<const float*>(ring + (n % G::NRING) * G::RING);
+      for (int st = 0; st < nsteps; st++, n++, lim -= NK, lo -= NK) {
+        const float* re = reinterpret_cast<const float*>(ring + (n % G::NRING) * G::RING) + NBH * kh;
         const float* kvf = re + NB;
         const float* ivs = re + 2 * NB;
         const int* ok = reinterpret_cast<const int*>(re + 3 * NB);
         fp8_wait(bar(SFULL + hf), ph_sfull, abort_flag, c.status);
         ph_sfull ^= 1;
         tc_fence_after();
-        const int pos0 = (kb0 + st * NB) * 16;
-        // the warp's rows all see the whole step: no mask (the usual case)
-        const bool full = __all_sync(0xffffffffu, pos0 >= lo && pos0 + NK <= lim && ok[NB] != 0);
-        // 64 columns (four blocks) at a time, as a loop: eighteen warps in five
-        // roles share the instruction caches, and steps written out in full
-        // stalled on instruction fetch more than on anything else
-#pragma unroll 1
-        for (int u = 0; u < NK / 64; u++) {
-          const float4 fk = *reinterpret_cast<const float4*>(re + 4 * u);
-          const float4 kvb = *reinterpret_cast<const float4*>(kvf + 4 * u);
-          // (never 0, so that a hidden key's -inf stays -inf)
-          const float f[4] = {fmaxf(cf * fk.x, FLT_MIN), fmaxf(cf * fk.y, FLT_MIN), fmaxf(cf * fk.z, FLT_MIN),
-                              fmaxf(cf * fk.w, FLT_MIN)};
-          const float kb[4] = {kvb.x, kvb.y, kvb.z, kvb.w};
-          float s[64];
-          tmem_ld64(tS + 64 * u, s);
+        // the warp's rows all see all its keys: no mask (the usual case)
+        const bool full = __all_sync(0xffffffffu, lo <= 0 && lim >= NC && ok[NB - NBH * kh] != 0);
+        // the scores of block b, hidden ones -inf, and their factor (never 0, so
+        // that -inf stays)
+        auto scores = [&](int b, float (&s)[16], float& f) {
+          f = fmaxf(cf * re[b], FLT_MIN);
+          uint32_t x[16];
+          tmem_ld16(tS + 16 * b, x);
+#pragma unroll
+          for (int k = 0; k < 16; k++) s[k] = __uint_as_float(x[k]);
           if (!full) {
-            __syncwarp();  // a branch, not 64 selects in every step
+            __syncwarp();  // a branch, not selects in every step
+            const int first = lo - 16 * b, last = lim - 16 * b;
+            uint32_t vis = first <= 0 ? 0xffffu : first >= 16 ? 0u : 0xffffu << first;
+            vis &= last >= 16 ? 0xffffu : last <= 0 ? 0u : 0xffffu >> (16 - last);
+            if (!ok[b]) vis = 0;
 #pragma unroll
-            for (int b = 0; b < 4; b++) {
-              // keys of block b that the row sees: [lo, lim), if it is usable
-              const int first = lo - pos0 - 64 * u - 16 * b, last = lim - pos0 - 64 * u - 16 * b;
-              uint32_t vis = first <= 0 ? 0xffffu : first >= 16 ? 0u : 0xffffu << first;
-              vis &= last >= 16 ? 0xffffu : last <= 0 ? 0u : 0xffffu >> (16 - last);
-              if (!ok[4 * u + b]) vis = 0;
-#pragma unroll
-              for (int k = 0; k < 16; k++)
-                if (!(vis & (1u << k))) s[16 * b + k] = -INFINITY;
-            }
+            for (int k = 0; k < 16; k++)
+              if (!(vis & (1u << k))) s[k] = -INFINITY;
           }
-          // moves the reference to the row's maximum where it has none or is more
-          // than 8 behind; whole numbers, so that O, l and the step's weights so
-          // far move by exact powers of two
-          auto find = [&]() {
+        };
+        uint32_t w[NC / 2];
+        float add, tot;
+        // find: the reference moves to the row's maximum where it has none or is
+        // more than 8 behind; whole numbers, so that O and l move exactly
+        bool find = st == 0;
+#pragma unroll 1
+        while (true) {
+          if (find) {
             float mx = -INFINITY;
+#pragma unroll 1
+            for (int b = 0; b < NBH; b++) {
+              float s[16], f;
+              scores(b, s, f);
+              float t = s[0];
 #pragma unroll
-            for (int b = 0; b < 4; b++) {
-              float t = s[16 * b];
-#pragma unroll
-              for (int k = 1; k < 16; k++) t = fmaxf(t, s[16 * b + k]);
-              mx = fmaxf(mx, fmaf(t, f[b], kb[b]));
+              for (int k = 1; k < 16; k++) t = fmaxf(t, s[k]);
+              mx = fmaxf(mx, fmaf(t, f, kvf[b]));
             }
-            mx = ceilf(mx);
+            sxch[kh * ROWS + r] = mx;
+            pair_sync();
+            mx = ceilf(fmaxf(mx, sxch[(kh ^ 1) * ROWS + r]));
+            pair_sync();  // read before anything else is written there
             const bool grow = mx > m_ref + (m_ref == -INFINITY ? 0.f : 8.f);
             const float alpha = grow && m_ref != -INFINITY ? fast_exp2(m_ref - mx) : 1.f;
             if (grow) m_ref = mx;
-            if (!__any_sync(0xffffffffu, alpha != 1.f)) return;
             l_run *= alpha;
-            // O is complete up to the previous step (S_h of this step was issued after it)
+            if (__any_sync(0xffffffffu, alpha != 1.f)) {
+              // O is complete up to the previous step (S_h of this step was
+              // issued after it); each key half rescales its share of the columns
 #pragma unroll 1
-            for (int cc = 0; cc < D / 32; cc++) {
-              float o[32];
-              tmem_ld32(tO + cc * 32, o);
+              for (int cc = kh; cc < D / 16; cc += 2) {
+                uint32_t o[16];
+                tmem_ld16(tO + 16 * cc, o);
 #pragma unroll
-              for (int i = 0; i < 32; i++) o[i] *= alpha;
-              tmem_st32(tO + cc * 32, o);
-            }
-            asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
-#pragma unroll 1
-            for (int cc = 0; cc < 2 * u; cc++) {
-              uint32_t x[16];
-              tmem_ld16(tS + 16 * cc, x);
-#pragma unroll
-              for (int i = 0; i < 16; i++) {
-                const float2 y = __half22float2(*reinterpret_cast<__half2*>(&x[i]));
-                x[i] = pack_f16x2(y.x * alpha, y.y * alpha);
+                for (int i = 0; i < 16; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                tmem_st16(tO + 16 * cc, o);
               }
-              tmem_st16(tS + 16 * cc, x);
             }
-          };
-          uint32_t w[32];
-          float tot[4];
-          auto weights = [&]() {
-            const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-#pragma unroll
-            for (int b = 0; b < 4; b++) {
-              const float2 g = make_float2(f[b], f[b]), o = make_float2(kb[b] - mu, kb[b] - mu);
-              float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-              for (int k = 0; k < 16; k += 2) {
-                const float2 a = f2fma(make_float2(s[16 * b + k], s[16 * b + k + 1]), g, o);
-                const float2 p = make_float2(fast_exp2(a.x), fast_exp2(a.y));
-                sum = f2add(sum, p);
-                w[8 * b + k / 2] = pack_f16x2(p.x, p.y);
-              }
-              tot[b] = sum.x + sum.y;
-            }
-          };
-          // The weights against the reference as it stands; their sum bounds the
-          // largest, so that maximum is only looked for where some row of the
-          // warp has no reference yet or a sum above 2^14
-          if (__any_sync(0xffffffffu, m_ref == -INFINITY)) find();
-          weights();
-          if (__any_sync(0xffffffffu, (tot[0] + tot[1]) + (tot[2] + tot[3]) > 16384.f)) {
-            find();
-            weights();
           }
-          const float4 iv = *reinterpret_cast<const float4*>(ivs + 4 * u);
-          l_run = fmaf(tot[0], iv.x, fmaf(tot[1], iv.y, fmaf(tot[2], iv.z, fmaf(tot[3], iv.w, l_run))));
-          tmem_st32w(tS + 32 * u, w);  // over columns [32 u, 32 u + 32), which have been read
+          const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+          add = tot = 0.f;
+#pragma unroll
+          for (int b = 0; b < NBH; b++) {
+            float s[16], f;
+            scores(b, s, f);
+            const float2 g = make_float2(f, f), o = make_float2(kvf[b] - mu, kvf[b] - mu);
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              const float2 a = f2fma(make_float2(s[k], s[k + 1]), g, o);
+              const float2 p = make_float2(fast_exp2(a.x), fast_exp2(a.y));
+              sum = f2add(sum, p);
+              w[8 * b + k / 2] = pack_f16x2(p.x, p.y);
+            }
+            const float both = sum.x + sum.y;
+            tot += both;
+            add = fmaf(both, ivs[b], add);
+          }
+          // the weights' sum bounds the largest; a row without a reference that
+          // sees keys now needs one
+          if (find || !pair_any(tot > 16384.f || (m_ref == -INFINITY && tot > 0.f))) break;
+          find = true;
         }
+        l_run += add;
+        // over this thread's own columns, which have been read
+#pragma unroll
+        for (int b = 0; b < NBH; b += 2) tmem_st16(tS + 8 * b, *reinterpret_cast<uint32_t(*)[16]>(w + 8 * b));
         asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
         tc_fence_before();
         __syncwarp();
         if (lane == 0) fp8_arrive(bar(PFULL + hf));
       }
 
-      // ---- epilogue: normalise, bf16, stored from registers ----
+      // ---- epilogue: normalise, bf16, stored from registers; each key half's
+      // threads take a share of the columns ----
+      sxch[kh * ROWS + r] = l_run;
+      pair_sync();
+      const float l = l_run + sxch[(kh ^ 1) * ROWS + r];
+      pair_sync();  // read before the next item's are written
       fp8_wait(bar(ODONE), ph_odone, abort_flag, c.status);
       ph_odone ^= 1;
       tc_fence_after();
       // a row that saw no usable key is zeros: O is 0 then, but for an item
       // without steps, whose O is not read (V's factor 2^-8 is undone here)
-      const float inv = l_run == 0.f ? 0.f : 256.f / l_run;
+      const float inv = l == 0.f ? 0.f : 256.f / l;
       const float2 inv2 = make_float2(inv, inv);
-      auto out_words = [&](int col, uint32_t* w) {  // 32 columns as bf16 pairs
-        if (nsteps == 0) {
-#pragma unroll
-          for (int i = 0; i < 16; i++) w[i] = 0;
-          return;
-        }
-        float o[32];
-        tmem_ld32(tO + col, o);
-#pragma unroll
-        for (int i = 0; i < 16; i++) {
-          const float2 y = __fmul2_rn(make_float2(o[2 * i], o[2 * i + 1]), inv2);
-          w[i] = pack_bf16x2_rn(y.x, y.y);
-        }
-      };
       uint16_t* const orow = c.out + (long long)(q0 + tok0 + (rok ? j : 0)) * c.out_stride +
                              (long long)(h * c.group + (rok ? r - j * c.group : 0)) * D;
       const bool al32 = ((reinterpret_cast<uintptr_t>(c.out) | (uintptr_t)(c.out_stride * 2) | (uintptr_t)(D * 2)) & 31) == 0;
-      auto st32 = [&](uint16_t* dst, const uint32_t* w) {
-        if (al32) {
-          asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                       "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                       : "memory");
-        } else {
-          reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        }
-      };
-      // A thread holds its row, and a lane quad's rows are usually heads of one
-      // token (contiguous when the group is a multiple of four): 64 columns at a
-      // time, the quad transposes its 32-byte units, so that each store writes a
-      // full 128-byte run per quad
-      uint16_t* qrow[4];
-#pragma unroll
-      for (int t = 0; t < 4; t++)
-        qrow[t] = reinterpret_cast<uint16_t*>(
-            __shfl_sync(0xffffffffu, rok ? reinterpret_cast<unsigned long long>(orow) : 0ull, (lane & ~3) | t));
-      const int qi = lane & 3;
+      constexpr int UNITS = D / 32, FIRST = (UNITS + 1) / 2;  // of 32 columns; the first key half's
 #pragma unroll 1
-      for (int base = 0; base < D / 64 * 64; base += 64) {
-        uint32_t u[32];  // unit t, words 8 t ..: columns base + 16 t .. of this thread's row
-        out_words(base, u);
-        out_words(base + 32, u + 16);
+      for (int u = kh ? FIRST : 0; u < (kh ? UNITS : FIRST); u++) {
+        uint32_t w[16];
 #pragma unroll
-        for (int x = 1; x <= 2; x <<= 1) {
-          const bool upper = (qi & x) != 0;
+        for (int hh = 0; hh < 2; hh++) {
+          uint32_t o[16];
+          if (nsteps > 0) {
+            tmem_ld16(tO + 32 * u + 16 * hh, o);
+          } else {
 #pragma unroll
-          for (int a = 0; a < 4; a++) {
-            if (a & x) continue;  // pairs (a, a + x)
+            for (int i = 0; i < 16; i++) o[i] = 0;
+          }
 #pragma unroll
-            for (int k = 0; k < 8; k++) {
-              const int mine = 8 * a + k, other = 8 * (a + x) + k;
-              const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? u[mine] : u[other], x);
-              if (upper) u[mine] = got;
-              else u[other] = got;
-            }
+          for (int i = 0; i < 8; i++) {
+            const float2 y = __fmul2_rn(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), inv2);
+            w[8 * hh + i] = pack_bf16x2_rn(y.x, y.y);
           }
         }
-#pragma unroll
-        for (int t = 0; t < 4; t++)
-          if (qrow[t] != nullptr) st32(qrow[t] + base + 16 * qi, u + 8 * t);
-      }
-      if constexpr (D % 64 != 0) {  // the last 32 columns, each thread its own row
-        uint32_t w[16];
-        out_words(D - 32, w);
         if (rok) {
-          st32(orow + D - 32, w);
-          st32(orow + D - 16, w + 8);
+          uint16_t* const dst = orow + 32 * u;
+          if (al32) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 8)
+              asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(dst + 2 * i), "r"(w[i]),
+                           "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]),
+                           "r"(w[i + 7])
+                           : "memory");
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+              *reinterpret_cast<uint4*>(dst + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+          }
         }
       }
     }
   } else {
     // ============== convert, producer and MMA warps ==============
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
     // waits for completions of a barrier pair indexed by step parity, counted
     auto wait_until = [&](int first, int& done, int count) {
       for (; done < count; done++) fp8_wait(bar(first + (done & 1)), (done >> 1) & 1, abort_flag, c.status);
     };
-    if (warp < 16) {
+    if (warp < 24) {
       // ================= convert warps =================
       // one team's loop: kv = 0 K codes, 1 V codes
       auto team = [&](auto kv_tag) {
@@ -601,11 +553,11 @@ __global__ void __launch_bounds__(20 * 32, 1)
           }
         }
       };
-      if (warp < 12)
+      if (warp < 20)
         team(std::integral_constant<int, 0>{});
       else
         team(std::integral_constant<int, 1>{});
-    } else if (warp == 16) {
+    } else if (warp == 24) {
       // ================= producer warp =================
       uint32_t ph_ifree = 0;
       int n = 0, nq = 0, kfree = 0;
@@ -694,7 +646,7 @@ __global__ void __launch_bounds__(20 * 32, 1)
       if (n > 0 && !(mbar_wait_bounded(bar(RKFULL), (n - 1) & 1) && mbar_wait_bounded(bar(RVFULL), (n - 1) & 1) &&
                      mbar_wait_bounded(bar(QFULL), (nq - 1) & 1)))
         flag(c.status, KV_INT4_DEV_TIMEOUT);
-    } else if (warp == 17) {
+    } else if (warp == 25) {
       // ================= MMA warp =================
       uint32_t lead;
       asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(lead));
@@ -715,7 +667,8 @@ __global__ void __launch_bounds__(20 * 32, 1)
         const uint64_t vt = dv + (uint64_t)(b * (G::KVBYTES >> 4));
 #pragma unroll
         for (int kk = 0; kk < NB; kk++)
-          fp8_mma_ts(lead, tm + G::O_COL + hh * D, tm + NK * hh + kk * 8, vt + (uint64_t)(kk * (2048 >> 4)), IDESC_O,
+          fp8_mma_ts(lead, tm + G::O_COL + hh * D,
+                     tm + NK * hh + (kk < NB / 2 ? kk * 8 : NK / 2 + (kk - NB / 2) * 8), vt + (uint64_t)(kk * (2048 >> 4)), IDESC_O,
                      !first || kk > 0);
       };
 #pragma unroll 1
@@ -774,7 +727,7 @@ __global__ void __launch_bounds__(20 * 32, 1)
       }
     }
   }
-  if (warp == 17) {
+  if (warp == 25) {
     // after a time-out MMAs may still be in flight: they end by themselves
     // and must end before the columns are freed
     if (lane == 0) umma_commit(bar(DRAIN));
