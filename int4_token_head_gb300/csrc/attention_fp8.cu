@@ -208,7 +208,7 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
       const int e = with_np(c.np, [&](auto np_tag) {
         constexpr int NP = decltype(np_tag)::value;
         return launch_pdl(decode_fp8_kernel<D, NP, true>, dim3((unsigned)(tasks * cl)), c.hg * 32,
-                          Fp8Dec<D, NP>::smem_bytes(c.hg), stream, cl, Fp8DecParams{c, pv, 0, cl});
+                          Fp8Dec<D, NP>::smem_bytes(c.hg), stream, cl, Fp8DecParams{c, pv, 0, cl, false});
       });
       timing_end(kTimedDecode, stream);
       return e;
@@ -255,7 +255,7 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
     if (e) return e;
   }
   if (any_decode) {
-    const Fp8DecParams prm{c, pv, dec_grid, 1};
+    const Fp8DecParams prm{c, pv, dec_grid, 1, may_prefill};
     const int threads = c.hg * 32;
     timing_begin(kTimedDecode, stream);
     int e = with_np(c.np, [&](auto np_tag) {

@@ -68,6 +68,7 @@ struct Fp8DecParams {
   PlanView pv;
   int num_ctas;
   int cluster;  // DIRECT: CTAs per (sequence, head group)
+  bool beside;  // the kernel before is a prefill of the same call
 };
 
 template <int NP>
@@ -135,7 +136,10 @@ __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
   const int g = lane >> 2, cq = lane & 3;
   const int SB = G::slot_bytes(HG);
   pdl_trigger();
-  pdl_wait();
+  // After a prefill launch, which waits for the schedule before it lets this
+  // kernel in, decode runs beside it (on the SMs that prefill leaves) and waits
+  // for it only at its end, so that what follows comes after both
+  if (!prm.beside) pdl_wait();
   int* sflag = reinterpret_cast<int*>(smem + G::NS * SB);
 
   Fp8Walk cw;
@@ -164,13 +168,19 @@ __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
     cw.npos = end;  // the CTA's last position ends its segment
   } else {
     const int n_dseq = pv.plan[0];
-    if (n_dseq == 0) return;
+    if (n_dseq == 0) {
+      if (prm.beside) pdl_wait();
+      return;
+    }
     const int gpl = c.ng / c.nl;  // head groups per lane
     const int my_lane = blockIdx.x % c.nl, rr = blockIdx.x / c.nl;
     const long long Tu = pv.dprefix[n_dseq] * gpl;
     const int R = prm.num_ctas / c.nl;
     const long long P0 = Tu * rr / R, P1 = Tu * (rr + 1) / R;
-    if (P0 >= P1) return;
+    if (P0 >= P1) {
+      if (prm.beside) pdl_wait();
+      return;
+    }
     nunits = (int)(P1 - P0);
 
     // largest i with dprefix[i] * gpl <= P0 (32-ary search, per warp)
@@ -542,6 +552,7 @@ __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
     if (cs >= G::NS) cs -= G::NS;
   }
   cp_async_wait<0>();
+  if (prm.beside) pdl_wait();
   if constexpr (DIRECT) {
     __syncthreads();
     flush();

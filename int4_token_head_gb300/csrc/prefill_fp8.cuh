@@ -29,8 +29,8 @@ __global__ void __launch_bounds__(Fp8Pre<D>::THREADS) prefill_fp8_kernel(Common 
   int* sitem = reinterpret_cast<int*>(sQ + G::ROWS * G::QSTRIDE);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, cq = lane & 3;
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();  // after the wait: the decode beside this kernel relies on the schedule
   const int n_items = pv.plan[1];
 
 #pragma unroll 1

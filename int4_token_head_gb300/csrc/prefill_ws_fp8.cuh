@@ -255,9 +255,10 @@ __global__ void __launch_bounds__(28 * 32, 1)
     fence_mbar_init();
   }
   // shared memory and TMEM are this CTA's own; the schedule and the caches come
-  // from the kernels before
-  pdl_trigger();
+  // from the kernels before.  The next kernel (decode) is let in after the wait:
+  // it may rely on the schedule being complete
   pdl_wait();
+  pdl_trigger();
   if (warp == 0) tmem_alloc(smem_addr(tslot), 512);
   tc_fence_before();
   __syncthreads();
