@@ -423,69 +423,68 @@ def _refuse(msg):
     raise ValueError(msg)
 
 
-def _stream_of(tensors, stream) -> int:
-    """The raw stream of a call on these tensors, which must share the current
-    CUDA device (None entries are skipped)."""
-    dev = tensors[0].get_device()  # -1: a CPU tensor
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            _refuse("tensors must be on one device")
+def _raw_stream(dev: int, same: bool, stream) -> int:
+    """The raw stream of a call on tensors of device `dev` (-1: the CPU), `same`
+    for all of them; it must be the current device."""
+    if not same:
+        _refuse("tensors must be on one device")
     if dev < 0:
         _refuse("tensors must be on a CUDA device")
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         _refuse(f"tensors are on cuda:{dev}, which is not the current device (torch.cuda.device selects it)")
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _status_ptr(dev_status: Optional[torch.Tensor]):
+def _status_ptr(dev_status: Optional[torch.Tensor], dev: int):
     if dev_status is None:
         return None
-    if dev_status.dtype != torch.int32 or dev_status.numel() < 1:
-        _refuse("dev_status must be int32 [1]")
+    if dev_status.dtype is not torch.int32 or dev_status.numel() < 1 or dev_status.get_device() != dev:
+        _refuse("dev_status must be int32 [1], on one device with the other tensors")
     return dev_status.data_ptr()
 
 
 def _rows(x: torch.Tensor, name: str, tokens: int, heads: int, d: int) -> int:
     """Token stride of bf16 head vectors [tokens, heads, d] (as _token_major, with
     nothing formatted unless it is refused)."""
-    shape, stride = x.shape, x.stride()
-    if len(shape) != 3 or shape[1] != heads or shape[2] != d:
-        _refuse(f"{name} must be [tokens, {heads}, {d}], got {tuple(shape)}")
-    if shape[0] != tokens:
-        _refuse(f"{name} must have {tokens} tokens: the tensors disagree on tokens, got {shape[0]}")
-    if x.dtype != torch.bfloat16:
-        _refuse(f"{name} must be bfloat16")
-    if stride[2] != 1 or (heads > 1 and stride[1] != d):
+    if x.shape == (tokens, heads, d) and x.dtype is torch.bfloat16:
+        stride = x.stride()
+        if stride[2] == 1 and (heads == 1 or stride[1] == d):
+            return stride[0] if tokens > 0 else heads * d
         _refuse(f"{name} must have contiguous heads and head dims")
-    return stride[0] if tokens > 0 else heads * d
+    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != d:
+        _refuse(f"{name} must be [tokens, {heads}, {d}], got {tuple(x.shape)}")
+    if x.shape[0] != tokens:
+        _refuse(f"{name} must have {tokens} tokens: the tensors disagree on tokens, got {x.shape[0]}")
+    _refuse(f"{name} must be bfloat16")
 
 
 def _cache_dims_fp8(k_cache, v_cache, k_scale, v_scale):
-    shape = k_cache.shape
-    if k_cache.dtype not in (torch.float8_e4m3fn, torch.uint8) or v_cache.dtype != k_cache.dtype:
+    dtype, shape = k_cache.dtype, k_cache.shape
+    if (dtype is not torch.float8_e4m3fn and dtype is not torch.uint8) or v_cache.dtype is not dtype:
         _refuse("fp8 caches must be float8_e4m3fn (or its bytes as uint8)")
     if len(shape) != 4 or shape != v_cache.shape:
         _refuse("caches must be [blocks, block_size, heads, d]")
     if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
         _refuse("caches must be contiguous")
-    nb, bs, hkv, d = shape
-    for s in (k_scale, v_scale):
-        if s.dtype != torch.float32 or s.shape != (nb, hkv) or not s.is_contiguous():
-            _refuse("scale caches must be contiguous float32 [blocks, heads]")
-    return nb, bs, hkv, d
+    nb, _, hkv, _ = shape
+    scale = (nb, hkv)
+    if not (k_scale.shape == scale and v_scale.shape == scale and k_scale.dtype is torch.float32 and
+            v_scale.dtype is torch.float32 and k_scale.is_contiguous() and v_scale.is_contiguous()):
+        _refuse("scale caches must be contiguous float32 [blocks, heads]")
+    return shape
 
 
 def _sequences(block_table, seq_lens, start_loc):
     table = block_table.shape
-    if block_table.dtype != torch.int32 or len(table) != 2 or not block_table.is_contiguous():
+    if block_table.dtype is not torch.int32 or len(table) != 2 or not block_table.is_contiguous():
         _refuse("block_table must be contiguous int32 [seqs, max_blocks]")
-    for t, n in ((seq_lens, table[0]), (start_loc, table[0] + 1)):
-        if t.dtype != torch.int32 or not t.is_contiguous():
-            _refuse("sequence lengths and start locations must be contiguous int32 vectors")
-        if t.shape != (n,):
-            _refuse("metadata shapes: seq_lens must be [seqs] and start locations [seqs + 1]")
+    if not (seq_lens.dtype is torch.int32 and start_loc.dtype is torch.int32 and seq_lens.is_contiguous() and
+            start_loc.is_contiguous()):
+        _refuse("sequence lengths and start locations must be contiguous int32 vectors")
+    if seq_lens.shape != (table[0],) or start_loc.shape != (table[0] + 1,):
+        _refuse("metadata shapes: seq_lens must be [seqs] and start locations [seqs + 1]")
     return table
 
 
@@ -497,11 +496,13 @@ def write_fp8(k, v, block_table, seq_lens, start_loc, max_len, k_cache, v_cache,
     num_seqs, width = _sequences(block_table, seq_lens, start_loc)
     tokens = k.shape[0]
     ks, vs = _rows(k, "k", tokens, hkv, d), _rows(v, "v", tokens, hkv, d)
-    st = _stream_of((k, v, block_table, seq_lens, start_loc, k_cache, v_cache, k_scale, v_scale, dev_status), stream)
+    dev = k_cache.get_device()
+    st = _raw_stream(dev, v_cache.get_device() == k_scale.get_device() == v_scale.get_device() == block_table.get_device()
+                     == seq_lens.get_device() == start_loc.get_device() == k.get_device() == v.get_device() == dev, stream)
     code = (_lib or load()).kv_fp8_write(
         k.data_ptr(), ks, v.data_ptr(), vs, block_table.data_ptr(), width, seq_lens.data_ptr(), start_loc.data_ptr(),
         num_seqs, tokens, max_len, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), nb,
-        bs, hkv, d, _status_ptr(dev_status), st)
+        bs, hkv, d, _status_ptr(dev_status, dev), st)
     if code:
         _raise(code, "kv_fp8_write")
 
@@ -514,11 +515,13 @@ def read_fp8(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, start_lo
     num_seqs, width = _sequences(block_table, seq_lens, start_loc)
     tokens = k.shape[0]
     ks, vs = _rows(k, "k", tokens, hkv, d), _rows(v, "v", tokens, hkv, d)
-    st = _stream_of((k, v, block_table, seq_lens, start_loc, k_cache, v_cache, k_scale, v_scale, dev_status), stream)
+    dev = k_cache.get_device()
+    st = _raw_stream(dev, v_cache.get_device() == k_scale.get_device() == v_scale.get_device() == block_table.get_device()
+                     == seq_lens.get_device() == start_loc.get_device() == k.get_device() == v.get_device() == dev, stream)
     code = (_lib or load()).kv_fp8_read(
         k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), width,
         seq_lens.data_ptr(), start_loc.data_ptr(), num_seqs, tokens, max_len, k.data_ptr(), ks, v.data_ptr(), vs, nb,
-        bs, hkv, d, _status_ptr(dev_status), st)
+        bs, hkv, d, _status_ptr(dev_status, dev), st)
     if code:
         _raise(code, "kv_fp8_read")
 
@@ -534,15 +537,17 @@ def attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, 
         _refuse("q must be [tokens, q_heads, d]")
     tokens, hq, _ = q.shape
     qs, os_ = _rows(q, "q", tokens, hq, d), _rows(out, "out", tokens, hq, d)
-    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+    if workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
         _refuse("workspace must be contiguous uint8")
-    st = _stream_of((q, out, block_table, seq_lens, query_start_loc, k_cache, v_cache, k_scale, v_scale, workspace,
-                     dev_status), stream)
+    dev = k_cache.get_device()
+    st = _raw_stream(dev, v_cache.get_device() == k_scale.get_device() == v_scale.get_device() == block_table.get_device()
+                     == seq_lens.get_device() == query_start_loc.get_device() == q.get_device() == out.get_device()
+                     == workspace.get_device() == dev, stream)
     code = (_lib or load()).kv_fp8_attention(
         q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
         block_table.data_ptr(), width, seq_lens.data_ptr(), query_start_loc.data_ptr(), num_seqs, tokens,
         max_query_len, max_seq_len, hq, hkv, d, bs, nb, softmax_scale, 1 if causal else 0, sliding_window,
-        out.data_ptr(), os_, workspace.data_ptr(), workspace.numel(), _status_ptr(dev_status), st)
+        out.data_ptr(), os_, workspace.data_ptr(), workspace.numel(), _status_ptr(dev_status, dev), st)
     if code:
         _raise(code, "kv_fp8_attention")
 
@@ -580,9 +585,15 @@ def qk_norm_rope(q, k, positions, cos_sin, q_weight, k_weight, eps, q_out, k_out
         pos, table = positions.data_ptr(), cos_sin.data_ptr()
     elif cos_sin is not positions:
         _refuse("positions and cos_sin: both or neither")
-    st = _stream_of((q, k, q_out, k_out, positions, cos_sin, q_weight, k_weight, dev_status), stream)
+    dev = q.get_device()
+    same = k.get_device() == q_out.get_device() == k_out.get_device() == dev
+    if qw is not None:
+        same = same and q_weight.get_device() == k_weight.get_device() == dev
+    if pos is not None:
+        same = same and positions.get_device() == cos_sin.get_device() == dev
+    st = _raw_stream(dev, same, stream)
     code = (_lib or load()).kv_qk_norm_rope(
         q.data_ptr(), qs, k.data_ptr(), ks, tokens, hq, hkv, d, qw, kw, eps, pos, table, max_pos, rot,
-        1 if interleaved else 0, q_out.data_ptr(), qo, k_out.data_ptr(), ko, _status_ptr(dev_status), st)
+        1 if interleaved else 0, q_out.data_ptr(), qo, k_out.data_ptr(), ko, _status_ptr(dev_status, dev), st)
     if code:
         _raise(code, "kv_qk_norm_rope")

@@ -221,10 +221,13 @@ __device__ void build_schedule(const Common& c, const PlanView& pv) {
     auto bucket = [&](int nkb) { return kBuckets - 1 - min(kBuckets - 1, nkb >> sh); };
     for (int i = threadIdx.x; i < kBuckets; i += kPrepThreads) hist[i] = 0;
     __syncthreads();  // the sequence table and the histogram
-    for (int p = threadIdx.x; p < n_pseq; p += kPrepThreads) {
+    // a few long sequences: a warp's lanes share a sequence's tiles; many: a
+    // thread each
+    const int lps = n_pseq >= kPrepThreads / 4 ? 1 : 32, tl = threadIdx.x % lps;
+    for (int p = threadIdx.x / lps; p < n_pseq; p += kPrepThreads / lps) {
       const int sq = pv.ptab[p].x, qn = c.qsl[sq + 1] - c.qsl[sq], Ls = c.seq_lens[sq];
       const int nt = (qn + c.tile_tokens - 1) / c.tile_tokens;
-      for (int t = 0; t < nt; t++) atomicAdd(&hist[bucket((prefill_tile_keys(c, Ls, qn, t) + 15) / 16)], 1);
+      for (int t = tl; t < nt; t += lps) atomicAdd(&hist[bucket((prefill_tile_keys(c, Ls, qn, t) + 15) / 16)], 1);
     }
     __syncthreads();
     // exclusive prefix over the buckets: thread j owns buckets [8j, 8j + 8)
@@ -241,10 +244,10 @@ __device__ void build_schedule(const Common& c, const PlanView& pv) {
       run += hb;
     }
     __syncthreads();
-    for (int p = threadIdx.x; p < n_pseq; p += kPrepThreads) {
+    for (int p = threadIdx.x / lps; p < n_pseq; p += kPrepThreads / lps) {
       const int sq = pv.ptab[p].x, qn = c.qsl[sq + 1] - c.qsl[sq], Ls = c.seq_lens[sq];
       const int nt = (qn + c.tile_tokens - 1) / c.tile_tokens;
-      for (int t = 0; t < nt; t++)
+      for (int t = tl; t < nt; t += lps)
         pv.plist[atomicAdd(&hist[bucket((prefill_tile_keys(c, Ls, qn, t) + 15) / 16)], 1)] = make_int2(sq, t);
     }
   }
