@@ -43,7 +43,7 @@
 //   vfree[b]  WV0 and WV1 that read V tile b complete
 //   sfull[h]  S_h complete (and every earlier MMA)
 //   pfull[h]  W_h in TMEM, O_h rescaled if it had to be
-//   odone     the item's last WV complete
+//   odone     the item's last WV complete (items with steps)
 // Ring entry n % 3 is written once S of step n - 2 is complete: it was issued
 // after both halves' W of step n - 3, the entry's last readers.  An item's Q is
 // copied once S of the previous item's last step is complete.
@@ -428,9 +428,11 @@ __global__ void __launch_bounds__(28 * 32, 1)
       pair_sync();
       const float l = l_run + sxch[(kh ^ 1) * ROWS + r];
       pair_sync();  // read before the next item's are written
-      fp8_wait(bar(ODONE), ph_odone, abort_flag, c.status);
-      ph_odone ^= 1;
-      tc_fence_after();
+      if (nsteps > 0) {
+        fp8_wait(bar(ODONE), ph_odone, abort_flag, c.status);
+        ph_odone ^= 1;
+        tc_fence_after();
+      }
       // a row that saw no usable key is zeros: O is 0 then, but for an item
       // without steps, whose O is not read (V's factor 2^-8 is undone here)
       const float inv = l == 0.f ? 0.f : 256.f / l;
@@ -520,8 +522,15 @@ __global__ void __launch_bounds__(28 * 32, 1)
               y[i] = *reinterpret_cast<const uint4*>(src + G::stage_off(k, (U + i) * TPK + (TPK > 1 ? g0 : 0)));
             }
             static_assert(2 * U == CH, "an even number of chunks");
-            __syncwarp();
-            if (lane == 0) fp8_arrive(bar(RKFREE + KV));
+            // ... once they have all arrived: the arrival's address depends on every
+            // load (by a mask that is 0), as nothing else orders shared loads in
+            // flight before it (TMA then overwrote codes that were still to be
+            // read)
+            uint32_t seen = 0;
+#pragma unroll
+            for (int i = 0; i < U; i++) seen |= x[i].x | y[i].x;
+            seen = __reduce_or_sync(0xffffffffu, seen & (uint32_t)(c.num_blocks >> 31));
+            if (lane == 0) fp8_arrive(bar(RKFREE + KV) + seen);
             wait_until(FREE, freed, n - 1);  // the MMAs of step n - 2 that read this tile
 #pragma unroll 1
             for (int i0 = 0; i0 < CH; i0 += U) {
@@ -724,7 +733,9 @@ __global__ void __launch_bounds__(28 * 32, 1)
             n++;
           }
         }
-        fp8_commit(lead, bar(ODONE));
+        // none for an item without steps: its completion would follow the last
+        // item's at once, before every softmax warp has seen that
+        if (nsteps > 0) fp8_commit(lead, bar(ODONE));
       }
     }
   }

@@ -95,7 +95,9 @@ def attention(q, caches, block_table, seq_lens, start, softmax_scale, causal, wi
     scale).  bound is what the kernels' roundings can add to each output before
     the final one to bf16:
       - a weight times its V scale is rounded to f16, half a step 2^-11 of it,
-        or 2^-25 of the largest where it is subnormal, at most itself;
+        or, where it is subnormal, 2^-24 of the largest: half the spacing is 2^-25,
+        and the largest is above 1/2, not 1, as exponents are taken relative to a
+        whole number at or above the greatest; at most itself;
       - a score is an fp32 sum of D products of f16 and E4M3 values and one
         fma: at most (D + 4) 2^-24 sum |q k| in it, with the f16 spacing
         2^-24 max|q| of small query elements; the exponent's error moves weight
@@ -145,7 +147,7 @@ def attention(q, caches, block_table, seq_lens, start, softmax_scale, causal, wi
                 part = np.where(seen, w * np.where(usable, scale_v, 0.0), 0.0)  # weights as the MMA holds them ...
                 most = part.max(1, keepdims=True)
                 u = part / np.where(most == 0, 1.0, most)                       # ... in units of the largest
-                err = np.minimum(u, np.maximum(2.0 ** -11 * u, 2.0 ** -25)) * most
+                err = np.minimum(u, np.maximum(2.0 ** -11 * u, 2.0 ** -24)) * most
                 code = np.abs(v) / np.where(any_seen & usable, vs[safe, h].astype(np.float64), 1.0)[:, None]
                 bound[a:b, h * group + j] = rel * (w @ np.abs(v)) + err @ code
     return out, bound

@@ -307,6 +307,50 @@ def test_prefill(d, hq, hkv):
     _check([(70, 70), (17, 200), (1, 40), (33, 33), (9, 9), (130, 150), (0, 3)], hq, hkv, d, seed=d + hq)
 
 
+@pytest.mark.parametrize("d", HEADS)
+def test_prefill_many_tiles_per_cta(d):
+    """More tiles than SMs, so that every CTA goes through several, short and
+    long ones after another, and rows without keys between them; run again and
+    again for the same bits."""
+    seqs = [(n, n) for n in (300, 290, 17, 310, 300, 5, 280, 300, 290, 40, 300, 310, 300, 260, 300, 290, 300, 33, 300, 310)]
+    b = Batch(seqs, 8, d, seed=d).fill(3)
+    q = _bf16((b.tokens, 16, d), 4)
+    dev, meta = b.device(), b.meta()
+    out = _attend(b, q.cuda(), dev, 16, meta=meta)
+    for _ in range(20):
+        assert torch.equal(_attend(b, q.cuda(), dev, 16, meta=meta), out)
+    ref, bound = F.attention(q.double().numpy(), b.host(), b.table, b.lens, b.start, d ** -0.5, True)
+    _assert_attention(out, ref, bound)
+    # cross attention, a third of the sequences without keys
+    seqs = [(200, (0, 400, 90)[i % 3]) for i in range(30)]
+    b = Batch(seqs, 8, d, seed=d).fill(5)
+    q = _bf16((b.tokens, 16, d), 6)
+    out = _attend(b, q.cuda(), b.device(), 16, causal=False)
+    ref, bound = F.attention(q.double().numpy(), b.host(), b.table, b.lens, b.start, d ** -0.5, False)
+    _assert_attention(out, ref, bound)
+    assert b.status.item() == 0
+
+
+@pytest.mark.parametrize("d", HEADS)
+def test_prefill_rising_scores(d):
+    """Keys that grow along the sequence: the running maximum moves in every step,
+    by little and by more than the weights can hold."""
+    b = Batch([(200, 900), (60, 700)], 2, d)
+    g = np.random.default_rng(2)
+    for i, (_, length) in enumerate(b.seqs):
+        for codes, scale, rising in ((b.kc, b.ks, True), (b.vc, b.vs, False)):
+            x = g.standard_normal((length, 2, d))
+            if rising:
+                x *= np.exp2(np.linspace(-4, 5, length))[:, None, None]
+            x = torch.from_numpy(x).to(torch.bfloat16).double().numpy()
+            F.write(x, b.table[i:i + 1], [length], [0, length], codes, scale)
+    q = _bf16((b.tokens, 8, d), 7)
+    for causal in (True, False):
+        out = _attend(b, q.cuda(), b.device(), 8, causal=causal)
+        ref, bound = F.attention(q.double().numpy(), b.host(), b.table, b.lens, b.start, d ** -0.5, causal)
+        _assert_attention(out, ref, bound)
+
+
 @pytest.mark.parametrize("d", [64, 96, 128, 192, 256])
 @pytest.mark.parametrize("window", [1, 5, 16, 33, 1000])
 def test_windows(d, window):
