@@ -157,9 +157,10 @@ KVINT4_API int kv_int8_write(const void* k, int64_t k_token_stride, const void* 
 
 /*
  * kv_int4_attention_workspace_size -- bytes of device workspace that
- * kv_int4_attention needs for these sizes (a pure host computation).  The
- * workspace holds the device-built schedule, the rotated queries and the
- * split-KV partial results; its contents need no initialisation.
+ * kv_int4_attention, kv_int8_attention and kv_fp8_attention need for these
+ * sizes (a pure host computation).  The workspace holds the device-built
+ * schedule, the rotated queries and the split-KV partial results; its contents
+ * need no initialisation.
  * Returns 0 for invalid arguments.
  */
 KVINT4_API size_t kv_int4_attention_workspace_size(int num_seqs, int num_q_tokens,
@@ -265,9 +266,9 @@ KVINT4_API int kv_int8_attention(const void* q, int64_t q_token_stride,
  * Arguments, layouts, results and errors are those of kv_int4_attention,
  * minus workspace and workspace_bytes.  The workspace is instead a static
  * device array of KV_INT4_NOALLOC_SCRATCH_BYTES (64 MiB) that every GPU which
- * loads the library holds until the process exits.  A call whose
- * kv_int4_attention_workspace_size(...) exceeds that returns
- * KV_INT4_ERR_SCRATCH_LIMIT and enqueues nothing.  The function allocates
+ * loads the library holds until the process exits.  A call that needs more
+ * (kv_int4_attention_workspace_size(...) bytes suffice, but count what only
+ * kv_fp8_attention uses) returns KV_INT4_ERR_SCRATCH_LIMIT and enqueues nothing.  The function allocates
  * nothing (no cudaMalloc, cudaFree or allocating library call).
  *
  * The first call on a device (with that device current) looks up the array's

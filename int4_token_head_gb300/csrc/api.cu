@@ -92,6 +92,36 @@ bool workspace_layout(int num_seqs, int num_q_tokens, int num_q_heads, int num_k
   return true;
 }
 
+bool workspace_layout_fp8(int num_seqs, int num_q_tokens, int num_q_heads, int num_kv_heads,
+                          int head_size, WorkspaceLayoutFp8* L) {
+  if (num_seqs < 0 || num_q_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_size <= 0) return false;
+  if (num_q_heads % num_kv_heads) return false;
+  const size_t group = num_q_heads / num_kv_heads;
+  const size_t tile_tokens = group < (size_t)kPrefillRows ? kPrefillRows / group : 1;  // of the smaller tile
+  const size_t S = num_seqs, T = num_q_tokens, Hkv = num_kv_heads, D = head_size;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align256(off + bytes);
+    return at;
+  };
+  L->max_pairs = T / tile_tokens + S;
+  L->plan = take(64 * 4);
+  L->dseq = take(S * 16);
+  L->dprefix = take((S + 1) * 8);
+  L->ptab = take((S + 1) * 8);
+  L->plist = take((L->max_pairs + kMaxPieces) * 32);
+  L->msplit = take(kMaxPieces / 2 * 16);
+  L->direct_o = take(S * Hkv * kDecodeColsFp8 * D * 4);
+  L->direct_ml = take(S * Hkv * kDecodeColsFp8 * 2 * 4);
+  L->warp_o = take((size_t)kMaxDecodeWarps * kDecodeCols * D * 4);
+  L->warp_ml = take((size_t)kMaxDecodeWarps * kDecodeCols * 2 * 4);
+  L->piece_o = take((size_t)kPieceRows * D * 4);
+  L->piece_ml = take((size_t)kPieceRows * 2 * 4);
+  L->total = off;
+  return true;
+}
+
 }  // namespace kvint4
 
 using namespace kvint4;
@@ -216,8 +246,11 @@ size_t kv_int4_attention_workspace_size(int num_seqs, int num_q_tokens, int num_
                                         int head_size) {
   if (!head_size_ok(head_size)) return 0;
   WorkspaceLayout L;
-  if (!workspace_layout(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_size, &L)) return 0;
-  return L.total;
+  WorkspaceLayoutFp8 F;  // one size serves both families of caches
+  if (!workspace_layout(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_size, &L) ||
+      !workspace_layout_fp8(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_size, &F))
+    return 0;
+  return L.total > F.total ? L.total : F.total;
 }
 
 static int do_attention(const void* q, int64_t q_token_stride, const uint8_t* k_cache, const uint8_t* v_cache,

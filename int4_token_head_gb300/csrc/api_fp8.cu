@@ -97,8 +97,8 @@ int kv_fp8_attention(const void* q, int64_t q_token_stride, const uint8_t* k_cac
   if (!aligned16(q) || !aligned16(out) || !stride_ok(q_token_stride) || !stride_ok(out_token_stride) ||
       !aligned(workspace, 256))
     return KV_INT4_ERR_ALIGN;
-  WorkspaceLayout L;
-  if (!workspace_layout(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_size, &L)) return KV_INT4_ERR_SIZE;
+  WorkspaceLayoutFp8 L;
+  if (!workspace_layout_fp8(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_size, &L)) return KV_INT4_ERR_SIZE;
   if (workspace_bytes < L.total) return KV_INT4_ERR_WORKSPACE;
   if (current_device() < 0) return KV_INT4_ERR_CUDA;
   AttnArgs a{q, q_token_stride, k_cache, v_cache, k_scale_cache, v_scale_cache, block_table, max_blocks_per_seq,

@@ -32,10 +32,11 @@
 namespace kvint4 {
 namespace {
 
+template <bool PREFILL>
 __global__ void __launch_bounds__(kPrepThreads) plan_fp8_kernel(Common c, PlanView pv) {
   pdl_trigger();
   pdl_wait();
-  build_schedule<true>(c, pv);
+  build_schedule<true, PREFILL>(c, pv);
 }
 
 // A query row's power of two from its largest bf16 magnitude bits: rows are
@@ -69,8 +70,9 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
-int launch_plan(const Common& c, const PlanView& pv, cudaStream_t stream) {
-  return launch_pdl(plan_fp8_kernel, dim3(1), kPrepThreads, 0, stream, 1, c, pv);
+int launch_plan(const Common& c, const PlanView& pv, bool may_prefill, cudaStream_t stream) {
+  return launch_pdl(may_prefill ? plan_fp8_kernel<true> : plan_fp8_kernel<false>, dim3(1), kPrepThreads, 0, stream, 1, c,
+                    pv);
 }
 
 // the tensor maps of a call's prefill; false where its tensors have no such
@@ -108,9 +110,9 @@ bool make_maps(const AttnArgs& a, int tile_tokens, Fp8Maps* m) {
 
 template <int D>
 int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
-  WorkspaceLayout L;
-  workspace_layout(a.num_seqs, a.num_q_tokens, a.num_q_heads, a.num_kv_heads, a.head_size, &L);
-  const PlanView pv = plan_view(a.workspace, L);
+  WorkspaceLayoutFp8 L;
+  workspace_layout_fp8(a.num_seqs, a.num_q_tokens, a.num_q_heads, a.num_kv_heads, a.head_size, &L);
+  const PlanView pv = plan_view_fp8(a.workspace, L);
   const int dev = current_device();
   const int sms = sm_count(dev);
   Common c{};
@@ -139,7 +141,7 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
   c.out = static_cast<uint16_t*>(a.out);
   c.out_stride = a.out_stride;
   c.status = a.dev_status;
-  c.max_items = L.max_prefill_items;
+  c.max_items = L.max_pairs * a.num_kv_heads;
   // f with the number of blocks per position as a constant
   auto with_np = [](int np, auto&& f) {
     if (np == 1) return f(std::integral_constant<int, 1>{});
@@ -218,42 +220,70 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
   // prefill items: 256 rows on the tensor-core kernel (head sizes up to 192:
   // two accumulators of 256 columns would leave no TMEM for scores), 64 on the
   // warp-MMA one
+  // Keys are split into pieces of at least four steps of the tensor-core kernel
+  // (512 keys; 256 at 192), eight of the other (256 keys)
   bool tc = false;
+  const long long pairs = L.max_pairs + kMaxPieces;
+  const long long most_items = pairs * a.num_kv_heads;
   if constexpr (D <= 192) {
+    using G = Fp8Ws<D>;
     Fp8Maps maps;
-    tc = may_prefill && make_maps<D>(a, Fp8Ws<D>::ROWS / c.group, &maps);
-    c.tile_tokens = (tc ? Fp8Ws<D>::ROWS : kPrefillRows) / c.group;
-    if (int e = launch_plan(c, pv, stream)) return e;
+    tc = may_prefill && make_maps<D>(a, G::ROWS / c.group, &maps);
     if (tc) {
-      using G = Fp8Ws<D>;
+      c.tile_tokens = G::ROWS / c.group;
+      c.step_blocks = G::NB;
+      c.split_steps = 4;
+      c.split_ctas = sms;
       static PerContext<int> occ_c;
       int occ = 0;
       if (!occ_c.get(dev, [](int* o) { return configure_tmem(prefill_ws_fp8_kernel<D>, G::SMEM, G::THREADS, 512, o); },
                      &occ))
         return KV_INT4_ERR_CUDA;
-      const long long grid = sms < L.max_prefill_items ? sms : L.max_prefill_items;
+      if (int e = launch_plan(c, pv, may_prefill, stream)) return e;
+      const long long grid = sms < most_items ? sms : most_items;
       timing_begin(kTimedPrefill, stream);
       const int e = launch_pdl(prefill_ws_fp8_kernel<D>, dim3((unsigned)grid), G::THREADS, G::SMEM, stream, 1, c, pv, maps);
       timing_end(kTimedPrefill, stream);
       if (e) return e;
     }
-  } else {
-    c.tile_tokens = kPrefillRows / c.group;
-    if (int e = launch_plan(c, pv, stream)) return e;
   }
-  if (may_prefill && !tc) {
-    static PerContext<int> occ_c;
-    int occ = 0;
+  if (!tc) {
     using G = Fp8Pre<D>;
-    if (!occ_c.get(dev, [](int* o) { return configure(prefill_fp8_kernel<D>, G::SMEM, G::THREADS, o); }, &occ))
-      return KV_INT4_ERR_CUDA;
-    long long grid = (long long)sms * occ;
-    if (grid > L.max_prefill_items) grid = L.max_prefill_items;
-    timing_begin(kTimedPrefill, stream);
-    const int e = launch_pdl(prefill_fp8_kernel<D>, dim3((unsigned)grid), G::THREADS, G::SMEM, stream, 1, c, pv);
-    timing_end(kTimedPrefill, stream);
-    if (e) return e;
+    long long grid = 1;
+    c.tile_tokens = kPrefillRows / c.group;
+    if (may_prefill) {
+      static PerContext<int> occ_c;
+      int occ = 0;
+      if (!occ_c.get(dev, [](int* o) { return configure(prefill_fp8_kernel<D>, G::SMEM, G::THREADS, o); }, &occ))
+        return KV_INT4_ERR_CUDA;
+      grid = (long long)sms * occ;
+    }
+    c.step_blocks = G::NB;
+    c.split_steps = 8;
+    c.split_ctas = (int)grid;
+    if (int e = launch_plan(c, pv, may_prefill, stream)) return e;
+    if (may_prefill) {
+      if (grid > most_items) grid = most_items;
+      timing_begin(kTimedPrefill, stream);
+      const int e = launch_pdl(prefill_fp8_kernel<D>, dim3((unsigned)grid), G::THREADS, G::SMEM, stream, 1, c, pv);
+      timing_end(kTimedPrefill, stream);
+      if (e) return e;
+    }
   }
+  // Whether tiles may be in pieces: a key range of two pieces or more, and fewer
+  // tiles than the schedule leaves whole (sequences decoded here have at most
+  // dcols / group tokens).  The merge then has CTAs for a warp per row, as far as
+  // they start at once when the prefill's last CTAs leave
+  const long long most_decode = any_decode ? (long long)a.num_seqs * (c.dcols / c.group) : 0;
+  const long long tiles = (a.num_q_tokens - most_decode + c.tile_tokens - 1) / c.tile_tokens;
+  const bool may_split = may_prefill && a.max_seq_len > 16ll * c.step_blocks * c.split_steps && tiles <= kSplitTiles &&
+                         tiles * a.num_kv_heads < 8ll * c.split_ctas;
+  auto merge_ctas = [&](long long segs, int warps) {
+    const long long rows = (long long)a.num_q_tokens * a.num_q_heads;
+    const long long want = ((rows < kPieceRows / 2 ? rows : kPieceRows / 2) + warps - 1) / warps;
+    const long long more = want < sms ? want : sms;
+    return may_split && more > segs ? more : segs;
+  };
   if (any_decode) {
     const Fp8DecParams prm{c, pv, dec_grid, 1, may_prefill};
     const int threads = c.hg * 32;
@@ -275,8 +305,15 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
     while (lanes < 16 && lanes < pieces && 2 * lanes * cols <= 32) lanes *= 2;
     if (segs > 0x7fffffff) return KV_INT4_ERR_SIZE;
     timing_begin(kTimedReduce, stream);
-    e = launch_pdl(merge_fp8_kernel<D>, dim3((unsigned)segs), cols * lanes * 32, merge_smem<D>(cols, lanes), stream, 1,
+    e = launch_pdl(may_split ? merge_fp8_kernel<D, true> : merge_fp8_kernel<D, false>,
+                   dim3((unsigned)merge_ctas(segs, cols * lanes)), cols * lanes * 32, merge_smem<D>(cols, lanes), stream, 1,
                    Fp8MergeParams{c, pv, dec_grid, cols, lanes});
+    timing_end(kTimedReduce, stream);
+    if (e) return e;
+  } else if (may_split) {
+    timing_begin(kTimedReduce, stream);
+    const int e = launch_pdl(merge_fp8_kernel<D, true>, dim3((unsigned)merge_ctas(1, 8)), 256, 0, stream, 1,
+                             Fp8MergeParams{c, pv, 0, 8, 1});
     timing_end(kTimedReduce, stream);
     if (e) return e;
   }

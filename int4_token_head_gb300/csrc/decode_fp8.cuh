@@ -619,7 +619,73 @@ __host__ __device__ constexpr int merge_smem(int cols, int lanes) {
   return lanes > 1 ? cols * lanes * (D + 2) * 4 : 0;
 }
 
+// The rows of prefill tiles that were split over their keys, a warp per row:
+// pieces weighted by 2^(m - M), added in their order.
 template <int D>
+__device__ void merge_prefill_pieces(const Common& c, const PlanView& pv, int first_warp, int num_warps) {
+  constexpr int PER = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int n_split = pv.plan[4];
+  int u = first_warp, base = 0;  // this warp's next row; rows before the 32 tiles in hand
+#pragma unroll 1
+  for (int e0 = 0; e0 < n_split; e0 += 32) {
+    int4 t = make_int4(0, 0, 0, 0);  // (sequence, tile, first piece row, pieces)
+    int R = 0, q0 = 0;               // rows per head, the tile's first query token
+    if (e0 + lane < n_split) {
+      t = pv.msplit[e0 + lane];
+      const int qa = c.qsl[t.x], left = c.qsl[t.x + 1] - qa - t.y * c.tile_tokens;
+      R = min(c.tile_tokens, left) * c.group;
+      q0 = qa + t.y * c.tile_tokens;
+    }
+    int incl = R * c.hkv;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const int total = __shfl_sync(0xffffffffu, incl, 31);
+#pragma unroll 1
+    for (; u < base + total; u += num_warps) {
+      const int who = __ffs(__ballot_sync(0xffffffffu, u - base < incl)) - 1;
+      const int rows = __shfl_sync(0xffffffffu, R, who), P = __shfl_sync(0xffffffffu, t.w, who);
+      const int idx = u - base - (__shfl_sync(0xffffffffu, incl, who) - rows * c.hkv);
+      const int h = idx / rows, r = idx - h * rows;
+      const long long at = __shfl_sync(0xffffffffu, t.z, who) + (long long)h * P * rows + r;  // piece k: + k rows
+      const int tok = __shfl_sync(0xffffffffu, q0, who);
+      float M = -INFINITY;
+      for (int k = lane; k < P; k += 32) M = fmaxf(M, pv.piece_ml[2 * (at + (long long)k * rows)]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const float mu = M == -INFINITY ? 0.f : M;
+      float acc[PER], Ls = 0.f;
+#pragma unroll
+      for (int i = 0; i < PER; i++) acc[i] = 0.f;
+#pragma unroll 1
+      for (int k0 = 0; k0 < P; k0 += 32) {
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (k0 + lane < P) ml = *reinterpret_cast<const float2*>(pv.piece_ml + 2 * (at + (long long)(k0 + lane) * rows));
+        const float a = fast_exp2(ml.x - mu);
+#pragma unroll 4
+        for (int k = 0; k < min(32, P - k0); k++) {
+          const float ak = __shfl_sync(0xffffffffu, a, k);
+          const float* o = pv.piece_o + (at + (long long)(k0 + k) * rows) * D;
+#pragma unroll
+          for (int i = 0; i < PER; i++) acc[i] = fmaf(o[lane + 32 * i], ak, acc[i]);
+          Ls = fmaf(__shfl_sync(0xffffffffu, ml.y, k), ak, Ls);
+        }
+      }
+      const float inv = Ls == 0.f ? 0.f : 1.f / Ls;  // no visible key: zeros
+      const int j = (int)c.gdiv.div((uint32_t)r), jj = r - j * c.group;
+      uint16_t* dst = c.out + (long long)(tok + j) * c.out_stride + (long long)(h * c.group + jj) * D;
+#pragma unroll
+      for (int i = 0; i < PER; i++)
+        dst[lane + 32 * i] = (uint16_t)(pack_bf16x2_rn(acc[i] * inv, 0.f) & 0xffffu);
+    }
+    base += total;
+  }
+}
+
+template <int D, bool PIECES>
 __global__ void __launch_bounds__(1024) merge_fp8_kernel(Fp8MergeParams prm) {
   const Common& c = prm.c;
   const PlanView& pv = prm.pv;
@@ -631,6 +697,11 @@ __global__ void __launch_bounds__(1024) merge_fp8_kernel(Fp8MergeParams prm) {
   const int col = warp % prm.cols, pl = warp / prm.cols;
   const int n_dseq = pv.plan[0];
   const int seg = blockIdx.x;
+  if constexpr (PIECES) {  // every CTA's warps take rows in turn, before its segment
+    const int warps = blockDim.x >> 5;
+    const long long first = (long long)seg * warps + warp;
+    if (first < kPieceRows) merge_prefill_pieces<D>(c, pv, (int)first, (int)min((long long)gridDim.x * warps, 1ll << 30));
+  }
   if (seg >= n_dseq * c.hkv) return;
   const int i = seg / c.hkv, h = seg - i * c.hkv;
   const int4 di = pv.dseq[i];  // (sequence, seq_len, first query token, q_len)

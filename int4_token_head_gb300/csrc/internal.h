@@ -233,6 +233,30 @@ constexpr int kPrefillRows = 64;    // query rows (q token x q head) per prefill
 bool workspace_layout(int num_seqs, int num_q_tokens, int num_q_heads, int num_kv_heads,
                       int head_size, WorkspaceLayout* out);
 
+// The FP8 attention's layout of the same workspace.
+struct WorkspaceLayoutFp8 {
+  size_t plan;          // int32 counters
+  size_t dseq;          // int4 [num_seqs] decode sequences
+  size_t dprefix;       // int64 [num_seqs + 1] position prefix over decode sequences
+  size_t ptab;          // int2 [num_seqs + 1] prefill sequence table
+  size_t plist;         // PrefillPiece [max_pairs + kMaxPieces] prefill tiles and pieces of tiles, longest first
+  size_t msplit;        // int4 [kMaxPieces / 2] tiles in pieces
+  size_t direct_o;      // f32 [num_seqs][Hkv][kDecodeColsFp8][d]
+  size_t direct_ml;     // f32 [num_seqs][Hkv][kDecodeColsFp8][2]
+  size_t warp_o;        // f32 [kMaxDecodeWarps][8][d], or half as many slots of 16 columns
+  size_t warp_ml;       // f32 [kMaxDecodeWarps][8][2]
+  size_t piece_o;       // f32 [kPieceRows][d] rows of pieces
+  size_t piece_ml;      // f32 [kPieceRows][2]
+  size_t total;
+  int64_t max_pairs;    // prefill (sequence, tile) pairs
+};
+constexpr int kDecodeColsFp8 = 16;  // most query columns per FP8 decode work unit
+constexpr int kMaxPieces = 2048;    // pieces of split prefill tiles, and their rows over all kv heads
+constexpr int kPieceRows = 40960;   // (a piece of a full 256-row tile for each of 160 CTAs)
+
+bool workspace_layout_fp8(int num_seqs, int num_q_tokens, int num_q_heads, int num_kv_heads,
+                          int head_size, WorkspaceLayoutFp8* out);
+
 int launch_attention(const AttnArgs& a, cudaStream_t stream);
 // FP8 block-scaled cache (attention_fp8.cu): E4M3 codes of d bytes per head
 // vector, one scale per (block, head)

@@ -17,7 +17,7 @@ struct Fp8Pre {
   static constexpr int TILE = KEYS * ROW;
   static constexpr int STAGE = 2 * TILE + 32;  // K rows, V rows, scales [K/V][NB], block flags [NB]
   static constexpr int QSTRIDE = D + 8;        // halves per Q' row
-  static constexpr int SMEM = STAGES * STAGE + ROWS * QSTRIDE * 2 + 32;
+  static constexpr int SMEM = STAGES * STAGE + ROWS * QSTRIDE * 2 + 32;  // and the item
 };
 
 template <int D>
@@ -36,19 +36,19 @@ __global__ void __launch_bounds__(Fp8Pre<D>::THREADS) prefill_fp8_kernel(Common 
 #pragma unroll 1
   while (true) {
     if (tid == 0) {
-      const int4 it = prefill_item(c, pv, atomicAdd(&pv.plan[2], 1), n_items);
-      sitem[0] = it.x; sitem[1] = it.y; sitem[2] = it.z; sitem[3] = it.w;
+      const PrefillItem it = prefill_piece_item(c, pv, atomicAdd(&pv.plan[2], 1), n_items);
+      sitem[0] = it.seq; sitem[1] = it.h; sitem[2] = it.tile;
+      sitem[3] = it.kb0; sitem[4] = it.nkb; sitem[5] = it.row;
     }
     __syncthreads();
-    const int4 item = make_int4(sitem[0], sitem[1], sitem[2], sitem[3]);
+    const PrefillItem item{sitem[0], sitem[1], sitem[2], sitem[3], sitem[4], sitem[5]};
     __syncthreads();
-    if (item.x < 0) break;
-    const int seq = item.x, h = item.y, tile = item.z, nkb = item.w;
+    if (item.seq < 0) break;
+    const int seq = item.seq, h = item.h, tile = item.tile, kb0 = item.kb0, nkb = item.nkb;
     const int q0 = c.qsl[seq], ql = c.qsl[seq + 1] - q0;
     const int L = c.seq_lens[seq], ctx = L - ql;
     const int tok0 = tile * c.tile_tokens;
     const int nrows = min(c.tile_tokens, ql - tok0) * c.group;
-    const int kb0 = window_lo(c, ctx + tok0) >> 4;  // blocks before the earliest row's window are skipped
     const int nsteps = (nkb - kb0 + G::NB - 1) / G::NB;
 
     auto issue = [&](int st, int stage) {
@@ -232,6 +232,22 @@ __global__ void __launch_bounds__(Fp8Pre<D>::THREADS) prefill_fp8_kernel(Common 
     for (int o = 1; o < 4; o <<= 1) {
       lr0 += __shfl_xor_sync(0xffffffffu, lr0, o);
       lr1 += __shfl_xor_sync(0xffffffffu, lr1, o);
+    }
+    if (item.row >= 0) {
+      // a piece: O, the running maximum and the sum
+      auto store_piece = [&](int r, int e, float m, float l) {
+        if (r >= nrows) return;
+        const long long at = item.row + r;
+#pragma unroll
+        for (int ch = 0; ch < D / 16; ch++)
+          *reinterpret_cast<float4*>(pv.piece_o + at * D + 16 * ch + 4 * cq) =
+              make_float4(oacc[2 * ch][e], oacc[2 * ch + 1][e], oacc[2 * ch][e + 1], oacc[2 * ch + 1][e + 1]);
+        if (cq == 0) *reinterpret_cast<float2*>(pv.piece_ml + 2 * at) = make_float2(m, l);
+      };
+      store_piece(r0, 0, mr0, lr0);
+      store_piece(r1, 2, mr1, lr1);
+      __syncthreads();  // the next item overwrites the stages
+      continue;
     }
     const float inv0 = lr0 == 0.f ? 0.f : 1.f / lr0, inv1 = lr1 == 0.f ? 0.f : 1.f / lr1;
     // dimensions 16 ch + 4 cq .. + 3: even ones in tile 2 ch, odd ones in 2 ch + 1

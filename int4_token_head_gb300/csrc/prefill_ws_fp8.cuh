@@ -70,7 +70,7 @@ struct Fp8Ws {
   static constexpr int NBARS = 23;
   static constexpr int S_COLS = NK, O_COL = 2 * NK;  // TMEM: S_h at h NK, O_h at 2 NK + h D
   static constexpr int XCH = 2 * ROWS * 4;  // a float per row and key half: maxima, sums
-  static constexpr int SMEM = QBYTES + 4 * KVBYTES + 2 * STG + NRING * RING + NBARS * 8 + 48 + XCH;
+  static constexpr int SMEM = QBYTES + 4 * KVBYTES + 2 * STG + NRING * RING + NBARS * 8 + 64 + XCH;
   static constexpr int THREADS = 28 * 32;  // seven warpgroups; the last two warps only give up registers
   static constexpr int CV_WARPS = 4;       // convert warps for K, and for V
   // byte offset of chunk g of key k in a stage
@@ -220,10 +220,10 @@ __global__ void __launch_bounds__(28 * 32, 1)
   uint8_t* const stg = sV + 2 * G::KVBYTES;   // staged K codes, V codes
   uint8_t* const ring = stg + 2 * G::STG;
   uint64_t* const bars = reinterpret_cast<uint64_t*>(ring + G::NRING * G::RING);
-  int* const sitem = reinterpret_cast<int*>(bars + G::NBARS);  // item ring [2][4], abort flag
-  uint32_t* const tslot = reinterpret_cast<uint32_t*>(sitem + 10);
-  volatile int* const abort_flag = sitem + 8;
-  float* const sxch = reinterpret_cast<float*>(sitem + 12);  // [key half][256 rows]
+  int* const sitem = reinterpret_cast<int*>(bars + G::NBARS);  // item ring [2][6], abort flag
+  uint32_t* const tslot = reinterpret_cast<uint32_t*>(sitem + 14);
+  volatile int* const abort_flag = sitem + 12;
+  float* const sxch = reinterpret_cast<float*>(sitem + 16);  // [key half][256 rows]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   enum {
@@ -265,16 +265,19 @@ __global__ void __launch_bounds__(28 * 32, 1)
   tc_fence_after();
   const uint32_t tmem = *tslot;
   const int n_items = pv.plan[1];
-  auto item_at = [&](int e) { return make_int4(sitem[4 * e], sitem[4 * e + 1], sitem[4 * e + 2], sitem[4 * e + 3]); };
+  auto item_at = [&](int e) {
+    const int* s = sitem + 6 * e;
+    return PrefillItem{s[0], s[1], s[2], s[3], s[4], s[5]};
+  };
   // a consumer's wait for ring entry e, warp-uniform
-  auto take_item = [&](int e, uint32_t& ph, int4& item) {
+  auto take_item = [&](int e, uint32_t& ph, PrefillItem& item) {
     const bool ok = __all_sync(0xffffffffu, fp8_wait(bar(IFULL + e), (ph >> e) & 1, abort_flag, c.status));
     ph ^= 1u << e;
     if (!ok) return false;
     item = item_at(e);
     __syncwarp();
     if (lane == 0) fp8_arrive(bar(IFREE + e));
-    return item.x >= 0;
+    return item.seq >= 0;
   };
   // registers: 72 a thread at launch (896 threads, 64,512); the softmax
   // warpgroups take 80, the others 56 (512 x 80 + 384 x 56 = 62,464)
@@ -305,15 +308,14 @@ __global__ void __launch_bounds__(28 * 32, 1)
     for (int itc = 0;; itc++) {
       // both warps of a row go on or neither (after a time-out one may get an
       // item that the other does not)
-      int4 item;
+      PrefillItem item;
       const bool taken = take_item(itc & 1, ph_ifull, item);
       if (pair_any(!taken)) break;
-      const int seq = item.x, h = item.y, tile = item.z, nkb = item.w;
+      const int seq = item.seq, h = item.h, tile = item.tile, kb0 = item.kb0, nkb = item.nkb;
       const int q0 = c.qsl[seq], ql = c.qsl[seq + 1] - q0;
       const int L = c.seq_lens[seq], ctx = L - ql;
       const int tok0 = tile * c.tile_tokens;
       const bool rok = r < min(c.tile_tokens, ql - tok0) * c.group;
-      const int kb0 = window_lo(c, ctx + tok0) >> 4;
       const int nsteps = (nkb - kb0 + NB - 1) / NB;
       const int qp = ctx + tok0 + (rok ? j : 0);
       // the row sees positions [lo, lim), counted from this thread's first key
@@ -433,6 +435,24 @@ __global__ void __launch_bounds__(28 * 32, 1)
         ph_odone ^= 1;
         tc_fence_after();
       }
+      constexpr int UNITS = D / 32, FIRST = (UNITS + 1) / 2;  // of 32 columns; the first key half's
+      if (item.row >= 0) {
+        // a piece: O (V's factor 2^-8 undone), the reference and the sum
+        const long long at = item.row + r;
+#pragma unroll 1
+        for (int u = kh ? 2 * FIRST : 0; u < (kh ? 2 * UNITS : 2 * FIRST); u++) {
+          uint32_t o[16];
+          tmem_ld16(tO + 16 * u, o);
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            if (rok)
+              *reinterpret_cast<float4*>(pv.piece_o + at * D + 16 * u + i) =
+                  make_float4(256.f * __uint_as_float(o[i]), 256.f * __uint_as_float(o[i + 1]),
+                              256.f * __uint_as_float(o[i + 2]), 256.f * __uint_as_float(o[i + 3]));
+        }
+        if (rok && kh == 0) *reinterpret_cast<float2*>(pv.piece_ml + 2 * at) = make_float2(m_ref, l);
+        continue;
+      }
       // a row that saw no usable key is zeros: O is 0 then, but for an item
       // without steps, whose O is not read (V's factor 2^-8 is undone here)
       const float inv = l == 0.f ? 0.f : 256.f / l;
@@ -440,7 +460,6 @@ __global__ void __launch_bounds__(28 * 32, 1)
       uint16_t* const orow = c.out + (long long)(q0 + tok0 + (rok ? j : 0)) * c.out_stride +
                              (long long)(h * c.group + (rok ? r - j * c.group : 0)) * D;
       const bool al32 = ((reinterpret_cast<uintptr_t>(c.out) | (uintptr_t)(c.out_stride * 2) | (uintptr_t)(D * 2)) & 31) == 0;
-      constexpr int UNITS = D / 32, FIRST = (UNITS + 1) / 2;  // of 32 columns; the first key half's
 #pragma unroll 1
       for (int u = kh ? FIRST : 0; u < (kh ? UNITS : FIRST); u++) {
         uint32_t w[16];
@@ -501,13 +520,10 @@ __global__ void __launch_bounds__(28 * 32, 1)
         int n = 0, freed = 0;
 #pragma unroll 1
         for (int itc = 0;; itc++) {
-          int4 item;
+          PrefillItem item;
           if (!take_item(itc & 1, ph_ifull, item)) break;
-          const int seq = item.x, nkb = item.w;
-          const int L = c.seq_lens[seq], ctx = L - (c.qsl[seq + 1] - c.qsl[seq]);
-          const int kb0 = window_lo(c, ctx + item.z * c.tile_tokens) >> 4;
-          const int nsteps = (nkb - kb0 + NB - 1) / NB;
-          int keys = L - kb0 * 16;  // rows of the step that hold keys
+          const int nsteps = (item.nkb - item.kb0 + NB - 1) / NB;
+          int keys = c.seq_lens[item.seq] - item.kb0 * 16;  // rows of the step that hold keys
 #pragma unroll 1
           for (int st = 0; st < nsteps; st++, n++, keys -= NK) {
             uint8_t* const dst = tile + (n & 1) * G::KVBYTES;
@@ -580,20 +596,20 @@ __global__ void __launch_bounds__(28 * 32, 1)
         }
         int itn = n_items;
         if (lane == 0 && !*abort_flag) itn = atomicAdd(&pv.plan[2], 1);
-        const int4 item = prefill_item(c, pv, __shfl_sync(0xffffffffu, itn, 0), n_items);
+        const PrefillItem item = prefill_piece_item(c, pv, __shfl_sync(0xffffffffu, itn, 0), n_items);
         if (lane == 0) {
-          sitem[4 * e] = item.x;
-          sitem[4 * e + 1] = item.y;
-          sitem[4 * e + 2] = item.z;
-          sitem[4 * e + 3] = item.w;
+          int* s = sitem + 6 * e;
+          s[0] = item.seq;
+          s[1] = item.h;
+          s[2] = item.tile;
+          s[3] = item.kb0;
+          s[4] = item.nkb;
+          s[5] = item.row;
           fp8_arrive(bar(IFULL + e));
         }
-        if (item.x < 0) break;
-        const int seq = item.x, h = item.y, tile = item.z, nkb = item.w;
-        const int q0 = c.qsl[seq], ql = c.qsl[seq + 1] - q0;
-        const int L = c.seq_lens[seq], ctx = L - ql;
-        const int tok0 = tile * c.tile_tokens;
-        const int kb0 = window_lo(c, ctx + tok0) >> 4;
+        if (item.seq < 0) break;
+        const int seq = item.seq, h = item.h, kb0 = item.kb0, nkb = item.nkb;
+        const int q0 = c.qsl[seq], tok0 = item.tile * c.tile_tokens;
         const int nsteps = (nkb - kb0 + NB - 1) / NB;
         // lane b < NB holds block b of a step: its row in the caches (behind
         // their end for a block that the table does not name) and its scales
@@ -684,18 +700,14 @@ __global__ void __launch_bounds__(28 * 32, 1)
 #pragma unroll 1
       for (int itc = 0;; itc++) {
         wait(IFULL + (itc & 1), (itc >> 1) & 1);
-        const int4 item = item_at(itc & 1);
+        const PrefillItem item = item_at(itc & 1);
         __syncwarp();
         if (lane == 0) fp8_arrive(bar(IFREE + (itc & 1)));
         __syncwarp();
         // the step count through a warp reduction, whose result is uniform;
         // none once a wait has run out
         int steps = -1;
-        if (item.x >= 0 && !*abort_flag) {
-          const int ql = c.qsl[item.x + 1] - c.qsl[item.x];
-          const int kb0 = window_lo(c, c.seq_lens[item.x] - ql + item.z * c.tile_tokens) >> 4;
-          steps = (item.w - kb0 + NB - 1) / NB;
-        }
+        if (item.seq >= 0 && !*abort_flag) steps = (item.nkb - item.kb0 + NB - 1) / NB;
         const int nsteps = __reduce_min_sync(0xffffffffu, steps);
         if (nsteps < 0) break;
         if (nsteps > 0) {

@@ -14,6 +14,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 struct PlanView {
   int32_t* plan;      // [0] n_dseq, [1] n_prefill_items, [2] prefill work counter, [3] n_pseq
+  int4* msplit;       // FP8: tiles in pieces: (sequence, tile, first piece row, pieces); plan[4] of them
+  struct PrefillPiece* pieces;  // FP8: prefill tiles and pieces of tiles, longest first (in place of plist)
+  float* piece_o;
+  float* piece_ml;
   int4* dseq;         // decode sequences in order: (sequence id, seq_len, first query token, q_len)
   int64_t* dprefix;
   int2* ptab;         // prefill sequences in order: (seq id, index of its first item); [n_pseq].y = items
@@ -25,9 +29,39 @@ struct PlanView {
   float* warp_ml;
 };
 
+// A prefill tile of a sequence, or a piece of its keys: entry i of the list
+// gives items i Hkv .. i Hkv + Hkv - 1.  Piece k of kv head h of a tile in P
+// pieces of R query rows leaves unnormalised rows row + h P R .. + R - 1.
+struct PrefillPiece {
+  int seq, tile;
+  int kb0, nkb;     // blocks [kb0, nkb) of the sequence
+  int row;          // first row of head 0, -1 if the tile is whole
+  int head_rows;    // P R
+  int unused[2];
+};
+static_assert(sizeof(PrefillPiece) == 32, "read as two int4");
+
+static PlanView plan_view_fp8(void* ws, const WorkspaceLayoutFp8& L) {
+  uint8_t* b = static_cast<uint8_t*>(ws);
+  PlanView v{};
+  v.plan = reinterpret_cast<int32_t*>(b + L.plan);
+  v.dseq = reinterpret_cast<int4*>(b + L.dseq);
+  v.dprefix = reinterpret_cast<int64_t*>(b + L.dprefix);
+  v.ptab = reinterpret_cast<int2*>(b + L.ptab);
+  v.pieces = reinterpret_cast<PrefillPiece*>(b + L.plist);
+  v.msplit = reinterpret_cast<int4*>(b + L.msplit);
+  v.direct_o = reinterpret_cast<float*>(b + L.direct_o);
+  v.direct_ml = reinterpret_cast<float*>(b + L.direct_ml);
+  v.warp_o = reinterpret_cast<float*>(b + L.warp_o);
+  v.warp_ml = reinterpret_cast<float*>(b + L.warp_ml);
+  v.piece_o = reinterpret_cast<float*>(b + L.piece_o);
+  v.piece_ml = reinterpret_cast<float*>(b + L.piece_ml);
+  return v;
+}
+
 static PlanView plan_view(void* ws, const WorkspaceLayout& L) {
   uint8_t* b = static_cast<uint8_t*>(ws);
-  PlanView v;
+  PlanView v{};
   v.plan = reinterpret_cast<int32_t*>(b + L.plan);
   v.dseq = reinterpret_cast<int4*>(b + L.dseq);
   v.dprefix = reinterpret_cast<int64_t*>(b + L.dprefix);
@@ -80,6 +114,9 @@ struct Common {
   int np;           // decode: 16-key blocks per schedule position (1, 2 or 4)
   int dcols;        // decode: query columns per block (8 / np); longer queries go to prefill
   long long max_items;  // capacity of the prefill item list
+  int step_blocks;      // FP8 prefill: cache blocks per step
+  int split_steps;      // FP8 prefill: least steps of a piece
+  int split_ctas;       // FP8 prefill: CTAs that run at once
 };
 
 // floor(n / d) for 0 <= n, 0 < d: one 32-bit division when both fit (the
@@ -114,6 +151,20 @@ __device__ __forceinline__ int4 prefill_item(const Common& c, const PlanView& pv
   const int qa = c.qsl[st.x], qn = c.qsl[st.x + 1] - qa;
   const int keys = prefill_tile_keys(c, c.seq_lens[st.x], qn, st.y);
   return make_int4(st.x, itn - pi * c.hkv, st.y, (keys + 15) / 16);
+}
+
+// item itn of the FP8 prefill: a tile or a piece of one, for one kv head
+struct PrefillItem {
+  int seq, h, tile;  // seq -1: past the last item
+  int kb0, nkb;      // blocks [kb0, nkb)
+  int row;           // first piece row, -1 if the tile is whole
+};
+__device__ __forceinline__ PrefillItem prefill_piece_item(const Common& c, const PlanView& pv, int itn, int n_items) {
+  if (itn >= n_items) return PrefillItem{-1, 0, 0, 0, 0, -1};
+  const int pi = itn / c.hkv, h = itn - pi * c.hkv;
+  const int4 a = reinterpret_cast<const int4*>(pv.pieces + pi)[0];
+  const int2 b = reinterpret_cast<const int2*>(pv.pieces + pi)[2];
+  return PrefillItem{a.x, h, a.y, a.z, a.w, b.x < 0 ? -1 : b.x + h * b.y};
 }
 
 constexpr int kPrepThreads = 256;  // threads of the CTA that builds the schedule
@@ -156,11 +207,187 @@ __device__ __forceinline__ bool schedule_seq_ok(const Common& c, int q0, int ql,
            ql > c.max_qlen || (long long)L > (long long)c.max_blocks * 16);
 }
 
-// The schedule, by one CTA of kPrepThreads threads.
-template <bool ANY_LEN>
+// The FP8 prefill's list of tiles, longest first, with tiles split over their
+// keys where that shortens the launch (few rows against a long cache: chunked
+// prompts, cross attention, queries of a few tokens; 2 x 256 tokens against
+// 16384 keys, 32/8 heads of 128: 163 us, whole tiles 267).  A tile of more than
+// S steps becomes ceil(steps / S) equal pieces: S is a CTA's share of all steps,
+// at least c.split_steps (a piece costs about two steps on top of its own, and
+// its rows are merged), twice that where decodes run beside on the SMs that
+// whole tiles leave (4 prompts of up to 400 tokens beside 28 decodes: 45.6 us,
+// in pieces 51.2).  If there are fewer tiles than CTAs, an S up to twice as
+// large whose pieces all run at once is taken; without one, only tiles of more
+// than two shares are worth it.  Everything follows from the call's lengths
+// alone, so results do not depend on the order of arrival.  Batches of more
+// than kSplitTiles tiles, or of eight items per CTA, which the order by length
+// balances, keep their tiles whole.  `seqs`: the prefill sequences in shared
+// memory, if the batch fits there.  The code is kept short (one loop for both
+// passes): a lone CTA that runs it once waits for its instructions most of the
+// time (with the loops inlined twice 2 to 3 us more per call).
+constexpr int kSplitTiles = 1024;
+template <int BUCKETS>
+__device__ void build_pieces(const Common& c, const PlanView& pv, int n_pseq, int n_tiles, bool with_decode,
+                             const int4* seqs, int* hist, int32_t* s_i32) {
+  __shared__ int4 tiles[kSplitTiles];  // (sequence, tile, first block, end block)
+  __shared__ short tile_rows[kSplitTiles];
+  __shared__ int2 s_cand[kPrepThreads / 32];
+  __shared__ int next_row, next_split;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // tiles base .. base + kSplitTiles - 1.  A few long sequences: a warp's lanes
+  // share a sequence's tiles; many: a thread each
+  auto fill = [&](int base) {
+    const int lps = n_pseq >= kPrepThreads / 4 ? 1 : 32;
+#pragma unroll 1
+    for (int p = threadIdx.x / lps; p < n_pseq; p += kPrepThreads / lps) {
+      int4 x;  // (sequence, query tokens, keys, index of its first tile)
+      if (seqs) {
+        x = seqs[p];
+      } else {
+        const int2 pt = pv.ptab[p];
+        x = make_int4(pt.x, c.qsl[pt.x + 1] - c.qsl[pt.x], c.seq_lens[pt.x], pt.y / c.hkv);
+      }
+      const int nt = (x.y + c.tile_tokens - 1) / c.tile_tokens;
+#pragma unroll 1
+      for (int t = threadIdx.x % lps; t < nt; t += lps) {
+        const int i = x.w + t - base, tok = t * c.tile_tokens;
+        if (i < 0 || i >= kSplitTiles) continue;
+        tiles[i] = make_int4(x.x, t, window_lo(c, x.z - x.y + tok) >> 4, (prefill_tile_keys(c, x.z, x.y, t) + 15) / 16);
+        tile_rows[i] = (short)(min(c.tile_tokens, x.y - tok) * c.group);
+      }
+    }
+  };
+  auto steps_of = [&](const int4& x) { return max(0, (x.w - x.z + c.step_blocks - 1) / c.step_blocks); };
+  if (threadIdx.x == 0) next_row = next_split = 0;
+  for (int i = threadIdx.x; i < BUCKETS; i += kPrepThreads) hist[i] = 0;
+  __syncthreads();  // the sequence table
+  fill(0);
+  __syncthreads();
+  int S = INT_MAX;
+  if (n_tiles <= kSplitTiles && (long long)n_tiles * c.hkv < 8ll * c.split_ctas) {
+    // every warp takes the sum, then one candidate for S: S0 to 2 S0, and 4 S0
+    long long sum = 0;
+    int longest = 0;
+#pragma unroll 1
+    for (int i = lane; i < n_tiles; i += 32) {
+      const int n = steps_of(tiles[i]);
+      sum += n;
+      longest = max(longest, n);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    const long long share = div_nn(sum * c.hkv + c.split_ctas - 1, c.split_ctas);
+    const long long S0 = max(share, (long long)c.split_steps << (with_decode ? 1 : 0));
+    const bool one_wave = (long long)n_tiles * c.hkv < c.split_ctas;
+    if (longest > (one_wave ? S0 : 2 * S0)) {  // else every tile stays whole
+      constexpr int W = kPrepThreads / 32;
+      const int cand = (int)min(warp == W - 1 ? 4 * S0 : S0 + (S0 * warp + W - 3) / (W - 2), (long long)INT_MAX);
+      long long p = 0, r = 0, all = 0;  // pieces of split tiles, their rows, all entries
+#pragma unroll 1
+      for (int i = lane; i < n_tiles; i += 32) {
+        const int n = steps_of(tiles[i]), P = n > cand ? (n - 1) / cand + 1 : 1;
+        all += P;
+        if (P > 1) {
+          p += P;
+          r += (long long)P * tile_rows[i] * c.hkv;
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        p += __shfl_xor_sync(0xffffffffu, p, o);
+        r += __shfl_xor_sync(0xffffffffu, r, o);
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+      }
+      // 2: fits the workspace and all of it runs at once; 1: fits
+      if (lane == 0)
+        s_cand[warp] = make_int2(cand, p > kMaxPieces || r > kPieceRows ? 0
+                                 : one_wave && all * c.hkv <= c.split_ctas ? 2 : longest > 2 * S0);
+      __syncthreads();
+      int best = 0;
+      for (int i = 0; i < W; i++)
+        if (s_cand[i].y > best) {
+          best = s_cand[i].y;
+          S = s_cand[i].x;
+        }
+    }
+  }
+
+  // counting sort by blocks, descending, within a bucket in arbitrary order
+  // (every item computes the same rows either way): pass 0 counts, pass 1
+  // writes the list.  Few tiles may have many pieces: a warp each, whose lanes
+  // take the pieces
+  int sh = 0;
+  while ((((long long)c.max_blocks + 1) >> sh) >= BUCKETS) sh++;
+  const int lpp = n_tiles <= kPrepThreads / 4 ? 32 : 1;
+  int total = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; pass++) {
+#pragma unroll 1
+    for (int base = 0; base < n_tiles; base += kSplitTiles) {
+      if (n_tiles > kSplitTiles) {
+        __syncthreads();
+        fill(base);
+        __syncthreads();
+      }
+      const int count = min(n_tiles - base, kSplitTiles);
+#pragma unroll 1
+      for (int i = threadIdx.x / lpp; i < count; i += kPrepThreads / lpp) {
+        const int4 x = tiles[i];
+        const int rows = tile_rows[i], n = steps_of(x), P = n > S ? (n - 1) / S + 1 : 1;
+        int row = 0;
+        if (pass && P > 1) {
+          if (threadIdx.x % lpp == 0) {
+            row = atomicAdd(&next_row, P * rows * c.hkv);
+            pv.msplit[atomicAdd(&next_split, 1)] = make_int4(x.x, x.y, row, P);
+          }
+          if (lpp > 1) row = __shfl_sync(0xffffffffu, row, 0);
+        }
+        const int each = n / P, more = n - each * P;  // the first `more` pieces have a step more
+#pragma unroll 1
+        for (int k = threadIdx.x % lpp; k < P; k += lpp) {
+          const int lo = x.z + c.step_blocks * (k * each + min(k, more));
+          const int hi = k + 1 < P ? lo + c.step_blocks * (each + (k < more)) : x.w;
+          const int at = atomicAdd(&hist[BUCKETS - 1 - min(BUCKETS - 1, max(0, hi - lo) >> sh)], 1);
+          if (pass) {
+            int4* dst = reinterpret_cast<int4*>(pv.pieces + at);
+            dst[0] = make_int4(x.x, x.y, lo, hi);
+            dst[1] = make_int4(P > 1 ? row + k * rows : -1, P * rows, 0, 0);
+          }
+        }
+      }
+    }
+    __syncthreads();
+    if (pass == 0) {
+      // exclusive prefix over the buckets: thread j owns buckets [8j, 8j + 8)
+      constexpr int PER = BUCKETS / kPrepThreads;
+      int mine = 0;
+#pragma unroll
+      for (int i = 0; i < PER; i++) mine += hist[threadIdx.x * PER + i];
+      int run = block_exclusive_scan<int>(mine, &total, s_i32);
+#pragma unroll
+      for (int i = 0; i < PER; i++) {
+        const int hb = hist[threadIdx.x * PER + i];
+        hist[threadIdx.x * PER + i] = run;
+        run += hb;
+      }
+      __syncthreads();
+    }
+  }
+  if (threadIdx.x == 0) {
+    pv.plan[1] = total * c.hkv;
+    pv.plan[4] = next_split;
+  }
+}
+
+// The schedule, by one CTA of kPrepThreads threads.  PREFILL false: no sequence
+// of the call can be a prefill (code that is not there is not fetched either: a
+// lone CTA runs at the pace of its instruction fetches).
+template <bool ANY_LEN, bool PREFILL = true>
 __device__ void build_schedule(const Common& c, const PlanView& pv) {
   __shared__ int32_t s_i32[kPrepThreads / 32];
   __shared__ long long s_i64[kPrepThreads / 32];
+  __shared__ long long s_i64t[ANY_LEN ? kPrepThreads / 32 : 1];
+  __shared__ int4 seqs[ANY_LEN && PREFILL ? kPrepThreads : 1];
   int n_dseq = 0, n_pseq = 0;
   long long dpre = 0, n_items = 0;
   for (int base = 0; base < c.num_seqs; base += kPrepThreads) {
@@ -178,19 +405,65 @@ __device__ void build_schedule(const Common& c, const PlanView& pv) {
         if (kind == 2) ntiles = (ql + c.tile_tokens - 1) / c.tile_tokens;
       }
     }
-    int tot_a, tot_p;
-    long long tot_b, tot_c;
-    const int ex_a = block_exclusive_scan<int>(kind == 1, &tot_a, s_i32);
+    int tot_a, tot_p = 0, ex_a, ex_p = 0;
+    long long tot_b, tot_c = 0, ex_b, ex_c = 0;
     const int npos = kind == 1 ? (nblk - first_block(c, L, ql) + c.np - 1) / c.np : 0;
-    const long long ex_b = block_exclusive_scan<long long>(npos, &tot_b, s_i64);
-    const int ex_p = block_exclusive_scan<int>(kind == 2, &tot_p, s_i32);
-    const long long ex_c = block_exclusive_scan<long long>((long long)ntiles * c.hkv, &tot_c, s_i64);
+    if constexpr (ANY_LEN) {
+      // the four sums in one pass with one barrier, counts in one word
+      const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+      int n = (kind == 1) | (kind == 2) << 16;
+      long long b = npos, t = (long long)ntiles * c.hkv;
+      const int n_in = n;
+      const long long b_in = b, t_in = t;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int yn = __shfl_up_sync(0xffffffffu, n, o);
+        const long long yb = __shfl_up_sync(0xffffffffu, b, o);
+        const long long yt = PREFILL ? __shfl_up_sync(0xffffffffu, t, o) : 0;
+        if (lane >= o) {
+          n += yn;
+          b += yb;
+          t += yt;
+        }
+      }
+      __syncthreads();  // the last round's sums have been read
+      if (lane == 31) {
+        s_i32[warp] = n;
+        s_i64[warp] = b;
+        s_i64t[warp] = t;
+      }
+      __syncthreads();
+      int en = n - n_in, tn = 0;
+      ex_b = b - b_in;
+      ex_c = t - t_in;
+      tot_b = 0;
+      for (int w = 0; w < kPrepThreads / 32; w++) {
+        if (w == warp) {
+          en += tn;
+          ex_b += tot_b;
+          ex_c += tot_c;
+        }
+        tn += s_i32[w];
+        tot_b += s_i64[w];
+        tot_c += s_i64t[w];
+      }
+      ex_a = en & 0xffff;
+      ex_p = en >> 16;
+      tot_a = tn & 0xffff;
+      tot_p = tn >> 16;
+    } else {
+      ex_a = block_exclusive_scan<int>(kind == 1, &tot_a, s_i32);
+      ex_b = block_exclusive_scan<long long>(npos, &tot_b, s_i64);
+      ex_p = block_exclusive_scan<int>(kind == 2, &tot_p, s_i32);
+      ex_c = block_exclusive_scan<long long>((long long)ntiles * c.hkv, &tot_c, s_i64);
+    }
     if (kind == 1) {
       pv.dseq[n_dseq + ex_a] = make_int4(s, L, q0, ql);
       pv.dprefix[n_dseq + ex_a] = dpre + ex_b;
-    } else if (kind == 2) {
+    } else if (PREFILL && kind == 2) {
       // the prefill kernel expands (tile, kv head) items from this table
       pv.ptab[n_pseq + ex_p] = make_int2(s, (int)min(n_items + ex_c, (long long)INT_MAX));
+      if (ANY_LEN && base == 0) seqs[ex_p] = make_int4(s, ql, L, (int)min(ex_c / c.hkv, (long long)INT_MAX));
     }
     n_dseq += tot_a;
     dpre += tot_b;
@@ -200,6 +473,7 @@ __device__ void build_schedule(const Common& c, const PlanView& pv) {
   if (threadIdx.x == 0) {
     pv.dprefix[n_dseq] = dpre;
     pv.plan[0] = n_dseq;
+    if constexpr (!PREFILL) return;
     // more items than the workspace was sized for only happens with
     // inconsistent query_start_loc: the prefill part is dropped and flagged
     const bool over = n_items > c.max_items || n_items > INT_MAX;
@@ -208,13 +482,21 @@ __device__ void build_schedule(const Common& c, const PlanView& pv) {
     pv.plan[1] = over ? 0 : (int)n_items;
     pv.plan[2] = 0;
     pv.plan[3] = n_pseq;
+    if (ANY_LEN) pv.plan[4] = 0;
   }
+  if constexpr (!PREFILL) return;
   // the prefill (sequence, tile) pairs, longest first: a counting sort over
   // buckets of 16-key blocks (descending), so that the longest items start
   // first and the shortest fill the end of the launch (within a bucket the
   // order is arbitrary; every item computes the same rows either way)
   constexpr int kBuckets = 2048;
   __shared__ int hist[kBuckets];
+  if constexpr (ANY_LEN) {
+    if (n_pseq > 0 && n_items <= c.max_items && n_items <= INT_MAX)
+      build_pieces<kBuckets>(c, pv, n_pseq, (int)(n_items / c.hkv), n_dseq > 0,
+                             c.num_seqs <= kPrepThreads ? seqs : nullptr, hist, s_i32);
+    return;
+  }
   if (n_pseq > 0 && n_items <= c.max_items && n_items <= INT_MAX) {
     int sh = 0;
     while ((((long long)c.max_blocks + 1) >> sh) >= kBuckets) sh++;

@@ -332,6 +332,36 @@ def test_prefill_many_tiles_per_cta(d):
 
 
 @pytest.mark.parametrize("d", HEADS)
+@pytest.mark.parametrize("hq,hkv,seqs", [
+    (16, 1, [(3, 5000)]),                                              # one tile, every piece of one step or two
+    (24, 2, [(7, 3000), (1, 9), (2, 2500), (30, 2100), (0, 5), (9, 9)]),  # pieces beside whole tiles and decodes
+    (8, 8, [(200, 1999), (260, 2200)]),                                # several tiles a sequence, rows of unlike limits
+])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 700)])
+def test_prefill_split_over_keys(d, hq, hkv, seqs, causal, window):
+    _check(seqs, hq, hkv, d, causal=causal, window=window, seed=d + hq)
+
+
+@pytest.mark.parametrize("d", HEADS)
+def test_prefill_split_repeats_bits_and_skips_bad_blocks(d):
+    b = Batch([(40, 3500), (5, 4100)], 2, d).fill(1)
+    q = _bf16((b.tokens, 10, d), 2).cuda()
+    dev = b.device()
+    first = _attend(b, q, dev, 10)
+    for _ in range(10):
+        assert torch.equal(_attend(b, q, dev, 10), first)
+    assert b.status.item() == 0
+    # every block of the first sequence's keys but the last three is unusable:
+    # whole pieces without a key
+    table, lens, start = b.meta()
+    table[0, :216] = -1
+    out = _attend(b, q, dev, 10, meta=(table, lens, start))
+    ref, bound = F.attention(q.double().cpu().numpy(), b.host(), table.cpu().numpy(), b.lens, b.start, d ** -0.5, True)
+    _assert_attention(out, ref, bound)
+    assert b.status.item() == _lib.DEV_BAD_BLOCK
+
+
+@pytest.mark.parametrize("d", HEADS)
 def test_prefill_rising_scores(d):
     """Keys that grow along the sequence: the running maximum moves in every step,
     by little and by more than the weights can hold."""
