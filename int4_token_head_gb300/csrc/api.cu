@@ -112,8 +112,10 @@ bool workspace_layout_fp8(int num_seqs, int num_q_tokens, int num_q_heads, int n
   L->ptab = take((S + 1) * 8);
   L->plist = take((L->max_pairs + kMaxPieces) * 32);
   L->msplit = take(kMaxPieces / 2 * 16);
-  L->direct_o = take(S * Hkv * kDecodeColsFp8 * D * 4);
-  L->direct_ml = take(S * Hkv * kDecodeColsFp8 * 2 * 4);
+  const size_t least = S * Hkv * kDecodeCols, most = S * Hkv * kDecodeColsFp8, twice = 2 * T * num_q_heads;
+  L->direct_rows = least > twice ? least : most < twice ? most : twice;
+  L->direct_o = take(L->direct_rows * D * 4);
+  L->direct_ml = take(L->direct_rows * 2 * 4);
   L->warp_o = take((size_t)kMaxDecodeWarps * kDecodeCols * D * 4);
   L->warp_ml = take((size_t)kMaxDecodeWarps * kDecodeCols * 2 * 4);
   L->piece_o = take((size_t)kPieceRows * D * 4);

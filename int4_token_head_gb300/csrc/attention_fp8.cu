@@ -142,46 +142,53 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
   c.out_stride = a.out_stride;
   c.status = a.dev_status;
   c.max_items = L.max_pairs * a.num_kv_heads;
-  // f with the number of blocks per position as a constant
-  auto with_np = [](int np, auto&& f) {
-    if (np == 1) return f(std::integral_constant<int, 1>{});
-    if (np == 2) return f(std::integral_constant<int, 2>{});
-    return f(std::integral_constant<int, kFp8Quad<D> ? 4 : 2>{});
+  // f with the number of blocks per position and of column groups as constants
+  auto with_np = [](int np, int cg, auto&& f) {
+    using std::integral_constant;
+    if (np == 2) return f(integral_constant<int, 2>{}, integral_constant<int, 1>{});
+    if (np == 4) return f(integral_constant<int, kFp8Quad<D> ? 4 : 2>{}, integral_constant<int, 1>{});
+    if (cg == 2) return f(integral_constant<int, 1>{}, integral_constant<int, 2>{});
+    if (cg == 4) return f(integral_constant<int, 1>{}, integral_constant<int, 4>{});
+    return f(integral_constant<int, 1>{}, integral_constant<int, 1>{});
   };
   // decode: blocks per position, kv heads per CTA, CTAs
   c.hg = c.ng = c.nl = c.np = 1;
-  const bool any_decode = c.group <= kDecodeCols;
+  // query columns of the batch's decode sequences: paired blocks need at most
+  // four, four blocks at most two, column groups take eight each up to 32 (as
+  // far as the workspace holds their results).  When the batch also holds longer
+  // queries decode is sized for single tokens and the others go to prefill
+  const long long mq = (long long)(a.max_query_len > 0 ? a.max_query_len : 1) * c.group;
+  const long long cols = mq <= kDecodeColsFp8 ? mq : c.group;
+  int cg = cols > 2 * kDecodeCols ? 4 : cols > kDecodeCols ? 2 : 1;
+  while (cg > 1 && (long long)a.num_seqs * a.num_kv_heads * kDecodeCols * cg > L.direct_rows) cg /= 2;
+  const bool any_decode = c.group <= kDecodeCols * cg;
   int dec_grid = 0, dec_occ = 0;
   if (any_decode) {
-    static PerContext<int> occ_cache[3][5];
+    static PerContext<int> occ_cache[5][5];
     int& occ = dec_occ;
-    auto take = [&](auto np_tag) {
-      constexpr int NP = decltype(np_tag)::value;
+    auto take = [&](auto np_tag, auto cg_tag) {
+      constexpr int NP = decltype(np_tag)::value, CG = decltype(cg_tag)::value;
       using G = Fp8Dec<D, NP>;
       c.np = NP;
-      // the largest divisor of Hkv up to 4 whose ring leaves room for two CTAs per SM
-      for (int h = 4; h >= 1; h--)
+      // the largest divisor of Hkv that gives up to four warps and whose ring
+      // leaves room for two CTAs per SM
+      for (int h = 4 / CG; h >= 1; h--)
         if (a.num_kv_heads % h == 0 && (h == 1 || 2 * (G::smem_bytes(h) + 1024) <= 228 * 1024)) {
           c.hg = h;
           break;
         }
-      return occ_cache[NP / 2][c.hg].get(dev, [&](int* v) {
+      return occ_cache[NP == 1 ? CG / 2 : NP / 2 + 2][c.hg].get(dev, [&](int* v) {
         int unused;  // the attribute is raised once, to the largest ring in use
-        return configure(decode_fp8_kernel<D, NP, true>, (228 * 1024) / 2 - 1024, 128, &unused) &&
-               configure(decode_fp8_kernel<D, NP, false>, (228 * 1024) / 2 - 1024, 128, &unused) &&
-               cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, decode_fp8_kernel<D, NP, false>, c.hg * 32,
+        return configure(decode_fp8_kernel<D, NP, CG, true>, (228 * 1024) / 2 - 1024, 128, &unused) &&
+               configure(decode_fp8_kernel<D, NP, CG, false>, (228 * 1024) / 2 - 1024, 128, &unused) &&
+               cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, decode_fp8_kernel<D, NP, CG, false>, c.hg * CG * 32,
                                                              G::smem_bytes(c.hg)) == cudaSuccess && *v >= 1;
       }, &occ);
     };
-    // query columns of the batch's decode sequences: paired blocks need at
-    // most four, four blocks at most two; when the batch also holds prefills
-    // decode is sized for single-token queries and longer ones go to prefill
-    const long long mq = (long long)(a.max_query_len > 0 ? a.max_query_len : 1) * c.group;
-    const long long cols = mq <= kDecodeCols ? mq : c.group;
-    if (!with_np(cols > 4 ? 1 : cols > 2 || !kFp8Quad<D> ? 2 : 4, take)) return KV_INT4_ERR_CUDA;
+    if (!with_np(cols > 4 ? 1 : cols > 2 || !kFp8Quad<D> ? 2 : 4, cg, take)) return KV_INT4_ERR_CUDA;
     c.ng = a.num_kv_heads / c.hg;
     long long grid = (long long)sms * occ;
-    if (grid * c.hg > kMaxDecodeWarps) grid = kMaxDecodeWarps / c.hg;
+    if (grid * c.hg * cg > kMaxDecodeWarps) grid = kMaxDecodeWarps / (c.hg * cg);
     // lanes: as many as divide the head groups, so that the groups' slices of
     // a block's rows are read side by side
     for (int l = (int)(grid < c.ng ? grid : c.ng); l >= 1; l--)
@@ -191,7 +198,7 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
       }
     dec_grid = (int)(grid / c.nl * c.nl);
   }
-  c.dcols = kDecodeCols / c.np;
+  c.dcols = kDecodeCols * cg / c.np;
 
   const bool may_prefill = c.group > c.dcols || (long long)a.max_query_len * c.group > c.dcols;
   if (!may_prefill) {
@@ -207,9 +214,9 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
     while (cl < 8 && 2 * tasks * cl <= room && most > 2 * cl) cl *= 2;
     if (tasks * cl <= room && most <= 16 * cl) {
       timing_begin(kTimedDecode, stream);
-      const int e = with_np(c.np, [&](auto np_tag) {
-        constexpr int NP = decltype(np_tag)::value;
-        return launch_pdl(decode_fp8_kernel<D, NP, true>, dim3((unsigned)(tasks * cl)), c.hg * 32,
+      const int e = with_np(c.np, cg, [&](auto np_tag, auto cg_tag) {
+        constexpr int NP = decltype(np_tag)::value, CG = decltype(cg_tag)::value;
+        return launch_pdl(decode_fp8_kernel<D, NP, CG, true>, dim3((unsigned)(tasks * cl)), c.hg * CG * 32,
                           Fp8Dec<D, NP>::smem_bytes(c.hg), stream, cl, Fp8DecParams{c, pv, 0, cl, false});
       });
       timing_end(kTimedDecode, stream);
@@ -286,12 +293,11 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
   };
   if (any_decode) {
     const Fp8DecParams prm{c, pv, dec_grid, 1, may_prefill};
-    const int threads = c.hg * 32;
     timing_begin(kTimedDecode, stream);
-    int e = with_np(c.np, [&](auto np_tag) {
-      constexpr int NP = decltype(np_tag)::value;
-      return launch_pdl(decode_fp8_kernel<D, NP, false>, dim3(dec_grid), threads, Fp8Dec<D, NP>::smem_bytes(c.hg), stream,
-                        1, prm);
+    int e = with_np(c.np, cg, [&](auto np_tag, auto cg_tag) {
+      constexpr int NP = decltype(np_tag)::value, CG = decltype(cg_tag)::value;
+      return launch_pdl(decode_fp8_kernel<D, NP, CG, false>, dim3(dec_grid), c.hg * CG * 32,
+                        Fp8Dec<D, NP>::smem_bytes(c.hg), stream, 1, prm);
     });
     timing_end(kTimedDecode, stream);
     if (e) return e;
@@ -307,13 +313,13 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
     timing_begin(kTimedReduce, stream);
     e = launch_pdl(may_split ? merge_fp8_kernel<D, true> : merge_fp8_kernel<D, false>,
                    dim3((unsigned)merge_ctas(segs, cols * lanes)), cols * lanes * 32, merge_smem<D>(cols, lanes), stream, 1,
-                   Fp8MergeParams{c, pv, dec_grid, cols, lanes});
+                   Fp8MergeParams{c, pv, dec_grid, cols, lanes, kDecodeCols * cg});
     timing_end(kTimedReduce, stream);
     if (e) return e;
   } else if (may_split) {
     timing_begin(kTimedReduce, stream);
     const int e = launch_pdl(merge_fp8_kernel<D, true>, dim3((unsigned)merge_ctas(1, 8)), 256, 0, stream, 1,
-                             Fp8MergeParams{c, pv, 0, 8, 1});
+                             Fp8MergeParams{c, pv, 0, 8, 1, kDecodeCols});
     timing_end(kTimedReduce, stream);
     if (e) return e;
   }

@@ -5,7 +5,9 @@
 // position) units, each CTA an equal contiguous range of its lane (the
 // schedule of decode.cuh; a position is NP consecutive 16-key blocks that
 // share the MMA's eight query columns, COLS = 8 / NP each).  A CTA has one
-// warp per kv head of its group; all its threads copy the blocks' codes of the
+// warp per kv head of its group, or CG warps that take eight query columns each
+// (queries of up to 32 columns: a few tokens at once, large groups; the warps
+// share the staged blocks, so the cache is still read once); all its threads copy the blocks' codes of the
 // group's heads (contiguous runs of the cache) with 16-byte cp.async into a
 // ring of block slots.  Rows behind the sequence's end, absent and unusable
 // blocks are filled with zeros by the copies, so that no stale byte (E4M3 has
@@ -46,6 +48,9 @@ struct Fp8Dec {
   }
   static_assert(WAIT >= 0 && HTILE % 16 == 0, "ring");
 };
+
+template <int D>
+constexpr bool kFp8PartsFit = Fp8Dec<D, 1>::smem_bytes(1) >= kDecodeColsFp8 * (D + 2) * 4;  // DIRECT's shares
 
 // head sizes with four blocks per position (queries of at most two columns):
 // where the eight-slot ring of four heads leaves room for two CTAs per SM
@@ -124,15 +129,20 @@ __device__ __forceinline__ float ld_cluster(const float* p, int rank) {
 // cluster of CTAs serves one (sequence, head group), its CTAs equal shares of
 // the positions, and merges them through distributed shared memory: one launch
 // for batches whose shares are short (latency counts there, not balance).
-template <int D, int NP, bool DIRECT>
+template <int D, int NP, int CG, bool DIRECT>
 __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
   using G = Fp8Dec<D, NP>;
+  static_assert(CG == 1 || (NP == 1 && kFp8PartsFit<D>), "column groups");
+  constexpr int SLOT = kDecodeCols * CG;           // columns of a result slot
+  constexpr int CPT = (G::CHR + CG - 1) / CG;      // chunks a thread copies per block
   const Common& c = prm.c;
   const PlanView& pv = prm.pv;
   extern __shared__ __align__(16) uint8_t smem[];
   const int HG = c.hg;
-  const int tid = threadIdx.x, nthr = HG * 32;
-  const int hl = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, nthr = HG * CG * 32;
+  const int warp = tid >> 5, lane = tid & 31;
+  const int hl = CG == 1 ? warp : warp / CG;       // head of the group
+  const int cbase = CG == 1 ? 0 : warp % CG * kDecodeCols;  // first query column
   const int g = lane >> 2, cq = lane & 3;
   const int SB = G::slot_bytes(HG);
   pdl_trigger();
@@ -208,13 +218,14 @@ __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
   }
   Fp8Walk pw = cw;
 
-  // staging: chunk index ((kv * 16 + r) * HG + h) * CHR + col, CHR chunks
+  // staging: chunk index ((kv * 16 + r) * HG + h) * CHR + col, CPT chunks
   // a thread; consecutive threads read consecutive bytes
-  uint32_t c_saddr[G::CHR];      // shared address within slot 0
-  const uint8_t* c_src[G::CHR];  // cache address within block 0, head group 0
+  uint32_t c_saddr[CPT];      // shared address within slot 0
+  const uint8_t* c_src[CPT];  // cache address within block 0, head group 0
+  const bool last_chunk = G::CHR % CG == 0 || tid + nthr * (CPT - 1) < 32 * HG * G::CHR;
 #pragma unroll
-  for (int j = 0; j < G::CHR; j++) {
-    const int idx = tid + nthr * j;
+  for (int j = 0; j < CPT; j++) {
+    const int idx = tid + nthr * (j < CPT - 1 || last_chunk ? j : 0);
     const int col = idx % G::CHR, rest = idx / G::CHR;
     const int h = rest % HG, kvr = rest / HG;
     const int kv = kvr / 16, r = kvr % 16;
@@ -237,11 +248,13 @@ __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
     const uint64_t base = ok ? (uint64_t)(uint32_t)blk * (uint64_t)c.geo.cblk + (uint64_t)(grp * HG) * D : 0;
     if (rows >= 16) {
 #pragma unroll
-      for (int j = 0; j < G::CHR; j++)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(c_saddr[j] + soff), "l"(c_src[j] + base));
+      for (int j = 0; j < CPT; j++)
+        if (j < CPT - 1 || last_chunk)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(c_saddr[j] + soff), "l"(c_src[j] + base));
     } else {
 #pragma unroll
-      for (int j = 0; j < G::CHR; j++) {
+      for (int j = 0; j < CPT; j++) {
+        if (j == CPT - 1 && !last_chunk) break;
         const int r = (tid + nthr * j) / G::CHR / HG % 16;
         const bool in = r < rows;
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(c_saddr[j] + soff),
@@ -294,8 +307,8 @@ __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
     const int4 di = DIRECT ? dseq0 : pv.dseq[cw.i];
     const int q0 = di.z, ql = di.w, L = di.y;
     const int ctx = L - ql;
-    // B fragments of this lane's column g, which holds query column g % COLS
-    const int n = g & (G::COLS - 1);
+    // B fragments of this lane's column g, which holds query column cbase + g % COLS
+    const int n = cbase + (g & (G::COLS - 1));
     const bool colok = n < ql * c.group;
     const int j = n / c.group, jj = n - j * c.group;
     const uint16_t* qrow = c.q + (long long)(q0 + (colok ? j : 0)) * c.q_stride +
@@ -321,7 +334,7 @@ __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
     const float cf = c.qscale * exp2_int(e);
     cf0 = __shfl_sync(0xffffffffu, cf, 8 * cq);      // column 2 cq is held by lanes 4 (2 cq) ..
     cf1 = __shfl_sync(0xffffffffu, cf, 8 * cq + 4);
-    const int col0 = (2 * cq) & (G::COLS - 1), col1 = (2 * cq + 1) & (G::COLS - 1);
+    const int col0 = cbase + ((2 * cq) & (G::COLS - 1)), col1 = cbase + ((2 * cq + 1) & (G::COLS - 1));
     const int j0 = min(col0 / c.group, max(ql - 1, 0)), j1 = min(col1 / c.group, max(ql - 1, 0));
     lim0 = c.causal ? min(L, ctx + j0 + 1) : L;
     lim1 = c.causal ? min(L, ctx + j1 + 1) : L;
@@ -370,17 +383,19 @@ __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
     float* dst_o;
     float* dst_ml;
     if constexpr (DIRECT) {  // over the ring: every copy has landed, every warp is done
-      dst_o = reinterpret_cast<float*>(smem) + hl * kDecodeCols * (D + 2);
-      dst_ml = dst_o + kDecodeCols * D;
+      dst_o = reinterpret_cast<float*>(smem) + hl * SLOT * (D + 2);
+      dst_ml = dst_o + SLOT * D;
     } else if (first_piece) {
       const long long slot = (long long)cw.i * c.hkv + cw.grp * HG + hl;
-      dst_o = pv.direct_o + slot * kDecodeCols * D;
-      dst_ml = pv.direct_ml + slot * kDecodeCols * 2;
+      dst_o = pv.direct_o + slot * SLOT * D;
+      dst_ml = pv.direct_ml + slot * SLOT * 2;
     } else {
       const long long slot = (long long)blockIdx.x * HG + hl;
-      dst_o = pv.warp_o + slot * kDecodeCols * D;
-      dst_ml = pv.warp_ml + slot * kDecodeCols * 2;
+      dst_o = pv.warp_o + slot * SLOT * D;
+      dst_ml = pv.warp_ml + slot * SLOT * 2;
     }
+    dst_o += cbase * D;
+    dst_ml += cbase * 2;
     // m-tile t holds d = 16 t + 2g (row g) and 16 t + 2g + 1 (row g + 8)
     float* o0 = dst_o + (2 * cq) * D + 2 * g;
     float* o1 = dst_o + (2 * cq + 1) * D + 2 * g;
@@ -563,9 +578,9 @@ __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
     constexpr int PER = D / 32, SUB = NP == 2 ? 2 : 1;
     const int cols = dseq0.w * c.group;
 #pragma unroll 1
-    for (int p = rank * HG + hl; p < HG * cols; p += prm.cluster * HG) {
+    for (int p = rank * HG * CG + warp; p < HG * cols; p += prm.cluster * HG * CG) {
       const int h = p / cols, col = p - h * cols;
-      const float* base = reinterpret_cast<const float*>(smem) + h * kDecodeCols * (D + 2);
+      const float* base = reinterpret_cast<const float*>(smem) + h * SLOT * (D + 2);
       float M = -INFINITY, Ls = 0.f, acc[PER];
 #pragma unroll
       for (int k = 0; k < PER; k++) acc[k] = 0.f;
@@ -575,8 +590,8 @@ __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
 #pragma unroll
         for (int sub = 0; sub < SUB; sub++) {
           const int cc = col + sub * G::COLS;
-          mw[sub] = ld_cluster(base + kDecodeCols * D + 2 * cc, r);
-          lw[sub] = ld_cluster(base + kDecodeCols * D + 2 * cc + 1, r);
+          mw[sub] = ld_cluster(base + SLOT * D + 2 * cc, r);
+          lw[sub] = ld_cluster(base + SLOT * D + 2 * cc + 1, r);
 #pragma unroll
           for (int k = 0; k < PER; k++) o[sub][k] = ld_cluster(base + cc * D + lane + 32 * k, r);
         }
@@ -612,6 +627,7 @@ struct Fp8MergeParams {
   int num_ctas;
   int cols;   // query columns per segment (warps)
   int lanes;  // piece lanes per column (warps)
+  int slot;   // columns of a result slot
 };
 
 template <int D>
@@ -757,8 +773,8 @@ __global__ void __launch_bounds__(1024) merge_fp8_kernel(Fp8MergeParams prm) {
         }
       }
       const long long sl = (w * c.nl + lane_g) * c.hg + hl;
-      const float* o = k > 0 ? pv.warp_o + sl * kDecodeCols * D : pv.direct_o + (long long)seg * kDecodeCols * D;
-      const float* ml = k > 0 ? pv.warp_ml + sl * kDecodeCols * 2 : pv.direct_ml + (long long)seg * kDecodeCols * 2;
+      const float* o = k > 0 ? pv.warp_o + sl * prm.slot * D : pv.direct_o + (long long)seg * prm.slot * D;
+      const float* ml = k > 0 ? pv.warp_ml + sl * prm.slot * 2 : pv.direct_ml + (long long)seg * prm.slot * 2;
       float mw[2], lw[2], ov[2][PER];
 #pragma unroll
       for (int sub = 0; sub < 2; sub++) {

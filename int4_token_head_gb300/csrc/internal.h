@@ -241,16 +241,17 @@ struct WorkspaceLayoutFp8 {
   size_t ptab;          // int2 [num_seqs + 1] prefill sequence table
   size_t plist;         // PrefillPiece [max_pairs + kMaxPieces] prefill tiles and pieces of tiles, longest first
   size_t msplit;        // int4 [kMaxPieces / 2] tiles in pieces
-  size_t direct_o;      // f32 [num_seqs][Hkv][kDecodeColsFp8][d]
-  size_t direct_ml;     // f32 [num_seqs][Hkv][kDecodeColsFp8][2]
-  size_t warp_o;        // f32 [kMaxDecodeWarps][8][d], or half as many slots of 16 columns
+  size_t direct_o;      // f32 [direct_rows][d]: query columns of (decode sequence, kv head) slots
+  size_t direct_ml;     // f32 [direct_rows][2]
+  size_t warp_o;        // f32 [kMaxDecodeWarps][8][d]
   size_t warp_ml;       // f32 [kMaxDecodeWarps][8][2]
   size_t piece_o;       // f32 [kPieceRows][d] rows of pieces
   size_t piece_ml;      // f32 [kPieceRows][2]
   size_t total;
   int64_t max_pairs;    // prefill (sequence, tile) pairs
+  int64_t direct_rows;  // 8 columns per slot; more, up to kDecodeColsFp8, as far as the call has twice the queries
 };
-constexpr int kDecodeColsFp8 = 16;  // most query columns per FP8 decode work unit
+constexpr int kDecodeColsFp8 = 32;  // most query columns per FP8 decode work unit
 constexpr int kMaxPieces = 2048;    // pieces of split prefill tiles, and their rows over all kv heads
 constexpr int kPieceRows = 40960;   // (a piece of a full 256-row tile for each of 160 CTAs)
 

@@ -333,6 +333,21 @@ def test_prefill_many_tiles_per_cta(d):
 
 @pytest.mark.parametrize("d", HEADS)
 @pytest.mark.parametrize("hq,hkv,seqs", [
+    (12, 1, [(1, 700), (1, 1), (0, 9), (1, 33)]),                # 12 columns, one launch
+    (32, 1, [(1, 40), (1, 900)]),
+    (48, 3, [(1, n) for n in (2600, 17, 900, 16)]),              # 16 columns, the balanced split and its merge
+    (16, 2, [(2, 2900), (4, 4), (3, 300), (1, 600), (0, 3)]),    # 8 to 32 columns side by side
+    (28, 4, [(3, 700), (1, 3000), (3, 3), (2, 250)]),
+    (8, 8, [(27, 1000), (9, 100), (1, 1)]),                      # up to 27 tokens
+    (24, 3, [(1, 100 + 7 * i) for i in range(40)] + [(4, 500), (3, 900)]),  # room for 16 columns, not for 32
+])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 50)])
+def test_decode_many_columns(d, hq, hkv, seqs, causal, window):
+    _check(seqs, hq, hkv, d, causal=causal, window=window, seed=d + hq)
+
+
+@pytest.mark.parametrize("d", HEADS)
+@pytest.mark.parametrize("hq,hkv,seqs", [
     (16, 1, [(3, 5000)]),                                              # one tile, every piece of one step or two
     (24, 2, [(7, 3000), (1, 9), (2, 2500), (30, 2100), (0, 5), (9, 9)]),  # pieces beside whole tiles and decodes
     (8, 8, [(200, 1999), (260, 2200)]),                                # several tiles a sequence, rows of unlike limits
