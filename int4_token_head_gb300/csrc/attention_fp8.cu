@@ -17,7 +17,8 @@
 // the fp32 score by that power.  Codes convert exactly to either type.
 //
 // Launches, all on the caller's stream: the schedule (one CTA), prefill (if a
-// sequence may need it), decode, merge.
+// sequence may need it), decode, merge (of decode's pieces and of prefill tiles
+// split over their keys).  Short batches that only decode: one launch.
 
 #include <cuda.h>
 #include <float.h>
@@ -32,7 +33,7 @@
 namespace kvint4 {
 namespace {
 
-template <bool PREFILL>
+template <int PREFILL>
 __global__ void __launch_bounds__(kPrepThreads) plan_fp8_kernel(Common c, PlanView pv) {
   pdl_trigger();
   pdl_wait();
@@ -70,9 +71,9 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
-int launch_plan(const Common& c, const PlanView& pv, bool may_prefill, cudaStream_t stream) {
-  return launch_pdl(may_prefill ? plan_fp8_kernel<true> : plan_fp8_kernel<false>, dim3(1), kPrepThreads, 0, stream, 1, c,
-                    pv);
+int launch_plan(const Common& c, const PlanView& pv, bool may_prefill, bool may_split, cudaStream_t stream) {
+  return launch_pdl(may_split ? plan_fp8_kernel<2> : may_prefill ? plan_fp8_kernel<1> : plan_fp8_kernel<0>, dim3(1),
+                    kPrepThreads, 0, stream, 1, c, pv);
 }
 
 // the tensor maps of a call's prefill; false where its tensors have no such
@@ -228,8 +229,17 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
   // two accumulators of 256 columns would leave no TMEM for scores), 64 on the
   // warp-MMA one
   // Keys are split into pieces of at least four steps of the tensor-core kernel
-  // (512 keys; 256 at 192), eight of the other (256 keys)
-  bool tc = false;
+  // (512 keys; 256 at 192), eight of the other (256 keys), where a tile may have
+  // four or two such pieces (looking for splits costs 3 us per call) and there
+  // are fewer tiles than the schedule leaves whole anyway (sequences decoded
+  // here have at most dcols / group tokens)
+  const long long most_decode = any_decode ? (long long)a.num_seqs * (c.dcols / c.group) : 0;
+  auto can_split = [&](int pieces) {
+    const long long tiles = (a.num_q_tokens - most_decode + c.tile_tokens - 1) / c.tile_tokens;
+    return may_prefill && a.max_seq_len > 16ll * c.step_blocks * c.split_steps * pieces && tiles <= kSplitTiles &&
+           tiles * a.num_kv_heads < (long long)kSplitWaves * c.split_ctas;
+  };
+  bool tc = false, may_split = false;
   const long long pairs = L.max_pairs + kMaxPieces;
   const long long most_items = pairs * a.num_kv_heads;
   if constexpr (D <= 192) {
@@ -246,7 +256,8 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
       if (!occ_c.get(dev, [](int* o) { return configure_tmem(prefill_ws_fp8_kernel<D>, G::SMEM, G::THREADS, 512, o); },
                      &occ))
         return KV_INT4_ERR_CUDA;
-      if (int e = launch_plan(c, pv, may_prefill, stream)) return e;
+      may_split = can_split(4);
+      if (int e = launch_plan(c, pv, may_prefill, may_split, stream)) return e;
       const long long grid = sms < most_items ? sms : most_items;
       timing_begin(kTimedPrefill, stream);
       const int e = launch_pdl(prefill_ws_fp8_kernel<D>, dim3((unsigned)grid), G::THREADS, G::SMEM, stream, 1, c, pv, maps);
@@ -268,7 +279,8 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
     c.step_blocks = G::NB;
     c.split_steps = 8;
     c.split_ctas = (int)grid;
-    if (int e = launch_plan(c, pv, may_prefill, stream)) return e;
+    may_split = can_split(2);
+    if (int e = launch_plan(c, pv, may_prefill, may_split, stream)) return e;
     if (may_prefill) {
       if (grid > most_items) grid = most_items;
       timing_begin(kTimedPrefill, stream);
@@ -277,14 +289,8 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
       if (e) return e;
     }
   }
-  // Whether tiles may be in pieces: a key range of two pieces or more, and fewer
-  // tiles than the schedule leaves whole (sequences decoded here have at most
-  // dcols / group tokens).  The merge then has CTAs for a warp per row, as far as
-  // they start at once when the prefill's last CTAs leave
-  const long long most_decode = any_decode ? (long long)a.num_seqs * (c.dcols / c.group) : 0;
-  const long long tiles = (a.num_q_tokens - most_decode + c.tile_tokens - 1) / c.tile_tokens;
-  const bool may_split = may_prefill && a.max_seq_len > 16ll * c.step_blocks * c.split_steps && tiles <= kSplitTiles &&
-                         tiles * a.num_kv_heads < 8ll * c.split_ctas;
+  // The merge of pieces has CTAs for a warp per row, as far as they start at once
+  // when the prefill's last CTAs leave
   auto merge_ctas = [&](long long segs, int warps) {
     const long long rows = (long long)a.num_q_tokens * a.num_q_heads;
     const long long want = ((rows < kPieceRows / 2 ? rows : kPieceRows / 2) + warps - 1) / warps;
@@ -301,25 +307,36 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
     });
     timing_end(kTimedDecode, stream);
     if (e) return e;
-    // merge: a CTA per (sequence, kv head) segment, a warp per query column
-    // and piece lane; lanes enough that each merges one or two pieces
+    // merge: one or more CTAs per (sequence, kv head) segment, a warp per query
+    // column and piece lane; lanes enough that each merges one or two pieces (1 to
+    // 3 tokens of 7 heads against up to 9611 keys of one kv head, 2 sequences:
+    // 201 us with the 21 columns in one CTA and so one lane each, 22 spread out),
+    // as far as all CTAs start at once (more: 52 us instead of 43 for 32 x 1
+    // token of group 16)
     const long long mcols = (long long)(a.max_query_len > 0 ? a.max_query_len : 1) * c.group;
-    const int cols = (int)(mcols < c.dcols ? mcols : c.dcols);
     const long long segs = (long long)a.num_seqs * a.num_kv_heads;
     const long long pieces = 1 + (long long)dec_grid * c.hg / (segs > 0 ? segs : 1);
+    constexpr int kWarps = 32;  // per CTA, and per SM over all CTAs
     int lanes = 1;
-    while (lanes < 16 && lanes < pieces && 2 * lanes * cols <= 32) lanes *= 2;
-    if (segs > 0x7fffffff) return KV_INT4_ERR_SIZE;
+    int cols = (int)(mcols < c.dcols ? mcols : c.dcols), parts = 1;
+    while (lanes < kWarps && lanes < pieces &&
+           (2 * lanes * cols <= kWarps || 2 * lanes * cols * segs <= (long long)kWarps * sms))
+      lanes *= 2;
+    if (cols * lanes > kWarps) {
+      parts = (cols * lanes + kWarps - 1) / kWarps;
+      cols = (cols + parts - 1) / parts;
+    }
+    if (segs * parts > 0x7fffffff) return KV_INT4_ERR_SIZE;
     timing_begin(kTimedReduce, stream);
     e = launch_pdl(may_split ? merge_fp8_kernel<D, true> : merge_fp8_kernel<D, false>,
-                   dim3((unsigned)merge_ctas(segs, cols * lanes)), cols * lanes * 32, merge_smem<D>(cols, lanes), stream, 1,
-                   Fp8MergeParams{c, pv, dec_grid, cols, lanes, kDecodeCols * cg});
+                   dim3((unsigned)merge_ctas(segs * parts, cols * lanes)), cols * lanes * 32,
+                   merge_smem<D>(cols, lanes), stream, 1, Fp8MergeParams{c, pv, dec_grid, cols, lanes, parts, kDecodeCols * cg});
     timing_end(kTimedReduce, stream);
     if (e) return e;
   } else if (may_split) {
     timing_begin(kTimedReduce, stream);
     const int e = launch_pdl(merge_fp8_kernel<D, true>, dim3((unsigned)merge_ctas(1, 8)), 256, 0, stream, 1,
-                             Fp8MergeParams{c, pv, 0, 8, 1, kDecodeCols});
+                             Fp8MergeParams{c, pv, 0, 8, 1, 1, kDecodeCols});
     timing_end(kTimedReduce, stream);
     if (e) return e;
   }

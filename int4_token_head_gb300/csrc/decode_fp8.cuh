@@ -625,8 +625,9 @@ struct Fp8MergeParams {
   Common c;
   PlanView pv;
   int num_ctas;
-  int cols;   // query columns per segment (warps)
+  int cols;   // query columns per CTA (warps)
   int lanes;  // piece lanes per column (warps)
+  int parts;  // CTAs per segment, cols columns each
   int slot;   // columns of a result slot
 };
 
@@ -710,12 +711,13 @@ __global__ void __launch_bounds__(1024) merge_fp8_kernel(Fp8MergeParams prm) {
   pdl_wait();
   constexpr int PER = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int col = warp % prm.cols, pl = warp / prm.cols;
+  const int pl = warp / prm.cols;
   const int n_dseq = pv.plan[0];
-  const int seg = blockIdx.x;
+  const int seg = blockIdx.x / prm.parts;
+  const int lcol = warp - pl * prm.cols, col = ((int)blockIdx.x - seg * prm.parts) * prm.cols + lcol;
   if constexpr (PIECES) {  // every CTA's warps take rows in turn, before its segment
     const int warps = blockDim.x >> 5;
-    const long long first = (long long)seg * warps + warp;
+    const long long first = (long long)blockIdx.x * warps + warp;
     if (first < kPieceRows) merge_prefill_pieces<D>(c, pv, (int)first, (int)min((long long)gridDim.x * warps, 1ll << 30));
   }
   if (seg >= n_dseq * c.hkv) return;
@@ -790,7 +792,7 @@ __global__ void __launch_bounds__(1024) merge_fp8_kernel(Fp8MergeParams prm) {
     }
   }
   if (prm.lanes > 1) {
-    float* mine = spart + (col * prm.lanes + pl) * (D + 2);
+    float* mine = spart + (lcol * prm.lanes + pl) * (D + 2);
     if (pl > 0) {
 #pragma unroll
       for (int k = 0; k < PER; k++) mine[lane + 32 * k] = acc[k];

@@ -219,13 +219,15 @@ __device__ __forceinline__ bool schedule_seq_ok(const Common& c, int q0, int ql,
 // large whose pieces all run at once is taken; without one, only tiles of more
 // than two shares are worth it.  Everything follows from the call's lengths
 // alone, so results do not depend on the order of arrival.  Batches of more
-// than kSplitTiles tiles, or of eight items per CTA, which the order by length
-// balances, keep their tiles whole.  `seqs`: the prefill sequences in shared
-// memory, if the batch fits there.  The code is kept short (one loop for both
-// passes): a lone CTA that runs it once waits for its instructions most of the
-// time (with the loops inlined twice 2 to 3 us more per call).
+// than kSplitTiles tiles, or of kSplitWaves items per CTA, which the order by
+// length balances, keep their tiles whole.  `seqs`: the prefill sequences in
+// shared memory, if the batch fits there.  The code is kept short (one loop for
+// both passes, none for splits where the host rules them out): a lone CTA that
+// runs it once waits for its instructions most of the time (with the loops
+// inlined twice 2 to 3 us more per call).
 constexpr int kSplitTiles = 1024;
-template <int BUCKETS>
+constexpr int kSplitWaves = 6;
+template <int BUCKETS, bool SPLIT>
 __device__ void build_pieces(const Common& c, const PlanView& pv, int n_pseq, int n_tiles, bool with_decode,
                              const int4* seqs, int* hist, int32_t* s_i32) {
   __shared__ int4 tiles[kSplitTiles];  // (sequence, tile, first block, end block)
@@ -263,7 +265,7 @@ __device__ void build_pieces(const Common& c, const PlanView& pv, int n_pseq, in
   fill(0);
   __syncthreads();
   int S = INT_MAX;
-  if (n_tiles <= kSplitTiles && (long long)n_tiles * c.hkv < 8ll * c.split_ctas) {
+  if (SPLIT && n_tiles <= kSplitTiles && (long long)n_tiles * c.hkv < (long long)kSplitWaves * c.split_ctas) {
     // every warp takes the sum, then one candidate for S: S0 to 2 S0, and 4 S0
     long long sum = 0;
     int longest = 0;
@@ -333,9 +335,9 @@ __device__ void build_pieces(const Common& c, const PlanView& pv, int n_pseq, in
 #pragma unroll 1
       for (int i = threadIdx.x / lpp; i < count; i += kPrepThreads / lpp) {
         const int4 x = tiles[i];
-        const int rows = tile_rows[i], n = steps_of(x), P = n > S ? (n - 1) / S + 1 : 1;
+        const int rows = tile_rows[i], n = steps_of(x), P = SPLIT && n > S ? (n - 1) / S + 1 : 1;
         int row = 0;
-        if (pass && P > 1) {
+        if (SPLIT && pass && P > 1) {
           if (threadIdx.x % lpp == 0) {
             row = atomicAdd(&next_row, P * rows * c.hkv);
             pv.msplit[atomicAdd(&next_split, 1)] = make_int4(x.x, x.y, row, P);
@@ -379,15 +381,15 @@ __device__ void build_pieces(const Common& c, const PlanView& pv, int n_pseq, in
   }
 }
 
-// The schedule, by one CTA of kPrepThreads threads.  PREFILL false: no sequence
-// of the call can be a prefill (code that is not there is not fetched either: a
-// lone CTA runs at the pace of its instruction fetches).
-template <bool ANY_LEN, bool PREFILL = true>
+// The schedule, by one CTA of kPrepThreads threads.  PREFILL 0: no sequence of
+// the call can be a prefill, 1: none can be split, 2: any (code that is not there
+// is not fetched either).
+template <bool ANY_LEN, int PREFILL = 1>
 __device__ void build_schedule(const Common& c, const PlanView& pv) {
   __shared__ int32_t s_i32[kPrepThreads / 32];
   __shared__ long long s_i64[kPrepThreads / 32];
   __shared__ long long s_i64t[ANY_LEN ? kPrepThreads / 32 : 1];
-  __shared__ int4 seqs[ANY_LEN && PREFILL ? kPrepThreads : 1];
+  __shared__ int4 seqs[ANY_LEN && PREFILL > 0 ? kPrepThreads : 1];
   int n_dseq = 0, n_pseq = 0;
   long long dpre = 0, n_items = 0;
   for (int base = 0; base < c.num_seqs; base += kPrepThreads) {
@@ -419,7 +421,7 @@ __device__ void build_schedule(const Common& c, const PlanView& pv) {
       for (int o = 1; o < 32; o <<= 1) {
         const int yn = __shfl_up_sync(0xffffffffu, n, o);
         const long long yb = __shfl_up_sync(0xffffffffu, b, o);
-        const long long yt = PREFILL ? __shfl_up_sync(0xffffffffu, t, o) : 0;
+        const long long yt = PREFILL > 0 ? __shfl_up_sync(0xffffffffu, t, o) : 0;
         if (lane >= o) {
           n += yn;
           b += yb;
@@ -460,7 +462,7 @@ __device__ void build_schedule(const Common& c, const PlanView& pv) {
     if (kind == 1) {
       pv.dseq[n_dseq + ex_a] = make_int4(s, L, q0, ql);
       pv.dprefix[n_dseq + ex_a] = dpre + ex_b;
-    } else if (PREFILL && kind == 2) {
+    } else if (PREFILL > 0 && kind == 2) {
       // the prefill kernel expands (tile, kv head) items from this table
       pv.ptab[n_pseq + ex_p] = make_int2(s, (int)min(n_items + ex_c, (long long)INT_MAX));
       if (ANY_LEN && base == 0) seqs[ex_p] = make_int4(s, ql, L, (int)min(ex_c / c.hkv, (long long)INT_MAX));
@@ -473,7 +475,7 @@ __device__ void build_schedule(const Common& c, const PlanView& pv) {
   if (threadIdx.x == 0) {
     pv.dprefix[n_dseq] = dpre;
     pv.plan[0] = n_dseq;
-    if constexpr (!PREFILL) return;
+    if constexpr (PREFILL == 0) return;
     // more items than the workspace was sized for only happens with
     // inconsistent query_start_loc: the prefill part is dropped and flagged
     const bool over = n_items > c.max_items || n_items > INT_MAX;
@@ -484,7 +486,7 @@ __device__ void build_schedule(const Common& c, const PlanView& pv) {
     pv.plan[3] = n_pseq;
     if (ANY_LEN) pv.plan[4] = 0;
   }
-  if constexpr (!PREFILL) return;
+  if constexpr (PREFILL == 0) return;
   // the prefill (sequence, tile) pairs, longest first: a counting sort over
   // buckets of 16-key blocks (descending), so that the longest items start
   // first and the shortest fill the end of the launch (within a bucket the
@@ -493,7 +495,7 @@ __device__ void build_schedule(const Common& c, const PlanView& pv) {
   __shared__ int hist[kBuckets];
   if constexpr (ANY_LEN) {
     if (n_pseq > 0 && n_items <= c.max_items && n_items <= INT_MAX)
-      build_pieces<kBuckets>(c, pv, n_pseq, (int)(n_items / c.hkv), n_dseq > 0,
+      build_pieces<kBuckets, PREFILL == 2>(c, pv, n_pseq, (int)(n_items / c.hkv), n_dseq > 0,
                              c.num_seqs <= kPrepThreads ? seqs : nullptr, hist, s_i32);
     return;
   }

@@ -158,7 +158,10 @@ class PagedKV:
         d, hkv, hq = w.head_size, w.num_kv_heads, w.num_q_heads
         total = 0
         for q, kv in w.seqs:
-            total += kv * hkv * 2 * (d // 2 + 4)
+            if self.fmt == "fp8":  # codes, and the scales of the blocks
+                total += 2 * hkv * (kv * d + 4 * ((kv + w.block_size - 1) // w.block_size))
+            else:
+                total += kv * hkv * 2 * (d // 2 + 4)
             total += 4 * ((kv + w.block_size - 1) // w.block_size)
             total += q * hq * d * 2 * 2
             total += 12

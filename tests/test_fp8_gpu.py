@@ -357,6 +357,15 @@ def test_prefill_split_over_keys(d, hq, hkv, seqs, causal, window):
     _check(seqs, hq, hkv, d, causal=causal, window=window, seed=d + hq)
 
 
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("n", [300, 1100])
+def test_prefill_of_many_sequences(d, n):
+    """More prompts than the schedule's threads, and more tiles than it looks at
+    for splits, beside decodes."""
+    seqs = [(1, 20 + i % 60) if i % 7 == 0 else (33 + i % 9, 42 + i % 50) for i in range(n)]
+    _check(seqs, 1, 1, d, seed=n)
+
+
 @pytest.mark.parametrize("d", HEADS)
 def test_prefill_split_repeats_bits_and_skips_bad_blocks(d):
     b = Batch([(40, 3500), (5, 4100)], 2, d).fill(1)
