@@ -423,6 +423,34 @@ def _refuse(msg):
     raise ValueError(msg)
 
 
+def _no_call(*args):
+    return None
+
+
+class _Calls:
+    """The FP8 calls of _fp8_binding (a status, or None for arguments that the
+    functions below look at themselves); without the module all return None."""
+    write = read = attention = norm_rope = staticmethod(_no_call)
+
+
+def _calls():
+    """The call module, bound to the library at its first use."""
+    global _fp8
+    lib = load()
+    try:
+        from . import _fp8_binding as m
+    except ImportError:
+        m = _Calls
+    else:
+        m.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
+                 for f in ("kv_fp8_write", "kv_fp8_read", "kv_fp8_attention", "kv_qk_norm_rope")))
+    _fp8 = m
+    return m
+
+
+_fp8 = None
+
+
 def _raw_stream(dev: int, same: bool, stream) -> int:
     """The raw stream of a call on tensors of device `dev` (-1: the CPU), `same`
     for all of them; it must be the current device."""
@@ -492,6 +520,12 @@ def write_fp8(k, v, block_table, seq_lens, start_loc, max_len, k_cache, v_cache,
               dev_status: Optional[torch.Tensor] = None, stream=None):
     """Quantise each sequence's last start_loc[i+1] - start_loc[i] positions into
     the FP8 cache through kv_fp8_write (max_len bounds those counts)."""
+    code = (_fp8 or _calls()).write(k, v, block_table, seq_lens, start_loc, max_len, k_cache, v_cache, k_scale, v_scale,
+                                    dev_status, stream)
+    if code == 0:
+        return
+    if code is not None:
+        _raise(code, "kv_fp8_write")
     nb, bs, hkv, d = _cache_dims_fp8(k_cache, v_cache, k_scale, v_scale)
     num_seqs, width = _sequences(block_table, seq_lens, start_loc)
     tokens = k.shape[0]
@@ -511,6 +545,12 @@ def read_fp8(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, start_lo
              dev_status: Optional[torch.Tensor] = None, stream=None):
     """Write each sequence's last start_loc[i+1] - start_loc[i] positions of the
     FP8 cache to k and v (bf16 [tokens, heads, d]) through kv_fp8_read."""
+    code = (_fp8 or _calls()).read(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, start_loc, max_len, k, v,
+                                   dev_status, stream)
+    if code == 0:
+        return
+    if code is not None:
+        _raise(code, "kv_fp8_read")
     nb, bs, hkv, d = _cache_dims_fp8(k_cache, v_cache, k_scale, v_scale)
     num_seqs, width = _sequences(block_table, seq_lens, start_loc)
     tokens = k.shape[0]
@@ -531,6 +571,13 @@ def attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, 
                   dev_status: Optional[torch.Tensor] = None, stream=None, sliding_window: int = 0):
     """Attention over the FP8 cache through kv_fp8_attention; writes ``out`` in
     place.  With ``causal`` false, queries may attend keys of any length."""
+    code = (_fp8 or _calls()).attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, query_start_loc,
+                                        max_query_len, max_seq_len, softmax_scale, causal, out, workspace, dev_status,
+                                        stream, sliding_window)
+    if code == 0:
+        return
+    if code is not None:
+        _raise(code, "kv_fp8_attention")
     nb, bs, hkv, d = _cache_dims_fp8(k_cache, v_cache, k_scale, v_scale)
     num_seqs, width = _sequences(block_table, seq_lens, query_start_loc)
     if q.dim() != 3:
@@ -561,6 +608,12 @@ def qk_norm_rope(q, k, positions, cos_sin, q_weight, k_weight, eps, q_out, k_out
     input).  positions: int64 [tokens]; cos_sin: float32 [max_position, rot]
     (cosines, then sines), or both None for no rotation.  q_weight, k_weight:
     bf16 [d], or both None for no norm."""
+    code = (_fp8 or _calls()).norm_rope(q, k, positions, cos_sin, q_weight, k_weight, eps, q_out, k_out, interleaved,
+                                        dev_status, stream)
+    if code == 0:
+        return
+    if code is not None:
+        _raise(code, "kv_qk_norm_rope")
     if q.dim() != 3 or k.dim() != 3:
         _refuse("q and k must be [tokens, heads, d]")
     tokens, hq, d = q.shape

@@ -9,11 +9,13 @@ built on another machine (or from other sources) is rebuilt.
 from __future__ import annotations
 
 import hashlib
+import importlib.util
 import os
 import platform
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,6 +27,8 @@ HEADER = os.path.join(ROOT, "include", "kvint4.h")
 
 SOURCES = ["api.cu", "write.cu", "write_int8.cu", "attention.cu", "rht.cu", "attention_fp8.cu",
            "cache_fp8.cu", "norm_rope.cu", "api_fp8.cu", "timing.cu", "noalloc.cu", "selftest.cu"]
+BINDING_SRC = os.path.join(CSRC, "fp8_binding.cpp")
+BINDING_PATH = os.path.join(PKG, "_fp8_binding.so")
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden"]
 
@@ -41,13 +45,35 @@ def nvcc_path() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC))
-             if f.endswith((".cu", ".cuh", ".h"))]
+             if f.endswith((".cu", ".cuh", ".h", ".cpp"))]
     return files + [HEADER, os.path.abspath(__file__)]
+
+
+def _torch_dir():
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec else None
+
+
+def _binding_command():
+    """g++ for the Python call module, which sees torch's tensors; None without
+    torch's or Python's headers."""
+    torch, py = _torch_dir(), sysconfig.get_paths()["include"]
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")
+    if torch is None or not os.path.exists(os.path.join(py, "Python.h")) or shutil.which("g++") is None:
+        return None
+    lib = os.path.join(torch, "lib")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I", os.path.join(torch, "include"),
+            "-I", os.path.join(torch, "include", "torch", "csrc", "api", "include"), "-I", py, "-I", cuda, BINDING_SRC,
+            "-o", BINDING_PATH + ".tmp", "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
 def _fingerprint(extra=()) -> str:
     h = hashlib.sha256()
     h.update(platform.machine().encode())
+    torch = _torch_dir()
+    if torch:  # the call module depends on its version
+        with open(os.path.join(torch, "version.py"), "rb") as fh:
+            h.update(fh.read())
     for f in _inputs():
         with open(f, "rb") as fh:
             h.update(os.path.basename(f).encode())
@@ -81,6 +107,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
+    binding = _binding_command()
+    if os.path.exists(BINDING_PATH):
+        os.remove(BINDING_PATH)
+    bp = binding and subprocess.Popen(binding, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
     logs = {}
     failed = []
     for src, p in procs:
@@ -88,6 +118,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         logs[src] = out
         if p.returncode != 0:
             failed.append(src)
+    if bp is not None:
+        out, _ = bp.communicate()
+        if bp.returncode == 0:
+            os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
+        else:  # the same calls go through ctypes, a few microseconds slower
+            print(f"{os.path.basename(BINDING_SRC)} was not built, calls go through ctypes:\n{out}", file=sys.stderr)
     if failed:
         msg = "\n".join(f"--- {s} ---\n{logs[s]}" for s in failed)
         raise RuntimeError(f"nvcc failed for {failed}:\n{msg}")

@@ -224,6 +224,41 @@ def test_write_many_sequences_search():
 
 
 # ---------------------------------------------------------------------------
+# the calls
+# ---------------------------------------------------------------------------
+def test_call_module_and_ctypes_agree(monkeypatch):
+    """The call module makes the calls; without it the same ones go through
+    ctypes, as they do on an explicit stream.  A stream that is current is used."""
+    assert _lib._calls() is not _lib._Calls
+    q0 = _bf16((5, 4, 64), 1)
+    b = Batch([(1, 30), (4, 50)], 2, 64).fill()
+    cos_sin = torch.rand(64, 32)
+    pos = torch.tensor([29, 46, 47, 48, 49])
+
+    def run(stream=None):
+        dev = b.device()
+        q, k, v = q0.cuda(), q0[:, :2].cuda(), q0[:, 2:].contiguous().cuda()
+        kv.qk_norm_rope(q, k, pos.cuda(), cos_sin.cuda(), None, None, 1e-6, q, k, dev_status=b.status, stream=stream)
+        kv.write_fp8(k, v, *b.meta(), 4, *dev, dev_status=b.status, stream=stream)
+        out = _attend(b, q, dev, 4, stream=stream)
+        back = torch.empty_like(v), torch.empty_like(v)
+        kv.read_fp8(*dev, *b.meta(), 4, *back, dev_status=b.status, stream=stream)
+        return (q, k, out, *back, *(x.view(torch.uint8) for x in dev))
+
+    want = run()
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(other):
+        got = run()
+    other.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+    assert all(torch.equal(x, y) for x, y in zip(want, run(torch.cuda.current_stream())))
+    monkeypatch.setattr(_lib, "_fp8", _lib._Calls)
+    assert all(torch.equal(x, y) for x, y in zip(want, run()))
+    assert b.status.item() == 0
+
+
+# ---------------------------------------------------------------------------
 # read
 # ---------------------------------------------------------------------------
 @pytest.mark.parametrize("d", HEADS)
