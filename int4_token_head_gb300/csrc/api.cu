@@ -112,8 +112,8 @@ bool workspace_layout_fp8(int num_seqs, int num_q_tokens, int num_q_heads, int n
   L->ptab = take((S + 1) * 8);
   L->plist = take((L->max_pairs + kMaxPieces) * 32);
   L->msplit = take(kMaxPieces / 2 * 16);
-  const size_t least = S * Hkv * kDecodeCols, most = S * Hkv * kDecodeColsFp8, twice = 2 * T * num_q_heads;
-  L->direct_rows = least > twice ? least : most < twice ? most : twice;
+  const size_t least = S * Hkv * kDecodeCols, most = S * Hkv * kDecodeColsFp8, room = 3 * T * num_q_heads;
+  L->direct_rows = least > room ? least : most < room ? most : room;
   L->direct_o = take(L->direct_rows * D * 4);
   L->direct_ml = take(L->direct_rows * 2 * 4);
   L->warp_o = take((size_t)kMaxDecodeWarps * kDecodeCols * D * 4);

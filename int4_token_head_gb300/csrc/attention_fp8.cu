@@ -225,9 +225,9 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
     }
   }
 
-  // prefill items: 256 rows on the tensor-core kernel (head sizes up to 192:
-  // two accumulators of 256 columns would leave no TMEM for scores), 64 on the
-  // warp-MMA one
+  // prefill items: 256 rows on the tensor-core kernel (128 of head size 256: two
+  // accumulators would leave no TMEM for scores), 64 on the warp-MMA one, for
+  // tensors without a tensor map
   // Keys are split into pieces of at least four steps of the tensor-core kernel
   // (512 keys; 256 at 192), eight of the other (256 keys), where a tile may have
   // four or two such pieces (looking for splits costs 3 us per call) and there
@@ -242,7 +242,7 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
   bool tc = false, may_split = false;
   const long long pairs = L.max_pairs + kMaxPieces;
   const long long most_items = pairs * a.num_kv_heads;
-  if constexpr (D <= 192) {
+  {
     using G = Fp8Ws<D>;
     Fp8Maps maps;
     tc = may_prefill && make_maps<D>(a, G::ROWS / c.group, &maps);

@@ -249,7 +249,7 @@ struct WorkspaceLayoutFp8 {
   size_t piece_ml;      // f32 [kPieceRows][2]
   size_t total;
   int64_t max_pairs;    // prefill (sequence, tile) pairs
-  int64_t direct_rows;  // 8 columns per slot; more, up to kDecodeColsFp8, as far as the call has twice the queries
+  int64_t direct_rows;  // 8 columns per slot; up to kDecodeColsFp8 where the call's queries fill a third of them
 };
 constexpr int kDecodeColsFp8 = 32;  // most query columns per FP8 decode work unit
 constexpr int kMaxPieces = 2048;    // pieces of split prefill tiles, and their rows over all kv heads

@@ -1,11 +1,13 @@
 // Warp-specialised prefill over the FP8 cache on the 5th-generation tensor
-// cores (tcgen05), included by attention_fp8.cu for head sizes up to 192.
+// cores (tcgen05), included by attention_fp8.cu.
 //
 // One CTA per SM (all 512 TMEM columns); an item is 256 query rows (query
 // token x q head of one kv group) in two halves of 128, the MMA's M.  A step
 // is NK keys: 128 for head sizes up to 128 (a 128 x 128 score tile per half,
-// full tensor rate), 64 at 192 (the accumulators leave no more TMEM).  Twenty-six
-// warps in five roles that meet only at mbarriers:
+// full tensor rate), 64 above (the accumulators leave no more TMEM, the K and V
+// tiles no more shared memory).  At 256 an item is one half, 128 rows: two
+// accumulators would fill TMEM.  Warps in five roles that meet only at mbarriers
+// (numbers for two halves):
 //   * producer warp (24): claims items (longest first) and hands them on
 //     through a two-entry ring; TMA copies of the item's Q rows (bf16, straight
 //     into the MMA's swizzled tile) and of the step's K and V code blocks (one
@@ -29,7 +31,8 @@
 //     barrier that votes; the weights stay in registers until then, S is whole.
 // 8 causal prompts of 512 to 2048 tokens, 32/8 heads of 128: 131 us = 0.39 of the
 // measured bf16 tensor rate, about 4100 cycles per step where the MMAs need
-// 2050; what bounds it is that chain, at 54 % of the issue slots.
+// 2050; what bounds it is that chain, at 54 % of the issue slots.  Of 256, one half
+// whose chain nothing hides: 314 us for twice the operations (0.32).
 // Shared operands are K-major (Q, K) or MN-major (V) tiles [D / 64][rows][128
 // bytes] with the 16-byte chunk index XORed by row % 8.
 //
@@ -53,7 +56,8 @@
 
 template <int D>
 struct Fp8Ws {
-  static constexpr int ROWS = 256;
+  static constexpr int H = D <= 192 ? 2 : 1;  // halves of 128 rows: TMEM holds one O of 256 columns beside scores
+  static constexpr int ROWS = 128 * H;
   static constexpr int NK = D <= 128 ? 128 : 64;  // keys per step
   static constexpr int NB = NK / 16;              // cache blocks per step
   static constexpr int KB = (D + 63) / 64;        // 128-byte blocks of an f16 head vector
@@ -71,10 +75,12 @@ struct Fp8Ws {
   static constexpr int RING = (4 * NB + 4) * 4;   // K scales, log2 V scales, 1 / V scales, block flags, all usable
   static constexpr int NRING = 3;
   static constexpr int NBARS = 23;
-  static constexpr int S_COLS = NK, O_COL = 2 * NK;  // TMEM: S_h at h NK, O_h at 2 NK + h D
+  static constexpr int S_COLS = NK, O_COL = H * NK;  // TMEM: S_h at h NK, O_h at H NK + h D
   static constexpr int XCH = 2 * ROWS * 4;  // a float per row and key half: maxima, sums
   static constexpr int SMEM = QBYTES + 4 * KVBYTES + 2 * STG + NRING * RING + NBARS * 8 + 64 + XCH;
-  static constexpr int THREADS = 28 * 32;  // seven warpgroups; the last two warps only give up registers
+  static constexpr int SM_WARPS = 8 * H;  // softmax
+  // two halves: seven warpgroups; the last two warps only give up registers
+  static constexpr int THREADS = (H == 2 ? 28 : SM_WARPS + 10) * 32;
   static constexpr int CV_WARPS = 4;       // convert warps for K, and for V
   // byte offset of chunk g of key k in a stage
   __device__ static constexpr int stage_off(int k, int g) {
@@ -82,7 +88,7 @@ struct Fp8Ws {
            : CHR == 4 ? k * 64 + ((g ^ ((k >> 1) & 3)) << 4)
                       : chunk(k * CHR + g) * 16;
   }
-  static_assert(O_COL + 2 * D <= 512 && SMEM <= 227 * 1024, "TMEM and shared memory");
+  static_assert(O_COL + H * D <= 512 && SMEM <= 227 * 1024, "TMEM and shared memory");
 };
 
 __device__ __forceinline__ uint32_t fp8_sw128(int rows, int r, int c) {
@@ -209,7 +215,7 @@ struct Fp8Maps {
 };
 
 template <int D>
-__global__ void __launch_bounds__(28 * 32, 1)
+__global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
     prefill_ws_fp8_kernel(Common c, PlanView pv, const __grid_constant__ Fp8Maps maps) {
   using G = Fp8Ws<D>;
   constexpr int KSTEPS = D / 16;
@@ -247,7 +253,7 @@ __global__ void __launch_bounds__(28 * 32, 1)
       mbar_init(bar(SFULL + b), 1);
       mbar_init(bar(PFULL + b), 8);
       mbar_init(bar(IFULL + b), 1);
-      mbar_init(bar(IFREE + b), 16 + 2 * G::CV_WARPS + 1);
+      mbar_init(bar(IFREE + b), G::SM_WARPS + 2 * G::CV_WARPS + 1);
       mbar_init(bar(RKFULL + b), 1);  // RKFULL, RVFULL
       mbar_init(bar(RKFREE + b), G::CV_WARPS);
     }
@@ -282,11 +288,11 @@ __global__ void __launch_bounds__(28 * 32, 1)
     if (lane == 0) fp8_arrive(bar(IFREE + e));
     return item.seq >= 0;
   };
-  // registers: 72 a thread at launch (896 threads, 64,512); the softmax
-  // warpgroups take 80, the others 56 (512 x 80 + 384 x 56 = 62,464)
-  if (warp < 16) {
+  // registers, with two halves: 72 a thread at launch (896 threads, 64,512); the
+  // softmax warpgroups take 80, the others 56 (512 x 80 + 384 x 56 = 62,464)
+  if (warp < G::SM_WARPS) {
     // ======================= softmax warpgroups =======================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 80;\n");
+    if constexpr (G::H == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 80;\n");
     uint32_t ph_sfull = 0, ph_odone = 0, ph_ifull = 0;
     const float cf = fabsf(c.qscale);  // its sign is in K
     const int hf = warp >> 3, kh = (warp >> 2) & 1;  // query half, key half
@@ -500,12 +506,12 @@ __global__ void __launch_bounds__(28 * 32, 1)
     }
   } else {
     // ============== convert, producer and MMA warps ==============
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
+    if constexpr (G::H == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
     // waits for completions of a barrier pair indexed by step parity, counted
     auto wait_until = [&](int first, int& done, int count) {
       for (; done < count; done++) fp8_wait(bar(first + (done & 1)), (done >> 1) & 1, abort_flag, c.status);
     };
-    if (warp < 24) {
+    if (warp < G::SM_WARPS + 2 * G::CV_WARPS) {
       // ================= convert warps =================
       // one team's loop: kv = 0 K codes, 1 V codes
       auto team = [&](auto kv_tag) {
@@ -582,11 +588,11 @@ __global__ void __launch_bounds__(28 * 32, 1)
           }
         }
       };
-      if (warp < 20)
+      if (warp < G::SM_WARPS + G::CV_WARPS)
         team(std::integral_constant<int, 0>{});
       else
         team(std::integral_constant<int, 1>{});
-    } else if (warp == 24) {
+    } else if (warp == G::SM_WARPS + 8) {
       // ================= producer warp =================
       uint32_t ph_ifree = 0;
       int n = 0, nq = 0, kfree = 0;
@@ -675,7 +681,7 @@ __global__ void __launch_bounds__(28 * 32, 1)
       if (n > 0 && !(mbar_wait_bounded(bar(RKFULL), (n - 1) & 1) && mbar_wait_bounded(bar(RVFULL), (n - 1) & 1) &&
                      mbar_wait_bounded(bar(QFULL), (nq - 1) & 1)))
         flag(c.status, KV_INT4_DEV_TIMEOUT);
-    } else if (warp == 25) {
+    } else if (warp == G::SM_WARPS + 9) {
       // ================= MMA warp =================
       uint32_t lead;
       asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(lead));
@@ -731,18 +737,19 @@ __global__ void __launch_bounds__(28 * 32, 1)
             fp8_wait_warp(bar(i), ph, abort_flag, c.status, idle);
           }
 #pragma unroll 1
-          for (int hh = 0; hh < 2; hh++) {
-            if (wv && hh) wait(PFULL + 1, pfull++ & 1);
+          for (int hh = 0; hh < G::H; hh++) {
+            if (wv && hh) wait(PFULL + 1, pfull & 1);
             tc_fence_after();
             if (wv) {
               issue_wv(hh, (n - 1) & 1, st == 1);
-              if (hh) fp8_commit(lead, bar(VFREE + ((n - 1) & 1)));
+              if (hh == G::H - 1) fp8_commit(lead, bar(VFREE + ((n - 1) & 1)));
             }
             if (sc) {
               issue_s(hh, n & 1);
               fp8_commit(lead, bar(SFULL + hh));
             }
           }
+          if (wv) pfull++;
           if (sc) {
             fp8_commit(lead, bar(KFREE + (n & 1)));
             n++;
@@ -754,7 +761,7 @@ __global__ void __launch_bounds__(28 * 32, 1)
       }
     }
   }
-  if (warp == 25) {
+  if (warp == G::SM_WARPS + 9) {
     // after a time-out MMAs may still be in flight: they end by themselves
     // and must end before the columns are freed
     if (lane == 0) umma_commit(bar(DRAIN));

@@ -402,6 +402,19 @@ def test_prefill_of_many_sequences(d, n):
 
 
 @pytest.mark.parametrize("d", HEADS)
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 60)])
+def test_prefill_of_broadcast_queries(d, causal, window):
+    """One row as every token's queries (stride 0), which no tensor map holds:
+    prefill without copies by the tensor memory accelerator."""
+    b = Batch([(70, 90), (100, 1500), (40, 2600), (1, 200), (0, 7), (50, 50)] + [(64, 0)] * (not causal), 2, d).fill(1)
+    row = _bf16((1, 6, d), 2)
+    out = _attend(b, row.cuda().expand(b.tokens, 6, d), b.device(), 6, causal, window)
+    q = row.double().numpy().repeat(b.tokens, 0)
+    ref, bound = F.attention(q, b.host(), b.table, b.lens, b.start, d ** -0.5, causal, window)
+    _assert_attention(out, ref, bound)
+
+
+@pytest.mark.parametrize("d", HEADS)
 def test_prefill_split_repeats_bits_and_skips_bad_blocks(d):
     b = Batch([(40, 3500), (5, 4100)], 2, d).fill(1)
     q = _bf16((b.tokens, 10, d), 2).cuda()
