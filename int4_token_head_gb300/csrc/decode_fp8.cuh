@@ -20,8 +20,8 @@
 // by ldmatrix.trans of byte pairs (one byte permute and two conversions per
 // four codes).
 //
-// Memory-bound: 32 x 32768 keys, 32/8 heads of 128, 2.15 GB of codes: 338 us a
-// call = 0.94 of the measured copy bandwidth.  More columns cost issue slots, as
+// Memory-bound: 32 x 32768 keys, 32/8 heads of 128, 2.15 GB of codes: 340 us a
+// call = 0.93 of the measured copy bandwidth.  More columns cost issue slots, as
 // every warp converts the codes for its own eight: 32 x 1 token of group 16
 // against 2048-4096 keys 43 us (floor 15; in 256-row prefill tiles 84).
 template <int D, int NP>

@@ -402,6 +402,42 @@ def test_prefill_of_many_sequences(d, n):
 
 
 @pytest.mark.parametrize("d", HEADS)
+def test_captured_splits_follow_the_lengths(d):
+    """Graphs of a call whose tiles are split and of one that decodes many columns,
+    in one workspace, replayed in turn after the lengths changed on the device."""
+    graphs, calls = [], []
+    ws = None
+    for seqs, hq, hkv in (([(50, 3000), (40, 4000), (1, 30)], 4, 2), ([(3, 3000), (1, 700), (2, 2)], 16, 2)):
+        b = Batch(seqs, hkv, d).fill(2)
+        q = _bf16((b.tokens, hq, d), 3)
+        dev, (table, lens, start) = b.device(), b.meta()
+        out = torch.empty(b.tokens, hq, d, dtype=torch.bfloat16, device="cuda")
+        if ws is None:
+            ws = torch.empty(kv.attention_workspace_size(3, 120, 16, 2, d), dtype=torch.uint8, device="cuda")
+        qc = q.cuda()
+
+        def call(qc=qc, dev=dev, table=table, lens=lens, start=start, b=b, out=out):
+            kv.attention_fp8(qc, *dev, table, lens, start, b.max_len, int(b.lens.max()), d ** -0.5, True, out, ws,
+                             dev_status=b.status)
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        graphs.append(g)
+        calls.append((b, q, lens, out, call))  # with every tensor that the graph reads
+    for step in range(3):
+        for g, (b, q, lens, out, _) in zip(graphs, calls):
+            now = np.maximum(b.lens - 700 * step, np.diff(b.start)).astype(np.int32)
+            lens.copy_(torch.from_numpy(now))
+            out.fill_(float("nan"))
+            g.replay()
+            ref, bound = F.attention(q.double().numpy(), b.host(), b.table, now, b.start, d ** -0.5, True)
+            _assert_attention(out, ref, bound)
+            assert b.status.item() == 0
+
+
+@pytest.mark.parametrize("d", HEADS)
 @pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 60)])
 def test_prefill_of_broadcast_queries(d, causal, window):
     """One row as every token's queries (stride 0), which no tensor map holds:
