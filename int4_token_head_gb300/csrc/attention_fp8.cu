@@ -230,12 +230,16 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
   // tensors without a tensor map
   // Keys are split into pieces of at least four steps of the tensor-core kernel
   // (512 keys; 256 at 192), eight of the other (256 keys), where a tile may have
-  // four or two such pieces (looking for splits costs 3 us per call) and there
-  // are fewer tiles than the schedule leaves whole anyway (sequences decoded
-  // here have at most dcols / group tokens)
+  // four such pieces (looking for splits costs 1 to 3 us per call), two where the
+  // query rows fill less than half of the CTAs (2 x 16 tokens against 1322 keys,
+  // 64/4 heads of 192: 36 us, in pieces 25; 2 prompts of 1221 tokens, 8/4 heads of
+  // 128: 43, 44), and there are fewer tiles than the schedule leaves whole anyway
+  // (sequences decoded here have at most dcols / group tokens)
   const long long most_decode = any_decode ? (long long)a.num_seqs * (c.dcols / c.group) : 0;
-  auto can_split = [&](int pieces) {
+  auto can_split = [&] {
     const long long tiles = (a.num_q_tokens - most_decode + c.tile_tokens - 1) / c.tile_tokens;
+    const long long rows = (long long)a.num_q_tokens * a.num_q_heads;
+    const int pieces = rows <= c.split_ctas / 2 * (long long)c.tile_tokens * c.group ? 2 : 4;
     return may_prefill && a.max_seq_len > 16ll * c.step_blocks * c.split_steps * pieces && tiles <= kSplitTiles &&
            tiles * a.num_kv_heads < (long long)kSplitWaves * c.split_ctas;
   };
@@ -256,7 +260,7 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
       if (!occ_c.get(dev, [](int* o) { return configure_tmem(prefill_ws_fp8_kernel<D>, G::SMEM, G::THREADS, 512, o); },
                      &occ))
         return KV_INT4_ERR_CUDA;
-      may_split = can_split(4);
+      may_split = can_split();
       if (int e = launch_plan(c, pv, may_prefill, may_split, stream)) return e;
       const long long grid = sms < most_items ? sms : most_items;
       timing_begin(kTimedPrefill, stream);
@@ -279,7 +283,7 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
     c.step_blocks = G::NB;
     c.split_steps = 8;
     c.split_ctas = (int)grid;
-    may_split = can_split(2);
+    may_split = can_split();
     if (int e = launch_plan(c, pv, may_prefill, may_split, stream)) return e;
     if (may_prefill) {
       if (grid > most_items) grid = most_items;
