@@ -24,11 +24,12 @@
 //     what bounds a step; 4700 cycles with one thread per row).  With
 //     f_b = |softmax_scale| log2 e ks_b (a negative scale's sign is in K) and
 //     kv_b per block, a weight is exp2(fma(s, f_b, kv_b - m_ref)).  m_ref moves to
-//     the row's maximum (and its O in TMEM is rescaled) only when a step's
-//     weights add up to more than 2^14: they stay inside f16 whatever the V
-//     scales, and most steps need no maximum (one fma, one exp2, one add and
-//     half a conversion per score).  The two warps of a row agree on that by a
-//     barrier that votes; the weights stay in registers until then, S is whole.
+//     the row's maximum (and its O in TMEM is rescaled) only in the step where the
+//     row first sees a usable key and when a step's weights add up to more than
+//     2^14: they stay inside f16 whatever the V scales, and most steps need no
+//     maximum (one fma, one exp2, one add and half a conversion per score).  The
+//     two warps of a row agree on that by a barrier that votes; the weights stay
+//     in registers until then, S is whole.
 // 8 causal prompts of 512 to 2048 tokens, 32/8 heads of 128: 131 us = 0.39 of the
 // measured bf16 tensor rate, about 4100 cycles per step where the MMAs need
 // 2050; what bounds it is that chain, at 54 % of the issue slots.  Of 256, one half
@@ -329,7 +330,8 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
       const int qp = ctx + tok0 + (rok ? j : 0);
       // the row sees positions [lo, lim), counted from this thread's first key
       int lim = (c.causal ? min(L, qp + 1) : L) - kb0 * 16 - NC * kh, lo = window_lo(c, qp) - kb0 * 16 - NC * kh;
-      float m_ref = -INFINITY, l_run = 0.f;
+      // rows that are not there never ask for a reference: theirs is above everything
+      float m_ref = rok ? -INFINITY : INFINITY, l_run = 0.f;
 #pragma unroll 1
       for (int st = 0; st < nsteps; st++, n++, lim -= NK, lo -= NK) {
         const float* re = reinterpret_cast<const float*>(ring + (n % G::NRING) * G::RING) + NBH * kh;
@@ -342,7 +344,8 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
         // the warp's rows all see all its keys: no mask (the usual case)
         const bool full = __all_sync(0xffffffffu, lo <= 0 && lim >= NC && ok[NB - NBH * kh] != 0);
         // the scores of block b, hidden ones -inf, and their factor (never 0, so
-        // that -inf stays)
+        // that -inf stays); seen: whether the row sees a usable key of this thread's
+        bool seen = full;
         auto scores = [&](int b, float (&s)[16], float& f) {
           f = fmaxf(cf * re[b], FLT_MIN);
           uint32_t x[16];
@@ -355,6 +358,7 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
             uint32_t vis = first <= 0 ? 0xffffu : first >= 16 ? 0u : 0xffffu << first;
             vis &= last >= 16 ? 0xffffu : last <= 0 ? 0u : 0xffffu >> (16 - last);
             if (!ok[b]) vis = 0;
+            seen |= vis != 0;
 #pragma unroll
             for (int k = 0; k < 16; k++)
               if (!(vis & (1u << k))) s[k] = -INFINITY;
@@ -418,9 +422,10 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
             tot += both;
             add = fmaf(both, ivs[b], add);
           }
-          // the weights' sum bounds the largest; a row without a reference that
-          // sees keys now needs one
-          if (find || !pair_any(tot > 16384.f || (m_ref == -INFINITY && tot > 0.f))) break;
+          // the weights' sum bounds the largest; a row without a reference needs one
+          // as soon as it sees a usable key, whatever the weights came to: against 0
+          // they vanish where every score is far below it
+          if (find || !pair_any(tot > 16384.f || (m_ref == -INFINITY && seen))) break;
           find = true;
         }
         l_run += add;

@@ -857,3 +857,54 @@ def test_negative_and_zero_softmax_scale(d):
             out = _attend(b, q.cuda(), b.device(), 4, scale=scale)
             ref, bound = F.attention(q.double().numpy(), b.host(), b.table, b.lens, b.start, scale, True)
             _assert_attention(out, ref, bound)
+
+
+# ---------------------------------------------------------------------------
+# logits far from zero
+# ---------------------------------------------------------------------------
+def _far(seqs, hkv, group, d, logit, seed=0, v_gain=1.0):
+    """A filled batch and its queries whose scores all lie near `logit`: a common
+    first element of the queries, and of the keys with its sign."""
+    b = Batch(seqs, hkv, d, seed=seed)
+    g = np.random.default_rng(seed + 1)
+    full = np.concatenate([[0], np.cumsum(b.lens)])
+    size = (abs(logit) * d ** 0.5) ** 0.5
+    for codes, scale, gain in ((b.kc, b.ks, 1.0), (b.vc, b.vs, v_gain)):
+        x = g.standard_normal((int(full[-1]), hkv, d)) * gain
+        if codes is b.kc:
+            x[..., 0] = math.copysign(size, logit)
+        x = torch.from_numpy(x).to(torch.bfloat16).double().numpy()
+        F.write(x, b.table, b.lens, full, codes, scale)
+    q = _bf16((b.tokens, hkv * group, d), seed + 2)
+    q[..., 0] = size
+    return b, q
+
+
+@pytest.mark.parametrize("d", HEADS)
+@pytest.mark.parametrize("group", [1, 2])
+@pytest.mark.parametrize("window", [1, 20, 100])
+@pytest.mark.parametrize("logit,v_gain", [(-100, 1.0), (-300, 1.0), (-60, 2.0 ** -50), (300, 1.0)])
+def test_windows_where_every_logit_is_far_from_zero(d, group, window, logit, v_gain):
+    """Softmax does not depend on a common offset: rows of a tile whose window
+    starts behind the tile's first keys, prefill and decode alike."""
+    for seqs, causal in (([(300, 300), (5, 260), (1, 200), (140, 500)], True), ([(280, 300), (1, 90)], False)):
+        b, q = _far(seqs, 2, group, d, logit, seed=window, v_gain=v_gain)
+        out = _attend(b, q.cuda(), b.device(), 2 * group, causal=causal, window=window)
+        ref, bound = F.attention(q.double().numpy(), b.host(), b.table, b.lens, b.start, d ** -0.5, causal, window)
+        _assert_attention(out, ref, bound)
+        assert b.status.item() == 0
+
+
+@pytest.mark.parametrize("d", HEADS)
+@pytest.mark.parametrize("bad", [8, 17])
+@pytest.mark.parametrize("logit", [-100, -300])
+def test_first_blocks_unusable_where_every_logit_is_far_from_zero(d, bad, logit):
+    """The rows' first usable keys come a step or more after the tile's first."""
+    b, q = _far([(250, 400), (40, 300), (1, 350)], 2, 2, d, logit)
+    table, lens, start = b.meta()
+    table[:, :bad] = -1
+    for causal in (True, False):
+        out = _attend(b, q.cuda(), b.device(), 4, causal=causal, meta=(table, lens, start))
+        ref, bound = F.attention(q.double().numpy(), b.host(), table.cpu().numpy(), b.lens, b.start, d ** -0.5, causal)
+        _assert_attention(out, ref, bound)
+    assert b.status.item() == _lib.DEV_BAD_BLOCK
