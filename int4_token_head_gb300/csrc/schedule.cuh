@@ -125,9 +125,11 @@ __device__ __forceinline__ long long div_nn(long long n, long long d) {
   return ((n | d) >> 31) == 0 ? (long long)((uint32_t)n / (uint32_t)d) : n / d;
 }
 
-// first key position visible to the query at position qpos
+// first key position visible to the query at position qpos, which is below 0
+// where queries outnumber keys: nothing is subtracted from it then (with a
+// window near 2^31 the difference would wrap to a position behind every key)
 __device__ __forceinline__ int window_lo(const Common& c, int qpos) {
-  return c.window > 0 ? max(0, qpos - c.window + 1) : 0;
+  return c.window > 0 && qpos >= c.window ? qpos - c.window + 1 : 0;
 }
 // first 16-key block a sequence's attention reads: blocks wholly before the
 // window of its earliest query (position L - q_len) are never visible

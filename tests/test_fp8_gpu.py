@@ -908,3 +908,15 @@ def test_first_blocks_unusable_where_every_logit_is_far_from_zero(d, bad, logit)
         ref, bound = F.attention(q.double().numpy(), b.host(), table.cpu().numpy(), b.lens, b.start, d ** -0.5, causal)
         _assert_attention(out, ref, bound)
     assert b.status.item() == _lib.DEV_BAD_BLOCK
+
+
+@pytest.mark.parametrize("d", HEADS)
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 4, 2 ** 30])
+def test_windows_wider_than_any_sequence(d, window):
+    """The largest windows hide nothing, of queries before the first key neither."""
+    for seqs, hq, hkv in (([(9, 4), (2, 30), (1, 0)], 2, 2),               # one launch
+                          ([(5, 1), (8, 3000), (7, 0), (3, 2)], 8, 2),     # planned decode of many columns
+                          ([(300, 5), (40, 200), (20, 0), (1, 1)], 4, 2),  # prefill
+                          ([(33, 2900), (70, 3)], 4, 2)):                  # tiles split over their keys
+        _check(seqs, hq, hkv, d, causal=False, window=window, seed=d)
+    _check([(30, 60), (1, 90), (7, 7)], 4, 2, d, window=window, seed=d)
