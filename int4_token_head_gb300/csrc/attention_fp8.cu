@@ -37,7 +37,16 @@ template <int PREFILL>
 __global__ void __launch_bounds__(kPrepThreads) plan_fp8_kernel(Common c, PlanView pv) {
   pdl_trigger();
   pdl_wait();
+  // The schedule's number: another one for every schedule built in this
+  // workspace, whatever the memory held before.  Who reads it with acquire
+  // sees the schedule and all that the kernels before it wrote
+  int number = 0;
+  if (PREFILL > 0 && threadIdx.x == 0) number = pv.plan[5];
   build_schedule<true, PREFILL>(c, pv);
+  if constexpr (PREFILL > 0) {
+    __syncthreads();
+    if (threadIdx.x == 0) st_release(&pv.plan[5], number + 1);
+  }
 }
 
 // A query row's power of two from its largest bf16 magnitude bits: rows are

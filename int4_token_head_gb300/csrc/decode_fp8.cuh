@@ -151,10 +151,30 @@ __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
   const int g = lane >> 2, cq = lane & 3;
   const int SB = G::slot_bytes(HG);
   pdl_trigger();
-  // After a prefill launch, which waits for the schedule before it lets this
-  // kernel in, decode runs beside it (on the SMs that prefill leaves) and waits
-  // for it only at its end, so that what follows comes after both
-  if (!prm.beside) pdl_wait();
+  // After a prefill launch decode runs beside it (on the SMs that prefill leaves)
+  // and waits for it only at its end, so that what follows comes after both.
+  // Before that wait it may rely on nothing but what it acquires: the schedule's
+  // number, published by the schedule once that is complete, and with it the
+  // schedule and everything written before.  Prefill lets this kernel in after
+  // its own wait for the schedule, so that the number read is this call's; the
+  // wait at the end shows whether it was, and if not the work is done again
+  bool beside = !DIRECT && prm.beside;
+  int32_t number = 0;
+  if (beside) {
+    if (lane == 0) number = ld_acquire(&pv.plan[5]);
+    __syncwarp();
+    number = __shfl_sync(0xffffffffu, number, 0);
+  } else {
+    pdl_wait();
+  }
+  // the end of the kernel: whether the work was done on this call's schedule
+  auto done = [&]() -> bool {
+    if (!beside) return true;
+    pdl_wait();
+    beside = false;
+    return !__syncthreads_or(ld_acquire(&pv.plan[5]) != number);
+  };
+again:
   int* sflag = reinterpret_cast<int*>(smem + G::NS * SB);
 
   Fp8Walk cw;
@@ -184,8 +204,8 @@ __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
   } else {
     const int n_dseq = pv.plan[0];
     if (n_dseq == 0) {
-      if (prm.beside) pdl_wait();
-      return;
+      if (done()) return;
+      goto again;
     }
     const int gpl = c.ng / c.nl;  // head groups per lane
     const int my_lane = blockIdx.x % c.nl, rr = blockIdx.x / c.nl;
@@ -193,8 +213,8 @@ __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
     const int R = prm.num_ctas / c.nl;
     const long long P0 = Tu * rr / R, P1 = Tu * (rr + 1) / R;
     if (P0 >= P1) {
-      if (prm.beside) pdl_wait();
-      return;
+      if (done()) return;
+      goto again;
     }
     nunits = (int)(P1 - P0);
 
@@ -572,7 +592,7 @@ __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
     if (cs >= G::NS) cs -= G::NS;
   }
   cp_async_wait<0>();
-  if (prm.beside) pdl_wait();
+  if (!done()) goto again;
   if constexpr (DIRECT) {
     __syncthreads();
     flush();

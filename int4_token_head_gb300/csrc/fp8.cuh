@@ -18,6 +18,17 @@ namespace kvint4 {
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 
+// A kernel that starts on work before its pdl_wait may use what it has found
+// published by st_release with ld_acquire, and what the publisher could see.
+__device__ __forceinline__ void st_release(int32_t* p, int32_t v) {
+  asm volatile("st.release.gpu.global.s32 [%0], %1;\n" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ int32_t ld_acquire(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];\n" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // launches on `stream` with that permission, as clusters of `cluster` CTAs;
 // KV_INT4_OK or KV_INT4_ERR_CUDA
 template <typename... P, typename... A>

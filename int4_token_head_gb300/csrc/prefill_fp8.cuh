@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(Fp8Pre<D>::THREADS) prefill_fp8_kernel(Common 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, cq = lane & 3;
   pdl_wait();
-  pdl_trigger();  // after the wait: the decode beside this kernel relies on the schedule
+  pdl_trigger();  // after the wait: the decode beside this kernel looks for the schedule
   const int n_items = pv.plan[1];
 
 #pragma unroll 1

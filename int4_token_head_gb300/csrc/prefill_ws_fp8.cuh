@@ -265,8 +265,8 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
     fence_mbar_init();
   }
   // shared memory and TMEM are this CTA's own; the schedule and the caches come
-  // from the kernels before.  The next kernel (decode) is let in after the wait:
-  // it may rely on the schedule being complete
+  // from the kernels before.  The next kernel (decode) is let in after the wait,
+  // so that it finds the schedule published
   pdl_wait();
   pdl_trigger();
   if (warp == 0) tmem_alloc(smem_addr(tslot), 512);

@@ -13,7 +13,8 @@ namespace kvint4 {
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct PlanView {
-  int32_t* plan;      // [0] n_dseq, [1] n_prefill_items, [2] prefill work counter, [3] n_pseq
+  int32_t* plan;      // [0] n_dseq, [1] n_prefill_items, [2] prefill work counter, [3] n_pseq,
+                      // FP8: [4] split tiles, [5] the schedule's number in this workspace
   int4* msplit;       // FP8: tiles in pieces: (sequence, tile, first piece row, pieces); plan[4] of them
   struct PrefillPiece* pieces;  // FP8: prefill tiles and pieces of tiles, longest first (in place of plist)
   float* piece_o;

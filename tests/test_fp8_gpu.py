@@ -920,3 +920,66 @@ def test_windows_wider_than_any_sequence(d, window):
                           ([(33, 2900), (70, 3)], 4, 2)):                  # tiles split over their keys
         _check(seqs, hq, hkv, d, causal=False, window=window, seed=d)
     _check([(30, 60), (1, 90), (7, 7)], 4, 2, d, window=window, seed=d)
+
+
+# ---------------------------------------------------------------------------
+# decode beside prefill
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("d", HEADS)
+def test_decode_beside_prefill_sees_what_was_written_just_before(d):
+    """Mixed calls whose queries, keys, values, table, lengths and schedule change
+    from call to call in the same memory, nothing waited for in between, eager
+    and replayed: the bits of a call that had the GPU to itself."""
+    hq, hkv = 8, 2
+    shapes = [[(1, 400), (90, 200), (1, 90), (1, 700), (40, 300)], [(60, 60), (1, 30), (1, 900), (70, 500), (1, 64)],
+              [(1, 16), (1, 17), (128, 150), (3, 800), (1, 333)]]
+    tokens = max(sum(n for n, _ in seqs) for seqs in shapes)
+    batches = [Batch(seqs, hkv, d, seed=i).fill(i + 1) for i, seqs in enumerate(shapes)]
+    nb, width = max(b.nb for b in batches), max(b.table.shape[1] for b in batches)
+
+    def padded(b, seed):
+        """One shape for all: spare blocks, table columns and tokens behind."""
+        codes = [np.concatenate([x, np.full((nb - b.nb, *x.shape[1:]), 0xFF, np.uint8)]) for x in (b.kc, b.vc)]
+        scales = [np.concatenate([x, np.full((nb - b.nb, hkv), np.nan, np.float32)]) for x in (b.ks, b.vs)]
+        table = np.pad(b.table, ((0, 0), (0, width - b.table.shape[1])), constant_values=-1)
+        return [torch.from_numpy(np.ascontiguousarray(x)).cuda() for x in (*codes, *scales, table, b.lens, b.start)] + [
+            _bf16((tokens, hq, d), seed).cuda()]
+
+    inputs = [padded(b, 10 + i) for i, b in enumerate(batches)]
+    live = [x.clone() for x in inputs[0]]
+    out = torch.empty(tokens, hq, d, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(kv.attention_workspace_size(5, tokens, hq, hkv, d), dtype=torch.uint8, device="cuda")
+    new = [(_bf16((tokens, hkv, d), 20 + i).cuda(), _bf16((tokens, hkv, d), 30 + i).cuda()) for i in range(3)]
+    new_k, new_v = (x.clone() for x in new[0])
+
+    def step():
+        kc, vc, ks, vs, table, lens, start, q = live
+        kv.write_fp8(new_k, new_v, table, lens, start, 128, kc, vc, ks, vs, dev_status=status)
+        kv.attention_fp8(q, kc, vc, ks, vs, table, lens, start, 128, 900, d ** -0.5, True, out, ws, dev_status=status)
+
+    def load(i):
+        for x, y in zip((*live, new_k, new_v), (*inputs[i], *new[i])):
+            x.copy_(y)
+
+    want = []
+    for i in range(3):
+        load(i)
+        torch.cuda.synchronize()
+        ws.fill_(0xFF)
+        step()
+        torch.cuda.synchronize()
+        want.append(out[:batches[i].tokens].clone())
+        assert torch.isfinite(want[i]).all()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for run in (step, graph.replay):
+        got = []
+        for n in range(12):
+            load(n % 3)
+            run()
+            got.append(out[:batches[n % 3].tokens].clone())
+        for n, x in enumerate(got):
+            assert torch.equal(x, want[n % 3])
+    assert status.item() == 0
