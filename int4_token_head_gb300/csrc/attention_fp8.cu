@@ -8,8 +8,9 @@
 // maximum M of t, the weights w_p = 2^(t_p - M) never exceed 1, whatever the
 // V scales are, so they fit f16 MMA operands without a range limit on V; the
 // denominator in the same units is sum_b 2^-kv_b sum_{p in b} w_p (a block's
-// sum times a power of two, fp32).  A score costs one FMA (scale and kv
-// together) and one exp2.
+// sum times a power of two, fp32; blocks of small kv_b, whose weights beside large
+// ones may leave fp32, have theirs summed again in larger units).  A score costs
+// one FMA (scale and kv together) and one exp2.
 // Queries are used at full precision: the tensor-core prefill multiplies them
 // as they are (bf16, K codes converted to bf16); the warp-MMA kernels divide a
 // row by the power of two of its largest magnitude (bf16 to f16, exact but for

@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
     if (!beside) return true;
     pdl_wait();
     beside = false;
-    return !__syncthreads_or(ld_acquire(&pv.plan[5]) != number);
+    return !__syncthreads_or(*const_cast<volatile int32_t*>(&pv.plan[5]) != number);
   };
 again:
   int* sflag = reinterpret_cast<int*>(smem + G::NS * SB);
@@ -389,10 +389,10 @@ again:
         const float p0 = __shfl_xor_sync(0xffffffffu, mm0, x), p1 = __shfl_xor_sync(0xffffffffu, mm1, x);
         const float n0 = fmaxf(mm0, p0), n1 = fmaxf(mm1, p1);
         const float u0 = n0 == -INFINITY ? 0.f : n0, u1 = n1 == -INFINITY ? 0.f : n1;
-        const float sa0 = fast_exp2(mm0 - u0), sb0 = fast_exp2(p0 - u0);
-        const float sa1 = fast_exp2(mm1 - u1), sb1 = fast_exp2(p1 - u1);
-        a0 = a0 * sa0 + __shfl_xor_sync(0xffffffffu, a0, x) * sb0;
-        a1 = a1 * sa1 + __shfl_xor_sync(0xffffffffu, a1, x) * sb1;
+        const Exp2Pair ea0(mm0 - u0), eb0(p0 - u0), ea1(mm1 - u1), eb1(p1 - u1);
+        const float sa0 = ea0.both(), sb0 = eb0.both(), sa1 = ea1.both(), sb1 = eb1.both();
+        a0 = ea0.of(a0) + eb0.of(__shfl_xor_sync(0xffffffffu, a0, x));
+        a1 = ea1.of(a1) + eb1.of(__shfl_xor_sync(0xffffffffu, a1, x));
 #pragma unroll
         for (int i = 0; i < G::KSTEPS; i++) {
           oacc[i][0] = oacc[i][0] * sa0 + __shfl_xor_sync(0xffffffffu, oacc[i][0], x) * sb0;
@@ -511,7 +511,9 @@ again:
     const int pos0 = (kb0 + jb) * 16 + g, pos1 = pos0 + 8;
     const float f0 = cf0 * ks, f1 = cf1 * ks;
     const float kvf = (float)exp_of(vs);                                  // log2 of the V scale
-    const float ivs = __uint_as_float((254u << 23) - (__float_as_uint(vs) & 0x7f800000u));  // its reciprocal
+    const bool low = vs < exp2_int(kFp8LowExp);
+    // its reciprocal; 0 where the denominator's share is taken below
+    const float ivs = low ? 0.f : __uint_as_float((254u << 23) - (__float_as_uint(vs) & 0x7f800000u));
     float t00 = fmaf(sa[0], f0, kvf), t01 = fmaf(sa[1], f1, kvf);
     float t10 = fmaf(sa[2], f0, kvf), t11 = fmaf(sa[3], f1, kvf);
     // keys outside a column's visible range (or in an unusable or absent
@@ -526,26 +528,33 @@ again:
     }
     float mx0 = fmaxf(t00, t10), mx1 = fmaxf(t01, t11);
     // exact running max: reduced across the key lanes only when some lane
-    // holds a value above its column's current max
-    if (__any_sync(0xffffffffu, mx0 > m0 || mx1 > m1)) {
+    // holds a value above its column's current max (or one of a small V scale)
+    if (__any_sync(0xffffffffu, mx0 > m0 || mx1 > m1 || low)) {
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) {
         mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
         mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
       }
       const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
-      const float al0 = mn0 == -INFINITY ? 1.f : fast_exp2(m0 - mn0);  // a column with no key yet keeps -inf
-      const float al1 = mn1 == -INFINITY ? 1.f : fast_exp2(m1 - mn1);
+      const Exp2Pair e0(mn0 == -INFINITY ? 0.f : m0 - mn0);  // a column with no key yet keeps -inf
+      const Exp2Pair e1(mn1 == -INFINITY ? 0.f : m1 - mn1);
+      const float al0 = e0.both(), al1 = e1.both();
       m0 = mn0;
       m1 = mn1;
-      l0 *= al0;
-      l1 *= al1;
+      l0 = e0.of(l0);
+      l1 = e1.of(l1);
 #pragma unroll
       for (int i = 0; i < G::KSTEPS; i++) {
         oacc[i][0] *= al0;
         oacc[i][1] *= al1;
         oacc[i][2] *= al0;
         oacc[i][3] *= al1;
+      }
+      if (low) {
+        const float up0 = (float)kFp8LowExp - kvf - (m0 == -INFINITY ? 0.f : m0);
+        const float up1 = (float)kFp8LowExp - kvf - (m1 == -INFINITY ? 0.f : m1);
+        l0 = fmaf(fast_exp2(t00 + up0) + fast_exp2(t10 + up0), exp2_int(-kFp8LowExp), l0);
+        l1 = fmaf(fast_exp2(t01 + up1) + fast_exp2(t11 + up1), exp2_int(-kFp8LowExp), l1);
       }
     }
     const float mu0 = m0 == -INFINITY ? 0.f : m0, mu1 = m1 == -INFINITY ? 0.f : m1;
@@ -624,10 +633,11 @@ again:
         for (int sub = 0; sub < SUB; sub++) {
           const float mn = fmaxf(M, mw[sub]);
           const float mu = mn == -INFINITY ? 0.f : mn;
-          const float a = fast_exp2(M - mu), b = fast_exp2(mw[sub] - mu);
+          const Exp2Pair ea(M - mu), eb(mw[sub] - mu);
+          const float a = ea.both(), b = eb.both();
 #pragma unroll
           for (int k = 0; k < PER; k++) acc[k] = acc[k] * a + o[sub][k] * b;
-          Ls = Ls * a + lw[sub] * b;
+          Ls = ea.of(Ls) + eb.of(lw[sub]);
           M = mn;
         }
       }
@@ -706,14 +716,15 @@ __device__ void merge_prefill_pieces(const Common& c, const PlanView& pv, int fi
       for (int k0 = 0; k0 < P; k0 += 32) {
         float2 ml = make_float2(-INFINITY, 0.f);
         if (k0 + lane < P) ml = *reinterpret_cast<const float2*>(pv.piece_ml + 2 * (at + (long long)(k0 + lane) * rows));
-        const float a = fast_exp2(ml.x - mu);
+        const Exp2Pair e(ml.x - mu);
+        const float a = e.both(), la = e.of(ml.y);
 #pragma unroll 4
         for (int k = 0; k < min(32, P - k0); k++) {
           const float ak = __shfl_sync(0xffffffffu, a, k);
           const float* o = pv.piece_o + (at + (long long)(k0 + k) * rows) * D;
 #pragma unroll
           for (int i = 0; i < PER; i++) acc[i] = fmaf(o[lane + 32 * i], ak, acc[i]);
-          Ls = fmaf(__shfl_sync(0xffffffffu, ml.y, k), ak, Ls);
+          Ls += __shfl_sync(0xffffffffu, la, k);
         }
       }
       const float inv = Ls == 0.f ? 0.f : 1.f / Ls;  // no visible key: zeros
@@ -776,10 +787,11 @@ __global__ void __launch_bounds__(1024) merge_fp8_kernel(Fp8MergeParams prm) {
   auto merge = [&](float m, float l, const float (&o)[PER]) {
     const float mn = fmaxf(M, m);
     const float mu = mn == -INFINITY ? 0.f : mn;
-    const float a = fast_exp2(M - mu), b = fast_exp2(m - mu);
+    const Exp2Pair ea(M - mu), eb(m - mu);
+    const float a = ea.both(), b = eb.both();
 #pragma unroll
     for (int k = 0; k < PER; k++) acc[k] = acc[k] * a + o[k] * b;
-    Ls = Ls * a + l * b;
+    Ls = ea.of(Ls) + eb.of(l);
     M = mn;
   };
   if (used) {

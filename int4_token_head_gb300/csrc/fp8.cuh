@@ -55,9 +55,28 @@ inline int launch_pdl(void (*kern)(P...), dim3 grid, int threads, size_t smem, c
 // Scales are 2^k with k in [kFp8MinExp, kFp8MaxExp].  E4M3 keeps four
 // significant bits at every magnitude, so a power of two loses nothing against
 // absmax / 448, and it moves codes between scales by their exponent alone
-// (exact unless a code becomes subnormal).  The range bounds 2^-k products:
-// attention sums weights in units of 2^k, which stay normal fp32 numbers.
+// (exact unless a code becomes subnormal).
 constexpr int kFp8MinExp = -60, kFp8MaxExp = 60;
+
+// Attention's weights carry their block's V scale, 2^(s + kv - M) with M the
+// largest s + kv, and the denominator takes it out again, 2^-kv times their sum.
+// M <= s_max + 61 (prefill rounds it up), so a key whose score is g below the
+// largest has a weight of at least 2^(kv - 61 - g): a normal fp32 number for
+// g <= 43 if kv >= -22.  Blocks
+// below that (of zeros, say) may weigh too little for fp32 beside a block of large
+// V and still count in the denominator: their share is summed from weights in
+// units of 2^-22.  Their products with V are below fp32's range then, as they
+// should be.
+constexpr int kFp8LowExp = -22;
+
+// 2^d, d <= 0, as two factors: a sum in units of 2^-kv times one and then the
+// other keeps what 2^d alone would flush to zero
+struct Exp2Pair {
+  float a, b;
+  __device__ __forceinline__ explicit Exp2Pair(float d) : a(fast_exp2(fmaxf(d, -100.f))), b(fast_exp2(fminf(d + 100.f, 0.f))) {}
+  __device__ __forceinline__ float both() const { return a * b; }
+  __device__ __forceinline__ float of(float x) const { return x * a * b; }
+};
 
 // 2^e as fp32, e in [-126, 127]
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }

@@ -183,15 +183,16 @@ __global__ void __launch_bounds__(Fp8Pre<D>::THREADS) prefill_fp8_kernel(Common 
       }
       const float mn0 = fmaxf(mr0, mx0), mn1 = fmaxf(mr1, mx1);
       const float mu0 = mn0 == -INFINITY ? 0.f : mn0, mu1 = mn1 == -INFINITY ? 0.f : mn1;
-      const float al0 = fast_exp2(mr0 - mu0), al1 = fast_exp2(mr1 - mu1);
+      const Exp2Pair e0(mr0 - mu0), e1(mr1 - mu1);
+      const float al0 = e0.both(), al1 = e1.both();
       mr0 = mn0;
       mr1 = mn1;
-      lr0 *= al0;
-      lr1 *= al1;
+      lr0 = e0.of(lr0);
+      lr1 = e1.of(lr1);
       uint32_t pa[G::NB][4];  // A fragments of W, one k-step of 16 keys per block
 #pragma unroll
       for (int b = 0; b < G::NB; b++) {
-        const float ivs = __uint_as_float((254u << 23) - (__float_as_uint(ssc[G::NB + b]) & 0x7f800000u));
+        float ivs = __uint_as_float((254u << 23) - (__float_as_uint(ssc[G::NB + b]) & 0x7f800000u));
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int hn = 0; hn < 2; hn++) {
@@ -202,6 +203,17 @@ __global__ void __launch_bounds__(Fp8Pre<D>::THREADS) prefill_fp8_kernel(Common 
           s1 += w2 + w3;
           pa[b][2 * hn] = pack_f16x2(w0, w1);
           pa[b][2 * hn + 1] = pack_f16x2(w2, w3);
+        }
+        if (ssc[G::NB + b] < exp2_int(kFp8LowExp)) {
+          const float up = (float)(kFp8LowExp - exp_of(ssc[G::NB + b]));
+          s0 = s1 = 0.f;
+#pragma unroll
+          for (int hn = 0; hn < 2; hn++) {
+            const float* t = sacc[2 * b + hn];
+            s0 += fast_exp2(t[0] - mu0 + up) + fast_exp2(t[1] - mu0 + up);
+            s1 += fast_exp2(t[2] - mu1 + up) + fast_exp2(t[3] - mu1 + up);
+          }
+          ivs = exp2_int(-kFp8LowExp);
         }
         lr0 = fmaf(s0, ivs, lr0);
         lr1 = fmaf(s1, ivs, lr1);

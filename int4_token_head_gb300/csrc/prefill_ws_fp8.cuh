@@ -73,7 +73,9 @@ struct Fp8Ws {
   __host__ __device__ static constexpr int chunk(int i) {
     return W == 128 ? i ^ ((i >> 3) & 7) : W == 64 ? i ^ ((i >> 3) & 3) : i ^ ((i >> 3) & 1);
   }
-  static constexpr int RING = (4 * NB + 4) * 4;   // K scales, log2 V scales, 1 / V scales, block flags, all usable
+  // K scales, log2 V scales, 1 / V scales (0 below 2^kFp8LowExp), block flags, step flags (1 all blocks
+  // usable, 2 a V scale below)
+  static constexpr int RING = (4 * NB + 4) * 4;
   static constexpr int NRING = 3;
   static constexpr int NBARS = 23;
   static constexpr int S_COLS = NK, O_COL = H * NK;  // TMEM: S_h at h NK, O_h at H NK + h D
@@ -342,7 +344,8 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
         ph_sfull ^= 1;
         tc_fence_after();
         // the warp's rows all see all its keys: no mask (the usual case)
-        const bool full = __all_sync(0xffffffffu, lo <= 0 && lim >= NC && ok[NB - NBH * kh] != 0);
+        const int step_flags = ok[NB - NBH * kh];
+        const bool full = __all_sync(0xffffffffu, lo <= 0 && lim >= NC && (step_flags & 1) != 0);
         // the scores of block b, hidden ones -inf, and their factor (never 0, so
         // that -inf stays); seen: whether the row sees a usable key of this thread's
         bool seen = full;
@@ -367,12 +370,14 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
         uint32_t w[NC / 2];
         float add, tot;
         // find: the reference moves to the row's maximum where it has none or is
-        // more than 8 behind; whole numbers, so that O and l move exactly
-        bool find = st == 0;
+        // more than 8 behind; whole numbers, so that O and l move exactly.  Blocks of
+        // small V scales (kFp8LowExp) have their share of the denominator taken there
+        // too, by a maximum of their own
+        bool find = st == 0 || (step_flags & 2) != 0;
 #pragma unroll 1
         while (true) {
           if (find) {
-            float mx = -INFINITY;
+            float mx = -INFINITY, top = -INFINITY, lows = 0.f;
 #pragma unroll 1
             for (int b = 0; b < NBH; b++) {
               float s[16], f;
@@ -381,15 +386,26 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
 #pragma unroll
               for (int k = 1; k < 16; k++) t = fmaxf(t, s[k]);
               mx = fmaxf(mx, fmaf(t, f, kvf[b]));
+              if (ivs[b] == 0.f) {
+                __syncwarp();
+                t = fmaxf(top, t * f);
+                const float o = t == -INFINITY ? 0.f : t;
+                lows *= fast_exp2(top - o);
+                top = t;
+#pragma unroll
+                for (int k = 0; k < 16; k++) lows += fast_exp2(fmaf(s[k], f, -o));
+              }
             }
             sxch[kh * ROWS + r] = mx;
             pair_sync();
             mx = ceilf(fmaxf(mx, sxch[(kh ^ 1) * ROWS + r]));
             pair_sync();  // read before anything else is written there
             const bool grow = mx > m_ref + (m_ref == -INFINITY ? 0.f : 8.f);
-            const float alpha = grow && m_ref != -INFINITY ? fast_exp2(m_ref - mx) : 1.f;
+            const Exp2Pair move(grow && m_ref != -INFINITY ? m_ref - mx : 0.f);
+            const float alpha = move.both();
             if (grow) m_ref = mx;
-            l_run *= alpha;
+            l_run = move.of(l_run);
+            if (lows > 0.f) l_run = fmaf(lows, fast_exp2(top - m_ref), l_run);
             if (__any_sync(0xffffffffu, alpha != 1.f)) {
               // O is complete up to the previous step (S_h of this step was
               // issued after it); each key half rescales its share of the columns
@@ -668,14 +684,17 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
           }
           wait_until(KFREE, kfree, n - 1);  // S of step n - 2: ring entry n % 3 has been read
           float* re = reinterpret_cast<float*>(ring + (n % G::NRING) * G::RING);
+          const bool low = vs < exp2_int(kFp8LowExp);
           if (lane < NB) {
             re[lane] = ks;
             re[NB + lane] = (float)exp_of(vs);
-            re[2 * NB + lane] = __uint_as_float((254u << 23) - (__float_as_uint(vs) & 0x7f800000u));
+            re[2 * NB + lane] =
+                low ? 0.f : __uint_as_float((254u << 23) - (__float_as_uint(vs) & 0x7f800000u));
             reinterpret_cast<int*>(re)[3 * NB + lane] = ok;
           }
           const bool all = __all_sync(0xffffffffu, ok || lane >= NB);
-          if (lane == 0) reinterpret_cast<int*>(re)[4 * NB] = all;
+          const bool lows = __any_sync(0xffffffffu, low && lane < NB);
+          if (lane == 0) reinterpret_cast<int*>(re)[4 * NB] = all | lows << 1;
           __syncwarp();
           if (lane == 0) fp8_arrive(bar(KFULL + b));
           blk = next;

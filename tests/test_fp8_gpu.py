@@ -983,3 +983,44 @@ def test_decode_beside_prefill_sees_what_was_written_just_before(d):
         for n, x in enumerate(got):
             assert torch.equal(x, want[n % 3])
     assert status.item() == 0
+
+
+# ---------------------------------------------------------------------------
+# V scales at both ends of their range
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("d", HEADS)
+@pytest.mark.parametrize("hq,hkv,seqs,broadcast", [
+    (4, 2, [(1, 200), (1, 90), (1, 700)], False),                # one launch
+    (4, 4, [(1, 3000), (1, 300)], False),                        # planned decode: four blocks at once,
+    (4, 1, [(1, 9000), (1, 300)], False),                        # two, one, and warps of columns
+    (8, 1, [(1, 9000), (1, 40)], False),
+    (16, 2, [(3, 3000), (1, 700), (2, 60)], False),
+    (4, 2, [(100, 300), (300, 300), (40, 90), (1, 500)], False),  # prefill beside decode
+    (8, 2, [(33, 2900), (5, 700)], False),                       # tiles split over their keys
+    (4, 2, [(60, 260), (9, 2900)], True),                        # queries without a tensor map
+])
+@pytest.mark.parametrize("gap", [0, 8, 20, -30])
+def test_v_scales_at_both_ends_of_their_range(d, hq, hkv, seqs, broadcast, gap):
+    """One block of scale 2^60 among blocks of 2^-60, its scores `gap` binary
+    orders above the others': their output does not show beside its, their
+    share of the denominator does."""
+    for where in (0.0, 0.5, 1.0):  # the block's place: first seen, later, in another piece
+        b = Batch(seqs, hkv, d, seed=d).fill(4)
+        g = np.random.default_rng(7)
+        for i, (_, length) in enumerate(seqs):
+            at = round(where * ((length - 1) // 16))
+            x = g.standard_normal((length, hkv, d)) * 0.05
+            x[:, :, 0] = 0.0
+            x[16 * at:16 * at + 16, :, 0] = gap * math.log(2)
+            x = torch.from_numpy(x).to(torch.bfloat16).double().numpy()
+            F.write(x, b.table[i:i + 1], [length], [0, length], b.kc, b.ks)
+            held = b.table[i, :-(-length // 16)]
+            b.vs[held] = 2.0 ** -60
+            b.vs[held[at]] = 2.0 ** 60
+        q = _bf16((1 if broadcast else b.tokens, hq, d), 5)
+        q[..., 0] = d ** 0.5
+        full = q.expand(b.tokens, hq, d)
+        out = _attend(b, q.cuda().expand(b.tokens, hq, d), b.device(), hq)
+        ref, bound = F.attention(full.double().numpy(), b.host(), b.table, b.lens, b.start, d ** -0.5, True)
+        _assert_attention(out, ref, bound)
+        assert b.status.item() == 0
