@@ -158,7 +158,8 @@ KVINT4_API int kv_int8_write(const void* k, int64_t k_token_stride, const void* 
 /*
  * kv_int4_attention_workspace_size -- bytes of device workspace that
  * kv_int4_attention, kv_int8_attention and kv_fp8_attention need for these
- * sizes (a pure host computation).  The workspace holds the device-built
+ * sizes (a pure host computation; kv_fp8_attention is faster with more, see
+ * kv_fp8_attention_workspace_size).  The workspace holds the device-built
  * schedule, the rotated queries and the split-KV partial results; its contents
  * need no initialisation.
  * Returns 0 for invalid arguments.
@@ -267,8 +268,8 @@ KVINT4_API int kv_int8_attention(const void* q, int64_t q_token_stride,
  * minus workspace and workspace_bytes.  The workspace is instead a static
  * device array of KV_INT4_NOALLOC_SCRATCH_BYTES (64 MiB) that every GPU which
  * loads the library holds until the process exits.  A call that needs more
- * (kv_int4_attention_workspace_size(...) bytes suffice, but count what only
- * kv_fp8_attention uses) returns KV_INT4_ERR_SCRATCH_LIMIT and enqueues nothing.  The function allocates
+ * (kv_int4_attention_workspace_size(...) bytes suffice) returns
+ * KV_INT4_ERR_SCRATCH_LIMIT and enqueues nothing.  The function allocates
  * nothing (no cudaMalloc, cudaFree or allocating library call).
  *
  * The first call on a device (with that device current) looks up the array's
@@ -412,12 +413,24 @@ KVINT4_API int kv_fp8_read(const uint8_t* k_cache, const uint8_t* v_cache, const
                            void* stream);
 
 /*
+ * kv_fp8_attention_workspace_size -- bytes with which kv_fp8_attention runs at
+ * its best for these sizes: prefill tiles may be split over their keys, which
+ * takes 10 to 42 MB by the head size, and decode may take up to 32 query columns
+ * per work unit.  Given less it does without both; what
+ * kv_int4_attention_workspace_size gives is always enough.  Results then differ
+ * by roundings, as sums are split elsewhere.
+ * Returns 0 for invalid arguments.
+ */
+KVINT4_API size_t kv_fp8_attention_workspace_size(int num_seqs, int num_q_tokens,
+                                                  int num_q_heads, int num_kv_heads, int head_size);
+
+/*
  * kv_fp8_attention -- attention over the FP8 cache with block scales:
  *   out[t][hq][:] = sum_p softmax_p(softmax_scale * q[t][hq] . k_hat_p) v_hat_p,
  *   k_hat_p = c_p * s_block(p), v_hat_p likewise.
- * Arguments, masks (causal, sliding_window), workspace
- * (kv_int4_attention_workspace_size), device status bits and errors are those
- * of kv_int8_attention, except for the caches (above) and:
+ * Arguments, masks (causal, sliding_window), device status bits and errors are
+ * those of kv_int8_attention, except for the caches and the workspace size
+ * (above) and:
  * - with causal == 0 the keys need not hold the queries: q_len may exceed
  *   seq_lens[i] (decoder queries over an encoder's states, say), and seq_lens[i]
  *   may be 0.  A sliding window then counts from query position

@@ -77,6 +77,7 @@ _SIGNATURES_FP8 = {
     "kv_qk_norm_rope": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_int, c_int, c_int, c_int, c_void_p, c_void_p,
                                 c_float, c_void_p, c_void_p, c_int64, c_int, c_int, c_void_p, c_int64, c_void_p,
                                 c_int64, c_void_p, c_void_p]),
+    "kv_fp8_attention_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int]),
 }
 
 OK = 0
@@ -263,8 +264,15 @@ def selftest_wait(iterations: int, dev_status: torch.Tensor, dev_cycles: Optiona
            "kv_int4_selftest_wait")
 
 
-def attention_workspace_size(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_size) -> int:
-    return int(load().kv_int4_attention_workspace_size(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_size))
+def attention_workspace_size(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_size,
+                             fmt: Optional[str] = None) -> int:
+    """Bytes of workspace for a call over an "int4", "int8" or "fp8" cache; without
+    ``fmt``, enough for a call over any of them."""
+    _check(fmt in (None, "int4", "int8", "fp8"), f"unknown cache format {fmt!r}")
+    sizes = num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_size
+    int4 = 0 if fmt == "fp8" else int(load().kv_int4_attention_workspace_size(*sizes))
+    fp8 = 0 if fmt in ("int4", "int8") else int(load().kv_fp8_attention_workspace_size(*sizes))
+    return max(int4, fp8)
 
 
 def attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, query_start_loc,

@@ -93,7 +93,7 @@ bool workspace_layout(int num_seqs, int num_q_tokens, int num_q_heads, int num_k
 }
 
 bool workspace_layout_fp8(int num_seqs, int num_q_tokens, int num_q_heads, int num_kv_heads,
-                          int head_size, WorkspaceLayoutFp8* L) {
+                          int head_size, bool compact, WorkspaceLayoutFp8* L) {
   if (num_seqs < 0 || num_q_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_size <= 0) return false;
   if (num_q_heads % num_kv_heads) return false;
   const size_t group = num_q_heads / num_kv_heads;
@@ -110,16 +110,18 @@ bool workspace_layout_fp8(int num_seqs, int num_q_tokens, int num_q_heads, int n
   L->dseq = take(S * 16);
   L->dprefix = take((S + 1) * 8);
   L->ptab = take((S + 1) * 8);
-  L->plist = take((L->max_pairs + kMaxPieces) * 32);
-  L->msplit = take(kMaxPieces / 2 * 16);
-  const size_t least = S * Hkv * kDecodeCols, most = S * Hkv * kDecodeColsFp8, room = 3 * T * num_q_heads;
+  L->max_pieces = compact ? 0 : kMaxPieces;
+  L->plist = take((L->max_pairs + L->max_pieces) * 32);
+  L->msplit = take(L->max_pieces / 2 * 16);
+  const size_t least = S * Hkv * kDecodeCols, most = S * Hkv * kDecodeColsFp8, room = compact ? 0 : 3 * T * num_q_heads;
   L->direct_rows = least > room ? least : most < room ? most : room;
   L->direct_o = take(L->direct_rows * D * 4);
   L->direct_ml = take(L->direct_rows * 2 * 4);
   L->warp_o = take((size_t)kMaxDecodeWarps * kDecodeCols * D * 4);
   L->warp_ml = take((size_t)kMaxDecodeWarps * kDecodeCols * 2 * 4);
-  L->piece_o = take((size_t)kPieceRows * D * 4);
-  L->piece_ml = take((size_t)kPieceRows * 2 * 4);
+  const size_t rows = compact ? 0 : kPieceRows;
+  L->piece_o = take(rows * D * 4);
+  L->piece_ml = take(rows * 2 * 4);
   L->total = off;
   return true;
 }
@@ -248,9 +250,9 @@ size_t kv_int4_attention_workspace_size(int num_seqs, int num_q_tokens, int num_
                                         int head_size) {
   if (!head_size_ok(head_size)) return 0;
   WorkspaceLayout L;
-  WorkspaceLayoutFp8 F;  // one size serves both families of caches
+  WorkspaceLayoutFp8 F;  // the compact layout is larger only where most sequences have no queries
   if (!workspace_layout(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_size, &L) ||
-      !workspace_layout_fp8(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_size, &F))
+      !workspace_layout_fp8(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_size, true, &F))
     return 0;
   return L.total > F.total ? L.total : F.total;
 }

@@ -75,6 +75,15 @@ int kv_fp8_read(const uint8_t* k_cache, const uint8_t* v_cache, const float* k_s
                   block_size, false, stream);
 }
 
+size_t kv_fp8_attention_workspace_size(int num_seqs, int num_q_tokens, int num_q_heads, int num_kv_heads,
+                                       int head_size) {
+  WorkspaceLayoutFp8 L;
+  if (!head_size_ok(head_size) ||
+      !workspace_layout_fp8(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_size, false, &L))
+    return 0;
+  return L.total;
+}
+
 int kv_fp8_attention(const void* q, int64_t q_token_stride, const uint8_t* k_cache, const uint8_t* v_cache,
                      const float* k_scale_cache, const float* v_scale_cache, const int32_t* block_table,
                      int max_blocks_per_seq, const int32_t* seq_lens, const int32_t* query_start_loc, int num_seqs,
@@ -98,7 +107,8 @@ int kv_fp8_attention(const void* q, int64_t q_token_stride, const uint8_t* k_cac
       !aligned(workspace, 256))
     return KV_INT4_ERR_ALIGN;
   WorkspaceLayoutFp8 L;
-  if (!workspace_layout_fp8(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_size, &L)) return KV_INT4_ERR_SIZE;
+  if (!workspace_layout_fp8(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_size, true, &L))
+    return KV_INT4_ERR_SIZE;
   if (workspace_bytes < L.total) return KV_INT4_ERR_WORKSPACE;
   if (current_device() < 0) return KV_INT4_ERR_CUDA;
   AttnArgs a{q, q_token_stride, k_cache, v_cache, k_scale_cache, v_scale_cache, block_table, max_blocks_per_seq,

@@ -122,7 +122,9 @@ bool make_maps(const AttnArgs& a, int tile_tokens, Fp8Maps* m) {
 template <int D>
 int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
   WorkspaceLayoutFp8 L;
-  workspace_layout_fp8(a.num_seqs, a.num_q_tokens, a.num_q_heads, a.num_kv_heads, a.head_size, &L);
+  if (!workspace_layout_fp8(a.num_seqs, a.num_q_tokens, a.num_q_heads, a.num_kv_heads, a.head_size, false, &L) ||
+      a.workspace_bytes < L.total)
+    workspace_layout_fp8(a.num_seqs, a.num_q_tokens, a.num_q_heads, a.num_kv_heads, a.head_size, true, &L);
   const PlanView pv = plan_view_fp8(a.workspace, L);
   const int dev = current_device();
   const int sms = sm_count(dev);
@@ -250,11 +252,11 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
     const long long tiles = (a.num_q_tokens - most_decode + c.tile_tokens - 1) / c.tile_tokens;
     const long long rows = (long long)a.num_q_tokens * a.num_q_heads;
     const int pieces = rows <= c.split_ctas / 2 * (long long)c.tile_tokens * c.group ? 2 : 4;
-    return may_prefill && a.max_seq_len > 16ll * c.step_blocks * c.split_steps * pieces && tiles <= kSplitTiles &&
+    return may_prefill && L.max_pieces > 0 && a.max_seq_len > 16ll * c.step_blocks * c.split_steps * pieces && tiles <= kSplitTiles &&
            tiles * a.num_kv_heads < (long long)kSplitWaves * c.split_ctas;
   };
   bool tc = false, may_split = false;
-  const long long pairs = L.max_pairs + kMaxPieces;
+  const long long pairs = L.max_pairs + L.max_pieces;
   const long long most_items = pairs * a.num_kv_heads;
   {
     using G = Fp8Ws<D>;

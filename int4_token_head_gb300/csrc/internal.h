@@ -233,21 +233,24 @@ constexpr int kPrefillRows = 64;    // query rows (q token x q head) per prefill
 bool workspace_layout(int num_seqs, int num_q_tokens, int num_q_heads, int num_kv_heads,
                       int head_size, WorkspaceLayout* out);
 
-// The FP8 attention's layout of the same workspace.
+// The FP8 attention's layout of the same workspace.  The compact one, about
+// what the INT4 attention needs, has no room for pieces of prefill tiles (they
+// stay whole) nor for more than eight columns per decode work unit.
 struct WorkspaceLayoutFp8 {
   size_t plan;          // int32 counters
   size_t dseq;          // int4 [num_seqs] decode sequences
   size_t dprefix;       // int64 [num_seqs + 1] position prefix over decode sequences
   size_t ptab;          // int2 [num_seqs + 1] prefill sequence table
-  size_t plist;         // PrefillPiece [max_pairs + kMaxPieces] prefill tiles and pieces of tiles, longest first
-  size_t msplit;        // int4 [kMaxPieces / 2] tiles in pieces
+  size_t plist;         // PrefillPiece [max_pairs + max_pieces] prefill tiles and pieces of tiles, longest first
+  size_t msplit;        // int4 [max_pieces / 2] tiles in pieces
   size_t direct_o;      // f32 [direct_rows][d]: query columns of (decode sequence, kv head) slots
   size_t direct_ml;     // f32 [direct_rows][2]
   size_t warp_o;        // f32 [kMaxDecodeWarps][8][d]
   size_t warp_ml;       // f32 [kMaxDecodeWarps][8][2]
-  size_t piece_o;       // f32 [kPieceRows][d] rows of pieces
+  size_t piece_o;       // f32 [kPieceRows][d] rows of pieces (none in the compact layout)
   size_t piece_ml;      // f32 [kPieceRows][2]
   size_t total;
+  int max_pieces;       // kMaxPieces, 0 in the compact layout
   int64_t max_pairs;    // prefill (sequence, tile) pairs
   int64_t direct_rows;  // 8 columns per slot; up to kDecodeColsFp8 where the call's queries fill a third of them
 };
@@ -256,7 +259,7 @@ constexpr int kMaxPieces = 2048;    // pieces of split prefill tiles, and their 
 constexpr int kPieceRows = 40960;   // (a piece of a full 256-row tile for each of 160 CTAs)
 
 bool workspace_layout_fp8(int num_seqs, int num_q_tokens, int num_q_heads, int num_kv_heads,
-                          int head_size, WorkspaceLayoutFp8* out);
+                          int head_size, bool compact, WorkspaceLayoutFp8* out);
 
 int launch_attention(const AttnArgs& a, cudaStream_t stream);
 // FP8 block-scaled cache (attention_fp8.cu): E4M3 codes of d bytes per head

@@ -57,7 +57,7 @@ extern "C" int kv_int4_attention_noalloc(
     int max_seq_len, int num_q_heads, int num_kv_heads, int head_size, int block_size, int num_blocks,
     float softmax_scale, int causal, int sliding_window, const int8_t* signs, void* out, int64_t out_token_stride,
     int32_t* dev_status, void* stream) {
-  // this call's own need: the public size also covers the FP8 cache's attention
+  // this call's own need: the public size is also enough for the FP8 cache's attention
   kvint4::WorkspaceLayout L;
   const size_t need =
       kv_int4_attention_workspace_size(num_seqs, num_q_tokens, num_q_heads, num_kv_heads, head_size) &&

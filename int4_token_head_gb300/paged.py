@@ -33,7 +33,7 @@ class PagedKV:
         self.query_start_loc = w.query_start_loc.to(device)
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
         self.softmax_scale = 1.0 / math.sqrt(w.head_size)
-        ws = _lib.attention_workspace_size(w.num_seqs, w.num_q_tokens, w.num_q_heads, w.num_kv_heads, w.head_size)
+        ws = _lib.attention_workspace_size(w.num_seqs, w.num_q_tokens, w.num_q_heads, w.num_kv_heads, w.head_size, fmt)
         self.workspace = torch.empty(ws, dtype=torch.uint8, device=device)
 
     # -------------------------------------------------------------------

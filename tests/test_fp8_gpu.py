@@ -1024,3 +1024,36 @@ def test_v_scales_at_both_ends_of_their_range(d, hq, hkv, seqs, broadcast, gap):
         ref, bound = F.attention(full.double().numpy(), b.host(), b.table, b.lens, b.start, d ** -0.5, True)
         _assert_attention(out, ref, bound)
         assert b.status.item() == 0
+
+
+# ---------------------------------------------------------------------------
+# the smaller workspace
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("d", HEADS)
+@pytest.mark.parametrize("hq,hkv,seqs", [
+    (4, 2, [(1, 300), (1, 40)]),                                  # one launch
+    (8, 2, [(1, 6000), (1, 17), (2, 700)]),
+    (16, 1, [(1, 3000), (3, 500), (1, 3)]),                       # 16 and 48 columns
+    (8, 8, [(200, 1999), (260, 2200)]),                           # tiles that would be split
+    (24, 2, [(7, 3000), (1, 9), (30, 2100), (0, 5), (9, 9)]),
+    (2, 2, [(1, 20)] + [(0, 0)] * 40),                            # mostly sequences without queries
+])
+def test_attention_in_the_workspace_of_int4(d, hq, hkv, seqs):
+    """kv_int4_attention_workspace_size bytes are enough: whole tiles, eight
+    columns; nothing is touched behind them."""
+    b = Batch(seqs, hkv, d, seed=d).fill(2)
+    q = _bf16((b.tokens, hq, d), 3)
+    sizes = len(seqs), b.tokens, hq, hkv, d
+    least, best = (kv.attention_workspace_size(*sizes, fmt=f) for f in ("int4", "fp8"))
+    assert least < best
+    ref, bound = F.attention(q.double().numpy(), b.host(), b.table, b.lens, b.start, d ** -0.5, True)
+    for size in (least, best - 256, best):
+        whole = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        out = torch.full((b.tokens, hq, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+        kv.attention_fp8(q.cuda(), *b.device(), *b.meta(), b.max_len, int(b.lens.max()), d ** -0.5, True, out,
+                         whole[:size], dev_status=b.status)
+        _assert_attention(out, ref, bound)
+        assert (whole[size:] == 0xA5).all() and b.status.item() == 0
+    with pytest.raises(kv.KvInt4Error, match="workspace"):
+        kv.attention_fp8(q.cuda(), *b.device(), *b.meta(), b.max_len, int(b.lens.max()), d ** -0.5, True, out,
+                         whole[:1024], dev_status=b.status)

@@ -241,3 +241,44 @@ def test_paged_cache_refuses_slot_writes_for_fp8():
         pk.write(None, None, None)
     with pytest.raises(ValueError, match="unknown cache format"):
         PagedKV(pk.w, device="cpu", fmt="fp16")
+
+
+# ---------------------------------------------------------------------------
+# workspaces
+# ---------------------------------------------------------------------------
+def _int4_workspace(seqs, tokens, hq, hkv, d):
+    """The INT4 attention's parts, each rounded up to 256 bytes: schedule, rotated
+    queries, eight columns per (sequence, kv head) and for each of 4096 warps."""
+    items = (tokens // max(1, 64 // (hq // hkv)) + seqs) * hkv
+    columns = 8 * seqs * hkv
+    parts = (256, 16 * seqs, 8 * (seqs + 1), 16 * items, 8 * items, 2 * tokens * hq * d, 4 * columns * d, 8 * columns,
+             4 * 4096 * 8 * d, 8 * 4096 * 8)
+    return sum(-(-x // 256) * 256 for x in parts)
+
+
+@pytest.mark.parametrize("sizes", [(1, 1, 32, 8, 128), (64, 64, 16, 8, 256), (8, 9000, 32, 8, 128), (300, 300, 12, 1, 96),
+                                   (1, 1, 1, 1, 64), (3, 70, 64, 1, 192)])
+def test_int4_callers_do_not_pay_for_the_fp8_workspace(lib, sizes):
+    assert lib.kv_int4_attention_workspace_size(*sizes) == _int4_workspace(*sizes)
+    for fmt in ("int4", "int8"):
+        assert kv.attention_workspace_size(*sizes, fmt=fmt) == _int4_workspace(*sizes)
+    best = lib.kv_fp8_attention_workspace_size(*sizes)
+    assert kv.attention_workspace_size(*sizes, fmt="fp8") == best > 0
+    assert kv.attention_workspace_size(*sizes) == max(best, _int4_workspace(*sizes))
+
+
+def test_workspace_sizes_refuse_what_no_call_takes(lib):
+    assert lib.kv_fp8_attention_workspace_size(4, 4, 32, 7, 128) == 0
+    assert lib.kv_fp8_attention_workspace_size(4, 4, 32, 8, 100) == 0
+    assert lib.kv_fp8_attention_workspace_size(-1, 4, 32, 8, 128) == 0
+    assert kv.attention_workspace_size(4, -4, 32, 8, 128) == 0
+    with pytest.raises(ValueError, match="format"):
+        kv.attention_workspace_size(4, 4, 32, 8, 128, fmt="fp4")
+
+
+def test_paged_caches_hold_their_own_workspace():
+    from int4_token_head_gb300 import synthetic
+    from int4_token_head_gb300.paged import PagedKV
+    w = synthetic.custom_workload(4, 2, 64, [(1, 20), (3, 9)])
+    for fmt in ("int4", "int8", "fp8"):
+        assert PagedKV(w, device="cpu", fmt=fmt).workspace.numel() == kv.attention_workspace_size(2, 4, 4, 2, 64, fmt=fmt)
