@@ -3,7 +3,9 @@
 The translation units are compiled in parallel and linked with the static
 CUDA runtime, so loading the library needs only the NVIDIA driver.  A stamp
 file records the host architecture and a hash of the sources, so a library
-built on another machine (or from other sources) is rebuilt.
+built on another machine (or from other sources) is rebuilt.  The Python call
+module of the FP8 operators, named for its interpreter, is built beside it and
+again whenever it is missing.
 """
 
 from __future__ import annotations
@@ -28,7 +30,8 @@ HEADER = os.path.join(ROOT, "include", "kvint4.h")
 SOURCES = ["api.cu", "write.cu", "write_int8.cu", "attention.cu", "rht.cu", "attention_fp8.cu",
            "cache_fp8.cu", "norm_rope.cu", "api_fp8.cu", "timing.cu", "noalloc.cu", "selftest.cu"]
 BINDING_SRC = os.path.join(CSRC, "fp8_binding.cpp")
-BINDING_PATH = os.path.join(PKG, "_fp8_binding.so")
+PYTHON_TAG = sysconfig.get_config_var("EXT_SUFFIX") or ".so"  # the interpreter's own: another one does not import it
+BINDING_PATH = os.path.join(PKG, "_fp8_binding" + PYTHON_TAG)
 GENCODE = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden"]
 
@@ -55,13 +58,15 @@ def _torch_dir():
 
 
 def _binding_command():
-    """g++ for the Python call module, which sees torch's tensors; None without
-    torch's or Python's headers."""
+    """g++ for the Python call module, which sees torch's tensors; None where it
+    cannot be built: without g++, Python's headers or a torch with CUDA."""
     torch, py = _torch_dir(), sysconfig.get_paths()["include"]
-    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")
     if torch is None or not os.path.exists(os.path.join(py, "Python.h")) or shutil.which("g++") is None:
         return None
     lib = os.path.join(torch, "lib")
+    if not os.path.exists(os.path.join(lib, "libc10_cuda.so")):
+        return None
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I", os.path.join(torch, "include"),
             "-I", os.path.join(torch, "include", "torch", "csrc", "api", "include"), "-I", py, "-I", cuda, BINDING_SRC,
             "-o", BINDING_PATH + ".tmp", "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
@@ -70,6 +75,7 @@ def _binding_command():
 def _fingerprint(extra=()) -> str:
     h = hashlib.sha256()
     h.update(platform.machine().encode())
+    h.update(PYTHON_TAG.encode())
     torch = _torch_dir()
     if torch:  # the call module depends on its version
         with open(os.path.join(torch, "version.py"), "rb") as fh:
@@ -83,16 +89,41 @@ def _fingerprint(extra=()) -> str:
     return h.hexdigest()
 
 
-def is_current(extra=()) -> bool:
+def _library_is_current(extra=()) -> bool:
     if not os.path.exists(LIB_PATH) or not os.path.exists(STAMP):
         return False
     with open(STAMP) as f:
         return f.read().strip() == _fingerprint(extra)
 
 
+def is_current(extra=()) -> bool:
+    return _library_is_current(extra) and (os.path.exists(BINDING_PATH) or _binding_command() is None)
+
+
+def _start_binding():
+    """Starts building the call module; what was there goes first."""
+    for old in (BINDING_PATH, os.path.join(PKG, "_fp8_binding.so")):
+        if os.path.exists(old):
+            os.remove(old)
+    cmd = _binding_command()
+    return cmd and subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+
+
+def _finish_binding(proc):
+    if proc is None:  # it cannot be built here: the same calls go through ctypes, some microseconds slower
+        return
+    out, _ = proc.communicate()
+    if proc.returncode != 0:
+        raise RuntimeError(f"g++ failed for {os.path.basename(BINDING_SRC)}:\n{out}")
+    os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile (if needed) and return the path of libkvint4.so."""
     if not force and is_current():
+        return LIB_PATH
+    if not force and _library_is_current():  # the call module alone is missing
+        _finish_binding(_start_binding())
         return LIB_PATH
     nvcc = nvcc_path()
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -107,10 +138,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)))
-    binding = _binding_command()
-    if os.path.exists(BINDING_PATH):
-        os.remove(BINDING_PATH)
-    bp = binding and subprocess.Popen(binding, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    binding = _start_binding()
     logs = {}
     failed = []
     for src, p in procs:
@@ -118,12 +146,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         logs[src] = out
         if p.returncode != 0:
             failed.append(src)
-    if bp is not None:
-        out, _ = bp.communicate()
-        if bp.returncode == 0:
-            os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
-        else:  # the same calls go through ctypes, a few microseconds slower
-            print(f"{os.path.basename(BINDING_SRC)} was not built, calls go through ctypes:\n{out}", file=sys.stderr)
+    _finish_binding(binding)
     if failed:
         msg = "\n".join(f"--- {s} ---\n{logs[s]}" for s in failed)
         raise RuntimeError(f"nvcc failed for {failed}:\n{msg}")
