@@ -9,6 +9,7 @@ built or loaded, these functions raise instead of computing anything else.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import threading
 from typing import Optional
@@ -473,6 +474,14 @@ def _raw_stream(dev: int, same: bool, stream) -> int:
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
+def _int32(x, name: str) -> int:
+    """An argument that the C ABI takes as int32 (ctypes would drop what is above)."""
+    i = operator.index(x)
+    if not -(1 << 31) <= i < 1 << 31:
+        _refuse(f"{name} must fit in 32 bits, got {i}")
+    return i
+
+
 def _status_ptr(dev_status: Optional[torch.Tensor], dev: int):
     if dev_status is None:
         return None
@@ -538,6 +547,7 @@ def write_fp8(k, v, block_table, seq_lens, start_loc, max_len, k_cache, v_cache,
     num_seqs, width = _sequences(block_table, seq_lens, start_loc)
     tokens = k.shape[0]
     ks, vs = _rows(k, "k", tokens, hkv, d), _rows(v, "v", tokens, hkv, d)
+    max_len = _int32(max_len, "max_len")
     dev = k_cache.get_device()
     st = _raw_stream(dev, v_cache.get_device() == k_scale.get_device() == v_scale.get_device() == block_table.get_device()
                      == seq_lens.get_device() == start_loc.get_device() == k.get_device() == v.get_device() == dev, stream)
@@ -563,6 +573,7 @@ def read_fp8(k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, start_lo
     num_seqs, width = _sequences(block_table, seq_lens, start_loc)
     tokens = k.shape[0]
     ks, vs = _rows(k, "k", tokens, hkv, d), _rows(v, "v", tokens, hkv, d)
+    max_len = _int32(max_len, "max_len")
     dev = k_cache.get_device()
     st = _raw_stream(dev, v_cache.get_device() == k_scale.get_device() == v_scale.get_device() == block_table.get_device()
                      == seq_lens.get_device() == start_loc.get_device() == k.get_device() == v.get_device() == dev, stream)
@@ -594,6 +605,8 @@ def attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, 
     qs, os_ = _rows(q, "q", tokens, hq, d), _rows(out, "out", tokens, hq, d)
     if workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
         _refuse("workspace must be contiguous uint8")
+    max_query_len, max_seq_len = _int32(max_query_len, "max_query_len"), _int32(max_seq_len, "max_seq_len")
+    sliding_window = _int32(sliding_window, "sliding_window")
     dev = k_cache.get_device()
     st = _raw_stream(dev, v_cache.get_device() == k_scale.get_device() == v_scale.get_device() == block_table.get_device()
                      == seq_lens.get_device() == query_start_loc.get_device() == q.get_device() == out.get_device()

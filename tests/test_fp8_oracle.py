@@ -282,3 +282,20 @@ def test_paged_caches_hold_their_own_workspace():
     w = synthetic.custom_workload(4, 2, 64, [(1, 20), (3, 9)])
     for fmt in ("int4", "int8", "fp8"):
         assert PagedKV(w, device="cpu", fmt=fmt).workspace.numel() == kv.attention_workspace_size(2, 4, 4, 2, 64, fmt=fmt)
+
+
+@pytest.mark.parametrize("big", [1 << 31, (1 << 32) + 5, -(1 << 31) - 1])
+def test_binding_refuses_counts_beyond_32_bits(big):
+    """They would reach the library without their upper bits."""
+    a = _cpu()
+    cache, seqs = [a[x] for x in ("kc", "vc", "ks", "vs")], [a[x] for x in ("bt", "sl", "st")]
+    q, ws = torch.zeros(3, 4, 64, dtype=torch.bfloat16), torch.zeros(16, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="max_len must fit"):
+        kv.write_fp8(a["k"], a["v"], *seqs, big, *cache)
+    with pytest.raises(ValueError, match="max_len must fit"):
+        kv.read_fp8(*cache, *seqs, big, a["k"], a["v"])
+    for name, counts, window in (("max_query_len", (big, 16), 0), ("max_seq_len", (2, big), 0), ("sliding_window", (2, 16), big)):
+        with pytest.raises(ValueError, match=f"{name} must fit"):
+            kv.attention_fp8(q, *cache, *seqs, *counts, 0.1, True, q, ws, sliding_window=window)
+    with pytest.raises(ValueError, match="CUDA device"):  # any whole number will do
+        kv.write_fp8(a["k"], a["v"], *seqs, np.int64(2), *cache)
