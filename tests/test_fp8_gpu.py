@@ -1057,3 +1057,65 @@ def test_attention_in_the_workspace_of_int4(d, hq, hkv, seqs):
     with pytest.raises(kv.KvInt4Error, match="workspace"):
         kv.attention_fp8(q.cuda(), *b.device(), *b.meta(), b.max_len, int(b.lens.max()), d ** -0.5, True, out,
                          whole[:1024], dev_status=b.status)
+
+
+# ---------------------------------------------------------------------------
+# the two bindings' checks
+# ---------------------------------------------------------------------------
+def _changed(x):
+    """What a call may not take in place of the tensor x, and some that it may."""
+    yield "cpu", x.cpu()
+    yield "type", x.to(torch.float64) if x.dtype != torch.float64 else x.float()
+    yield "half", x.to(torch.float16)
+    yield "int64", x.to(torch.int64)
+    yield "bytes", x.to(torch.int32).to(torch.uint8)
+    yield "another row", torch.cat([x, x[:1] if x.shape[0] else x.new_zeros(1, *x.shape[1:])])
+    yield "less of the last dimension", x[..., :-1]
+    yield "a dimension more", x[None]
+    yield "flat", x.reshape(-1)
+    yield "every other element", torch.stack([x, x], -1).flatten(-2)[..., ::2]
+    yield "turned", x.transpose(0, -1).contiguous().transpose(0, -1)
+    yield "wide rows", torch.cat([x, x], -1)[..., :x.shape[-1]]
+    yield "none", None
+
+
+@pytest.mark.parametrize("op", ["write", "read", "attention", "norm"])
+def test_both_bindings_refuse_the_same_calls(monkeypatch, op):
+    """Every argument changed in turn, in calls without tokens (nothing is
+    launched): through the call module and through ctypes the same outcome."""
+    assert _lib._calls() is not _lib._Calls
+    d, cuda = 64, dict(device="cuda")
+    cache = [torch.zeros(4, 16, 2, d, dtype=torch.uint8, **cuda).view(torch.float8_e4m3fn) for _ in range(2)] + [
+        torch.ones(4, 2, **cuda) for _ in range(2)]
+    seqs = [torch.zeros(3, 5, dtype=torch.int32, **cuda), torch.zeros(3, dtype=torch.int32, **cuda),
+            torch.zeros(4, dtype=torch.int32, **cuda)]
+    kv_rows = [torch.zeros(0, 2, d, dtype=torch.bfloat16, **cuda) for _ in range(2)]
+    q_rows = [torch.zeros(0, 4, d, dtype=torch.bfloat16, **cuda) for _ in range(2)]
+    status = torch.zeros(1, dtype=torch.int32, **cuda)
+    w = torch.ones(d, dtype=torch.bfloat16, **cuda)
+    f, args = {
+        "write": (kv.write_fp8, [*kv_rows, *seqs, 3, *cache, status]),
+        "read": (kv.read_fp8, [*cache, *seqs, 3, *kv_rows, status]),
+        "attention": (kv.attention_fp8, [q_rows[0], *cache, *seqs, 3, 64, 0.1, True, q_rows[1],
+                                         torch.zeros(64, dtype=torch.uint8, **cuda), status]),
+        "norm": (kv.qk_norm_rope, [q_rows[0], kv_rows[0], torch.zeros(0, dtype=torch.int64, **cuda), torch.ones(8, 32, **cuda),
+                                   w, w.clone(), 1e-6, q_rows[1], kv_rows[1], False, status]),
+    }[op]
+
+    def outcome(args):
+        try:
+            return f(*args)
+        except Exception as e:
+            return type(e), str(e)
+
+    module, refused = _lib._calls(), 0
+    assert outcome(args) is None
+    for i, x in enumerate(args):
+        for what, y in _changed(x) if torch.is_tensor(x) else [("text", "3"), ("none", None), ("half", 0.5), ("large", 1 << 40)]:
+            call = [*args[:i], y, *args[i + 1:]]
+            monkeypatch.setattr(_lib, "_fp8", module)
+            first = outcome(call)
+            monkeypatch.setattr(_lib, "_fp8", _lib._Calls)
+            assert outcome(call) == first, (i, what)
+            refused += first is not None
+    assert refused > 5 * len(args)
