@@ -4,7 +4,8 @@
 //   y = x / sqrt(mean(x^2) + eps) * w            (no norm without weights)
 //   (y_i, y_j) <- (y_i cos - y_j sin, y_j cos + y_i sin)   for the rot / 2
 //     pairs of the first rot elements: (i, i + rot / 2), or (2 i, 2 i + 1)
-// in fp32, rounded once to bf16.
+// in fp32, rounded once to bf16; squares that leave fp32's range are taken in
+// units of the vector's largest element (far_rsqrt).
 //
 // HBM-bound (2 d bytes in and 2 d out per head vector).  d / 16 lanes hold a
 // vector, each lane two 16-byte chunks: pair lanes (lane c < rot / 16) hold
@@ -47,6 +48,28 @@ __device__ __forceinline__ float vector_sum(float s, int base, int c) {
     s = a + b + __shfl_sync(0xffffffffu, s, base + 2);
   }
   return s;
+}
+
+// 1 / sqrt(s / D + eps), s the sum of squares, where that is no normal fp32
+// number or close to one: from the elements in units of 2^e, e the exponent of
+// the largest one
+template <int D, int N>
+__device__ float far_rsqrt(const float (&f0)[8], const float (&f1)[8], float eps, int base, int c) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; i++) m = fmaxf(m, fmaxf(fabsf(f0[i]), fabsf(f1[i])));
+#pragma unroll 1
+  for (int i = 0; i < N; i++) m = fmaxf(m, __shfl_sync(0xffffffffu, m, base + i));
+  const int e = min(max(exp_of(m), -63), 126);
+  const float unit = exp2_int(-e);
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const float a = f0[i] * unit, b = f1[i] * unit;
+    s = fmaf(a, a, fmaf(b, b, s));
+  }
+  s = vector_sum<N>(s, base, c);
+  return rsqrtf(s * (1.f / D) + eps * unit * unit) * unit;
 }
 
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
@@ -126,8 +149,15 @@ __global__ void __launch_bounds__(kNormWarps * 32, 8) norm_rope_kernel(NormRope 
       float s = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; i++) s = fmaf(f0[i], f0[i], fmaf(f1[i], f1[i], s));
-      s = vector_sum<LPV>(s, vsub * LPV < 32 - LPV ? vsub * LPV : 32 - LPV, c);
-      const float r = rsqrtf(s * (1.f / D) + a.eps);
+      const int base = vsub * LPV < 32 - LPV ? vsub * LPV : 32 - LPV;
+      s = vector_sum<LPV>(s, base, c);
+      const float mean = s * (1.f / D) + a.eps;
+      float r = rsqrtf(mean);
+      const bool far = mean > 0x1p120f || mean < 0x1p-80f;
+      if (__any_sync(0xffffffffu, far)) {
+        const float rf = far_rsqrt<D, LPV>(f0, f1, a.eps, base, c);
+        if (far) r = rf;
+      }
       const uint16_t* w = static_cast<const uint16_t*>(isq ? a.q_weight : a.k_weight);
       float w0[8], w1[8];
       unpack8(*reinterpret_cast<const uint4*>(w + 8 * c0), w0);

@@ -1119,3 +1119,21 @@ def test_both_bindings_refuse_the_same_calls(monkeypatch, op):
             assert outcome(call) == first, (i, what)
             refused += first is not None
     assert refused > 5 * len(args)
+
+
+@pytest.mark.parametrize("d", HEADS)
+@pytest.mark.parametrize("gain,eps", [(2.0 ** 70, 1e-6), (2.0 ** 120, 1e-6), (2.0 ** 120, 0.0), (2.0 ** -70, 0.0),
+                                      (2.0 ** -110, 0.0), (2.0 ** -70, 2.0 ** -140), (2.0 ** -60, 2.0 ** -120)])
+def test_norm_of_vectors_whose_squares_leave_fp32(d, gain, eps):
+    """Beside ordinary vectors and one of zeros in the same warp."""
+    q, k, pos, cs, w = _norm_inputs(9, 6, 2, d, 32, seed=d)
+    far = torch.ones(9, 6, 1, dtype=torch.bool)
+    far[::2, 1::3] = False
+    q = torch.where(far, (q.double() * gain).to(torch.bfloat16), q)
+    k = (k.double() * gain).to(torch.bfloat16)
+    if eps > 0:
+        q[1, 0] = 0
+    qo, ko = torch.empty_like(q, device="cuda"), torch.empty_like(k, device="cuda")
+    kv.qk_norm_rope(q.cuda(), k.cuda(), pos.cuda(), cs.cuda(), w[0].cuda(), w[1].cuda(), eps, qo, ko)
+    _norm_check(qo, q, w[0], eps, cs, pos, False)
+    _norm_check(ko, k, w[1], eps, cs, pos, False)
