@@ -457,7 +457,8 @@ KVINT4_API int kv_fp8_attention(const void* q, int64_t q_token_stride, const uin
  *   (y_i, y_j) <- (y_i cos - y_j sin, y_j cos + y_i sin)
  * over the rot_dim / 2 pairs of the first rot_dim elements: (i, i + rot_dim / 2),
  * or (2 i, 2 i + 1) with interleaved != 0; later elements are only normed.
- * fp32 arithmetic, one rounding to bf16 (nearest even).
+ * fp32 arithmetic (squares that leave its range are taken in units of the vector's
+ * largest element), one rounding to bf16 (nearest even).
  *
  * q, k: bf16, element (t, h, i) at q[t*q_token_stride + h*head_size + i], h <
  *   num_q_heads (k: num_kv_heads); q_out, k_out likewise.  16-byte aligned,

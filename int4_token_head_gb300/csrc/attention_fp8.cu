@@ -217,8 +217,8 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
   if (!may_prefill) {
     // one launch of clusters where the whole batch runs at once and the shares
     // are short: the largest cluster that leaves every CTA resident, or shares
-    // of two positions (1 x 97 keys: 7.4 us against 11.5; 8 x 1024: 12 against
-    // 18; shares of more than 16 positions, or a second wave of CTAs, do better
+    // of two positions (1 x 97 keys: 7.4 us against 12.7; 8 x 1024: 13 against
+    // 16; shares of more than 16 positions, or a second wave of CTAs, do better
     // with the balanced split)
     const long long tasks = (long long)a.num_seqs * c.ng, room = (long long)sms * dec_occ;
     const long long table = (long long)a.max_blocks_per_seq * 16;
@@ -244,8 +244,8 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
   // (512 keys; 256 at 192), eight of the other (256 keys), where a tile may have
   // four such pieces (looking for splits costs 1 to 3 us per call), two where the
   // query rows fill less than half of the CTAs (2 x 16 tokens against 1322 keys,
-  // 64/4 heads of 192: 36 us, in pieces 25; 2 prompts of 1221 tokens, 8/4 heads of
-  // 128: 43, 44), and there are fewer tiles than the schedule leaves whole anyway
+  // 64/4 heads of 192: 46 us, in pieces 38; 2 prompts of 1221 tokens, 8/4 heads of
+  // 128: 37, 37), and there are fewer tiles than the schedule leaves whole anyway
   // (sequences decoded here have at most dcols / group tokens)
   const long long most_decode = any_decode ? (long long)a.num_seqs * (c.dcols / c.group) : 0;
   auto can_split = [&] {
@@ -326,9 +326,9 @@ int launch_attention_t(const AttnArgs& a, cudaStream_t stream) {
     // merge: one or more CTAs per (sequence, kv head) segment, a warp per query
     // column and piece lane; lanes enough that each merges one or two pieces (1 to
     // 3 tokens of 7 heads against up to 9611 keys of one kv head, 2 sequences:
-    // 201 us with the 21 columns in one CTA and so one lane each, 22 spread out),
-    // as far as all CTAs start at once (more: 52 us instead of 43 for 32 x 1
-    // token of group 16)
+    // 201 us with the 21 columns in one CTA and so one lane each, 24 spread out),
+    // as far as all CTAs start at once (more: 55 us instead of 46 for 32 x 1
+    // token of group 16, 4 kv heads)
     const long long mcols = (long long)(a.max_query_len > 0 ? a.max_query_len : 1) * c.group;
     const long long segs = (long long)a.num_seqs * a.num_kv_heads;
     const long long pieces = 1 + (long long)dec_grid * c.hg / (segs > 0 ? segs : 1);

@@ -19,9 +19,10 @@
 // scale never leave the warp: no second pass, no atomics, and results that
 // depend on neither the launch shape nor the order of warps.  Four-warp CTAs at
 // most 72 registers a thread (28 warps per SM) and streaming loads of K and V:
-// 65,536 tokens, 8 heads of 128, 403 MB: 65.8 us = 0.90 of the measured copy
-// bandwidth (eight-warp CTAs 68.5; streaming stores of the codes 65.0, not kept:
-// attention reads them next).  Read: 396 MB in 60 us = 0.97.
+// 65,536 tokens, 8 heads of 128, 403 MB: 66.5 us = 0.89 of the measured copy
+// bandwidth (on the same tensors again 65.9; eight-warp CTAs 70.4; streaming
+// stores of the codes 65.0, not kept: attention reads them next).  Read: 396 MB in
+// 60 us = 0.97.
 
 #include <cuda_runtime.h>
 

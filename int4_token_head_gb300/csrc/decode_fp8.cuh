@@ -20,10 +20,10 @@
 // by ldmatrix.trans of byte pairs (one byte permute and two conversions per
 // four codes).
 //
-// Memory-bound: 32 x 32768 keys, 32/8 heads of 128, 2.15 GB of codes: 340 us a
+// Memory-bound: 32 x 32768 keys, 32/8 heads of 128, 2.15 GB of codes: 342 us a
 // call = 0.93 of the measured copy bandwidth.  More columns cost issue slots, as
-// every warp converts the codes for its own eight: 32 x 1 token of group 16
-// against 2048-4096 keys 43 us (floor 15; in 256-row prefill tiles 84).
+// every warp converts the codes for its own eight: 32 x 1 token of group 16, 4 kv
+// heads, against 2048-4096 keys 46 us (floor 15.5; in 256-row prefill tiles 81).
 template <int D, int NP>
 struct Fp8Dec {
   static constexpr int COLS = kDecodeCols / NP;
@@ -40,8 +40,8 @@ struct Fp8Dec {
   static constexpr int HTILE = (KTILE + VTILE + 63) / 128 * 128 + 64;
   // block slots: the copies in flight per SM set the pace.  Two CTAs of four
   // heads fit an SM with six slots at 128 (two of two heads at 256), with eight
-  // at 96 and 192 (32 x 32768 keys, 32/8 heads of 128: five slots 350 us, six
-  // 325, seven, one CTA, 447)
+  // at 96 and 192 (32 x 32768 keys, 32/8 heads of 128: five slots 360 us, six
+  // 344, seven, one CTA, 443)
   static constexpr int NS = NP == 1 ? 4 : NP == 4 || !SWZ ? 8 : 6;
   static constexpr int WAIT = NS - 2 * NP;                  // copy groups that may stay pending
   static constexpr int KSTEPS = D / 16;

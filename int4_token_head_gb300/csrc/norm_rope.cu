@@ -14,8 +14,9 @@
 // sines it loads once.  Inputs are loaded as streaming data, and outputs too
 // large to wait in L2 for the kernels that read them are stored as such: written
 // back in the order they were made they leave the bandwidth to the loads (16384
-// tokens, 32/8 heads of 128, 344 MB: 65 us without either hint, 54.5 with both
-// = 0.93 of the measured copy bandwidth).
+// tokens, 32/8 heads of 128, 344 MB, a call on the same tensors again: 64.5 us
+// without either hint, 55.3 with both; on other tensors in each call 58 to 60 =
+// 0.86 of the measured copy bandwidth).
 
 #include <cuda_runtime.h>
 

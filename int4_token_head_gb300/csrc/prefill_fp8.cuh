@@ -1,7 +1,7 @@
 // Prefill over the FP8 cache on warp-level MMAs, included by attention_fp8.cu,
 // for queries that no tensor map holds (token rows that overlap: one row for
-// all tokens, say; 8 prompts of 512 to 2048 tokens, 32/8 heads of 256: 945 us, on
-// the tensor cores 314):
+// all tokens, say; 8 prompts of 512 to 2048 tokens, 32/8 heads of 256: 897 us, on
+// the tensor cores 325):
 // 64 query rows (query token x q head of one kv group) per item, 16 per warp,
 // 32 keys (two cache blocks) per step.  Codes are staged as they are (cp.async,
 // three stages) and become f16 B fragments in registers: for S, a lane's four

@@ -30,10 +30,12 @@
 //     maximum (one fma, one exp2, one add and half a conversion per score).  The
 //     two warps of a row agree on that by a barrier that votes; the weights stay
 //     in registers until then, S is whole.
-// 8 causal prompts of 512 to 2048 tokens, 32/8 heads of 128: 131 us = 0.39 of the
-// measured bf16 tensor rate, about 4100 cycles per step where the MMAs need
-// 2050; what bounds it is that chain, at 54 % of the issue slots.  Of 256, one half
-// whose chain nothing hides: 314 us for twice the operations (0.32).
+// 8 causal prompts of 512 to 2048 tokens, 32/8 heads of 128: 146 us a call = 0.35
+// of the measured bf16 tensor rate (140 us as replays on the same tensors), about
+// 4300 cycles per step where the MMAs need 2050; what bounds it is that chain, at
+// 53 % of the issue slots.  Of 256, one half whose chain nothing hides: 325 us for
+// twice the operations (0.31).  Steps with a V scale below 2^kFp8LowExp take the
+// search for the maximum too (all of them: 193 us).
 // Shared operands are K-major (Q, K) or MN-major (V) tiles [D / 64][rows][128
 // bytes] with the 16-byte chunk index XORed by row % 8.
 //

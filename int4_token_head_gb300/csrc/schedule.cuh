@@ -213,12 +213,12 @@ __device__ __forceinline__ bool schedule_seq_ok(const Common& c, int q0, int ql,
 // The FP8 prefill's list of tiles, longest first, with tiles split over their
 // keys where that shortens the launch (few rows against a long cache: chunked
 // prompts, cross attention, queries of a few tokens; 2 x 256 tokens against
-// 16384 keys, 32/8 heads of 128: 163 us, whole tiles 267).  A tile of more than
+// 16384 keys, 32/8 heads of 128: 165 us, whole tiles 281).  A tile of more than
 // S steps becomes ceil(steps / S) equal pieces: S is a CTA's share of all steps,
 // at least c.split_steps (a piece costs about two steps on top of its own, and
 // its rows are merged), twice that where decodes run beside on the SMs that
-// whole tiles leave (4 prompts of up to 400 tokens beside 28 decodes: 45.6 us,
-// in pieces 51.2).  If there are fewer tiles than CTAs, an S up to twice as
+// whole tiles leave (4 prompts of up to 400 tokens beside 28 decodes: 45.9 us,
+// in pieces 55.3).  If there are fewer tiles than CTAs, an S up to twice as
 // large whose pieces all run at once is taken; without one, only tiles of more
 // than two shares are worth it.  Everything follows from the call's lengths
 // alone, so results do not depend on the order of arrival.  Batches of more
