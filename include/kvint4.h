@@ -63,7 +63,8 @@ extern "C" {
 #define KV_INT4_ERR_WORKSPACE 6     /* workspace NULL or smaller than kv_int4_attention_workspace_size() */
 #define KV_INT4_ERR_SIZE 7          /* a negative count, or a size that overflows the index types */
 #define KV_INT4_ERR_CUDA 8          /* a CUDA call or kernel launch failed */
-#define KV_INT4_ERR_ROT 10          /* kv_qk_norm_rope: rot_dim negative, above head_size or no multiple of 16 */
+#define KV_INT4_ERR_ROT 10          /* kv_qk_norm_rope: rot_dim negative, above head_size or no multiple of 16;
+                                       kv_qk_norm_rope_axes also: axes outside their range */
 #define KV_INT4_ERR_SCRATCH_LIMIT 9 /* kv_int4_attention_noalloc: the call needs more workspace than
                                        KV_INT4_NOALLOC_SCRATCH_BYTES */
 
@@ -451,6 +452,82 @@ KVINT4_API int kv_fp8_attention(const void* q, int64_t q_token_stride, const uin
                                 int32_t* dev_status, void* stream);
 
 /*
+ * kv_fp8_attention_mass -- the attention weight that every position of an FP8
+ * cache receives, added up over calls: the measure by which kv_fp8_evict keeps
+ * positions.  For sequence i, kv head h and position p < seq_lens[i], with n_i
+ * query tokens that are its last n_i positions and a causal mask:
+ *   w = sum over the sequence's query rows (t, hq) of kv head h that see p of
+ *       exp(softmax_scale * q[t][hq] . k_hat_p - lse[t][hq])
+ *   mass[i][h][p] = w                    for the call's own positions, p >= seq_lens[i] - n_i
+ *                 = mass[i][h][p] + w    for the positions before
+ * so that a position's mass starts with the call that brings it and needs no
+ * clearing.  fp32 arithmetic and sums, in an order that the call's sizes and
+ * lengths fix.  Only K is read.
+ *
+ * lse: float, element (t, hq) at lse[t*lse_token_stride + hq]: the natural
+ *   logarithm of the row's denominator sum exp(softmax_scale * q . k_hat), as
+ *   kv_fp8_attention_shared returns it.  A row whose lse is an infinity adds nothing.
+ * mass: float, element (i, h, p) at mass[i*mass_seq_stride + h*mass_head_stride
+ *   + p], p < mass_len; rows must not overlap (KV_INT4_ERR_SIZE).  Positions at or behind
+ *   seq_lens[i] are left as they are.
+ * The other arguments, the device status bits and the errors are those of
+ * kv_fp8_attention.  A sequence with seq_lens[i] > mass_len is skipped and sets
+ * KV_INT4_DEV_BAD_SEQ; positions of a block outside [0, num_blocks) receive
+ * nothing and set KV_INT4_DEV_BAD_BLOCK.  Sequences may share blocks.
+ * max_seq_len bounds the seq_lens[i] (it sizes the launch); a longer sequence is
+ * skipped and sets KV_INT4_DEV_BAD_SEQ.
+ */
+KVINT4_API int kv_fp8_attention_mass(const void* q, int64_t q_token_stride, const float* lse, int64_t lse_token_stride,
+                                     const uint8_t* k_cache, const float* k_scale_cache, const int32_t* block_table,
+                                     int max_blocks_per_seq, const int32_t* seq_lens, const int32_t* query_start_loc,
+                                     int num_seqs, int num_q_tokens, int max_query_len, int max_seq_len,
+                                     int num_q_heads, int num_kv_heads, int head_size, int block_size, int num_blocks,
+                                     float softmax_scale, float* mass, int64_t mass_seq_stride,
+                                     int64_t mass_head_stride, int mass_len, int32_t* dev_status, void* stream);
+
+/*
+ * kv_fp8_evict -- shorten the sequences of an FP8 cache.  Sequence i with more
+ * than `budget` positions keeps, for each kv head on its own, its last `recent`
+ * ones and of the others the budget - recent with the largest mass (of equal
+ * ones the lowest; NaN counts as the smallest).  What is kept moves to the
+ * front in the order it had: with kept[i][h][j] the old position of row j,
+ *   row j of kv head h of the destination blocks = K and V of position kept[i][h][j]
+ *   mass_out[i][h][j] = mass[i][h][kept[i][h][j]]
+ *   new_lens[i] = min(seq_lens[i], budget)
+ * for j < new_lens[i]; elements behind are left as they are.  Sequences of at
+ * most `budget` positions keep all of them.  Codes and scales of a destination
+ * block are what kv_fp8_write would store for its rows' values (code * scale) in
+ * one call; a block whose rows all are where they were (in place, before the
+ * first position that goes) is left untouched.  Positions carry no order for
+ * attention but the mask's: keys keep the rotation that they were written with.
+ *
+ * dst_block_table: int32 [num_seqs][dst_max_blocks_per_seq]: block_table itself
+ *   or the same entries (in place), or blocks that no sequence of the call
+ *   reads.  No destination block may be named twice, and in place no other
+ *   sequence may share a block.  It must hold min(budget, mass_len,
+ *   max_blocks_per_seq * 16) positions (KV_INT4_ERR_SIZE otherwise).
+ * mass, mass_out: float, strides in elements, positions contiguous, mass_len of
+ *   them (mass_out: min(budget, mass_len), in rows that do not overlap:
+ *   KV_INT4_ERR_SIZE otherwise); mass_out may be mass.  Other overlaps are not
+ *   allowed.
+ * new_lens: int32 [num_seqs], not seq_lens (KV_INT4_ERR_SIZE).  kept: int32
+ *   [num_seqs][num_kv_heads][budget].
+ * budget >= 1, 0 <= recent <= budget (KV_INT4_ERR_SIZE otherwise).
+ * A sequence with seq_lens[i] < 0, above max_blocks_per_seq * 16 or above mass_len
+ * is left alone, its new_lens is its seq_lens, and it sets KV_INT4_DEV_BAD_SEQ.
+ * Rows of a block outside [0, num_blocks), or with a scale that no write stores,
+ * move as zeros; the former, and a destination block outside, which is not
+ * written, set KV_INT4_DEV_BAD_BLOCK.  num_seqs == 0 is a no-op.
+ */
+KVINT4_API int kv_fp8_evict(uint8_t* k_cache, uint8_t* v_cache, float* k_scale_cache, float* v_scale_cache,
+                            int num_blocks, int block_size, int num_kv_heads, int head_size, const float* mass,
+                            int64_t mass_seq_stride, int64_t mass_head_stride, int mass_len,
+                            const int32_t* block_table, int max_blocks_per_seq, const int32_t* seq_lens, int num_seqs,
+                            int budget, int recent, const int32_t* dst_block_table, int dst_max_blocks_per_seq,
+                            float* mass_out, int64_t mass_out_seq_stride, int64_t mass_out_head_stride,
+                            int32_t* new_lens, int32_t* kept, int32_t* dev_status, void* stream);
+
+/*
  * kv_qk_norm_rope -- RMS norm of every query and key head vector and the rotary
  * position rotation in one pass, the step before a cache write:
  *   y = x / sqrt(mean_i(x_i^2) + eps) * w
@@ -479,6 +556,28 @@ KVINT4_API int kv_qk_norm_rope(const void* q, int64_t q_token_stride, const void
                                const float* cos_sin, int64_t max_position, int rot_dim, int interleaved,
                                void* q_out, int64_t q_out_token_stride, void* k_out, int64_t k_out_token_stride,
                                int32_t* dev_status, void* stream);
+
+/*
+ * kv_qk_norm_rope_axes -- kv_qk_norm_rope for tokens whose positions have
+ * several axes (time, height and width of an image's or a video's tokens): pair
+ * i takes the cosine and sine in column i of the row cos_sin[positions of axis
+ * pair_axis[i]].  Everything else is as there.
+ *
+ * positions: int64, axis x of token t at positions[x*position_axis_stride + t]
+ *   (a stride of 0: all axes the same); num_axes of them, 1 to 4
+ *   (KV_INT4_ERR_ROT otherwise).  A token with a position outside [0,
+ *   max_position) along any axis is skipped and sets KV_INT4_DEV_BAD_POS.
+ * pair_axis: a HOST array of rot_dim / 2 axes below num_axes (KV_INT4_ERR_ROT
+ *   otherwise), read during the call; not read when rot_dim == 0.  Where every
+ *   axis has frequencies of its own, the table's columns hold them.
+ */
+KVINT4_API int kv_qk_norm_rope_axes(const void* q, int64_t q_token_stride, const void* k, int64_t k_token_stride,
+                                    int num_tokens, int num_q_heads, int num_kv_heads, int head_size,
+                                    const void* q_weight, const void* k_weight, float eps, const int64_t* positions,
+                                    int64_t position_axis_stride, int num_axes, const uint8_t* pair_axis,
+                                    const float* cos_sin, int64_t max_position, int rot_dim, int interleaved,
+                                    void* q_out, int64_t q_out_token_stride, void* k_out, int64_t k_out_token_stride,
+                                    int32_t* dev_status, void* stream);
 
 /*
  * kv_int4_rht -- the block-diagonal randomized Hadamard rotation on its own:

@@ -22,6 +22,7 @@ _lock = threading.Lock()
 _lib = None
 
 c_int, c_int64, c_void_p, c_size_t, c_float = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
+c_char_p = ctypes.c_char_p
 
 _SIGNATURES = {
     "kv_int4_write": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int, c_void_p, c_void_p,
@@ -79,6 +80,15 @@ _SIGNATURES_FP8 = {
                                 c_float, c_void_p, c_void_p, c_int64, c_int, c_int, c_void_p, c_int64, c_void_p,
                                 c_int64, c_void_p, c_void_p]),
     "kv_fp8_attention_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int]),
+    "kv_qk_norm_rope_axes": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_int, c_int, c_int, c_int, c_void_p,
+                                     c_void_p, c_float, c_void_p, c_int64, c_int, c_char_p, c_void_p, c_int64, c_int,
+                                     c_int, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p]),
+    "kv_fp8_attention_mass": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_int,
+                                      c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
+                                      c_int, c_float, c_void_p, c_int64, c_int64, c_int, c_void_p, c_void_p]),
+    "kv_fp8_evict": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_int64,
+                             c_int64, c_int, c_void_p, c_int, c_void_p, c_int, c_int, c_int, c_void_p, c_int, c_void_p,
+                             c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_void_p]),
 }
 
 OK = 0
@@ -439,7 +449,7 @@ def _no_call(*args):
 class _Calls:
     """The FP8 calls of _fp8_binding (a status, or None for arguments that the
     functions below look at themselves); without the module all return None."""
-    write = read = attention = norm_rope = staticmethod(_no_call)
+    write = read = attention = norm_rope = norm_rope_axes = mass = evict = staticmethod(_no_call)
 
 
 def _calls():
@@ -452,7 +462,8 @@ def _calls():
         m = _Calls
     else:
         m.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
-                 for f in ("kv_fp8_write", "kv_fp8_read", "kv_fp8_attention", "kv_qk_norm_rope")))
+                 for f in ("kv_fp8_write", "kv_fp8_read", "kv_fp8_attention", "kv_qk_norm_rope",
+                           "kv_qk_norm_rope_axes", "kv_fp8_attention_mass", "kv_fp8_evict")))
     _fp8 = m
     return m
 
@@ -620,6 +631,31 @@ def attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, 
         _raise(code, "kv_fp8_attention")
 
 
+def _norm_rope_vectors(q, k, q_weight, k_weight, q_out, k_out):
+    """(tokens, q heads, kv heads, d, token strides of q, k, q_out and k_out, weight pointers)."""
+    if q.dim() != 3 or k.dim() != 3:
+        _refuse("q and k must be [tokens, heads, d]")
+    tokens, hq, d = q.shape
+    hkv = k.shape[1]
+    qs, ks = _rows(q, "q", tokens, hq, d), _rows(k, "k", tokens, hkv, d)
+    qo, ko = _rows(q_out, "q_out", tokens, hq, d), _rows(k_out, "k_out", tokens, hkv, d)
+    qw = kw = None
+    if q_weight is not None and k_weight is not None:
+        for w in (q_weight, k_weight):
+            if w.dtype != torch.bfloat16 or w.shape != (d,) or not w.is_contiguous():
+                _refuse("weights must be bfloat16 [d]")
+        qw, kw = q_weight.data_ptr(), k_weight.data_ptr()
+    elif q_weight is not k_weight:
+        _refuse("q_weight and k_weight: both or neither")
+    return tokens, hq, hkv, d, qs, ks, qo, ko, qw, kw
+
+
+def _cos_sin(cos_sin):
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        _refuse("cos_sin must be contiguous float32 [max_position, rot]")
+    return cos_sin.shape
+
+
 def qk_norm_rope(q, k, positions, cos_sin, q_weight, k_weight, eps, q_out, k_out, interleaved: bool = False,
                  dev_status: Optional[torch.Tensor] = None, stream=None):
     """RMS norm of every query and key head vector, then the rotary rotation,
@@ -635,27 +671,14 @@ def qk_norm_rope(q, k, positions, cos_sin, q_weight, k_weight, eps, q_out, k_out
         return
     if code is not None:
         _raise(code, "kv_qk_norm_rope")
-    if q.dim() != 3 or k.dim() != 3:
-        _refuse("q and k must be [tokens, heads, d]")
-    tokens, hq, d = q.shape
-    hkv = k.shape[1]
-    qs, ks = _rows(q, "q", tokens, hq, d), _rows(k, "k", tokens, hkv, d)
-    qo, ko = _rows(q_out, "q_out", tokens, hq, d), _rows(k_out, "k_out", tokens, hkv, d)
-    qw = kw = pos = table = None
+    vectors = _norm_rope_vectors(q, k, q_weight, k_weight, q_out, k_out)
+    tokens, hq, hkv, d, qs, ks, qo, ko, qw, kw = vectors
+    pos = table = None
     max_pos = rot = 0
-    if q_weight is not None and k_weight is not None:
-        for w in (q_weight, k_weight):
-            if w.dtype != torch.bfloat16 or w.shape != (d,) or not w.is_contiguous():
-                _refuse("weights must be bfloat16 [d]")
-        qw, kw = q_weight.data_ptr(), k_weight.data_ptr()
-    elif q_weight is not k_weight:
-        _refuse("q_weight and k_weight: both or neither")
     if cos_sin is not None and positions is not None:
-        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
-            _refuse("cos_sin must be contiguous float32 [max_position, rot]")
+        max_pos, rot = _cos_sin(cos_sin)
         if positions.dtype != torch.int64 or positions.shape != (tokens,) or not positions.is_contiguous():
             _refuse("positions must be contiguous int64 [tokens]")
-        max_pos, rot = cos_sin.shape
         pos, table = positions.data_ptr(), cos_sin.data_ptr()
     elif cos_sin is not positions:
         _refuse("positions and cos_sin: both or neither")
@@ -671,3 +694,143 @@ def qk_norm_rope(q, k, positions, cos_sin, q_weight, k_weight, eps, q_out, k_out
         1 if interleaved else 0, q_out.data_ptr(), qo, k_out.data_ptr(), ko, _status_ptr(dev_status, dev), st)
     if code:
         _raise(code, "kv_qk_norm_rope")
+
+
+def rope_axes(sections, turns: bool = False) -> bytes:
+    """The axis of every rotation pair for qk_norm_rope_axes: sections[a] pairs
+    of axis a, the axes one after the other, or (turns) a pair of each axis in turn
+    while it has pairs left: rope_axes((24, 20, 20), turns=True) begins 0 1 2 0 1 2
+    and ends 0 0 0 0."""
+    left = [operator.index(n) for n in sections]
+    if min(left, default=0) < 0:
+        _refuse("sections must not be negative")
+    if not turns:
+        return bytes(a for a, n in enumerate(left) for _ in range(n))
+    return bytes(a for i in range(max(left, default=0)) for a, n in enumerate(left) if i < n)
+
+
+def qk_norm_rope_axes(q, k, positions, cos_sin, pair_axis, q_weight, k_weight, eps, q_out, k_out,
+                      interleaved: bool = False, dev_status: Optional[torch.Tensor] = None, stream=None):
+    """qk_norm_rope for positions with several axes, through kv_qk_norm_rope_axes.
+
+    positions: int64 [axes, tokens]; cos_sin: float32 [max_position, rot];
+    pair_axis: the axis of every rotation pair as rot / 2 bytes (rope_axes gives
+    them).  The rest is as in qk_norm_rope."""
+    code = (_fp8 or _calls()).norm_rope_axes(q, k, positions, cos_sin, pair_axis, q_weight, k_weight, eps, q_out, k_out,
+                                             interleaved, dev_status, stream)
+    if code == 0:
+        return
+    if code is not None:
+        _raise(code, "kv_qk_norm_rope_axes")
+    tokens, hq, hkv, d, qs, ks, qo, ko, qw, kw = _norm_rope_vectors(q, k, q_weight, k_weight, q_out, k_out)
+    max_pos, rot = _cos_sin(cos_sin)
+    if positions.dtype != torch.int64 or positions.dim() != 2 or positions.shape[1] != tokens or (
+            tokens > 1 and positions.stride(1) != 1):
+        _refuse("positions must be int64 [axes, tokens], contiguous along the tokens")
+    pair_axis = bytes(pair_axis)
+    if len(pair_axis) != rot // 2:
+        _refuse(f"pair_axis must name the axes of {rot // 2} pairs, got {len(pair_axis)}")
+    dev = q.get_device()
+    same = k.get_device() == q_out.get_device() == k_out.get_device() == positions.get_device() == cos_sin.get_device() == dev
+    if qw is not None:
+        same = same and q_weight.get_device() == k_weight.get_device() == dev
+    st = _raw_stream(dev, same, stream)
+    code = (_lib or load()).kv_qk_norm_rope_axes(
+        q.data_ptr(), qs, k.data_ptr(), ks, tokens, hq, hkv, d, qw, kw, eps, positions.data_ptr(), positions.stride(0),
+        positions.shape[0], pair_axis, cos_sin.data_ptr(), max_pos, rot, 1 if interleaved else 0, q_out.data_ptr(), qo,
+        k_out.data_ptr(), ko, _status_ptr(dev_status, dev), st)
+    if code:
+        _raise(code, "kv_qk_norm_rope_axes")
+
+
+def _mass_rows(x, name: str, seqs: int, hkv: int):
+    """(sequence stride, head stride, positions) of float32 [seqs, heads, positions]."""
+    if x.dtype is not torch.float32 or x.dim() != 3 or x.shape[0] != seqs or x.shape[1] != hkv:
+        _refuse(f"{name} must be float32 [{seqs}, {hkv}, positions]")
+    if x.shape[2] > 1 and x.stride(2) != 1:
+        _refuse(f"{name} must be contiguous along the positions")
+    return x.stride(0), x.stride(1), x.shape[2]
+
+
+def attention_mass_fp8(q, lse, k_cache, k_scale, block_table, seq_lens, query_start_loc, max_query_len, max_seq_len,
+                       softmax_scale, mass, dev_status: Optional[torch.Tensor] = None, stream=None):
+    """Add the causal attention weight that every position receives from the
+    call's queries to mass (float32 [seqs, kv heads, positions]), in place, through
+    kv_fp8_attention_mass; the call's own positions start from it.
+
+    lse: float32 [tokens, q_heads], the logarithm of the rows' denominators as
+    attention_fp8_shared gives it.  mass rows must not overlap."""
+    code = (_fp8 or _calls()).mass(q, lse, k_cache, k_scale, block_table, seq_lens, query_start_loc, max_query_len,
+                                   max_seq_len, softmax_scale, mass, dev_status, stream)
+    if code == 0:
+        return
+    if code is not None:
+        _raise(code, "kv_fp8_attention_mass")
+    nb, bs, hkv, d = _cache_dims_fp8(k_cache, k_cache, k_scale, k_scale)
+    num_seqs, width = _sequences(block_table, seq_lens, query_start_loc)
+    if q.dim() != 3:
+        _refuse("q must be [tokens, q_heads, d]")
+    tokens, hq, _ = q.shape
+    qs = _rows(q, "q", tokens, hq, d)
+    if lse.dtype is not torch.float32 or lse.shape != (tokens, hq) or (hq > 1 and lse.stride(1) != 1):
+        _refuse("lse must be float32 [tokens, q_heads], contiguous along the heads")
+    ms, mh, room = _mass_rows(mass, "mass", num_seqs, hkv)
+    max_query_len, max_seq_len = _int32(max_query_len, "max_query_len"), _int32(max_seq_len, "max_seq_len")
+    dev = k_cache.get_device()
+    st = _raw_stream(dev, k_scale.get_device() == block_table.get_device() == seq_lens.get_device()
+                     == query_start_loc.get_device() == q.get_device() == lse.get_device() == mass.get_device() == dev, stream)
+    code = (_lib or load()).kv_fp8_attention_mass(
+        q.data_ptr(), qs, lse.data_ptr(), lse.stride(0) if tokens > 1 else hq, k_cache.data_ptr(), k_scale.data_ptr(),
+        block_table.data_ptr(), width, seq_lens.data_ptr(), query_start_loc.data_ptr(), num_seqs, tokens, max_query_len,
+        max_seq_len, hq, hkv, d, bs, nb, softmax_scale, mass.data_ptr(), ms, mh, _int32(room, "positions"),
+        _status_ptr(dev_status, dev), st)
+    if code:
+        _raise(code, "kv_fp8_attention_mass")
+
+
+def evict_fp8(k_cache, v_cache, k_scale, v_scale, mass, block_table, seq_lens, budget, recent, dst_block_table,
+              mass_out, new_lens, kept, dev_status: Optional[torch.Tensor] = None, stream=None):
+    """Keep `budget` positions per (sequence, kv head) of the FP8 cache, the last
+    `recent` ones and the heaviest others, moved to the front of the blocks of
+    dst_block_table (block_table itself: in place), through kv_fp8_evict.
+
+    mass: float32 [seqs, kv heads, positions]; mass_out gets the kept ones' (it
+    may be mass).  new_lens: int32 [seqs]; kept: int32 [seqs, kv heads, budget], the
+    old positions."""
+    code = (_fp8 or _calls()).evict(k_cache, v_cache, k_scale, v_scale, mass, block_table, seq_lens, budget, recent,
+                                    dst_block_table, mass_out, new_lens, kept, dev_status, stream)
+    if code == 0:
+        return
+    if code is not None:
+        _raise(code, "kv_fp8_evict")
+    nb, bs, hkv, d = _cache_dims_fp8(k_cache, v_cache, k_scale, v_scale)
+    budget, recent = _int32(budget, "budget"), _int32(recent, "recent")
+    tables = []
+    for t, name in ((block_table, "block_table"), (dst_block_table, "dst_block_table")):
+        if t.dtype is not torch.int32 or t.dim() != 2 or not t.is_contiguous():
+            _refuse(f"{name} must be contiguous int32 [seqs, max_blocks]")
+        tables.append(t.shape)
+    (num_seqs, width), (dst_seqs, dst_width) = tables
+    if dst_seqs != num_seqs:
+        _refuse("the block tables disagree on sequences")
+    for t, name in ((seq_lens, "seq_lens"), (new_lens, "new_lens")):
+        if t.dtype is not torch.int32 or t.shape != (num_seqs,) or not t.is_contiguous():
+            _refuse(f"{name} must be contiguous int32 [seqs]")
+    if num_seqs and new_lens.data_ptr() == seq_lens.data_ptr():
+        _refuse("new_lens must not be seq_lens")
+    if kept.dtype is not torch.int32 or kept.shape != (num_seqs, hkv, budget) or not kept.is_contiguous():
+        _refuse("kept must be contiguous int32 [seqs, kv heads, budget]")
+    ms, mh, room = _mass_rows(mass, "mass", num_seqs, hkv)
+    os_, oh, out_room = _mass_rows(mass_out, "mass_out", num_seqs, hkv)
+    if out_room < min(budget, room):
+        _refuse("mass_out must have room for budget positions")
+    dev = k_cache.get_device()
+    st = _raw_stream(dev, all(t.get_device() == dev for t in (v_cache, k_scale, v_scale, mass, block_table, seq_lens,
+                                                              dst_block_table, mass_out, new_lens, kept)), stream)
+    code = (_lib or load()).kv_fp8_evict(
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), nb, bs, hkv, d, mass.data_ptr(),
+        ms, mh, _int32(room, "positions"), block_table.data_ptr(), width, seq_lens.data_ptr(), num_seqs, budget, recent,
+        dst_block_table.data_ptr(), dst_width, mass_out.data_ptr(), os_, oh, new_lens.data_ptr(), kept.data_ptr(),
+        _status_ptr(dev_status, dev), st)
+    if code:
+        _raise(code, "kv_fp8_evict")

@@ -34,6 +34,15 @@ int check_cache(const void* k_cache, const void* v_cache, const float* k_scale, 
   return KV_INT4_OK;
 }
 
+// whether rows of len floats at (sequence, head) strides do not overlap
+bool rows_apart(int64_t seqs, int64_t seq_stride, int64_t heads, int64_t head_stride, int64_t len) {
+  if (seqs <= 1) return heads <= 1 || head_stride >= len;
+  if (heads <= 1) return seq_stride >= len;
+  const bool by_seq = seq_stride >= head_stride;  // the outer index
+  const int64_t outer = by_seq ? seq_stride : head_stride, inner = by_seq ? head_stride : seq_stride;
+  return inner >= len && outer >= len && (outer - len) / ((by_seq ? heads : seqs) - 1) >= inner;
+}
+
 int do_cache(const CacheFp8Args& a, int block_size, bool write, void* stream) {
   int e = check_sizes(a.num_seqs, a.num_tokens, a.max_len, a.max_blocks_per_seq, a.num_blocks, block_size,
                       a.num_kv_heads, a.head_size);
@@ -46,6 +55,26 @@ int do_cache(const CacheFp8Args& a, int block_size, bool write, void* stream) {
   if (current_device() < 0) return KV_INT4_ERR_CUDA;
   return write ? launch_write_fp8(a, static_cast<cudaStream_t>(stream))
                : launch_read_fp8(a, static_cast<cudaStream_t>(stream));
+}
+
+// both rotary entry points: validation, then the launch
+int do_norm_rope(const NormRopeArgs& a, void* stream) {
+  if (a.num_tokens < 0 || a.max_position < 0 || !(a.eps >= 0.f)) return KV_INT4_ERR_SIZE;
+  if (a.num_q_heads <= 0 || a.num_kv_heads <= 0) return KV_INT4_ERR_HEADS;
+  if (!head_size_ok(a.head_size)) return KV_INT4_ERR_HEAD_SIZE;
+  if (a.rot_dim < 0 || a.rot_dim > a.head_size || a.rot_dim % 16) return KV_INT4_ERR_ROT;
+  if ((int64_t)a.num_tokens * ((int64_t)a.num_q_heads + a.num_kv_heads) >= (1ll << 31)) return KV_INT4_ERR_SIZE;
+  if (a.num_tokens == 0) return KV_INT4_OK;
+  if (!a.q || !a.k || !a.q_out || !a.k_out || !a.q_weight != !a.k_weight ||
+      (a.rot_dim > 0 && (!a.positions || !a.cos_sin)))
+    return KV_INT4_ERR_NULL;
+  if (!aligned16(a.q) || !aligned16(a.k) || !aligned16(a.q_out) || !aligned16(a.k_out) || !aligned16(a.q_weight) ||
+      !aligned16(a.k_weight) || !stride_ok(a.q_stride) || !stride_ok(a.k_stride) || !stride_ok(a.q_out_stride) ||
+      !stride_ok(a.k_out_stride) || !aligned(a.dev_status, 4) ||
+      (a.rot_dim > 0 && (!aligned(a.positions, 8) || !aligned16(a.cos_sin))))
+    return KV_INT4_ERR_ALIGN;
+  if (current_device() < 0) return KV_INT4_ERR_CUDA;
+  return launch_norm_rope(a, static_cast<cudaStream_t>(stream));
 }
 
 }  // namespace
@@ -124,24 +153,94 @@ int kv_qk_norm_rope(const void* q, int64_t q_token_stride, const void* k, int64_
                     float eps, const int64_t* positions, const float* cos_sin, int64_t max_position, int rot_dim,
                     int interleaved, void* q_out, int64_t q_out_token_stride, void* k_out,
                     int64_t k_out_token_stride, int32_t* dev_status, void* stream) {
-  if (num_tokens < 0 || max_position < 0 || !(eps >= 0.f)) return KV_INT4_ERR_SIZE;
-  if (num_q_heads <= 0 || num_kv_heads <= 0) return KV_INT4_ERR_HEADS;
-  if (!head_size_ok(head_size)) return KV_INT4_ERR_HEAD_SIZE;
-  if (rot_dim < 0 || rot_dim > head_size || rot_dim % 16) return KV_INT4_ERR_ROT;
-  if ((int64_t)num_tokens * ((int64_t)num_q_heads + num_kv_heads) >= (1ll << 31)) return KV_INT4_ERR_SIZE;
-  if (num_tokens == 0) return KV_INT4_OK;
-  if (!q || !k || !q_out || !k_out || !q_weight != !k_weight || (rot_dim > 0 && (!positions || !cos_sin)))
-    return KV_INT4_ERR_NULL;
-  if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out) || !aligned16(q_weight) ||
-      !aligned16(k_weight) || !stride_ok(q_token_stride) || !stride_ok(k_token_stride) ||
-      !stride_ok(q_out_token_stride) || !stride_ok(k_out_token_stride) || !aligned(dev_status, 4) ||
-      (rot_dim > 0 && (!aligned(positions, 8) || !aligned16(cos_sin))))
-    return KV_INT4_ERR_ALIGN;
+  return do_norm_rope(NormRopeArgs{q, q_token_stride, k, k_token_stride, num_tokens, num_q_heads, num_kv_heads,
+                                   head_size, q_weight, k_weight, eps, positions, cos_sin, max_position, rot_dim,
+                                   interleaved != 0, q_out, q_out_token_stride, k_out, k_out_token_stride,
+                                   dev_status, 0, 0, {}},
+                      stream);
+}
+
+int kv_qk_norm_rope_axes(const void* q, int64_t q_token_stride, const void* k, int64_t k_token_stride, int num_tokens,
+                         int num_q_heads, int num_kv_heads, int head_size, const void* q_weight,
+                         const void* k_weight, float eps, const int64_t* positions, int64_t position_axis_stride,
+                         int num_axes, const uint8_t* pair_axis, const float* cos_sin, int64_t max_position,
+                         int rot_dim, int interleaved, void* q_out, int64_t q_out_token_stride, void* k_out,
+                         int64_t k_out_token_stride, int32_t* dev_status, void* stream) {
+  NormRopeArgs a{q, q_token_stride, k, k_token_stride, num_tokens, num_q_heads, num_kv_heads,
+                 head_size, q_weight, k_weight, eps, positions, cos_sin, max_position, rot_dim,
+                 interleaved != 0, q_out, q_out_token_stride, k_out, k_out_token_stride,
+                 dev_status, num_axes, position_axis_stride, {}};
+  if (num_axes < 1 || num_axes > kMaxAxes || rot_dim < 0 || rot_dim > 256) return KV_INT4_ERR_ROT;
+  if (position_axis_stride < 0) return KV_INT4_ERR_SIZE;
+  if (rot_dim > 0 && num_tokens > 0) {
+    if (!pair_axis) return KV_INT4_ERR_NULL;
+    for (int i = 0; i < rot_dim / 2; i++) {
+      if (pair_axis[i] >= num_axes) return KV_INT4_ERR_ROT;
+      a.pair_axis[i / 16] |= (uint32_t)pair_axis[i] << (2 * (i % 16));
+    }
+  }
+  return do_norm_rope(a, stream);
+}
+
+int kv_fp8_attention_mass(const void* q, int64_t q_token_stride, const float* lse, int64_t lse_token_stride,
+                          const uint8_t* k_cache, const float* k_scale_cache, const int32_t* block_table,
+                          int max_blocks_per_seq, const int32_t* seq_lens, const int32_t* query_start_loc, int num_seqs,
+                          int num_q_tokens, int max_query_len, int max_seq_len, int num_q_heads, int num_kv_heads,
+                          int head_size, int block_size, int num_blocks, float softmax_scale, float* mass,
+                          int64_t mass_seq_stride, int64_t mass_head_stride, int mass_len, int32_t* dev_status,
+                          void* stream) {
+  if (max_seq_len < 0 || mass_len < 0 || lse_token_stride < 0 || mass_seq_stride < 0 || mass_head_stride < 0)
+    return KV_INT4_ERR_SIZE;
+  if (num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads || num_q_heads / num_kv_heads > kPrefillRows)
+    return KV_INT4_ERR_HEADS;
+  int e = check_sizes(num_seqs, num_q_tokens, max_query_len, max_blocks_per_seq, num_blocks, block_size, num_kv_heads,
+                      head_size);
+  if (e != KV_INT4_OK) return e;
+  if ((int64_t)num_q_tokens * num_q_heads >= (1ll << 31)) return KV_INT4_ERR_SIZE;
+  if (num_seqs == 0 || num_q_tokens == 0) return KV_INT4_OK;
+  if (!q || !lse || !mass) return KV_INT4_ERR_NULL;
+  e = check_cache(k_cache, k_cache, k_scale_cache, k_scale_cache, block_table, seq_lens, query_start_loc, dev_status);
+  if (e != KV_INT4_OK) return e;
+  if (!aligned16(q) || !stride_ok(q_token_stride) || !aligned(lse, 4) || !aligned(mass, 4)) return KV_INT4_ERR_ALIGN;
+  if (!rows_apart(num_seqs, mass_seq_stride, num_kv_heads, mass_head_stride, mass_len)) return KV_INT4_ERR_SIZE;
   if (current_device() < 0) return KV_INT4_ERR_CUDA;
-  return launch_norm_rope(NormRopeArgs{q, q_token_stride, k, k_token_stride, num_tokens, num_q_heads, num_kv_heads,
-                                       head_size, q_weight, k_weight, eps, positions, cos_sin, max_position, rot_dim,
-                                       interleaved != 0, q_out, q_out_token_stride, k_out, k_out_token_stride,
-                                       dev_status},
+  return launch_mass_fp8(MassArgs{q, q_token_stride, lse, lse_token_stride, k_cache, k_scale_cache, block_table,
+                                  max_blocks_per_seq, seq_lens, query_start_loc, num_seqs, num_q_tokens, max_query_len,
+                                  max_seq_len, num_q_heads, num_kv_heads, head_size, num_blocks, softmax_scale, mass,
+                                  mass_seq_stride, mass_head_stride, mass_len, dev_status},
+                         static_cast<cudaStream_t>(stream));
+}
+
+int kv_fp8_evict(uint8_t* k_cache, uint8_t* v_cache, float* k_scale_cache, float* v_scale_cache, int num_blocks,
+                 int block_size, int num_kv_heads, int head_size, const float* mass, int64_t mass_seq_stride,
+                 int64_t mass_head_stride, int mass_len, const int32_t* block_table, int max_blocks_per_seq,
+                 const int32_t* seq_lens, int num_seqs, int budget, int recent, const int32_t* dst_block_table,
+                 int dst_max_blocks_per_seq, float* mass_out, int64_t mass_out_seq_stride, int64_t mass_out_head_stride,
+                 int32_t* new_lens, int32_t* kept, int32_t* dev_status, void* stream) {
+  if (budget < 1 || recent < 0 || recent > budget || mass_len < 0 || dst_max_blocks_per_seq < 0 ||
+      mass_seq_stride < 0 || mass_head_stride < 0 || mass_out_seq_stride < 0 || mass_out_head_stride < 0)
+    return KV_INT4_ERR_SIZE;
+  int e = check_sizes(num_seqs, 0, 0, max_blocks_per_seq, num_blocks, block_size, num_kv_heads, head_size);
+  if (e != KV_INT4_OK) return e;
+  // the longest sequence that is worked on, and what is kept of it
+  const int64_t table = (int64_t)max_blocks_per_seq * 16, most = table < mass_len ? table : mass_len;
+  if ((int64_t)dst_max_blocks_per_seq * 16 < (most < budget ? most : budget) ||
+      (int64_t)num_seqs * num_kv_heads >= (1ll << 26))
+    return KV_INT4_ERR_SIZE;
+  if (num_seqs == 0) return KV_INT4_OK;
+  if (!mass || !mass_out || !new_lens || !kept || !dst_block_table) return KV_INT4_ERR_NULL;
+  e = check_cache(k_cache, v_cache, k_scale_cache, v_scale_cache, block_table, seq_lens, new_lens, dev_status);
+  if (e != KV_INT4_OK) return e;
+  if (!aligned(mass, 4) || !aligned(mass_out, 4) || !aligned(kept, 4) || !aligned(dst_block_table, 4))
+    return KV_INT4_ERR_ALIGN;
+  if (new_lens == seq_lens || !rows_apart(num_seqs, mass_out_seq_stride, num_kv_heads, mass_out_head_stride,
+                                          most < budget ? most : budget))
+    return KV_INT4_ERR_SIZE;
+  if (current_device() < 0) return KV_INT4_ERR_CUDA;
+  return launch_evict_fp8(EvictArgs{k_cache, v_cache, k_scale_cache, v_scale_cache, num_blocks, num_kv_heads, head_size,
+                                    mass, mass_seq_stride, mass_head_stride, mass_len, block_table, max_blocks_per_seq,
+                                    seq_lens, num_seqs, budget, recent, dst_block_table, dst_max_blocks_per_seq,
+                                    mass_out, mass_out_seq_stride, mass_out_head_stride, new_lens, kept, dev_status},
                           static_cast<cudaStream_t>(stream));
 }
 

@@ -22,6 +22,9 @@ decltype(&kv_fp8_write) g_write = nullptr;
 decltype(&kv_fp8_read) g_read = nullptr;
 decltype(&kv_fp8_attention) g_attention = nullptr;
 decltype(&kv_qk_norm_rope) g_norm_rope = nullptr;
+decltype(&kv_qk_norm_rope_axes) g_norm_rope_axes = nullptr;
+decltype(&kv_fp8_attention_mass) g_mass = nullptr;
+decltype(&kv_fp8_evict) g_evict = nullptr;
 
 struct NotPlain {};
 
@@ -199,38 +202,58 @@ PyObject* fp8_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// the head vectors, their outputs and weights of the rotary calls
+struct Vectors {
+  int tokens, hq, hkv, d;
+  int64_t qs, ks, qos, kos;
+  void *q, *k, *qo, *ko, *qw = nullptr, *kw = nullptr;
+  Vectors(Device& dev, PyObject* aq, PyObject* ak, PyObject* wq, PyObject* wk, PyObject* oq, PyObject* ok) {
+    const at::Tensor &x = tensor(aq), &y = tensor(ak), &xo = tensor(oq), &yo = tensor(ok);
+    need(x.dim() == 3 && y.dim() == 3 && x.size(0) <= INT_MAX && x.size(1) <= INT_MAX && y.size(1) <= INT_MAX &&
+         x.size(2) <= INT_MAX);
+    tokens = (int)x.size(0), hq = (int)x.size(1), hkv = (int)y.size(1), d = (int)x.size(2);
+    qs = rows(x, tokens, hq, d), ks = rows(y, tokens, hkv, d);
+    qos = rows(xo, tokens, hq, d), kos = rows(yo, tokens, hkv, d);
+    q = dev.of(x), k = dev.of(y), qo = dev.of(xo), ko = dev.of(yo);
+    need((wq == Py_None) == (wk == Py_None));
+    if (wq != Py_None) {
+      const at::Tensor &w = tensor(wq), &v = tensor(wk);
+      for (const at::Tensor* t : {&w, &v})
+        need(t->scalar_type() == at::kBFloat16 && t->dim() == 1 && t->size(0) == d && t->is_contiguous());
+      qw = dev.of(w);
+      kw = dev.of(v);
+    }
+  }
+};
+
+// a table of cosines and sines
+struct Table {
+  float* of;
+  int max_pos, rot;
+  Table(Device& dev, const at::Tensor& t) {
+    need(t.scalar_type() == at::kFloat && t.dim() == 2 && t.is_contiguous() && t.size(0) <= INT_MAX &&
+         t.size(1) <= INT_MAX);
+    max_pos = (int)t.size(0), rot = (int)t.size(1);
+    of = static_cast<float*>(dev.of(t));
+  }
+};
+
 // (q, k, positions, cos_sin, q_weight, k_weight, eps, q_out, k_out, interleaved, dev_status, stream)
 PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return call([&] {
     need(n == 12 && g_norm_rope);
     Device dev;
-    const at::Tensor &q = tensor(a[0]), &k = tensor(a[1]), &qo = tensor(a[7]), &ko = tensor(a[8]);
-    need(q.dim() == 3 && k.dim() == 3 && q.size(0) <= INT_MAX && q.size(1) <= INT_MAX && k.size(1) <= INT_MAX &&
-         q.size(2) <= INT_MAX);
-    const int tokens = (int)q.size(0), hq = (int)q.size(1), hkv = (int)k.size(1), d = (int)q.size(2);
-    const int64_t qs = rows(q, tokens, hq, d), ks = rows(k, tokens, hkv, d);
-    const int64_t qos = rows(qo, tokens, hq, d), kos = rows(ko, tokens, hkv, d);
-    void *qp = dev.of(q), *kp = dev.of(k), *qop = dev.of(qo), *kop = dev.of(ko);
-    void *qw = nullptr, *kw = nullptr;
+    const Vectors x(dev, a[0], a[1], a[4], a[5], a[7], a[8]);
     int64_t* pos = nullptr;
     float* table = nullptr;
     int max_pos = 0, rot = 0;
-    need((a[4] == Py_None) == (a[5] == Py_None) && (a[2] == Py_None) == (a[3] == Py_None));
-    if (a[4] != Py_None) {
-      const at::Tensor &w = tensor(a[4]), &x = tensor(a[5]);
-      for (const at::Tensor* t : {&w, &x})
-        need(t->scalar_type() == at::kBFloat16 && t->dim() == 1 && t->size(0) == d && t->is_contiguous());
-      qw = dev.of(w);
-      kw = dev.of(x);
-    }
+    need((a[2] == Py_None) == (a[3] == Py_None));
     if (a[2] != Py_None) {
-      const at::Tensor &p = tensor(a[2]), &t = tensor(a[3]);
-      need(t.scalar_type() == at::kFloat && t.dim() == 2 && t.is_contiguous() && t.size(0) <= INT_MAX &&
-           t.size(1) <= INT_MAX);
-      need(p.scalar_type() == at::kLong && p.dim() == 1 && p.size(0) == tokens && p.is_contiguous());
-      max_pos = (int)t.size(0), rot = (int)t.size(1);
+      const at::Tensor& p = tensor(a[2]);
+      need(p.scalar_type() == at::kLong && p.dim() == 1 && p.size(0) == x.tokens && p.is_contiguous());
+      const Table t(dev, tensor(a[3]));
+      max_pos = t.max_pos, rot = t.rot, table = t.of;
       pos = static_cast<int64_t*>(dev.of(p));
-      table = static_cast<float*>(dev.of(t));
     }
     const float eps = real(a[6]);
     need(PyBool_Check(a[9]));
@@ -238,20 +261,124 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int32_t* st = dev.status(a[10]);
     void* stream = dev.stream(a[11]);
     return [=] {
-      return g_norm_rope(qp, qs, kp, ks, tokens, hq, hkv, d, qw, kw, eps, pos, table, max_pos, rot, inter, qop, qos, kop,
-                         kos, st, stream);
+      return g_norm_rope(x.q, x.qs, x.k, x.ks, x.tokens, x.hq, x.hkv, x.d, x.qw, x.kw, eps, pos, table, max_pos, rot,
+                         inter, x.qo, x.qos, x.ko, x.kos, st, stream);
     };
   });
 }
 
-// bind(write, read, attention, norm_rope): the library's functions
+// (q, k, positions, cos_sin, pair_axis, q_weight, k_weight, eps, q_out, k_out, interleaved, dev_status, stream)
+PyObject* norm_rope_axes(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call([&] {
+    need(n == 13 && g_norm_rope_axes);
+    Device dev;
+    const Vectors x(dev, a[0], a[1], a[5], a[6], a[8], a[9]);
+    const at::Tensor& p = tensor(a[2]);
+    need(p.scalar_type() == at::kLong && p.dim() == 2 && p.size(0) <= INT_MAX && p.size(1) == x.tokens &&
+         (x.tokens <= 1 || p.stride(1) == 1));
+    const Table t(dev, tensor(a[3]));
+    need(PyBytes_Check(a[4]) && PyBytes_GET_SIZE(a[4]) == t.rot / 2);
+    const uint8_t* axes = reinterpret_cast<const uint8_t*>(PyBytes_AS_STRING(a[4]));  // the caller holds it
+    const int num_axes = (int)p.size(0);
+    const int64_t axis_stride = p.stride(0);
+    int64_t* pos = static_cast<int64_t*>(dev.of(p));
+    const float eps = real(a[7]);
+    need(PyBool_Check(a[10]));
+    const int inter = a[10] == Py_True;
+    int32_t* st = dev.status(a[11]);
+    void* stream = dev.stream(a[12]);
+    return [=] {
+      return g_norm_rope_axes(x.q, x.qs, x.k, x.ks, x.tokens, x.hq, x.hkv, x.d, x.qw, x.kw, eps, pos, axis_stride,
+                              num_axes, axes, t.of, t.max_pos, t.rot, inter, x.qo, x.qos, x.ko, x.kos, st, stream);
+    };
+  });
+}
+
+// masses [sequences, kv heads, positions]
+struct Mass {
+  float* of;
+  int64_t seq, head;
+  int room;
+  Mass(Device& dev, const at::Tensor& t, int64_t seqs, int64_t heads) {
+    need(t.scalar_type() == at::kFloat && t.dim() == 3 && t.size(0) == seqs && t.size(1) == heads &&
+         t.size(2) <= INT_MAX && (t.size(2) <= 1 || t.stride(2) == 1));
+    seq = t.stride(0), head = t.stride(1), room = (int)t.size(2);
+    of = static_cast<float*>(dev.of(t));
+  }
+};
+
+// (q, lse, k_cache, k_scale, block_table, seq_lens, query_start_loc, max_query_len, max_seq_len, softmax_scale, mass,
+//  dev_status, stream)
+PyObject* fp8_mass(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call([&] {
+    need(n == 13 && g_mass);
+    Device dev;
+    PyObject* const caches[4] = {a[2], a[2], a[3], a[3]};
+    const Caches c(dev, caches);
+    const Sequences s(dev, a + 4);
+    const at::Tensor &q = tensor(a[0]), &lse = tensor(a[1]);
+    need(q.dim() == 3 && q.size(0) <= INT_MAX && q.size(1) <= INT_MAX);
+    const int tokens = (int)q.size(0), hq = (int)q.size(1);
+    const int64_t qs = rows(q, tokens, hq, c.d);
+    need(lse.scalar_type() == at::kFloat && lse.dim() == 2 && lse.size(0) == tokens && lse.size(1) == hq &&
+         (hq <= 1 || lse.stride(1) == 1));
+    const int64_t ls = tokens > 1 ? lse.stride(0) : hq;
+    const Mass m(dev, tensor(a[10]), s.num, c.hkv);
+    const int max_q = integer(a[7]), max_len = integer(a[8]);
+    const float scale = real(a[9]);
+    void* qp = dev.of(q);
+    float* lp = static_cast<float*>(dev.of(lse));
+    int32_t* st = dev.status(a[11]);
+    void* stream = dev.stream(a[12]);
+    return [=] {
+      return g_mass(qp, qs, lp, ls, c.k, c.ks, s.table, s.width, s.lens, s.start, s.num, tokens, max_q, max_len, hq,
+                    (int)c.hkv, (int)c.d, (int)c.bs, (int)c.nb, scale, m.of, m.seq, m.head, m.room, st, stream);
+    };
+  });
+}
+
+// (k_cache, v_cache, k_scale, v_scale, mass, block_table, seq_lens, budget, recent, dst_block_table, mass_out, new_lens,
+//  kept, dev_status, stream)
+PyObject* fp8_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call([&] {
+    need(n == 15 && g_evict);
+    Device dev;
+    const Caches c(dev, a);
+    const int budget = integer(a[7]), recent = integer(a[8]);
+    const at::Tensor &t = tensor(a[5]), &to = tensor(a[9]), &l = tensor(a[6]), &nl = tensor(a[11]), &kept = tensor(a[12]);
+    for (const at::Tensor* x : {&t, &to})
+      need(x->scalar_type() == at::kInt && x->dim() == 2 && x->is_contiguous() && x->size(0) < INT_MAX &&
+           x->size(1) <= INT_MAX);
+    const int num = (int)t.size(0), width = (int)t.size(1), to_width = (int)to.size(1);
+    need(to.size(0) == num);
+    for (const at::Tensor* x : {&l, &nl})
+      need(x->scalar_type() == at::kInt && x->dim() == 1 && x->size(0) == num && x->is_contiguous());
+    need(kept.scalar_type() == at::kInt && kept.dim() == 3 && kept.size(0) == num && kept.size(1) == c.hkv &&
+         kept.size(2) == budget && kept.is_contiguous());
+    const Mass m(dev, tensor(a[4]), num, c.hkv), mo(dev, tensor(a[10]), num, c.hkv);
+    need(mo.room >= (m.room < budget ? m.room : budget));
+    int32_t *tp = static_cast<int32_t*>(dev.of(t)), *top = static_cast<int32_t*>(dev.of(to));
+    int32_t *lp = static_cast<int32_t*>(dev.of(l)), *nlp = static_cast<int32_t*>(dev.of(nl));
+    int32_t* kp = static_cast<int32_t*>(dev.of(kept));
+    need(num == 0 || lp != nlp);
+    int32_t* st = dev.status(a[13]);
+    void* stream = dev.stream(a[14]);
+    return [=] {
+      return g_evict(c.k, c.v, c.ks, c.vs, (int)c.nb, (int)c.bs, (int)c.hkv, (int)c.d, m.of, m.seq, m.head, m.room, tp,
+                     width, lp, num, budget, recent, top, to_width, mo.of, mo.seq, mo.head, nlp, kp, st, stream);
+    };
+  });
+}
+
+// bind(write, read, attention, norm_rope, norm_rope_axes, mass, evict): the library's functions
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  void* f[4];
-  if (n != 4) {
-    PyErr_SetString(PyExc_TypeError, "four addresses");
+  constexpr int N = 7;
+  void* f[N];
+  if (n != N) {
+    PyErr_SetString(PyExc_TypeError, "an address for each function");
     return nullptr;
   }
-  for (int i = 0; i < 4; i++) {
+  for (int i = 0; i < N; i++) {
     f[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred()) return nullptr;
   }
@@ -259,6 +386,9 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_read = reinterpret_cast<decltype(g_read)>(f[1]);
   g_attention = reinterpret_cast<decltype(g_attention)>(f[2]);
   g_norm_rope = reinterpret_cast<decltype(g_norm_rope)>(f[3]);
+  g_norm_rope_axes = reinterpret_cast<decltype(g_norm_rope_axes)>(f[4]);
+  g_mass = reinterpret_cast<decltype(g_mass)>(f[5]);
+  g_evict = reinterpret_cast<decltype(g_evict)>(f[6]);
   Py_RETURN_NONE;
 }
 
@@ -268,7 +398,8 @@ PyMethodDef method(const char* name) {
 }
 PyMethodDef g_methods[] = {method<bind>("bind"),           method<fp8_write>("write"),
                            method<fp8_read>("read"),       method<fp8_attention>("attention"),
-                           method<norm_rope>("norm_rope"), {nullptr, nullptr, 0, nullptr}};
+                           method<norm_rope>("norm_rope"), method<norm_rope_axes>("norm_rope_axes"),
+                           method<fp8_mass>("mass"),       method<fp8_evict>("evict"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_fp8_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

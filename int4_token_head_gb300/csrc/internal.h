@@ -151,7 +151,7 @@ struct CacheFp8Args {
 int launch_write_fp8(const CacheFp8Args& a, cudaStream_t stream);
 int launch_read_fp8(const CacheFp8Args& a, cudaStream_t stream);
 
-// kv_qk_norm_rope (norm_rope.cu)
+// kv_qk_norm_rope and kv_qk_norm_rope_axes (norm_rope.cu)
 struct NormRopeArgs {
   const void* q;
   int64_t q_stride;
@@ -174,8 +174,68 @@ struct NormRopeArgs {
   void* k_out;
   int64_t k_out_stride;
   int32_t* dev_status;
+  int num_axes;           // 0: one position per token
+  int64_t axis_stride;    // axis x's positions start at positions + x * axis_stride
+  uint32_t pair_axis[8];  // the axis of every rotation pair, two bits each (pair i: bits 2 i of word i / 16)
 };
+constexpr int kMaxAxes = 4;
 int launch_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
+
+// kv_fp8_evict (evict_fp8.cu)
+struct EvictArgs {
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  float* k_scale;
+  float* v_scale;
+  int num_blocks;
+  int num_kv_heads;
+  int head_size;
+  const float* mass;  // strides in elements, positions contiguous
+  int64_t mass_seq_stride, mass_head_stride;
+  int mass_len;
+  const int32_t* block_table;
+  int max_blocks_per_seq;
+  const int32_t* seq_lens;
+  int num_seqs;
+  int budget;
+  int recent;
+  const int32_t* dst_block_table;
+  int dst_max_blocks;
+  float* mass_out;
+  int64_t out_seq_stride, out_head_stride;
+  int32_t* new_lens;
+  int32_t* kept;  // [num_seqs][num_kv_heads][budget]
+  int32_t* dev_status;
+};
+int launch_evict_fp8(const EvictArgs& a, cudaStream_t stream);
+
+// kv_fp8_attention_mass (mass_fp8.cu)
+struct MassArgs {
+  const void* q;
+  int64_t q_stride;
+  const float* lse;  // [num_q_tokens][num_q_heads], token stride lse_stride
+  int64_t lse_stride;
+  const uint8_t* k_cache;
+  const float* k_scale;
+  const int32_t* block_table;
+  int max_blocks_per_seq;
+  const int32_t* seq_lens;
+  const int32_t* query_start_loc;
+  int num_seqs;
+  int num_q_tokens;
+  int max_query_len;
+  int max_seq_len;
+  int num_q_heads;
+  int num_kv_heads;
+  int head_size;
+  int num_blocks;
+  float softmax_scale;
+  float* mass;
+  int64_t mass_seq_stride, mass_head_stride;
+  int mass_len;
+  int32_t* dev_status;
+};
+int launch_mass_fp8(const MassArgs& a, cudaStream_t stream);
 
 struct AttnArgs {
   const void* q;

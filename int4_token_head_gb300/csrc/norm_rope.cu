@@ -1,10 +1,13 @@
-// kv_qk_norm_rope: RMS norm of every query and key head vector and the rotary
+// kv_qk_norm_rope, kv_qk_norm_rope_axes: RMS norm of every query and key head vector and the rotary
 // position rotation, in one pass over the heads.
 //
 //   y = x / sqrt(mean(x^2) + eps) * w            (no norm without weights)
 //   (y_i, y_j) <- (y_i cos - y_j sin, y_j cos + y_i sin)   for the rot / 2
 //     pairs of the first rot elements: (i, i + rot / 2), or (2 i, 2 i + 1)
-// in fp32, rounded once to bf16; squares that leave fp32's range are taken in
+// The angle of a pair is its token's position's, or with several axes (time,
+// height and width of an image's or a video's tokens) the position along the
+// axis that owns the pair (kv_qk_norm_rope_axes).
+// In fp32, rounded once to bf16; squares that leave fp32's range are taken in
 // units of the vector's largest element (far_rsqrt).
 //
 // HBM-bound (2 d bytes in and 2 d out per head vector).  d / 16 lanes hold a
@@ -86,8 +89,12 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     pack_bf16x2_rn(f[6], f[7]));
 }
 
-template <int D, int U>
-__global__ void __launch_bounds__(kNormWarps * 32, 8) norm_rope_kernel(NormRope p) {
+// AXES: a pair's cosine and sine come from the row of its axis's position.  A
+// lane loads its eight columns of the row of every axis that owns one of its
+// pairs: one row where the axes' pairs lie side by side, up to num_axes where they
+// take turns.
+template <int D, int U, bool AXES>
+__global__ void __launch_bounds__(kNormWarps * 32, AXES ? 7 : 8) norm_rope_kernel(NormRope p) {
   constexpr int LPV = D / 16;    // lanes per vector
   constexpr int VPW = 32 / LPV;  // vectors per warp step
   const NormRopeArgs& a = p.a;
@@ -125,19 +132,43 @@ __global__ void __launch_bounds__(kNormWarps * 32, 8) norm_rope_kernel(NormRope 
     cs[i] = 1.f;
     sn[i] = 0.f;
   }
+  auto load_row = [&](int64_t pos, uint32_t pairs) {  // pairs: bit 2 i set if pair 8 c + i is this row's
+    const float* row = a.cos_sin + pos * a.rot_dim + 8 * c;
+    const float4* pc = reinterpret_cast<const float4*>(row);
+    const float4* ps = reinterpret_cast<const float4*>(row + a.rot_dim / 2);
+    const float4 q0 = pc[0], q1 = pc[1], r0 = ps[0], r1 = ps[1];
+    const float x[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+    const float y[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+      if (!AXES || (pairs >> (2 * i) & 1)) {
+        cs[i] = x[i];
+        sn[i] = y[i];
+      }
+  };
   if (a.rot_dim > 0) {
-    const int64_t pos = a.positions[t];
-    if (pos < 0 || pos >= a.max_position) {
-      if (part == 0 && lane == 0) flag(a.dev_status, KV_INT4_DEV_BAD_POS);
-      return;
-    }
-    if (rotated) {
-      const float* row = a.cos_sin + pos * a.rot_dim + 8 * c;
-      const float4* pc = reinterpret_cast<const float4*>(row);
-      const float4* ps = reinterpret_cast<const float4*>(row + a.rot_dim / 2);
-      const float4 q0 = pc[0], q1 = pc[1], r0 = ps[0], r1 = ps[1];
-      cs[0] = q0.x; cs[1] = q0.y; cs[2] = q0.z; cs[3] = q0.w; cs[4] = q1.x; cs[5] = q1.y; cs[6] = q1.z; cs[7] = q1.w;
-      sn[0] = r0.x; sn[1] = r0.y; sn[2] = r0.z; sn[3] = r0.w; sn[4] = r1.x; sn[5] = r1.y; sn[6] = r1.z; sn[7] = r1.w;
+    if constexpr (AXES) {
+      const uint32_t owners = a.pair_axis[c >> 1] >> ((c & 1) * 16);  // two bits a pair
+      bool bad = false;
+#pragma unroll 1
+      for (int ax = 0; ax < a.num_axes; ax++) {
+        const int64_t pos = a.positions[ax * a.axis_stride + t];
+        bad = bad || pos < 0 || pos >= a.max_position;
+        const uint32_t other = owners ^ (0x5555u * ax);
+        const uint32_t pairs = ~(other | other >> 1) & 0x5555u;
+        if (rotated && !bad && pairs) load_row(pos, pairs);
+      }
+      if (bad) {
+        if (part == 0 && lane == 0) flag(a.dev_status, KV_INT4_DEV_BAD_POS);
+        return;
+      }
+    } else {
+      const int64_t pos = a.positions[t];
+      if (pos < 0 || pos >= a.max_position) {
+        if (part == 0 && lane == 0) flag(a.dev_status, KV_INT4_DEV_BAD_POS);
+        return;
+      }
+      if (rotated) load_row(pos, 0);
     }
   }
 #pragma unroll
@@ -215,7 +246,8 @@ int launch_t(const NormRopeArgs& a, cudaStream_t stream) {
   p.by_parts = FastDiv((uint32_t)p.parts);
   const int64_t warps = (int64_t)a.num_tokens * p.parts;
   if (warps >= (1ll << 31) - kNormWarps) return KV_INT4_ERR_SIZE;
-  return launch_pdl(norm_rope_kernel<D, U>, dim3((unsigned)((warps + kNormWarps - 1) / kNormWarps)), kNormWarps * 32, 0,
+  return launch_pdl(a.num_axes > 0 && a.rot_dim > 0 ? norm_rope_kernel<D, U, true> : norm_rope_kernel<D, U, false>,
+                    dim3((unsigned)((warps + kNormWarps - 1) / kNormWarps)), kNormWarps * 32, 0,
                     stream, 1, p);
 }
 

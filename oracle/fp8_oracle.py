@@ -1,5 +1,6 @@
-"""fp64 CPU definition of the FP8 block-scaled cache, of attention over it and
-of the query/key norm with the rotary rotation.
+"""fp64 CPU definition of the FP8 block-scaled cache, of attention over it, of the
+weights that positions receive and eviction by them, and of the query/key norm
+with the rotary rotation.
 
 Plain numpy written from the formulas, one sequence, block and head at a time;
 it shares no code with the CUDA path and is test infrastructure only.
@@ -168,3 +169,132 @@ def norm_rope(x, w, eps, cos_sin, positions, interleaved):
         y[..., lo] = u * cos - v * sin
         y[..., hi] = v * cos + u * sin
     return y
+
+
+def norm_rope_axes(x, w, eps, cos_sin, positions, pair_axis, interleaved):
+    """norm_rope with positions [axes, T] and the axis of every pair: pair by pair."""
+    y = norm_rope(x, w, eps, None, None, interleaved)
+    half = cos_sin.shape[1] // 2
+    table = np.asarray(cos_sin, np.float64)
+    for i, a in enumerate(pair_axis):
+        lo, hi = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+        cos, sin = table[positions[a], i][:, None], table[positions[a], half + i][:, None]
+        u, v = y[..., lo].copy(), y[..., hi].copy()
+        y[..., lo] = u * cos - v * sin
+        y[..., hi] = v * cos + u * sin
+    return y
+
+
+def _scores(q, codes, scale, table, length, n, i, h, group, softmax_scale, num_blocks):
+    """Causal scores [n, group, length] of sequence i's queries (q [n, Hq, D]) against kv head h, -inf where hidden or
+    without a block, and sums of |q k| and of max|q| |k| over the head."""
+    p = np.arange(length)
+    blk = table[i, p // BLOCK].astype(np.int64)
+    usable = (blk >= 0) & (blk < num_blocks)
+    safe = np.where(usable, blk, 0)
+    k = e4m3_values(codes[safe, p % BLOCK, h]) * scale[safe, h].astype(np.float64)[:, None]
+    k[~usable] = 0.0
+    x = q[:, h * group:(h + 1) * group]
+    seen = usable[None] & (p[None] <= (length - n + np.arange(n))[:, None])
+    s = np.einsum("ngd,kd->ngk", x, k) * softmax_scale
+    s = np.where(seen[:, None], s, -np.inf)
+    size = np.einsum("ngd,kd->ngk", np.abs(x), np.abs(k))
+    small = np.abs(x).max(2)[:, :, None] * np.abs(k).sum(1)[None, None]
+    return s, size, small
+
+
+def score_error(size, small, d, softmax_scale):
+    """What the kernels' arithmetic can be off in a score: an fp32 sum of D exact products and a final product or fma,
+    and the f16 spacing 2^-24 max|q| of query elements far below their row's largest."""
+    return abs(softmax_scale) * 2.0 ** -24 * ((d + 4) * size + small)
+
+
+def log_sum_exp(q, codes, scale, table, lens, start, softmax_scale, num_blocks=None):
+    """(lse, bound) [T, Hq] of causal attention; -inf for a row that sees no key.  bound: the scores' errors, exp2 and
+    the fp32 sums (n 2^-24 at most, 64 of them as in attention) move the sum by a share, the logarithm's own step and
+    the maximum that is added are 2^-22 of the result and of the largest score."""
+    q = np.asarray(q, np.float64)
+    nb = codes.shape[0] if num_blocks is None else num_blocks
+    hkv, d = codes.shape[2], codes.shape[3]
+    group = q.shape[1] // hkv
+    lse, bound = np.full(q.shape[:2], -np.inf), np.zeros(q.shape[:2])
+    for i in range(len(lens)):
+        a, b = int(start[i]), int(start[i + 1])
+        for h in range(hkv) if b > a else ():
+            s, size, small = _scores(q[a:b], codes, scale, table, int(lens[i]), b - a, i, h, group, softmax_scale, nb)
+            top = s.max(2, keepdims=True)
+            safe = np.where(np.isfinite(top), top, 0.0)
+            with np.errstate(divide="ignore"):
+                lse[a:b, h * group:(h + 1) * group] = (safe + np.log(np.exp(s - safe).sum(2, keepdims=True)))[..., 0]
+            err = np.where(np.isfinite(s), score_error(size, small, d, softmax_scale), 0.0).max(2)
+            bound[a:b, h * group:(h + 1) * group] = err + 2.0 ** -20 + 64 * 2.0 ** -24 + 2.0 ** -22 * (
+                np.abs(safe[..., 0]) + np.abs(np.where(np.isfinite(top[..., 0]), lse[a:b, h * group:(h + 1) * group], 0.0)))
+    return lse, bound
+
+
+def mass(q, lse, codes, scale, table, lens, start, softmax_scale, m, num_blocks=None):
+    """(mass, bound) [S, Hkv, positions] after a call on m.  A weight's exponent is off by the score's error and by the
+    rounding of lse log2 e and of the sum, 2^-23 (|s| + |lse|); exp2 adds 2^-21; the sum over the rows n 2^-24."""
+    q, lse = np.asarray(q, np.float64), np.asarray(lse, np.float64)
+    nb = codes.shape[0] if num_blocks is None else num_blocks
+    hkv, d = codes.shape[2], codes.shape[3]
+    group = q.shape[1] // hkv
+    m, bound = np.array(m, np.float64), np.zeros(m.shape)
+    for i in range(len(lens)):
+        a, b, length = int(start[i]), int(start[i + 1]), int(lens[i])
+        n = b - a
+        if n == 0:
+            continue
+        m[i, :, length - n:length] = 0.0
+        for h in range(hkv):
+            s, size, small = _scores(q[a:b], codes, scale, table, length, n, i, h, group, softmax_scale, nb)
+            l = lse[a:b, h * group:(h + 1) * group, None]
+            fine = np.isfinite(l)
+            l = np.where(fine, l, 0.0)
+            w = np.where(fine, np.exp(s - l), 0.0)
+            err = score_error(size, small, d, softmax_scale) + 2.0 ** -23 * (np.where(np.isfinite(s), np.abs(s), 0) + np.abs(l))
+            got = w.sum((0, 1))
+            m[i, h, :length] += got
+            bound[i, h, :length] = (w * (np.expm1(err) + 2.0 ** -21)).sum((0, 1)) + (n * group + 2) * 2.0 ** -24 * got
+            bound[i, h, :length] += 2.0 ** -24 * np.abs(m[i, h, :length])
+    return m, bound
+
+
+def keep(m, length, budget, recent):
+    """The positions that stay of a sequence for one kv head, ascending: the last `recent`, and of the others those of
+    the largest mass, equal ones from the lowest position on, NaN below everything."""
+    if length <= budget:
+        return np.arange(length)
+    x = np.where(np.isnan(m[:length - recent]), -np.inf, np.asarray(m[:length - recent], np.float64))
+    nan = np.isnan(m[:length - recent])
+    order = sorted(range(length - recent), key=lambda p: (nan[p], -x[p], p))
+    return np.array(sorted(order[:budget - recent] + list(range(length - recent, length))), np.int64)
+
+
+def evict(caches, m, table, lens, budget, recent, into, m_out, kept):
+    """Moves what stays of every sequence in the numpy arrays given; returns the new lengths."""
+    before = [np.array(x) for x in caches]
+    m = np.array(m)
+    new = []
+    for i, length in enumerate(int(x) for x in lens):
+        new.append(min(length, budget))
+        for h in range(caches[0].shape[2]):
+            idx = keep(m[i, h], length, budget, recent)
+            n = len(idx)
+            kept[i, h, :n], m_out[i, h, :n] = idx, m[i, h, idx]
+            for b in range(-(-n // BLOCK)):
+                rows = idx[b * BLOCK:(b + 1) * BLOCK]
+                to = int(into[i, b])
+                src = table[i, rows // BLOCK].astype(np.int64)
+                if (rows == b * BLOCK + np.arange(len(rows))).all() and (src == to).all() or not 0 <= to < caches[0].shape[0]:
+                    continue
+                for codes, scale, old_codes, old_scale in ((caches[0], caches[2], before[0], before[2]),
+                                                           (caches[1], caches[3], before[1], before[3])):
+                    x = np.zeros((len(rows), codes.shape[3]))
+                    for r, (s, p) in enumerate(zip(src, rows)):
+                        if 0 <= s < codes.shape[0] and stored_exponent(old_scale[s, h]) is not None:
+                            x[r] = e4m3_values(old_codes[s, p % BLOCK, h]) * float(old_scale[s, h])
+                    k = exponent(np.abs(x).max())
+                    codes[to, :len(rows), h] = e4m3_bytes(e4m3(np.ldexp(x, -k)))
+                    scale[to, h] = 2.0 ** k
+    return np.array(new, np.int32)
