@@ -452,6 +452,50 @@ KVINT4_API int kv_fp8_attention(const void* q, int64_t q_token_stride, const uin
                                 int32_t* dev_status, void* stream);
 
 /*
+ * kv_fp8_attention_shared -- causal attention over the FP8 cache for a batch in
+ * which groups of sequences have their first positions in common (answers to one
+ * prompt, conversations about one document): what a group shares is read once
+ * for all of its queries.  Results are those of kv_fp8_attention with causal != 0
+ * and no window, but for the order of sums; lse is also given.
+ *
+ * group_start: int32 [num_groups + 1], ascending from >= 0 to <= num_seqs: group
+ *   g are the sequences [group_start[g], group_start[g+1]); sequences outside all
+ *   groups share nothing.  num_groups in [0, 1024] (KV_INT4_ERR_SIZE otherwise).
+ *   One that does not ascend within the batch sets KV_INT4_DEV_BAD_SEQ, and
+ *   nothing is shared.
+ * prefix_lens: int32 [num_groups]: the first prefix_lens[g] positions of the
+ *   group's sequences are in the same blocks: their block table rows begin with
+ *   the same entries for prefix_lens[g] / 16 blocks, of which one row's are read.
+ *   What follows (the rest of a last block too) is each sequence's own.
+ * max_group_tokens: a bound of a group's query tokens, query_start_loc[
+ *   group_start[g+1]] - query_start_loc[group_start[g]] (it sizes the launch); a
+ *   group with more shares nothing.
+ * Sharing is a matter of speed alone: positions that some sequence's queries do
+ *   not follow, groups that save too little or whose rows outnumber the
+ *   workspace's, and short batches are computed without it.
+ * lse: float or NULL, element (t, hq) at lse[t*lse_token_stride + hq]: the natural
+ *   logarithm of the row's denominator, log sum_p exp(softmax_scale * q . k_hat_p);
+ *   -infinity for a row that sees no key (its output is zeros).
+ * Token strides of q, out and lse are at least a token's elements and num_blocks
+ *   is in [1, 2^27) (KV_INT4_ERR_SIZE otherwise).
+ * workspace: kv_fp8_attention_shared_workspace_size bytes at least; calls that may
+ *   run at the same time need one each.
+ * The other arguments, device status bits and errors are those of kv_fp8_attention.
+ */
+KVINT4_API size_t kv_fp8_attention_shared_workspace_size(int num_seqs, int num_groups, int num_q_tokens,
+                                                         int num_q_heads, int num_kv_heads, int head_size);
+KVINT4_API int kv_fp8_attention_shared(const void* q, int64_t q_token_stride, const uint8_t* k_cache,
+                                       const uint8_t* v_cache, const float* k_scale_cache,
+                                       const float* v_scale_cache, const int32_t* block_table, int max_blocks_per_seq,
+                                       const int32_t* seq_lens, const int32_t* query_start_loc, int num_seqs,
+                                       int num_q_tokens, int max_query_len, int max_seq_len, const int32_t* group_start,
+                                       const int32_t* prefix_lens, int num_groups, int max_group_tokens,
+                                       int num_q_heads, int num_kv_heads, int head_size, int block_size,
+                                       int num_blocks, float softmax_scale, void* out, int64_t out_token_stride,
+                                       float* lse, int64_t lse_token_stride, void* workspace, size_t workspace_bytes,
+                                       int32_t* dev_status, void* stream);
+
+/*
  * kv_fp8_attention_mass -- the attention weight that every position of an FP8
  * cache receives, added up over calls: the measure by which kv_fp8_evict keeps
  * positions.  For sequence i, kv head h and position p < seq_lens[i], with n_i

@@ -83,6 +83,11 @@ _SIGNATURES_FP8 = {
     "kv_qk_norm_rope_axes": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_int, c_int, c_int, c_int, c_void_p,
                                      c_void_p, c_float, c_void_p, c_int64, c_int, c_char_p, c_void_p, c_int64, c_int,
                                      c_int, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p]),
+    "kv_fp8_attention_shared_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int, c_int]),
+    "kv_fp8_attention_shared": (c_int, [c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int,
+                                        c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_int,
+                                        c_int, c_int, c_int, c_int, c_int, c_int, c_float, c_void_p, c_int64, c_void_p,
+                                        c_int64, c_void_p, c_size_t, c_void_p, c_void_p]),
     "kv_fp8_attention_mass": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_int,
                                       c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
                                       c_int, c_float, c_void_p, c_int64, c_int64, c_int, c_void_p, c_void_p]),
@@ -449,7 +454,7 @@ def _no_call(*args):
 class _Calls:
     """The FP8 calls of _fp8_binding (a status, or None for arguments that the
     functions below look at themselves); without the module all return None."""
-    write = read = attention = norm_rope = norm_rope_axes = mass = evict = staticmethod(_no_call)
+    write = read = attention = norm_rope = norm_rope_axes = mass = evict = shared = staticmethod(_no_call)
 
 
 def _calls():
@@ -463,7 +468,8 @@ def _calls():
     else:
         m.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
                  for f in ("kv_fp8_write", "kv_fp8_read", "kv_fp8_attention", "kv_qk_norm_rope",
-                           "kv_qk_norm_rope_axes", "kv_fp8_attention_mass", "kv_fp8_evict")))
+                           "kv_qk_norm_rope_axes", "kv_fp8_attention_mass", "kv_fp8_evict",
+                           "kv_fp8_attention_shared")))
     _fp8 = m
     return m
 
@@ -743,6 +749,72 @@ def qk_norm_rope_axes(q, k, positions, cos_sin, pair_axis, q_weight, k_weight, e
         _raise(code, "kv_qk_norm_rope_axes")
 
 
+def attention_shared_workspace_size(num_seqs: int, num_groups: int, num_q_tokens: int, num_q_heads: int,
+                                    num_kv_heads: int, head_size: int) -> int:
+    """Bytes of workspace for attention_fp8_shared."""
+    sizes = (num_seqs, num_groups, num_q_tokens, num_q_heads, num_kv_heads, head_size)
+    got = int(load().kv_fp8_attention_shared_workspace_size(*(_int32(x, "a size") for x in sizes)))
+    _check(got > 0, "invalid attention sizes")
+    return got
+
+
+def attention_fp8_shared(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, query_start_loc, max_query_len,
+                         max_seq_len, group_start, prefix_lens, max_group_tokens, softmax_scale, out, workspace, lse=None,
+                         dev_status: Optional[torch.Tensor] = None, stream=None):
+    """Causal attention over the FP8 cache for a batch in which groups of
+    sequences have their first positions in common, through
+    kv_fp8_attention_shared; writes ``out`` and ``lse`` in place.
+
+    group_start: int32 [groups + 1], the groups' first sequences; prefix_lens:
+    int32 [groups], the positions that a group's sequences have in the same blocks;
+    max_group_tokens bounds a group's query tokens.  lse: float32 [tokens,
+    q_heads] or None, the logarithm of the rows' denominators."""
+    code = (_fp8 or _calls()).shared(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, query_start_loc,
+                                     max_query_len, max_seq_len, group_start, prefix_lens, max_group_tokens,
+                                     softmax_scale, out, workspace, lse, dev_status, stream)
+    if code == 0:
+        return
+    if code is not None:
+        _raise(code, "kv_fp8_attention_shared")
+    nb, bs, hkv, d = _cache_dims_fp8(k_cache, v_cache, k_scale, v_scale)
+    num_seqs, width = _sequences(block_table, seq_lens, query_start_loc)
+    if q.dim() != 3:
+        _refuse("q must be [tokens, q_heads, d]")
+    tokens, hq, _ = q.shape
+    qs, os_ = _rows(q, "q", tokens, hq, d), _rows(out, "out", tokens, hq, d)
+    if prefix_lens.dtype is not torch.int32 or prefix_lens.dim() != 1 or not prefix_lens.is_contiguous():
+        _refuse("prefix_lens must be contiguous int32 [groups]")
+    groups = prefix_lens.shape[0]
+    if group_start.dtype is not torch.int32 or group_start.shape != (groups + 1,) or not group_start.is_contiguous():
+        _refuse("group_start must be contiguous int32 [groups + 1]")
+    if workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        _refuse("workspace must be contiguous uint8")
+    tensors = [v_cache, k_scale, v_scale, block_table, seq_lens, query_start_loc, q, out, group_start, prefix_lens, workspace]
+    lp, ls = None, 0
+    if lse is not None:
+        ls = _lse_stride(lse, tokens, hq)
+        lp = lse.data_ptr()
+        tensors.append(lse)
+    max_query_len, max_seq_len = _int32(max_query_len, "max_query_len"), _int32(max_seq_len, "max_seq_len")
+    max_group_tokens = _int32(max_group_tokens, "max_group_tokens")
+    dev = k_cache.get_device()
+    st = _raw_stream(dev, all(t.get_device() == dev for t in tensors), stream)
+    code = (_lib or load()).kv_fp8_attention_shared(
+        q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        block_table.data_ptr(), width, seq_lens.data_ptr(), query_start_loc.data_ptr(), num_seqs, tokens, max_query_len,
+        max_seq_len, group_start.data_ptr(), prefix_lens.data_ptr(), groups, max_group_tokens, hq, hkv, d, bs, nb,
+        softmax_scale, out.data_ptr(), os_, lp, ls, workspace.data_ptr(), workspace.numel(), _status_ptr(dev_status, dev),
+        st)
+    if code:
+        _raise(code, "kv_fp8_attention_shared")
+
+
+def _lse_stride(lse, tokens: int, hq: int) -> int:
+    if lse.dtype is not torch.float32 or lse.shape != (tokens, hq) or (hq > 1 and lse.stride(1) != 1):
+        _refuse("lse must be float32 [tokens, q_heads], contiguous along the heads")
+    return lse.stride(0) if tokens > 1 else hq
+
+
 def _mass_rows(x, name: str, seqs: int, hkv: int):
     """(sequence stride, head stride, positions) of float32 [seqs, heads, positions]."""
     if x.dtype is not torch.float32 or x.dim() != 3 or x.shape[0] != seqs or x.shape[1] != hkv:
@@ -772,15 +844,14 @@ def attention_mass_fp8(q, lse, k_cache, k_scale, block_table, seq_lens, query_st
         _refuse("q must be [tokens, q_heads, d]")
     tokens, hq, _ = q.shape
     qs = _rows(q, "q", tokens, hq, d)
-    if lse.dtype is not torch.float32 or lse.shape != (tokens, hq) or (hq > 1 and lse.stride(1) != 1):
-        _refuse("lse must be float32 [tokens, q_heads], contiguous along the heads")
+    ls = _lse_stride(lse, tokens, hq)
     ms, mh, room = _mass_rows(mass, "mass", num_seqs, hkv)
     max_query_len, max_seq_len = _int32(max_query_len, "max_query_len"), _int32(max_seq_len, "max_seq_len")
     dev = k_cache.get_device()
     st = _raw_stream(dev, k_scale.get_device() == block_table.get_device() == seq_lens.get_device()
                      == query_start_loc.get_device() == q.get_device() == lse.get_device() == mass.get_device() == dev, stream)
     code = (_lib or load()).kv_fp8_attention_mass(
-        q.data_ptr(), qs, lse.data_ptr(), lse.stride(0) if tokens > 1 else hq, k_cache.data_ptr(), k_scale.data_ptr(),
+        q.data_ptr(), qs, lse.data_ptr(), ls, k_cache.data_ptr(), k_scale.data_ptr(),
         block_table.data_ptr(), width, seq_lens.data_ptr(), query_start_loc.data_ptr(), num_seqs, tokens, max_query_len,
         max_seq_len, hq, hkv, d, bs, nb, softmax_scale, mass.data_ptr(), ms, mh, _int32(room, "positions"),
         _status_ptr(dev_status, dev), st)

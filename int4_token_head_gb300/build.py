@@ -27,7 +27,7 @@ LIB_PATH = os.path.join(PKG, "libkvint4.so")
 STAMP = os.path.join(BUILD_DIR, "stamp.txt")
 HEADER = os.path.join(ROOT, "include", "kvint4.h")
 
-SOURCES = ["api.cu", "write.cu", "write_int8.cu", "attention.cu", "rht.cu", "attention_fp8.cu",
+SOURCES = ["api.cu", "write.cu", "write_int8.cu", "attention.cu", "rht.cu", "attention_fp8.cu", "attention_shared_fp8.cu",
            "cache_fp8.cu", "evict_fp8.cu", "mass_fp8.cu", "norm_rope.cu", "api_fp8.cu", "timing.cu", "noalloc.cu", "selftest.cu"]
 BINDING_SRC = os.path.join(CSRC, "fp8_binding.cpp")
 PYTHON_TAG = sysconfig.get_config_var("EXT_SUFFIX") or ".so"  # the interpreter's own: another one does not import it

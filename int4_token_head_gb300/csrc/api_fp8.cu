@@ -34,6 +34,44 @@ int check_cache(const void* k_cache, const void* v_cache, const float* k_scale, 
   return KV_INT4_OK;
 }
 
+}  // namespace
+
+bool kvint4::shared_layout(int num_seqs, int num_groups, int num_q_tokens, int num_q_heads, int num_kv_heads,
+                           int head_size, SharedLayout* L) {
+  if (num_seqs < 0 || num_groups < 0 || num_groups > kMostGroups || num_q_tokens < 0 || num_q_tokens >= (1 << 30) ||
+      num_seqs > INT32_MAX - num_groups)
+    return false;
+  const size_t V = (size_t)num_seqs + num_groups;
+  // groups' query tokens once more; the base's own room for decode columns goes by
+  // one sequence's, a group's are more: up to 32 per virtual sequence and head here
+  if (!workspace_layout_fp8((int)V, 2 * num_q_tokens, num_q_heads, num_kv_heads, head_size, false, &L->base)) return false;
+  size_t off = L->base.total;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = (off + bytes + 255) / 256 * 256;
+    return at;
+  };
+  const int64_t columns = (int64_t)V * num_kv_heads * kDecodeColsFp8;
+  if (num_groups > 0 && columns > L->base.direct_rows && columns <= kSharedRows) {
+    L->base.direct_rows = columns;
+    L->base.direct_o = take(columns * head_size * 4);
+    L->base.direct_ml = take(columns * 2 * 4);
+  }
+  L->vrec = take(V * 32);
+  L->dseq2 = take(V * 16);
+  L->vinfo = take(V * 8);
+  L->tloc = take(L->base.max_pairs * 8);
+  const int64_t most = kSharedRows / num_q_heads;
+  L->row_tokens = num_groups == 0 ? 0 : (int)(num_q_tokens < most ? num_q_tokens : most);
+  const size_t rows = 2 * (size_t)L->row_tokens * num_q_heads;
+  L->row_o = take(rows * head_size * 4);
+  L->row_ml = take(rows * 2 * 4);
+  L->total = off;
+  return true;
+}
+
+namespace {
+
 // whether rows of len floats at (sequence, head) strides do not overlap
 bool rows_apart(int64_t seqs, int64_t seq_stride, int64_t heads, int64_t head_stride, int64_t len) {
   if (seqs <= 1) return heads <= 1 || head_stride >= len;
@@ -180,6 +218,57 @@ int kv_qk_norm_rope_axes(const void* q, int64_t q_token_stride, const void* k, i
     }
   }
   return do_norm_rope(a, stream);
+}
+
+size_t kv_fp8_attention_shared_workspace_size(int num_seqs, int num_groups, int num_q_tokens, int num_q_heads,
+                                              int num_kv_heads, int head_size) {
+  SharedLayout L;
+  if (!head_size_ok(head_size) || num_q_heads <= 0 || num_kv_heads <= 0 ||
+      !shared_layout(num_seqs, num_groups, num_q_tokens, num_q_heads, num_kv_heads, head_size, &L))
+    return 0;
+  return L.total;
+}
+
+int kv_fp8_attention_shared(const void* q, int64_t q_token_stride, const uint8_t* k_cache, const uint8_t* v_cache,
+                            const float* k_scale_cache, const float* v_scale_cache, const int32_t* block_table,
+                            int max_blocks_per_seq, const int32_t* seq_lens, const int32_t* query_start_loc, int num_seqs,
+                            int num_q_tokens, int max_query_len, int max_seq_len, const int32_t* group_start,
+                            const int32_t* prefix_lens, int num_groups, int max_group_tokens, int num_q_heads,
+                            int num_kv_heads, int head_size, int block_size, int num_blocks, float softmax_scale, void* out,
+                            int64_t out_token_stride, float* lse, int64_t lse_token_stride, void* workspace,
+                            size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  if (max_seq_len < 0 || num_groups < 0 || num_groups > kMostGroups || max_group_tokens < 0) return KV_INT4_ERR_SIZE;
+  if (num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads || num_q_heads / num_kv_heads > kPrefillRows)
+    return KV_INT4_ERR_HEADS;
+  int e = check_sizes(num_seqs, num_q_tokens, max_query_len, max_blocks_per_seq, num_blocks, block_size, num_kv_heads,
+                      head_size);
+  if (e != KV_INT4_OK) return e;
+  SharedLayout L;
+  if ((int64_t)num_q_tokens * num_q_heads >= (1ll << 31) ||
+      !shared_layout(num_seqs, num_groups, num_q_tokens, num_q_heads, num_kv_heads, head_size, &L))
+    return KV_INT4_ERR_SIZE;
+  if (num_seqs == 0 || num_q_tokens == 0) return KV_INT4_OK;
+  // query rows that do not overlap, blocks that a tensor map holds
+  const int64_t row = (int64_t)num_q_heads * head_size;
+  if (num_blocks < 1 || (int64_t)num_blocks * 16 >= (1ll << 31) ||
+      (num_q_tokens > 1 && (q_token_stride < row || out_token_stride < row || (lse && lse_token_stride < num_q_heads))))
+    return KV_INT4_ERR_SIZE;
+  if (!workspace || workspace_bytes < L.total) return KV_INT4_ERR_WORKSPACE;
+  if (!q || !out || (num_groups > 0 && (!group_start || !prefix_lens))) return KV_INT4_ERR_NULL;
+  e = check_cache(k_cache, v_cache, k_scale_cache, v_scale_cache, block_table, seq_lens, query_start_loc, dev_status);
+  if (e != KV_INT4_OK) return e;
+  if (!aligned16(q) || !aligned16(out) || !stride_ok(q_token_stride) || !stride_ok(out_token_stride) ||
+      !aligned(workspace, 256) || !aligned(group_start, 4) || !aligned(prefix_lens, 4) || !aligned(lse, 4))
+    return KV_INT4_ERR_ALIGN;
+  if (current_device() < 0) return KV_INT4_ERR_CUDA;
+  const AttnArgs a{q, q_token_stride, k_cache, v_cache, k_scale_cache, v_scale_cache, block_table, max_blocks_per_seq,
+                   seq_lens, query_start_loc, num_seqs, num_q_tokens, max_query_len, max_seq_len, num_q_heads,
+                   num_kv_heads, head_size, block_size, num_blocks, softmax_scale, 1, 0, nullptr, out,
+                   out_token_stride, workspace, workspace_bytes, dev_status, false,
+                   block_scale_geo(num_kv_heads, head_size)};
+  return launch_attention_shared_fp8(SharedAttnArgs{a, group_start, prefix_lens, num_groups, max_group_tokens, lse,
+                                                    lse_token_stride},
+                                     static_cast<cudaStream_t>(stream));
 }
 
 int kv_fp8_attention_mass(const void* q, int64_t q_token_stride, const float* lse, int64_t lse_token_stride,

@@ -1,0 +1,410 @@
+// kv_fp8_attention_shared: causal attention over the FP8 cache for batches whose
+// groups of sequences share their first positions, and the rows' log-sum-exp.
+//
+// All queries of a group see all of its shared keys, so the shared part is
+// attention without a mask of one sequence with the group's queries: the cache's
+// bytes are read once per group, and where the group's rows fill a tensor-core tile
+// its keys are converted once for all of them.  What a sequence has behind the
+// shared part is attended as ever.  The two are one batch of virtual sequences
+// (schedule.cuh) for the kernels of kv_fp8_attention, so that long prefixes and
+// short ends are balanced in one launch each, and a row's results are merged by
+//   M = max m_i,  l = sum l_i 2^(m_i - M),  out = sum o_i 2^(m_i - M) / l,
+//   lse = (M + log2 l) log 2
+// over the pieces of both.
+//
+// Launches: the schedule, prefill (if any rows may need it), decode, merge; short
+// batches that only decode: one launch that shares nothing.
+
+#include <cuda.h>
+#include <float.h>
+
+#include <type_traits>
+
+#include "common.cuh"
+#include "fp8.cuh"
+#include "internal.h"
+#include "schedule.cuh"
+
+namespace kvint4 {
+namespace {
+
+#include "attention_fp8.cuh"
+
+constexpr int kMergeWarps = 16;  // per CTA; two such CTAs per SM
+
+struct SharedMergeParams {
+  Common c;
+  PlanView pv;
+  int num_ctas;  // of the decode launch
+  int cols;      // rows per CTA (warps)
+  int lanes;     // warps per row
+  int parts;     // CTAs per (sequence, kv head), cols rows each and in turn
+  int slot;      // columns of a result slot
+};
+
+// The decode pieces of virtual sequence record i of dseq and a kv head: the
+// direct slot (the piece that starts the segment), then every CTA whose range is
+// not empty and starts strictly inside it; candidates are those CTAs or the
+// positions, whichever are fewer (as merge_fp8_kernel finds them)
+struct DecodePieces {
+  long long seg, sbeg, Tu, w_first;
+  int cand, W, lane_g, hl;
+  bool by_cta;
+  __device__ void find(const Common& c, const PlanView& pv, int num_ctas, int i, int h) {
+    const int n_dseq = pv.plan[0];
+    const int npos = ((pv.dseq[i].y + 15) / 16 + c.np - 1) / c.np;
+    const int grp = h / c.hg, gpl = c.ng / c.nl, gs = grp / c.nl;
+    hl = h - grp * c.hg;
+    lane_g = grp % c.nl;
+    seg = (long long)i * c.hkv + h;
+    Tu = pv.dprefix[n_dseq] * gpl;
+    sbeg = pv.dprefix[i] * gpl + (long long)gs * npos;
+    W = num_ctas / c.nl;
+    w_first = div_nn((sbeg + 1) * W + Tu - 1, Tu);
+    const long long w_end = div_nn((sbeg + npos) * W + Tu - 1, Tu);
+    by_cta = w_end - w_first <= npos - 1;
+    cand = 1 + (int)(by_cta ? w_end - w_first : (long long)npos - 1);
+  }
+  // candidate k's result slot, false if there is none: direct ones first
+  __device__ __forceinline__ bool slot(const Common& c, int k, long long* at) const {
+    if (k == 0) {
+      *at = seg;
+      return true;
+    }
+    long long w;
+    bool ok;
+    if (by_cta) {
+      w = w_first + k - 1;
+      ok = div_nn(Tu * (w + 1), W) > div_nn(Tu * w, W);
+    } else {
+      const long long p = sbeg + k;
+      w = div_nn((p + 1) * W + Tu - 1, Tu) - 1;
+      ok = div_nn(Tu * w, W) == p;
+    }
+    *at = (w * c.nl + lane_g) * c.hg + hl;
+    return ok;
+  }
+};
+
+// a virtual sequence's results, for one kv head
+struct Results {
+  int kind, index;  // of vinfo
+  int ql, first;    // query tokens, first row-buffer token
+  DecodePieces dec;
+  __device__ void find(const Common& c, const PlanView& pv, int num_ctas, int v, int h) {
+    const int2 x = pv.vinfo[v];
+    kind = x.x == 2 && pv.plan[1] == 0 ? 0 : x.x;  // more tiles than the workspace holds: none was worked on
+    index = x.y;
+    ql = pv.vrec[2 * v].y;
+    first = pv.vrec[2 * v + 1].z;
+    if (kind == 1) dec.find(c, pv, num_ctas, index, h);
+  }
+  // its pieces for token j of the virtual sequence; 0 where a whole tile went out by itself
+  __device__ __forceinline__ int pieces(const Common& c, const PlanView& pv, int j, int2* tile) const {
+    if (kind == 1) return dec.cand;
+    if (kind != 2) return 0;
+    *tile = pv.tloc[index + j / c.tile_tokens];
+    return tile->y > 1 || first >= 0 ? tile->y : 0;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) merge_shared_kernel(SharedMergeParams prm) {
+  const Common& c = prm.c;
+  const PlanView& pv = prm.pv;
+  extern __shared__ __align__(16) float spart[];  // [cols][lanes][D + 2]
+  pdl_trigger();
+  pdl_wait();
+  constexpr int PER = D / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int pl = warp / prm.cols, lcol = warp - pl * prm.cols;
+  const int seg = blockIdx.x / prm.parts, part = blockIdx.x - seg * prm.parts;
+  const int s = seg / c.hkv, h = seg - s * c.hkv, v = c.sh.num_groups + s;
+  const int4 rec = pv.vrec[2 * v];
+  const int g = pv.vrec[2 * v + 1].w;
+  const int q0 = rec.x, ql = rec.y;
+  if (ql == 0) return;
+  Results own, pre;
+  own.find(c, pv, prm.num_ctas, v, h);
+  pre.kind = 0;
+  int off = 0;  // the sequence's first token in its group
+  if (g >= 0) {
+    pre.find(c, pv, prm.num_ctas, g, h);
+    off = q0 - pv.vrec[2 * g].x;
+  }
+  const int nsub = c.np == 2 ? 2 : 1;  // paired blocks: columns col and col + dcols hold the same query
+#pragma unroll 1
+  for (int c0 = part * prm.cols; c0 < ql * c.group; c0 += prm.parts * prm.cols) {
+    const int col = c0 + lcol;
+    const int j = col / c.group, jj = col - j * c.group;
+    float acc[PER], M = -INFINITY, Ls = 0.f;
+#pragma unroll
+    for (int k = 0; k < PER; k++) acc[k] = 0.f;
+    auto merge = [&](float m, float l, const float (&o)[PER]) {
+      const float mn = fmaxf(M, m);
+      const float mu = mn == -INFINITY ? 0.f : mn;
+      const Exp2Pair ea(M - mu), eb(m - mu);
+      const float a = ea.both(), b = eb.both();
+#pragma unroll
+      for (int k = 0; k < PER; k++) acc[k] = acc[k] * a + o[k] * b;
+      Ls = ea.of(Ls) + eb.of(l);
+      M = mn;
+    };
+    int2 own_tile = make_int2(0, 0), pre_tile = make_int2(0, 0);
+    int n_own = 0, n_pre = 0;
+    if (col < ql * c.group) {
+      n_own = own.pieces(c, pv, j, &own_tile);
+      if (g >= 0) n_pre = pre.pieces(c, pv, j + off, &pre_tile);
+    }
+#pragma unroll 2
+    for (int k = pl; k < n_own + n_pre; k += prm.lanes) {
+      const bool mine = k >= n_pre;  // the prefix's pieces first
+      const Results& x = mine ? own : pre;
+      const int kk = mine ? k - n_pre : k, jx = mine ? j : j + off;
+      const float *o, *ml;
+      bool ok = true;
+      int subs = 1, sub_step = 0;
+      if (x.kind == 1) {
+        long long at;
+        ok = x.dec.slot(c, kk, &at);
+        at = at * prm.slot + jx * c.group + jj;
+        o = (kk == 0 ? pv.direct_o : pv.warp_o) + at * D;
+        ml = (kk == 0 ? pv.direct_ml : pv.warp_ml) + at * 2;
+        subs = nsub;
+        sub_step = c.dcols;
+      } else {
+        const int2 tile = mine ? own_tile : pre_tile;
+        if (tile.y > 1) {
+          const int t = jx / c.tile_tokens, tok = t * c.tile_tokens;
+          const int R = min(c.tile_tokens, x.ql - tok) * c.group;
+          const long long at = tile.x + ((long long)h * tile.y + kk) * R + (jx - tok) * c.group + jj;
+          o = pv.piece_o + at * D;
+          ml = pv.piece_ml + at * 2;
+        } else {
+          const long long at = (long long)(x.first + jx) * c.hq + h * c.group + jj;
+          o = pv.row_o + at * D;
+          ml = pv.row_ml + at * 2;
+        }
+      }
+      float mw[2], lw[2], ov[2][PER];
+#pragma unroll
+      for (int sub = 0; sub < 2; sub++) {
+        const bool use = ok && sub < subs;
+        const float2 w = use ? *reinterpret_cast<const float2*>(ml + 2 * sub * sub_step) : make_float2(-INFINITY, 0.f);
+        mw[sub] = w.x;
+        lw[sub] = w.y;
+#pragma unroll
+        for (int e = 0; e < PER; e++) ov[sub][e] = use ? o[sub * sub_step * D + lane + 32 * e] : 0.f;
+      }
+      merge(mw[0], lw[0], ov[0]);
+      if (subs > 1) merge(mw[1], lw[1], ov[1]);
+    }
+    if (prm.lanes > 1) {
+      float* mine = spart + (lcol * prm.lanes + pl) * (D + 2);
+      if (pl > 0) {
+#pragma unroll
+        for (int k = 0; k < PER; k++) mine[lane + 32 * k] = acc[k];
+        if (lane == 0) {
+          mine[D] = M;
+          mine[D + 1] = Ls;
+        }
+      }
+      __syncthreads();
+      if (pl == 0) {
+#pragma unroll 1
+        for (int p = 1; p < prm.lanes; p++) {
+          const float* o = mine + p * (D + 2);
+          float x[PER];
+#pragma unroll
+          for (int k = 0; k < PER; k++) x[k] = o[lane + 32 * k];
+          merge(o[D], o[D + 1], x);
+        }
+      }
+      __syncthreads();  // read before the next rows' are written
+    }
+    if (pl > 0 || n_own + n_pre == 0) continue;
+    const float inv = Ls == 0.f ? 0.f : 1.f / Ls;  // no visible key: zeros
+    uint16_t* dst = c.out + (long long)(q0 + j) * c.out_stride + (long long)(h * c.group + jj) * D;
+#pragma unroll
+    for (int k = 0; k < PER; k++)
+      dst[lane + 32 * k] = (uint16_t)(pack_bf16x2_rn(acc[k] * inv, 0.f) & 0xffffu);
+    if (c.sh.lse && lane == 0) c.sh.lse[(q0 + j) * c.sh.lse_stride + h * c.group + jj] = log_sum_exp(M, Ls);
+  }
+}
+
+template <int D>
+int launch_t(const SharedAttnArgs& s, cudaStream_t stream) {
+  const AttnArgs& a = s.attn;
+  SharedLayout L;
+  if (!shared_layout(a.num_seqs, s.num_groups, a.num_q_tokens, a.num_q_heads, a.num_kv_heads, D, &L)) return KV_INT4_ERR_SIZE;
+  PlanView pv = plan_view_fp8(a.workspace, L.base);
+  uint8_t* const ws = static_cast<uint8_t*>(a.workspace);
+  pv.vrec = reinterpret_cast<int4*>(ws + L.vrec);
+  pv.dseq2 = reinterpret_cast<int4*>(ws + L.dseq2);
+  pv.vinfo = reinterpret_cast<int2*>(ws + L.vinfo);
+  pv.tloc = reinterpret_cast<int2*>(ws + L.tloc);
+  pv.row_o = reinterpret_cast<float*>(ws + L.row_o);
+  pv.row_ml = reinterpret_cast<float*>(ws + L.row_ml);
+  const int dev = current_device();
+  const int sms = sm_count(dev);
+  Common c{};
+  c.q = static_cast<const uint16_t*>(a.q);
+  c.q_stride = a.q_stride;
+  c.k_cache = a.k_cache;
+  c.v_cache = a.v_cache;
+  c.k_scale = a.k_scale;
+  c.v_scale = a.v_scale;
+  c.geo = a.geo;
+  c.block_table = a.block_table;
+  c.max_blocks = a.max_blocks_per_seq;
+  c.seq_lens = a.seq_lens;
+  c.qsl = a.query_start_loc;
+  c.num_seqs = a.num_seqs;
+  c.num_q_tokens = a.num_q_tokens;
+  c.max_qlen = a.max_query_len;
+  c.hq = a.num_q_heads;
+  c.hkv = a.num_kv_heads;
+  c.group = a.num_q_heads / a.num_kv_heads;
+  c.gdiv = FastDiv((uint32_t)c.group);
+  c.num_blocks = a.num_blocks;
+  c.causal = 1;
+  c.qscale = a.softmax_scale * kLog2e;
+  c.out = static_cast<uint16_t*>(a.out);
+  c.out_stride = a.out_stride;
+  c.status = a.dev_status;
+  c.max_items = L.base.max_pairs * a.num_kv_heads;
+  c.sh = SharedArgs{s.group_start, s.prefix_lens, s.num_groups, s.max_group_tokens, L.row_tokens, Fp8Ws<D>::ROWS, 64,
+                    s.lse, s.lse_stride};
+  auto with_np = [](int np, int cg, auto&& f) {
+    using std::integral_constant;
+    if (np == 2) return f(integral_constant<int, 2>{}, integral_constant<int, 1>{});
+    if (np == 4) return f(integral_constant<int, kFp8Quad<D> ? 4 : 2>{}, integral_constant<int, 1>{});
+    if (cg == 2) return f(integral_constant<int, 1>{}, integral_constant<int, 2>{});
+    if (cg == 4) return f(integral_constant<int, 1>{}, integral_constant<int, 4>{});
+    return f(integral_constant<int, 1>{}, integral_constant<int, 1>{});
+  };
+  // decode, as in kv_fp8_attention; a group's queries count as one sequence's
+  c.hg = c.ng = c.nl = c.np = 1;
+  const long long most_own = (long long)(a.max_query_len > 0 ? a.max_query_len : 1) * c.group;
+  const long long most_tokens = s.num_groups > 0 && s.max_group_tokens > a.max_query_len ? s.max_group_tokens : a.max_query_len;
+  const long long mq = (most_tokens > 0 ? most_tokens : 1) * c.group;
+  const long long cols = mq <= kDecodeColsFp8 ? mq : most_own <= kDecodeColsFp8 ? most_own : c.group;
+  int cg = cols > 2 * kDecodeCols ? 4 : cols > kDecodeCols ? 2 : 1;
+  const long long virt = (long long)a.num_seqs + s.num_groups;
+  while (cg > 1 && virt * a.num_kv_heads * kDecodeCols * cg > L.base.direct_rows) cg /= 2;
+  const bool any_decode = c.group <= kDecodeCols * cg;
+  int dec_grid = 0, dec_occ = 0;
+  if (any_decode) {
+    static PerContext<int> occ_cache[5][5];
+    auto take = [&](auto np_tag, auto cg_tag) {
+      constexpr int NP = decltype(np_tag)::value, CG = decltype(cg_tag)::value;
+      using G = Fp8Dec<D, NP>;
+      c.np = NP;
+      for (int h = 4 / CG; h >= 1; h--)
+        if (a.num_kv_heads % h == 0 && (h == 1 || 2 * (G::smem_bytes(h) + 1024) <= 228 * 1024)) {
+          c.hg = h;
+          break;
+        }
+      return occ_cache[NP == 1 ? CG / 2 : NP / 2 + 2][c.hg].get(dev, [&](int* v) {
+        int unused;
+        return configure(decode_fp8_kernel<D, NP, CG, true, true>, (228 * 1024) / 2 - 1024, 128, &unused) &&
+               configure(decode_fp8_kernel<D, NP, CG, false, true>, (228 * 1024) / 2 - 1024, 128, &unused) &&
+               cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, decode_fp8_kernel<D, NP, CG, false, true>, c.hg * CG * 32,
+                                                             G::smem_bytes(c.hg)) == cudaSuccess && *v >= 1;
+      }, &dec_occ);
+    };
+    if (!with_np(cols > 4 ? 1 : cols > 2 || !kFp8Quad<D> ? 2 : 4, cg, take)) return KV_INT4_ERR_CUDA;
+    c.ng = a.num_kv_heads / c.hg;
+    long long grid = (long long)sms * dec_occ;
+    if (grid * c.hg * cg > kMaxDecodeWarps) grid = kMaxDecodeWarps / (c.hg * cg);
+    for (int l = (int)(grid < c.ng ? grid : c.ng); l >= 1; l--)
+      if (c.ng % l == 0) {
+        c.nl = l;
+        break;
+      }
+    dec_grid = (int)(grid / c.nl * c.nl);
+  }
+  c.dcols = kDecodeCols * cg / c.np;
+
+  if (any_decode && most_own <= c.dcols) {
+    // one launch of clusters that share nothing where kv_fp8_attention would make it
+    const long long tasks = (long long)a.num_seqs * c.ng, room = (long long)sms * dec_occ;
+    const long long table = (long long)a.max_blocks_per_seq * 16;
+    const long long most = ((a.max_seq_len < table ? a.max_seq_len : table) + 16 * c.np - 1) / (16 * c.np);
+    int cl = 1;
+    while (cl < 8 && 2 * tasks * cl <= room && most > 2 * cl) cl *= 2;
+    if (tasks * cl <= room && most <= 16 * cl) {
+      timing_begin(kTimedDecode, stream);
+      const int e = with_np(c.np, cg, [&](auto np_tag, auto cg_tag) {
+        constexpr int NP = decltype(np_tag)::value, CG = decltype(cg_tag)::value;
+        return launch_pdl(decode_fp8_kernel<D, NP, CG, true, true>, dim3((unsigned)(tasks * cl)), c.hg * CG * 32,
+                          Fp8Dec<D, NP>::smem_bytes(c.hg), stream, cl, Fp8DecParams{c, pv, 0, cl, false});
+      });
+      timing_end(kTimedDecode, stream);
+      return e;
+    }
+  }
+
+  using G = Fp8Ws<D>;
+  const bool may_prefill = c.group > c.dcols || most_tokens * c.group > c.dcols;
+  c.tile_tokens = G::ROWS / c.group;
+  c.step_blocks = G::NB;
+  c.split_steps = 4;
+  c.split_ctas = sms;
+  Fp8Maps maps;
+  if (may_prefill) {
+    if (!make_maps<D>(a, c.tile_tokens, &maps)) return KV_INT4_ERR_CUDA;
+    static PerContext<int> occ_c;
+    int occ = 0;
+    if (!occ_c.get(dev, [](int* o) { return configure_tmem(prefill_ws_fp8_kernel<D, true>, G::SMEM, G::THREADS, 512, o); },
+                   &occ))
+      return KV_INT4_ERR_CUDA;
+  }
+  const bool may_split = may_prefill && a.max_seq_len > 2ll * 16 * c.step_blocks * c.split_steps;
+  if (int e = launch_plan<true>(c, pv, may_prefill, may_split, stream)) return e;
+  if (may_prefill) {
+    const long long items = (L.base.max_pairs + L.base.max_pieces) * a.num_kv_heads;
+    const long long grid = sms < items ? sms : items;
+    timing_begin(kTimedPrefill, stream);
+    const int e = launch_pdl(prefill_ws_fp8_kernel<D, true>, dim3((unsigned)grid), G::THREADS, G::SMEM, stream, 1, c, pv, maps);
+    timing_end(kTimedPrefill, stream);
+    if (e) return e;
+  }
+  if (any_decode) {
+    timing_begin(kTimedDecode, stream);
+    const int e = with_np(c.np, cg, [&](auto np_tag, auto cg_tag) {
+      constexpr int NP = decltype(np_tag)::value, CG = decltype(cg_tag)::value;
+      return launch_pdl(decode_fp8_kernel<D, NP, CG, false, true>, dim3(dec_grid), c.hg * CG * 32,
+                        Fp8Dec<D, NP>::smem_bytes(c.hg), stream, 1, Fp8DecParams{c, pv, dec_grid, 1, may_prefill});
+    });
+    timing_end(kTimedDecode, stream);
+    if (e) return e;
+  }
+  // merge: CTAs per (sequence, kv head), a warp per row and piece lane, lanes as
+  // far as all CTAs start at once
+  const long long segs = (long long)a.num_seqs * a.num_kv_heads, warps = 2ll * kMergeWarps * sms;
+  int mcols = (int)(most_own < 8 ? most_own : 8), parts = 1, lanes = 1;
+  while ((long long)mcols * parts < most_own && segs * parts * mcols < warps) parts *= 2;
+  while (mcols * lanes * 2 <= kMergeWarps && 2ll * lanes * mcols * parts * segs <= warps) lanes *= 2;
+  if (segs * parts > 0x7fffffff) return KV_INT4_ERR_SIZE;
+  timing_begin(kTimedReduce, stream);
+  const int e = launch_pdl(merge_shared_kernel<D>, dim3((unsigned)(segs * parts)), mcols * lanes * 32, merge_smem<D>(mcols, lanes),
+                           stream, 1, SharedMergeParams{c, pv, dec_grid, mcols, lanes, parts, kDecodeCols * cg});
+  timing_end(kTimedReduce, stream);
+  return e;
+}
+
+}  // namespace
+
+int launch_attention_shared_fp8(const SharedAttnArgs& a, cudaStream_t stream) {
+  switch (a.attn.head_size) {
+    case 64: return launch_t<64>(a, stream);
+    case 96: return launch_t<96>(a, stream);
+    case 128: return launch_t<128>(a, stream);
+    case 192: return launch_t<192>(a, stream);
+    case 256: return launch_t<256>(a, stream);
+    default: return KV_INT4_ERR_HEAD_SIZE;
+  }
+}
+
+}  // namespace kvint4

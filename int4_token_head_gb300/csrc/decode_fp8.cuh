@@ -71,6 +71,7 @@ struct Fp8Walk {
   int fb;    // first block read (the sliding window's)
   int seq;   // sequence id
   int len;   // keys
+  long long tab;  // first entry of its block table
 };
 
 struct Fp8DecParams {
@@ -81,16 +82,22 @@ struct Fp8DecParams {
   bool beside;  // the kernel before is a prefill of the same call
 };
 
-template <int NP>
+template <int NP, bool SH>
 __device__ __forceinline__ void fp8_walk_load(Fp8Walk& w, const Common& c, const PlanView& pv) {
   const int4 di = pv.dseq[w.i];  // (sequence, seq_len, first query token, q_len)
   w.seq = di.x;
   w.len = di.y;
+  if constexpr (SH) {
+    const int2 at = *reinterpret_cast<const int2*>(pv.dseq2 + w.i);
+    w.tab = (long long)(uint32_t)at.x | (long long)at.y << 32;
+  } else {
+    w.tab = (long long)di.x * c.max_blocks;
+  }
   w.fb = first_block(c, di.y, di.w);
   w.npos = ((di.y + 15) / 16 - w.fb + NP - 1) / NP;
 }
 // the next unit of the lane (there is one: the caller counts)
-template <int NP>
+template <int NP, bool SH>
 __device__ __forceinline__ void fp8_walk_next(Fp8Walk& w, const Common& c, const PlanView& pv) {
   if (++w.kp == w.npos) {
     w.kp = 0;
@@ -98,7 +105,7 @@ __device__ __forceinline__ void fp8_walk_next(Fp8Walk& w, const Common& c, const
       w.grp = w.lane;
       do {
         ++w.i;
-        fp8_walk_load<NP>(w, c, pv);
+        fp8_walk_load<NP, SH>(w, c, pv);
       } while (w.npos == 0);  // sequences without keys have no units
     }
   }
@@ -134,7 +141,8 @@ __device__ __forceinline__ float ld_cluster(const float* p, int rank) {
 // cluster of CTAs serves one (sequence, head group), its CTAs equal shares of
 // the positions, and merges them through distributed shared memory: one launch
 // for batches whose shares are short (latency counts there, not balance).
-template <int D, int NP, int CG, bool DIRECT>
+// SH: over virtual sequences (shared prefixes), and the rows' log-sum-exp.
+template <int D, int NP, int CG, bool DIRECT, bool SH = false>
 __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
   using G = Fp8Dec<D, NP>;
   static_assert(CG == 1 || (NP == 1 && kFp8PartsFit<D>), "column groups");
@@ -195,6 +203,7 @@ again:
     if (ql == 0) return;
     dseq0 = make_int4(cw.seq, cw.len, q0, ql);
     cw.i = cw.lane = 0;
+    cw.tab = (long long)cw.seq * c.max_blocks;
     cw.fb = first_block(c, cw.len, ql);
     const int npos = ((cw.len + 15) / 16 - cw.fb + NP - 1) / NP;
     const int first = (int)((long long)npos * rank / prm.cluster), end = (int)((long long)npos * (rank + 1) / prm.cluster);
@@ -233,7 +242,7 @@ again:
     }
     cw.i = lo;
     cw.lane = my_lane;
-    fp8_walk_load<NP>(cw, c, pv);
+    fp8_walk_load<NP, SH>(cw, c, pv);
     {
       const long long off = P0 - pv.dprefix[cw.i] * gpl;
       const int gs = (int)(off / cw.npos);
@@ -264,7 +273,7 @@ again:
   // block j of a position
   auto block_at = [&](const Fp8Walk& w, int j) {
     const int kb = w.fb + w.kp * NP + j;
-    return kb * 16 < w.len ? c.block_table[(long long)w.seq * c.max_blocks + kb] : -1;
+    return kb * 16 < w.len ? c.block_table[w.tab + kb] : -1;
   };
   auto issue = [&](int blk, int kb, int len, int grp, int slot) {
     const bool ok = blk >= 0 && blk < c.num_blocks;
@@ -297,7 +306,7 @@ again:
   };
   auto next = [&](Fp8Walk& w) {
     if constexpr (DIRECT) ++w.kp;
-    else fp8_walk_next<NP>(w, c, pv);
+    else fp8_walk_next<NP, SH>(w, c, pv);
   };
   // producer: one block per call into the next ring slot, the next block id
   // loaded one call ahead; one commit group per call (empty past the range)
@@ -331,7 +340,7 @@ again:
     const int head = cw.grp * HG + hl;
     const int4 di = DIRECT ? dseq0 : pv.dseq[cw.i];
     const int q0 = di.z, ql = di.w, L = di.y;
-    const int ctx = L - ql;
+    const int ctx = SH && !DIRECT ? pv.dseq2[cw.i].z : L - ql;
     // B fragments of this lane's column g, which holds query column cbase + g % COLS
     const int n = cbase + (g & (G::COLS - 1));
     const bool colok = n < ql * c.group;
@@ -648,6 +657,8 @@ again:
 #pragma unroll
       for (int k = 0; k < PER; k++)
         dst[lane + 32 * k] = (uint16_t)(pack_bf16x2_rn(acc[k] * inv, 0.f) & 0xffffu);
+      if (SH && c.sh.lse && lane == 0)
+        c.sh.lse[(dseq0.z + j) * c.sh.lse_stride + (cw.grp * HG + h) * c.group + jj] = log_sum_exp(M, Ls);
     }
     cluster_sync();  // no CTA leaves while its shares are read
   }

@@ -78,6 +78,11 @@ struct Exp2Pair {
   __device__ __forceinline__ float of(float x) const { return x * a * b; }
 };
 
+// the natural logarithm of l 2^M, a row's denominator; -infinity for a row without keys
+__device__ __forceinline__ float log_sum_exp(float M, float l) {
+  return l == 0.f ? -INFINITY : (M + log2f(l)) * 0.693147180559945309f;
+}
+
 // 2^e as fp32, e in [-126, 127]
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
 // the exponent field of a positive normal fp32, unbiased

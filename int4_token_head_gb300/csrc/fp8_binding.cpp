@@ -25,6 +25,7 @@ decltype(&kv_qk_norm_rope) g_norm_rope = nullptr;
 decltype(&kv_qk_norm_rope_axes) g_norm_rope_axes = nullptr;
 decltype(&kv_fp8_attention_mass) g_mass = nullptr;
 decltype(&kv_fp8_evict) g_evict = nullptr;
+decltype(&kv_fp8_attention_shared) g_shared = nullptr;
 
 struct NotPlain {};
 
@@ -294,6 +295,51 @@ PyObject* norm_rope_axes(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// token stride of fp32 [tokens, q heads]
+int64_t lse_stride(const at::Tensor& x, int64_t tokens, int64_t heads) {
+  need(x.scalar_type() == at::kFloat && x.dim() == 2 && x.size(0) == tokens && x.size(1) == heads &&
+       (heads <= 1 || x.stride(1) == 1));
+  return tokens > 1 ? x.stride(0) : heads;
+}
+
+// (q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, query_start_loc, max_query_len, max_seq_len, group_start,
+//  prefix_lens, max_group_tokens, softmax_scale, out, workspace, lse, dev_status, stream)
+PyObject* fp8_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call([&] {
+    need(n == 19 && g_shared);
+    Device dev;
+    const Caches c(dev, a + 1);
+    const Sequences s(dev, a + 5);
+    const at::Tensor &q = tensor(a[0]), &out = tensor(a[14]), &ws = tensor(a[15]);
+    need(q.dim() == 3 && q.size(0) <= INT_MAX && q.size(1) <= INT_MAX);
+    const int tokens = (int)q.size(0), hq = (int)q.size(1);
+    const int64_t qs = rows(q, tokens, hq, c.d), os = rows(out, tokens, hq, c.d);
+    const at::Tensor &gs = tensor(a[10]), &pl = tensor(a[11]);
+    need(pl.scalar_type() == at::kInt && pl.dim() == 1 && pl.is_contiguous() && pl.size(0) < INT_MAX);
+    need(gs.scalar_type() == at::kInt && gs.dim() == 1 && gs.is_contiguous() && gs.size(0) == pl.size(0) + 1);
+    need(ws.scalar_type() == at::kByte && ws.is_contiguous());
+    const int groups = (int)pl.size(0), max_q = integer(a[8]), max_len = integer(a[9]), max_group = integer(a[12]);
+    const float scale = real(a[13]);
+    float* lp = nullptr;
+    int64_t ls = 0;
+    if (a[16] != Py_None) {
+      const at::Tensor& lse = tensor(a[16]);
+      ls = lse_stride(lse, tokens, hq);
+      lp = static_cast<float*>(dev.of(lse));
+    }
+    void *qp = dev.of(q), *op = dev.of(out), *wp = dev.of(ws);
+    int32_t *gp = static_cast<int32_t*>(dev.of(gs)), *pp = static_cast<int32_t*>(dev.of(pl));
+    const size_t bytes = (size_t)ws.numel();
+    int32_t* st = dev.status(a[17]);
+    void* stream = dev.stream(a[18]);
+    return [=] {
+      return g_shared(qp, qs, c.k, c.v, c.ks, c.vs, s.table, s.width, s.lens, s.start, s.num, tokens, max_q, max_len, gp,
+                      pp, groups, max_group, hq, (int)c.hkv, (int)c.d, (int)c.bs, (int)c.nb, scale, op, os, lp, ls, wp,
+                      bytes, st, stream);
+    };
+  });
+}
+
 // masses [sequences, kv heads, positions]
 struct Mass {
   float* of;
@@ -320,9 +366,7 @@ PyObject* fp8_mass(PyObject*, PyObject* const* a, Py_ssize_t n) {
     need(q.dim() == 3 && q.size(0) <= INT_MAX && q.size(1) <= INT_MAX);
     const int tokens = (int)q.size(0), hq = (int)q.size(1);
     const int64_t qs = rows(q, tokens, hq, c.d);
-    need(lse.scalar_type() == at::kFloat && lse.dim() == 2 && lse.size(0) == tokens && lse.size(1) == hq &&
-         (hq <= 1 || lse.stride(1) == 1));
-    const int64_t ls = tokens > 1 ? lse.stride(0) : hq;
+    const int64_t ls = lse_stride(lse, tokens, hq);
     const Mass m(dev, tensor(a[10]), s.num, c.hkv);
     const int max_q = integer(a[7]), max_len = integer(a[8]);
     const float scale = real(a[9]);
@@ -370,9 +414,9 @@ PyObject* fp8_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// bind(write, read, attention, norm_rope, norm_rope_axes, mass, evict): the library's functions
+// bind(write, read, attention, norm_rope, norm_rope_axes, mass, evict, shared): the library's functions
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  constexpr int N = 7;
+  constexpr int N = 8;
   void* f[N];
   if (n != N) {
     PyErr_SetString(PyExc_TypeError, "an address for each function");
@@ -389,6 +433,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_norm_rope_axes = reinterpret_cast<decltype(g_norm_rope_axes)>(f[4]);
   g_mass = reinterpret_cast<decltype(g_mass)>(f[5]);
   g_evict = reinterpret_cast<decltype(g_evict)>(f[6]);
+  g_shared = reinterpret_cast<decltype(g_shared)>(f[7]);
   Py_RETURN_NONE;
 }
 
@@ -399,7 +444,8 @@ PyMethodDef method(const char* name) {
 PyMethodDef g_methods[] = {method<bind>("bind"),           method<fp8_write>("write"),
                            method<fp8_read>("read"),       method<fp8_attention>("attention"),
                            method<norm_rope>("norm_rope"), method<norm_rope_axes>("norm_rope_axes"),
-                           method<fp8_mass>("mass"),       method<fp8_evict>("evict"), {nullptr, nullptr, 0, nullptr}};
+                           method<fp8_mass>("mass"),       method<fp8_evict>("evict"),
+                           method<fp8_shared>("shared"),   {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_fp8_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

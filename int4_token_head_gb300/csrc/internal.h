@@ -321,6 +321,36 @@ constexpr int kPieceRows = 40960;   // (a piece of a full 256-row tile for each 
 bool workspace_layout_fp8(int num_seqs, int num_q_tokens, int num_q_heads, int num_kv_heads,
                           int head_size, bool compact, WorkspaceLayoutFp8* out);
 
+// The workspace of kv_fp8_attention_shared: the FP8 attention's for the virtual
+// sequences (a prefix per group, then the sequences) and, behind it, their records
+// and the rows of whole prefill tiles that are merged.
+struct SharedLayout {
+  WorkspaceLayoutFp8 base;
+  size_t vrec;     // int4 [2 (groups + sequences)]
+  size_t dseq2;    // int4 [groups + sequences]
+  size_t vinfo;    // int2 [groups + sequences]
+  size_t tloc;     // int2 [max_pairs]
+  size_t row_o;    // f32 [2][row_tokens][Hq][d]
+  size_t row_ml;   // f32 [2][row_tokens][Hq][2]
+  size_t total;
+  int row_tokens;  // query tokens in groups that share
+};
+constexpr int kSharedRows = 1 << 17;  // most rows (token x q head) of sequences that share
+constexpr int kMostGroups = 1024;
+bool shared_layout(int num_seqs, int num_groups, int num_q_tokens, int num_q_heads, int num_kv_heads, int head_size,
+                   SharedLayout* out);
+
+struct SharedAttnArgs {
+  AttnArgs attn;
+  const int32_t* group_start;
+  const int32_t* prefix_lens;
+  int num_groups;
+  int max_group_tokens;
+  float* lse;  // nullable
+  int64_t lse_stride;
+};
+int launch_attention_shared_fp8(const SharedAttnArgs& a, cudaStream_t stream);
+
 int launch_attention(const AttnArgs& a, cudaStream_t stream);
 // FP8 block-scaled cache (attention_fp8.cu): E4M3 codes of d bytes per head
 // vector, one scale per (block, head)

@@ -219,7 +219,8 @@ struct Fp8Maps {
   CUtensorMap q, k, v;
 };
 
-template <int D>
+// SH: over virtual sequences (shared prefixes), and the rows' log-sum-exp
+template <int D, bool SH = false>
 __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
     prefill_ws_fp8_kernel(Common c, PlanView pv, const __grid_constant__ Fp8Maps maps) {
   using G = Fp8Ws<D>;
@@ -326,8 +327,8 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
       const bool taken = take_item(itc & 1, ph_ifull, item);
       if (pair_any(!taken)) break;
       const int seq = item.seq, h = item.h, tile = item.tile, kb0 = item.kb0, nkb = item.nkb;
-      const int q0 = c.qsl[seq], ql = c.qsl[seq + 1] - q0;
-      const int L = c.seq_lens[seq], ctx = L - ql;
+      const SeqView view = seq_view<SH>(c, pv, seq);
+      const int q0 = view.q0, ql = view.ql, L = view.L, ctx = view.ctx;
       const int tok0 = tile * c.tile_tokens;
       const bool rok = r < min(c.tile_tokens, ql - tok0) * c.group;
       const int nsteps = (nkb - kb0 + NB - 1) / NB;
@@ -468,9 +469,18 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
         tc_fence_after();
       }
       constexpr int UNITS = D / 32, FIRST = (UNITS + 1) / 2;  // of 32 columns; the first key half's
-      if (item.row >= 0) {
+      float *piece_o = pv.piece_o, *piece_ml = pv.piece_ml;
+      long long at = item.row < 0 ? -1 : item.row + r;
+      if constexpr (SH) {
+        const int first = pv.vrec[2 * seq + 1].z;
+        if (item.row < 0 && first >= 0) {  // a whole tile of a sequence with a shared prefix, or of such a prefix
+          at = (long long)(first + tok0 + (rok ? j : 0)) * c.hq + h * c.group + (rok ? r - j * c.group : 0);
+          piece_o = pv.row_o;
+          piece_ml = pv.row_ml;
+        }
+      }
+      if (at >= 0) {
         // a piece: O (V's factor 2^-8 undone), the reference and the sum
-        const long long at = item.row + r;
 #pragma unroll 1
         for (int u = kh ? 2 * FIRST : 0; u < (kh ? 2 * UNITS : 2 * FIRST); u++) {
           uint32_t o[16];
@@ -478,16 +488,18 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 16; i += 4)
             if (rok)
-              *reinterpret_cast<float4*>(pv.piece_o + at * D + 16 * u + i) =
+              *reinterpret_cast<float4*>(piece_o + at * D + 16 * u + i) =
                   make_float4(256.f * __uint_as_float(o[i]), 256.f * __uint_as_float(o[i + 1]),
                               256.f * __uint_as_float(o[i + 2]), 256.f * __uint_as_float(o[i + 3]));
         }
-        if (rok && kh == 0) *reinterpret_cast<float2*>(pv.piece_ml + 2 * at) = make_float2(m_ref, l);
+        if (rok && kh == 0) *reinterpret_cast<float2*>(piece_ml + 2 * at) = make_float2(m_ref, l);
         continue;
       }
       // a row that saw no usable key is zeros: O is 0 then, but for an item
       // without steps, whose O is not read (V's factor 2^-8 is undone here)
       const float inv = l == 0.f ? 0.f : 256.f / l;
+      if (SH && c.sh.lse && rok && kh == 0)
+        c.sh.lse[(q0 + tok0 + j) * c.sh.lse_stride + h * c.group + r - j * c.group] = log_sum_exp(m_ref, l);
       const float2 inv2 = make_float2(inv, inv);
       uint16_t* const orow = c.out + (long long)(q0 + tok0 + (rok ? j : 0)) * c.out_stride +
                              (long long)(h * c.group + (rok ? r - j * c.group : 0)) * D;
@@ -555,7 +567,7 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
           PrefillItem item;
           if (!take_item(itc & 1, ph_ifull, item)) break;
           const int nsteps = (item.nkb - item.kb0 + NB - 1) / NB;
-          int keys = c.seq_lens[item.seq] - item.kb0 * 16;  // rows of the step that hold keys
+          int keys = (SH ? pv.vrec[2 * item.seq].z : c.seq_lens[item.seq]) - item.kb0 * 16;  // rows of the step that hold keys
 #pragma unroll 1
           for (int st = 0; st < nsteps; st++, n++, keys -= NK) {
             uint8_t* const dst = tile + (n & 1) * G::KVBYTES;
@@ -641,7 +653,8 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
         }
         if (item.seq < 0) break;
         const int seq = item.seq, h = item.h, kb0 = item.kb0, nkb = item.nkb;
-        const int q0 = c.qsl[seq], tok0 = item.tile * c.tile_tokens;
+        const SeqView view = seq_view<SH>(c, pv, seq);
+        const int q0 = view.q0, tok0 = item.tile * c.tile_tokens;
         const int nsteps = (nkb - kb0 + NB - 1) / NB;
         // lane b < NB holds block b of a step: its row in the caches (behind
         // their end for a block that the table does not name) and its scales
@@ -649,7 +662,7 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
         auto block_of = [&](int st) -> int {
           const int kb = kb0 + st * NB + lane;
           if (st >= nsteps || lane >= NB || kb >= nkb) return -1;
-          const int id = c.block_table[(long long)seq * c.max_blocks + kb];
+          const int id = c.block_table[view.tab + kb];
           if (id >= 0 && id < c.num_blocks) return id;
           flag(c.status, KV_INT4_DEV_BAD_BLOCK);
           return -1;

@@ -28,6 +28,30 @@ struct PlanView {
   float* direct_ml;
   float* warp_o;
   float* warp_ml;
+  // shared prefixes only (SH below)
+  int4* vrec;    // two per virtual sequence: (first query token, query tokens, keys, position of the first query),
+                 // (table offset, two words; first row-buffer token or -1; group or -1)
+  int4* dseq2;   // with dseq: (table offset, two words; position of the first query; -)
+  int2* vinfo;   // per virtual sequence: (0 nothing, 1 decode, 2 prefill; index in dseq, first tile)
+  int2* tloc;    // per prefill tile: (first piece row, pieces), (-1, 1) for a whole one
+  float* row_o;  // [2][row_tokens][q heads][d] whole tiles' rows: prefixes', then the sequences'
+  float* row_ml;
+};
+
+// Shared prefixes (kernels with SH set): the batch is worked on as virtual
+// sequences, the groups' prefixes (all query tokens of a group against the keys
+// that its sequences share, no mask) and then the sequences themselves (their own
+// keys, or all of them where nothing is shared).  A row's two results are merged.
+struct SharedArgs {
+  const int32_t* group_start;
+  const int32_t* prefix_lens;
+  int num_groups;
+  int max_group_tokens;
+  int row_tokens;    // query tokens that the row buffer holds
+  int max_rows;      // query rows per kv head up to which a sequence shares
+  int min_saved;     // key positions that a group must save
+  float* lse;
+  int64_t lse_stride;
 };
 
 // A prefill tile of a sequence, or a piece of its keys: entry i of the list
@@ -118,7 +142,26 @@ struct Common {
   int step_blocks;      // FP8 prefill: cache blocks per step
   int split_steps;      // FP8 prefill: least steps of a piece
   int split_ctas;       // FP8 prefill: CTAs that run at once
+  SharedArgs sh;        // kernels with SH set
 };
+
+// a sequence as attention sees it; with SH set a virtual one
+struct SeqView {
+  int q0, ql;     // query tokens [q0, q0 + ql)
+  int L;          // keys
+  int ctx;        // position of the first query: it sees keys up to there, the next ones one more each
+  long long tab;  // first entry of its block table
+};
+template <bool SH>
+__device__ __forceinline__ SeqView seq_view(const Common& c, const PlanView& pv, int s) {
+  if constexpr (SH) {
+    const int4 a = pv.vrec[2 * s], b = pv.vrec[2 * s + 1];
+    return SeqView{a.x, a.y, a.z, a.w, (long long)(uint32_t)b.x | (long long)b.y << 32};
+  } else {
+    const int q0 = c.qsl[s], ql = c.qsl[s + 1] - q0, L = c.seq_lens[s];
+    return SeqView{q0, ql, L, L - ql, (long long)s * c.max_blocks};
+  }
+}
 
 // floor(n / d) for 0 <= n, 0 < d: one 32-bit division when both fit (the
 // usual case for schedule arithmetic), the 64-bit routine otherwise
@@ -230,7 +273,7 @@ __device__ __forceinline__ bool schedule_seq_ok(const Common& c, int q0, int ql,
 // inlined twice 2 to 3 us more per call).
 constexpr int kSplitTiles = 1024;
 constexpr int kSplitWaves = 6;
-template <int BUCKETS, bool SPLIT>
+template <int BUCKETS, bool SPLIT, bool SH>
 __device__ void build_pieces(const Common& c, const PlanView& pv, int n_pseq, int n_tiles, bool with_decode,
                              const int4* seqs, int* hist, int32_t* s_i32) {
   __shared__ int4 tiles[kSplitTiles];  // (sequence, tile, first block, end block)
@@ -249,14 +292,17 @@ __device__ void build_pieces(const Common& c, const PlanView& pv, int n_pseq, in
         x = seqs[p];
       } else {
         const int2 pt = pv.ptab[p];
-        x = make_int4(pt.x, c.qsl[pt.x + 1] - c.qsl[pt.x], c.seq_lens[pt.x], pt.y / c.hkv);
+        const SeqView v = seq_view<SH>(c, pv, pt.x);
+        x = make_int4(pt.x, v.ql, v.L, pt.y / c.hkv);
       }
+      const bool whole = SH && x.x < c.sh.num_groups;  // every query sees every key
       const int nt = (x.y + c.tile_tokens - 1) / c.tile_tokens;
 #pragma unroll 1
       for (int t = threadIdx.x % lps; t < nt; t += lps) {
         const int i = x.w + t - base, tok = t * c.tile_tokens;
         if (i < 0 || i >= kSplitTiles) continue;
-        tiles[i] = make_int4(x.x, t, window_lo(c, x.z - x.y + tok) >> 4, (prefill_tile_keys(c, x.z, x.y, t) + 15) / 16);
+        tiles[i] = make_int4(x.x, t, window_lo(c, x.z - x.y + tok) >> 4,
+                             ((whole ? x.z : prefill_tile_keys(c, x.z, x.y, t)) + 15) / 16);
         tile_rows[i] = (short)(min(c.tile_tokens, x.y - tok) * c.group);
       }
     }
@@ -347,6 +393,7 @@ __device__ void build_pieces(const Common& c, const PlanView& pv, int n_pseq, in
           }
           if (lpp > 1) row = __shfl_sync(0xffffffffu, row, 0);
         }
+        if (SH && pass && threadIdx.x % lpp == 0) pv.tloc[base + i] = make_int2(P > 1 ? row : -1, P);
         const int each = n / P, more = n - each * P;  // the first `more` pieces have a step more
 #pragma unroll 1
         for (int k = threadIdx.x % lpp; k < P; k += lpp) {
@@ -384,25 +431,119 @@ __device__ void build_pieces(const Common& c, const PlanView& pv, int n_pseq, in
   }
 }
 
+// The virtual sequences of a call with shared prefixes, by the schedule's CTA.  A
+// group shares its first P positions, whole blocks of them that come before the
+// queries of all its sequences; it does where that saves keys (two sequences with
+// queries at least, none of which fills a prefill tile by itself) and where the row
+// buffer has room for its rows, in the groups' order.  Else its sequences are
+// worked on whole.  group_start is looked at first: one that does not ascend within
+// the batch shares nothing.
+__device__ inline void build_shared(const Common& c, const PlanView& pv) {
+  __shared__ int gs[kMostGroups + 1], least[kMostGroups], first[kMostGroups], count[kMostGroups];
+  __shared__ int s_sum[kPrepThreads / 32];
+  const SharedArgs& sh = c.sh;
+  const int tid = threadIdx.x, NG = sh.num_groups;
+  bool bad = false;
+  for (int g = tid; NG > 0 && g <= NG; g += kPrepThreads) {
+    const int x = sh.group_start[g];
+    gs[g] = x;
+    bad = bad || x < 0 || x > c.num_seqs || (g > 0 && x < sh.group_start[g - 1]);
+    if (g < NG) {
+      least[g] = INT_MAX;
+      first[g] = INT_MAX;
+      count[g] = 0;
+    }
+  }
+  bad = __syncthreads_or(bad);
+  if (bad && tid == 0 && NG > 0) flag(c.status, KV_INT4_DEV_BAD_SEQ);
+  // the group of sequence s: the last one that starts at or before it, -1 for none
+  auto group_of = [&](int s) {
+    if (NG == 0 || bad || s < gs[0] || s >= gs[NG]) return -1;
+    int lo = 0, hi = NG;
+    while (hi - lo > 1) {
+      const int m = (lo + hi) >> 1;
+      if (gs[m] <= s) lo = m;
+      else hi = m;
+    }
+    return lo;
+  };
+  for (int s = tid; s < c.num_seqs; s += kPrepThreads) {
+    const int q0 = c.qsl[s], ql = c.qsl[s + 1] - q0, L = c.seq_lens[s], g = group_of(s);
+    if (g < 0 || ql == 0) continue;
+    if (!schedule_seq_ok<true>(c, q0, ql, L) || (long long)ql * c.group > sh.max_rows) {
+      atomicMin(&least[g], 0);
+    } else {
+      atomicMin(&least[g], L - ql);
+      atomicMin(&first[g], s);
+      atomicAdd(&count[g], 1);
+    }
+  }
+  __syncthreads();
+  int before = 0;  // row-buffer tokens of earlier rounds
+  for (int g0 = 0; g0 < NG; g0 += kPrepThreads) {
+    const int g = g0 + tid;
+    int P = 0, tokens = 0, q0 = 0;
+    if (g < NG && !bad && count[g] >= 2) {
+      q0 = c.qsl[gs[g]];
+      tokens = c.qsl[gs[g + 1]] - q0;
+      P = max(0, min(sh.prefix_lens[g], least[g])) & ~15;
+      if ((long long)P * (count[g] - 1) < sh.min_saved || q0 < 0 || tokens <= 0 || tokens > sh.max_group_tokens ||
+          q0 > c.num_q_tokens - tokens)
+        P = 0;
+    }
+    int total;
+    const int at = before + block_exclusive_scan<int>(P > 0 ? tokens : 0, &total, s_sum);
+    before = min(before + total, sh.row_tokens);  // no overflow: a round adds at most num_q_tokens
+    if (P > 0 && (long long)at + tokens > sh.row_tokens) P = 0;
+    if (g < NG) {
+      const long long tab = P > 0 ? (long long)first[g] * c.max_blocks : 0;
+      pv.vrec[2 * g] = make_int4(q0, P > 0 ? tokens : 0, P, P);
+      pv.vrec[2 * g + 1] = make_int4((int)(uint32_t)tab, (int)(tab >> 32), P > 0 ? at : -1, -1);
+      least[g] = P;  // from here on: the shared positions, the group's first token and its place in the row buffer
+      first[g] = q0;
+      count[g] = at;
+    }
+  }
+  __syncthreads();
+  for (int s = tid; s < c.num_seqs; s += kPrepThreads) {
+    const int q0 = c.qsl[s], L = c.seq_lens[s], g = group_of(s);
+    int ql = c.qsl[s + 1] - q0;
+    if (!schedule_seq_ok<true>(c, q0, ql, L)) {
+      flag(c.status, KV_INT4_DEV_BAD_SEQ);
+      ql = 0;
+    }
+    const int P = g >= 0 && ql > 0 ? least[g] : 0;
+    const long long tab = (long long)s * c.max_blocks + (P >> 4);
+    const int v = NG + s;
+    pv.vrec[2 * v] = make_int4(q0, ql, L - P, L - P - ql);
+    pv.vrec[2 * v + 1] = make_int4((int)(uint32_t)tab, (int)(tab >> 32),
+                                   P > 0 ? sh.row_tokens + count[g] + q0 - first[g] : -1, P > 0 ? g : -1);
+  }
+  __syncthreads();  // the records are read by other threads of the CTA
+}
+
 // The schedule, by one CTA of kPrepThreads threads.  PREFILL 0: no sequence of
 // the call can be a prefill, 1: none can be split, 2: any (code that is not there
 // is not fetched either).
-template <bool ANY_LEN, int PREFILL = 1>
+template <bool ANY_LEN, int PREFILL = 1, bool SH = false>
 __device__ void build_schedule(const Common& c, const PlanView& pv) {
+  const int num_seqs = SH ? c.sh.num_groups + c.num_seqs : c.num_seqs;
   __shared__ int32_t s_i32[kPrepThreads / 32];
   __shared__ long long s_i64[kPrepThreads / 32];
   __shared__ long long s_i64t[ANY_LEN ? kPrepThreads / 32 : 1];
   __shared__ int4 seqs[ANY_LEN && PREFILL > 0 ? kPrepThreads : 1];
   int n_dseq = 0, n_pseq = 0;
   long long dpre = 0, n_items = 0;
-  for (int base = 0; base < c.num_seqs; base += kPrepThreads) {
+  for (int base = 0; base < num_seqs; base += kPrepThreads) {
     const int s = base + threadIdx.x;
     int kind = 0, nblk = 0, ntiles = 0, ql = 0, L = 0, q0 = 0;
-    if (s < c.num_seqs) {
-      q0 = c.qsl[s];
-      L = c.seq_lens[s];
-      ql = c.qsl[s + 1] - q0;
-      if (!schedule_seq_ok<ANY_LEN>(c, q0, ql, L)) {
+    SeqView view{};
+    if (s < num_seqs) {
+      view = seq_view<SH>(c, pv, s);
+      q0 = view.q0;
+      L = view.L;
+      ql = view.ql;
+      if (!SH && !schedule_seq_ok<ANY_LEN>(c, q0, ql, L)) {
         flag(c.status, KV_INT4_DEV_BAD_SEQ);
       } else if (ql > 0) {
         kind = is_decode_kind(ql, c) ? 1 : 2;
@@ -465,11 +606,14 @@ __device__ void build_schedule(const Common& c, const PlanView& pv) {
     if (kind == 1) {
       pv.dseq[n_dseq + ex_a] = make_int4(s, L, q0, ql);
       pv.dprefix[n_dseq + ex_a] = dpre + ex_b;
+      if (SH) pv.dseq2[n_dseq + ex_a] = make_int4((int)(uint32_t)view.tab, (int)(view.tab >> 32), view.ctx, 0);
     } else if (PREFILL > 0 && kind == 2) {
       // the prefill kernel expands (tile, kv head) items from this table
       pv.ptab[n_pseq + ex_p] = make_int2(s, (int)min(n_items + ex_c, (long long)INT_MAX));
       if (ANY_LEN && base == 0) seqs[ex_p] = make_int4(s, ql, L, (int)min(ex_c / c.hkv, (long long)INT_MAX));
     }
+    if (SH && s < num_seqs)
+      pv.vinfo[s] = make_int2(kind, kind == 1 ? n_dseq + ex_a : kind == 2 ? (int)min((n_items + ex_c) / c.hkv, (long long)INT_MAX) : 0);
     n_dseq += tot_a;
     dpre += tot_b;
     n_pseq += tot_p;
@@ -498,8 +642,8 @@ __device__ void build_schedule(const Common& c, const PlanView& pv) {
   __shared__ int hist[kBuckets];
   if constexpr (ANY_LEN) {
     if (n_pseq > 0 && n_items <= c.max_items && n_items <= INT_MAX)
-      build_pieces<kBuckets, PREFILL == 2>(c, pv, n_pseq, (int)(n_items / c.hkv), n_dseq > 0,
-                             c.num_seqs <= kPrepThreads ? seqs : nullptr, hist, s_i32);
+      build_pieces<kBuckets, PREFILL == 2, SH>(c, pv, n_pseq, (int)(n_items / c.hkv), n_dseq > 0,
+                             num_seqs <= kPrepThreads ? seqs : nullptr, hist, s_i32);
     return;
   }
   if (n_pseq > 0 && n_items <= c.max_items && n_items <= INT_MAX) {
