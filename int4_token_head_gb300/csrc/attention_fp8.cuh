@@ -1,5 +1,5 @@
-// The FP8 attention's kernels and launch helpers, included by attention_fp8.cu
-// and attention_shared_fp8.cu in a namespace of their own.
+// The FP8 attention's kernels and launch helpers, included by attention_fp8.cu,
+// attention_shared_fp8.cu and mass_fp8.cu in a namespace of their own.
 template <int PREFILL, bool SH = false>
 __global__ void __launch_bounds__(kPrepThreads) plan_fp8_kernel(Common c, PlanView pv) {
   pdl_trigger();
@@ -54,25 +54,32 @@ int launch_plan(const Common& c, const PlanView& pv, bool may_prefill, bool may_
                     kPrepThreads, 0, stream, 1, c, pv);
 }
 
+// the tensor map of query rows: boxes of 64 elements x a kv head's q heads x
+// tile_tokens tokens; false where there is none (rows that overlap, say)
+bool make_q_map(CUtensorMap* m, const void* q, int64_t q_stride, int tokens, int q_heads, int head_size, int group,
+                int tile_tokens) {
+  const EncodeTiled enc = encode_tiled();
+  const cuuint64_t hq = q_heads, d = head_size;
+  if (!enc || (tokens > 1 && q_stride < (int64_t)(hq * d))) return false;
+  const cuuint64_t dims[3] = {d, hq, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {d * 2, (tokens > 1 ? (cuuint64_t)q_stride : hq * d) * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)tile_tokens}, ones[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, ones,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // the tensor maps of a call's prefill; false where its tensors have no such
 // map (query rows that overlap, say)
 template <int D>
 bool make_maps(const AttnArgs& a, int tile_tokens, Fp8Maps* m) {
   using G = Fp8Ws<D>;
   const EncodeTiled enc = encode_tiled();
-  const cuuint64_t hq = a.num_q_heads, hkv = a.num_kv_heads, rows = (cuuint64_t)a.num_blocks * 16;
-  const cuuint64_t group = hq / hkv;
-  if (!enc || rows == 0 || rows >= (1ull << 31) || (a.num_q_tokens > 1 && a.q_stride < (int64_t)(hq * D))) return false;
+  const cuuint64_t hkv = a.num_kv_heads, rows = (cuuint64_t)a.num_blocks * 16;
+  if (!enc || rows == 0 || rows >= (1ull << 31) ||
+      !make_q_map(&m->q, a.q, a.q_stride, a.num_q_tokens, a.num_q_heads, D, a.num_q_heads / a.num_kv_heads, tile_tokens))
+    return false;
   const cuuint32_t ones[4] = {1, 1, 1, 1};
-  {
-    const cuuint64_t dims[3] = {D, hq, (cuuint64_t)a.num_q_tokens};
-    const cuuint64_t strides[2] = {D * 2, (a.num_q_tokens > 1 ? (cuuint64_t)a.q_stride : hq * D) * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)tile_tokens};
-    if (enc(&m->q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), dims, strides, box, ones,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return false;
-  }
   const cuuint64_t dims[4] = {G::W, D / G::W, hkv, rows};
   const cuuint64_t strides[3] = {G::W, D, hkv * D};
   const cuuint32_t box[4] = {G::W, D / G::W, 1, 16};

@@ -7,7 +7,11 @@
 // The rows' denominators are known, so nothing is carried from key to key: a
 // warp takes 16-key blocks of one kv head and needs no other warp's results.
 
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <float.h>
+
+#include <type_traits>
 
 #include "../../include/kvint4.h"
 #include "common.cuh"
@@ -18,6 +22,8 @@
 namespace kvint4 {
 namespace {
 
+#include "attention_fp8.cuh"
+
 constexpr int kMassCols = 32;  // query rows staged at once
 
 struct MassParams {
@@ -26,7 +32,7 @@ struct MassParams {
   int warp_blocks;    // 16-key blocks per warp
   int few_groups;     // column groups of eight rows that mass_few_kernel stages per head
   float qscale;       // softmax_scale log2 e
-  FastDiv by_groups{1}, by_chunks{1};
+  FastDiv by_group{1}, by_groups{1}, by_chunks{1};
 };
 
 __device__ __forceinline__ bool mass_seq_ok(const MassArgs& a, int q0, int ql, int L) {
@@ -323,12 +329,15 @@ __global__ void __launch_bounds__(128) mass_rows_kernel(MassParams p) {
       if (table[b] < 0 || table[b] >= a.num_blocks) flag(a.dev_status, KV_INT4_DEV_BAD_BLOCK);
 }
 
+#include "mass_ws_fp8.cuh"
+
 template <int D>
 int launch_t(const MassArgs& a, cudaStream_t stream) {
   const int dev = current_device();
   const int sms = sm_count(dev);
   MassParams p{a, a.num_q_heads / a.num_kv_heads, a.num_kv_heads % 4 == 0 ? 4 : a.num_kv_heads % 2 == 0 ? 2 : 1, 16,
                1, a.softmax_scale * kLog2e};
+  p.by_group = FastDiv((uint32_t)p.group);
   const int64_t most_rows = (int64_t)a.max_query_len * p.group;
   p.few_groups = most_rows < 8 ? 1 : most_rows < kMassCols ? (int)(most_rows + 7) / 8 : kMassCols / 8;
   const int64_t table = (int64_t)a.max_blocks_per_seq * 16;
@@ -361,6 +370,18 @@ int launch_t(const MassArgs& a, cudaStream_t stream) {
   if (!grid_of(per, &grid)) return KV_INT4_ERR_SIZE;
   if (int e = launch_pdl(mass_few_kernel<D>, dim3(grid), 128, MassFew<D>::smem(p.hg, p.few_groups), stream, 1, p)) return e;
   if (most_rows <= kMassCols) return KV_INT4_OK;
+  using W = MassWs<D>;
+  const int tile_tokens = W::QR / p.group;
+  CUtensorMap qmap;
+  if (make_q_map(&qmap, a.q, a.q_stride, a.num_q_tokens, a.num_q_heads, D, p.group, tile_tokens)) {
+    static PerContext<int> occ_c;
+    int occ = 0;
+    if (!occ_c.get(dev, [](int* o) { return configure_tmem(mass_ws_kernel<D>, W::SMEM, W::THREADS, W::S_COLS, o); }, &occ))
+      return KV_INT4_ERR_CUDA;
+    const int64_t items = (int64_t)a.num_seqs * ((most + 127) / 128) * a.num_kv_heads;
+    return launch_pdl(mass_ws_kernel<D>, dim3((unsigned)(items < sms ? (items > 0 ? items : 1) : sms)), W::THREADS, W::SMEM, stream,
+                      1, p, tile_tokens, qmap);
+  }
   if (!grid_of(16, &grid)) return KV_INT4_ERR_SIZE;
   const size_t smem = (size_t)p.hg * kMassCols * (D * 2 + 8) + 4 * p.warp_blocks * 16 * 4;
   return launch_pdl(mass_rows_kernel<D>, dim3(grid), 128, smem, stream, 1, p);

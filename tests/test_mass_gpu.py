@@ -71,6 +71,49 @@ def test_a_long_prompt(d):
     _all([(530, 530), (300, 900)], 4, 1, d)
 
 
+@pytest.mark.parametrize("d", HEADS)
+@pytest.mark.parametrize("hq,hkv", [(3, 3), (5, 1), (24, 2), (33, 1), (64, 1)])
+def test_many_rows_of_odd_groups(d, hq, hkv):
+    """Groups that do not divide a tile of query rows; sequences with few rows beside them."""
+    _all([(40, 40), (1, 300), (129, 270), (0, 9), (2, 140)], hq, hkv, d)
+
+
+def test_many_sequences_with_many_rows():
+    """The orders of work: by distance from the end, one after the other, in windows of sequences."""
+    g = np.random.default_rng(5)
+    _all([(int(n), int(n + g.integers(0, 200))) for n in g.integers(30, 60, 100)], 2, 2, 64)
+    _all([(int(n), int(n + g.integers(0, 200))) for n in g.integers(30, 60, 200)], 2, 2, 64)
+    _all([(int(n), int(n)) for n in g.integers(30, 40, 1100)], 1, 1, 64)
+
+
+def test_a_chunk_behind_a_very_long_history():
+    _all([(40, 140000), (70, 3000)], 1, 1, 64)
+
+
+@pytest.mark.parametrize("d", HEADS)
+def test_one_query_row_for_every_token(d):
+    """Queries that no tensor map holds."""
+    b = Batch([(50, 70), (1, 40), (90, 200)], 2, d).fill()
+    q, _, mass, scale = _inputs(b, 4)
+    q = q[:1].expand(b.tokens, -1, -1)
+    lse = torch.from_numpy(F.log_sum_exp(q.double().numpy(), b.kc, b.ks, b.table, b.lens, b.start, scale)[0]).float()
+    m = torch.from_numpy(mass.copy()).cuda()
+    kc, _, ks, _ = b.device()
+    kv.attention_mass_fp8(q[:1].cuda().expand(b.tokens, -1, -1), lse.cuda(), kc, ks, *b.meta(), b.max_len, 200, scale, m,
+                          dev_status=b.status)
+    _check(m, b, q, lse, mass, scale)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_nan_queries_of_one_sequence_stay_in_its_masses(d):
+    b = Batch([(40, 60), (33, 90), (1, 20)], 2, d).fill()
+    q, lse, mass, scale = _inputs(b, 4)
+    want = _call(b, q, lse, mass, scale)
+    q[40:73] = float("nan")
+    got = _call(b, q, lse, mass, scale)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2]) and torch.isnan(got[1, :, :90]).all()
+
+
 def test_sharp_and_flat_scores():
     _all([(1, 400), (40, 100)], 8, 2, 128, q_gain=12.0)
     _all([(1, 400), (40, 100)], 8, 2, 128, q_gain=1e-3)
