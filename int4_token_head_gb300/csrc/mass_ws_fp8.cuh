@@ -5,15 +5,14 @@
 // S = K Q^T with a tile of QR query rows as N, so that a key is a TMEM lane and
 // the sum over the rows stays in one thread: per score one fma (the key's factor,
 // the row's -lse log2 e), one exp2 and one add, and nothing crosses threads until
-// an item's two partial sums meet.  Warps in four roles that meet at mbarriers:
-//   * scheduler warp (12): the items of this CTA in an order that it computes by
+// an item's four partial sums meet.  Warps in four roles that meet at mbarriers:
+//   * scheduler warp (20): the items of this CTA in an order that it computes by
 //     itself (below), through a ring of four; TMA copies of the Q tiles that see an
 //     item's keys (bf16, straight into the MMA's swizzled tile) into NQ slots;
-//   * convert warps (8-11): an item's codes from global memory into one of two bf16
+//   * convert warps (16-19): an item's codes from global memory into one of two bf16
 //     tiles, and its blocks' scales into the item's ring entry;
-//   * MMA warp (13): tile t of an item into a score buffer of warpgroup t mod 2 (two
-//     buffers each);
-//   * sum warps (0-7): warpgroup w takes the tiles t = w mod 2; the rows' lse are
+//   * MMA warp (21): tile t of an item into the score buffer of warpgroup t mod 4;
+//   * sum warps (0-15): warpgroup w takes the tiles t = w mod 4; the rows' lse are
 //     loaded a tile ahead and shared through shared memory.
 // What bounds it is the exp2 of every score and the MMAs, about alike (128 x 128
 // scores: 512 cycles of tensor work at head size 128).
@@ -36,13 +35,14 @@ struct MassWs {
   static constexpr int QBYTES = QR * 128 * KB, KBYTES = 128 * 128 * KB;
   static constexpr int NQ = D == 256 ? 2 : 4;     // Q slots
   static constexpr int NI = 4;                    // item ring
-  static constexpr int S_COLS = 4 * QR;           // TMEM: four score buffers
-  static constexpr int THREADS = 14 * 32;
+  static constexpr int S_COLS = 4 * QR;           // TMEM: a score buffer per warpgroup
+  static constexpr int WG = 4;                    // warpgroups that sum
+  static constexpr int THREADS = (4 * WG + 6) * 32;
   // item ring entry: 8 ints, 8 scales
   static constexpr int ENTRY = 64;
-  static constexpr int NBARS = 2 * NI + 2 * NQ + 4 + 8 + NI + 1;
+  static constexpr int NBARS = 2 * NI + 2 * NQ + 4 + 2 * WG + NI + 1;
   static constexpr int BARS = (NBARS * 8 + 15) / 16 * 16;  // what follows is read in 16-byte words
-  static constexpr int TAIL = NI * ENTRY + BARS + 16 + 2 * 2 * 128 * 4 + NI * 128 * 4 + kMassWindow * 8;
+  static constexpr int TAIL = NI * ENTRY + BARS + 16 + WG * 2 * 128 * 4 + NI * (WG - 1) * 128 * 4 + kMassWindow * 8;
   static constexpr int SMEM = 2 * KBYTES + NQ * QBYTES + TAIL;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert((2 * KBYTES + NQ * QBYTES) % 1024 == 0 && (NI * ENTRY + BARS) % 16 == 0, "alignment");
@@ -54,30 +54,25 @@ struct MassItem {
   int q0, ql, len;
 };
 
-__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
   // the registers are outputs so that no use of them moves before the wait
   asm volatile("tcgen05.wait::ld.sync.aligned;\n"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
-                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
-                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 
 template <int D>
 __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
     mass_ws_kernel(MassParams p, int tile_tokens, const __grid_constant__ CUtensorMap qmap) {
   using G = MassWs<D>;
-  constexpr int KSTEPS = D / 16, QR = G::QR, NQ = G::NQ, NI = G::NI, CH = D / 16;
+  constexpr int KSTEPS = D / 16, QR = G::QR, NQ = G::NQ, NI = G::NI, WG = G::WG, CH = D / 16;
   constexpr uint32_t IDESC = umma_idesc_f16(128, QR, false) | (1u << 7) | (1u << 10);  // bf16 operands
   extern __shared__ __align__(1024) uint8_t smem_mass[];
   uint8_t* const sK = smem_mass;                   // two tiles [KB][128][128 B], swizzled
@@ -86,14 +81,14 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
   uint64_t* const bars = reinterpret_cast<uint64_t*>(ring + NI * G::ENTRY);
   int* const sctl = reinterpret_cast<int*>(ring + NI * G::ENTRY + G::BARS);  // abort flag, TMEM address
   float* const snl = reinterpret_cast<float*>(sctl + 4);      // [warpgroup][2][128]: -lse log2 e of a tile's rows
-  float* const spart = snl + 2 * 2 * 128;                     // [NI][128]: the second warpgroup's sums
-  int2* const slist = reinterpret_cast<int2*>(spart + NI * 128);  // [kMassWindow] (sequence, key tiles)
+  float* const spart = snl + WG * 2 * 128;                    // [NI][WG - 1][128]: the other warpgroups' sums
+  int2* const slist = reinterpret_cast<int2*>(spart + NI * (WG - 1) * 128);  // [kMassWindow] (sequence, key tiles)
   volatile int* const abort_flag = sctl;
   const MassArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   enum {
     IFULL = 0, IFREE = IFULL + NI, QFULL = IFREE + NI, QFREE = QFULL + NQ, KFULL = QFREE + NQ, KFREE = KFULL + 2,
-    SFULL = KFREE + 2, SFREE = SFULL + 4, PART = SFREE + 4, DRAIN = PART + NI
+    SFULL = KFREE + 2, SFREE = SFULL + WG, PART = SFREE + WG, DRAIN = PART + NI
   };
   static_assert(DRAIN + 1 == G::NBARS, "barriers");
   auto bar = [&](int i) { return smem_addr(&bars[i]); };
@@ -104,8 +99,8 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
   if (tid == 0) {
     for (int b = 0; b < NI; b++) {
       mbar_init(bar(IFULL + b), 1);
-      mbar_init(bar(IFREE + b), 13);
-      mbar_init(bar(PART + b), 4);
+      mbar_init(bar(IFREE + b), 4 * WG + 5);
+      mbar_init(bar(PART + b), 4 * (WG - 1));
     }
     for (int b = 0; b < NQ; b++) {
       mbar_init(bar(QFULL + b), 1);
@@ -115,7 +110,7 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
       mbar_init(bar(KFULL + b), 4);
       mbar_init(bar(KFREE + b), 1);
     }
-    for (int b = 0; b < 4; b++) {
+    for (int b = 0; b < WG; b++) {
       mbar_init(bar(SFULL + b), 1);
       mbar_init(bar(SFREE + b), 4);
     }
@@ -145,18 +140,57 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
     return it;
   };
 
-  if (warp < 8) {
+  if (warp < 4 * WG) {
     // ======================= sums =======================
     const int wg = warp >> 2, r = tid & 127;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const int tile_rows = tile_tokens * p.group;
     float* const nls = snl + wg * 2 * 128;
-    auto row_lse = [&](const MassItem& it, int t) {  // of column r of tile t, as -lse log2 e; -infinity for none
-      const int j = (int)p.by_group.div((uint32_t)r), tok = it.tok0 + t * tile_tokens + j;
+    const int j = (int)p.by_group.div((uint32_t)r), jj = r - j * p.group;  // this thread's column of every tile
+    auto row_lse = [&](const MassItem& it, int t) {  // the column's of tile t; infinity for none
+      const int tok = it.tok0 + t * tile_tokens + j;
       float l = INFINITY;
-      if (it.seq >= 0 && t < it.tiles && r < tile_rows && tok < it.ql)
-        l = a.lse[(int64_t)(it.q0 + tok) * a.lse_stride + it.head * p.group + (r - j * p.group)];
+      if (it.seq >= 0 && r < tile_rows && tok < it.ql)
+        l = a.lse[(int64_t)(it.q0 + tok) * a.lse_stride + it.head * p.group + jj];
       return l;
+    };
+    // sum of a tile's weights for this key; the columns [lo, hi) see it
+    auto sum_tile = [&](auto masked, const float* nl, float f, int lo, int hi) {
+      constexpr bool MASKED = decltype(masked)::value;
+      const uint32_t ts = tmem + QR * wg + lane_off;
+      uint32_t x[2][16];
+      tmem_ld16_async(ts, x[0]);
+      float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+      const float2 ff = make_float2(f, f);
+#pragma unroll
+      for (int c = 0; c < QR / 16; c++) {
+        tmem_ld_wait(x[c & 1]);
+        if (c + 1 < QR / 16) {
+          tmem_ld16_async(ts + 16 * (c + 1), x[(c + 1) & 1]);
+        } else {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) fp8_arrive(bar(SFREE + wg));
+        }
+        const uint32_t (&v)[16] = x[c & 1];
+#pragma unroll
+        for (int k = 0; k < 16; k += 4) {
+          const float4 b = *reinterpret_cast<const float4*>(nl + 16 * c + k);
+          const float2 t0 = f2fma(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), ff, make_float2(b.x, b.y));
+          const float2 t1 = f2fma(make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), ff, make_float2(b.z, b.w));
+          float2 e0 = make_float2(fast_exp2(t0.x), fast_exp2(t0.y)), e1 = make_float2(fast_exp2(t1.x), fast_exp2(t1.y));
+          if (MASKED) {
+            const int q = 16 * c + k;
+            e0.x = q >= lo && q < hi ? e0.x : 0.f;
+            e0.y = q + 1 >= lo && q + 1 < hi ? e0.y : 0.f;
+            e1.x = q + 2 >= lo && q + 2 < hi ? e1.x : 0.f;
+            e1.y = q + 3 >= lo && q + 3 < hi ? e1.y : 0.f;
+          }
+          s0 = f2add(s0, e0);
+          s1 = f2add(s1, e1);
+        }
+      }
+      return (s0.x + s0.y) + (s1.x + s1.y);
     };
     // the warpgroup's warps go on together or not at all (after a time-out one may
     // get an item that the others do not)
@@ -185,71 +219,41 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
       MassItem next{-1, 0, 0, 0, 0, 0, 0, 0};
       bool taken = false;
 #pragma unroll 1
-      for (int t = wg; t < it.tiles; t += 2, cnt++) {
+      for (int t = wg; t < it.tiles; t += WG, cnt++) {
         float* const nl = nls + (cnt & 1) * 128;
         nl[r] = fabsf(l) == INFINITY ? -INFINITY : -l * kLog2e;
-        if (t + 2 < it.tiles) {
-          l = row_lse(it, t + 2);
+        if (t + WG < it.tiles) {
+          l = row_lse(it, t + WG);
         } else {
           next = take_all(n + 1);
           taken = true;
           l = row_lse(next, wg);
         }
         asm volatile("bar.sync %0, 128;\n" ::"r"(1 + wg) : "memory");
-        const int buf = wg + 2 * (cnt & 1);
-        fp8_wait(bar(SFULL + buf), (cnt >> 1) & 1, abort_flag, a.dev_status);
+        fp8_wait(bar(SFULL + wg), cnt & 1, abort_flag, a.dev_status);
         tc_fence_after();
         if (t == wg) f = p.qscale * reinterpret_cast<const float*>(entry(e) + 8)[r >> 4];
         const int tok = it.tok0 + t * tile_tokens;
         // this key is hidden from columns before `lo` and there are none from `hi` on
         const int lo = (pos - ctx - tok) * p.group, hi = min(tile_tokens, it.ql - tok) * p.group;
         const bool full = __all_sync(0xffffffffu, lo <= 0) && hi == tile_rows;
-        const uint32_t ts = tmem + QR * buf + lane_off;
-        uint32_t x[2][32];
-        tmem_ld32_async(ts, x[0]);
-        float2 s0 = make_float2(0.f, 0.f), s1 = s0;
-        const float2 ff = make_float2(f, f);
-#pragma unroll
-        for (int c = 0; c < QR / 32; c++) {
-          tmem_ld_wait(x[c & 1]);
-          if (c + 1 < QR / 32) {
-            tmem_ld32_async(ts + 32 * (c + 1), x[(c + 1) & 1]);
-          } else {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) fp8_arrive(bar(SFREE + buf));
-          }
-          uint32_t (&v)[32] = x[c & 1];
-#pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            const float4 b = *reinterpret_cast<const float4*>(nl + 32 * c + k);
-            const float2 t0 = f2fma(make_float2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), ff, make_float2(b.x, b.y));
-            const float2 t1 = f2fma(make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), ff, make_float2(b.z, b.w));
-            float2 e0 = make_float2(fast_exp2(t0.x), fast_exp2(t0.y)), e1 = make_float2(fast_exp2(t1.x), fast_exp2(t1.y));
-            if (!full) {
-              const int q = 32 * c + k;
-              e0.x = q >= lo && q < hi ? e0.x : 0.f;
-              e0.y = q + 1 >= lo && q + 1 < hi ? e0.y : 0.f;
-              e1.x = q + 2 >= lo && q + 2 < hi ? e1.x : 0.f;
-              e1.y = q + 3 >= lo && q + 3 < hi ? e1.y : 0.f;
-            }
-            s0 = f2add(s0, e0);
-            s1 = f2add(s1, e1);
-          }
-        }
-        w += (s0.x + s0.y) + (s1.x + s1.y);
+        // two copies of the loop: a branch in it keeps its loads, exponentials and sums
+        // from overlapping (2900 cycles a tile)
+        w += full ? sum_tile(std::false_type{}, nl, f, lo, hi) : sum_tile(std::true_type{}, nl, f, lo, hi);
       }
       if (!taken) {
         next = take_all(n + 1);
         l = row_lse(next, wg);
       }
-      if (wg == 1) {
-        spart[e * 128 + r] = w;
+      float* const part = spart + e * (WG - 1) * 128 + r;
+      if (wg > 0) {
+        part[(wg - 1) * 128] = w;
         __syncwarp();
         if (lane == 0) fp8_arrive(bar(PART + e));
       } else {
         fp8_wait(bar(PART + e), (n / NI) & 1, abort_flag, a.dev_status);
-        w += spart[e * 128 + r];
+#pragma unroll
+        for (int x = 0; x < WG - 1; x++) w += part[x * 128];
         const float ks = reinterpret_cast<const float*>(entry(e) + 8)[r >> 4];
         if (pos < it.len) *out = (ks == 0.f ? 0.f : w) + old;  // a position without a block receives nothing
       }
@@ -257,7 +261,7 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
       if (lane == 0) fp8_arrive(bar(IFREE + e));
       it = next;
     }
-  } else if (warp < 12) {
+  } else if (warp < 4 * WG + 4) {
     // ======================= codes =======================
     const int t = tid & 127;
     const __nv_bfloat162 kf = __float2bfloat162_rn(exp2_int(120));
@@ -272,35 +276,39 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
         int id = b < nblk ? table[b] : -1;
         return id >= 0 && id < a.num_blocks ? id : -1;
       };
-      uint4 x[CH];
-      int id[CH];
-#pragma unroll
-      for (int i = 0; i < CH; i++) id[i] = block_at(it.kt * 8 + ((t + 128 * i) / CH >> 4));
-#pragma unroll
-      for (int i = 0; i < CH; i++) {
-        const int c = t + 128 * i, row = c / CH, col = c - row * CH;
-        x[i] = make_uint4(0, 0, 0, 0);
-        if (id[i] >= 0 && it.kt * 128 + row < it.len)
-          x[i] = *reinterpret_cast<const uint4*>(a.k_cache + (((int64_t)id[i] * 16 + (row & 15)) * a.num_kv_heads + it.head) * D +
-                                                 16 * col);
-      }
       if (t < 8) {
         const int b = it.kt * 8 + t, blk = block_at(b);
         reinterpret_cast<float*>(entry(n % NI) + 8)[t] = blk >= 0 ? a.k_scale[(int64_t)blk * a.num_kv_heads + it.head] : 0.f;
         if (b < nblk && blk < 0 && it.head == 0) flag(a.dev_status, KV_INT4_DEV_BAD_BLOCK);
       }
-      for (; freed < n - 1; freed++) fp8_wait(bar(KFREE + (freed & 1)), (freed >> 1) & 1, abort_flag, a.dev_status);
       uint8_t* const dst = sK + (n & 1) * G::KBYTES;
+      constexpr int PART_CH = CH < 8 ? CH : CH % 8 ? CH / 2 : 8;  // chunks in flight per thread
+#pragma unroll 1
+      for (int i0 = 0; i0 < CH; i0 += PART_CH) {
+        uint4 x[PART_CH];
+        int id[PART_CH];
 #pragma unroll
-      for (int i = 0; i < CH; i++) {
-        const int c = t + 128 * i, row = c / CH, col = c - row * CH;
-        uint4 lo, hi;
-        e4m3x4_to_bf16x2(x[i].x, kf, lo.x, lo.y);
-        e4m3x4_to_bf16x2(x[i].y, kf, lo.z, lo.w);
-        e4m3x4_to_bf16x2(x[i].z, kf, hi.x, hi.y);
-        e4m3x4_to_bf16x2(x[i].w, kf, hi.z, hi.w);
-        *reinterpret_cast<uint4*>(dst + fp8_sw128(128, row, 2 * col)) = lo;
-        *reinterpret_cast<uint4*>(dst + fp8_sw128(128, row, 2 * col + 1)) = hi;
+        for (int i = 0; i < PART_CH; i++) id[i] = block_at(it.kt * 8 + ((t + 128 * (i0 + i)) / CH >> 4));
+#pragma unroll
+        for (int i = 0; i < PART_CH; i++) {
+          const int c = t + 128 * (i0 + i), row = c / CH, col = c - row * CH;
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (id[i] >= 0 && it.kt * 128 + row < it.len)
+            x[i] = *reinterpret_cast<const uint4*>(
+                a.k_cache + (((int64_t)id[i] * 16 + (row & 15)) * a.num_kv_heads + it.head) * D + 16 * col);
+        }
+        for (; freed < n - 1; freed++) fp8_wait(bar(KFREE + (freed & 1)), (freed >> 1) & 1, abort_flag, a.dev_status);
+#pragma unroll
+        for (int i = 0; i < PART_CH; i++) {
+          const int c = t + 128 * (i0 + i), row = c / CH, col = c - row * CH;
+          uint4 lo, hi;
+          e4m3x4_to_bf16x2(x[i].x, kf, lo.x, lo.y);
+          e4m3x4_to_bf16x2(x[i].y, kf, lo.z, lo.w);
+          e4m3x4_to_bf16x2(x[i].z, kf, hi.x, hi.y);
+          e4m3x4_to_bf16x2(x[i].w, kf, hi.z, hi.w);
+          *reinterpret_cast<uint4*>(dst + fp8_sw128(128, row, 2 * col)) = lo;
+          *reinterpret_cast<uint4*>(dst + fp8_sw128(128, row, 2 * col + 1)) = hi;
+        }
       }
       fence_proxy_async_smem();  // the tile is read by the tensor cores
       __syncwarp();
@@ -309,7 +317,7 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
         fp8_arrive(bar(IFREE + n % NI));
       }
     }
-  } else if (warp == 12) {
+  } else if (warp == 4 * WG + 4) {
     // ======================= scheduler, Q copies =======================
     const int grid = gridDim.x, hkv = a.num_kv_heads;
     int n = 0, nq = 0;  // items handed on, Q tiles copied
@@ -433,7 +441,8 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(lead));
     const uint64_t dk = umma_desc(smem_addr(sK), 16, 1024), dq = umma_desc(smem_addr(sQ), 16, 1024);
     const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);  // in a uniform register
-    int nq = 0, cnt[2] = {0, 0};
+    int nq = 0;
+    uint32_t used = 0, odd = 0;  // by score buffer: whether it has been, and an odd number of times
 #pragma unroll 1
     for (int n = 0;; n++) {
       const MassItem it = take(n);
@@ -442,11 +451,11 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
       const uint64_t kt = dk + (uint64_t)((n & 1) * (G::KBYTES >> 4));
 #pragma unroll 1
       for (int t = 0; t < it.tiles; t++, nq++) {
-        const int s = nq % NQ, c = t & 1 ? cnt[1] : cnt[0], buf = (t & 1) + 2 * (c & 1);
+        const int s = nq % NQ, buf = t % WG;
         // the tile's rows, and its score buffer
         const int i = lane == 0 ? QFULL + s : SFREE + buf;
-        const uint32_t ph = lane == 0 ? (nq / NQ) & 1 : ((c >> 1) - 1) & 1;
-        fp8_wait_warp(bar(i), ph, abort_flag, a.dev_status, lane > 1 || (lane == 1 && c < 2));
+        const uint32_t ph = lane == 0 ? (nq / NQ) & 1 : (odd >> buf & 1) ^ 1;
+        fp8_wait_warp(bar(i), ph, abort_flag, a.dev_status, lane > 1 || (lane == 1 && !(used >> buf & 1)));
         tc_fence_after();
         const uint64_t qt = dq + (uint64_t)(s * (G::QBYTES >> 4));
 #pragma unroll
@@ -455,8 +464,8 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
                   qt + (uint64_t)(((ks >> 2) * QR * 128 + (ks & 3) * 32) >> 4), IDESC, ks > 0);
         fp8_commit(lead, bar(SFULL + buf));
         fp8_commit(lead, bar(QFREE + s));
-        if (t & 1) cnt[1]++;
-        else cnt[0]++;
+        used |= 1u << buf;
+        odd ^= 1u << buf;
       }
       fp8_commit(lead, bar(KFREE + (n & 1)));
       __syncwarp();
