@@ -13,8 +13,8 @@
 // j, so a row may be overwritten once every destination row at or before it has
 // been read: the CTA (or cluster) of a (sequence, kv head, K or V) takes its
 // destination blocks in order, a chunk at a time, and no one stores a chunk before
-// everyone has loaded it.  The loads of the next chunk lie behind the stores of
-// this one and are issued before them.
+// everyone has loaded it.  The rows of the next chunks lie behind the stores of
+// this one and are on their way (cp.async) before them.
 
 #include <cuda_runtime.h>
 
@@ -38,17 +38,26 @@ __device__ __forceinline__ uint32_t mass_key(float x) {
 }
 
 constexpr int kBins = 2048;
-constexpr int kCopies = 4;  // histograms by lane: neighbouring masses share their upper bits, and with them a bin
 constexpr int kCachedMasses = 40960;
+constexpr int kListed = 1024;
 
 template <int THREADS>
-__global__ void __launch_bounds__(THREADS) evict_select_kernel(EvictArgs a, int cached) {
-  constexpr int WARPS = THREADS / 32, PER = kBins / THREADS;
+struct Select {
+  // histograms by lane: neighbouring masses share their upper bits, and with them a
+  // bin (few masses: one, which is sooner cleared and summed)
+  static constexpr int COPIES = THREADS > 256 ? 4 : 1;
+  static size_t smem(int cached) { return (size_t)(COPIES * kBins + cached) * 4; }
+};
+
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS > 256 ? 2 : 4) evict_select_kernel(EvictArgs a, int cached) {
+  constexpr int WARPS = THREADS / 32, PER = kBins / THREADS, COPIES = Select<THREADS>::COPIES;
   extern __shared__ __align__(16) uint32_t sdyn[];
-  uint32_t* const hist = sdyn;                    // [kCopies][kBins]
-  uint32_t* const keys = sdyn + kCopies * kBins;  // [cached]
-  __shared__ uint32_t s_warp[2][WARPS];
-  __shared__ uint32_t s_bin, s_left;
+  uint32_t* const hist = sdyn;                                            // [COPIES][kBins]
+  float* const masses = reinterpret_cast<float*>(sdyn + COPIES * kBins);  // [cached]
+  __shared__ uint32_t s_warp[2][32], s_key[kListed];
+  __shared__ int s_pos[kListed];
+  __shared__ uint32_t s_bin, s_left, s_count, s_listed;
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -73,27 +82,74 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(EvictArgs a, int 
     }
     return;
   }
-  const int last = L - a.recent;        // candidates are [0, last); last > take
+  const int last = L - a.recent;  // candidates are [0, last); last > take
   const int take = a.budget - a.recent;
-  const bool in_smem = last <= cached;
-  auto key_at = [&](int p) { return in_smem ? keys[p] : mass_key(mass[p]); };
+  const bool in_smem = L <= cached;
+  auto key_at = [&](int p) { return mass_key(in_smem ? masses[p] : mass[p]); };
+  if (in_smem) {
+#pragma unroll 8
+    for (int p = tid; p < L; p += THREADS) masses[p] = mass[p];
+  }
+  for (int w = WARPS + tid; w < 32; w += THREADS) s_warp[0][w] = s_warp[1][w] = 0;  // warps that are not there
+  if (tid == 0) s_listed = 0;
+  // sum of x over the warps before this one, of values that lane 0 of each has left
+  auto before_warp = [&](const uint32_t* x) {
+    const uint32_t mine = x[lane];
+    uint32_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    return __shfl_sync(0xffffffffu, incl - mine, warp);
+  };
 
-  // the take-th largest key and how many of its equals are taken
+  // a warp's walk over positions [q0, q1): four keys per lane are loaded before the
+  // ballots of the first are used; put(position, key, the test's answer, its ballot)
+  const uint32_t below = (1u << lane) - 1;
+  auto walk = [&](int q0, int q1, auto&& test, auto&& put) {
+    constexpr int U = 4;
+#pragma unroll 1
+    for (int q = q0; q < q1; q += 32 * U) {
+      uint32_t k[U], m[U];
+      bool t[U];
+#pragma unroll
+      for (int u = 0; u < U; u++) {
+        const int p = q + 32 * u + lane;
+        k[u] = p < q1 ? key_at(p) : 0u;
+      }
+#pragma unroll
+      for (int u = 0; u < U; u++) {
+        const int p = q + 32 * u + lane;
+        t[u] = test(p, k[u], p < q1);
+        m[u] = __ballot_sync(0xffffffffu, t[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; u++) put(q + 32 * u + lane, k[u], t[u], m[u]);
+    }
+  };
+
+  // Each warp owns a run of candidates in the ordered pass at the end.  The
+  // take-th largest key and how many of its equals are taken, bin by bin; the keys of
+  // the first pass's bin are few as a rule and are listed, so that the other passes
+  // touch no more than those
+  const int run = (last + WARPS - 1) / WARPS, p0 = min(last, warp * run), p1 = min(last, p0 + run);
   uint32_t prefix = 0, mask = 0, left = take;
+  uint32_t listed = 0;  // candidates on the list, 0: there is none
+  uint32_t gt = 0, eq = 0;
   if (take > 0) {
 #pragma unroll 1
     for (int pass = 0; pass < 3; pass++) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const uint32_t bins = pass == 2 ? 1023u : 2047u;
-      for (int b = tid; b < kCopies * kBins; b += THREADS) hist[b] = 0;
+#pragma unroll
+      for (int b = 0; b < COPIES * PER; b++) hist[b * THREADS + tid] = 0;
       __syncthreads();
-      uint32_t* const mine = hist + (lane & (kCopies - 1)) * kBins;
-      if (pass == 0) {
-#pragma unroll 4
-        for (int p = tid; p < last; p += THREADS) {
-          const uint32_t k = mass_key(mass[p]);
-          if (in_smem) keys[p] = k;
-          atomicAdd(mine + (k >> shift), 1u);
+      uint32_t* const mine = hist + (lane & (COPIES - 1)) * kBins;
+      if (listed) {
+        for (uint32_t x = tid; x < listed; x += THREADS) {
+          const uint32_t k = s_key[x];
+          if ((k & mask) == prefix) atomicAdd(mine + ((k >> shift) & bins), 1u);
         }
       } else {
 #pragma unroll 4
@@ -110,7 +166,7 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(EvictArgs a, int 
         const int b = kBins - 1 - (tid * PER + e);
         c[e] = 0;
 #pragma unroll
-        for (int x = 0; x < kCopies; x++) c[e] += hist[x * kBins + b];
+        for (int x = 0; x < COPIES; x++) c[e] += hist[x * kBins + b];
         sum += c[e];
       }
       uint32_t incl = sum;
@@ -121,13 +177,13 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(EvictArgs a, int 
       }
       if (lane == 31) s_warp[0][warp] = incl;
       __syncthreads();
-      uint32_t before = incl - sum;
-      for (int w = 0; w < warp; w++) before += s_warp[0][w];
+      uint32_t before = incl - sum + before_warp(s_warp[0]);
 #pragma unroll
       for (int e = 0; e < PER; e++) {
         if (before < left && left <= before + c[e]) {
           s_bin = kBins - 1 - (tid * PER + e);
           s_left = left - before;
+          s_count = c[e];
         }
         before += c[e];
       }
@@ -135,25 +191,45 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(EvictArgs a, int 
       prefix |= s_bin << shift;
       mask |= bins << shift;
       left = s_left;
-      __syncthreads();
+      if (pass == 0 && s_count <= kListed) {
+        listed = s_count;
+        // counted first, so that the warp takes its place on the list once
+        uint32_t found = 0;
+#pragma unroll 4
+        for (int p = p0 + lane; p < p1; p += 32) {
+          const uint32_t k = key_at(p) & mask;
+          gt += k > prefix;
+          found += k == prefix;
+        }
+        found = __reduce_add_sync(0xffffffffu, found);
+        uint32_t at = 0;
+        if (lane == 0 && found) at = atomicAdd(&s_listed, found);
+        at = __shfl_sync(0xffffffffu, at, 0);
+        walk(p0, p1, [&](int p, uint32_t k, bool in) { return in && (k & mask) == prefix; },
+             [&](int p, uint32_t k, bool put, uint32_t m) {
+               if (put) {
+                 const uint32_t x = at + __popc(m & below);
+                 s_key[x] = k;
+                 s_pos[x] = p;
+               }
+               at += __popc(m);
+             });
+      }
     }
   } else {
-    if (in_smem) {
-      for (int p = tid; p < last; p += THREADS) keys[p] = 0;
-      __syncthreads();
-    }
     prefix = 0xffffffffu;  // above every key (the largest is that of +infinity)
     left = 0;
   }
+  __syncthreads();  // the masses in shared memory; the last sums and the list have been read
 
-  // the kept positions in order: each warp owns a run of candidates
-  const int run = (last + WARPS - 1) / WARPS, p0 = min(last, warp * run), p1 = min(last, p0 + run);
-  uint32_t gt = 0, eq = 0;
-#pragma unroll 2
-  for (int p = p0 + lane; p < p1; p += 32) {
-    const uint32_t k = key_at(p);
-    gt += k > prefix;
-    eq += k == prefix;
+  // larger and equal keys of every warp's run
+  if (!listed) {
+#pragma unroll 4
+    for (int p = p0 + lane; p < p1; p += 32) {
+      const uint32_t k = key_at(p);
+      gt += k > prefix;
+      eq += k == prefix;
+    }
   }
   gt = __reduce_add_sync(0xffffffffu, gt);
   eq = __reduce_add_sync(0xffffffffu, eq);
@@ -162,25 +238,36 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(EvictArgs a, int 
     s_warp[1][warp] = eq;
   }
   __syncthreads();
-  uint32_t gt_before = 0, eq_before = 0;
-  for (int w = 0; w < warp; w++) {
-    gt_before += s_warp[0][w];
-    eq_before += s_warp[1][w];
+  if (listed) {
+    for (uint32_t x = tid; x < listed; x += THREADS)
+      if (s_key[x] >= prefix) atomicAdd(&s_warp[s_key[x] == prefix][s_pos[x] / run], 1u);
+    __syncthreads();
   }
-  const uint32_t below = (1u << lane) - 1;
-#pragma unroll 2
-  for (int p = p0; p < p1; p += 32) {
-    const uint32_t k = p + lane < p1 ? key_at(p + lane) : 0u;
-    const bool g = p + lane < p1 && k > prefix, e = p + lane < p1 && k == prefix;
-    const uint32_t mg = __ballot_sync(0xffffffffu, g), me = __ballot_sync(0xffffffffu, e);
-    const uint32_t rank = eq_before + __popc(me & below);
-    if (g || (e && rank < left)) kept[gt_before + __popc(mg & below) + min(rank, left)] = p + lane;
-    gt_before += __popc(mg);
-    eq_before += __popc(me);
+  uint32_t gt_before = before_warp(s_warp[0]), eq_before = before_warp(s_warp[1]);
+  {
+    walk(p0, p1,
+         [&](int p, uint32_t k, bool in) { return in && k > prefix; },
+         [&](int p, uint32_t k, bool larger, uint32_t mg) {
+           const bool e = p < p1 && k == prefix;
+           const uint32_t me = __ballot_sync(0xffffffffu, e);
+           const uint32_t rank = eq_before + __popc(me & below);
+           if (larger || (e && rank < left)) {
+             const uint32_t j = gt_before + __popc(mg & below) + min(rank, left);
+             kept[j] = p;
+             if (in_smem) out[j] = masses[p];
+           }
+           gt_before += __popc(mg);
+           eq_before += __popc(me);
+         });
   }
-  for (int p = tid; p < a.recent; p += THREADS) kept[take + p] = last + p;
+  for (int p = tid; p < a.recent; p += THREADS) {
+    kept[take + p] = last + p;
+    if (in_smem) out[take + p] = masses[last + p];
+  }
+  if (in_smem) return;
+  // masses that did not fit go with their positions now; the output may be the input,
+  // a chunk is loaded before it is stored
   __syncthreads();  // kept is read below by other threads of the CTA
-  // the masses go with them; the output may be the input, a chunk is loaded before it is stored
   constexpr int U = 4;
 #pragma unroll 1
   for (int j0 = 0; j0 < n; j0 += U * THREADS) {
@@ -201,11 +288,16 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(EvictArgs a, int 
 
 constexpr int kMoveWarps = 8;
 
-// what a warp needs to load its destination block of a chunk: lane r < 16 has row r's
-struct MoveRow {
-  int pos;    // position of the sequence, -1: none
-  int block;  // its cache block, -1: none
-};
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
+// four f16 to E4M3, nearest even, saturating at +-448
+__device__ __forceinline__ uint32_t f16x4_to_e4m3(__half2 lo, __half2 hi) {
+  uint32_t r;
+  asm("{\n .reg .b16 a, b;\n cvt.rn.satfinite.e4m3x2.f16x2 a, %1;\n cvt.rn.satfinite.e4m3x2.f16x2 b, %2;\n "
+      "mov.b32 %0, {a, b};\n}\n"
+      : "=r"(r)
+      : "r"(*reinterpret_cast<uint32_t*>(&lo)), "r"(*reinterpret_cast<uint32_t*>(&hi)));
+  return r;
+}
 
 __device__ __forceinline__ void move_barrier(int cluster) {
   if (cluster > 1)
@@ -214,10 +306,17 @@ __device__ __forceinline__ void move_barrier(int cluster) {
     __syncthreads();
 }
 
+// rows in flight per warp, in chunks of a destination block each
+constexpr int kMoveAhead = 2;
 template <int D>
-__global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(EvictArgs a, int cluster) {
+constexpr int kMoveSmem = kMoveWarps * (kMoveAhead + 1) * 16 * D;
+
+template <int D>
+__global__ void __launch_bounds__(kMoveWarps * 32, D <= 128 ? 4 : 2) evict_move_kernel(EvictArgs a, int cluster) {
   constexpr int CH = D / 16;   // 16-byte chunks per row
   constexpr int PER = D / 32;  // chunks per lane (16 rows)
+  constexpr int SLOTS = kMoveAhead + 1;
+  extern __shared__ __align__(16) uint8_t srows[];  // [warp][SLOTS][16 rows]; a lane reads what it copied
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -237,9 +336,9 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(EvictArgs a
   const int64_t row_bytes = (int64_t)a.num_kv_heads * D;
   const int step = kMoveWarps * cluster;  // blocks per chunk
   const int b0 = rank * kMoveWarps + warp;
+  uint8_t* const ring = srows + warp * SLOTS * 16 * D;
 
-  // the pipeline: positions two chunks ahead, their blocks and the destination
-  // one ahead, then the rows
+  // the pipeline, by chunk: positions, a chunk later their blocks, then the rows
   auto position = [&](int b) { return lane < 16 && b * 16 + lane < n ? kept[b * 16 + lane] : -1; };
   auto block_of = [&](int pos) {
     int blk = -1;
@@ -253,96 +352,101 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(EvictArgs a
     return blk;
   };
   auto target = [&](int b) { return b < nblk ? into[b] : -1; };
-  struct Rows {
-    uint4 x[PER];
-    float scale;  // lane r < 16: the scale of row r's block; 0: the row is zeros
-  };
-  auto load = [&](const MoveRow& m, Rows& r) {
-    r.scale = 0.f;
-    if (m.block >= 0) {
-      const float s = *const_cast<const volatile float*>(scales + (int64_t)m.block * a.num_kv_heads);
-      if (fp8_scale_exponent(s) <= kFp8MaxExp) r.scale = s;
-    }
+  // the rows' copies, and of lane r < 16 the scale of row r's block
+  auto load = [&](int pos, int block, int slot) {
+    float s = 0.f;
+    if (block >= 0) s = *const_cast<const volatile float*>(scales + (int64_t)block * a.num_kv_heads);
 #pragma unroll
     for (int j = 0; j < PER; j++) {
       const int c = lane + 32 * j, row = c / CH, col = c - row * CH;
-      const int blk = __shfl_sync(0xffffffffu, m.block, row), pos = __shfl_sync(0xffffffffu, m.pos, row);
-      r.x[j] = make_uint4(0, 0, 0, 0);
-      if (blk >= 0)
-        r.x[j] = __ldcg(reinterpret_cast<const uint4*>(codes + ((int64_t)blk * 16 + (pos & 15)) * row_bytes + col * 16));
+      const int blk = __shfl_sync(0xffffffffu, block, row), p = __shfl_sync(0xffffffffu, pos, row);
+      const uint8_t* src = codes + (blk >= 0 ? ((int64_t)blk * 16 + (p & 15)) * row_bytes + col * 16 : 0);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_addr(ring + slot * 16 * D + c * 16)), "l"(src),
+                   "r"(blk >= 0 ? 16 : 0));
     }
+    cp_async_commit();
+    return s;
   };
 
-  MoveRow m0{position(b0), -1};
-  m0.block = block_of(m0.pos);
-  MoveRow m1{position(b0 + step), -1};
-  int to = target(b0), to1 = target(b0 + step);
-  Rows r;
-  load(m0, r);
-  m1.block = block_of(m1.pos);
-  int pos2 = position(b0 + 2 * step);
+  // chunks now, next, and the one after, whose rows are not yet under way
+  int pos0 = position(b0), pos1 = position(b0 + step), pos2 = position(b0 + 2 * step), pos3 = position(b0 + 3 * step);
+  int blk0 = block_of(pos0), blk1 = block_of(pos1);
+  int to0 = target(b0), to1 = target(b0 + step);
+  float sc0 = load(pos0, blk0, 0);
+  int blk2 = block_of(pos2);
+  float sc1 = load(pos1, blk1, 1);
+  int slot = 0;
 #pragma unroll 1
   for (int c0 = 0; c0 < nblk; c0 += step) {
     const int b = c0 + b0;
+    const float sc2 = load(pos2, blk2, slot == 0 ? 2 : slot - 1);
+    const int blk3 = block_of(pos3), to2 = target(b + 2 * step), pos4 = position(b + 4 * step);
+    cp_async_wait<kMoveAhead>();  // this chunk's rows
     // ---- the block's largest magnitude, and with it every load of the chunk ----
+    const float scale = fp8_scale_exponent(sc0) <= kFp8MaxExp ? sc0 : 0.f;  // 0: the row is zeros
+    uint4 x[PER];
     float rs[PER];
     uint32_t top = 0;
 #pragma unroll
     for (int j = 0; j < PER; j++) {
       const int row = (lane + 32 * j) / CH;
-      rs[j] = __shfl_sync(0xffffffffu, r.scale, row);
-      if (rs[j] == 0.f) r.x[j] = make_uint4(0, 0, 0, 0);
-      const uint32_t m = __vmaxu4(__vmaxu4(r.x[j].x & 0x7f7f7f7fu, r.x[j].y & 0x7f7f7f7fu),
-                                  __vmaxu4(r.x[j].z & 0x7f7f7f7fu, r.x[j].w & 0x7f7f7f7fu));
-      uint32_t code = max(max(m & 0xffu, (m >> 8) & 0xffu), max((m >> 16) & 0xffu, m >> 24));
-      code = min(code, 0x7eu);  // a NaN code takes no part
-      const uint32_t f = e4m3x2_to_f16x2(code);
-      top = max(top, __float_as_uint(__half2float(__ushort_as_half((unsigned short)(f & 0xffffu))) * rs[j]));
+      rs[j] = __shfl_sync(0xffffffffu, scale, row);
+      x[j] = *reinterpret_cast<const uint4*>(ring + slot * 16 * D + (lane + 32 * j) * 16);
+      if (rs[j] == 0.f) x[j] = make_uint4(0, 0, 0, 0);
+      // code magnitudes order as integers: even and odd bytes as 16-bit lanes
+      const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < 4; e++) m = __vmaxu2(m, __vmaxu2(w[e] & 0x007f007fu, (w[e] >> 8) & 0x007f007fu));
+      m = min(max(m & 0xffffu, m >> 16), 0x7eu);  // a NaN code counts as the largest number
+      top = max(top, __float_as_uint(__half2float(__low2half(as_half2(e4m3x2_to_f16x2(m)))) * rs[j]));
     }
     top = __reduce_max_sync(0xffffffffu, top);
     // smallest k in range with top <= 448 2^k = 1.75 2^(8 + k)
     const int k = min(max((int)(top >> 23) - 127 - 8 + ((top & 0x7fffffu) > 0x600000u), kFp8MinExp), kFp8MaxExp);
-    const int pos_of_row = m0.pos;
-    Rows next;
-    load(m1, next);
-    const int blk2 = block_of(pos2), to2 = target(b + 2 * step), pos3 = position(b + 3 * step);
     move_barrier(cluster);  // every row of this chunk has been read
     // rows that all stay where they are are left alone
-    const bool here = __all_sync(0xffffffffu, pos_of_row < 0 || (pos_of_row == b * 16 + lane && m0.block == to));
+    const bool here = __all_sync(0xffffffffu, pos0 < 0 || (pos0 == b * 16 + lane && blk0 == to0));
     if (b < nblk && !here) {
-      if (to < 0 || to >= a.num_blocks) {
+      if (to0 < 0 || to0 >= a.num_blocks) {
         if (lane == 0) flag(a.dev_status, KV_INT4_DEV_BAD_BLOCK);
       } else {
-        uint8_t* const dst = codes + (int64_t)to * 16 * row_bytes;
+        uint8_t* const dst = codes + (int64_t)to0 * 16 * row_bytes;
 #pragma unroll
         for (int j = 0; j < PER; j++) {
           const int c = lane + 32 * j, row = c / CH, col = c - row * CH;
-          if (b * 16 + row >= n) continue;
-          const int shift = rs[j] == 0.f ? 0 : exp_of(rs[j]) - k;
+          // Codes * 2^shift in f16, exact wherever the code that comes out depends on it:
+          // below 2^-24 all become zeros; a row that needs more than 2^15 has codes of
+          // 2^-7 at most, and takes two steps
+          uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+          const int shift = rs[j] == 0.f ? 0 : max(exp_of(rs[j]) - k, -24);
           if (shift != 0) {
-            const float f = exp2_int(shift);
-            uint32_t* w = reinterpret_cast<uint32_t*>(&r.x[j]);
+            const __half2 s0 = __float2half2_rn(exp2_int(min(shift, 15)));
+            const __half2 s1 = __float2half2_rn(exp2_int(min(max(shift - 15, 0), 15)));
 #pragma unroll
             for (int e = 0; e < 4; e++) {
               uint32_t lo, hi;
               e4m3x4_to_f16x2(w[e], lo, hi);
-              const float2 p0 = __half22float2(*reinterpret_cast<__half2*>(&lo));
-              const float2 p1 = __half22float2(*reinterpret_cast<__half2*>(&hi));
-              w[e] = f32x4_to_e4m3(p0.x * f, p0.y * f, p1.x * f, p1.y * f);
+              __half2 l2 = __hmul2(as_half2(lo), s0), h2 = __hmul2(as_half2(hi), s0);
+              if (shift > 15) {
+                l2 = __hmul2(l2, s1);
+                h2 = __hmul2(h2, s1);
+              }
+              w[e] = f16x4_to_e4m3(l2, h2);
             }
           }
-          *reinterpret_cast<uint4*>(dst + row * row_bytes + col * 16) = r.x[j];
+          if (b * 16 + row < n) *reinterpret_cast<uint4*>(dst + row * row_bytes + col * 16) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        if (lane == 0) scales[(int64_t)to * a.num_kv_heads] = exp2_int(k);
+        if (lane == 0) scales[(int64_t)to0 * a.num_kv_heads] = exp2_int(k);
       }
     }
-    r = next;
-    m0 = m1;
-    m1 = MoveRow{pos2, blk2};
-    pos2 = pos3;
-    to = to1;
-    to1 = to2;
+    pos0 = pos1, pos1 = pos2, pos2 = pos3, pos3 = pos4;
+    blk0 = blk1, blk1 = blk2, blk2 = blk3;
+    to0 = to1, to1 = to2;
+    sc0 = sc1, sc1 = sc2;
+    slot = slot + 1 == SLOTS ? 0 : slot + 1;
   }
+  cp_async_wait<0>();
 }
 
 template <int D>
@@ -350,28 +454,29 @@ int launch_t(const EvictArgs& a, cudaStream_t stream) {
   const int dev = current_device();
   const int sms = sm_count(dev);
   const int64_t pairs = (int64_t)a.num_seqs * a.num_kv_heads;
-  // few masses: small CTAs (their barriers cost less), many: one CTA's threads share the passes
   const int most = a.mass_len < (int64_t)a.max_blocks_per_seq * 16 ? a.mass_len : a.max_blocks_per_seq * 16;
   const int cached = most < kCachedMasses ? most : kCachedMasses;
-  const size_t smem = (size_t)(kCopies * kBins + cached) * 4;
-  constexpr int kMostSmem = (kCopies * kBins + kCachedMasses) * 4;
   static PerContext<int> attr;
   int set = 0;
   if (!attr.get(dev, [](int* v) {
         *v = 1;
-        return cudaFuncSetAttribute(evict_select_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem) == cudaSuccess &&
-               cudaFuncSetAttribute(evict_select_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem) == cudaSuccess;
+        auto most_smem = [](auto kern, size_t bytes) {
+          return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+        };
+        return most_smem(evict_move_kernel<D>, kMoveSmem<D>) && most_smem(evict_select_kernel<256>, Select<256>::smem(kCachedMasses)) &&
+               most_smem(evict_select_kernel<512>, Select<512>::smem(kCachedMasses));
       }, &set))
     return KV_INT4_ERR_CUDA;
-  int e = launch_pdl(most <= 2048 ? evict_select_kernel<256> : evict_select_kernel<1024>, dim3((unsigned)pairs),
-                     most <= 2048 ? 256 : 1024, smem, stream, 1, a, cached);
+  const bool small = most <= 2048;
+  int e = launch_pdl(small ? evict_select_kernel<256> : evict_select_kernel<512>, dim3((unsigned)pairs), small ? 256 : 512,
+                     small ? Select<256>::smem(cached) : Select<512>::smem(cached), stream, 1, a, cached);
   if (e) return e;
   // as many CTAs per task as run at once and have a block per warp
   const int64_t tasks = 2 * pairs;
   const int64_t blocks = ((int64_t)(a.budget < most ? a.budget : most) + 15) / 16;
   int cluster = 1;
   while (cluster < 8 && 2 * tasks * cluster <= 2ll * sms && blocks > (int64_t)kMoveWarps * cluster) cluster *= 2;
-  return launch_pdl(evict_move_kernel<D>, dim3((unsigned)(tasks * cluster)), kMoveWarps * 32, 0, stream, cluster, a, cluster);
+  return launch_pdl(evict_move_kernel<D>, dim3((unsigned)(tasks * cluster)), kMoveWarps * 32, kMoveSmem<D>, stream, cluster, a, cluster);
 }
 
 }  // namespace
