@@ -30,7 +30,7 @@ namespace {
 
 #include "attention_fp8.cuh"
 
-constexpr int kMergeWarps = 16;  // per CTA; two such CTAs per SM
+constexpr int kMergeWarps = 16;  // per CTA, and about per SM over all CTAs
 
 struct SharedMergeParams {
   Common c;
@@ -40,74 +40,92 @@ struct SharedMergeParams {
   int lanes;     // warps per row
   int parts;     // CTAs per (sequence, kv head), cols rows each and in turn
   int slot;      // columns of a result slot
+  bool prefill;  // whether there was a prefill launch
 };
 
-// The decode pieces of virtual sequence record i of dseq and a kv head: the
-// direct slot (the piece that starts the segment), then every CTA whose range is
-// not empty and starts strictly inside it; candidates are those CTAs or the
-// positions, whichever are fewer (as merge_fp8_kernel finds them)
-struct DecodePieces {
+// The results of a virtual sequence for one kv head: pieces of the decode launch,
+// of split prefill tiles, or whole tiles' rows
+struct Results {
+  int kind;         // 0 nothing, 1 decode, 2 prefill
+  int index;        // in dseq; first tile
+  int ql, first;    // query tokens, first row-buffer token (-1: whole tiles went out by themselves)
+  // decode: the direct slot (the piece that starts the segment), then every CTA whose
+  // range is not empty and starts strictly inside it; candidates are those CTAs or
+  // the positions, whichever are fewer (as merge_fp8_kernel finds them)
   long long seg, sbeg, Tu, w_first;
   int cand, W, lane_g, hl;
   bool by_cta;
-  __device__ void find(const Common& c, const PlanView& pv, int num_ctas, int i, int h) {
-    const int n_dseq = pv.plan[0];
-    const int npos = ((pv.dseq[i].y + 15) / 16 + c.np - 1) / c.np;
+
+  __device__ void find(const Common& c, const PlanView& pv, int num_ctas, int2 info, int4 rec, int4 rec2, int n_dseq,
+                       int n_items, int h) {
+    kind = info.x == 2 && n_items == 0 ? 0 : info.x;  // more tiles than the workspace holds: none was worked on
+    index = info.y;
+    ql = rec.y;
+    first = rec2.z;
+    cand = 0;
+    if (kind != 1) return;
+    const long long all = pv.dprefix[n_dseq], mine = pv.dprefix[index];
+    const int npos = ((rec.z + 15) / 16 + c.np - 1) / c.np;
     const int grp = h / c.hg, gpl = c.ng / c.nl, gs = grp / c.nl;
     hl = h - grp * c.hg;
     lane_g = grp % c.nl;
-    seg = (long long)i * c.hkv + h;
-    Tu = pv.dprefix[n_dseq] * gpl;
-    sbeg = pv.dprefix[i] * gpl + (long long)gs * npos;
+    seg = (long long)index * c.hkv + h;
+    Tu = all * gpl;
+    sbeg = mine * gpl + (long long)gs * npos;
     W = num_ctas / c.nl;
     w_first = div_nn((sbeg + 1) * W + Tu - 1, Tu);
     const long long w_end = div_nn((sbeg + npos) * W + Tu - 1, Tu);
     by_cta = w_end - w_first <= npos - 1;
     cand = 1 + (int)(by_cta ? w_end - w_first : (long long)npos - 1);
   }
-  // candidate k's result slot, false if there is none: direct ones first
-  __device__ __forceinline__ bool slot(const Common& c, int k, long long* at) const {
-    if (k == 0) {
-      *at = seg;
-      return true;
-    }
-    long long w;
-    bool ok;
-    if (by_cta) {
-      w = w_first + k - 1;
-      ok = div_nn(Tu * (w + 1), W) > div_nn(Tu * w, W);
-    } else {
-      const long long p = sbeg + k;
-      w = div_nn((p + 1) * W + Tu - 1, Tu) - 1;
-      ok = div_nn(Tu * w, W) == p;
-    }
-    *at = (w * c.nl + lane_g) * c.hg + hl;
-    return ok;
-  }
-};
-
-// a virtual sequence's results, for one kv head
-struct Results {
-  int kind, index;  // of vinfo
-  int ql, first;    // query tokens, first row-buffer token
-  DecodePieces dec;
-  __device__ void find(const Common& c, const PlanView& pv, int num_ctas, int v, int h) {
-    const int2 x = pv.vinfo[v];
-    kind = x.x == 2 && pv.plan[1] == 0 ? 0 : x.x;  // more tiles than the workspace holds: none was worked on
-    index = x.y;
-    ql = pv.vrec[2 * v].y;
-    first = pv.vrec[2 * v + 1].z;
-    if (kind == 1) dec.find(c, pv, num_ctas, index, h);
-  }
-  // its pieces for token j of the virtual sequence; 0 where a whole tile went out by itself
+  // its tile that holds token j, and the pieces of a row of that token
   __device__ __forceinline__ int pieces(const Common& c, const PlanView& pv, int j, int2* tile) const {
-    if (kind == 1) return dec.cand;
+    if (kind == 1) return cand;
     if (kind != 2) return 0;
     *tile = pv.tloc[index + j / c.tile_tokens];
     return tile->y > 1 || first >= 0 ? tile->y : 0;
   }
+  // piece k of token j's row jj (q head of the group): its values and (maximum, sum); null for none
+  __device__ __forceinline__ const float* piece(const Common& c, const PlanView& pv, int D, int slot, int2 tile, int h, int j,
+                                                int jj, int k, int sub, const float** ml) const {
+    const float *o, *m;
+    long long at;
+    if (kind == 1) {
+      o = k == 0 ? pv.direct_o : pv.warp_o;
+      m = k == 0 ? pv.direct_ml : pv.warp_ml;
+      at = seg;
+      if (k > 0) {
+        long long w;
+        if (by_cta) {
+          w = w_first + k - 1;
+          if (div_nn(Tu * (w + 1), W) <= div_nn(Tu * w, W)) return nullptr;
+        } else {
+          const long long p = sbeg + k;
+          w = div_nn((p + 1) * W + Tu - 1, Tu) - 1;  // last CTA starting at or before p
+          if (div_nn(Tu * w, W) != p) return nullptr;
+        }
+        at = (w * c.nl + lane_g) * c.hg + hl;
+      }
+      at = at * slot + j * c.group + jj + sub * c.dcols;
+    } else if (tile.y > 1) {
+      const int tok = j / c.tile_tokens * c.tile_tokens, R = min(c.tile_tokens, ql - tok) * c.group;
+      at = tile.x + ((long long)h * tile.y + k) * R + (j - tok) * c.group + jj;
+      o = pv.piece_o;
+      m = pv.piece_ml;
+    } else {
+      at = (long long)(first + j) * c.hq + h * c.group + jj;
+      o = pv.row_o;
+      m = pv.row_ml;
+    }
+    *ml = m + 2 * at;
+    return o + at * D;
+  }
 };
 
+// A row's pieces: a lane finds one and loads its maximum and sum, the warp knows the
+// row's maximum and every weight then, and the values are added in the pieces'
+// order with several loads under way (a piece at a time, each waiting for its own
+// weight, took 16 us instead of the 5 for 64 sequences over one prefix).
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) merge_shared_kernel(SharedMergeParams prm) {
   const Common& c = prm.c;
@@ -115,24 +133,28 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_shared_kernel(SharedMe
   extern __shared__ __align__(16) float spart[];  // [cols][lanes][D + 2]
   pdl_trigger();
   pdl_wait();
-  constexpr int PER = D / 32;
+  constexpr int PER = D / 32, VEC = D % 128 == 0 ? 4 : D % 64 == 0 ? 2 : 1;  // values a lane has side by side
+  auto element = [](int lane, int e) { return (lane + 32 * (e / VEC)) * VEC + e % VEC; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pl = warp / prm.cols, lcol = warp - pl * prm.cols;
   const int seg = blockIdx.x / prm.parts, part = blockIdx.x - seg * prm.parts;
   const int s = seg / c.hkv, h = seg - s * c.hkv, v = c.sh.num_groups + s;
-  const int4 rec = pv.vrec[2 * v];
-  const int g = pv.vrec[2 * v + 1].w;
-  const int q0 = rec.x, ql = rec.y;
+  const int4 rec = pv.vrec[2 * v], rec2 = pv.vrec[2 * v + 1];
+  const int2 info = pv.vinfo[v];
+  const int n_dseq = pv.plan[0], n_items = prm.prefill ? pv.plan[1] : 0;
+  const int g = rec2.w, q0 = rec.x, ql = rec.y;
   if (ql == 0) return;
   Results own, pre;
-  own.find(c, pv, prm.num_ctas, v, h);
   pre.kind = 0;
   int off = 0;  // the sequence's first token in its group
   if (g >= 0) {
-    pre.find(c, pv, prm.num_ctas, g, h);
-    off = q0 - pv.vrec[2 * g].x;
+    const int4 grec = pv.vrec[2 * g], grec2 = pv.vrec[2 * g + 1];
+    pre.find(c, pv, prm.num_ctas, pv.vinfo[g], grec, grec2, n_dseq, n_items, h);
+    off = q0 - grec.x;
   }
-  const int nsub = c.np == 2 ? 2 : 1;  // paired blocks: columns col and col + dcols hold the same query
+  own.find(c, pv, prm.num_ctas, info, rec, rec2, n_dseq, n_items, h);
+  // paired blocks: columns col and col + dcols of a decode piece hold the same query
+  const int own_subs = own.kind == 1 && c.np == 2 ? 2 : 1, pre_subs = pre.kind == 1 && c.np == 2 ? 2 : 1;
 #pragma unroll 1
   for (int c0 = part * prm.cols; c0 < ql * c.group; c0 += prm.parts * prm.cols) {
     const int col = c0 + lcol;
@@ -140,64 +162,62 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_shared_kernel(SharedMe
     float acc[PER], M = -INFINITY, Ls = 0.f;
 #pragma unroll
     for (int k = 0; k < PER; k++) acc[k] = 0.f;
-    auto merge = [&](float m, float l, const float (&o)[PER]) {
-      const float mn = fmaxf(M, m);
-      const float mu = mn == -INFINITY ? 0.f : mn;
-      const Exp2Pair ea(M - mu), eb(m - mu);
-      const float a = ea.both(), b = eb.both();
-#pragma unroll
-      for (int k = 0; k < PER; k++) acc[k] = acc[k] * a + o[k] * b;
-      Ls = ea.of(Ls) + eb.of(l);
-      M = mn;
-    };
     int2 own_tile = make_int2(0, 0), pre_tile = make_int2(0, 0);
     int n_own = 0, n_pre = 0;
     if (col < ql * c.group) {
-      n_own = own.pieces(c, pv, j, &own_tile);
-      if (g >= 0) n_pre = pre.pieces(c, pv, j + off, &pre_tile);
+      if (g >= 0) n_pre = pre.pieces(c, pv, j + off, &pre_tile) * pre_subs;
+      n_own = own.pieces(c, pv, j, &own_tile) * own_subs;
     }
-#pragma unroll 2
-    for (int k = pl; k < n_own + n_pre; k += prm.lanes) {
-      const bool mine = k >= n_pre;  // the prefix's pieces first
-      const Results& x = mine ? own : pre;
-      const int kk = mine ? k - n_pre : k, jx = mine ? j : j + off;
-      const float *o, *ml;
-      bool ok = true;
-      int subs = 1, sub_step = 0;
-      if (x.kind == 1) {
-        long long at;
-        ok = x.dec.slot(c, kk, &at);
-        at = at * prm.slot + jx * c.group + jj;
-        o = (kk == 0 ? pv.direct_o : pv.warp_o) + at * D;
-        ml = (kk == 0 ? pv.direct_ml : pv.warp_ml) + at * 2;
-        subs = nsub;
-        sub_step = c.dcols;
-      } else {
-        const int2 tile = mine ? own_tile : pre_tile;
-        if (tile.y > 1) {
-          const int t = jx / c.tile_tokens, tok = t * c.tile_tokens;
-          const int R = min(c.tile_tokens, x.ql - tok) * c.group;
-          const long long at = tile.x + ((long long)h * tile.y + kk) * R + (jx - tok) * c.group + jj;
-          o = pv.piece_o + at * D;
-          ml = pv.piece_ml + at * 2;
-        } else {
-          const long long at = (long long)(x.first + jx) * c.hq + h * c.group + jj;
-          o = pv.row_o + at * D;
-          ml = pv.row_ml + at * 2;
+    const int n = n_pre + n_own;  // the prefix's first
+#pragma unroll 1
+    for (int k0 = pl; k0 < n; k0 += 32 * prm.lanes) {
+      const int k = k0 + prm.lanes * lane;
+      const float *o = nullptr, *ml = nullptr;
+      if (k < n_pre) o = pre.piece(c, pv, D, prm.slot, pre_tile, h, j + off, jj, k / pre_subs, k % pre_subs, &ml);
+      else if (k < n) o = own.piece(c, pv, D, prm.slot, own_tile, h, j, jj, (k - n_pre) / own_subs, (k - n_pre) % own_subs, &ml);
+      float2 x = make_float2(-INFINITY, 0.f);
+      if (o) x = *reinterpret_cast<const float2*>(ml);
+      float mn = x.x;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, d));
+      mn = fmaxf(M, mn);
+      const float mu = mn == -INFINITY ? 0.f : mn;
+      const Exp2Pair ea(M - mu), eb(x.x - mu);
+      const float scale = ea.both(), w = o ? eb.both() : 0.f;
+      const float l = o ? eb.of(x.y) : 0.f;
+      M = mn;
+      Ls = ea.of(Ls);
+#pragma unroll
+      for (int e = 0; e < PER; e++) acc[e] *= scale;
+      const uint32_t there = __ballot_sync(0xffffffffu, o != nullptr);
+      if (!there) continue;
+      // absent pieces read the first one there with a weight of 0 (its values are finite)
+      const unsigned long long some = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), __ffs(there) - 1);
+      const unsigned long long mine = o ? reinterpret_cast<unsigned long long>(o) : some;
+      const int count = 32 - __clz(there);
+#pragma unroll 4
+      for (int kk = 0; kk < count; kk++) {
+        const float* src = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, mine, kk));
+        const float a = __shfl_sync(0xffffffffu, w, kk);
+        Ls += __shfl_sync(0xffffffffu, l, kk);
+        float val[PER];
+#pragma unroll
+        for (int e = 0; e < PER; e += VEC) {
+          const float* p = src + element(lane, e);
+          if constexpr (VEC == 4) {
+            const float4 y = *reinterpret_cast<const float4*>(p);
+            val[e] = y.x, val[e + 1] = y.y, val[e + 2] = y.z, val[e + 3] = y.w;
+          } else if constexpr (VEC == 2) {
+            const float2 y = *reinterpret_cast<const float2*>(p);
+            val[e] = y.x, val[e + 1] = y.y;
+          } else {
+            val[e] = *p;
+          }
         }
-      }
-      float mw[2], lw[2], ov[2][PER];
+        // a piece without keys holds zeros (or nothing that its weight of 0 may meet)
 #pragma unroll
-      for (int sub = 0; sub < 2; sub++) {
-        const bool use = ok && sub < subs;
-        const float2 w = use ? *reinterpret_cast<const float2*>(ml + 2 * sub * sub_step) : make_float2(-INFINITY, 0.f);
-        mw[sub] = w.x;
-        lw[sub] = w.y;
-#pragma unroll
-        for (int e = 0; e < PER; e++) ov[sub][e] = use ? o[sub * sub_step * D + lane + 32 * e] : 0.f;
+        for (int e = 0; e < PER; e++) acc[e] = a == 0.f ? acc[e] : fmaf(val[e], a, acc[e]);
       }
-      merge(mw[0], lw[0], ov[0]);
-      if (subs > 1) merge(mw[1], lw[1], ov[1]);
     }
     if (prm.lanes > 1) {
       float* mine = spart + (lcol * prm.lanes + pl) * (D + 2);
@@ -214,20 +234,31 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_shared_kernel(SharedMe
 #pragma unroll 1
         for (int p = 1; p < prm.lanes; p++) {
           const float* o = mine + p * (D + 2);
-          float x[PER];
+          const float m = o[D], mn = fmaxf(M, m), mu = mn == -INFINITY ? 0.f : mn;
+          const Exp2Pair ea(M - mu), eb(m - mu);
+          const float a = ea.both(), b = eb.both();
 #pragma unroll
-          for (int k = 0; k < PER; k++) x[k] = o[lane + 32 * k];
-          merge(o[D], o[D + 1], x);
+          for (int k = 0; k < PER; k++) acc[k] = acc[k] * a + o[lane + 32 * k] * b;
+          Ls = ea.of(Ls) + eb.of(o[D + 1]);
+          M = mn;
         }
       }
       __syncthreads();  // read before the next rows' are written
     }
-    if (pl > 0 || n_own + n_pre == 0) continue;
+    if (pl > 0 || n == 0) continue;
     const float inv = Ls == 0.f ? 0.f : 1.f / Ls;  // no visible key: zeros
     uint16_t* dst = c.out + (long long)(q0 + j) * c.out_stride + (long long)(h * c.group + jj) * D;
 #pragma unroll
-    for (int k = 0; k < PER; k++)
-      dst[lane + 32 * k] = (uint16_t)(pack_bf16x2_rn(acc[k] * inv, 0.f) & 0xffffu);
+    for (int e = 0; e < PER; e += VEC) {
+      uint16_t* p = dst + element(lane, e);
+      if constexpr (VEC == 4)
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2_rn(acc[e] * inv, acc[e + 1] * inv),
+                                                  pack_bf16x2_rn(acc[e + 2] * inv, acc[e + 3] * inv));
+      else if constexpr (VEC == 2)
+        *reinterpret_cast<uint32_t*>(p) = pack_bf16x2_rn(acc[e] * inv, acc[e + 1] * inv);
+      else
+        *p = (uint16_t)(pack_bf16x2_rn(acc[e] * inv, 0.f) & 0xffffu);
+    }
     if (c.sh.lse && lane == 0) c.sh.lse[(q0 + j) * c.sh.lse_stride + h * c.group + jj] = log_sum_exp(M, Ls);
   }
 }
@@ -382,14 +413,14 @@ int launch_t(const SharedAttnArgs& s, cudaStream_t stream) {
   }
   // merge: CTAs per (sequence, kv head), a warp per row and piece lane, lanes as
   // far as all CTAs start at once
-  const long long segs = (long long)a.num_seqs * a.num_kv_heads, warps = 2ll * kMergeWarps * sms;
+  const long long segs = (long long)a.num_seqs * a.num_kv_heads, warps = (long long)kMergeWarps * sms;
   int mcols = (int)(most_own < 8 ? most_own : 8), parts = 1, lanes = 1;
   while ((long long)mcols * parts < most_own && segs * parts * mcols < warps) parts *= 2;
   while (mcols * lanes * 2 <= kMergeWarps && 2ll * lanes * mcols * parts * segs <= warps) lanes *= 2;
   if (segs * parts > 0x7fffffff) return KV_INT4_ERR_SIZE;
   timing_begin(kTimedReduce, stream);
   const int e = launch_pdl(merge_shared_kernel<D>, dim3((unsigned)(segs * parts)), mcols * lanes * 32, merge_smem<D>(mcols, lanes),
-                           stream, 1, SharedMergeParams{c, pv, dec_grid, mcols, lanes, parts, kDecodeCols * cg});
+                           stream, 1, SharedMergeParams{c, pv, dec_grid, mcols, lanes, parts, kDecodeCols * cg, may_prefill});
   timing_end(kTimedReduce, stream);
   return e;
 }
