@@ -32,6 +32,14 @@ namespace {
 
 constexpr int kMergeWarps = 16;  // per CTA, and about per SM over all CTAs
 
+#include "few_ws_fp8.cuh"
+
+// query columns of a group up to which its prefix is the decode kernel's: more are
+// the tensor cores', in tiles of few rows (up to 64) or of many.  Head sizes above 128
+// have no tiles of few rows.
+template <int D>
+constexpr int kMostGroupCols = D <= 128 ? kDecodeCols : kDecodeColsFp8;
+
 struct SharedMergeParams {
   Common c;
   PlanView pv;
@@ -306,47 +314,102 @@ int launch_t(const SharedAttnArgs& s, cudaStream_t stream) {
   c.max_items = L.base.max_pairs * a.num_kv_heads;
   c.sh = SharedArgs{s.group_start, s.prefix_lens, s.num_groups, s.max_group_tokens, L.row_tokens, Fp8Ws<D>::ROWS, 64,
                     s.lse, s.lse_stride};
+  // f with blocks per position, warps per head and column groups per warp as constants
+  using std::integral_constant;
+  constexpr int kWide = D <= 128 ? 4 : 2;  // most column groups per warp: registers allow them
   auto with_np = [](int np, int cg, auto&& f) {
-    using std::integral_constant;
-    if (np == 2) return f(integral_constant<int, 2>{}, integral_constant<int, 1>{});
-    if (np == 4) return f(integral_constant<int, kFp8Quad<D> ? 4 : 2>{}, integral_constant<int, 1>{});
-    if (cg == 2) return f(integral_constant<int, 1>{}, integral_constant<int, 2>{});
-    if (cg == 4) return f(integral_constant<int, 1>{}, integral_constant<int, 4>{});
-    return f(integral_constant<int, 1>{}, integral_constant<int, 1>{});
+    using One = integral_constant<int, 1>;
+    using Two = integral_constant<int, 2>;
+    if (np == 2) return f(Two{}, One{}, One{});
+    if (np == 4) return f(integral_constant<int, kFp8Quad<D> ? 4 : 2>{}, One{}, One{});
+    if (cg == 2) return f(One{}, One{}, Two{});
+    if (cg == 4) return f(One{}, integral_constant<int, 4 / kWide>{}, integral_constant<int, kWide>{});
+    return f(One{}, One{}, One{});
   };
+  auto groups_of = [](long long cols) { return cols > 2 * kDecodeCols ? 4 : cols > kDecodeCols ? 2 : 1; };
+  auto blocks_of = [](long long cols) { return cols > 4 ? 1 : cols > 2 || !kFp8Quad<D> ? 2 : 4; };
+  // the largest divisor of Hkv that gives up to four warps of `warps` each and whose
+  // ring leaves room for two CTAs per SM
+  auto heads_of = [&](int warps, auto smem_bytes) {
+    for (int h = 4 / warps; h > 1; h--)
+      if (a.num_kv_heads % h == 0 && 2 * (smem_bytes(h) + 1024) <= 228 * 1024) return h;
+    return 1;
+  };
+  const long long most_own = (long long)(a.max_query_len > 0 ? a.max_query_len : 1) * c.group;
+
+  // one launch of clusters that share nothing where kv_fp8_attention would make it
+  if (most_own <= kDecodeColsFp8) {
+    auto direct = [&](auto np_tag, auto cg_tag) -> int {  // a status, -1: not here
+      constexpr int NP = decltype(np_tag)::value, CG = decltype(cg_tag)::value;
+      using G = Fp8Dec<D, NP>;
+      constexpr auto kern = decode_fp8_kernel<D, NP, CG, true, true>;
+      c.np = NP;
+      c.hg = heads_of(CG, [](int h) { return G::smem_bytes(h); });
+      c.ng = a.num_kv_heads / c.hg;
+      c.dcols = kDecodeCols * CG / NP;
+      static PerContext<int> occ_cache[5];
+      int occ = 0;
+      if (!occ_cache[c.hg].get(dev, [&](int* v) {
+            int unused;  // the attribute is raised once, to the largest ring in use
+            return configure(kern, (228 * 1024) / 2 - 1024, 128, &unused) &&
+                   cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, kern, c.hg * CG * 32, G::smem_bytes(c.hg)) == cudaSuccess &&
+                   *v >= 1;
+          }, &occ))
+        return KV_INT4_ERR_CUDA;
+      const long long tasks = (long long)a.num_seqs * c.ng, room = (long long)sms * occ;
+      const long long table = (long long)a.max_blocks_per_seq * 16;
+      const long long most = ((a.max_seq_len < table ? a.max_seq_len : table) + 16 * NP - 1) / (16 * NP);
+      int cl = 1;
+      while (cl < 8 && 2 * tasks * cl <= room && most > 2 * cl) cl *= 2;
+      if (tasks * cl > room || most > 16 * cl) return -1;
+      timing_begin(kTimedDecode, stream);
+      const int e = launch_pdl(kern, dim3((unsigned)(tasks * cl)), c.hg * CG * 32, G::smem_bytes(c.hg), stream, cl,
+                               Fp8DecParams{c, pv, 0, cl, false});
+      timing_end(kTimedDecode, stream);
+      return e;
+    };
+    using One = integral_constant<int, 1>;
+    const int np = blocks_of(most_own), cg = groups_of(most_own);
+    c.nl = 1;
+    const int e = np == 4   ? direct(integral_constant<int, kFp8Quad<D> ? 4 : 2>{}, One{})
+                  : np == 2 ? direct(integral_constant<int, 2>{}, One{})
+                  : cg == 4 ? direct(One{}, integral_constant<int, 4>{})
+                  : cg == 2 ? direct(One{}, integral_constant<int, 2>{})
+                            : direct(One{}, One{});
+    if (e >= 0) return e;
+  }
+
   // decode, as in kv_fp8_attention; a group's queries count as one sequence's
   c.hg = c.ng = c.nl = c.np = 1;
-  const long long most_own = (long long)(a.max_query_len > 0 ? a.max_query_len : 1) * c.group;
   const long long most_tokens = s.num_groups > 0 && s.max_group_tokens > a.max_query_len ? s.max_group_tokens : a.max_query_len;
   const long long mq = (most_tokens > 0 ? most_tokens : 1) * c.group;
-  const long long cols = mq <= kDecodeColsFp8 ? mq : most_own <= kDecodeColsFp8 ? most_own : c.group;
-  int cg = cols > 2 * kDecodeCols ? 4 : cols > kDecodeCols ? 2 : 1;
+  const long long cols = mq <= kMostGroupCols<D> ? mq : most_own <= kDecodeColsFp8 ? most_own : c.group;
+  int cg = groups_of(cols);
   const long long virt = (long long)a.num_seqs + s.num_groups;
   while (cg > 1 && virt * a.num_kv_heads * kDecodeCols * cg > L.base.direct_rows) cg /= 2;
   const bool any_decode = c.group <= kDecodeCols * cg;
-  int dec_grid = 0, dec_occ = 0;
+  const int np = blocks_of(cols);
+  int dec_grid = 0;
   if (any_decode) {
-    static PerContext<int> occ_cache[5][5];
-    auto take = [&](auto np_tag, auto cg_tag) {
-      constexpr int NP = decltype(np_tag)::value, CG = decltype(cg_tag)::value;
+    int occ = 0;
+    auto take = [&](auto np_tag, auto cg_tag, auto gw_tag) {
+      constexpr int NP = decltype(np_tag)::value, CG = decltype(cg_tag)::value, GW = decltype(gw_tag)::value;
       using G = Fp8Dec<D, NP>;
+      constexpr auto kern = decode_fp8_kernel<D, NP, CG, false, true, GW>;
       c.np = NP;
-      for (int h = 4 / CG; h >= 1; h--)
-        if (a.num_kv_heads % h == 0 && (h == 1 || 2 * (G::smem_bytes(h) + 1024) <= 228 * 1024)) {
-          c.hg = h;
-          break;
-        }
-      return occ_cache[NP == 1 ? CG / 2 : NP / 2 + 2][c.hg].get(dev, [&](int* v) {
+      c.hg = heads_of(CG, [](int h) { return G::smem_bytes(h, h * CG, GW); });
+      static PerContext<int> occ_cache[5];
+      return occ_cache[c.hg].get(dev, [&](int* v) {
         int unused;
-        return configure(decode_fp8_kernel<D, NP, CG, true, true>, (228 * 1024) / 2 - 1024, 128, &unused) &&
-               configure(decode_fp8_kernel<D, NP, CG, false, true>, (228 * 1024) / 2 - 1024, 128, &unused) &&
-               cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, decode_fp8_kernel<D, NP, CG, false, true>, c.hg * CG * 32,
-                                                             G::smem_bytes(c.hg)) == cudaSuccess && *v >= 1;
-      }, &dec_occ);
+        return configure(kern, (228 * 1024) / 2 - 1024, 128, &unused) &&
+               cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, kern, c.hg * CG * 32, G::smem_bytes(c.hg, c.hg * CG, GW)) ==
+                   cudaSuccess &&
+               *v >= 1;
+      }, &occ);
     };
-    if (!with_np(cols > 4 ? 1 : cols > 2 || !kFp8Quad<D> ? 2 : 4, cg, take)) return KV_INT4_ERR_CUDA;
+    if (!with_np(np, cg, take)) return KV_INT4_ERR_CUDA;
     c.ng = a.num_kv_heads / c.hg;
-    long long grid = (long long)sms * dec_occ;
+    long long grid = (long long)sms * occ;
     if (grid * c.hg * cg > kMaxDecodeWarps) grid = kMaxDecodeWarps / (c.hg * cg);
     for (int l = (int)(grid < c.ng ? grid : c.ng); l >= 1; l--)
       if (c.ng % l == 0) {
@@ -357,28 +420,10 @@ int launch_t(const SharedAttnArgs& s, cudaStream_t stream) {
   }
   c.dcols = kDecodeCols * cg / c.np;
 
-  if (any_decode && most_own <= c.dcols) {
-    // one launch of clusters that share nothing where kv_fp8_attention would make it
-    const long long tasks = (long long)a.num_seqs * c.ng, room = (long long)sms * dec_occ;
-    const long long table = (long long)a.max_blocks_per_seq * 16;
-    const long long most = ((a.max_seq_len < table ? a.max_seq_len : table) + 16 * c.np - 1) / (16 * c.np);
-    int cl = 1;
-    while (cl < 8 && 2 * tasks * cl <= room && most > 2 * cl) cl *= 2;
-    if (tasks * cl <= room && most <= 16 * cl) {
-      timing_begin(kTimedDecode, stream);
-      const int e = with_np(c.np, cg, [&](auto np_tag, auto cg_tag) {
-        constexpr int NP = decltype(np_tag)::value, CG = decltype(cg_tag)::value;
-        return launch_pdl(decode_fp8_kernel<D, NP, CG, true, true>, dim3((unsigned)(tasks * cl)), c.hg * CG * 32,
-                          Fp8Dec<D, NP>::smem_bytes(c.hg), stream, cl, Fp8DecParams{c, pv, 0, cl, false});
-      });
-      timing_end(kTimedDecode, stream);
-      return e;
-    }
-  }
-
   using G = Fp8Ws<D>;
   const bool may_prefill = c.group > c.dcols || most_tokens * c.group > c.dcols;
-  c.tile_tokens = G::ROWS / c.group;
+  const bool few = D <= 128 && most_tokens * c.group <= Few<D <= 128 ? D : 128>::RN;
+  c.tile_tokens = (few ? Few<D <= 128 ? D : 128>::RN : G::ROWS) / c.group;
   c.step_blocks = G::NB;
   c.split_steps = 4;
   c.split_ctas = sms;
@@ -387,8 +432,12 @@ int launch_t(const SharedAttnArgs& s, cudaStream_t stream) {
     if (!make_maps<D>(a, c.tile_tokens, &maps)) return KV_INT4_ERR_CUDA;
     static PerContext<int> occ_c;
     int occ = 0;
-    if (!occ_c.get(dev, [](int* o) { return configure_tmem(prefill_ws_fp8_kernel<D, true>, G::SMEM, G::THREADS, 512, o); },
-                   &occ))
+    if (!occ_c.get(dev, [](int* o) {
+          if constexpr (D <= 128) {
+            if (!configure_tmem(few_ws_kernel<D>, Few<D>::SMEM, Few<D>::THREADS, 256, o)) return false;
+          }
+          return configure_tmem(prefill_ws_fp8_kernel<D, true>, G::SMEM, G::THREADS, 512, o);
+        }, &occ))
       return KV_INT4_ERR_CUDA;
   }
   const bool may_split = may_prefill && a.max_seq_len > 2ll * 16 * c.step_blocks * c.split_steps;
@@ -397,16 +446,23 @@ int launch_t(const SharedAttnArgs& s, cudaStream_t stream) {
     const long long items = (L.base.max_pairs + L.base.max_pieces) * a.num_kv_heads;
     const long long grid = sms < items ? sms : items;
     timing_begin(kTimedPrefill, stream);
-    const int e = launch_pdl(prefill_ws_fp8_kernel<D, true>, dim3((unsigned)grid), G::THREADS, G::SMEM, stream, 1, c, pv, maps);
+    int e;
+    if constexpr (D <= 128) {
+      e = few ? launch_pdl(few_ws_kernel<D>, dim3((unsigned)grid), Few<D>::THREADS, Few<D>::SMEM, stream, 1, c, pv, maps)
+              : launch_pdl(prefill_ws_fp8_kernel<D, true>, dim3((unsigned)grid), G::THREADS, G::SMEM, stream, 1, c, pv, maps);
+    } else {
+      e = launch_pdl(prefill_ws_fp8_kernel<D, true>, dim3((unsigned)grid), G::THREADS, G::SMEM, stream, 1, c, pv, maps);
+    }
     timing_end(kTimedPrefill, stream);
     if (e) return e;
   }
   if (any_decode) {
     timing_begin(kTimedDecode, stream);
-    const int e = with_np(c.np, cg, [&](auto np_tag, auto cg_tag) {
+    const int e = with_np(np, cg, [&](auto np_tag, auto cg_tag, auto gw_tag) {
       constexpr int NP = decltype(np_tag)::value, CG = decltype(cg_tag)::value;
-      return launch_pdl(decode_fp8_kernel<D, NP, CG, false, true>, dim3(dec_grid), c.hg * CG * 32,
-                        Fp8Dec<D, NP>::smem_bytes(c.hg), stream, 1, Fp8DecParams{c, pv, dec_grid, 1, may_prefill});
+      constexpr int GW = decltype(gw_tag)::value;
+      return launch_pdl(decode_fp8_kernel<D, NP, CG, false, true, GW>, dim3(dec_grid), c.hg * CG * 32,
+                        Fp8Dec<D, NP>::smem_bytes(c.hg, c.hg * CG, GW), stream, 1, Fp8DecParams{c, pv, dec_grid, 1, may_prefill});
     });
     timing_end(kTimedDecode, stream);
     if (e) return e;

@@ -48,6 +48,10 @@ struct Fp8Dec {
   // head tiles, then the scales [K/V][hg]
   __host__ __device__ static constexpr int slot_bytes(int hg) { return hg * HTILE + 32; }
   __host__ __device__ static constexpr int smem_bytes(int hg) { return NS * slot_bytes(hg) + 32; }
+  // with the query fragments of `warps` warps of gw column groups each
+  __host__ __device__ static constexpr int smem_bytes(int hg, int warps, int gw) {
+    return smem_bytes(hg) + (gw > 1 ? warps * gw * KSTEPS * 256 : 0);
+  }
   __host__ __device__ static constexpr int swz(int r) {
     return CHR >= 8 ? ((r & 1) << 2) | ((r >> 1) & 3) : (r >> 1) & 3;
   }
@@ -71,7 +75,7 @@ struct Fp8Walk {
   int fb;    // first block read (the sliding window's)
   int seq;   // sequence id
   int len;   // keys
-  long long tab;  // first entry of its block table
+  long long tab;  // SH: first entry of its block table
 };
 
 struct Fp8DecParams {
@@ -90,8 +94,6 @@ __device__ __forceinline__ void fp8_walk_load(Fp8Walk& w, const Common& c, const
   if constexpr (SH) {
     const int2 at = *reinterpret_cast<const int2*>(pv.dseq2 + w.i);
     w.tab = (long long)(uint32_t)at.x | (long long)at.y << 32;
-  } else {
-    w.tab = (long long)di.x * c.max_blocks;
   }
   w.fb = first_block(c, di.y, di.w);
   w.npos = ((di.y + 15) / 16 - w.fb + NP - 1) / NP;
@@ -142,11 +144,14 @@ __device__ __forceinline__ float ld_cluster(const float* p, int rank) {
 // the positions, and merges them through distributed shared memory: one launch
 // for batches whose shares are short (latency counts there, not balance).
 // SH: over virtual sequences (shared prefixes), and the rows' log-sum-exp.
-template <int D, int NP, int CG, bool DIRECT, bool SH = false>
+// GW: column groups of eight per warp, which converts a code once for all of them
+// and finds their query fragments in shared memory (behind the ring).
+template <int D, int NP, int CG, bool DIRECT, bool SH = false, int GW = 1>
 __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
   using G = Fp8Dec<D, NP>;
-  static_assert(CG == 1 || (NP == 1 && kFp8PartsFit<D>), "column groups");
-  constexpr int SLOT = kDecodeCols * CG;           // columns of a result slot
+  static_assert((CG == 1 && GW == 1) || (NP == 1 && kFp8PartsFit<D>), "column groups");
+  static_assert(GW == 1 || !DIRECT, "column groups of a warp");
+  constexpr int SLOT = kDecodeCols * CG * GW;      // columns of a result slot
   constexpr int CPT = (G::CHR + CG - 1) / CG;      // chunks a thread copies per block
   const Common& c = prm.c;
   const PlanView& pv = prm.pv;
@@ -155,7 +160,7 @@ __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
   const int tid = threadIdx.x, nthr = HG * CG * 32;
   const int warp = tid >> 5, lane = tid & 31;
   const int hl = CG == 1 ? warp : warp / CG;       // head of the group
-  const int cbase = CG == 1 ? 0 : warp % CG * kDecodeCols;  // first query column
+  const int cbase = CG == 1 ? 0 : warp % CG * (kDecodeCols * GW);  // first query column
   const int g = lane >> 2, cq = lane & 3;
   const int SB = G::slot_bytes(HG);
   pdl_trigger();
@@ -203,7 +208,6 @@ again:
     if (ql == 0) return;
     dseq0 = make_int4(cw.seq, cw.len, q0, ql);
     cw.i = cw.lane = 0;
-    cw.tab = (long long)cw.seq * c.max_blocks;
     cw.fb = first_block(c, cw.len, ql);
     const int npos = ((cw.len + 15) / 16 - cw.fb + NP - 1) / NP;
     const int first = (int)((long long)npos * rank / prm.cluster), end = (int)((long long)npos * (rank + 1) / prm.cluster);
@@ -273,7 +277,7 @@ again:
   // block j of a position
   auto block_at = [&](const Fp8Walk& w, int j) {
     const int kb = w.fb + w.kp * NP + j;
-    return kb * 16 < w.len ? c.block_table[w.tab + kb] : -1;
+    return kb * 16 < w.len ? c.block_table[(SH && !DIRECT ? w.tab : (long long)w.seq * c.max_blocks) + kb] : -1;
   };
   auto issue = [&](int blk, int kb, int len, int grp, int slot) {
     const bool ok = blk >= 0 && blk < c.num_blocks;
@@ -328,11 +332,13 @@ again:
   for (int s = 0; s < G::NS - NP; s++) produce();
 
   // per-segment state of this warp's head
-  uint32_t qb[G::KSTEPS][2];
-  float oacc[G::KSTEPS][4];
-  float m0, m1, l0, l1;
-  float cf0, cf1;  // score factor of columns 2cq, 2cq+1: 2^e of the query row * softmax_scale * log2 e
-  int lim0, lim1, lo0, lo1;  // keys visible to the columns: positions [lo, lim)
+  constexpr bool QS = GW > 1;
+  uint32_t qb[QS ? 1 : G::KSTEPS][2];
+  uint2* const sqb = reinterpret_cast<uint2*>(smem + G::smem_bytes(HG)) + (QS ? warp * GW * G::KSTEPS * 32 + lane : 0);
+  float oacc[GW][G::KSTEPS][4];
+  float m0[GW], m1[GW], l0[GW], l1[GW];
+  float cf0[GW], cf1[GW];  // score factor of columns 2cq, 2cq+1: 2^e of the query row * softmax_scale * log2 e
+  int lim0[GW], lim1[GW], lo0[GW], lo1[GW];  // keys visible to the columns: positions [lo, lim)
   int lim_warp, lo_warp;     // smallest limit, largest first position of all columns
   bool first_piece = cw.kp == 0;
 
@@ -341,55 +347,68 @@ again:
     const int4 di = DIRECT ? dseq0 : pv.dseq[cw.i];
     const int q0 = di.z, ql = di.w, L = di.y;
     const int ctx = SH && !DIRECT ? pv.dseq2[cw.i].z : L - ql;
-    // B fragments of this lane's column g, which holds query column cbase + g % COLS
-    const int n = cbase + (g & (G::COLS - 1));
-    const bool colok = n < ql * c.group;
-    const int j = n / c.group, jj = n - j * c.group;
-    const uint16_t* qrow = c.q + (long long)(q0 + (colok ? j : 0)) * c.q_stride +
-                           (long long)(head * c.group + (colok ? jj : 0)) * D;
-    uint2 qv[G::KSTEPS];
-    uint32_t am = 0;
+    int lim_least = INT_MAX, lo_most = 0;
 #pragma unroll
-    for (int s = 0; s < G::KSTEPS; s++) {
-      qv[s] = make_uint2(0, 0);
-      if (colok) qv[s] = *reinterpret_cast<const uint2*>(qrow + fp8_kdim<D>(cq, s));
-      am = __vmaxu2(am, __vmaxu2(qv[s].x & 0x7fff7fffu, qv[s].y & 0x7fff7fffu));
+    for (int w = 0; w < GW; w++) {
+      const int wbase = cbase + kDecodeCols * w;
+      // B fragments of this lane's column g, which holds query column wbase + g % COLS
+      const int n = wbase + (g & (G::COLS - 1));
+      const bool colok = n < ql * c.group;
+      const int j = n / c.group, jj = n - j * c.group;
+      const uint16_t* qrow = c.q + (long long)(q0 + (colok ? j : 0)) * c.q_stride +
+                             (long long)(head * c.group + (colok ? jj : 0)) * D;
+      uint2 qv[G::KSTEPS];
+      uint32_t am = 0;
+#pragma unroll
+      for (int s = 0; s < G::KSTEPS; s++) {
+        qv[s] = make_uint2(0, 0);
+        if (colok) qv[s] = *reinterpret_cast<const uint2*>(qrow + fp8_kdim<D>(cq, s));
+        am = __vmaxu2(am, __vmaxu2(qv[s].x & 0x7fff7fffu, qv[s].y & 0x7fff7fffu));
+      }
+      am = max(am & 0xffffu, am >> 16);
+      am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+      am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+      const int e = q_exponent(am);
+      const float mul = exp2_int(-e);
+#pragma unroll
+      for (int s = 0; s < G::KSTEPS; s++) {
+        const uint32_t b0 = pack_f16x2(bf16lo_to_f32(qv[s].x) * mul, bf16hi_to_f32(qv[s].x) * mul);
+        const uint32_t b1 = pack_f16x2(bf16lo_to_f32(qv[s].y) * mul, bf16hi_to_f32(qv[s].y) * mul);
+        if constexpr (QS) {
+          sqb[(w * G::KSTEPS + s) * 32] = make_uint2(b0, b1);  // read by this lane alone
+        } else {
+          qb[s][0] = b0;
+          qb[s][1] = b1;
+        }
+      }
+      const float cf = c.qscale * exp2_int(e);
+      cf0[w] = __shfl_sync(0xffffffffu, cf, 8 * cq);      // column 2 cq is held by lanes 4 (2 cq) ..
+      cf1[w] = __shfl_sync(0xffffffffu, cf, 8 * cq + 4);
+      const int col0 = wbase + ((2 * cq) & (G::COLS - 1)), col1 = wbase + ((2 * cq + 1) & (G::COLS - 1));
+      const int j0 = min(col0 / c.group, max(ql - 1, 0)), j1 = min(col1 / c.group, max(ql - 1, 0));
+      lim0[w] = c.causal ? min(L, ctx + j0 + 1) : L;
+      lim1[w] = c.causal ? min(L, ctx + j1 + 1) : L;
+      lo0[w] = window_lo(c, ctx + j0);
+      lo1[w] = window_lo(c, ctx + j1);
+      lim_least = min(lim_least, min(lim0[w], lim1[w]));
+      lo_most = max(lo_most, max(lo0[w], lo1[w]));
+#pragma unroll
+      for (int i = 0; i < G::KSTEPS; i++) oacc[w][i][0] = oacc[w][i][1] = oacc[w][i][2] = oacc[w][i][3] = 0.f;
+      m0[w] = m1[w] = -INFINITY;
+      l0[w] = l1[w] = 0.f;
     }
-    am = max(am & 0xffffu, am >> 16);
-    am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
-    am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
-    const int e = q_exponent(am);
-    const float mul = exp2_int(-e);
-#pragma unroll
-    for (int s = 0; s < G::KSTEPS; s++) {
-      qb[s][0] = pack_f16x2(bf16lo_to_f32(qv[s].x) * mul, bf16hi_to_f32(qv[s].x) * mul);
-      qb[s][1] = pack_f16x2(bf16lo_to_f32(qv[s].y) * mul, bf16hi_to_f32(qv[s].y) * mul);
-    }
-    const float cf = c.qscale * exp2_int(e);
-    cf0 = __shfl_sync(0xffffffffu, cf, 8 * cq);      // column 2 cq is held by lanes 4 (2 cq) ..
-    cf1 = __shfl_sync(0xffffffffu, cf, 8 * cq + 4);
-    const int col0 = cbase + ((2 * cq) & (G::COLS - 1)), col1 = cbase + ((2 * cq + 1) & (G::COLS - 1));
-    const int j0 = min(col0 / c.group, max(ql - 1, 0)), j1 = min(col1 / c.group, max(ql - 1, 0));
-    lim0 = c.causal ? min(L, ctx + j0 + 1) : L;
-    lim1 = c.causal ? min(L, ctx + j1 + 1) : L;
-    lo0 = window_lo(c, ctx + j0);
-    lo1 = window_lo(c, ctx + j1);
-    lim_warp = __reduce_min_sync(0xffffffffu, min(lim0, lim1));
-    lo_warp = __reduce_max_sync(0xffffffffu, max(lo0, lo1));
-#pragma unroll
-    for (int i = 0; i < G::KSTEPS; i++) oacc[i][0] = oacc[i][1] = oacc[i][2] = oacc[i][3] = 0.f;
-    m0 = m1 = -INFINITY;
-    l0 = l1 = 0.f;
+    lim_warp = __reduce_min_sync(0xffffffffu, lim_least);
+    lo_warp = __reduce_max_sync(0xffffffffu, lo_most);
   };
 
-  auto flush = [&]() {
-    float a0 = l0, a1 = l1;
+  auto flush_group = [&](int w) {
+    float a0 = l0[w], a1 = l1[w];
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       a0 += __shfl_xor_sync(0xffffffffu, a0, o);
       a1 += __shfl_xor_sync(0xffffffffu, a1, o);
     }
-    float mm0 = m0, mm1 = m1;
+    float mm0 = m0[w], mm1 = m1[w];
     if constexpr (NP == 4) {
       // the four blocks' columns c, c + 2, c + 4, c + 6 hold the same queries:
       // merged here, so that a piece leaves columns 0 and 1 only
@@ -404,10 +423,10 @@ again:
         a1 = ea1.of(a1) + eb1.of(__shfl_xor_sync(0xffffffffu, a1, x));
 #pragma unroll
         for (int i = 0; i < G::KSTEPS; i++) {
-          oacc[i][0] = oacc[i][0] * sa0 + __shfl_xor_sync(0xffffffffu, oacc[i][0], x) * sb0;
-          oacc[i][2] = oacc[i][2] * sa0 + __shfl_xor_sync(0xffffffffu, oacc[i][2], x) * sb0;
-          oacc[i][1] = oacc[i][1] * sa1 + __shfl_xor_sync(0xffffffffu, oacc[i][1], x) * sb1;
-          oacc[i][3] = oacc[i][3] * sa1 + __shfl_xor_sync(0xffffffffu, oacc[i][3], x) * sb1;
+          oacc[w][i][0] = oacc[w][i][0] * sa0 + __shfl_xor_sync(0xffffffffu, oacc[w][i][0], x) * sb0;
+          oacc[w][i][2] = oacc[w][i][2] * sa0 + __shfl_xor_sync(0xffffffffu, oacc[w][i][2], x) * sb0;
+          oacc[w][i][1] = oacc[w][i][1] * sa1 + __shfl_xor_sync(0xffffffffu, oacc[w][i][1], x) * sb1;
+          oacc[w][i][3] = oacc[w][i][3] * sa1 + __shfl_xor_sync(0xffffffffu, oacc[w][i][3], x) * sb1;
         }
         mm0 = n0;
         mm1 = n1;
@@ -428,15 +447,15 @@ again:
       dst_o = pv.warp_o + slot * SLOT * D;
       dst_ml = pv.warp_ml + slot * SLOT * 2;
     }
-    dst_o += cbase * D;
-    dst_ml += cbase * 2;
+    dst_o += (cbase + kDecodeCols * w) * D;
+    dst_ml += (cbase + kDecodeCols * w) * 2;
     // m-tile t holds d = 16 t + 2g (row g) and 16 t + 2g + 1 (row g + 8)
     float* o0 = dst_o + (2 * cq) * D + 2 * g;
     float* o1 = dst_o + (2 * cq + 1) * D + 2 * g;
 #pragma unroll
     for (int i = 0; i < G::KSTEPS; i++) {
-      *reinterpret_cast<float2*>(o0 + 16 * i) = make_float2(oacc[i][0], oacc[i][2]);
-      *reinterpret_cast<float2*>(o1 + 16 * i) = make_float2(oacc[i][1], oacc[i][3]);
+      *reinterpret_cast<float2*>(o0 + 16 * i) = make_float2(oacc[w][i][0], oacc[w][i][2]);
+      *reinterpret_cast<float2*>(o1 + 16 * i) = make_float2(oacc[w][i][1], oacc[w][i][3]);
     }
     if (g == 0) {
       dst_ml[(2 * cq) * 2 + 0] = mm0;
@@ -444,6 +463,10 @@ again:
       dst_ml[(2 * cq + 1) * 2 + 0] = mm1;
       dst_ml[(2 * cq + 1) * 2 + 1] = a1;
     }
+  };
+  auto flush = [&]() {
+#pragma unroll
+    for (int w = 0; w < GW; w++) flush_group(w);
   };
 
   begin_segment();
@@ -478,10 +501,11 @@ again:
     const float ks = sc[0], vs = sc[HG];
 
     // ---- S^T = K Q'^T, one accumulator per block ----
-    float sacc[NP][4];
+    float sacc[GW][NP][4];
 #pragma unroll
     for (int j = 0; j < NP; j++) {
-      sacc[j][0] = sacc[j][1] = sacc[j][2] = sacc[j][3] = 0.f;
+#pragma unroll
+      for (int w = 0; w < GW; w++) sacc[w][j][0] = sacc[w][j][1] = sacc[w][j][2] = sacc[w][j][3] = 0.f;
       const uint8_t* x = smem + slot[j] * SB + hl * G::HTILE + g * D;
       const uint8_t* y = x + 8 * D;
       uint32_t xk[G::KSTEPS], yk[G::KSTEPS];
@@ -507,77 +531,95 @@ again:
         uint32_t a[4];
         e4m3x4_to_f16x2(xk[s], a[0], a[2]);
         e4m3x4_to_f16x2(yk[s], a[1], a[3]);
-        mma_16816(sacc[j], a, qb[s][0], qb[s][1]);
+#pragma unroll
+        for (int w = 0; w < GW; w++) {
+          if constexpr (QS) {
+            const uint2 b = sqb[(w * G::KSTEPS + s) * 32];
+            mma_16816(sacc[w][j], a, b.x, b.y);
+          } else {
+            mma_16816(sacc[w][j], a, qb[s][0], qb[s][1]);
+          }
+        }
       }
     }
-    float sa[4] = {sacc[0][0], sacc[0][1], sacc[0][2], sacc[0][3]};
-#pragma unroll
-    for (int j = 1; j < NP; j++)
-#pragma unroll
-      for (int e = 0; e < 4; e++) sa[e] = jb == j ? sacc[j][e] : sa[e];
-
     const int kb0 = cw.fb + cw.kp * NP;
     const int pos0 = (kb0 + jb) * 16 + g, pos1 = pos0 + 8;
-    const float f0 = cf0 * ks, f1 = cf1 * ks;
     const float kvf = (float)exp_of(vs);                                  // log2 of the V scale
     const bool low = vs < exp2_int(kFp8LowExp);
     // its reciprocal; 0 where the denominator's share is taken below
     const float ivs = low ? 0.f : __uint_as_float((254u << 23) - (__float_as_uint(vs) & 0x7f800000u));
-    float t00 = fmaf(sa[0], f0, kvf), t01 = fmaf(sa[1], f1, kvf);
-    float t10 = fmaf(sa[2], f0, kvf), t11 = fmaf(sa[3], f1, kvf);
     // keys outside a column's visible range (or in an unusable or absent
     // block) only occur in positions that reach past the smallest limit or
     // start before the largest window start
     const bool full = allok && (kb0 + NP) * 16 <= lim_warp && kb0 * 16 >= lo_warp;
-    if (!full) {
-      t00 = (bok && pos0 < lim0 && pos0 >= lo0) ? t00 : -INFINITY;
-      t01 = (bok && pos0 < lim1 && pos0 >= lo1) ? t01 : -INFINITY;
-      t10 = (bok && pos1 < lim0 && pos1 >= lo0) ? t10 : -INFINITY;
-      t11 = (bok && pos1 < lim1 && pos1 >= lo1) ? t11 : -INFINITY;
-    }
-    float mx0 = fmaxf(t00, t10), mx1 = fmaxf(t01, t11);
-    // exact running max: reduced across the key lanes only when some lane
-    // holds a value above its column's current max (or one of a small V scale)
-    if (__any_sync(0xffffffffu, mx0 > m0 || mx1 > m1 || low)) {
+    uint32_t b0[GW], b1[GW];  // the weights' transpose
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
-      }
-      const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
-      const Exp2Pair e0(mn0 == -INFINITY ? 0.f : m0 - mn0);  // a column with no key yet keeps -inf
-      const Exp2Pair e1(mn1 == -INFINITY ? 0.f : m1 - mn1);
-      const float al0 = e0.both(), al1 = e1.both();
-      m0 = mn0;
-      m1 = mn1;
-      l0 = e0.of(l0);
-      l1 = e1.of(l1);
+    for (int w = 0; w < GW; w++) {
+      float sa[4] = {sacc[w][0][0], sacc[w][0][1], sacc[w][0][2], sacc[w][0][3]};
 #pragma unroll
-      for (int i = 0; i < G::KSTEPS; i++) {
-        oacc[i][0] *= al0;
-        oacc[i][1] *= al1;
-        oacc[i][2] *= al0;
-        oacc[i][3] *= al1;
+      for (int j = 1; j < NP; j++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) sa[e] = jb == j ? sacc[w][j][e] : sa[e];
+
+      const float f0 = cf0[w] * ks, f1 = cf1[w] * ks;
+      float t00 = fmaf(sa[0], f0, kvf), t01 = fmaf(sa[1], f1, kvf);
+      float t10 = fmaf(sa[2], f0, kvf), t11 = fmaf(sa[3], f1, kvf);
+      if (!full) {
+        t00 = (bok && pos0 < lim0[w] && pos0 >= lo0[w]) ? t00 : -INFINITY;
+        t01 = (bok && pos0 < lim1[w] && pos0 >= lo1[w]) ? t01 : -INFINITY;
+        t10 = (bok && pos1 < lim0[w] && pos1 >= lo0[w]) ? t10 : -INFINITY;
+        t11 = (bok && pos1 < lim1[w] && pos1 >= lo1[w]) ? t11 : -INFINITY;
       }
-      if (low) {
-        const float up0 = (float)kFp8LowExp - kvf - (m0 == -INFINITY ? 0.f : m0);
-        const float up1 = (float)kFp8LowExp - kvf - (m1 == -INFINITY ? 0.f : m1);
-        l0 = fmaf(fast_exp2(t00 + up0) + fast_exp2(t10 + up0), exp2_int(-kFp8LowExp), l0);
-        l1 = fmaf(fast_exp2(t01 + up1) + fast_exp2(t11 + up1), exp2_int(-kFp8LowExp), l1);
+      float mx0 = fmaxf(t00, t10), mx1 = fmaxf(t01, t11);
+      // exact running max: reduced across the key lanes only when some lane
+      // holds a value above its column's current max (or one of a small V scale)
+      if (__any_sync(0xffffffffu, mx0 > m0[w] || mx1 > m1[w] || low)) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+        }
+        const float mn0 = fmaxf(m0[w], mx0), mn1 = fmaxf(m1[w], mx1);
+        const Exp2Pair e0(mn0 == -INFINITY ? 0.f : m0[w] - mn0);  // a column with no key yet keeps -inf
+        const Exp2Pair e1(mn1 == -INFINITY ? 0.f : m1[w] - mn1);
+        const float al0 = e0.both(), al1 = e1.both();
+        m0[w] = mn0;
+        m1[w] = mn1;
+        l0[w] = e0.of(l0[w]);
+        l1[w] = e1.of(l1[w]);
+#pragma unroll
+        for (int i = 0; i < G::KSTEPS; i++) {
+          oacc[w][i][0] *= al0;
+          oacc[w][i][1] *= al1;
+          oacc[w][i][2] *= al0;
+          oacc[w][i][3] *= al1;
+        }
+        if (low) {
+          const float up0 = (float)kFp8LowExp - kvf - (m0[w] == -INFINITY ? 0.f : m0[w]);
+          const float up1 = (float)kFp8LowExp - kvf - (m1[w] == -INFINITY ? 0.f : m1[w]);
+          l0[w] = fmaf(fast_exp2(t00 + up0) + fast_exp2(t10 + up0), exp2_int(-kFp8LowExp), l0[w]);
+          l1[w] = fmaf(fast_exp2(t01 + up1) + fast_exp2(t11 + up1), exp2_int(-kFp8LowExp), l1[w]);
+        }
       }
+      const float mu0 = m0[w] == -INFINITY ? 0.f : m0[w], mu1 = m1[w] == -INFINITY ? 0.f : m1[w];
+      const float w00 = fast_exp2(t00 - mu0), w01 = fast_exp2(t01 - mu1);
+      const float w10 = fast_exp2(t10 - mu0), w11 = fast_exp2(t11 - mu1);
+      l0[w] = fmaf(w00 + w10, ivs, l0[w]);
+      l1[w] = fmaf(w01 + w11, ivs, l1[w]);
+      b0[w] = movmatrix_trans(pack_f16x2(w00, w01));
+      b1[w] = movmatrix_trans(pack_f16x2(w10, w11));
     }
-    const float mu0 = m0 == -INFINITY ? 0.f : m0, mu1 = m1 == -INFINITY ? 0.f : m1;
-    const float w00 = fast_exp2(t00 - mu0), w01 = fast_exp2(t01 - mu1);
-    const float w10 = fast_exp2(t10 - mu0), w11 = fast_exp2(t11 - mu1);
-    l0 = fmaf(w00 + w10, ivs, l0);
-    l1 = fmaf(w01 + w11, ivs, l1);
-    const uint32_t b0 = movmatrix_trans(pack_f16x2(w00, w01)), b1 = movmatrix_trans(pack_f16x2(w10, w11));
 
     // ---- O'^T += V^T W^T ----
 #pragma unroll
     for (int j = 0; j < NP; j++) {
       // block j's weights only: the other blocks' columns are zero
-      const uint32_t bj0 = NP == 1 || jv == j ? b0 : 0u, bj1 = NP == 1 || jv == j ? b1 : 0u;
+      uint32_t bj0[GW], bj1[GW];
+#pragma unroll
+      for (int w = 0; w < GW; w++) {
+        bj0[w] = NP == 1 || jv == j ? b0[w] : 0u;
+        bj1[w] = NP == 1 || jv == j ? b1[w] : 0u;
+      }
       const uint32_t va = v_lane + slot[j] * SB;
 #pragma unroll
       for (int p = 0; p < G::CHR / 2; p++) {
@@ -591,7 +633,8 @@ again:
           uint32_t a[4];
           e4m3x4_to_f16x2(__byte_perm(r[2 * q], 0, 0x3120), a[0], a[1]);
           e4m3x4_to_f16x2(__byte_perm(r[2 * q + 1], 0, 0x3120), a[2], a[3]);
-          mma_16816(oacc[2 * p + q], a, bj0, bj1);
+#pragma unroll
+          for (int w = 0; w < GW; w++) mma_16816(oacc[w][2 * p + q], a, bj0[w], bj1[w]);
         }
       }
     }

@@ -204,13 +204,14 @@ struct PrefillItem {
   int seq, h, tile;  // seq -1: past the last item
   int kb0, nkb;      // blocks [kb0, nkb)
   int row;           // first piece row, -1 if the tile is whole
+  bool split;        // SH: the halves take the steps in turn (prefill_ws_fp8.cuh)
 };
 __device__ __forceinline__ PrefillItem prefill_piece_item(const Common& c, const PlanView& pv, int itn, int n_items) {
-  if (itn >= n_items) return PrefillItem{-1, 0, 0, 0, 0, -1};
+  if (itn >= n_items) return PrefillItem{-1, 0, 0, 0, 0, -1, false};
   const int pi = itn / c.hkv, h = itn - pi * c.hkv;
   const int4 a = reinterpret_cast<const int4*>(pv.pieces + pi)[0];
   const int2 b = reinterpret_cast<const int2*>(pv.pieces + pi)[2];
-  return PrefillItem{a.x, h, a.y, a.z, a.w, b.x < 0 ? -1 : b.x + h * b.y};
+  return PrefillItem{a.x, h, a.y, a.z, a.w, b.x < 0 ? -1 : b.x + h * b.y, false};
 }
 
 constexpr int kPrepThreads = 256;  // threads of the CTA that builds the schedule
@@ -261,7 +262,8 @@ __device__ __forceinline__ bool schedule_seq_ok(const Common& c, int q0, int ql,
 // at least c.split_steps (a piece costs about two steps on top of its own, and
 // its rows are merged), twice that where decodes run beside on the SMs that
 // whole tiles leave (4 prompts of up to 400 tokens beside 28 decodes: 45.9 us,
-// in pieces 55.3).  If there are fewer tiles than CTAs, an S up to twice as
+// in pieces 55.3; not so beside shared prefixes, whose tiles are most of the work:
+// 64 sequences over 8192 positions 63 us, without 59).  If there are fewer tiles than CTAs, an S up to twice as
 // large whose pieces all run at once is taken; without one, only tiles of more
 // than two shares are worth it.  Everything follows from the call's lengths
 // alone, so results do not depend on the order of arrival.  Batches of more
@@ -328,7 +330,7 @@ __device__ void build_pieces(const Common& c, const PlanView& pv, int n_pseq, in
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     longest = __reduce_max_sync(0xffffffffu, longest);
     const long long share = div_nn(sum * c.hkv + c.split_ctas - 1, c.split_ctas);
-    const long long S0 = max(share, (long long)c.split_steps << (with_decode ? 1 : 0));
+    const long long S0 = max(share, (long long)c.split_steps << (with_decode && !SH ? 1 : 0));
     const bool one_wave = (long long)n_tiles * c.hkv < c.split_ctas;
     if (longest > (one_wave ? S0 : 2 * S0)) {  // else every tile stays whole
       constexpr int W = kPrepThreads / 32;
