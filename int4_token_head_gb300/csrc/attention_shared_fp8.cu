@@ -32,14 +32,6 @@ namespace {
 
 constexpr int kMergeWarps = 16;  // per CTA, and about per SM over all CTAs
 
-#include "few_ws_fp8.cuh"
-
-// query columns of a group up to which its prefix is the decode kernel's: more are
-// the tensor cores', in tiles of few rows (up to 64) or of many.  Head sizes above 128
-// have no tiles of few rows.
-template <int D>
-constexpr int kMostGroupCols = D <= 128 ? kDecodeCols : kDecodeColsFp8;
-
 struct SharedMergeParams {
   Common c;
   PlanView pv;
@@ -383,7 +375,7 @@ int launch_t(const SharedAttnArgs& s, cudaStream_t stream) {
   c.hg = c.ng = c.nl = c.np = 1;
   const long long most_tokens = s.num_groups > 0 && s.max_group_tokens > a.max_query_len ? s.max_group_tokens : a.max_query_len;
   const long long mq = (most_tokens > 0 ? most_tokens : 1) * c.group;
-  const long long cols = mq <= kMostGroupCols<D> ? mq : most_own <= kDecodeColsFp8 ? most_own : c.group;
+  const long long cols = mq <= kDecodeColsFp8 ? mq : most_own <= kDecodeColsFp8 ? most_own : c.group;
   int cg = groups_of(cols);
   const long long virt = (long long)a.num_seqs + s.num_groups;
   while (cg > 1 && virt * a.num_kv_heads * kDecodeCols * cg > L.base.direct_rows) cg /= 2;
@@ -422,8 +414,7 @@ int launch_t(const SharedAttnArgs& s, cudaStream_t stream) {
 
   using G = Fp8Ws<D>;
   const bool may_prefill = c.group > c.dcols || most_tokens * c.group > c.dcols;
-  const bool few = D <= 128 && most_tokens * c.group <= Few<D <= 128 ? D : 128>::RN;
-  c.tile_tokens = (few ? Few<D <= 128 ? D : 128>::RN : G::ROWS) / c.group;
+  c.tile_tokens = G::ROWS / c.group;
   c.step_blocks = G::NB;
   c.split_steps = 4;
   c.split_ctas = sms;
@@ -432,12 +423,8 @@ int launch_t(const SharedAttnArgs& s, cudaStream_t stream) {
     if (!make_maps<D>(a, c.tile_tokens, &maps)) return KV_INT4_ERR_CUDA;
     static PerContext<int> occ_c;
     int occ = 0;
-    if (!occ_c.get(dev, [](int* o) {
-          if constexpr (D <= 128) {
-            if (!configure_tmem(few_ws_kernel<D>, Few<D>::SMEM, Few<D>::THREADS, 256, o)) return false;
-          }
-          return configure_tmem(prefill_ws_fp8_kernel<D, true>, G::SMEM, G::THREADS, 512, o);
-        }, &occ))
+    if (!occ_c.get(dev, [](int* o) { return configure_tmem(prefill_ws_fp8_kernel<D, true>, G::SMEM, G::THREADS, 512, o); },
+                   &occ))
       return KV_INT4_ERR_CUDA;
   }
   const bool may_split = may_prefill && a.max_seq_len > 2ll * 16 * c.step_blocks * c.split_steps;
@@ -446,13 +433,7 @@ int launch_t(const SharedAttnArgs& s, cudaStream_t stream) {
     const long long items = (L.base.max_pairs + L.base.max_pieces) * a.num_kv_heads;
     const long long grid = sms < items ? sms : items;
     timing_begin(kTimedPrefill, stream);
-    int e;
-    if constexpr (D <= 128) {
-      e = few ? launch_pdl(few_ws_kernel<D>, dim3((unsigned)grid), Few<D>::THREADS, Few<D>::SMEM, stream, 1, c, pv, maps)
-              : launch_pdl(prefill_ws_fp8_kernel<D, true>, dim3((unsigned)grid), G::THREADS, G::SMEM, stream, 1, c, pv, maps);
-    } else {
-      e = launch_pdl(prefill_ws_fp8_kernel<D, true>, dim3((unsigned)grid), G::THREADS, G::SMEM, stream, 1, c, pv, maps);
-    }
+    const int e = launch_pdl(prefill_ws_fp8_kernel<D, true>, dim3((unsigned)grid), G::THREADS, G::SMEM, stream, 1, c, pv, maps);
     timing_end(kTimedPrefill, stream);
     if (e) return e;
   }

@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(Fp8Pre<D>::THREADS) prefill_fp8_kernel(Common 
       sitem[3] = it.kb0; sitem[4] = it.nkb; sitem[5] = it.row;
     }
     __syncthreads();
-    const PrefillItem item{sitem[0], sitem[1], sitem[2], sitem[3], sitem[4], sitem[5], false};
+    const PrefillItem item{sitem[0], sitem[1], sitem[2], sitem[3], sitem[4], sitem[5]};
     __syncthreads();
     if (item.seq < 0) break;
     const int seq = item.seq, h = item.h, tile = item.tile, kb0 = item.kb0, nkb = item.nkb;

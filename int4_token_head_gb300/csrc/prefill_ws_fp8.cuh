@@ -8,11 +8,6 @@
 // tiles no more shared memory).  At 256 an item is one half, 128 rows: two
 // accumulators would fill TMEM.  Warps in five roles that meet only at mbarriers
 // (numbers for two halves):
-// Items in turns (SH, two halves, at most 128 rows): both halves hold the same rows
-// and take the steps in turn, so that two chains run side by side over one item
-// (four documents of 32768 positions, eight conversations about each, 32/8 heads of
-// 128: 32 rows an item; TODO us, one half alone TODO).  A warp without rows only keeps
-// step.  At the end the four warps of a row join their halves' sums.
 //   * producer warp (24): claims items (longest first) and hands them on
 //     through a two-entry ring; TMA copies of the item's Q rows (bf16, straight
 //     into the MMA's swizzled tile) and of the step's K and V code blocks (one
@@ -58,9 +53,8 @@
 //   sfull[h]  S_h complete (and every earlier MMA)
 //   pfull[h]  W_h in TMEM, O_h rescaled if it had to be
 //   odone     the item's last WV complete (items with steps)
-// Ring entry n % 4 is written once S of step n - 2 is complete: it was issued
-// after both halves' W of step n - 3 (of an item in turns, its half's of step
-// n - 4), the entry's last readers.  An item's Q is
+// Ring entry n % 3 is written once S of step n - 2 is complete: it was issued
+// after both halves' W of step n - 3, the entry's last readers.  An item's Q is
 // copied once S of the previous item's last step is complete.
 
 template <int D>
@@ -84,7 +78,7 @@ struct Fp8Ws {
   // K scales, log2 V scales, 1 / V scales (0 below 2^kFp8LowExp), block flags, step flags (1 all blocks
   // usable, 2 a V scale below)
   static constexpr int RING = (4 * NB + 4) * 4;
-  static constexpr int NRING = 4;
+  static constexpr int NRING = 3;
   static constexpr int NBARS = 23;
   static constexpr int S_COLS = NK, O_COL = H * NK;  // TMEM: S_h at h NK, O_h at H NK + h D
   static constexpr int XCH = 2 * ROWS * 4;  // a float per row and key half: maxima, sums
@@ -232,7 +226,8 @@ struct Fp8Maps {
   CUtensorMap q, k, v;
 };
 
-// SH: over virtual sequences (shared prefixes), and the rows' log-sum-exp
+// SH: over virtual sequences (shared prefixes), and the rows' log-sum-exp.  A warp
+// without rows only keeps step (32 rows against 32768 keys: TODO).
 template <int D, bool SH = false>
 __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
     prefill_ws_fp8_kernel(Common c, PlanView pv, const __grid_constant__ Fp8Maps maps) {
@@ -295,8 +290,7 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
   const int n_items = pv.plan[1];
   auto item_at = [&](int e) {
     const int* s = sitem + 6 * e;
-    if constexpr (SH && G::H == 2) return PrefillItem{s[0], s[1], s[2], s[3], s[4] & 0x3fffffff, s[5], (s[4] >> 30 & 1) != 0};
-    return PrefillItem{s[0], s[1], s[2], s[3], s[4], s[5], false};
+    return PrefillItem{s[0], s[1], s[2], s[3], s[4], s[5]};
   };
   // a consumer's wait for ring entry e, warp-uniform
   auto take_item = [&](int e, uint32_t& ph, PrefillItem& item) {
@@ -316,8 +310,8 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
     uint32_t ph_sfull = 0, ph_odone = 0, ph_ifull = 0;
     const float cf = fabsf(c.qscale);  // its sign is in K
     const int hf = warp >> 3, kh = (warp >> 2) & 1;  // query half, key half
-    const int rx = hf * 128 + (warp & 3) * 32 + lane;  // this thread's place; its row of an item of two halves
-    const int jx = (int)c.gdiv.div((uint32_t)rx);
+    const int r = hf * 128 + (warp & 3) * 32 + lane;  // row of the item
+    const int j = (int)c.gdiv.div((uint32_t)r);
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     constexpr int NC = NK / 2, NBH = NB / 2;  // keys and blocks of a key half
     const uint32_t tS = tmem + NK * hf + NC * kh + lane_off, tO = tmem + G::O_COL + hf * D + lane_off;
@@ -332,31 +326,18 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
           : "memory");
       return any != 0;
     };
-    // the four warps of a row of an item in turns
-    auto row_any = [&](bool v) -> bool {
-      uint32_t any;
-      asm volatile(
-          "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-          : "=r"(any)
-          : "r"((uint32_t)v), "r"(9 + (warp & 3))
-          : "memory");
-      return any != 0;
-    };
-    auto row_sync = [&]() { asm volatile("bar.sync %0, 128;\n" ::"r"(9 + (warp & 3)) : "memory"); };
     int n = 0;  // steps of earlier items
 #pragma unroll 1
     for (int itc = 0;; itc++) {
-      // both warps of a row (all four of an item in turns) go on or none (after a
-      // time-out one may get an item that another does not)
+      // both warps of a row go on or neither (after a time-out one may get an
+      // item that the other does not)
       PrefillItem item;
       const bool taken = take_item(itc & 1, ph_ifull, item);
-      if (SH && G::H == 2 ? row_any(!taken) : pair_any(!taken)) break;
+      if (pair_any(!taken)) break;
       const int seq = item.seq, h = item.h, tile = item.tile, kb0 = item.kb0, nkb = item.nkb;
       const SeqView view = seq_view<SH>(c, pv, seq);
       const int q0 = view.q0, ql = view.ql, L = view.L, ctx = view.ctx;
       const int tok0 = tile * c.tile_tokens;
-      const bool split = SH && G::H == 2 && item.split;
-      const int r = split ? rx & 127 : rx, j = SH && split ? (int)c.gdiv.div((uint32_t)r) : jx;
       const bool rok = r < min(c.tile_tokens, ql - tok0) * c.group;
       const int nsteps = (nkb - kb0 + NB - 1) / NB;
       const int qp = ctx + tok0 + (rok ? j : 0);
@@ -364,12 +345,9 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
       int lim = (c.causal ? min(L, qp + 1) : L) - kb0 * 16 - NC * kh, lo = window_lo(c, qp) - kb0 * 16 - NC * kh;
       // rows that are not there never ask for a reference: theirs is above everything
       float m_ref = rok ? -INFINITY : INFINITY, l_run = 0.f;
-      const int st0 = split ? hf : 0, turn = split ? 2 : 1;  // this half's steps
-      lim -= NK * st0;
-      lo -= NK * st0;
       const bool idle = SH && !__any_sync(0xffffffffu, rok);  // no row of this warp's is there
 #pragma unroll 1
-      for (int st = st0; st < nsteps; st += turn, n += SH ? 0 : 1, lim -= NK * turn, lo -= NK * turn) {
+      for (int st = 0; st < nsteps; st++, n++, lim -= NK, lo -= NK) {
         if (SH && idle) {
           fp8_wait(bar(SFULL + hf), ph_sfull, abort_flag, c.status);
           ph_sfull ^= 1;
@@ -377,7 +355,7 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
           if (lane == 0) fp8_arrive(bar(PFULL + hf));
           continue;
         }
-        const float* re = reinterpret_cast<const float*>(ring + ((SH ? n + st : n) % G::NRING) * G::RING) + NBH * kh;
+        const float* re = reinterpret_cast<const float*>(ring + (n % G::NRING) * G::RING) + NBH * kh;
         const float* kvf = re + NB;
         const float* ivs = re + 2 * NB;
         const int* ok = reinterpret_cast<const int*>(re + 3 * NB);
@@ -414,7 +392,7 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
         // more than 8 behind; whole numbers, so that O and l move exactly.  Blocks of
         // small V scales (kFp8LowExp) have their share of the denominator taken there
         // too, by a maximum of their own
-        bool find = st == st0 || (step_flags & 2) != 0;
+        bool find = st == 0 || (step_flags & 2) != 0;
 #pragma unroll 1
         while (true) {
           if (find) {
@@ -437,9 +415,9 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
                 for (int k = 0; k < 16; k++) lows += fast_exp2(fmaf(s[k], f, -o));
               }
             }
-            sxch[kh * ROWS + rx] = mx;
+            sxch[kh * ROWS + r] = mx;
             pair_sync();
-            mx = ceilf(fmaxf(mx, sxch[(kh ^ 1) * ROWS + rx]));
+            mx = ceilf(fmaxf(mx, sxch[(kh ^ 1) * ROWS + r]));
             pair_sync();  // read before anything else is written there
             const bool grow = mx > m_ref + (m_ref == -INFINITY ? 0.f : 8.f);
             const Exp2Pair move(grow && m_ref != -INFINITY ? m_ref - mx : 0.f);
@@ -495,75 +473,16 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
         if (lane == 0) fp8_arrive(bar(PFULL + hf));
       }
 
-      if (SH) n += nsteps;
-
       // ---- epilogue: normalise, bf16, stored from registers; each key half's
       // threads take a share of the columns ----
-      sxch[kh * ROWS + rx] = l_run;
+      sxch[kh * ROWS + r] = l_run;
       pair_sync();
-      const float l = l_run + sxch[(kh ^ 1) * ROWS + rx];
+      const float l = l_run + sxch[(kh ^ 1) * ROWS + r];
       pair_sync();  // read before the next item's are written
       if (nsteps > 0) {
         fp8_wait(bar(ODONE), ph_odone, abort_flag, c.status);
         ph_odone ^= 1;
         tc_fence_after();
-      }
-      if (SH && split) {
-        // the halves' sums meet: each of a row's four warps takes a quarter of the columns
-        if (kh == 0) {
-          sxch[rx] = m_ref;
-          sxch[ROWS + rx] = l;
-        }
-        row_sync();
-        const float m0 = sxch[r], l0 = sxch[ROWS + r], m1 = sxch[128 + r], l1 = sxch[ROWS + 128 + r];
-        const float M = fmaxf(m0, m1), mu = M == -INFINITY ? 0.f : M;
-        const Exp2Pair e0(rok ? m0 - mu : 0.f), e1(rok ? m1 - mu : 0.f);
-        const float L2 = e0.of(l0) + e1.of(l1);
-        const int first = pv.vrec[2 * seq + 1].z;
-        const long long head_row = h * c.group + (rok ? r - j * c.group : 0);
-        float *o_dst = nullptr, *ml_dst = nullptr;  // a piece, or a row that is merged
-        if (item.row >= 0) {
-          o_dst = pv.piece_o + (long long)(item.row + r) * D;
-          ml_dst = pv.piece_ml + 2ll * (item.row + r);
-        } else if (first >= 0) {
-          const long long at = (long long)(first + tok0 + (rok ? j : 0)) * c.hq + head_row;
-          o_dst = pv.row_o + at * D;
-          ml_dst = pv.row_ml + 2 * at;
-        }
-        // V's factor 2^-8 is undone here
-        const float norm = o_dst ? 256.f : L2 == 0.f ? 0.f : 256.f / L2;
-        const float f0 = e0.both() * norm, f1 = nsteps > 1 ? e1.both() * norm : 0.f;
-        uint16_t* const orow = c.out + (long long)(q0 + tok0 + (rok ? j : 0)) * c.out_stride + head_row * D;
-#pragma unroll 1
-        for (int u = hf * 2 + kh; u < D / 16; u += 4) {
-          uint32_t x[16];
-          float y[16];
-          tmem_ld16(tmem + G::O_COL + lane_off + 16 * u, x);
-#pragma unroll
-          for (int i = 0; i < 16; i++) y[i] = __uint_as_float(x[i]) * f0;
-          if (nsteps > 1) {
-            tmem_ld16(tmem + G::O_COL + D + lane_off + 16 * u, x);
-#pragma unroll
-            for (int i = 0; i < 16; i++) y[i] = fmaf(__uint_as_float(x[i]), f1, y[i]);
-          }
-          if (!rok) continue;
-          if (o_dst) {
-#pragma unroll
-            for (int i = 0; i < 16; i += 8) st_sector(o_dst + 16 * u + i, y + i);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; i += 8)
-              *reinterpret_cast<uint4*>(orow + 16 * u + i) =
-                  make_uint4(pack_bf16x2_rn(y[i], y[i + 1]), pack_bf16x2_rn(y[i + 2], y[i + 3]),
-                             pack_bf16x2_rn(y[i + 4], y[i + 5]), pack_bf16x2_rn(y[i + 6], y[i + 7]));
-          }
-        }
-        if (rok && hf == 0 && kh == 0) {
-          if (ml_dst) *reinterpret_cast<float2*>(ml_dst) = make_float2(M, L2);
-          else if (c.sh.lse) c.sh.lse[(q0 + tok0 + j) * c.sh.lse_stride + head_row] = log_sum_exp(M, L2);
-        }
-        row_sync();  // both accumulators and the exchange have been read
-        continue;
       }
       constexpr int UNITS = D / 32, FIRST = (UNITS + 1) / 2;  // of 32 columns; the first key half's
       float *piece_o = pv.piece_o, *piece_ml = pv.piece_ml;
@@ -748,18 +667,13 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
         int itn = n_items;
         if (lane == 0 && !*abort_flag) itn = atomicAdd(&pv.plan[2], 1);
         const PrefillItem item = prefill_piece_item(c, pv, __shfl_sync(0xffffffffu, itn, 0), n_items);
-        int split = 0;
-        if constexpr (SH && G::H == 2) {
-          if (item.seq >= 0)
-            split = min(c.tile_tokens, pv.vrec[2 * item.seq].y - item.tile * c.tile_tokens) * c.group <= 128 ? 1 << 30 : 0;
-        }
         if (lane == 0) {
           int* s = sitem + 6 * e;
           s[0] = item.seq;
           s[1] = item.h;
           s[2] = item.tile;
           s[3] = item.kb0;
-          s[4] = item.nkb | split;
+          s[4] = item.nkb;
           s[5] = item.row;
           fp8_arrive(bar(IFULL + e));
         }
@@ -836,18 +750,17 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
       // ================= MMA warp =================
       uint32_t lead;
       asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(lead));
-      int n = 0, items = 0;
-      uint32_t pfull = 0;  // parities of PFULL's halves
+      int n = 0, items = 0, pfull = 0;
       const uint64_t dq = umma_desc(smem_addr(sQ), 16, 1024);
       const uint64_t dk = umma_desc(smem_addr(sK), 16, 1024);
       const uint64_t dv = umma_desc(smem_addr(sV), NK * 128, 1024);
       const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);  // in a uniform register
       auto wait = [&](int i, uint32_t parity) { fp8_wait_warp(bar(i), parity, abort_flag, c.status); };
-      auto issue_s = [&](int hh, int b, int rows_of) {
+      auto issue_s = [&](int hh, int b) {
         const uint64_t kt = dk + (uint64_t)(b * (G::KVBYTES >> 4));
 #pragma unroll
         for (int ks = 0; ks < KSTEPS; ks++)
-          fp8_mma(lead, tm + NK * hh, dq + (uint64_t)(((ks >> 2) * ROWS * 128 + rows_of * 128 * 128 + (ks & 3) * 32) >> 4),
+          fp8_mma(lead, tm + NK * hh, dq + (uint64_t)(((ks >> 2) * ROWS * 128 + hh * 128 * 128 + (ks & 3) * 32) >> 4),
                   kt + (uint64_t)(((ks >> 2) * NK * 128 + (ks & 3) * 32) >> 4), IDESC_S, ks > 0);
       };
       auto issue_wv = [&](int hh, int b, bool first) {
@@ -875,39 +788,6 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
           wait(QFULL, items & 1);
           items++;
         }
-        if constexpr (SH && G::H == 2) {
-          // in turns: iteration st is half st & 1's, the WV of step st - 2 and the S of
-          // step st
-          const int turns = __reduce_min_sync(0xffffffffu, item.split ? 1 : 0);
-          if (turns && nsteps > 0) {
-#pragma unroll 1
-            for (int st = 0; st < nsteps + 2; st++, n++) {
-              const int hh = st & 1;
-              const bool wv = st > 1, sc = st < nsteps;  // step n - 2 has tiles of the same parity
-              {
-                const int i = lane == 0 ? VFULL + (n & 1) : lane == 1 ? PFULL + hh : KFULL + (n & 1);
-                const uint32_t ph = lane == 0 ? ((n - 2) >> 1) & 1 : lane == 1 ? pfull >> hh & 1 : (n >> 1) & 1;
-                fp8_wait_warp(bar(i), ph, abort_flag, c.status, lane > 2 || !(lane == 2 ? sc : wv));
-              }
-              tc_fence_after();
-              if (wv) {
-                if (hh) issue_wv(1, n & 1, st < 4);
-                else issue_wv(0, n & 1, st < 4);
-                fp8_commit(lead, bar(VFREE + (n & 1)));
-                pfull ^= 1u << hh;
-              }
-              if (sc) {
-                if (hh) issue_s(1, n & 1, 0);
-                else issue_s(0, n & 1, 0);
-                fp8_commit(lead, bar(SFULL + hh));
-                fp8_commit(lead, bar(KFREE + (n & 1)));
-              }
-            }
-            n -= 2;
-            fp8_commit(lead, bar(ODONE));
-            continue;
-          }
-        }
         // iteration st: for each half, the WV of step st - 1 and the S of step
         // st.  A wait costs the warp some 400 cycles even when it is satisfied,
         // so the first half's three barriers are waited for at once, a lane each
@@ -923,18 +803,18 @@ __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
           }
 #pragma unroll 1
           for (int hh = 0; hh < G::H; hh++) {
-            if (wv && hh) wait(PFULL + 1, pfull >> 1 & 1);
+            if (wv && hh) wait(PFULL + 1, pfull & 1);
             tc_fence_after();
             if (wv) {
               issue_wv(hh, (n - 1) & 1, st == 1);
               if (hh == G::H - 1) fp8_commit(lead, bar(VFREE + ((n - 1) & 1)));
             }
             if (sc) {
-              issue_s(hh, n & 1, hh);
+              issue_s(hh, n & 1);
               fp8_commit(lead, bar(SFULL + hh));
             }
           }
-          if (wv) pfull ^= G::H == 2 ? 3u : 1u;
+          if (wv) pfull++;
           if (sc) {
             fp8_commit(lead, bar(KFREE + (n & 1)));
             n++;

@@ -204,14 +204,13 @@ struct PrefillItem {
   int seq, h, tile;  // seq -1: past the last item
   int kb0, nkb;      // blocks [kb0, nkb)
   int row;           // first piece row, -1 if the tile is whole
-  bool split;        // SH: the halves take the steps in turn (prefill_ws_fp8.cuh)
 };
 __device__ __forceinline__ PrefillItem prefill_piece_item(const Common& c, const PlanView& pv, int itn, int n_items) {
-  if (itn >= n_items) return PrefillItem{-1, 0, 0, 0, 0, -1, false};
+  if (itn >= n_items) return PrefillItem{-1, 0, 0, 0, 0, -1};
   const int pi = itn / c.hkv, h = itn - pi * c.hkv;
   const int4 a = reinterpret_cast<const int4*>(pv.pieces + pi)[0];
   const int2 b = reinterpret_cast<const int2*>(pv.pieces + pi)[2];
-  return PrefillItem{a.x, h, a.y, a.z, a.w, b.x < 0 ? -1 : b.x + h * b.y, false};
+  return PrefillItem{a.x, h, a.y, a.z, a.w, b.x < 0 ? -1 : b.x + h * b.y};
 }
 
 constexpr int kPrepThreads = 256;  // threads of the CTA that builds the schedule
