@@ -93,8 +93,12 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 // lane loads its eight columns of the row of every axis that owns one of its
 // pairs: one row where the axes' pairs lie side by side, up to num_axes where they
 // take turns.
-template <int D, int U, bool AXES>
-__global__ void __launch_bounds__(kNormWarps * 32, AXES ? 7 : 8) norm_rope_kernel(NormRope p) {
+// WHOLE: a warp keeps them for all heads of a token, so that they are fetched once
+// per token.  Without it 40 heads of 128 over three axes take 7.0 us for 1024 tokens
+// (with it 9.3: too few warps), 18.7 for 4096 (18.5), 28.1 for 6000 (24.2) and 72.0
+// for 16384 (61.3, 5.5 TB/s); the rule takes it from 32 tokens per SM.
+template <int D, int U, bool AXES, bool WHOLE>
+__global__ void __launch_bounds__(kNormWarps * 32, WHOLE ? 6 : AXES ? 7 : 8) norm_rope_kernel(NormRope p) {
   constexpr int LPV = D / 16;    // lanes per vector
   constexpr int VPW = 32 / LPV;  // vectors per warp step
   const NormRopeArgs& a = p.a;
@@ -104,7 +108,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, AXES ? 7 : 8) norm_rope_kerne
   const int gw = blockIdx.x * kNormWarps + (threadIdx.x >> 5);
   const int t = (int)p.by_parts.div((uint32_t)gw);
   if (t >= a.num_tokens) return;
-  const int part = gw - t * p.parts;
+  const int part0 = gw - t * p.parts;
   const int vsub = lane / LPV, c = lane - vsub * LPV;
   const bool rotated = c < a.rot_dim / 16;
   // the lane's two chunks (of 8 elements)
@@ -113,19 +117,22 @@ __global__ void __launch_bounds__(kNormWarps * 32, AXES ? 7 : 8) norm_rope_kerne
 
   uint4 x[U][2];
   int head[U];
+  auto load = [&](int part) {
 #pragma unroll
-  for (int u = 0; u < U; u++) {
-    head[u] = (part * U + u) * VPW + vsub;
-    if (vsub >= VPW || head[u] >= p.heads) head[u] = -1;
-    x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
-    if (head[u] >= 0) {
-      const uint16_t* src = head[u] < a.num_q_heads
-                                ? static_cast<const uint16_t*>(a.q) + t * a.q_stride + (int64_t)head[u] * D
-                                : static_cast<const uint16_t*>(a.k) + t * a.k_stride + (int64_t)(head[u] - a.num_q_heads) * D;
-      x[u][0] = __ldcs(reinterpret_cast<const uint4*>(src + 8 * c0));
-      x[u][1] = __ldcs(reinterpret_cast<const uint4*>(src + 8 * c1));
+    for (int u = 0; u < U; u++) {
+      head[u] = (part * U + u) * VPW + vsub;
+      if (vsub >= VPW || head[u] >= p.heads) head[u] = -1;
+      x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
+      if (head[u] >= 0) {
+        const uint16_t* src = head[u] < a.num_q_heads
+                                  ? static_cast<const uint16_t*>(a.q) + t * a.q_stride + (int64_t)head[u] * D
+                                  : static_cast<const uint16_t*>(a.k) + t * a.k_stride + (int64_t)(head[u] - a.num_q_heads) * D;
+        x[u][0] = __ldcs(reinterpret_cast<const uint4*>(src + 8 * c0));
+        x[u][1] = __ldcs(reinterpret_cast<const uint4*>(src + 8 * c1));
+      }
     }
-  }
+  };
+  load(part0);
   float cs[8], sn[8];
 #pragma unroll
   for (int i = 0; i < 8; i++) {
@@ -159,78 +166,88 @@ __global__ void __launch_bounds__(kNormWarps * 32, AXES ? 7 : 8) norm_rope_kerne
         if (rotated && !bad && pairs) load_row(pos, pairs);
       }
       if (bad) {
-        if (part == 0 && lane == 0) flag(a.dev_status, KV_INT4_DEV_BAD_POS);
+        if (part0 == 0 && lane == 0) flag(a.dev_status, KV_INT4_DEV_BAD_POS);
         return;
       }
     } else {
       const int64_t pos = a.positions[t];
       if (pos < 0 || pos >= a.max_position) {
-        if (part == 0 && lane == 0) flag(a.dev_status, KV_INT4_DEV_BAD_POS);
+        if (part0 == 0 && lane == 0) flag(a.dev_status, KV_INT4_DEV_BAD_POS);
         return;
       }
       if (rotated) load_row(pos, 0);
     }
   }
+  auto turn = [&]() {
 #pragma unroll
-  for (int u = 0; u < U; u++) {
-    float f0[8], f1[8];
-    unpack8(x[u][0], f0);
-    unpack8(x[u][1], f1);
-    const bool isq = head[u] < a.num_q_heads;
-    if (a.q_weight) {  // both weights or neither
-      float s = 0.f;
+    for (int u = 0; u < U; u++) {
+      float f0[8], f1[8];
+      unpack8(x[u][0], f0);
+      unpack8(x[u][1], f1);
+      const bool isq = head[u] < a.num_q_heads;
+      if (a.q_weight) {  // both weights or neither
+        float s = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; i++) s = fmaf(f0[i], f0[i], fmaf(f1[i], f1[i], s));
-      const int base = vsub * LPV < 32 - LPV ? vsub * LPV : 32 - LPV;
-      s = vector_sum<LPV>(s, base, c);
-      const float mean = s * (1.f / D) + a.eps;
-      float r = rsqrtf(mean);
-      const bool far = mean > 0x1p120f || mean < 0x1p-80f;
-      if (__any_sync(0xffffffffu, far)) {
-        const float rf = far_rsqrt<D, LPV>(f0, f1, a.eps, base, c);
-        if (far) r = rf;
-      }
-      const uint16_t* w = static_cast<const uint16_t*>(isq ? a.q_weight : a.k_weight);
-      float w0[8], w1[8];
-      unpack8(*reinterpret_cast<const uint4*>(w + 8 * c0), w0);
-      unpack8(*reinterpret_cast<const uint4*>(w + 8 * c1), w1);
-#pragma unroll
-      for (int i = 0; i < 8; i++) {
-        f0[i] = f0[i] * r * w0[i];
-        f1[i] = f1[i] * r * w1[i];
-      }
-    }
-    if (rotated) {
-      if (!a.interleaved) {
+        for (int i = 0; i < 8; i++) s = fmaf(f0[i], f0[i], fmaf(f1[i], f1[i], s));
+        const int base = vsub * LPV < 32 - LPV ? vsub * LPV : 32 - LPV;
+        s = vector_sum<LPV>(s, base, c);
+        const float mean = s * (1.f / D) + a.eps;
+        float r = rsqrtf(mean);
+        const bool far = mean > 0x1p120f || mean < 0x1p-80f;
+        if (__any_sync(0xffffffffu, far)) {
+          const float rf = far_rsqrt<D, LPV>(f0, f1, a.eps, base, c);
+          if (far) r = rf;
+        }
+        const uint16_t* w = static_cast<const uint16_t*>(isq ? a.q_weight : a.k_weight);
+        float w0[8], w1[8];
+        unpack8(*reinterpret_cast<const uint4*>(w + 8 * c0), w0);
+        unpack8(*reinterpret_cast<const uint4*>(w + 8 * c1), w1);
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-          const float y0 = f0[i], y1 = f1[i];
-          f0[i] = y0 * cs[i] - y1 * sn[i];
-          f1[i] = y1 * cs[i] + y0 * sn[i];
+          f0[i] = f0[i] * r * w0[i];
+          f1[i] = f1[i] * r * w1[i];
         }
-      } else {
+      }
+      if (rotated) {
+        if (!a.interleaved) {
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const float y0 = f0[2 * i], y1 = f0[2 * i + 1], z0 = f1[2 * i], z1 = f1[2 * i + 1];
-          f0[2 * i] = y0 * cs[i] - y1 * sn[i];
-          f0[2 * i + 1] = y1 * cs[i] + y0 * sn[i];
-          f1[2 * i] = z0 * cs[4 + i] - z1 * sn[4 + i];
-          f1[2 * i + 1] = z1 * cs[4 + i] + z0 * sn[4 + i];
+          for (int i = 0; i < 8; i++) {
+            const float y0 = f0[i], y1 = f1[i];
+            f0[i] = y0 * cs[i] - y1 * sn[i];
+            f1[i] = y1 * cs[i] + y0 * sn[i];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            const float y0 = f0[2 * i], y1 = f0[2 * i + 1], z0 = f1[2 * i], z1 = f1[2 * i + 1];
+            f0[2 * i] = y0 * cs[i] - y1 * sn[i];
+            f0[2 * i + 1] = y1 * cs[i] + y0 * sn[i];
+            f1[2 * i] = z0 * cs[4 + i] - z1 * sn[4 + i];
+            f1[2 * i + 1] = z1 * cs[4 + i] + z0 * sn[4 + i];
+          }
+        }
+      }
+      if (head[u] >= 0) {
+        uint16_t* dst = isq ? static_cast<uint16_t*>(a.q_out) + t * a.q_out_stride + (int64_t)head[u] * D
+                            : static_cast<uint16_t*>(a.k_out) + t * a.k_out_stride + (int64_t)(head[u] - a.num_q_heads) * D;
+        uint4* const d0 = reinterpret_cast<uint4*>(dst + 8 * c0);
+        uint4* const d1 = reinterpret_cast<uint4*>(dst + 8 * c1);
+        if (p.stream_out) {
+          __stcs(d0, pack8(f0));
+          __stcs(d1, pack8(f1));
+        } else {
+          *d0 = pack8(f0);
+          *d1 = pack8(f1);
         }
       }
     }
-    if (head[u] >= 0) {
-      uint16_t* dst = isq ? static_cast<uint16_t*>(a.q_out) + t * a.q_out_stride + (int64_t)head[u] * D
-                          : static_cast<uint16_t*>(a.k_out) + t * a.k_out_stride + (int64_t)(head[u] - a.num_q_heads) * D;
-      uint4* const d0 = reinterpret_cast<uint4*>(dst + 8 * c0);
-      uint4* const d1 = reinterpret_cast<uint4*>(dst + 8 * c1);
-      if (p.stream_out) {
-        __stcs(d0, pack8(f0));
-        __stcs(d1, pack8(f1));
-      } else {
-        *d0 = pack8(f0);
-        *d1 = pack8(f1);
-      }
+  };
+  turn();
+  if constexpr (WHOLE) {
+#pragma unroll 1
+    for (int part = 1; part * U * VPW < p.heads; part++) {
+      load(part);
+      turn();
     }
   }
 }
@@ -243,10 +260,15 @@ int launch_t(const NormRopeArgs& a, cudaStream_t stream) {
   p.heads = a.num_q_heads + a.num_kv_heads;
   p.stream_out = (int64_t)a.num_tokens * p.heads * D * 2 > (48ll << 20);  // of 126 MB of L2
   p.parts = (p.heads + VPW * U - 1) / (VPW * U);
+  const bool axes = a.num_axes > 0 && a.rot_dim > 0;
+  const bool whole = axes && p.parts > 1 && a.num_tokens >= 32 * sm_count(current_device());
+  if (whole) p.parts = 1;
   p.by_parts = FastDiv((uint32_t)p.parts);
   const int64_t warps = (int64_t)a.num_tokens * p.parts;
   if (warps >= (1ll << 31) - kNormWarps) return KV_INT4_ERR_SIZE;
-  return launch_pdl(a.num_axes > 0 && a.rot_dim > 0 ? norm_rope_kernel<D, U, true> : norm_rope_kernel<D, U, false>,
+  return launch_pdl(whole  ? norm_rope_kernel<D, U, true, true>
+                    : axes ? norm_rope_kernel<D, U, true, false>
+                           : norm_rope_kernel<D, U, false, false>,
                     dim3((unsigned)((warps + kNormWarps - 1) / kNormWarps)), kNormWarps * 32, 0,
                     stream, 1, p);
 }

@@ -124,6 +124,27 @@ def test_a_bad_position_along_any_axis_leaves_its_rows(axis):
             assert (got[t] == 7).all() if t in (2, 5) else torch.equal(got[t], ref[t])
 
 
+@pytest.mark.parametrize("d", HEADS)
+def test_many_tokens_have_the_bits_of_few(d):
+    """Above 32 tokens per SM a warp takes all heads of a token; in place, with bad positions among them."""
+    t, hq, hkv = 32 * torch.cuda.get_device_properties(0).multi_processor_count + 7, 7, 6
+    q, k, pos, table, w = _inputs(t, hq, hkv, d, d // 2, 3)
+    pairs = kv.rope_axes((d // 8, d // 16, d // 16), turns=True)
+    pos[1, 11::97] = 50
+    args = [x.cuda() for x in (q, k, pos, table)]
+    dw = [x.cuda() for x in w]
+    want = [x.clone() for x in args[:2]]
+    for i in range(0, t, 700):
+        rows = slice(i, min(t, i + 700))
+        kv.qk_norm_rope_axes(args[0][rows], args[1][rows], args[2][:, rows], args[3], pairs, *dw, 1e-6,
+                             want[0][rows], want[1][rows])
+    kv.qk_norm_rope_axes(*args, pairs, *dw, 1e-6, args[0], args[1])
+    assert torch.equal(args[0], want[0]) and torch.equal(args[1], want[1])
+    assert torch.equal(args[0][11::97].cpu(), q[11::97])
+    some = slice(4000, 4040)
+    _check(args[0][some].cpu()[:10], q[some][:10], w[0], 1e-6, table, pos[:, some][:, :10], pairs, False)
+
+
 def test_streams_graph_and_ctypes_give_the_same_bits(monkeypatch):
     q, k, pos, table, w = _inputs(40, 8, 2, 128, 64, 3)
     pairs = kv.rope_axes((12, 10, 10))
