@@ -57,6 +57,10 @@ bool kvint4::shared_layout(int num_seqs, int num_groups, int num_q_tokens, int n
     L->base.direct_o = take(columns * head_size * 4);
     L->base.direct_ml = take(columns * 2 * 4);
   }
+  if (num_groups > 0) {  // a group's columns fill more warps' slots than one token's
+    L->base.warp_o = take((size_t)kSharedDecodeWarps * kDecodeCols * head_size * 4);
+    L->base.warp_ml = take((size_t)kSharedDecodeWarps * kDecodeCols * 2 * 4);
+  }
   L->vrec = take(V * 32);
   L->dseq2 = take(V * 16);
   L->vinfo = take(V * 8);

@@ -402,7 +402,8 @@ int launch_t(const SharedAttnArgs& s, cudaStream_t stream) {
     if (!with_np(np, cg, take)) return KV_INT4_ERR_CUDA;
     c.ng = a.num_kv_heads / c.hg;
     long long grid = (long long)sms * occ;
-    if (grid * c.hg * cg > kMaxDecodeWarps) grid = kMaxDecodeWarps / (c.hg * cg);
+    const int most_warps = s.num_groups > 0 ? kSharedDecodeWarps : kMaxDecodeWarps;  // as the workspace has slots
+    if (grid * c.hg * cg > most_warps) grid = most_warps / (c.hg * cg);
     for (int l = (int)(grid < c.ng ? grid : c.ng); l >= 1; l--)
       if (c.ng % l == 0) {
         c.nl = l;

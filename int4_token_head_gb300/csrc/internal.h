@@ -335,6 +335,7 @@ struct SharedLayout {
   size_t total;
   int row_tokens;  // query tokens in groups that share
 };
+constexpr int kSharedDecodeWarps = 2 * kMaxDecodeWarps;
 constexpr int kSharedRows = 1 << 17;  // most rows (token x q head) of sequences that share
 constexpr int kMostGroups = 1024;
 bool shared_layout(int num_seqs, int num_groups, int num_q_tokens, int num_q_heads, int num_kv_heads, int head_size,

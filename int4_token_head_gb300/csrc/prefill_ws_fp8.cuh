@@ -227,7 +227,7 @@ struct Fp8Maps {
 };
 
 // SH: over virtual sequences (shared prefixes), and the rows' log-sum-exp.  A warp
-// without rows only keeps step (32 rows against 32768 keys: TODO).
+// without rows only keeps step.
 template <int D, bool SH = false>
 __global__ void __launch_bounds__(Fp8Ws<D>::THREADS, 1)
     prefill_ws_fp8_kernel(Common c, PlanView pv, const __grid_constant__ Fp8Maps maps) {

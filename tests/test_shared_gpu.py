@@ -84,7 +84,7 @@ def test_single_tokens(d, hq, hkv):
 def test_many_sequences_over_one_prefix(d, hq, hkv):
     """A group's rows in prefill tiles, the ends on the decode kernel beside them."""
     g = np.random.default_rng(d)
-    _check([(2400, [(1, int(n)) for n in g.integers(1, 90, 40)])], hq, hkv, d)
+    _check([(720, [(1, int(n)) for n in g.integers(1, 90, 34)])], hq, hkv, d)
 
 
 @pytest.mark.parametrize("d", HEADS)
