@@ -552,8 +552,8 @@ KVINT4_API int kv_fp8_attention_mass(const void* q, int64_t q_token_stride, cons
  *   max_blocks_per_seq * 16) positions (KV_INT4_ERR_SIZE otherwise).
  * mass, mass_out: float, strides in elements, positions contiguous, mass_len of
  *   them (mass_out: min(budget, mass_len), in rows that do not overlap:
- *   KV_INT4_ERR_SIZE otherwise); mass_out may be mass.  Other overlaps are not
- *   allowed.
+ *   KV_INT4_ERR_SIZE otherwise); mass_out may be mass, with its strides
+ *   (KV_INT4_ERR_SIZE otherwise).  Other overlaps are not allowed.
  * new_lens: int32 [num_seqs], not seq_lens (KV_INT4_ERR_SIZE).  kept: int32
  *   [num_seqs][num_kv_heads][budget].
  * budget >= 1, 0 <= recent <= budget (KV_INT4_ERR_SIZE otherwise).
@@ -697,7 +697,8 @@ KVINT4_API int kv_int4_selftest_wait(int iterations, int32_t* dev_status, uint64
  * entry points kv_int8_write / kv_int8_attention, sliding_window in the attention entry points;
  * 3: the in-slot entry points, kv_int4_attention_noalloc's window argument, kv_int4_selftest_wait;
  * 4: kv_int4_selftest_wait takes its stream as void*, like every other entry point; the kv_fp8_*
- * entry points and kv_qk_norm_rope came under version 4 too, which changed nothing that was there). */
+ * entry points, kv_qk_norm_rope and kv_qk_norm_rope_axes came under version 4 too, which changed
+ * nothing that was there). */
 KVINT4_API int kv_int4_version(void);
 
 #ifdef __cplusplus

@@ -326,6 +326,10 @@ int kv_fp8_evict(uint8_t* k_cache, uint8_t* v_cache, float* k_scale_cache, float
   if (e != KV_INT4_OK) return e;
   if (!aligned(mass, 4) || !aligned(mass_out, 4) || !aligned(kept, 4) || !aligned(dst_block_table, 4))
     return KV_INT4_ERR_ALIGN;
+  // in place only row by row
+  if (mass_out == mass && ((num_seqs > 1 && mass_out_seq_stride != mass_seq_stride) ||
+                           (num_kv_heads > 1 && mass_out_head_stride != mass_head_stride)))
+    return KV_INT4_ERR_SIZE;
   if (new_lens == seq_lens || !rows_apart(num_seqs, mass_out_seq_stride, num_kv_heads, mass_out_head_stride,
                                           most < budget ? most : budget))
     return KV_INT4_ERR_SIZE;
