@@ -264,7 +264,12 @@ __device__ __forceinline__ bool schedule_seq_ok(const Common& c, int q0, int ql,
 // in pieces 55.3; not so beside shared prefixes, whose tiles are most of the work:
 // 64 sequences over 8192 positions 63 us, without 59).  If there are fewer tiles than CTAs, an S up to twice as
 // large whose pieces all run at once is taken; without one, only tiles of more
-// than two shares are worth it.  Everything follows from the call's lengths
+// than two shares are worth it.
+// With shared prefixes (SH) a few long tiles meet many short ones, a sequence's
+// own, which fit beside them: the S is taken whose longest pieces are done first,
+// wave by wave (16 questions to one prefix of 16384 positions, 16/4 heads of 192: 80
+// pieces of 64 steps and 64 short tiles, which by the rule above must all run at
+// once, 144 us; 140 pieces of 37 steps 103).  Everything follows from the call's lengths
 // alone, so results do not depend on the order of arrival.  Batches of more
 // than kSplitTiles tiles, or of kSplitWaves items per CTA, which the order by
 // length balances, keep their tiles whole.  `seqs`: the prefill sequences in
@@ -331,7 +336,36 @@ __device__ void build_pieces(const Common& c, const PlanView& pv, int n_pseq, in
     const long long share = div_nn(sum * c.hkv + c.split_ctas - 1, c.split_ctas);
     const long long S0 = max(share, (long long)c.split_steps << (with_decode && !SH ? 1 : 0));
     const bool one_wave = (long long)n_tiles * c.hkv < c.split_ctas;
-    if (longest > (one_wave ? S0 : 2 * S0)) {  // else every tile stays whole
+    if (SH && longest > S0) {
+      constexpr int W = kPrepThreads / 32;
+      constexpr float PIECE = 4.f;  // steps' time that an item takes on top of its own
+      const int cand = (int)min(warp == W - 1 ? (long long)longest : warp == W - 2 ? 4 * S0 : S0 + S0 * warp / (W - 3),
+                                (long long)longest);
+      int r = 0, all = 0, most = 0;  // rows of the pieces, all items, the long ones (of one kv head)
+#pragma unroll 1
+      for (int i = lane; i < n_tiles; i += 32) {
+        const int n = steps_of(tiles[i]), P = n > cand ? min((n - 1) / cand + 1, 2 * kMaxPieces) : 1;
+        all += P;
+        if (2 * n > P * cand) most += P;
+        if (P > 1) r += P * tile_rows[i];
+      }
+      r = __reduce_add_sync(0xffffffffu, r);
+      all = __reduce_add_sync(0xffffffffu, all);
+      most = __reduce_add_sync(0xffffffffu, most);
+      if (lane == 0) {
+        const float heads = (float)c.hkv / c.split_ctas;
+        const float time = fmaxf(ceilf(most * heads) * (cand + PIECE), ((float)sum + PIECE * all) * heads);
+        s_cand[warp] = make_int2(cand, all > kMaxPieces || (long long)r * c.hkv > kPieceRows ? INT_MAX : __float_as_int(time));
+      }
+      __syncthreads();
+      int best = INT_MAX;
+#pragma unroll 1
+      for (int i = 0; i < W; i++)
+        if (s_cand[i].y < best) {
+          best = s_cand[i].y;
+          S = s_cand[i].x;
+        }
+    } else if (!SH && longest > (one_wave ? S0 : 2 * S0)) {  // else every tile stays whole
       constexpr int W = kPrepThreads / 32;
       const int cand = (int)min(warp == W - 1 ? 4 * S0 : S0 + (S0 * warp + W - 3) / (W - 2), (long long)INT_MAX);
       long long p = 0, r = 0, all = 0;  // pieces of split tiles, their rows, all entries
