@@ -65,7 +65,7 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
   // the registers are outputs so that no use of them moves before the wait
   asm volatile("tcgen05.wait::ld.sync.aligned;\n"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
 }
 
 template <int D>
@@ -322,9 +322,11 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
     const int grid = gridDim.x, hkv = a.num_kv_heads;
     int n = 0, nq = 0;  // items handed on, Q tiles copied
     MassItem held{-1, 0, 0, 0, 0, 0, 0, 0};
-    auto copies = [&]() {  // the Q tiles of the item that was handed on before
+    int copied = 0;
+    auto copies = [&](int count) {  // Q tiles of the item that was handed on before, up to `count`
 #pragma unroll 1
-      for (int t = 0; t < held.tiles && held.seq >= 0; t++, nq++) {
+      for (; copied < count && held.seq >= 0; copied++, nq++) {
+        const int t = copied;
         const int s = nq % NQ;
         if (nq >= NQ) fp8_wait(bar(QFREE + s), (nq / NQ - 1) & 1, abort_flag, a.dev_status);
         if (__any_sync(0xffffffffu, *abort_flag)) return;
@@ -349,8 +351,10 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
       }
       __syncwarp();
       n++;
-      copies();  // one item behind, so that the next one's codes are converted meanwhile
+      copies(held.tiles);  // one item behind, so that the next one's codes are converted meanwhile
       held = it;
+      copied = 0;
+      if (n == 1) copies(min(it.tiles, NQ));
     };
     auto item = [&](int seq, int head, int kt) {
       const int q0 = a.query_start_loc[seq], ql = a.query_start_loc[seq + 1] - q0, len = a.seq_lens[seq];
