@@ -11,7 +11,7 @@ from ._lib import (DEV_BAD_BLOCK, DEV_BAD_POS, DEV_BAD_SEQ, DEV_BAD_SIGNS, DEV_B
                    attention_workspace_size, evict_fp8, library_path, load, qk_norm_rope, qk_norm_rope_axes, read_fp8, rope_axes, status_string, write, write_fp8)
 
 __all__ = ["write", "attention", "write_fp8", "read_fp8", "attention_fp8", "attention_fp8_shared", "attention_mass_fp8",
-           "evict_fp8",            "qk_norm_rope", "qk_norm_rope_axes", "rope_axes",
+           "evict_fp8", "qk_norm_rope", "qk_norm_rope_axes", "rope_axes",
            "attention_workspace_size", "attention_shared_workspace_size", "load", "library_path",
            "status_string", "KvInt4Error", "DEV_BAD_SLOT", "DEV_BAD_BLOCK", "DEV_BAD_SEQ", "DEV_BAD_SIGNS",
            "DEV_NONFINITE", "DEV_BAD_POS"]

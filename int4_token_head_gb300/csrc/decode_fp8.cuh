@@ -145,7 +145,9 @@ __device__ __forceinline__ float ld_cluster(const float* p, int rank) {
 // for batches whose shares are short (latency counts there, not balance).
 // SH: over virtual sequences (shared prefixes), and the rows' log-sum-exp.
 // GW: column groups of eight per warp, which converts a code once for all of them
-// and finds their query fragments in shared memory (behind the ring).
+// and finds their query fragments in shared memory (behind the ring): 8 sequences
+// over one of four prefixes of 32768 positions, 32 columns per kv head, 135 us; a
+// warp per column group, which converts each code four times, 157.
 template <int D, int NP, int CG, bool DIRECT, bool SH = false, int GW = 1>
 __global__ void __launch_bounds__(128) decode_fp8_kernel(Fp8DecParams prm) {
   using G = Fp8Dec<D, NP>;
