@@ -5,22 +5,27 @@
 // S = K Q^T with a tile of QR query rows as N, so that a key is a TMEM lane and
 // the sum over the rows stays in one thread: per score one fma (the key's factor,
 // the row's -lse log2 e), one exp2 and one add, and nothing crosses threads until
-// an item's four partial sums meet.  Warps in four roles that meet at mbarriers:
+// an item's four partial sums meet.  Row tiles are numbered over all items of a
+// CTA (g); warps in five roles that meet at mbarriers:
 //   * scheduler warp (20): the items of this CTA in an order that it computes by
-//     itself (below), through a ring of four; TMA copies of the Q tiles that see an
-//     item's keys (bf16, straight into the MMA's swizzled tile) into NQ slots;
+//     itself (below), through a ring of four;
+//   * copy warps (21, 22), even and odd g: TMA copies of the Q tiles that see an
+//     item's keys (bf16, straight into the MMA's swizzled tile) into slot g mod NQ;
 //   * convert warps (16-19): an item's codes from global memory into one of two bf16
 //     tiles, and its blocks' scales into the item's ring entry;
-//   * MMA warp (21): tile t of an item into the score buffer of warpgroup t mod 4;
-//   * sum warps (0-15): warpgroup w takes the tiles t = w mod 4; the rows' lse are
-//     loaded a tile ahead and shared through shared memory.
+//   * MMA warps (23, 24), even and odd g: a tile into the score buffer of warpgroup g
+//     mod 4.  NQ is even, so that a slot's and a buffer's barriers each have one
+//     warp that waits for them in turn;
+//   * sum warps (0-15): warpgroup g mod 4; the rows' lse are loaded a tile ahead
+//     and shared through shared memory.
 // Bounds are the exp2 of every score and the MMAs, alike: 512 cycles each for 128 x
-// 128 scores at head size 128.  Eight prompts of 512 to 2048 tokens, 32/8 heads: 68.8
-// us, a tile every 950 cycles and 1.5 us from an item to the next; both pipes are
-// active 0.40 of the time.  A warpgroup sums for 1400 cycles and waits for its next
-// scores as long, as it has one score buffer (TMEM is full).  Two warpgroups with two
-// buffers each took 90 us, four over items of 256 keys, which halve the copies of Q,
-// 81 (their longest items end too late); an MMA warp for every other tile 70.
+// 128 scores at head size 128.  Eight prompts of 512 to 2048 tokens, 32/8 heads: 66.4
+// us, a tile every 900 cycles and 1.5 us from an item to the next; both pipes are
+// active 0.43 of the time.  A warpgroup sums for 1700 cycles and has its next scores
+// 1200 after it has freed its one buffer (TMEM is full).  Not faster: two warpgroups
+// with two buffers each 90 us; items of 256 keys, which halve the copies of Q, 81
+// (the longest end too late); halves of a buffer freed by themselves, MMAs of 64
+// columns, 76; a buffer's scores, the copies or the exponents left out 63 to 73.
 //
 // Order of items: an item's work is the query rows that see it, which falls with
 // the key tile's index where the queries start at the front.  Items are taken by
@@ -38,11 +43,11 @@ struct MassWs {
   static constexpr int QR = D <= 128 ? 128 : 64;  // query rows per tile
   static constexpr int KB = (D + 63) / 64;        // 128-byte blocks of a bf16 head vector
   static constexpr int QBYTES = QR * 128 * KB, KBYTES = 128 * 128 * KB;
-  static constexpr int NQ = D == 256 ? 2 : 4;     // Q slots
+  static constexpr int NQ = D == 256 ? 2 : 4;     // Q slots, an even number
   static constexpr int NI = 4;                    // item ring
   static constexpr int S_COLS = 4 * QR;           // TMEM: a score buffer per warpgroup
   static constexpr int WG = 4;                    // warpgroups that sum
-  static constexpr int THREADS = (4 * WG + 6) * 32;
+  static constexpr int THREADS = (4 * WG + 9) * 32;
   // item ring entry: 8 ints, 8 scales
   static constexpr int ENTRY = 64;
   static constexpr int NBARS = 2 * NI + 2 * NQ + 4 + 2 * WG + NI + 1;
@@ -104,7 +109,7 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
   if (tid == 0) {
     for (int b = 0; b < NI; b++) {
       mbar_init(bar(IFULL + b), 1);
-      mbar_init(bar(IFREE + b), 4 * WG + 5);
+      mbar_init(bar(IFREE + b), 4 * WG + 8);
       mbar_init(bar(PART + b), 4 * (WG - 1));
     }
     for (int b = 0; b < NQ; b++) {
@@ -113,13 +118,13 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
     }
     for (int b = 0; b < 2; b++) {
       mbar_init(bar(KFULL + b), 4);
-      mbar_init(bar(KFREE + b), 1);
+      mbar_init(bar(KFREE + b), 2);
     }
     for (int b = 0; b < WG; b++) {
       mbar_init(bar(SFULL + b), 1);
       mbar_init(bar(SFREE + b), 4);
     }
-    mbar_init(bar(DRAIN), 1);
+    mbar_init(bar(DRAIN), 2);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -178,6 +183,12 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
           if (lane == 0) fp8_arrive(bar(SFREE + wg));
         }
         const uint32_t (&v)[16] = x[c & 1];
+        uint32_t vis = 0xffffu;  // the chunk's columns that see the key
+        if (MASKED) {
+          const int from = lo - 16 * c, to = hi - 16 * c;
+          vis = from <= 0 ? 0xffffu : from >= 16 ? 0u : 0xffffu << from;
+          vis &= to >= 16 ? 0xffffu : to <= 0 ? 0u : 0xffffu >> (16 - to);
+        }
 #pragma unroll
         for (int k = 0; k < 16; k += 4) {
           const float4 b = *reinterpret_cast<const float4*>(nl + 16 * c + k);
@@ -185,11 +196,10 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
           const float2 t1 = f2fma(make_float2(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), ff, make_float2(b.z, b.w));
           float2 e0 = make_float2(fast_exp2(t0.x), fast_exp2(t0.y)), e1 = make_float2(fast_exp2(t1.x), fast_exp2(t1.y));
           if (MASKED) {
-            const int q = 16 * c + k;
-            e0.x = q >= lo && q < hi ? e0.x : 0.f;
-            e0.y = q + 1 >= lo && q + 1 < hi ? e0.y : 0.f;
-            e1.x = q + 2 >= lo && q + 2 < hi ? e1.x : 0.f;
-            e1.y = q + 3 >= lo && q + 3 < hi ? e1.y : 0.f;
+            e0.x = vis & (1u << k) ? e0.x : 0.f;
+            e0.y = vis & (2u << k) ? e0.y : 0.f;
+            e1.x = vis & (4u << k) ? e1.x : 0.f;
+            e1.y = vis & (8u << k) ? e1.y : 0.f;
           }
           s0 = f2add(s0, e0);
           s1 = f2add(s1, e1);
@@ -211,7 +221,8 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
       return x;
     };
     MassItem it = take_all(0);
-    float l = row_lse(it, wg);
+    int first = wg, before = 0;  // this warpgroup's first tile of the item, row tiles of earlier items
+    float l = row_lse(it, first);
     int cnt = 0;  // tiles of this warpgroup
 #pragma unroll 1
     for (int n = 0; it.seq >= 0; n++) {
@@ -222,9 +233,11 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
       if (wg == 0 && pos < ctx) old = *out;
       float w = 0.f, f = 0.f;
       MassItem next{-1, 0, 0, 0, 0, 0, 0, 0};
+      before += it.tiles;
+      const int next_first = (wg - before) & (WG - 1);
       bool taken = false;
 #pragma unroll 1
-      for (int t = wg; t < it.tiles; t += WG, cnt++) {
+      for (int t = first; t < it.tiles; t += WG, cnt++) {
         float* const nl = nls + (cnt & 1) * 128;
         nl[r] = fabsf(l) == INFINITY ? -INFINITY : -l * kLog2e;
         if (t + WG < it.tiles) {
@@ -232,12 +245,12 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
         } else {
           next = take_all(n + 1);
           taken = true;
-          l = row_lse(next, wg);
+          l = row_lse(next, next_first);
         }
         asm volatile("bar.sync %0, 128;\n" ::"r"(1 + wg) : "memory");
         fp8_wait(bar(SFULL + wg), cnt & 1, abort_flag, a.dev_status);
         tc_fence_after();
-        if (t == wg) f = p.qscale * reinterpret_cast<const float*>(entry(e) + 8)[r >> 4];
+        if (t == first) f = p.qscale * reinterpret_cast<const float*>(entry(e) + 8)[r >> 4];
         const int tok = it.tok0 + t * tile_tokens;
         // this key is hidden from columns before `lo` and there are none from `hi` on
         const int lo = (pos - ctx - tok) * p.group, hi = min(tile_tokens, it.ql - tok) * p.group;
@@ -248,7 +261,7 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
       }
       if (!taken) {
         next = take_all(n + 1);
-        l = row_lse(next, wg);
+        l = row_lse(next, next_first);
       }
       float* const part = spart + e * (WG - 1) * 128 + r;
       if (wg > 0) {
@@ -265,6 +278,7 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
       __syncwarp();
       if (lane == 0) fp8_arrive(bar(IFREE + e));
       it = next;
+      first = next_first;
     }
   } else if (warp < 4 * WG + 4) {
     // ======================= codes =======================
@@ -323,28 +337,9 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
       }
     }
   } else if (warp == 4 * WG + 4) {
-    // ======================= scheduler, Q copies =======================
+    // ======================= scheduler =======================
     const int grid = gridDim.x, hkv = a.num_kv_heads;
-    int n = 0, nq = 0;  // items handed on, Q tiles copied
-    MassItem held{-1, 0, 0, 0, 0, 0, 0, 0};
-    int copied = 0;
-    auto copies = [&](int count) {  // Q tiles of the item that was handed on before, up to `count`
-#pragma unroll 1
-      for (; copied < count && held.seq >= 0; copied++, nq++) {
-        const int t = copied;
-        const int s = nq % NQ;
-        if (nq >= NQ) fp8_wait(bar(QFREE + s), (nq / NQ - 1) & 1, abort_flag, a.dev_status);
-        if (__any_sync(0xffffffffu, *abort_flag)) return;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar(QFULL + s), p.group * tile_tokens * 128 * G::KB);
-#pragma unroll
-          for (int x = 0; x < G::KB; x++)
-            tma_box3(smem_addr(sQ + s * G::QBYTES + x * QR * 128), &qmap, 64 * x, held.head * p.group,
-                     held.q0 + held.tok0 + t * tile_tokens, bar(QFULL + s));
-        }
-        __syncwarp();
-      }
-    };
+    int n = 0;  // items handed on
     auto hand_on = [&](const MassItem& it) {
       const int e = n % NI;
       if (n >= NI) fp8_wait(bar(IFREE + e), (n / NI - 1) & 1, abort_flag, a.dev_status);
@@ -356,10 +351,6 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
       }
       __syncwarp();
       n++;
-      copies(held.tiles);  // one item behind, so that the next one's codes are converted meanwhile
-      held = it;
-      copied = 0;
-      if (n == 1) copies(min(it.tiles, NQ));
     };
     auto item = [&](int seq, int head, int kt) {
       const int q0 = a.query_start_loc[seq], ql = a.query_start_loc[seq + 1] - q0, len = a.seq_lens[seq];
@@ -439,32 +430,57 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
       __syncwarp();  // the list is read before the next window's is written
     }
     hand_on(MassItem{-1, 0, 0, 0, 0, 0, 0, 0});
-    // every copy has landed before the CTA ends, after an abort too
-    for (int s = 0; s < NQ; s++) {
-      const int last = (nq - 1 - s) / NQ;  // the slot's last copy
-      if (nq > s && !mbar_wait_bounded(bar(QFULL + s), last & 1)) flag(a.dev_status, KV_INT4_DEV_TIMEOUT);
+  } else if (warp < 4 * WG + 7) {
+    // ============ Q copies: row tiles of even number (over all items), and odd ============
+    const int mine = warp - (4 * WG + 5);
+    int g = mine, end = 0, last = -1;  // next tile; of lane s: the last fill of slot s
+#pragma unroll 1
+    for (int n = 0;; n++) {
+      const MassItem it = take(n);
+      if (it.seq < 0) break;
+      const int begin = end;
+      end += it.tiles;
+#pragma unroll 1
+      for (; g < end; g += 2) {
+        const int s = g % NQ;
+        if (g >= NQ) fp8_wait(bar(QFREE + s), (g / NQ - 1) & 1, abort_flag, a.dev_status);
+        if (__any_sync(0xffffffffu, *abort_flag)) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(QFULL + s), p.group * tile_tokens * 128 * G::KB);
+#pragma unroll
+          for (int x = 0; x < G::KB; x++)
+            tma_box3(smem_addr(sQ + s * G::QBYTES + x * QR * 128), &qmap, 64 * x, it.head * p.group,
+                     it.q0 + it.tok0 + (g - begin) * tile_tokens, bar(QFULL + s));
+        }
+        if (lane == s) last = g / NQ;
+        __syncwarp();
+      }
+      __syncwarp();
+      if (lane == 0) fp8_arrive(bar(IFREE + n % NI));
     }
+    // every copy has landed before the CTA ends, after an abort too
+    if (last >= 0 && !mbar_wait_bounded(bar(QFULL + lane), last & 1)) flag(a.dev_status, KV_INT4_DEV_TIMEOUT);
   } else {
-    // ======================= MMA =======================
+    // ============ MMA: row tiles of even number, and odd ============
+    const int mine = warp - (4 * WG + 7);
     uint32_t lead;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(lead));
     const uint64_t dk = umma_desc(smem_addr(sK), 16, 1024), dq = umma_desc(smem_addr(sQ), 16, 1024);
     const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);  // in a uniform register
-    int nq = 0;
-    uint32_t used = 0, odd = 0;  // by score buffer: whether it has been, and an odd number of times
+    int g = mine, end = 0;  // next tile
 #pragma unroll 1
     for (int n = 0;; n++) {
       const MassItem it = take(n);
       if (it.seq < 0) break;
       fp8_wait_warp(bar(KFULL + (n & 1)), (n >> 1) & 1, abort_flag, a.dev_status);
       const uint64_t kt = dk + (uint64_t)((n & 1) * (G::KBYTES >> 4));
+      end += it.tiles;
 #pragma unroll 1
-      for (int t = 0; t < it.tiles; t++, nq++) {
-        const int s = nq % NQ, buf = t % WG;
+      for (; g < end; g += 2) {
+        const int s = g % NQ, buf = g % WG;
         // the tile's rows, and its score buffer
-        const int i = lane == 0 ? QFULL + s : SFREE + buf;
-        const uint32_t ph = lane == 0 ? (nq / NQ) & 1 : (odd >> buf & 1) ^ 1;
-        fp8_wait_warp(bar(i), ph, abort_flag, a.dev_status, lane > 1 || (lane == 1 && !(used >> buf & 1)));
+        fp8_wait_warp(bar(lane == 0 ? QFULL + s : SFREE + buf), lane == 0 ? (g / NQ) & 1 : (g / WG - 1) & 1, abort_flag,
+                      a.dev_status, lane > 1 || (lane == 1 && g < WG));
         tc_fence_after();
         const uint64_t qt = dq + (uint64_t)(s * (G::QBYTES >> 4));
 #pragma unroll
@@ -473,8 +489,6 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
                   qt + (uint64_t)(((ks >> 2) * QR * 128 + (ks & 3) * 32) >> 4), IDESC, ks > 0);
         fp8_commit(lead, bar(SFULL + buf));
         fp8_commit(lead, bar(QFREE + s));
-        used |= 1u << buf;
-        odd ^= 1u << buf;
       }
       fp8_commit(lead, bar(KFREE + (n & 1)));
       __syncwarp();
