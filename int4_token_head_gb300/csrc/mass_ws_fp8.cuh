@@ -252,9 +252,10 @@ __global__ void __launch_bounds__(MassWs<D>::THREADS, 1)
         tc_fence_after();
         if (t == first) f = p.qscale * reinterpret_cast<const float*>(entry(e) + 8)[r >> 4];
         const int tok = it.tok0 + t * tile_tokens;
-        // this key is hidden from columns before `lo` and there are none from `hi` on
-        const int lo = (pos - ctx - tok) * p.group, hi = min(tile_tokens, it.ql - tok) * p.group;
-        const bool full = __all_sync(0xffffffffu, lo <= 0) && hi == tile_rows;
+        // this key is hidden from columns before `lo` (0: from none; the distance to a far
+        // key times the group is more than 32 bits) and there are none from `hi` on
+        const int lo = max(pos - ctx - tok, 0) * p.group, hi = min(tile_tokens, it.ql - tok) * p.group;
+        const bool full = __all_sync(0xffffffffu, lo == 0) && hi == tile_rows;
         // two copies of the loop: a branch in it keeps its loads, exponentials and sums
         // from overlapping (2900 cycles a tile)
         w += full ? sum_tile(std::false_type{}, nl, f, lo, hi) : sum_tile(std::true_type{}, nl, f, lo, hi);

@@ -252,3 +252,23 @@ def test_repeats_streams_graphs_and_ctypes(monkeypatch, seqs):
     assert torch.equal(m, again)
     monkeypatch.setattr(_lib, "_fp8", _lib._Calls)
     assert torch.equal(_call(b, q, lse, mass, scale), want)
+
+
+def test_keys_farther_from_the_queries_than_32_bits_of_rows():
+    """64 rows to a token and 2^25 positions before the queries: distances times rows leave 32 bits.  The history
+    repeats four blocks, so that a position has the mass of its place among their 64."""
+    period, history = 64, (1 << 25) + 4096
+    b = Batch([(2, 2 * period + 2)], 1, 64).fill()
+    b.table[0, 4:8] = b.table[0, :4]
+    q, lse, mass, scale = _inputs(b, 64, lse=np.full((2, 64), 3.0))
+    mass[:] = 0
+    want, bound = F.mass(q.double().numpy(), lse.double().numpy(), b.kc, b.ks, b.table, b.lens, b.start, scale, mass)
+    table = torch.from_numpy(np.concatenate([np.tile(b.table[0, :4], history // period), b.table[0, 8:9]])[None]).cuda()
+    kc, _, ks, _ = b.device()
+    m = torch.zeros(1, 1, history + 16, device="cuda")
+    kv.attention_mass_fp8(q.cuda(), lse.cuda(), kc, ks, table, torch.tensor([history + 2], dtype=torch.int32, device="cuda"),
+                          b.meta()[2], 2, history + 2, scale, m, dev_status=b.status)
+    got = m[0, 0].double().cpu().numpy()
+    assert (np.abs(got[:history].reshape(-1, period) - want[0, 0, :period]) <= bound[0, 0, :period]).all()
+    assert (np.abs(got[history:history + 2] - want[0, 0, 2 * period:2 * period + 2]) <= bound[0, 0, 2 * period:2 * period + 2]).all()
+    assert (got[history + 2:] == 0).all() and b.status.item() == 0
