@@ -13,7 +13,8 @@
 // over the pieces of both.
 //
 // Launches: the schedule, prefill (if any rows may need it), decode, merge; short
-// batches that only decode: one launch that shares nothing.
+// batches that only decode: one launch that shares nothing (and reports groups that
+// do not ascend, as the schedule does).
 //
 // A group's rows stay on the decode kernel up to 32 columns per kv head, above that
 // they are tensor-core tiles (2 groups over 16384 positions, 8 heads of 128: 16
@@ -358,6 +359,7 @@ int launch_t(const SharedAttnArgs& s, cudaStream_t stream) {
                    *v >= 1;
           }, &occ))
         return KV_INT4_ERR_CUDA;
+      const int checks = s.num_groups > 0;  // a cluster that looks at the groups
       const long long tasks = (long long)a.num_seqs * c.ng, room = (long long)sms * occ;
       const long long table = (long long)a.max_blocks_per_seq * 16;
       const long long most = ((a.max_seq_len < table ? a.max_seq_len : table) + 16 * NP - 1) / (16 * NP);
@@ -365,7 +367,7 @@ int launch_t(const SharedAttnArgs& s, cudaStream_t stream) {
       while (cl < 8 && 2 * tasks * cl <= room && most > 2 * cl) cl *= 2;
       if (tasks * cl > room || most > 16 * cl) return -1;
       timing_begin(kTimedDecode, stream);
-      const int e = launch_pdl(kern, dim3((unsigned)(tasks * cl)), c.hg * CG * 32, G::smem_bytes(c.hg), stream, cl,
+      const int e = launch_pdl(kern, dim3((unsigned)((tasks + checks) * cl)), c.hg * CG * 32, G::smem_bytes(c.hg), stream, cl,
                                Fp8DecParams{c, pv, 0, cl, false});
       timing_end(kTimedDecode, stream);
       return e;

@@ -325,3 +325,25 @@ def test_prefixes_written_just_before_and_masses_after(d):
     ref, bound = F.attention(q.double().numpy(), b.host(), b.table, b.lens, b.start, d ** -0.5, True)
     _assert_attention(out, ref, bound)
     assert b.status.item() == 0
+
+
+@pytest.mark.parametrize("hq", [2, 8, 32, 64])
+def test_groups_that_do_not_ascend_are_reported_by_every_path(hq):
+    """Short batches in one launch (tables without room to spare) read the groups for the status alone, the first
+    sequences may be empty or unusable."""
+    for wide in (1, WIDE):
+        for seqs in ([(1, 20), (1, 33), (1, 8), (1, 50)], [(0, 20), (1, 33), (1, 8), (1, 50)]):
+            s = Shared([(0, seqs)], 2, 64, wide=wide)
+            b = s.b
+            q = _bf16((b.tokens, hq, 64), 5)
+            groups = np.arange(0, 400) // 100  # more entries than a CTA has threads
+            for gs, bad in (([0, 3, 2], True), ([0, 2, 5], True), ([-1, 2, 4], True), (groups[::-1], True), ([0, 2, 4], False),
+                            (groups, False), ([4, 4], False), ([0], False)):
+                b.status.zero_()
+                s.check(s.call(q, hq, group_start=gs, prefix=[0] * (len(gs) - 1)), q)
+                assert b.status.item() == (_lib.DEV_BAD_SEQ if bad else 0), (wide, gs)
+            lens = b.lens.copy()
+            lens[0] = -1 if seqs[0][0] else 20
+            b.status.zero_()
+            s.call(q, hq, group_start=[0, 3, 2], prefix=[0, 0], meta=[torch.from_numpy(x).cuda() for x in (b.table, lens, b.start)])
+            assert b.status.item() == _lib.DEV_BAD_SEQ
