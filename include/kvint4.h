@@ -519,7 +519,8 @@ KVINT4_API int kv_fp8_attention_shared(const void* q, int64_t q_token_stride, co
  * KV_INT4_DEV_BAD_SEQ; positions of a block outside [0, num_blocks) receive
  * nothing and set KV_INT4_DEV_BAD_BLOCK.  Sequences may share blocks.
  * max_seq_len bounds the seq_lens[i] (it sizes the launch); a longer sequence is
- * skipped and sets KV_INT4_DEV_BAD_SEQ.
+ * skipped and sets KV_INT4_DEV_BAD_SEQ.  The smallest of max_seq_len, mass_len and
+ * max_blocks_per_seq * 16 is at most 2^31 - 2^16 (KV_INT4_ERR_SIZE otherwise).
  */
 KVINT4_API int kv_fp8_attention_mass(const void* q, int64_t q_token_stride, const float* lse, int64_t lse_token_stride,
                                      const uint8_t* k_cache, const float* k_scale_cache, const int32_t* block_table,
@@ -556,7 +557,8 @@ KVINT4_API int kv_fp8_attention_mass(const void* q, int64_t q_token_stride, cons
  *   (KV_INT4_ERR_SIZE otherwise).  Other overlaps are not allowed.
  * new_lens: int32 [num_seqs], not seq_lens (KV_INT4_ERR_SIZE).  kept: int32
  *   [num_seqs][num_kv_heads][budget].
- * budget >= 1, 0 <= recent <= budget (KV_INT4_ERR_SIZE otherwise).
+ * budget >= 1, 0 <= recent <= budget; the smaller of mass_len and
+ * max_blocks_per_seq * 16 is at most 2^31 - 2^16 (KV_INT4_ERR_SIZE otherwise).
  * A sequence with seq_lens[i] < 0, above max_blocks_per_seq * 16 or above mass_len
  * is left alone, its new_lens is its seq_lens, and it sets KV_INT4_DEV_BAD_SEQ.
  * Rows of a block outside [0, num_blocks), or with a scale that no write stores,

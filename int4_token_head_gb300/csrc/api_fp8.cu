@@ -85,6 +85,10 @@ bool rows_apart(int64_t seqs, int64_t seq_stride, int64_t heads, int64_t head_st
   return inner >= len && outer >= len && (outer - len) / ((by_seq ? heads : seqs) - 1) >= inner;
 }
 
+// the longest sequence that the kernels' loops over positions go through in 32 bits (a
+// step of a few thousand positions beyond the end included)
+constexpr int64_t kMostPositions = (1ll << 31) - (1 << 16);
+
 int do_cache(const CacheFp8Args& a, int block_size, bool write, void* stream) {
   int e = check_sizes(a.num_seqs, a.num_tokens, a.max_len, a.max_blocks_per_seq, a.num_blocks, block_size,
                       a.num_kv_heads, a.head_size);
@@ -289,7 +293,9 @@ int kv_fp8_attention_mass(const void* q, int64_t q_token_stride, const float* ls
   int e = check_sizes(num_seqs, num_q_tokens, max_query_len, max_blocks_per_seq, num_blocks, block_size, num_kv_heads,
                       head_size);
   if (e != KV_INT4_OK) return e;
-  if ((int64_t)num_q_tokens * num_q_heads >= (1ll << 31)) return KV_INT4_ERR_SIZE;
+  if ((int64_t)num_q_tokens * num_q_heads >= (1ll << 31) ||
+      (max_seq_len > kMostPositions && mass_len > kMostPositions && (int64_t)max_blocks_per_seq * 16 > kMostPositions))
+    return KV_INT4_ERR_SIZE;
   if (num_seqs == 0 || num_q_tokens == 0) return KV_INT4_OK;
   if (!q || !lse || !mass) return KV_INT4_ERR_NULL;
   e = check_cache(k_cache, k_cache, k_scale_cache, k_scale_cache, block_table, seq_lens, query_start_loc, dev_status);
@@ -317,7 +323,7 @@ int kv_fp8_evict(uint8_t* k_cache, uint8_t* v_cache, float* k_scale_cache, float
   if (e != KV_INT4_OK) return e;
   // the longest sequence that is worked on, and what is kept of it
   const int64_t table = (int64_t)max_blocks_per_seq * 16, most = table < mass_len ? table : mass_len;
-  if ((int64_t)dst_max_blocks_per_seq * 16 < (most < budget ? most : budget) ||
+  if (most > kMostPositions || (int64_t)dst_max_blocks_per_seq * 16 < (most < budget ? most : budget) ||
       (int64_t)num_seqs * num_kv_heads >= (1ll << 26))
     return KV_INT4_ERR_SIZE;
   if (num_seqs == 0) return KV_INT4_OK;

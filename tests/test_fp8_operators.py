@@ -220,6 +220,20 @@ def test_a_destination_holds_what_can_be_kept(lib):
             assert got == (OK if dmb == need else SIZE)
 
 
+def test_lengths_whose_loops_would_leave_32_bits_are_refused(lib):
+    """Masses and evictions of sequences of up to 2^31 - 2^16 positions, by the smallest bound of their lengths (calls
+    of no sequences launch nothing)."""
+    top, wide = (1 << 31) - 1, (1 << 27) - 1
+    for ml, mb, ms, ok in ((top, wide, top, False), (top - (1 << 16) + 1, wide, top, True), (top - (1 << 16) + 2, wide, top, False),
+                           (top, wide - (1 << 12) + 1, top, True), (top, wide - (1 << 12) + 2, top, False), (1000, wide, top, True)):
+        assert lib.kv_fp8_evict(FAKE, FAKE, FAKE, FAKE, 16, 16, 8, 128, FAKE, ml, ml, ml, FAKE, mb, FAKE, 0, 64, 1, FAKE, 4,
+                                FAKE2, 64, 64, FAKE2, FAKE, None, None) == (OK if ok else SIZE)
+    for ml, mb, ms, ok in ((top, wide, top, False), (top, wide, top - (1 << 16) + 1, True), (top, wide, top - (1 << 16) + 2, False),
+                           (top, 1000, top, True), (5, wide, top, True)):
+        assert lib.kv_fp8_attention_mass(FAKE, 4096, FAKE, 32, FAKE, FAKE, FAKE, mb, FAKE, FAKE, 0, 8, 4, ms, 32, 8, 128, 16,
+                                         16, 0.1, FAKE, ml, ml, ml, None, None) == (OK if ok else SIZE)
+
+
 def test_shared_workspace_sizes(lib):
     size = lib.kv_fp8_attention_shared_workspace_size
     assert size(4, 2, 4, 32, 8, 128) == kv.attention_shared_workspace_size(4, 2, 4, 32, 8, 128) > 0
