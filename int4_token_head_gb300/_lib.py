@@ -733,7 +733,11 @@ def qk_norm_rope_axes(q, k, positions, cos_sin, pair_axis, q_weight, k_weight, e
     if positions.dtype != torch.int64 or positions.dim() != 2 or positions.shape[1] != tokens or (
             tokens > 1 and positions.stride(1) != 1):
         _refuse("positions must be int64 [axes, tokens], contiguous along the tokens")
-    pair_axis = bytes(pair_axis)
+    if not isinstance(pair_axis, bytes):  # an integer is no sequence: bytes(n) would be n pairs of axis 0
+        try:
+            pair_axis = bytes(operator.index(a) for a in pair_axis)
+        except (TypeError, ValueError) as e:
+            _refuse(f"pair_axis must be the pairs' axes as bytes: {e}")
     if len(pair_axis) != rot // 2:
         _refuse(f"pair_axis must name the axes of {rot // 2} pairs, got {len(pair_axis)}")
     dev = q.get_device()

@@ -329,3 +329,18 @@ def test_norm_rope_axes_binding_refusals():
                        ((q, k, pos, cs, pairs, w, w, 0.0, k, k), "q_out")]:
         with pytest.raises(ValueError, match=what):
             kv.qk_norm_rope_axes(*args)
+
+
+@pytest.mark.parametrize("pairs,what", [
+    (32, "as bytes"), (1 << 40, "as bytes"), (np.int64(32), "as bytes"), (torch.tensor(32), "as bytes"), (torch.tensor([32]), "32 pairs"),
+    (np.array(32), "as bytes"), (None, "as bytes"), ("0" * 32, "as bytes"), ([0] * 31 + [256], "as bytes"), ([-1] * 32, "as bytes"),
+    ([0.0] * 32, "as bytes"), ([0] * 31, "32 pairs"), (True, "as bytes"),
+    # axes that are taken: the next refusal is the tensors'
+    ([0, 1] * 16, "CUDA device"), (bytearray(32), "CUDA device"), (np.zeros(32, np.int64), "CUDA device"),
+    (torch.zeros(32, dtype=torch.int32), "CUDA device"), (tuple(kv.rope_axes((16, 16))), "CUDA device"),
+])
+def test_pair_axes_that_are_no_list_are_refused(pairs, what):
+    """An integer would otherwise be as many pairs of axis 0."""
+    q, k = torch.zeros(3, 4, 64, dtype=torch.bfloat16), torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match=what):
+        kv.qk_norm_rope_axes(q, k, torch.zeros(2, 3, dtype=torch.int64), torch.zeros(8, 64), pairs, None, None, 0.0, q, k)
