@@ -61,7 +61,9 @@ extern "C" {
                                        K/V/Q/out and code caches, 8 for slot_mapping, 4 for scale
                                        caches and int32 metadata) */
 #define KV_INT4_ERR_WORKSPACE 6     /* workspace NULL or smaller than kv_int4_attention_workspace_size() */
-#define KV_INT4_ERR_SIZE 7          /* a negative count, or a size that overflows the index types */
+#define KV_INT4_ERR_SIZE 7          /* a negative count, a size that overflows the index types, or what a call's own
+                                       comment names: a parameter outside its range, rows that overlap, a
+                                       destination too short, an output that is an input */
 #define KV_INT4_ERR_CUDA 8          /* a CUDA call or kernel launch failed */
 #define KV_INT4_ERR_ROT 10          /* kv_qk_norm_rope: rot_dim negative, above head_size or no multiple of 16;
                                        kv_qk_norm_rope_axes also: axes outside their range */

@@ -145,9 +145,13 @@ const char* kv_int4_status_string(int status) {
       return "a pointer breaks its alignment rule (16 bytes for K/V/Q/out and code caches, 8 for slot_mapping, "
              "4 for scale caches and int32 metadata) or a token stride is not a multiple of 8 elements";
     case KV_INT4_ERR_WORKSPACE: return "workspace is NULL or smaller than kv_int4_attention_workspace_size()";
-    case KV_INT4_ERR_SIZE: return "a count is negative or a size overflows the index types";
+    case KV_INT4_ERR_SIZE:
+      return "a count or stride is negative or a size overflows the index types, a parameter is outside its range (group, "
+             "block, budget, recent or eps), rows of q, out, lse or masses overlap, a destination table is too short for what "
+             "is kept, or an output is an input that it must not be";
     case KV_INT4_ERR_CUDA: return "a CUDA call or kernel launch failed";
-    case KV_INT4_ERR_ROT: return "rot_dim must be a multiple of 16 between 0 and head_size";
+    case KV_INT4_ERR_ROT:
+      return "rot_dim must be a multiple of 16 between 0 and head_size, the position axes 1 to 4, and every pair's axis one of them";
     case KV_INT4_ERR_SCRATCH_LIMIT:
       return "the call needs more workspace than the static no-allocation scratch holds "
              "(KV_INT4_NOALLOC_SCRATCH_BYTES); use kv_int4_attention with a caller workspace";

@@ -344,3 +344,12 @@ def test_pair_axes_that_are_no_list_are_refused(pairs, what):
     q, k = torch.zeros(3, 4, 64, dtype=torch.bfloat16), torch.zeros(3, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match=what):
         kv.qk_norm_rope_axes(q, k, torch.zeros(2, 3, dtype=torch.int64), torch.zeros(8, 64), pairs, None, None, 0.0, q, k)
+
+
+@pytest.mark.parametrize("code,words", [
+    (ROT, ["rot_dim", "16", "head_size", "axes 1 to 4", "pair's axis"]),
+    (SIZE, ["negative", "overflows", "budget", "recent", "eps", "group", "overlap", "destination", "output is an input"]),
+])
+def test_status_strings_name_every_reason(lib, code, words):
+    text = _lib.status_string(code)
+    assert all(w in text for w in words), text
