@@ -93,7 +93,7 @@ bool workspace_layout(int num_seqs, int num_q_tokens, int num_q_heads, int num_k
 }
 
 bool workspace_layout_fp8(int num_seqs, int num_q_tokens, int num_q_heads, int num_kv_heads,
-                          int head_size, bool compact, WorkspaceLayoutFp8* L) {
+                          int head_size, bool compact, WorkspaceLayoutFp8* L, int decode_warps, int64_t least_direct) {
   if (num_seqs < 0 || num_q_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_size <= 0) return false;
   if (num_q_heads % num_kv_heads) return false;
   const size_t group = num_q_heads / num_kv_heads;
@@ -115,10 +115,11 @@ bool workspace_layout_fp8(int num_seqs, int num_q_tokens, int num_q_heads, int n
   L->msplit = take(L->max_pieces / 2 * 16);
   const size_t least = S * Hkv * kDecodeCols, most = S * Hkv * kDecodeColsFp8, room = compact ? 0 : 3 * T * num_q_heads;
   L->direct_rows = least > room ? least : most < room ? most : room;
+  if (L->direct_rows < least_direct) L->direct_rows = least_direct;
   L->direct_o = take(L->direct_rows * D * 4);
   L->direct_ml = take(L->direct_rows * 2 * 4);
-  L->warp_o = take((size_t)kMaxDecodeWarps * kDecodeCols * D * 4);
-  L->warp_ml = take((size_t)kMaxDecodeWarps * kDecodeCols * 2 * 4);
+  L->warp_o = take((size_t)decode_warps * kDecodeCols * D * 4);
+  L->warp_ml = take((size_t)decode_warps * kDecodeCols * 2 * 4);
   const size_t rows = compact ? 0 : kPieceRows;
   L->piece_o = take(rows * D * 4);
   L->piece_ml = take(rows * 2 * 4);

@@ -42,25 +42,20 @@ bool kvint4::shared_layout(int num_seqs, int num_groups, int num_q_tokens, int n
       num_seqs > INT32_MAX - num_groups)
     return false;
   const size_t V = (size_t)num_seqs + num_groups;
-  // groups' query tokens once more; the base's own room for decode columns goes by
-  // one sequence's, a group's are more: up to 32 per virtual sequence and head here
-  if (!workspace_layout_fp8((int)V, 2 * num_q_tokens, num_q_heads, num_kv_heads, head_size, false, &L->base)) return false;
+  // groups' query tokens once more.  The base's own room for decode columns goes by
+  // one sequence's, a group's are more: up to 32 per virtual sequence and head here,
+  // and they fill more warps' slots than one token's
+  const int64_t columns = (int64_t)V * num_kv_heads * kDecodeColsFp8;
+  if (!workspace_layout_fp8((int)V, 2 * num_q_tokens, num_q_heads, num_kv_heads, head_size, false, &L->base,
+                            num_groups > 0 ? kSharedDecodeWarps : kMaxDecodeWarps,
+                            num_groups > 0 && columns <= kSharedRows ? columns : 0))
+    return false;
   size_t off = L->base.total;
   auto take = [&](size_t bytes) {
     const size_t at = off;
     off = (off + bytes + 255) / 256 * 256;
     return at;
   };
-  const int64_t columns = (int64_t)V * num_kv_heads * kDecodeColsFp8;
-  if (num_groups > 0 && columns > L->base.direct_rows && columns <= kSharedRows) {
-    L->base.direct_rows = columns;
-    L->base.direct_o = take(columns * head_size * 4);
-    L->base.direct_ml = take(columns * 2 * 4);
-  }
-  if (num_groups > 0) {  // a group's columns fill more warps' slots than one token's
-    L->base.warp_o = take((size_t)kSharedDecodeWarps * kDecodeCols * head_size * 4);
-    L->base.warp_ml = take((size_t)kSharedDecodeWarps * kDecodeCols * 2 * 4);
-  }
   L->vrec = take(V * 32);
   L->dseq2 = take(V * 16);
   L->vinfo = take(V * 8);

@@ -305,8 +305,8 @@ struct WorkspaceLayoutFp8 {
   size_t msplit;        // int4 [max_pieces / 2] tiles in pieces
   size_t direct_o;      // f32 [direct_rows][d]: query columns of (decode sequence, kv head) slots
   size_t direct_ml;     // f32 [direct_rows][2]
-  size_t warp_o;        // f32 [kMaxDecodeWarps][8][d]
-  size_t warp_ml;       // f32 [kMaxDecodeWarps][8][2]
+  size_t warp_o;        // f32 [decode warps][8][d]
+  size_t warp_ml;       // f32 [decode warps][8][2]
   size_t piece_o;       // f32 [kPieceRows][d] rows of pieces (none in the compact layout)
   size_t piece_ml;      // f32 [kPieceRows][2]
   size_t total;
@@ -318,8 +318,10 @@ constexpr int kDecodeColsFp8 = 32;  // most query columns per FP8 decode work un
 constexpr int kMaxPieces = 2048;    // pieces of split prefill tiles, and their rows over all kv heads
 constexpr int kPieceRows = 40960;   // (a piece of a full 256-row tile for each of 160 CTAs)
 
+// decode_warps: warps with a slot for a piece; least_direct: rows of direct_o at least
 bool workspace_layout_fp8(int num_seqs, int num_q_tokens, int num_q_heads, int num_kv_heads,
-                          int head_size, bool compact, WorkspaceLayoutFp8* out);
+                          int head_size, bool compact, WorkspaceLayoutFp8* out, int decode_warps = kMaxDecodeWarps,
+                          int64_t least_direct = 0);
 
 // The workspace of kv_fp8_attention_shared: the FP8 attention's for the virtual
 // sequences (a prefix per group, then the sequences) and, behind it, their records

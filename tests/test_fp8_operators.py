@@ -353,3 +353,16 @@ def test_pair_axes_that_are_no_list_are_refused(pairs, what):
 def test_status_strings_name_every_reason(lib, code, words):
     text = _lib.status_string(code)
     assert all(w in text for w in words), text
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_a_small_shared_workspace_holds_its_slots_once(lib, d):
+    """Slots of 8192 decode warps and rows of 40960 pieces, each of d values and two numbers; the rest is small.  Without
+    groups: slots of 4096."""
+    size, row = lib.kv_fp8_attention_shared_workspace_size, (d + 2) * 4
+    for groups, warps in ((1, 8192), (0, 4096)):
+        least = (warps * 8 + 40960) * row
+        assert least <= size(1, groups, 1, 1, 1, d) < least + (1 << 19)
+    # direct slots of 32 columns, once: 400 sequences and 8 groups of 8 kv heads
+    small = size(1, 1, 1, 1, 1, d)
+    assert size(400, 8, 400, 32, 8, d) < small + (408 * 8 * 32 + 2 * 400 * 32) * row + (1 << 19)
