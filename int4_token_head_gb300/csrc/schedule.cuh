@@ -466,6 +466,12 @@ __device__ void build_pieces(const Common& c, const PlanView& pv, int n_pseq, in
   }
 }
 
+// What a group asks of the row buffer: if it does not fit, one token more than there
+// is asks for all the same, and what a round of groups asks for stays in 32 bits
+// (groups of a query_start_loc that does not ascend may hold the same tokens each)
+__host__ __device__ constexpr int row_claim(int tokens, int room) { return tokens <= room ? tokens : room + 1; }
+static_assert((long long)kPrepThreads * row_claim(INT_MAX, kSharedRows) + kSharedRows <= INT_MAX, "claims of a round");
+
 // The virtual sequences of a call with shared prefixes, by the schedule's CTA.  A
 // group shares its first P positions, whole blocks of them that come before the
 // queries of all its sequences; it does where that saves keys (two sequences with
@@ -527,8 +533,8 @@ __device__ inline void build_shared(const Common& c, const PlanView& pv) {
         P = 0;
     }
     int total;
-    const int at = before + block_exclusive_scan<int>(P > 0 ? tokens : 0, &total, s_sum);
-    before = min(before + total, sh.row_tokens);  // no overflow: a round adds at most num_q_tokens
+    const int at = before + block_exclusive_scan<int>(P > 0 ? row_claim(tokens, sh.row_tokens) : 0, &total, s_sum);
+    before = min(before + total, sh.row_tokens);
     if (P > 0 && (long long)at + tokens > sh.row_tokens) P = 0;
     if (g < NG) {
       const long long tab = P > 0 ? (long long)first[g] * c.max_blocks : 0;
