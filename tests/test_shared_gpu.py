@@ -347,3 +347,79 @@ def test_groups_that_do_not_ascend_are_reported_by_every_path(hq):
             b.status.zero_()
             s.call(q, hq, group_start=[0, 3, 2], prefix=[0, 0], meta=[torch.from_numpy(x).cuda() for x in (b.table, lens, b.start)])
             assert b.status.item() == _lib.DEV_BAD_SEQ
+
+
+def _bounded(s, q, hq, max_seq_len, group_start=None, prefix=None):
+    """Shared.call with a bound of the lengths."""
+    b, scale = s.b, s.b.d ** -0.5
+    gs = torch.tensor(s.group_start if group_start is None else group_start, dtype=torch.int32, device="cuda")
+    pl = torch.tensor(s.prefix if prefix is None else prefix, dtype=torch.int32, device="cuda")
+    ws = torch.empty(kv.attention_shared_workspace_size(len(b.seqs), len(pl), q.shape[0], hq, b.hkv, b.d), dtype=torch.uint8,
+                     device="cuda").fill_(0xFF)
+    out = torch.full((q.shape[0], hq, b.d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((q.shape[0], hq), float("nan"), device="cuda")
+    kv.attention_fp8_shared(q.cuda(), *b.device(), *b.meta(), b.max_len, max_seq_len, gs, pl, s.max_group, scale, out, ws, lse=lse,
+                            dev_status=b.status)
+    return out, lse
+
+
+@pytest.mark.parametrize("d", HEADS)
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (8, 2), (7, 1)])
+def test_bounds_under_which_no_tile_is_split(d, hq, hkv):
+    """Tiles in batches whose longest sequence rules splits out on the host.  Up to 256 positions no bound splits
+    them: the same bits."""
+    g = np.random.default_rng(d)
+    ends = [(1, int(n)) for n in g.integers(1, 50, 34)]
+    most = 1000 if d <= 128 else 500
+    for groups, same in (([(192, ends), (0, [(40, 60), (1, 200)])], True),
+                         ([(most - 100, ends[:20] + [(9, 20), (30, 90)]), (0, [(most // 2, most // 2)]), (64, [(1, 5)] * 40)], False)):
+        s = Shared(groups, hkv, d, seed=d)
+        q = _bf16((s.b.tokens, hq, d), 5)
+        want = _bounded(s, q, hq, int(s.b.lens.max()))
+        s.check(want, q)
+        loose = _bounded(s, q, hq, 1 << 30)
+        s.check(loose, q)
+        assert not same or (torch.equal(want[0], loose[0]) and torch.equal(want[1], loose[1]))
+        s.check(_bounded(s, q, hq, int(s.b.lens.max()), [0], []), q)
+        assert s.b.status.item() == 0
+
+
+@pytest.mark.parametrize("d", HEADS)
+@pytest.mark.parametrize("hq", [2, 4, 16, 64])
+def test_one_launch_by_the_bound_of_the_lengths(d, hq):
+    """Tables with room to spare, lengths that fit the one-launch path, or just not."""
+    for groups in ([(64, [(1, 33), (1, 64)])], [(0, [(1, 1)])], [(160, [(1, 9)] * 3), (0, [(1, 31)])]):
+        s = Shared(groups, 2, d, seed=hq, wide=WIDE)
+        q = _bf16((s.b.tokens, hq, d), 5)
+        for bound in (int(s.b.lens.max()), 512, 4096):
+            s.check(_bounded(s, q, hq, bound), q)
+        assert s.b.status.item() == 0
+
+
+@pytest.mark.parametrize("d", HEADS)
+def test_more_sequences_over_a_longer_prefix(d):
+    g = np.random.default_rng(d)
+    _check([(2400, [(1, int(n)) for n in g.integers(1, 90, 40)])], 8, 2, d)
+
+
+@pytest.mark.parametrize("d", [64, 192])
+def test_more_pieces_than_a_warp_has_lanes(d):
+    """One kv head's tile of 34 rows over 20480 positions is 40 pieces (80 at head size 192), and with 1284 sequences
+    a row is merged by one warp: in two rounds or more."""
+    prefix, members, others = 20480, 34, 1250
+    g = np.random.default_rng(d)
+    own = [int(n) for n in g.integers(1, 40, members)]
+    short = [int(n) for n in g.integers(1, 20, others)]
+    b = Batch([(0, prefix)] + [(1, n) for n in own + short], 1, d, seed=d).fill(2)
+    table = np.full((members + others, prefix // 16 + 4), -1, np.int32)
+    for i, n in enumerate(own + short):
+        at = prefix // 16 if i < members else 0
+        table[i, :at] = b.table[0, :at]
+        table[i, at:at + -(-n // 16)] = b.table[1 + i, :-(-n // 16)]
+    b.table, b.seqs, b.start = table, b.seqs[1:], b.start[1:]
+    b.lens = np.array([prefix + n for n in own] + short, np.int32)
+    s = Shared.__new__(Shared)
+    s.b, s.group_start, s.prefix, s.max_group = b, np.array([0, members], np.int32), np.array([prefix], np.int32), members
+    q = _bf16((b.tokens, 1, d), 5, 3.0)
+    s.check(s.call(q, 1), q)
+    assert b.status.item() == 0
