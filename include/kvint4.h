@@ -474,7 +474,9 @@ KVINT4_API int kv_fp8_attention(const void* q, int64_t q_token_stride, const uin
  *   group with more shares nothing.
  * Sharing is a matter of speed alone: positions that some sequence's queries do
  *   not follow, groups that save too little or whose rows outnumber the
- *   workspace's, and short batches are computed without it.
+ *   workspace's, and short batches are computed without it.  It pays where prefixes
+ *   outweigh what the sequences have behind them; next to own parts of thousands of
+ *   positions a short prefix costs more than it saves, and num_groups = 0 is faster.
  * lse: float or NULL, element (t, hq) at lse[t*lse_token_stride + hq]: the natural
  *   logarithm of the row's denominator, log sum_p exp(softmax_scale * q . k_hat_p);
  *   -infinity for a row that sees no key (its output is zeros).

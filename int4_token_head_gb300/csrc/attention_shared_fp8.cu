@@ -19,11 +19,11 @@
 // A group's rows stay on the decode kernel up to 32 columns per kv head, above that
 // they are tensor-core tiles (2 groups over 16384 positions, 8 heads of 128: 16
 // columns 42 us on decode and 65 in tiles, 32 columns 61 to 64 and 66 to 70).
-// Measured: 64 sequences over one prefix of 8192 positions, 32/8 heads of 128, 58 us
+// Measured: 64 sequences over one prefix of 8192 positions, 32/8 heads of 128, 59 us
 // (schedule 9, tiles 20 with decode on the SMs that they leave and behind them, merge
 // 9; every sequence on its own reads 30 times the bytes); 4 x 8 sequences over 32768
 // positions 135 (2.3 TB/s of codes, issue and latency of the conversion at two warps
-// per scheduler); 16 questions to 16384 positions, 16/4 heads of 192, 104 (a step of
+// per scheduler); 16 questions to 16384 positions, 16/4 heads of 192, 103 (a step of
 // 64 keys takes 3300 cycles for 1900 of tensor work).
 
 #include <cuda.h>

@@ -83,7 +83,7 @@ __device__ __forceinline__ void stage_rows(const MassParams& p, int q0, int head
 // holds whole 16-byte chunks cq, cq + 4, ... of rows g and g + 8 (a quarter of the
 // row at 96), which are MMA A fragments once converted, as the order of dimensions
 // within a product is free.  U blocks are in flight per warp.
-// 32 sequences of 32768 positions, 32/8 heads of 128: 188 us, 6.1 TB/s (0.91 of a
+// 32 sequences of 32768 positions, 32/8 heads of 128: 190 us, 6.0 TB/s (0.90 of a
 // copy's).
 template <int D>
 struct MassFew {
