@@ -423,3 +423,30 @@ def test_more_pieces_than_a_warp_has_lanes(d):
     q = _bf16((b.tokens, 1, d), 5, 3.0)
     s.check(s.call(q, 1), q)
     assert b.status.item() == 0
+
+
+def test_one_launch_captured_with_groups_that_change(monkeypatch):
+    s = Shared([(64, [(1, 33), (1, 64), (1, 5)])], 4, 128, wide=1)
+    b, hq = s.b, 16
+    q = _bf16((b.tokens, hq, 128), 5)
+    want = s.call(q, hq)
+    s.check(want, q)
+    dev, meta, dq = b.device(), b.meta(), q.cuda()
+    gs, pl = (torch.from_numpy(x).cuda() for x in (s.group_start, s.prefix))
+    ws = torch.empty(kv.attention_shared_workspace_size(3, 1, b.tokens, hq, 4, 128), dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kv.attention_fp8_shared(dq, *dev, *meta, 1, b.table.shape[1] * 16, gs, pl, 3, 128 ** -0.5, out, ws, lse=lse, dev_status=b.status)
+    for groups, status in (([0, 3], 0), ([1, 4], _lib.DEV_BAD_SEQ), ([2, 2], 0), ([3, 1], _lib.DEV_BAD_SEQ)):
+        gs.copy_(torch.tensor(groups, dtype=torch.int32))
+        b.status.zero_()
+        out.zero_(), lse.zero_()
+        graph.replay()
+        s.check((out, lse), q)
+        assert b.status.item() == status
+    monkeypatch.setattr(_lib, "_fp8", _lib._Calls)
+    b.status.zero_()
+    s.check(s.call(q, hq, group_start=[0, 4]), q)
+    assert b.status.item() == _lib.DEV_BAD_SEQ
